@@ -263,6 +263,112 @@ int mha_decode_static(const void* q, const void* k_cache, const void* v_cache, v
 size_t mha_decode_static_scratch_bytes(void);
 
 /*
+ * The 8-bit key/value cache: half the bytes of a bf16 cache to keep and to
+ * read at every step.  Not from the pages, which keep every number as the
+ * model computes it; its format is this library's definition.
+ *   k_cache, v_cache  [B, Lk, H, d_k] e4m3 codes (4 exponent bits, 3 mantissa
+ *                     bits, no infinity), 16-byte aligned.
+ *   k_scale, v_scale  [B, H, Lk] uint8: a biased exponent per position and
+ *                     head; byte s scales its row's codes by 2^(s - 127).
+ *   d_k               a multiple of 16 from 16 to 256.
+ *
+ * mha_cache_write_f8 -- quantises T new rows per sequence into the cache.
+ * Row x = k[b, t, h] (v likewise) goes to position start[b] + t as
+ *     e = the smallest integer >= -64 with max |x| <= 448 * 2^e,
+ *     code = x * 2^-e rounded to e4m3 (nearest even),  scale byte e + 127
+ * (448 is the largest e4m3 value).  The scale is a power of two: the one
+ * rounding is the code's, at most 2^-4 of a value whose magnitude is at least
+ * 2^-14 of the row's largest.
+ *   k, v          device bf16, row (b, t) at b * seq_stride + t * token_stride
+ *                 elements with its H * d_k values contiguous; 16-byte
+ *                 aligned, strides multiples of 8 (0: dense rows, T tokens to
+ *                 a sequence), so the K and V columns of a packed projection
+ *                 are read in place.
+ *   start         device int32 [B], the first position of each sequence.
+ *   counts        device int32 [B] or NULL (T): tokens t >= counts[b] are not
+ *                 written (clamped to [0, T]).
+ * A token whose position falls outside [0, Lk) is dropped; every other row of
+ * the cache is left as it was.  A NaN is kept as a NaN code; infinities
+ * saturate the row's scale (the attention entries want finite rows).
+ * The caches and scales overlap none of the inputs and not each other
+ * (MHA_ERR_ALIAS).
+ */
+int mha_cache_write_f8(const void* k, const void* v, long long token_stride, long long seq_stride,
+                       void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int B,
+                       int T, int H, int Lk, int d_k, const int32_t* start, const int32_t* counts,
+                       void* stream);
+
+/*
+ * mha_cache_read_f8 -- the first lens[b] positions of an 8-bit cache back in
+ * bf16: k[b, j, h] = code * 2^(s - 127), exact (a code has 4 significant bits).
+ *   k, v   device bf16 [B, Lk, H, d_k], 16-byte aligned; positions from
+ *          lens[b] on are left as they were.
+ *   lens   device int32 [B] (clamped to [0, Lk]); required (MHA_ERR_NULL).
+ */
+int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                      const uint8_t* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,
+                      const int32_t* lens, void* stream);
+
+/*
+ * mha_decode_f8 -- mha_decode over an 8-bit cache, with key heads that query
+ * heads may share: query head h attends to key head h / (H / H_kv).
+ *   q, out, lse, cache_lens, scale   as mha_decode ([B, H, d_k], [B, H]).
+ *   k_cache, v_cache, k_scale, v_scale   as mha_cache_write_f8 writes them,
+ *              with H_kv heads; H a multiple of H_kv (MHA_ERR_SHAPE).
+ *              Positions from cache_lens[b] on may hold anything.
+ *   workspace  device, mha_decode_f8_workspace_bytes(...) bytes, 16-byte
+ *              aligned, owned by the caller and overlapping no argument (NULL
+ *              allowed when that is 0); not shared with a concurrent call.
+ * The tensor cores read the codes as they are.  q enters as two e4m3 pieces
+ * that give its bf16 values back (to 2^-22 of the row's largest), the weights
+ * as three e5m2 pieces (2^-11 relative); products accumulate in float32.
+ */
+int mha_decode_f8(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                  const uint8_t* v_scale, void* out, float* lse, int B, int H, int H_kv, int Lk,
+                  int d_k, const int32_t* cache_lens, float scale, void* workspace,
+                  size_t workspace_bytes, void* stream);
+size_t mha_decode_f8_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k);
+
+/*
+ * mha_decode_tree, mha_decode_tree_f8 -- one step of a tree of T drafted
+ * tokens per sequence over a bf16 or an 8-bit cache.  A decoder that drafts
+ * several continuations at once (beam search keeps four, cookipedia article,
+ * section "Transformer 全体") checks them in one step: each drafted token
+ * attends to the prefix and to the drafted tokens it follows.
+ *   q      device bf16 [B, T, H, d_k]: row t is drafted token t.
+ *   k_cache, v_cache   [B, Lk, H_kv, d_k], bf16 (d_k a multiple of 8 from 8
+ *          to 256) or 8-bit with scales (as mha_decode_f8).  Drafted token
+ *          j's key and value are expected at position prefix_lens[b] + j.
+ *   out    device bf16 [B, T, H, d_k];  lse NULL or float32 [B, H, T].
+ *   prefix_lens  device int32 [B], clamped to [0, Lk]; required
+ *          (MHA_ERR_MASK when NULL): the positions every drafted token sees.
+ *   draft_lens   device int32 [B] or NULL (T): drafted tokens of a sequence,
+ *          clamped to [0, T].  Rows t >= draft_lens[b] get output 0 and lse
+ *          -inf, and their keys are seen by no row.
+ *   tree_mask    device uint64 [B, T, ceil(T / 64)] or NULL: row t sees
+ *          drafted token j when bit j % 64 of word j / 64 is set.  NULL: a
+ *          chain, row t sees the drafted tokens 0 .. t.
+ * A row that sees no key gets output 0 and lse -inf.  Drafted positions past
+ * the capacity Lk are not seen.  Positions past the prefix and the drafted
+ * tokens may hold anything; every position seen by some row of a sequence
+ * must hold finite values.  T up to 256 (MHA_ERR_UNSUPPORTED beyond); other
+ * arguments, the workspace and errors as mha_decode_f8.
+ * Products accumulate in float32; over a bf16 cache the weights enter the
+ * product with V as two bf16 pieces (2^-16 relative).
+ */
+int mha_decode_tree(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                    int B, int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
+                    const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
+                    void* workspace, size_t workspace_bytes, void* stream);
+size_t mha_decode_tree_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k);
+int mha_decode_tree_f8(const void* q, const void* k_cache, const void* v_cache,
+                       const uint8_t* k_scale, const uint8_t* v_scale, void* out, float* lse,
+                       int B, int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
+                       const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t mha_decode_tree_f8_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k);
+
+/*
  * mha_layer_fwd -- one multi-head attention layer ("Attention Is All You
  * Need", Section 3.2.2):
  *     y = MultiHead(x, m, m) = Concat(head_1, ..., head_H) W^O,

@@ -88,6 +88,22 @@ def lib():
             h.mha_decode_static_scratch_bytes.argtypes = []
             h.mha_decode_workspace_bytes.restype = ctypes.c_size_t
             h.mha_decode_workspace_bytes.argtypes = [_c_i] * 4
+            h.mha_cache_write_f8.restype = _c_i
+            h.mha_cache_write_f8.argtypes = [_c_p] * 2 + [ctypes.c_longlong] * 2 + [_c_p] * 4 + \
+                [_c_i] * 5 + [_c_p] * 3
+            h.mha_cache_read_f8.restype = _c_i
+            h.mha_cache_read_f8.argtypes = [_c_p] * 6 + [_c_i] * 4 + [_c_p] * 2
+            h.mha_decode_f8.restype = _c_i
+            h.mha_decode_f8.argtypes = [_c_p] * 7 + [_c_i] * 5 + [_c_p, ctypes.c_float, _c_p,
+                                                                  ctypes.c_size_t, _c_p]
+            h.mha_decode_f8_workspace_bytes.restype = ctypes.c_size_t
+            h.mha_decode_f8_workspace_bytes.argtypes = [_c_i] * 5
+            for name, n_ptr in (("mha_decode_tree", 5), ("mha_decode_tree_f8", 7)):
+                getattr(h, name).restype = _c_i
+                getattr(h, name).argtypes = [_c_p] * n_ptr + [_c_i] * 6 + [_c_p] * 3 + \
+                    [ctypes.c_float, _c_p, ctypes.c_size_t, _c_p]
+                getattr(h, name + "_workspace_bytes").restype = ctypes.c_size_t
+                getattr(h, name + "_workspace_bytes").argtypes = [_c_i] * 6
             h.mha_fwd_host_workspace_bytes.restype = ctypes.c_size_t
             h.mha_fwd_host_workspace_bytes.argtypes = [_c_i] * 6
             h.mha_fwd_host.restype = _c_i
@@ -384,6 +400,262 @@ def mha_decode(q, k_cache, v_cache, cache_lens, out=None, scale: float = 0.0, wo
     if rc != MHA_OK:
         raise MhaError(rc, "mha_decode")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache, and steps of a few rows per sequence over a cache
+# ---------------------------------------------------------------------------
+def _same_device(tensors):
+    """Checks (tensor, name, dtype) triples: dtype, contiguous, all on one CUDA
+    device, which is returned."""
+    device = tensors[0][0].device
+    for t, name, dtype in tensors:
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on cuda, got {t.device}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, {tensors[0][1]} on {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return device
+
+
+def _call_on(device, stream, made, fn_name, *args):
+    """Calls an entry with `device` current and its stream (the current one
+    unless given).  ``made``: tensors allocated here for the call; on a stream
+    other than the current one the allocator must not hand them out again
+    before that stream is done."""
+    current = torch.cuda.current_stream(device).cuda_stream
+    handle = current if stream is None else (stream if isinstance(stream, int)
+                                             else stream.cuda_stream)
+    if handle != current:
+        other = torch.cuda.ExternalStream(handle, device=device)
+        for t in made:
+            t.record_stream(other)
+    fn = getattr(lib(), fn_name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc != MHA_OK:
+        raise MhaError(rc, fn_name)
+
+
+def _row_strides(t, name):
+    """(token stride, sequence stride) in elements of rows [B, T, H, d] whose
+    H * d values are contiguous."""
+    B, T, H, d = t.shape
+    if t.numel() == 0:
+        return 0, 0
+    if t.stride(3) != 1 or (H > 1 and t.stride(2) != d):
+        raise ValueError(f"{name}'s rows of H * d_k values must be contiguous")
+    token = t.stride(1) if T > 1 else H * d
+    seq = t.stride(0) if B > 1 else T * token
+    if token < H * d or seq < H * d:
+        raise ValueError(f"{name}'s rows overlap (expanded?)")
+    return token, seq
+
+
+def _cache_tensors(k_cache, v_cache, k_scale, v_scale):
+    """Checks the shapes of an 8-bit cache; returns (B, Lk, H, d) and the
+    triples for _same_device."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} "
+                         "must be [B, Lk, H, d_k] alike")
+    B, Lk, H, d = k_cache.shape
+    if tuple(k_scale.shape) != (B, H, Lk) or tuple(v_scale.shape) != (B, H, Lk):
+        raise ValueError(f"k_scale and v_scale must be [B, H, Lk] = {(B, H, Lk)}")
+    f8 = torch.float8_e4m3fn
+    return (B, Lk, H, d), [(k_cache, "k_cache", f8), (v_cache, "v_cache", f8),
+                           (k_scale, "k_scale", torch.uint8), (v_scale, "v_scale", torch.uint8)]
+
+
+def _lens(t, name, B):
+    if tuple(t.shape) != (B,):
+        raise ValueError(f"{name} must be [B]")
+    return (t, name, torch.int32)
+
+
+def mha_cache_write_f8(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=None, stream=None):
+    """Quantises new rows k, v [B, T, H, d] (bf16; rows of a packed projection
+    are read in place) into the 8-bit cache at positions start[b] .. : codes
+    k_cache, v_cache [B, Lk, H, d] (float8_e4m3fn), biased exponents k_scale,
+    v_scale [B, H, Lk] (uint8).  ``counts`` [B] limits the tokens of a
+    sequence; positions outside the cache are dropped."""
+    (B, Lk, H, d), tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
+    if k.dim() != 4 or k.shape[0] != B or k.shape[2] != H or k.shape[3] != d or v.shape != k.shape:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, T, H, d_k] of "
+                         f"the cache {tuple(k_cache.shape)}")
+    T = k.shape[1]
+    strides = _row_strides(k, "k")
+    if _row_strides(v, "v") != strides:
+        raise ValueError("k and v must have the same strides")
+    tensors.append(_lens(start, "start", B))
+    if counts is not None:
+        tensors.append(_lens(counts, "counts", B))
+    device = _same_device(tensors)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, k_cache on {device}")
+    _call_on(device, stream, (), "mha_cache_write_f8", k.data_ptr(), v.data_ptr(), *strides,
+             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, T,
+             H, Lk, d, start.data_ptr(), counts.data_ptr() if counts is not None else None)
+
+
+def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, stream=None):
+    """The first lens[b] positions of an 8-bit cache as bf16: returns (k, v)
+    [B, Lk, H, d].  Positions from lens[b] on keep what ``k`` and ``v`` held
+    (0 when they are allocated here)."""
+    shape, tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
+    B, Lk, H, d = shape
+    tensors.append(_lens(lens, "lens", B))
+    made = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have the cache's shape {shape}")
+            tensors.append((t, name, torch.bfloat16))
+    device = _same_device(tensors)
+    if k is None:
+        k = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        made.append(k)
+    if v is None:
+        v = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        made.append(v)
+    if made and stream is not None:
+        # the zeros are written on the current stream
+        _wait_current(device, stream)
+    _call_on(device, stream, made, "mha_cache_read_f8", k_cache.data_ptr(), v_cache.data_ptr(),
+             k_scale.data_ptr(), v_scale.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, Lk, d,
+             lens.data_ptr())
+    return k, v
+
+
+def _wait_current(device, stream):
+    """Makes ``stream`` wait for what the current stream has queued."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    stream.wait_stream(torch.cuda.current_stream(device))
+
+
+def _rows_call(fn_name, q, T, tensors, cache_shape, ptrs, lens, lens_name, extra, out, scale,
+               workspace, stream, return_lse, lse, ws_args, lse_shape):
+    """What the steps of a few rows have in common: checks, allocation, call."""
+    B, Lk, H_kv, d = cache_shape
+    H = q.shape[-2]
+    if q.shape[0] != B or q.shape[-1] != d or H_kv == 0 or H % H_kv != 0:
+        raise ValueError(f"cache {tuple(cache_shape)} does not match q {tuple(q.shape)}")
+    tensors = [(q, "q", torch.bfloat16)] + tensors + [_lens(lens, lens_name, B)]
+    if out is not None:
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        tensors.append((out, "out", torch.bfloat16))
+    if lse is not None:
+        if tuple(lse.shape) != lse_shape:
+            raise ValueError(f"lse must be {lse_shape}")
+        tensors.append((lse, "lse", torch.float32))
+    if workspace is not None:
+        tensors.append((workspace, "workspace", torch.uint8))
+    device = _same_device(tensors)
+    made = []
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+    if return_lse and lse is None:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
+        made.append(lse)
+    if workspace is None:
+        need = int(getattr(lib(), fn_name + "_workspace_bytes")(*ws_args))
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            made.append(workspace)
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _call_on(device, stream, made, fn_name, q.data_ptr(), *ptrs, out.data_ptr(),
+             lse.data_ptr() if return_lse else None, *ws_args, lens.data_ptr(), *extra,
+             float(scale), *ws)
+    return (out, lse) if return_lse else out
+
+
+def decode_f8_workspace_bytes(B, H, H_kv, Lk, d_k) -> int:
+    return int(lib().mha_decode_f8_workspace_bytes(B, H, H_kv, Lk, d_k))
+
+
+def decode_tree_workspace_bytes(B, T, H, H_kv, Lk, d_k) -> int:
+    return int(lib().mha_decode_tree_workspace_bytes(B, T, H, H_kv, Lk, d_k))
+
+
+def decode_tree_f8_workspace_bytes(B, T, H, H_kv, Lk, d_k) -> int:
+    return int(lib().mha_decode_tree_f8_workspace_bytes(B, T, H, H_kv, Lk, d_k))
+
+
+def mha_decode_f8(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, scale: float = 0.0,
+                  workspace=None, stream=None, return_lse: bool = False, lse=None):
+    """One decode step over an 8-bit cache: q [B, H, d] (or [B, 1, H, d], bf16)
+    against the first cache_lens[b] positions of k_cache, v_cache
+    [B, Lk, H_kv, d] with scales [B, H_kv, Lk] (mha_cache_write_f8's format);
+    query head h reads key head h // (H / H_kv).  Returns out (q's shape), or
+    (out, lse) with ``return_lse`` (lse [B, H]).  ``workspace`` (uint8 CUDA
+    tensor) is allocated when not given."""
+    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[1] != 1):
+        raise ValueError("q must be [B, H, d] or [B, 1, H, d]")
+    shape, tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
+    B, Lk, H_kv, d = shape
+    H = q.shape[-2]
+    ptrs = (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    return _rows_call("mha_decode_f8", q, 1, tensors, shape, ptrs, cache_lens, "cache_lens", (),
+                      out, scale, workspace, stream, return_lse, lse, (B, H, H_kv, Lk, d), (B, H))
+
+
+def _tree(fn_name, q, shape, tensors, ptrs, prefix_lens, draft_lens, tree_mask, out, scale,
+          workspace, stream, return_lse, lse):
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, H, d]")
+    B, T, H = q.shape[0], q.shape[1], q.shape[2]
+    if draft_lens is not None:
+        tensors.append(_lens(draft_lens, "draft_lens", B))
+    if tree_mask is not None:
+        words = (T + 63) // 64
+        if tuple(tree_mask.shape) != (B, T, words):
+            raise ValueError(f"tree_mask must be [B, T, ceil(T / 64)] = {(B, T, words)}")
+        tensors.append((tree_mask, "tree_mask", torch.int64))
+    extra = (draft_lens.data_ptr() if draft_lens is not None else None,
+             tree_mask.data_ptr() if tree_mask is not None else None)
+    return _rows_call(fn_name, q, T, tensors, shape, ptrs, prefix_lens, "prefix_lens", extra, out,
+                      scale, workspace, stream, return_lse, lse,
+                      (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
+
+
+def mha_decode_tree(q, k_cache, v_cache, prefix_lens, draft_lens=None, tree_mask=None, out=None,
+                    scale: float = 0.0, workspace=None, stream=None, return_lse: bool = False,
+                    lse=None):
+    """One step of a tree of T drafted tokens per sequence over a bf16 cache:
+    q [B, T, H, d]; k_cache, v_cache [B, Lk, H_kv, d] hold the prefix
+    (prefix_lens[b] positions, seen by every row) and drafted token j at
+    position prefix_lens[b] + j.  ``tree_mask`` int64 [B, T, ceil(T / 64)]: row
+    t sees drafted token j where bit j is set (None: a chain, j <= t).
+    ``draft_lens`` [B]: drafted tokens per sequence (None: T); rows past them
+    get output 0.  Returns out [B, T, H, d], or (out, lse [B, H, T])."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} "
+                         "must be [B, Lk, H_kv, d] alike")
+    tensors = [(k_cache, "k_cache", torch.bfloat16), (v_cache, "v_cache", torch.bfloat16)]
+    return _tree("mha_decode_tree", q, tuple(k_cache.shape), tensors,
+                 (k_cache.data_ptr(), v_cache.data_ptr()), prefix_lens, draft_lens, tree_mask,
+                 out, scale, workspace, stream, return_lse, lse)
+
+
+def mha_decode_tree_f8(q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens=None,
+                       tree_mask=None, out=None, scale: float = 0.0, workspace=None, stream=None,
+                       return_lse: bool = False, lse=None):
+    """mha_decode_tree over an 8-bit cache (mha_cache_write_f8's format)."""
+    shape, tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
+    ptrs = (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    return _tree("mha_decode_tree_f8", q, shape, tensors, ptrs, prefix_lens, draft_lens, tree_mask,
+                 out, scale, workspace, stream, return_lse, lse)
 
 
 def host_workspace_bytes(B, H, Lq, Lk, d_k, elem_bytes) -> int:

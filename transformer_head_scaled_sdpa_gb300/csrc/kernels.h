@@ -175,4 +175,54 @@ struct GemmParams {
 // of 128 x 256, or 256 x 256 when K is long); adds one to info->kernels.
 cudaError_t launch_gemm(const GemmParams& p, cudaStream_t stream, LaunchInfo* info);
 
+// The 8-bit cache: rows written (quantised) or read back, mha_cache.cu.
+struct CacheParams {
+  const void* k;  // write: bf16 rows [B, T, H, d], row_elems and seq_elems apart
+  const void* v;
+  long long row_elems, seq_elems;
+  void* k_cache;  // [B, Lk, H, d] e4m3 codes
+  void* v_cache;
+  uint8_t* k_scale;  // [B, H, Lk] biased exponents
+  uint8_t* v_scale;
+  void* k_out;  // read: bf16 [B, Lk, H, d]
+  void* v_out;
+  const int32_t* lens;    // write: first position per sequence; read: positions held
+  const int32_t* counts;  // write: tokens per sequence (null: T)
+  int B, T, H, Lk, d;     // (read: T = Lk)
+};
+
+// Blocks of the launch for these sizes (must fit a grid dimension).
+long long cache_blocks(int B, int T, int H);
+cudaError_t launch_cache(const CacheParams& p, bool write, cudaStream_t stream, LaunchInfo* info);
+
+// A few query rows per sequence over a cache, mha_rows.cu.
+struct RowsParams {
+  const void* q;      // [B, T, H, d] bf16
+  const void* k;      // [B, Lk, H_kv, d] bf16, or e4m3 codes when k_scale is set
+  const void* v;
+  const uint8_t* k_scale;  // [B, H_kv, Lk] biased exponents, or null (bf16 cache)
+  const uint8_t* v_scale;
+  void* out;          // [B, T, H, d] bf16
+  float* lse;         // [B, H, T] or null
+  const int32_t* prefix_lens;  // [B] keys every row sees (clamped to [0, Lk])
+  const int32_t* draft_lens;   // [B] rows (and drafted keys) of a sequence, or null: T
+  const uint64_t* tree_mask;   // [B, T, words] drafted keys a row sees, or null: j <= t
+  float* part_o;      // [n_splits, B*T*H, kernel width]  (n_splits > 1)
+  float* part_m;      // [n_splits, B*T*H]
+  float* part_l;      // [n_splits, B*T*H]
+  DeviceStatus* status;
+  int B, T, H, H_kv, G;  // G = H / H_kv query heads share a key head
+  int Lk, d;
+  int drafts;         // 1: drafted keys follow the prefix in the cache; 0: the prefix alone
+  int words;          // 64-bit mask words per row
+  int n_splits;
+  float scale_log2;   // scale * log2(e)
+};
+
+// Splits of the key axis for these sizes (1: no workspace), and the width the
+// split partials are kept at.
+int rows_splits(int B, int T, int H, int H_kv, int Lk, int d, bool f8);
+int rows_kernel_width(int d, bool f8);
+cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
+
 }  // namespace mha

@@ -543,6 +543,279 @@ int mha_decode_static(const void* q, const void* k_cache, const void* v_cache, v
 
 size_t mha_decode_static_scratch_bytes(void) { return kDecodeStaticScratchBytes; }
 
+// ---------------------------------------------------------------------------
+// The 8-bit cache and the attention of a few rows per sequence over a cache.
+// ---------------------------------------------------------------------------
+// 8-bit cache rows: multiples of 16 (16-byte strides for the tensor maps)
+static bool f8_width_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
+
+// The bytes of codes and of scales that a cache [B, Lk, H, d] holds.
+static bool cache_sizes(int B, int H, int Lk, int d, size_t* codes, size_t* scales) {
+  const long long rows = static_cast<long long>(B) * H;
+  if (rows > 0x7fffffffll || rows * Lk > (1ll << 40)) return false;
+  *scales = static_cast<size_t>(rows) * Lk;
+  *codes = *scales * d;
+  return true;
+}
+
+int mha_cache_write_f8(const void* k, const void* v, long long token_stride, long long seq_stride,
+                       void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int B,
+                       int T, int H, int Lk, int d_k, const int32_t* start, const int32_t* counts,
+                       void* stream) {
+  t_info = mha::LaunchInfo{};
+  if (B < 0 || T < 0 || H < 0 || Lk < 0 || token_stride < 0 || seq_stride < 0) return MHA_ERR_SHAPE;
+  if (!f8_width_ok(d_k)) return MHA_ERR_UNSUPPORTED;
+  size_t codes = 0, scales = 0;
+  if (!cache_sizes(B, H, Lk, d_k, &codes, &scales) ||
+      static_cast<long long>(B) * H * T > (1ll << 40))
+    return MHA_ERR_SHAPE;
+  const long long hd = static_cast<long long>(H) * d_k;
+  if (token_stride == 0) token_stride = hd;
+  if (seq_stride == 0) seq_stride = T * token_stride;
+  if (B == 0 || T == 0 || H == 0 || Lk == 0) return MHA_OK;
+  if (token_stride < hd || token_stride > (1ll << 40) || seq_stride < hd || seq_stride > (1ll << 50))
+    return MHA_ERR_SHAPE;
+  if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !start) return MHA_ERR_NULL;
+  if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+        reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) ||
+      (token_stride | seq_stride) % 8 != 0)
+    return MHA_ERR_UNSUPPORTED;
+  const size_t span = (static_cast<size_t>(B - 1) * seq_stride +
+                       static_cast<size_t>(T - 1) * token_stride + hd) * 2;
+  void* outs[4] = {k_cache, v_cache, k_scale, v_scale};
+  const size_t outs_b[4] = {codes, codes, scales, scales};
+  for (int o = 0; o < 4; ++o) {
+    if (overlaps(outs[o], outs_b[o], k, span) || overlaps(outs[o], outs_b[o], v, span) ||
+        overlaps(outs[o], outs_b[o], start, static_cast<size_t>(B) * 4) ||
+        overlaps(outs[o], outs_b[o], counts, static_cast<size_t>(B) * 4))
+      return MHA_ERR_ALIAS;
+    for (int i = o + 1; i < 4; ++i)
+      if (overlaps(outs[o], outs_b[o], outs[i], outs_b[i])) return MHA_ERR_ALIAS;
+  }
+  if (mha::cache_blocks(B, T, H) > 0x7fffffffll) return MHA_ERR_SHAPE;
+  DeviceState* dev = nullptr;
+  const int rc = device_state(&dev);
+  if (rc != MHA_OK) return rc;
+  mha::CacheParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.k = k;
+  p.v = v;
+  p.row_elems = token_stride;
+  p.seq_elems = seq_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.lens = start;
+  p.counts = counts;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.Lk = Lk;
+  p.d = d_k;
+  return mha::launch_cache(p, true, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess
+             ? MHA_OK
+             : MHA_ERR_LAUNCH;
+}
+
+int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                      const uint8_t* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,
+                      const int32_t* lens, void* stream) {
+  t_info = mha::LaunchInfo{};
+  if (B < 0 || H < 0 || Lk < 0) return MHA_ERR_SHAPE;
+  if (!f8_width_ok(d_k)) return MHA_ERR_UNSUPPORTED;
+  size_t codes = 0, scales = 0;
+  if (!cache_sizes(B, H, Lk, d_k, &codes, &scales)) return MHA_ERR_SHAPE;
+  if (scales == 0) return MHA_OK;
+  if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !lens) return MHA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+       reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u)
+    return MHA_ERR_UNSUPPORTED;
+  const void* ins[5] = {k_cache, v_cache, k_scale, v_scale, lens};
+  const size_t ins_b[5] = {codes, codes, scales, scales, static_cast<size_t>(B) * 4};
+  for (int i = 0; i < 5; ++i)
+    if (overlaps(k, 2 * codes, ins[i], ins_b[i]) || overlaps(v, 2 * codes, ins[i], ins_b[i]))
+      return MHA_ERR_ALIAS;
+  if (overlaps(k, 2 * codes, v, 2 * codes)) return MHA_ERR_ALIAS;
+  if (mha::cache_blocks(B, Lk, H) > 0x7fffffffll) return MHA_ERR_SHAPE;
+  DeviceState* dev = nullptr;
+  const int rc = device_state(&dev);
+  if (rc != MHA_OK) return rc;
+  mha::CacheParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.k_cache = const_cast<void*>(k_cache);
+  p.v_cache = const_cast<void*>(v_cache);
+  p.k_scale = const_cast<uint8_t*>(k_scale);
+  p.v_scale = const_cast<uint8_t*>(v_scale);
+  p.k_out = k;
+  p.v_out = v;
+  p.lens = lens;
+  p.B = B;
+  p.T = Lk;
+  p.H = H;
+  p.Lk = Lk;
+  p.d = d_k;
+  return mha::launch_cache(p, false, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess
+             ? MHA_OK
+             : MHA_ERR_LAUNCH;
+}
+
+// Most drafted tokens of one step (four mask words).
+static constexpr int kMaxDrafts = 256;
+
+// Workspace of a rows step: partial outputs, maxima and sums of every split
+// (none with a single split).
+static size_t rows_ws_bytes(int B, int T, int H, int H_kv, int Lk, int d_k, bool f8, int* splits) {
+  const int S = mha::rows_splits(B, T, H, H_kv, Lk, d_k, f8);
+  if (splits) *splits = S;
+  if (S <= 1) return 0;
+  const size_t rows = static_cast<size_t>(B) * T * H;
+  return align256(static_cast<size_t>(S) * rows * mha::rows_kernel_width(d_k, f8) * 4) +
+         2 * align256(static_cast<size_t>(S) * rows * 4);
+}
+
+// Sizes of a rows step: MHA_OK, or the code of what is wrong.
+static int rows_sizes_ok(int B, int T, int H, int H_kv, int Lk, int d_k, bool f8) {
+  if (B < 0 || T < 0 || H < 0 || H_kv < 0 || Lk < 0) return MHA_ERR_SHAPE;
+  if (H > 0 && (H_kv == 0 || H % H_kv != 0)) return MHA_ERR_SHAPE;
+  if (!(f8 ? f8_width_ok(d_k) : decode_width_ok(d_k)) || T > kMaxDrafts) return MHA_ERR_UNSUPPORTED;
+  const long long bh = static_cast<long long>(B) * H;
+  if (bh > 0x7fffffffll || bh * T > 0x7fffffffll || bh * Lk > (1ll << 40)) return MHA_ERR_SHAPE;
+  return MHA_OK;
+}
+
+static size_t rows_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k, bool f8) {
+  if (rows_sizes_ok(B, T, H, H_kv, Lk, d_k, f8) != MHA_OK ||
+      static_cast<long long>(B) * T * H == 0)
+    return 0;
+  return rows_ws_bytes(B, T, H, H_kv, Lk, d_k, f8, nullptr);
+}
+
+size_t mha_decode_f8_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k) {
+  return rows_workspace_bytes(B, 1, H, H_kv, Lk, d_k, true);
+}
+size_t mha_decode_tree_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k) {
+  return rows_workspace_bytes(B, T, H, H_kv, Lk, d_k, false);
+}
+size_t mha_decode_tree_f8_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k) {
+  return rows_workspace_bytes(B, T, H, H_kv, Lk, d_k, true);
+}
+
+// T query rows per sequence against a cache (8-bit when f8): the keys of the
+// prefix and, with `drafts`, of the drafted tokens after it.
+static int rows_step(const void* q, const void* k_cache, const void* v_cache,
+                     const uint8_t* k_scale, const uint8_t* v_scale, void* out, float* lse, int B,
+                     int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
+                     bool drafts, const int32_t* draft_lens, const uint64_t* tree_mask, bool f8,
+                     float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  t_info = mha::LaunchInfo{};
+  int rc = rows_sizes_ok(B, T, H, H_kv, Lk, d_k, f8);
+  if (rc != MHA_OK) return rc;
+  if (!std::isfinite(scale) || scale < 0.f) return MHA_ERR_SCALE;
+  const long long rows = static_cast<long long>(B) * T * H;
+  if (rows == 0) return MHA_OK;
+  if (!q || !out) return MHA_ERR_NULL;
+  if (!prefix_lens) return MHA_ERR_MASK;
+  if (Lk > 0 && (!k_cache || !v_cache || (f8 && (!k_scale || !v_scale)))) return MHA_ERR_NULL;
+  const uintptr_t mis = (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+                         (Lk > 0 ? (reinterpret_cast<uintptr_t>(k_cache) |
+                                    reinterpret_cast<uintptr_t>(v_cache))
+                                 : 0)) &
+                        15u;
+  if (mis || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      ((reinterpret_cast<uintptr_t>(prefix_lens) | reinterpret_cast<uintptr_t>(draft_lens)) & 3u) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return MHA_ERR_UNSUPPORTED;
+  const int words = (T + 63) / 64;
+  const size_t qb = static_cast<size_t>(rows) * d_k * 2;
+  const size_t scales = static_cast<size_t>(B) * H_kv * Lk;
+  const size_t kb = scales * d_k * (f8 ? 1 : 2);
+  const size_t lb = static_cast<size_t>(rows) * 4;
+  const void* ins[8] = {q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens, tree_mask};
+  const size_t ins_b[8] = {qb, kb, kb, scales, scales, static_cast<size_t>(B) * 4,
+                           static_cast<size_t>(B) * 4, static_cast<size_t>(B) * T * words * 8};
+  for (int i = 0; i < 8; ++i)
+    if (overlaps(out, qb, ins[i], ins_b[i]) || overlaps(lse, lb, ins[i], ins_b[i]))
+      return MHA_ERR_ALIAS;
+  if (overlaps(lse, lb, out, qb)) return MHA_ERR_ALIAS;
+  int S = 1;
+  const size_t need = rows_ws_bytes(B, T, H, H_kv, Lk, d_k, f8, &S);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+      return MHA_ERR_WORKSPACE;
+    for (int i = 0; i < 8; ++i)
+      if (overlaps(workspace, need, ins[i], ins_b[i])) return MHA_ERR_ALIAS;
+    if (overlaps(workspace, need, out, qb) || overlaps(workspace, need, lse, lb))
+      return MHA_ERR_ALIAS;
+  }
+  DeviceState* dev = nullptr;
+  rc = device_state(&dev);
+  if (rc != MHA_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (Lk == 0) return no_keys(out, qb, lse, static_cast<size_t>(rows), s);
+  mha::RowsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.k_scale = f8 ? k_scale : nullptr;
+  p.v_scale = f8 ? v_scale : nullptr;
+  p.out = out;
+  p.lse = lse;
+  p.prefix_lens = prefix_lens;
+  p.draft_lens = draft_lens;
+  p.tree_mask = tree_mask;
+  if (S > 1) {
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    p.part_o = reinterpret_cast<float*>(w);
+    w += align256(static_cast<size_t>(S) * rows * mha::rows_kernel_width(d_k, f8) * 4);
+    p.part_m = reinterpret_cast<float*>(w);
+    w += align256(static_cast<size_t>(S) * rows * 4);
+    p.part_l = reinterpret_cast<float*>(w);
+  }
+  p.status = dev->status;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.G = H / H_kv;
+  p.Lk = Lk;
+  p.d = d_k;
+  p.drafts = drafts ? 1 : 0;
+  p.words = words;
+  p.n_splits = S;
+  p.scale_log2 = effective_scale(scale, d_k) * kLog2e;
+  return mha::launch_rows(p, s, &t_info) == cudaSuccess ? MHA_OK : MHA_ERR_LAUNCH;
+}
+
+int mha_decode_f8(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                  const uint8_t* v_scale, void* out, float* lse, int B, int H, int H_kv, int Lk,
+                  int d_k, const int32_t* cache_lens, float scale, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  return rows_step(q, k_cache, v_cache, k_scale, v_scale, out, lse, B, 1, H, H_kv, Lk, d_k,
+                   cache_lens, false, nullptr, nullptr, true, scale, workspace, workspace_bytes,
+                   stream);
+}
+
+int mha_decode_tree(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                    int B, int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
+                    const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  return rows_step(q, k_cache, v_cache, nullptr, nullptr, out, lse, B, T, H, H_kv, Lk, d_k,
+                   prefix_lens, true, draft_lens, tree_mask, false, scale, workspace,
+                   workspace_bytes, stream);
+}
+
+int mha_decode_tree_f8(const void* q, const void* k_cache, const void* v_cache,
+                       const uint8_t* k_scale, const uint8_t* v_scale, void* out, float* lse,
+                       int B, int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
+                       const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return rows_step(q, k_cache, v_cache, k_scale, v_scale, out, lse, B, T, H, H_kv, Lk, d_k,
+                   prefix_lens, true, draft_lens, tree_mask, true, scale, workspace,
+                   workspace_bytes, stream);
+}
+
 size_t mha_bwd_workspace_bytes(int B, int H, int Lq, int Lk, int d_k) {
   if (B < 0 || H < 0 || Lq < 0 || Lk < 0 || !bf16_bwd_width_ok(d_k)) return 0;
   return align256(static_cast<size_t>(B) * H * Lq * 4);

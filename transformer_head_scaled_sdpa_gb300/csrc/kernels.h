@@ -197,9 +197,9 @@ cudaError_t launch_cache(const CacheParams& p, bool write, cudaStream_t stream, 
 
 // A few query rows per sequence over a cache, mha_rows.cu.
 struct RowsParams {
+  CUtensorMap tm_k;   // [B, Lk, H_kv, d] bf16, or e4m3 codes when k_scale is set;
+  CUtensorMap tm_v;   // box {128 bytes, 1, rows_box_keys(), 1}, 128-byte swizzle
   const void* q;      // [B, T, H, d] bf16
-  const void* k;      // [B, Lk, H_kv, d] bf16, or e4m3 codes when k_scale is set
-  const void* v;
   const uint8_t* k_scale;  // [B, H_kv, Lk] biased exponents, or null (bf16 cache)
   const uint8_t* v_scale;
   void* out;          // [B, T, H, d] bf16
@@ -223,6 +223,9 @@ struct RowsParams {
 // split partials are kept at.
 int rows_splits(int B, int T, int H, int H_kv, int Lk, int d, bool f8);
 int rows_kernel_width(int d, bool f8);
+int rows_box_keys();
+// CTAs of one split (must fit a grid dimension).
+long long rows_blocks(int B, int T, int H, int H_kv, int d, bool f8);
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
 
 }  // namespace mha

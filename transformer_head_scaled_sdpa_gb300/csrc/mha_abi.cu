@@ -209,6 +209,21 @@ bool encode_map(CUtensorMap* m, const void* base, int B, int L, int H, int d, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4-D map over an 8-bit cache [B, L, H, d]; box = 128 features x 1 head x
+// `rows` rows x 1 sequence, 128-byte swizzle.
+bool encode_map_f8(CUtensorMap* m, const void* base, int B, int L, int H, int d, int rows) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H) * d,
+                                 static_cast<cuuint64_t>(L) * H * d};
+  const cuuint32_t box[4] = {128, 1, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // lse, when requested: [B, H, Lq] float32, 4-byte aligned, overlapping none of
@@ -753,11 +768,16 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   if (rc != MHA_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Lk == 0) return no_keys(out, qb, lse, static_cast<size_t>(rows), s);
+  if (mha::rows_blocks(B, T, H, H_kv, d_k, f8) > 0x7fffffffll) return MHA_ERR_SHAPE;
   mha::RowsParams p;
   std::memset(&p, 0, sizeof(p));
+  const int box = mha::rows_box_keys();
+  if (f8 ? (!encode_map_f8(&p.tm_k, k_cache, B, Lk, H_kv, d_k, box) ||
+            !encode_map_f8(&p.tm_v, v_cache, B, Lk, H_kv, d_k, box))
+         : (!encode_map(&p.tm_k, k_cache, B, Lk, H_kv, d_k, box) ||
+            !encode_map(&p.tm_v, v_cache, B, Lk, H_kv, d_k, box)))
+    return MHA_ERR_UNSUPPORTED;
   p.q = q;
-  p.k = k_cache;
-  p.v = v_cache;
   p.k_scale = f8 ? k_scale : nullptr;
   p.v_scale = f8 ? v_scale : nullptr;
   p.out = out;

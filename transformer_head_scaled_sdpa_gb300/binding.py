@@ -48,6 +48,8 @@ def library_path() -> str:
 def lib():
     """The loaded libmha.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -412,29 +414,32 @@ def _same_device(tensors):
     for t, name, dtype in tensors:
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on cuda, got {t.device}")
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, {tensors[0][1]} on {device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    if device.type != "cuda":
+        raise ValueError(f"{tensors[0][1]} must be on cuda, got {device}")
     return device
 
 
-def _call_on(device, stream, made, fn_name, *args):
+def _call_on(device, stream, made, fn_name, args):
     """Calls an entry with `device` current and its stream (the current one
     unless given).  ``made``: tensors allocated here for the call; on a stream
     other than the current one the allocator must not hand them out again
     before that stream is done."""
-    current = torch.cuda.current_stream(device).cuda_stream
-    handle = current if stream is None else (stream if isinstance(stream, int)
-                                             else stream.cuda_stream)
-    if handle != current:
-        other = torch.cuda.ExternalStream(handle, device=device)
-        for t in made:
-            t.record_stream(other)
+    index = device.index
+    # (the raw handle: building a Stream object costs more than the launch)
+    current = torch._C._cuda_getCurrentRawStream(index)
+    handle = current
+    if stream is not None:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if handle != current:
+            other = torch.cuda.ExternalStream(handle, device=device)
+            for t in made:
+                t.record_stream(other)
     fn = getattr(lib(), fn_name)
-    if torch.cuda.current_device() == device.index:
+    if torch.cuda.current_device() == index:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -465,7 +470,7 @@ def _cache_tensors(k_cache, v_cache, k_scale, v_scale):
         raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} "
                          "must be [B, Lk, H, d_k] alike")
     B, Lk, H, d = k_cache.shape
-    if tuple(k_scale.shape) != (B, H, Lk) or tuple(v_scale.shape) != (B, H, Lk):
+    if k_scale.shape != (B, H, Lk) or v_scale.shape != (B, H, Lk):
         raise ValueError(f"k_scale and v_scale must be [B, H, Lk] = {(B, H, Lk)}")
     f8 = torch.float8_e4m3fn
     return (B, Lk, H, d), [(k_cache, "k_cache", f8), (v_cache, "v_cache", f8),
@@ -473,7 +478,7 @@ def _cache_tensors(k_cache, v_cache, k_scale, v_scale):
 
 
 def _lens(t, name, B):
-    if tuple(t.shape) != (B,):
+    if t.shape != (B,):
         raise ValueError(f"{name} must be [B]")
     return (t, name, torch.int32)
 
@@ -501,9 +506,10 @@ def mha_cache_write_f8(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=N
             raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, k_cache on {device}")
-    _call_on(device, stream, (), "mha_cache_write_f8", k.data_ptr(), v.data_ptr(), *strides,
-             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, T,
-             H, Lk, d, start.data_ptr(), counts.data_ptr() if counts is not None else None)
+    _call_on(device, stream, (), "mha_cache_write_f8",
+             (k.data_ptr(), v.data_ptr(), *strides, k_cache.data_ptr(), v_cache.data_ptr(),
+              k_scale.data_ptr(), v_scale.data_ptr(), B, T, H, Lk, d, start.data_ptr(),
+              counts.data_ptr() if counts is not None else None))
 
 
 def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, stream=None):
@@ -516,7 +522,7 @@ def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, 
     made = []
     for t, name in ((k, "k"), (v, "v")):
         if t is not None:
-            if tuple(t.shape) != shape:
+            if t.shape != shape:
                 raise ValueError(f"{name} must have the cache's shape {shape}")
             tensors.append((t, name, torch.bfloat16))
     device = _same_device(tensors)
@@ -529,9 +535,9 @@ def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, 
     if made and stream is not None:
         # the zeros are written on the current stream
         _wait_current(device, stream)
-    _call_on(device, stream, made, "mha_cache_read_f8", k_cache.data_ptr(), v_cache.data_ptr(),
-             k_scale.data_ptr(), v_scale.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, Lk, d,
-             lens.data_ptr())
+    _call_on(device, stream, made, "mha_cache_read_f8",
+             (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+              k.data_ptr(), v.data_ptr(), B, H, Lk, d, lens.data_ptr()))
     return k, v
 
 
@@ -555,7 +561,7 @@ def _rows_call(fn_name, q, T, tensors, cache_shape, ptrs, lens, lens_name, extra
             raise ValueError("out must have q's shape")
         tensors.append((out, "out", torch.bfloat16))
     if lse is not None:
-        if tuple(lse.shape) != lse_shape:
+        if lse.shape != lse_shape:
             raise ValueError(f"lse must be {lse_shape}")
         tensors.append((lse, "lse", torch.float32))
     if workspace is not None:
@@ -574,9 +580,9 @@ def _rows_call(fn_name, q, T, tensors, cache_shape, ptrs, lens, lens_name, extra
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
             made.append(workspace)
     ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    _call_on(device, stream, made, fn_name, q.data_ptr(), *ptrs, out.data_ptr(),
-             lse.data_ptr() if return_lse else None, *ws_args, lens.data_ptr(), *extra,
-             float(scale), *ws)
+    _call_on(device, stream, made, fn_name,
+             (q.data_ptr(), *ptrs, out.data_ptr(), lse.data_ptr() if return_lse else None,
+              *ws_args, lens.data_ptr(), *extra, float(scale), *ws))
     return (out, lse) if return_lse else out
 
 
@@ -619,7 +625,7 @@ def _tree(fn_name, q, shape, tensors, ptrs, prefix_lens, draft_lens, tree_mask, 
         tensors.append(_lens(draft_lens, "draft_lens", B))
     if tree_mask is not None:
         words = (T + 63) // 64
-        if tuple(tree_mask.shape) != (B, T, words):
+        if tree_mask.shape != (B, T, words):
             raise ValueError(f"tree_mask must be [B, T, ceil(T / 64)] = {(B, T, words)}")
         tensors.append((tree_mask, "tree_mask", torch.int64))
     extra = (draft_lens.data_ptr() if draft_lens is not None else None,

@@ -198,7 +198,9 @@ cudaError_t launch_cache(const CacheParams& p, bool write, cudaStream_t stream, 
 // A few query rows per sequence over a cache, mha_rows.cu.
 struct RowsParams {
   CUtensorMap tm_k;   // [B, Lk, H_kv, d] bf16, or e4m3 codes when k_scale is set;
-  CUtensorMap tm_v;   // box {128 bytes, 1, rows_box_keys(), 1}, 128-byte swizzle
+  CUtensorMap tm_v;   // box {128 bytes, 1, rows_tile_keys(), 1}, 128-byte swizzle
+  CUtensorMap tm_k_box;  // the same with boxes of rows_box_keys() keys
+  CUtensorMap tm_v_box;
   const void* q;      // [B, T, H, d] bf16
   const uint8_t* k_scale;  // [B, H_kv, Lk] biased exponents, or null (bf16 cache)
   const uint8_t* v_scale;
@@ -207,25 +209,32 @@ struct RowsParams {
   const int32_t* prefix_lens;  // [B] keys every row sees (clamped to [0, Lk])
   const int32_t* draft_lens;   // [B] rows (and drafted keys) of a sequence, or null: T
   const uint64_t* tree_mask;   // [B, T, words] drafted keys a row sees, or null: j <= t
-  float* part_o;      // [n_splits, B*T*H, kernel width]  (n_splits > 1)
-  float* part_m;      // [n_splits, B*T*H]
-  float* part_l;      // [n_splits, B*T*H]
+  float* part_o;      // [part_rows, kernel width] partials of cut units, or null
+  float* part_m;      // [part_rows]
+  float* part_l;      // [part_rows]
   DeviceStatus* status;
   int B, T, H, H_kv, G;  // G = H / H_kv query heads share a key head
   int Lk, d;
   int drafts;         // 1: drafted keys follow the prefix in the cache; 0: the prefix alone
   int words;          // 64-bit mask words per row
-  int n_splits;
+  int units;          // units (key head, block of rows) per sequence
+  int lanes, groups;  // CTAs: groups (one share of the keys each) of lanes (units)
+  int whole_units;    // 1: shares end at sequence borders, no partials
   float scale_log2;   // scale * log2(e)
 };
 
-// Splits of the key axis for these sizes (1: no workspace), and the width the
-// split partials are kept at.
-int rows_splits(int B, int T, int H, int H_kv, int Lk, int d, bool f8);
-int rows_kernel_width(int d, bool f8);
+// How a launch of these sizes divides its work.
+struct RowsPlan {
+  long long units;    // per sequence
+  long long lanes, groups;
+  long long weight;   // of all sequences at the cache's capacity (a 32-bit count)
+  bool whole_units;
+  size_t part_rows;   // rows of partials in the workspace (0: none)
+  int width;          // features a partial row is kept at
+};
+RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8);
+int rows_tile_keys();
 int rows_box_keys();
-// CTAs of one split (must fit a grid dimension).
-long long rows_blocks(int B, int T, int H, int H_kv, int d, bool f8);
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
 
 }  // namespace mha

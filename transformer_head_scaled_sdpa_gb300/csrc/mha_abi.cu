@@ -678,15 +678,10 @@ int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k
 // Most drafted tokens of one step (four mask words).
 static constexpr int kMaxDrafts = 256;
 
-// Workspace of a rows step: partial outputs, maxima and sums of every split
-// (none with a single split).
-static size_t rows_ws_bytes(int B, int T, int H, int H_kv, int Lk, int d_k, bool f8, int* splits) {
-  const int S = mha::rows_splits(B, T, H, H_kv, Lk, d_k, f8);
-  if (splits) *splits = S;
-  if (S <= 1) return 0;
-  const size_t rows = static_cast<size_t>(B) * T * H;
-  return align256(static_cast<size_t>(S) * rows * mha::rows_kernel_width(d_k, f8) * 4) +
-         2 * align256(static_cast<size_t>(S) * rows * 4);
+// Workspace of a rows step: partial outputs, maxima and sums of units that the
+// plan's shares cut (none when units stay whole).
+static size_t rows_ws_bytes(const mha::RowsPlan& plan) {
+  return align256(plan.part_rows * plan.width * 4) + 2 * align256(plan.part_rows * 4);
 }
 
 // Sizes of a rows step: MHA_OK, or the code of what is wrong.
@@ -703,7 +698,7 @@ static size_t rows_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_
   if (rows_sizes_ok(B, T, H, H_kv, Lk, d_k, f8) != MHA_OK ||
       static_cast<long long>(B) * T * H == 0)
     return 0;
-  return rows_ws_bytes(B, T, H, H_kv, Lk, d_k, f8, nullptr);
+  return rows_ws_bytes(mha::rows_plan(B, T, H, H_kv, Lk, d_k, f8));
 }
 
 size_t mha_decode_f8_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k) {
@@ -753,8 +748,10 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
     if (overlaps(out, qb, ins[i], ins_b[i]) || overlaps(lse, lb, ins[i], ins_b[i]))
       return MHA_ERR_ALIAS;
   if (overlaps(lse, lb, out, qb)) return MHA_ERR_ALIAS;
-  int S = 1;
-  const size_t need = rows_ws_bytes(B, T, H, H_kv, Lk, d_k, f8, &S);
+  const mha::RowsPlan plan = mha::rows_plan(B, T, H, H_kv, Lk, d_k, f8);
+  // (weights and blocks are 32-bit counts)
+  if (plan.weight > 0x7fffffffll || plan.groups * plan.units > 0x7fffffffll) return MHA_ERR_SHAPE;
+  const size_t need = rows_ws_bytes(plan);
   if (need > 0) {
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u))
       return MHA_ERR_WORKSPACE;
@@ -768,14 +765,14 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   if (rc != MHA_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Lk == 0) return no_keys(out, qb, lse, static_cast<size_t>(rows), s);
-  if (mha::rows_blocks(B, T, H, H_kv, d_k, f8) > 0x7fffffffll) return MHA_ERR_SHAPE;
   mha::RowsParams p;
   std::memset(&p, 0, sizeof(p));
-  const int box = mha::rows_box_keys();
-  if (f8 ? (!encode_map_f8(&p.tm_k, k_cache, B, Lk, H_kv, d_k, box) ||
-            !encode_map_f8(&p.tm_v, v_cache, B, Lk, H_kv, d_k, box))
-         : (!encode_map(&p.tm_k, k_cache, B, Lk, H_kv, d_k, box) ||
-            !encode_map(&p.tm_v, v_cache, B, Lk, H_kv, d_k, box)))
+  auto encode = [&](CUtensorMap* m, const void* base, int keys) {
+    return f8 ? encode_map_f8(m, base, B, Lk, H_kv, d_k, keys) : encode_map(m, base, B, Lk, H_kv, d_k, keys);
+  };
+  if (!encode(&p.tm_k, k_cache, mha::rows_tile_keys()) || !encode(&p.tm_v, v_cache, mha::rows_tile_keys()) ||
+      !encode(&p.tm_k_box, k_cache, mha::rows_box_keys()) ||
+      !encode(&p.tm_v_box, v_cache, mha::rows_box_keys()))
     return MHA_ERR_UNSUPPORTED;
   p.q = q;
   p.k_scale = f8 ? k_scale : nullptr;
@@ -785,12 +782,12 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   p.prefix_lens = prefix_lens;
   p.draft_lens = draft_lens;
   p.tree_mask = tree_mask;
-  if (S > 1) {
+  if (need > 0) {
     uint8_t* w = static_cast<uint8_t*>(workspace);
     p.part_o = reinterpret_cast<float*>(w);
-    w += align256(static_cast<size_t>(S) * rows * mha::rows_kernel_width(d_k, f8) * 4);
+    w += align256(plan.part_rows * plan.width * 4);
     p.part_m = reinterpret_cast<float*>(w);
-    w += align256(static_cast<size_t>(S) * rows * 4);
+    w += align256(plan.part_rows * 4);
     p.part_l = reinterpret_cast<float*>(w);
   }
   p.status = dev->status;
@@ -803,7 +800,10 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   p.d = d_k;
   p.drafts = drafts ? 1 : 0;
   p.words = words;
-  p.n_splits = S;
+  p.units = static_cast<int>(plan.units);
+  p.lanes = static_cast<int>(plan.lanes);
+  p.groups = static_cast<int>(plan.groups);
+  p.whole_units = plan.whole_units ? 1 : 0;
   p.scale_log2 = effective_scale(scale, d_k) * kLog2e;
   return mha::launch_rows(p, s, &t_info) == cudaSuccess ? MHA_OK : MHA_ERR_LAUNCH;
 }

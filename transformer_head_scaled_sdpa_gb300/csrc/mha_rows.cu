@@ -34,7 +34,8 @@
 //   v's scale 2^ev is folded into the weight: p_j = 2^(s_j + ev_j - m) with m
 //      the row's largest s_j + ev_j, so that pieces are relative to the largest
 //      contribution, and the denominator adds p_j 2^-ev_j.
-// bf16 cache: kind::f16, q exact, p as two bf16 pieces (2^-16).
+// bf16 cache: kind::f16, q exact, p as two bf16 pieces (2^-15: the first is p
+// cut to 8 bits, the second the rest rounded).
 //
 // Online softmax (scores in log2 units, q's factor scale * log2 e): the
 // reference m of a row moves only when a tile's largest score exceeds it by
@@ -42,16 +43,28 @@
 // and the sums are rescaled.  Sums are float32, one partial per thread and row,
 // added up once at the end.
 //
-// The key axis is split over gridDim.y CTAs per (sequence, key head, block of
-// rows) when those alone would leave SMs idle; each sequence's own key count is
-// divided, so short sequences of a ragged batch use fewer splits.  Partials
-// (o, m, l) go to the workspace and rows_combine_kernel merges them exactly.
+// Work: a unit is (sequence, key head, block of NR rows).  The grid is about one
+// wave of persistent CTAs, in groups of `lanes` CTAs: CTA l of a group takes the
+// key heads and row blocks l, l + lanes, ... (passes), and every CTA of group g
+// the g-th equal share of the batch's keys, counted in tiles plus kUnitCost per
+// sequence (each CTA scans the lengths for its start).  So ragged batches
+// balance, and a group reads the rows of neighbouring heads, which lie side by
+// side in the cache, and the same rows for its row blocks, at the same time: one
+// head's rows alone are 128-byte pieces of DRAM pages (measured, 16 sequences x
+// 96 heads x 2048 keys of 128 features in 8 bits: 161 us when a CTA's share ran
+// over consecutive heads instead).  A share that ends inside a sequence leaves
+// a partial (o, m, l) per unit in the workspace, and rows_combine_kernel merges
+// the partials exactly; where sequences are many and short the shares end at
+// their borders instead and no second kernel runs (rows_plan).
 //
-// 192 threads: warps 0-3 softmax and epilogue (thread = key = TMEM lane), warp
-// 4 TMEM allocation and MMA issue, warp 5 TMA producer.  The MMA warp runs
-// S(0), S(1), PV(0), S(2), PV(1), ...: the next tile's scores are computed
-// while the softmax works on this one's.  K and V tiles share one ring in that
-// order.  Every wait is bounded (abort flag, MHA_ERR_TIMEOUT).
+// Roles: 4 warps per 32 rows softmax and epilogue (thread = key = TMEM lane),
+// then one warp each for MMA issue (and TMEM) and TMA, and two that prepare the
+// next unit's Q pieces, output rows and mask words in a double buffer (over an
+// 8-bit cache one of them keeps the next tiles' scales in a ring instead).  The MMA
+// warp runs S(0), S(1), PV(0), S(2), PV(1), ... over all tiles of its share
+// without a break at unit borders: the next scores, and the loads of a whole
+// ring, run during a unit's epilogue.  Every wait is bounded (abort flag,
+// MHA_ERR_TIMEOUT).
 #include <cuda_bf16.h>
 
 #include "fp8.cuh"
@@ -61,62 +74,93 @@ namespace mha {
 namespace {
 
 constexpr int kKeys = 128;         // keys per tile
-constexpr int kBoxKeys = 32;       // keys per TMA box: a ragged last tile loads only what it needs
-constexpr int kRowThreads = 192;
-constexpr int kMmaWarp = 4, kLoadWarp = 5;
-constexpr int kRoleRowsLoad = 16, kRoleRowsMma = 17, kRoleRowsSoftmax = 18;
+constexpr int kBoxKeys = 32;       // keys per small TMA box: a ragged last tile loads only what it needs
+constexpr int kScaleTiles = 8;     // tiles whose 8-bit scales are kept ahead
+constexpr int kSms = 152;
+constexpr int kUnitCost = 2;       // a unit's fixed cost in tiles (its start and epilogue)
+constexpr int kMinShare = 2 + kUnitCost;  // least weight worth a CTA of its own
+constexpr int kSeqCache = 256;     // sequences whose lengths are kept in shared memory
+constexpr int kMaskWords = 4;      // 256 drafted tokens
+constexpr int kRoleRowsLoad = 16, kRoleRowsMma = 17, kRoleRowsSoftmax = 18, kRoleRowsQ = 19;
 
 template <bool F8_, int W_, int NR_>
 struct RowsCfg {
   static constexpr bool F8 = F8_;
   static constexpr int W = W_;    // widest head
-  static constexpr int NR = NR_;  // rows per CTA
+  static constexpr int NR = NR_;  // rows per unit
+  static constexpr int WGS = NR <= 32 ? 1 : NR / 32;     // softmax warpgroups
+  static constexpr int RPT = NR / WGS;                   // rows per softmax thread
+  static constexpr int THREADS = 128 * WGS + 128;
   static constexpr int EB = F8 ? 1 : 2;                  // bytes per cached element
   static constexpr int CHUNK = kKeys * 128;              // [128 keys x 128 B], 128-byte swizzle
-  static constexpr int TILE = kKeys * W * EB;            // a K or V tile
+  static constexpr int BLKS = W <= 128 ? 1 : 2;          // blocks of 128 features
+  static constexpr int SLOT = kKeys * (W / BLKS) * EB;   // a ring slot: one block of a K or V tile
   static constexpr int QP = F8 ? 2 : 1;                  // pieces of q
   static constexpr int PP = F8 ? 3 : 2;                  // pieces of p
-  static constexpr int NQ = QP * NR, NP = PP * NR;       // columns of S^T and O^T
+  // columns of S^T and O^T (multiples of 16: what is past the pieces is not read)
+  static constexpr int NQ = QP * NR < 16 ? 16 : QP * NR;
+  static constexpr int NP = (PP * NR + 15) / 16 * 16;
+  static constexpr int GW = RPT < 16 ? RPT : 16;         // rows handled together
+  static constexpr int GROUPS = RPT / GW;
   static constexpr int Q_BYTES = NQ * W * EB;
   static constexpr int P_BYTES = kKeys * NP * EB;
-  static constexpr int MISC = NR > 32 ? 4096 : 2048;
-  // two CTAs per SM when three tiles of the ring fit, else one with a deep ring
-  static constexpr int FIXED = Q_BYTES + P_BYTES + MISC + 1024;
-  static constexpr int SLOTS2 = (115712 - FIXED) / TILE;
-  static constexpr bool TWO = SLOTS2 >= 3 && NR <= 32;
-  static constexpr int SLOTS = TWO ? SLOTS2 : (232448 - FIXED) / TILE;
-  static constexpr int MIN_BLOCKS = TWO ? 2 : 1;
-  static_assert(SLOTS >= 3, "ring");
-  static constexpr int OFF_Q = SLOTS * TILE;
-  static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_MISC = OFF_P + P_BYTES;
-  static constexpr int SMEM = OFF_MISC + MISC + 1024;
-  // barriers
-  static constexpr int FULL = 0;              // + slot
-  static constexpr int EMPTY = SLOTS;         // + slot
-  static constexpr int Q_FULL = 2 * SLOTS;    // 128 arrivals
-  static constexpr int S_FULL = Q_FULL + 1;   // + buffer
-  static constexpr int P_FULL = S_FULL + 2;   // 128 arrivals
-  static constexpr int PV_DONE = P_FULL + 1;
-  static constexpr int DRAIN = PV_DONE + 1;
-  static constexpr int NBAR = DRAIN + 1;
-  // misc area: barriers, TMEM slot, abort flag, then per-row values
-  static constexpr int OFF_TMEM = OFF_MISC + 8 * NBAR;
-  static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int OFF_ROWS = OFF_MISC + (8 * NBAR + 8 + 15) / 16 * 16;
-  // [factor | reference | alpha | red: 4 warps | output row | draft], NR each
-  static_assert(OFF_ROWS - OFF_MISC + 9 * NR * 4 <= MISC, "misc area");
+  // barriers (512 bytes), lengths, scales, per-row values of two units and of the softmax
+  static constexpr int SCALES = F8 ? kScaleTiles * kKeys * 2 : 0;
+  static constexpr int MISC = 512 + 8 * kSeqCache + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
+  static constexpr int FIXED = 2 * Q_BYTES + P_BYTES + MISC + 1024;
   // TMEM: S0 | S1 | O (per 128 features)
   static constexpr int M_O = W == 64 ? 64 : 128;         // rows of the O^T tile
-  static constexpr int BLKS = W <= 128 ? 1 : 2;          // blocks of 128 features
   static constexpr uint32_t TM_S1 = NQ, TM_O = 2 * NQ;
   static constexpr uint32_t TM_USED = 2 * NQ + BLKS * NP;
   static constexpr uint32_t TMEM_COLS =
       TM_USED <= 32 ? 32 : (TM_USED <= 64 ? 64 : (TM_USED <= 128 ? 128 : (TM_USED <= 256 ? 256 : 512)));
-  static_assert(TM_USED <= 512 && (!TWO || TMEM_COLS <= 256), "TMEM budget");
-  static_assert(OFF_Q % 1024 == 0 && OFF_P % 128 == 0 && OFF_MISC % 16 == 0, "alignment");
+  static_assert(TM_USED <= 512, "TMEM budget");
+  // two CTAs per SM when each can hold two tiles' worth of ring, else one with
+  // a deep ring
+  static constexpr int SLOTS2 = (115712 - FIXED) / SLOT;
+  static constexpr bool TWO = SLOTS2 >= 4 && WGS == 1 && TMEM_COLS <= 256;
+  static constexpr int SLOTS1 = (232448 - FIXED) / SLOT;
+  static constexpr int SLOTS = TWO ? SLOTS2 : (SLOTS1 > 16 ? 16 : SLOTS1);
+  static constexpr int MIN_BLOCKS = TWO ? 2 : 1;
+  static_assert(SLOTS >= 2 * BLKS + 1, "ring: the next K tile while V waits");
+  static constexpr int OFF_Q = SLOTS * SLOT;             // + buffer * Q_BYTES
+  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_MISC = OFF_P + P_BYTES;
+  static constexpr int SMEM = OFF_MISC + MISC + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+  // barriers
+  static constexpr int FULL = 0;              // + slot
+  static constexpr int EMPTY = SLOTS;         // + slot
+  static constexpr int Q_THREADS = F8 ? 32 : 64;
+  static constexpr int Q_FULL = 2 * SLOTS;    // + buffer: Q and the unit's row values (Q_THREADS arrivals)
+  static constexpr int Q_EMPTY = Q_FULL + 2;  // + buffer: the last scores and the epilogue are done
+  static constexpr int S_FULL = Q_EMPTY + 2;  // + buffer
+  static constexpr int P_FULL = S_FULL + 2;   // every softmax thread
+  static constexpr int PV_DONE = P_FULL + 1;
+  static constexpr int O_FREE = PV_DONE + 1;  // the epilogue has read O (every softmax thread)
+  static constexpr int DRAIN = O_FREE + 1;
+  static constexpr int SC_FULL = DRAIN + 1;            // + tile: scales (8-bit; 32 arrivals)
+  static constexpr int SC_EMPTY = SC_FULL + (F8 ? kScaleTiles : 0);  // + tile: read (each softmax warp)
+  static constexpr int NBAR = SC_EMPTY + (F8 ? kScaleTiles : 0);
+  static constexpr int OFF_TMEM = OFF_MISC + 8 * NBAR;
+  static constexpr int OFF_ABORT = OFF_TMEM + 4;
+  static constexpr int OFF_START = OFF_TMEM + 8;         // Share
+  static_assert(8 * NBAR + 8 + 16 <= 512, "barrier area");
+  static constexpr int OFF_SEQ = OFF_MISC + 512;         // int2 [kSeqCache]
+  static constexpr int OFF_SCALES = OFF_SEQ + 8 * kSeqCache;  // [kScaleTiles][128]: k's byte, v's byte
+  static constexpr int OFF_ROWS = OFF_SCALES + SCALES;
+  // per buffer: factor, output row, lse index, live [NR each], mask words [NR][4]
+  static constexpr int ROWS_BYTES = (16 + 8 * kMaskWords) * NR;
+  static constexpr int OFF_SOFT = OFF_ROWS + 2 * ROWS_BYTES;  // reference, shift [NR each], red [NR][4]
+  static_assert(OFF_Q % 1024 == 0 && OFF_P % 128 == 0 && OFF_MISC % 16 == 0 && ROWS_BYTES % 16 == 0, "alignment");
   static constexpr float SLACK = F8 ? 5.f : 8.f;         // reference moves beyond this (log2)
   static constexpr float LIFT = F8 ? 10.f : 0.f;         // weights are 2^LIFT at the reference
+  // registers: the softmax warpgroups take from the others
+  static constexpr bool SPLIT_REGS = TWO || WGS > 1;
+  static constexpr int REGS_OTHER = NR <= 16 ? 96 : 80;
+  static constexpr int REGS_SOFT = TWO ? 256 - REGS_OTHER : 208;
+  static_assert(!TWO || (REGS_OTHER + REGS_SOFT) * 128 <= 256 * 128, "register split");
+  static_assert(WGS != 2 || REGS_OTHER * 128 + REGS_SOFT * 256 <= 168 * 384, "register split");
 };
 
 // Shared-memory matrix descriptor without swizzle: core matrices of 8 rows x
@@ -153,16 +197,17 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
   }
 }
 
-// True for every softmax thread when any of them passes true (named barrier 1).
-__device__ __forceinline__ bool any_of_128(bool x) {
+// True for every thread of a softmax warpgroup when any of them passes true
+// (named barrier `id` over its 128 threads).
+__device__ __forceinline__ bool any_of_128(uint32_t id, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x))
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
       : "memory");
   return r != 0;
 }
@@ -186,32 +231,222 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 
-// What a CTA works on.
-struct RowsWork {
-  int n;              // prefix keys
-  int live;           // drafted tokens (rows) of the sequence
-  int end;            // keys any row may see
-  int per, active;    // tiles per split, splits with work (>= 1)
-};
-__device__ __forceinline__ RowsWork rows_work(const RowsParams& p, int b) {
-  RowsWork w;
-  const int n = __ldg(p.prefix_lens + b);
-  w.n = n < 0 ? 0 : (n > p.Lk ? p.Lk : n);
-  w.live = p.T;
-  if (p.draft_lens) {
-    const int live = __ldg(p.draft_lens + b);
-    w.live = live < 0 ? 0 : (live > p.T ? p.T : live);
-  }
-  w.end = p.drafts ? min(p.Lk, w.n + w.live) : w.n;
-  if (w.live == 0) w.end = 0;  // every row is empty
-  const int tiles = (w.end + kKeys - 1) / kKeys;
-  w.per = (tiles + p.n_splits - 1) / p.n_splits;
-  w.active = w.per > 0 ? (tiles + w.per - 1) / w.per : 1;
-  return w;
+// mbar_wait by a whole warp with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          DeviceStatus* status, int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, site));
 }
 
+// Largest value of the warp.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sums of N values over the warp, N <= 32 a power of two: each step halves the
+// values a lane keeps and adds its partner's for them.  Lane i returns the sum
+// of value i / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&v)[N], int lane) {
+  float x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = v[i];
+  int keep = N;
+#pragma unroll
+  for (int bit = 16; bit; bit >>= 1) {
+    if (keep > 1) {
+      keep >>= 1;
+      const bool hi = (lane & bit) != 0;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= keep) break;
+        const float send = hi ? x[i] : x[i + keep];
+        x[i] = (hi ? x[i + keep] : x[i]) + __shfl_xor_sync(0xffffffffu, send, bit);
+      }
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], bit);
+    }
+  }
+  return x[0];
+}
+
+// 8 or 16 consecutive 32-bit columns of this warp's TMEM lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16, "columns");
+  if constexpr (N == 16) {
+    tmem_ld16(at, r);
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7])
+                 : "r"(at));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16, "columns");
+  if constexpr (N == 16) {
+    tmem_st16(at, r);
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Shares of the work
+// ---------------------------------------------------------------------------
+// A sequence's lengths: prefix keys and drafted tokens, clamped.
+__device__ __forceinline__ int2 seq_lens(const RowsParams& p, int b) {
+  const int n = __ldg(p.prefix_lens + b);
+  int live = p.T;
+  if (p.draft_lens) {
+    live = __ldg(p.draft_lens + b);
+    live = live < 0 ? 0 : (live > p.T ? p.T : live);
+  }
+  return make_int2(n < 0 ? 0 : (n > p.Lk ? p.Lk : n), live);
+}
+// Keys any row may see (none without a row).
+__device__ __forceinline__ int seq_end(const RowsParams& p, int2 s) {
+  return s.y == 0 ? 0 : (p.drafts ? min(p.Lk, s.x + s.y) : s.x);
+}
+__device__ __forceinline__ int seq_tiles(const RowsParams& p, int2 s) {
+  return (seq_end(p, s) + kKeys - 1) / kKeys;
+}
+
+// A position in the sequences' weights: sequence and weight before it in that
+// sequence.
+struct Place {
+  int b, lo;
+  int wt;  // weight of the sequence
+};
+
+// Whole warp: the weight of all sequences.  `seq`: where to keep the lengths of
+// up to kSeqCache of them, or null.
+__device__ __forceinline__ int total_weight(const RowsParams& p, int2* seq) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  int sum = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const int2 s = seq_lens(p, b);
+    if (seq && b < kSeqCache) seq[b] = s;
+    sum += seq_tiles(p, s) + kUnitCost;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Whole warp: where `pos` (less than the total) falls.
+__device__ __forceinline__ Place find_place(const RowsParams& p, int pos) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  int before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int b = b0 + lane;
+    const int wt = b < p.B ? seq_tiles(p, seq_lens(p, b)) + kUnitCost : 0;
+    int upto = wt;  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, before + upto > pos);
+    if (here != 0 || b0 + 32 >= p.B) {
+      const int src = here != 0 ? __ffs(here) - 1 : 31;
+      Place q;
+      q.b = b0 + src;
+      q.wt = __shfl_sync(0xffffffffu, wt, src);
+      q.lo = __shfl_sync(0xffffffffu, pos - before - (upto - wt), src);
+      return q;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+
+// Shares that are worth a group each, and where share c starts.
+__device__ __forceinline__ int share_count(int total, int most) {
+  const int n = total / kMinShare;
+  return n < 1 ? 1 : (n < most ? n : most);
+}
+__device__ __forceinline__ int share_start(int total, int shares, int c) {
+  return static_cast<int>(static_cast<long long>(total) * c / shares);
+}
+
+// A group's share (in shared memory).
+struct Share {
+  int b, lo, left, pad;
+};
+
+// The units (parts of units) of a CTA, in order: its passes over the share.
+struct UnitIter {
+  int u;              // key head and block of rows
+  int b, lo;          // sequence, weight of it done before
+  int left;           // weight left from lo on
+  int2 s;             // the sequence's lengths
+  int t0, t1, tiles;  // this part's tiles, of the sequence's
+
+  // kEmpty: units without keys are visited too (they belong to the share that
+  // holds their sequence's start)
+  template <bool kEmpty = false>
+  __device__ __forceinline__ bool start(const RowsParams& p, const Share& at, const int2* seq) {
+    u = static_cast<int>(blockIdx.x) % p.lanes;
+    if (at.left <= 0 || u >= p.units) return false;
+    b = at.b;
+    lo = at.lo;
+    left = at.left;
+    load(p, seq);
+    return here<kEmpty>() || next<kEmpty>(p, at, seq);
+  }
+  template <bool kEmpty = false>
+  __device__ __forceinline__ bool next(const RowsParams& p, const Share& at, const int2* seq) {
+    for (;;) {
+      left -= tiles + kUnitCost - lo;
+      if (left > 0) {
+        lo = 0;
+        ++b;
+      } else {
+        u += p.lanes;
+        if (u >= p.units) return false;
+        b = at.b;
+        lo = at.lo;
+        left = at.left;
+      }
+      load(p, seq);
+      if (here<kEmpty>()) return true;
+    }
+  }
+  template <bool kEmpty>
+  __device__ __forceinline__ bool here() const {
+    return t1 > t0 || (kEmpty && tiles == 0 && lo == 0);
+  }
+  __device__ __forceinline__ void load(const RowsParams& p, const int2* seq) {
+    s = b < kSeqCache ? seq[b] : seq_lens(p, b);
+    tiles = seq_tiles(p, s);
+    t0 = max(0, lo - kUnitCost);
+    t1 = left >= tiles + kUnitCost - lo ? tiles : max(0, lo + left - kUnitCost);
+  }
+  __device__ __forceinline__ int count() const { return t1 - t0; }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// A position in the ring of K and V blocks, which are loaded and used in the
+// order K(0) K(1) V(0) K(2) V(1) ... V(last) of the CTA's tiles.
+template <int SLOTS>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == SLOTS) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 template <bool F8, int W, int NR>
-__global__ void __launch_bounds__(kRowThreads, (RowsCfg<F8, W, NR>::MIN_BLOCKS))
+__global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W, NR>::MIN_BLOCKS))
     rows_kernel(const __grid_constant__ RowsParams p) {
   using C = RowsCfg<F8, W, NR>;
   extern __shared__ uint8_t smem_raw[];
@@ -219,40 +454,48 @@ __global__ void __launch_bounds__(kRowThreads, (RowsCfg<F8, W, NR>::MIN_BLOCKS))
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t s_base = smem_u32(smem);
   auto bar = [&](int id) { return s_base + C::OFF_MISC + 8u * static_cast<uint32_t>(id); };
-  const uint32_t sQ = s_base + C::OFF_Q, sP = s_base + C::OFF_P;
+  const uint32_t sP = s_base + C::OFF_P;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-  float* row_factor = reinterpret_cast<float*>(smem + C::OFF_ROWS);
-  float* row_ref = row_factor + NR;
-  float* row_alpha = row_ref + NR;
-  float* red = row_alpha + NR;                       // [4][NR]
-  int* row_out = reinterpret_cast<int*>(red + 4 * NR);  // output row, -1: none
-  int* row_t = row_out + NR;                         // drafted token, -1: an empty row
+  Share* share = reinterpret_cast<Share*>(smem + C::OFF_START);
+  int2* seq = reinterpret_cast<int2*>(smem + C::OFF_SEQ);
+  auto row_factor = [&](int buf) { return reinterpret_cast<float*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES); };
+  auto row_out = [&](int buf) { return reinterpret_cast<int*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES) + NR; };
+  auto row_lse = [&](int buf) { return reinterpret_cast<int*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES) + 2 * NR; };
+  auto row_live = [&](int buf) { return reinterpret_cast<int*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES) + 3 * NR; };
+  auto row_mask = [&](int buf) {
+    return reinterpret_cast<uint64_t*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES + 16 * NR);
+  };
+  float* row_ref = reinterpret_cast<float*>(smem + C::OFF_SOFT);  // references less LIFT
+  float* row_shift = row_ref + NR;
+  float* red = row_shift + NR;  // [NR][4 warps]
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int tid = static_cast<int>(threadIdx.x);
-
-  // (rows block fastest, then key head: CTAs that read the same or neighbouring
-  // cache rows run together)
+  constexpr int SOFT = 128 * C::WGS;            // softmax threads
+  constexpr int kMmaWarp = 4 * C::WGS, kLoadWarp = kMmaWarp + 1, kQWarp = kMmaWarp + 2;
   const int n_rows = p.T * p.G;
-  const int blocks = (n_rows + NR - 1) / NR;
-  int x = static_cast<int>(blockIdx.x);
-  const int rb = x % blocks;
-  x /= blocks;
-  const int hk = x % p.H_kv, b = x / p.H_kv;
-  const int split = static_cast<int>(blockIdx.y);
-  const int rows_here = min(NR, n_rows - rb * NR);
+  const int blocks = (n_rows + NR - 1) / NR;    // blocks of rows per key head (the faster index of a unit)
 
   if (tid == 0) {
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(bar(C::FULL + s), 1);
       mbar_init(bar(C::EMPTY + s), 1);
     }
-    mbar_init(bar(C::Q_FULL), 128);
-    mbar_init(bar(C::S_FULL), 1);
-    mbar_init(bar(C::S_FULL + 1), 1);
-    mbar_init(bar(C::P_FULL), 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::Q_FULL + i), C::Q_THREADS);
+      mbar_init(bar(C::Q_EMPTY + i), 1 + SOFT);
+      mbar_init(bar(C::S_FULL + i), 1);
+    }
+    mbar_init(bar(C::P_FULL), SOFT);
     mbar_init(bar(C::PV_DONE), 1);
+    mbar_init(bar(C::O_FREE), SOFT);
     mbar_init(bar(C::DRAIN), 1);
+    if constexpr (F8) {
+      for (int i = 0; i < kScaleTiles; ++i) {
+        mbar_init(bar(C::SC_FULL + i), 32);
+        mbar_init(bar(C::SC_EMPTY + i), 4 * C::WGS);
+      }
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -260,64 +503,120 @@ __global__ void __launch_bounds__(kRowThreads, (RowsCfg<F8, W, NR>::MIN_BLOCKS))
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
     tmem_relinquish();
   }
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == kQWarp && lane == 0) {
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
+    tma_prefetch_desc(&p.tm_k_box);
+    tma_prefetch_desc(&p.tm_v_box);
+  }
+  if (warp == kLoadWarp) {
+    griddep_wait();  // global memory only from here on
+    const int total = total_weight(p, seq);
+    const int shares = share_count(total, p.groups);
+    const int c = static_cast<int>(blockIdx.x) / p.lanes;
+    Share at = {0, 0, 0, 0};
+    if (c < shares) {
+      int a = share_start(total, shares, c), z = share_start(total, shares, c + 1);
+      Place q = find_place(p, a);
+      if (p.whole_units) {
+        // both ends to the nearer border of a sequence
+        auto border = [&](int pos, const Place& x) { return pos - x.lo + (2 * x.lo >= x.wt ? x.wt : 0); };
+        a = border(a, q);
+        if (2 * q.lo >= q.wt) ++q.b;
+        q.lo = 0;
+        if (z < total) z = border(z, find_place(p, z));
+      }
+      at.b = q.b;
+      at.lo = q.lo;
+      at.left = z - a;
+    }
+    if (lane == 0) *share = at;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_wait();  // global memory only from here on
+  const Share at = *share;
+  // the next launch may set itself up (it waits for this grid before it touches
+  // global memory)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  griddep_wait();
 
-  const RowsWork w = rows_work(p, b);
-  const int k_begin = split * w.per * kKeys;
-  const int k_end = min(w.end, k_begin + w.per * kKeys);
-  const int n = (k_end > k_begin) ? (k_end - k_begin + kKeys - 1) / kKeys : 0;
-  const bool works = split < w.active;
-  // order of the ring: K0 K1 V0 K2 V1 ... V(n-1)
-  auto k_item = [&](int i) { return i == 0 ? 0 : 2 * i - 1; };
-  auto v_item = [&](int i) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
+  const int blks = C::BLKS == 1 ? 1 : (p.d + 127) / 128;  // 128-feature blocks in use
+  auto unit_hk = [&](const UnitIter& it) { return blocks == 1 ? it.u : it.u / blocks; };
+  auto unit_rb = [&](const UnitIter& it) { return blocks == 1 ? 0 : it.u % blocks; };
 
+  if (warp >= kMmaWarp) {
+  if constexpr (C::SPLIT_REGS) regs_decrease<C::REGS_OTHER>();
   if (warp == kLoadWarp) {
-    // ---- TMA producer
+    // ---- TMA producer (one lane)
     const int site = kRoleRowsLoad * 64;
-    const int chunks = (p.d * C::EB + 127) / 128;
-    int item = 0;
-    bool ok = true;
-    auto load = [&](const CUtensorMap* map, int tile) {
-      const int s = item % C::SLOTS;
-      if (item >= C::SLOTS &&
-          !mbar_wait(bar(C::EMPTY + s), ((item / C::SLOTS) - 1) & 1, abort_flag, p.status,
-                     site + C::EMPTY + s))
-        return false;
-      if (elect_one()) {
-        const int key = k_begin + tile * kKeys;
-        const int boxes = (min(kKeys, k_end - key) + kBoxKeys - 1) / kBoxKeys;
-        mbar_arrive_expect_tx(bar(C::FULL + s), static_cast<uint32_t>(boxes * chunks * kBoxKeys * 128));
-        for (int c = 0; c < chunks; ++c)
-          for (int x = 0; x < boxes; ++x)
-            tma_load_4d(s_base + s * C::TILE + c * C::CHUNK + x * kBoxKeys * 128, map,
-                        bar(C::FULL + s), c * (128 / C::EB), hk, key + x * kBoxKeys, b);
+    if (elect_one()) {
+      Ring<C::SLOTS> ring;
+      int loaded = 0;  // slots filled so far
+      bool ok = true;
+      // one tile of K or V: whole in boxes of 128 keys, a ragged one in boxes of
+      // kBoxKeys as far as it goes
+      auto load = [&](const CUtensorMap* big, const CUtensorMap* small, int key, int end, int hk, int b) {
+        const int boxes = end - key >= kKeys ? 0 : (end - key + kBoxKeys - 1) / kBoxKeys;
+        const uint32_t box_bytes = boxes == 0 ? kKeys * 128 : boxes * kBoxKeys * 128;
+#pragma unroll
+        for (int blk = 0; blk < C::BLKS; ++blk) {
+          if (blk >= blks) break;
+          const int s = ring.slot;
+          ok = ok && (loaded < C::SLOTS ||
+                      mbar_wait(bar(C::EMPTY + s), ring.phase ^ 1, abort_flag, p.status, site + C::EMPTY + s));
+          if (!ok) return;
+          const int f0 = blk * 128;
+          const int chunks = (min(p.d - f0, 128) * C::EB + 127) / 128;
+          const uint32_t full = bar(C::FULL + s);
+          mbar_arrive_expect_tx(full, chunks * box_bytes);
+          for (int c = 0; c < chunks; ++c) {
+            const uint32_t dst = s_base + s * C::SLOT + c * C::CHUNK;
+            const int f = f0 + c * (128 / C::EB);
+            if (boxes == 0) {
+              tma_load_4d(dst, big, full, f, hk, key, b);
+            } else {
+              for (int x = 0; x < boxes; ++x)
+                tma_load_4d(dst + x * kBoxKeys * 128, small, full, f, hk, key + x * kBoxKeys, b);
+            }
+          }
+          ++loaded;
+          ring.advance();
+        }
+      };
+      UnitIter it;
+      bool any = false;
+      int v_key = 0, v_end = 0, v_hk = 0, v_b = 0;  // the tile whose V is next
+      for (bool more = it.start(p, at, seq); more && ok; more = it.next(p, at, seq)) {
+        const int hk = unit_hk(it), end = seq_end(p, it.s), b = it.b, t1 = it.t1;
+        for (int x = it.t0; x < t1 && ok; ++x) {
+          load(&p.tm_k, &p.tm_k_box, x * kKeys, end, hk, b);
+          if (any && ok) load(&p.tm_v, &p.tm_v_box, v_key, v_end, v_hk, v_b);
+          any = true;
+          v_key = x * kKeys;
+          v_end = end;
+          v_hk = hk;
+          v_b = b;
+        }
       }
-      __syncwarp();
-      ++item;
-      return true;
-    };
-    if (n > 0) ok = load(&p.tm_k, 0);
-    for (int i = 0; i < n && ok; ++i) {
-      if (i + 1 < n) ok = load(&p.tm_k, i + 1);
-      if (ok) ok = load(&p.tm_v, i);
+      if (any && ok) load(&p.tm_v, &p.tm_v_box, v_key, v_end, v_hk, v_b);
+      // every copy started must land before the CTA exits
+      volatile int never = 0;
+      for (int x = min(loaded, C::SLOTS); x > 0; --x) {
+        // (the slot x before the next one)
+        const int s = ring.slot >= x ? ring.slot - x : ring.slot - x + C::SLOTS;
+        mbar_wait(bar(C::FULL + s), ring.slot >= x ? ring.phase : ring.phase ^ 1, &never, p.status,
+                  site + C::FULL + s);
+      }
     }
-    // every copy started must land before the CTA exits
-    volatile int never = 0;
-    for (int t = (item > C::SLOTS ? item - C::SLOTS : 0); t < item; ++t)
-      mbar_wait(bar(C::FULL + t % C::SLOTS), (t / C::SLOTS) & 1, &never, p.status, site + C::FULL);
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---- MMA issuer
     const int site = kRoleRowsMma * 64;
     constexpr int KSTEP = F8 ? 32 : 16;                 // reduction elements per MMA
     const int n_ks = (p.d + KSTEP - 1) / KSTEP;
+    constexpr int KS_BLK = 128 / KSTEP;                 // steps of a 128-feature block
     constexpr uint32_t idesc_s = F8 ? idesc_f8_f32(128, C::NQ, 0, false, false)
                                     : idesc_bf16_f32(128, C::NQ, false, false);
     constexpr uint32_t idesc_o = F8 ? idesc_f8_f32(C::M_O, C::NP, 1, true, true)
@@ -327,417 +626,600 @@ __global__ void __launch_bounds__(kRowThreads, (RowsCfg<F8, W, NR>::MIN_BLOCKS))
     // chunk of features CHUNK apart, 8-key groups 1024 B apart.
     const uint64_t dk0 = smem_desc_sw128(s_base, 16, 1024);
     const uint64_t dv0 = smem_desc_sw128(s_base, C::CHUNK, 1024);
-    const uint64_t dq0 = smem_desc_plain(sQ, C::NQ * 16, 128);
+    const uint64_t dq0 = smem_desc_plain(s_base + C::OFF_Q, C::NQ * 16, 128);
     const uint64_t dp0 = smem_desc_plain(sP, 128, kKeys * 16);
-    const int blks = W <= 128 ? 1 : (p.d + 127) / 128;
-    auto issue_s = [&](int i) {
-      const int it = k_item(i), s = it % C::SLOTS;
-      if (!mbar_wait(bar(C::FULL + s), (it / C::SLOTS) & 1, abort_flag, p.status, site + C::FULL + s))
-        return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t d = tmem + ((i & 1) ? C::TM_S1 : 0u);
-        const uint64_t a = dk0 + static_cast<uint64_t>((s * C::TILE) >> 4);
-        for (int ks = 0; ks < n_ks; ++ks)
-          umma<F8>(d, a + static_cast<uint64_t>(((ks >> 2) * C::CHUNK + (ks & 3) * 32) >> 4),
-                   dq0 + static_cast<uint64_t>(ks * 2 * C::NQ), idesc_s, ks > 0 ? 1u : 0u);
-        umma_commit(bar(C::S_FULL + (i & 1)));
-        umma_commit(bar(C::EMPTY + s));
-      }
-      __syncwarp();
-      return true;
+    Ring<C::SLOTS> ring;
+    bool ok = true;
+    auto wait = [&](int id, uint32_t parity) {
+      ok = ok && warp_wait(bar(id), parity, abort_flag, p.status, site + id);
     };
-    bool ok = n > 0 && mbar_wait(bar(C::Q_FULL), 0, abort_flag, p.status, site + C::Q_FULL) && issue_s(0);
-    for (int i = 0; i < n && ok; ++i) {
-      if (i + 1 < n && !(ok = issue_s(i + 1))) break;
-      const int it = v_item(i), s = it % C::SLOTS;
-      ok = mbar_wait(bar(C::FULL + s), (it / C::SLOTS) & 1, abort_flag, p.status, site + C::FULL + s) &&
-           mbar_wait(bar(C::P_FULL), i & 1, abort_flag, p.status, site + C::P_FULL);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        for (int blk = 0; blk < blks; ++blk) {
-          const uint32_t d = tmem + C::TM_O + blk * C::NP;
-          const uint64_t a =
-              dv0 + static_cast<uint64_t>((s * C::TILE + blk * (F8 ? 1 : 2) * C::CHUNK) >> 4);
+    // scores of the next tile into S buffer `s_buf`; `q`: its unit's Q; `done`: the
+    // barrier to tell when the unit's last scores are done, or -1
+    auto issue_s = [&](uint32_t s_buf, uint64_t q, int done) {
 #pragma unroll
-          for (int ks = 0; ks < kKeys / KSTEP; ++ks)
-            umma<F8>(d, a + static_cast<uint64_t>((ks * KSTEP * 128) >> 4),
-                     dp0 + static_cast<uint64_t>((ks * KSTEP * 16) >> 4), idesc_o,
-                     (i > 0 || ks > 0) ? 1u : 0u);
+      for (int blk = 0; blk < C::BLKS; ++blk) {
+        if (blk >= blks) break;
+        wait(C::FULL + ring.slot, ring.phase);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + (s_buf ? C::TM_S1 : 0u);
+          const uint64_t a = dk0 + static_cast<uint64_t>((ring.slot * C::SLOT) >> 4);
+#pragma unroll
+          for (int x = 0; x < KS_BLK; ++x) {
+            const int ks = blk * KS_BLK + x;
+            if (ks < n_ks)
+              umma<F8>(d, a + static_cast<uint64_t>(((x >> 2) * C::CHUNK + (x & 3) * 32) >> 4),
+                       q + static_cast<uint64_t>(ks * 2 * C::NQ), idesc_s, ks > 0 ? 1u : 0u);
+          }
+          if (blk == blks - 1) umma_commit(bar(C::S_FULL + s_buf));
+          umma_commit(bar(C::EMPTY + ring.slot));
+          if (blk == blks - 1 && done >= 0) umma_commit(bar(done));
         }
-        umma_commit(bar(C::PV_DONE));
-        umma_commit(bar(C::EMPTY + s));
+        __syncwarp();
+        ring.advance();
       }
-      __syncwarp();
+    };
+    auto unit_q = [&](int k) { return dq0 + static_cast<uint64_t>(((k & 1) * C::Q_BYTES) >> 4); };
+    UnitIter it;
+    bool more = it.start(p, at, seq);
+    int k = 0;             // units
+    uint32_t t = 0;        // tiles
+    if (more) {
+      wait(C::Q_FULL, 0);
+      if (ok) issue_s(0, unit_q(0), it.count() == 1 ? C::Q_EMPTY : -1);
+    }
+    while (more && ok) {
+      const int n = it.count();
+      more = it.next(p, at, seq);
+      const int n_next = more ? it.count() : 0;
+      for (int i = 0; i < n && ok; ++i, ++t) {
+        // the next tile's scores, of this unit or the next
+        if (i + 1 < n) {
+          issue_s((t + 1) & 1, unit_q(k), i + 2 == n ? C::Q_EMPTY + (k & 1) : -1);
+        } else if (n_next > 0) {
+          wait(C::Q_FULL + ((k + 1) & 1), ((k + 1) >> 1) & 1);
+          if (ok) issue_s((t + 1) & 1, unit_q(k + 1), n_next == 1 ? C::Q_EMPTY + ((k + 1) & 1) : -1);
+        }
+        // (O is free once the last unit's epilogue has read it)
+        if (i == 0 && k > 0) wait(C::O_FREE, (k - 1) & 1);
+        wait(C::P_FULL, t & 1);
+#pragma unroll
+        for (int blk = 0; blk < C::BLKS; ++blk) {
+          if (blk >= blks) break;
+          wait(C::FULL + ring.slot, ring.phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t d = tmem + C::TM_O + blk * C::NP;
+            const uint64_t a = dv0 + static_cast<uint64_t>((ring.slot * C::SLOT) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < kKeys / KSTEP; ++ks)
+              umma<F8>(d, a + static_cast<uint64_t>((ks * KSTEP * 128) >> 4),
+                       dp0 + static_cast<uint64_t>((ks * KSTEP * 16) >> 4), idesc_o,
+                       (i > 0 || ks > 0) ? 1u : 0u);
+            if (blk == blks - 1) umma_commit(bar(C::PV_DONE));
+            umma_commit(bar(C::EMPTY + ring.slot));
+          }
+          __syncwarp();
+          ring.advance();
+        }
+      }
+      ++k;
     }
     // every tensor-core operation issued must be complete before TMEM is freed
     if (elect_one()) umma_commit(bar(C::DRAIN));
     __syncwarp();
     volatile int never = 0;
     mbar_wait(bar(C::DRAIN), 0, &never, p.status, site + C::DRAIN);
-  } else if (works) {
-    // ---- softmax: thread = key
-    const int site = kRoleRowsSoftmax * 64;
-    // per-row values (row r of the block: drafted token and query head)
-    if (tid < NR) {
-      int out = -1, t = -1;
-      if (tid < rows_here) {
-        const int gr = rb * NR + tid;
-        t = gr / p.G;
-        out = (b * p.T + t) * p.H + hk * p.G + gr % p.G;
-        if (t >= w.live) t = -1;
-      }
-      row_out[tid] = out;
-      row_t[tid] = t;
-      row_ref[tid] = -INFINITY;
-    }
-    // scales of the keys of four tiles, requested four tiles ahead
-    int raw_k[4] = {}, raw_v[4] = {};
-    uint32_t cur_k = 0, cur_v = 0;
-    const long long s_row = (static_cast<long long>(b) * p.H_kv + hk) * p.Lk;
-    auto request_scales = [&](int i0) {
+  } else {
+    if (F8 && warp == kQWarp + 1) {
+      // ---- 8-bit: the scales of the tiles to come, four keys per lane
+      const int site = kRoleRowsQ * 64;
+      uint16_t* ring = reinterpret_cast<uint16_t*>(smem + C::OFF_SCALES);
+      UnitIter it;
+      int t = 0;
+      bool ok = true;
+      for (bool more = it.start(p, at, seq); more && ok; more = it.next(p, at, seq)) {
+        const int end = seq_end(p, it.s);
+        const long long row = (static_cast<long long>(it.b) * p.H_kv + unit_hk(it)) * p.Lk;
+        // (up to four tiles' loads in flight)
+        for (int x = it.t0; x < it.t1 && ok; x += 4) {
+          const int m = min(4, it.t1 - x);
+          uint32_t kv[4][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int key = k_begin + (i0 + u) * kKeys + tid;
-        raw_k[u] = raw_v[u] = 127;
-        if (key < k_end) {
-          raw_k[u] = __ldg(p.k_scale + s_row + key);
-          raw_v[u] = __ldg(p.v_scale + s_row + key);
-        }
-      }
-    };
-    if constexpr (F8) request_scales(0);
-    named_barrier(1, 128);
-    // Q into shared memory: eight threads per row
-    if (n > 0) {
-      const int sub = tid & 7;
-      for (int r = tid >> 3; r < NR; r += 16) {
-        const bool real = r < rows_here;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                          static_cast<long long>(real ? row_out[r] : 0) * p.d);
-        if constexpr (F8) {
-          constexpr int PER = W / 128;  // 16-element pieces of the row per thread
-          uint4 v[PER][2];
-          float amax = 0.f;
+          for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int u = 0; u < PER; ++u) {
-            const int c = sub + 8 * u;  // elements 16c .. 16c + 15
-            v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
-            if (real && 16 * c < p.d) {
-              v[u][0] = __ldg(src + 2 * c);
-              v[u][1] = __ldg(src + 2 * c + 1);
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t q4[4] = {v[u][y].x, v[u][y].y, v[u][y].z, v[u][y].w};
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q4[z])), fabsf(bf16_hi(q4[z]))));
-            }
-          }
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // q 2^-e with the largest magnitude in [128, 256)
-          const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7, -100);
-          const float inv = pow2i(-e);
-          if (sub == 0) row_factor[r] = pow2i(e) * p.scale_log2;
-#pragma unroll
-          for (int u = 0; u < PER; ++u) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t q4[4] = {v[u][y].x, v[u][y].y, v[u][y].z, v[u][y].w};
-              uint32_t a[4], c2[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const float x0 = bf16_lo(q4[z]) * inv, x1 = bf16_hi(q4[z]) * inv;
-                a[z] = pack_e4m3x2(x0, x1);
-                const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[z]));
-                c2[z] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
+            for (int z = 0; z < 4; ++z) {
+              const int key = (x + y) * kKeys + 32 * z + lane;
+              uint32_t a = 127, c = 127;
+              if (y < m && key < end) {
+                a = __ldg(p.k_scale + row + key);
+                c = __ldg(p.v_scale + row + key);
               }
-              hi[2 * y] = a[0] | (a[1] << 16);
-              hi[2 * y + 1] = a[2] | (a[3] << 16);
-              lo[2 * y] = c2[0] | (c2[1] << 16);
-              lo[2 * y + 1] = c2[2] | (c2[3] << 16);
+              kv[y][z] = a | (c << 8);
             }
-            const uint32_t at = sQ + (sub + 8 * u) * (C::NQ * 16) + r * 16;
-            st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(at + NR * 16, lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
 #pragma unroll
-          for (int u = 0; u < W / 64; ++u) {
-            const int c = sub + 8 * u;  // elements 8c .. 8c + 7
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (real && 8 * c < p.d) v = __ldg(src + c);
-            st_shared_v4(sQ + c * (C::NQ * 16) + r * 16, v.x, v.y, v.z, v.w);
-          }
-        }
-      }
-    }
-    fence_proxy_async_smem();
-    mbar_arrive(bar(C::Q_FULL));
-    named_barrier(1, 128);  // row_factor
-
-    constexpr int GROUPS = NR / 16;
-    float l[NR];
+          for (int y = 0; y < 4; ++y) {
+            if (y >= m || !ok) break;
+            const int slot = t % kScaleTiles;
+            ok = t < kScaleTiles || warp_wait(bar(C::SC_EMPTY + slot), ((t / kScaleTiles) - 1) & 1, abort_flag,
+                                              p.status, site + C::SC_EMPTY + slot);
+            if (!ok) break;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) l[r] = 0.f;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int key = k_begin + i * kKeys + tid;
-      float kf = 1.f, ev = 0.f, vinv = 1.f;
-      if constexpr (F8) {
-        if ((i & 3) == 0) {
-          cur_k = raw_k[0] | (raw_k[1] << 8) | (raw_k[2] << 16) | (raw_k[3] << 24);
-          cur_v = raw_v[0] | (raw_v[1] << 8) | (raw_v[2] << 16) | (raw_v[3] << 24);
-          if (i + 4 < n) request_scales(i + 4);
-        }
-        const uint32_t kb = (cur_k >> (8 * (i & 3))) & 255u;
-        const uint32_t vb = min((cur_v >> (8 * (i & 3))) & 255u, 254u);
-        kf = __uint_as_float(kb << 23);
-        ev = static_cast<float>(static_cast<int>(vb) - 127);
-        vinv = __uint_as_float((254u - vb) << 23);
-      }
-      // which rows see this key (a tile inside the prefix: all)
-      const bool masked = k_begin + (i + 1) * kKeys > min(w.n, k_end);
-      uint64_t sees = ~0ull;
-      if (masked) {
-        if (key >= k_end) {
-          sees = 0;
-        } else if (key >= w.n) {
-          const int j = key - w.n;
-          sees = 0;
-          for (int r = 0; r < rows_here; ++r) {
-            const int t = row_t[r];
-            if (t < 0) continue;
-            const bool on =
-                p.tree_mask
-                    ? (__ldg(p.tree_mask + (static_cast<long long>(b) * p.T + t) * p.words + (j >> 6)) >>
-                       (j & 63)) & 1
-                    : j <= t;
-            if (on) sees |= 1ull << r;
+            for (int z = 0; z < 4; ++z) ring[slot * kKeys + 32 * z + lane] = static_cast<uint16_t>(kv[y][z]);
+            mbar_arrive(bar(C::SC_FULL + slot));
+            ++t;
           }
         }
       }
-      ok = ok && mbar_wait(bar(C::S_FULL + (i & 1)), (i >> 1) & 1, abort_flag, p.status,
-                           site + C::S_FULL + (i & 1));
-      tc_fence_after();
-      // this key's scores
-      float s[NR];
-      bool over = false;
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g) {
-        if (g * 16 >= rows_here) continue;
-        uint32_t c1[16];
-        const uint32_t at = t_lane + ((i & 1) ? C::TM_S1 : 0u) + g * 16;
-        tmem_ld16(at, c1);
-        if constexpr (F8) {
-          uint32_t c2[16];
-          tmem_ld16(at + NR, c2);
-          tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            s[g * 16 + r] = fmaf(fmaf(__uint_as_float(c2[r]), 1.f / 32.f, __uint_as_float(c1[r])),
-                                 kf * row_factor[g * 16 + r], ev);
-        } else {
-          tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[g * 16 + r] = __uint_as_float(c1[r]) * p.scale_log2;
+    } else {
+    // ---- the next units' Q, output rows and mask words
+    const int site = kRoleRowsQ * 64;
+    constexpr int QT = C::Q_THREADS, RP = QT / 8;  // eight threads per row
+    constexpr int PER = W / 64;                    // 16-byte pieces of a row per thread
+    constexpr int MOST = PER > 2 ? 2 : 4;
+    constexpr int BATCH = NR / RP < MOST ? NR / RP : MOST;  // rows per thread in flight
+    const int qt = tid - 32 * kQWarp;
+    const int sub = qt & 7;
+    UnitIter it;
+    int k = 0;  // units with keys
+    for (bool more = it.start<true>(p, at, seq); more; more = it.next<true>(p, at, seq)) {
+      const int buf = k & 1;
+      const uint32_t sQ = s_base + C::OFF_Q + buf * C::Q_BYTES;
+      const int hk = unit_hk(it), rb = unit_rb(it);
+      // output row of row r of the block (-1 past the last), t: its drafted token
+      auto out_row = [&](int r, int* t) {
+        const int gr = rb * NR + r;
+        *t = -1;
+        if (gr >= n_rows) return -1;
+        *t = p.G == 1 ? gr : gr / p.G;
+        return (it.b * p.T + *t) * p.H + hk * p.G + (gr - *t * p.G);
+      };
+      if (it.tiles == 0) {
+        // no key at all: output 0, log-sum-exp -inf
+        for (int r = qt >> 3; r < NR; r += RP) {
+          int t;
+          const int out = out_row(r, &t);
+          if (out < 0) break;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d);
+          for (int x = sub; 8 * x < p.d; x += 8) dst[x] = make_uint4(0, 0, 0, 0);
+          if (p.lse && sub == 0) p.lse[(it.b * p.H + out % p.H) * p.T + t] = -INFINITY;
         }
-        if (masked) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (!((sees >> (g * 16 + r)) & 1)) s[g * 16 + r] = -INFINITY;
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) over |= s[g * 16 + r] > row_ref[g * 16 + r] + C::SLACK;
+        continue;
       }
-      tc_fence_before();
-      if (any_of_128(over)) {
-        // move the references to this tile's maxima and rescale
+      // (the first rows are requested before the buffer is free)
+      for (int rr = 0; rr < NR; rr += RP * BATCH) {
+        uint4 v[BATCH][PER];
+        int t[BATCH], out[BATCH];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          if ((r & ~15) >= rows_here) continue;
-          float m = s[r];
+        for (int y = 0; y < BATCH; ++y) {
+          out[y] = out_row(rr + y * RP + (qt >> 3), &t[y]);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                            static_cast<long long>(max(out[y], 0)) * p.d);
 #pragma unroll
-          for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (lane == 0) red[warp * NR + r] = m;
-        }
-        named_barrier(1, 128);
-        // (rows past the block's own, up to the next 16, move along: their
-        // scores are 0, not -inf)
-        if (tid < NR && (tid & ~15) < rows_here) {
-          const float old = row_ref[tid];
-          const float m = fmaxf(fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid])), old);
-          row_alpha[tid] = m == -INFINITY ? 1.f : ex2_approx(old - m);
-          row_ref[tid] = m;
-        }
-        named_barrier(1, 128);
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-          if ((r & ~15) < rows_here) l[r] *= row_alpha[r];
-        if (i > 0) {
-          ok = ok && mbar_wait(bar(C::PV_DONE), (i - 1) & 1, abort_flag, p.status, site + C::PV_DONE);
-          tc_fence_after();
-          for (int c = 0; c < C::BLKS * C::NP; c += 16) {
-            if (c % NR >= rows_here) continue;
-            uint32_t o[16];
-            tmem_ld16(t_lane + C::TM_O + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * row_alpha[c % NR + r]);
-            tmem_st16(t_lane + C::TM_O + c, o);
+          for (int z = 0; z < PER; ++z) {
+            // 8-bit: 16 elements to a thread, in two pieces; bf16: 8
+            const int piece = F8 ? 2 * (sub + 8 * (z >> 1)) + (z & 1) : sub + 8 * z;
+            v[y][z] = make_uint4(0, 0, 0, 0);
+            if (out[y] >= 0 && 8 * piece < p.d) v[y][z] = __ldg(src + piece);
           }
-          tmem_st_wait();
-          tc_fence_before();
         }
-      }
-      // P and the V tile's rows past the last key: the previous product must
-      // have read P
-      if (i > 0) ok = ok && mbar_wait(bar(C::PV_DONE), (i - 1) & 1, abort_flag, p.status, site + C::PV_DONE);
+        if (rr == 0 && k >= 2 && !warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, p.status,
+                                            site + C::Q_EMPTY + buf)) {
+          more = false;
+          break;
+        }
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) {
-        if (g * 16 >= rows_here) continue;
-        uint32_t w1[8], w2[8], w3[8];
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          const int a = g * 16 + r;
-          const float m0 = row_ref[a], m1 = row_ref[a + 1];
-          const float p0 = ex2_approx(s[a] - (m0 == -INFINITY ? 0.f : m0 - C::LIFT));
-          const float p1 = ex2_approx(s[a + 1] - (m1 == -INFINITY ? 0.f : m1 - C::LIFT));
+        for (int y = 0; y < BATCH; ++y) {
+          const int r = rr + y * RP + (qt >> 3);
+          const bool live = t[y] >= 0 && t[y] < it.s.y;
+          if (sub == 0) {
+            row_out(buf)[r] = out[y];
+            row_lse(buf)[r] = out[y] < 0 ? 0 : (it.b * p.H + out[y] % p.H) * p.T + t[y];
+            row_live(buf)[r] = live;
+          }
+          if (sub < kMaskWords) {
+            // (a chain's words: bits 0 .. t)
+            uint64_t word = 0;
+            if (live && p.tree_mask) {
+              if (sub < p.words)
+                word = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t[y]) * p.words + sub);
+            } else if (live) {
+              const int bits = t[y] + 1 - 64 * sub;
+              word = bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
+            }
+            row_mask(buf)[r * kMaskWords + sub] = word;
+          }
           if constexpr (F8) {
-            l[a] = fmaf(p0, vinv, l[a]);
-            l[a + 1] = fmaf(p1, vinv, l[a + 1]);
-            const uint32_t h = pack_half2(p0, p1);
-            const uint32_t b1 = half2_to_e5m2x2(h);
-            const uint32_t h2 = half2_sub(h, e5m2x2_to_half2(b1));
-            const uint32_t b2 = half2_to_e5m2x2(h2);
-            const uint32_t b3 = half2_to_e5m2x2(half2_sub(h2, e5m2x2_to_half2(b2)));
-            const int x4 = r >> 2;
-            if ((r & 2) == 0) {
-              w1[x4] = b1;
-              w2[x4] = b2;
-              w3[x4] = b3;
-            } else {
-              w1[x4] |= b1 << 16;
-              w2[x4] |= b2 << 16;
-              w3[x4] |= b3 << 16;
+            float amax = 0.f;
+#pragma unroll
+            for (int z = 0; z < PER; ++z) {
+              const uint32_t q4[4] = {v[y][z].x, v[y][z].y, v[y][z].z, v[y][z].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q4[e])), fabsf(bf16_hi(q4[e]))));
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // q 2^-e with the largest magnitude in [128, 256)
+            const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7, -100);
+            const float inv = pow2i(-e);
+            if (sub == 0) row_factor(buf)[r] = pow2i(e) * p.scale_log2;
+#pragma unroll
+            for (int u = 0; u < PER / 2; ++u) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint4 w4 = v[y][2 * u + z];
+                const uint32_t q4[4] = {w4.x, w4.y, w4.z, w4.w};
+                uint32_t a[4], c2[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float x0 = bf16_lo(q4[x]) * inv, x1 = bf16_hi(q4[x]) * inv;
+                  a[x] = pack_e4m3x2(x0, x1);
+                  const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[x]));
+                  c2[x] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
+                }
+                hi[2 * z] = a[0] | (a[1] << 16);
+                hi[2 * z + 1] = a[2] | (a[3] << 16);
+                lo[2 * z] = c2[0] | (c2[1] << 16);
+                lo[2 * z + 1] = c2[2] | (c2[3] << 16);
+              }
+              const uint32_t to = sQ + (sub + 8 * u) * (C::NQ * 16) + r * 16;
+              st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
+              st_shared_v4(to + NR * 16, lo[0], lo[1], lo[2], lo[3]);
             }
           } else {
-            l[a] += p0;
-            l[a + 1] += p1;
-            w1[r >> 1] = pack_bf16x2(p0, p1);
-            w2[r >> 1] = pack_bf16x2(p0 - bf16_lo(w1[r >> 1]), p1 - bf16_hi(w1[r >> 1]));
+#pragma unroll
+            for (int z = 0; z < PER; ++z)
+              st_shared_v4(sQ + (sub + 8 * z) * (C::NQ * 16) + r * 16, v[y][z].x, v[y][z].y, v[y][z].z,
+                           v[y][z].w);
           }
         }
-        // 16-byte units [column of units][key]
-        if constexpr (F8) {
-          const uint32_t at = sP + g * (kKeys * 16) + tid * 16;
-          st_shared_v4(at, w1[0], w1[1], w1[2], w1[3]);
-          st_shared_v4(at + GROUPS * (kKeys * 16), w2[0], w2[1], w2[2], w2[3]);
-          st_shared_v4(at + 2 * GROUPS * (kKeys * 16), w3[0], w3[1], w3[2], w3[3]);
-        } else {
-          const uint32_t at = sP + 2 * g * (kKeys * 16) + tid * 16;
-          st_shared_v4(at, w1[0], w1[1], w1[2], w1[3]);
-          st_shared_v4(at + kKeys * 16, w1[4], w1[5], w1[6], w1[7]);
-          st_shared_v4(at + 2 * GROUPS * (kKeys * 16), w2[0], w2[1], w2[2], w2[3]);
-          st_shared_v4(at + (2 * GROUPS + 1) * (kKeys * 16), w2[4], w2[5], w2[6], w2[7]);
-        }
       }
-      if (i == n - 1 && k_begin + n * kKeys > k_end) {
-        // rows past the last key may hold anything (0 * NaN would be NaN)
-        const int it = v_item(i), sl = it % C::SLOTS;
-        ok = ok && mbar_wait(bar(C::FULL + sl), (it / C::SLOTS) & 1, abort_flag, p.status, site + C::FULL + sl);
-        if (key >= k_end) {
-#pragma unroll
-          for (int c = 0; c < C::TILE / C::CHUNK; ++c)
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              st_shared_v4(s_base + sl * C::TILE + c * C::CHUNK + tid * 128 + u * 16, 0, 0, 0, 0);
-        }
-      }
+      if (!more) break;
       fence_proxy_async_smem();
-      mbar_arrive(bar(C::P_FULL));
+      mbar_arrive(bar(C::Q_FULL + buf));
+      ++k;
     }
+    }
+  }
+  } else {
+    if constexpr (C::SPLIT_REGS) regs_increase<C::REGS_SOFT>();
+    // ---- softmax: thread = key; warpgroup wg has rows r0 .. r0 + RPT - 1
+    const int site = kRoleRowsSoftmax * 64;
+    constexpr int RPT = C::RPT, GW = C::GW, GROUPS = C::GROUPS;
+    const int wg = warp >> 2, r0 = wg * RPT, kt = tid & 127, w4 = warp & 3;
+    const uint32_t nbar = 1 + wg;  // this warpgroup's named barrier
+    const int group = static_cast<int>(blockIdx.x) / p.lanes;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+    bool ok = true;
+    auto wait = [&](int id, uint32_t parity) {
+      ok = ok && mbar_wait(bar(id), parity, abort_flag, p.status, site + id);
+    };
+    if (kt < RPT) row_ref[r0 + kt] = 0.f;
+    named_barrier(nbar, 128);
+    UnitIter it;
+    int k = 0, t = 0;  // units, tiles
+    for (bool more = it.start(p, at, seq); more; more = it.next(p, at, seq), ++k) {
+      const int buf = k & 1, n = it.count();
+      const int rows_here = min(NR, n_rows - unit_rb(it) * NR) - r0;  // this warpgroup's (may be <= 0)
+      const int k_end = seq_end(p, it.s);
+      float l[RPT];
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) l[r] = 0.f;
+      wait(C::Q_FULL + buf, (k >> 1) & 1);
+      const float* factor = row_factor(buf) + r0;
+      float* ref = row_ref + r0;
+      float* shift = row_shift + r0;  // (in the epilogue: 1 / sum)
+      bool forced = true, seen = false;  // (seen: of row kt)
+      for (int i = 0; i < n; ++i, ++t) {
+        const int key = (it.t0 + i) * kKeys + kt;
+        float kf = 1.f, ev = 0.f, vinv = 1.f;
+        if constexpr (F8) {
+          const int slot = t % kScaleTiles;
+          wait(C::SC_FULL + slot, (t / kScaleTiles) & 1);
+          const uint32_t kv = reinterpret_cast<const uint16_t*>(smem + C::OFF_SCALES)[slot * kKeys + kt];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::SC_EMPTY + slot));
+          const uint32_t kb = kv & 255u, vb = min(kv >> 8, 254u);
+          kf = __uint_as_float(kb << 23);
+          ev = static_cast<float>(static_cast<int>(vb) - 127);
+          vinv = __uint_as_float((254u - vb) << 23);
+        }
+        // which of this warpgroup's rows see the key (a tile inside the prefix: all)
+        const bool masked = (it.t0 + i + 1) * kKeys > it.s.x;
+        uint32_t sees = ~0u;
+        if (masked && key >= it.s.x) {
+          sees = 0;
+          if (key < k_end) {
+            const int j = key - it.s.x;
+            const uint64_t* words = row_mask(buf) + r0 * kMaskWords + (j >> 6);
+#pragma unroll 8
+            for (int r = 0; r < RPT; ++r)
+              sees |= static_cast<uint32_t>((words[r * kMaskWords] >> (j & 63)) & 1) << r;
+          }
+        }
+        wait(C::S_FULL + (t & 1), (t >> 1) & 1);
+        tc_fence_after();
+        const uint32_t s_at = t_lane + ((t & 1) ? C::TM_S1 : 0u) + r0;
+        // the rows' scores of this key (log2 units, v's exponent added) less their
+        // references
+        float x[RPT];
+        {
+          // (all columns requested at once, but for 32 rows of two pieces each)
+          constexpr int LG = F8 ? 1 : GROUPS;
+#pragma unroll
+          for (int g0 = 0; g0 < GROUPS; g0 += LG) {
+          if (g0 * GW >= rows_here) continue;
+          uint32_t c1[LG][GW], c2[F8 ? LG : 1][GW];
+#pragma unroll
+          for (int g = 0; g < LG; ++g) {
+            if ((g0 + g) * GW >= rows_here) continue;
+            tmem_ld_cols<GW>(s_at + (g0 + g) * GW, c1[g]);
+            if constexpr (F8) tmem_ld_cols<GW>(s_at + NR + (g0 + g) * GW, c2[g]);
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int gg = 0; gg < LG; ++gg) {
+            const int g = g0 + gg;
+            if (g * GW >= rows_here) continue;
+#pragma unroll
+            for (int r = 0; r < GW; r += 4) {
+              float* y = x + g * GW + r;
+              const float4 m = *reinterpret_cast<const float4*>(ref + g * GW + r);
+              const uint32_t* a = c1[gg] + r;
+              if constexpr (F8) {
+                const float4 f = *reinterpret_cast<const float4*>(factor + g * GW + r);
+                const uint32_t* c = c2[gg] + r;
+                float b[4], h[4];
+                fma2(b[0], b[1], __uint_as_float(c[0]), __uint_as_float(c[1]), 1.f / 32.f, 1.f / 32.f,
+                     __uint_as_float(a[0]), __uint_as_float(a[1]));
+                fma2(b[2], b[3], __uint_as_float(c[2]), __uint_as_float(c[3]), 1.f / 32.f, 1.f / 32.f,
+                     __uint_as_float(a[2]), __uint_as_float(a[3]));
+                mul2(h[0], h[1], f.x, f.y, kf, kf);
+                mul2(h[2], h[3], f.z, f.w, kf, kf);
+                fma2(y[0], y[1], b[0], b[1], h[0], h[1], ev - m.x, ev - m.y);
+                fma2(y[2], y[3], b[2], b[3], h[2], h[3], ev - m.z, ev - m.w);
+              } else {
+                fma2(y[0], y[1], __uint_as_float(a[0]), __uint_as_float(a[1]), p.scale_log2, p.scale_log2, -m.x,
+                     -m.y);
+                fma2(y[2], y[3], __uint_as_float(a[2]), __uint_as_float(a[3]), p.scale_log2, p.scale_log2, -m.z,
+                     -m.w);
+              }
+            }
+          }
+          }
+          if (masked) {
+#pragma unroll
+            for (int r = 0; r < RPT; ++r)
+              if (!((sees >> r) & 1)) x[r] = -INFINITY;
+          }
+        }
+        bool move = forced;
+        if (!forced) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < RPT; r += 2)
+            if (r / GW * GW < rows_here) top = fmax3(top, x[r], x[r + 1]);
+          move = any_of_128(nbar, top > C::SLACK + C::LIFT);
+        }
+        if (move) {
+          // move the references to this tile's maxima (always in a unit's first
+          // tile, and while a row has seen no key) and rescale
+#pragma unroll
+          for (int r = 0; r < RPT; ++r) {
+            if (r / GW * GW >= rows_here) continue;
+            const float m = warp_max(x[r]);
+            if (lane == r) red[(r0 + r) * 4 + w4] = m;
+          }
+          named_barrier(nbar, 128);
+          bool unseen = false;
+          if (kt < RPT && kt / GW * GW < rows_here) {
+            const float4 m4 = *reinterpret_cast<const float4*>(red + (r0 + kt) * 4);
+            const float m = fmaxf(fmax3(m4.x, m4.y, m4.z), m4.w);
+            // (a row's first key sets its reference, which was 0, up or down)
+            const float by = m == -INFINITY ? 0.f : (seen ? fmaxf(m - C::LIFT, 0.f) : m - C::LIFT);
+            seen = seen || m > -INFINITY;
+            ref[kt] += by;
+            shift[kt] = by;
+            unseen = !seen && kt < rows_here && row_live(buf)[r0 + kt];
+          }
+          forced = any_of_128(nbar, unseen);
+#pragma unroll
+          for (int r = 0; r < RPT; r += 4) {
+            if (r / GW * GW >= rows_here) continue;
+            const float4 by = *reinterpret_cast<const float4*>(shift + r);
+            x[r] -= by.x;
+            x[r + 1] -= by.y;
+            x[r + 2] -= by.z;
+            x[r + 3] -= by.w;
+            if (i > 0) {
+              l[r] *= ex2_approx(-by.x);
+              l[r + 1] *= ex2_approx(-by.y);
+              l[r + 2] *= ex2_approx(-by.z);
+              l[r + 3] *= ex2_approx(-by.w);
+            }
+          }
+          if (i > 0) {
+            wait(C::PV_DONE, (t - 1) & 1);
+            tc_fence_after();
+            for (int c = 0; c < C::BLKS * C::PP; ++c)
+              for (int g = 0; g < GROUPS; ++g) {
+                if (g * GW >= rows_here) continue;
+                const uint32_t o_at =
+                    t_lane + C::TM_O + (c / C::PP) * C::NP + (c % C::PP) * NR + r0 + g * GW;
+                uint32_t o[GW];
+                tmem_ld_cols<GW>(o_at, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int r = 0; r < GW; ++r)
+                  o[r] = __float_as_uint(__uint_as_float(o[r]) * ex2_approx(-shift[g * GW + r]));
+                tmem_st_cols<GW>(o_at, o);
+              }
+            tmem_st_wait();
+          }
+        }
+        tc_fence_before();
+        // weights; the previous product must have read P
+        if (t > 0) wait(C::PV_DONE, (t - 1) & 1);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          if (g * GW >= rows_here) continue;
+          uint32_t w1[GW / 2], w2[GW / 2], w3[GW / 4];  // (8-bit: the first GW / 4 of each)
+#pragma unroll
+          for (int r = 0; r < GW; r += 2) {
+            const int a = g * GW + r;
+            const float p0 = ex2_approx(x[a]), p1 = ex2_approx(x[a + 1]);
+            if constexpr (F8) {
+              fma2(l[a], l[a + 1], p0, p1, vinv, vinv, l[a], l[a + 1]);
+              const uint32_t h = pack_half2(p0, p1);
+              const uint32_t b1 = half2_to_e5m2x2(h);
+              const uint32_t h2 = half2_sub(h, e5m2x2_to_half2(b1));
+              const uint32_t b2 = half2_to_e5m2x2(h2);
+              const uint32_t b3 = half2_to_e5m2x2(half2_sub(h2, e5m2x2_to_half2(b2)));
+              const int x4 = r >> 2;
+              if ((r & 2) == 0) {
+                w1[x4] = b1;
+                w2[x4] = b2;
+                w3[x4] = b3;
+              } else {
+                w1[x4] |= b1 << 16;
+                w2[x4] |= b2 << 16;
+                w3[x4] |= b3 << 16;
+              }
+            } else {
+              add2(l[a], l[a + 1], l[a], l[a + 1], p0, p1);
+              // the first piece is cut, not rounded: its bits are p's own
+              const uint32_t u0 = __float_as_uint(p0) & 0xffff0000u, u1 = __float_as_uint(p1) & 0xffff0000u;
+              w1[r >> 1] = __byte_perm(u0, u1, 0x7632);
+              w2[r >> 1] = pack_bf16x2(p0 - __uint_as_float(u0), p1 - __uint_as_float(u1));
+            }
+          }
+          // 16-byte units [column of units][key]: 16 (8-bit) or 8 rows of a piece
+          constexpr int COL = kKeys * 16;
+          if constexpr (F8 && GW == 8) {
+            // two pieces to a unit; nothing reads the second half of the last
+            const uint32_t to = sP + kt * 16;
+            st_shared_v4(to, w1[0], w1[1], w2[0], w2[1]);
+            st_shared_v4(to + COL, w3[0], w3[1], 0, 0);
+          } else if constexpr (F8) {
+            const uint32_t to = sP + (r0 / 16 + g) * COL + kt * 16;
+            st_shared_v4(to, w1[0], w1[1], w1[2], w1[3]);
+            st_shared_v4(to + (NR / 16) * COL, w2[0], w2[1], w2[2], w2[3]);
+            st_shared_v4(to + 2 * (NR / 16) * COL, w3[0], w3[1], w3[2], w3[3]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < GW / 8; ++h) {
+              const uint32_t to = sP + ((r0 + g * GW) / 8 + h) * COL + kt * 16;
+              st_shared_v4(to, w1[4 * h], w1[4 * h + 1], w1[4 * h + 2], w1[4 * h + 3]);
+              st_shared_v4(to + (NR / 8) * COL, w2[4 * h], w2[4 * h + 1], w2[4 * h + 2], w2[4 * h + 3]);
+            }
+          }
+        }
+        if (wg == 0 && (it.t0 + i + 1) * kKeys > k_end) {
+          // a ragged last tile: the V rows past the last key may hold anything
+          // (0 * NaN would be NaN)
+          // (before V(t) in the ring: K(0) .. K(t), K(t + 1) if there is one,
+          // V(0) .. V(t - 1))
+          UnitIter next = it;
+          const int before = 2 * t + 1 + (next.next(p, at, seq) ? 1 : 0);
+          for (int blk = 0; blk < blks; ++blk) {
+            const int item = before * blks + blk, sl = item % C::SLOTS;
+            wait(C::FULL + sl, (item / C::SLOTS) & 1);
+            if (key >= k_end) {
+#pragma unroll
+              for (int c = 0; c < C::SLOT / C::CHUNK; ++c)
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  st_shared_v4(s_base + sl * C::SLOT + c * C::CHUNK + kt * 128 + u * 16, 0, 0, 0, 0);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::P_FULL));
+      }
 
-    // ---- epilogue: sums over the keys, then O
-    if (n > 0) {
-      ok = ok && mbar_wait(bar(C::PV_DONE), (n - 1) & 1, abort_flag, p.status, site + C::PV_DONE);
+      // ---- epilogue: sums over the keys, then O
+      {
+        // (the lanes of a row's group all hold its sum)
+        const float y = warp_sums<RPT>(l, lane);
+        if (lane % (32 / RPT) == 0) red[(r0 + lane / (32 / RPT)) * 4 + w4] = y;
+      }
+      wait(C::PV_DONE, (t - 1) & 1);
       tc_fence_after();
-    }
-    if (*abort_flag) ok = false;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      if ((r & ~15) >= rows_here) continue;
-      float t = l[r];
-#pragma unroll
-      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (lane == 0) red[warp * NR + r] = t;
-    }
-    named_barrier(1, 128);
-    const bool whole = w.active == 1;  // no other split: this is the result
-    const long long total_rows = static_cast<long long>(p.B) * p.T * p.H;
-    if (tid < rows_here) {
-      float L = red[tid] + red[NR + tid] + red[2 * NR + tid] + red[3 * NR + tid];
-      float m = row_ref[tid] - C::LIFT;
-      if (row_t[tid] < 0 || !ok) {  // an empty row (or a CTA that gave up: an empty partial)
-        L = 0.f;
-        m = -INFINITY;
-      }
-      row_alpha[tid] = L > 0.f ? (whole ? 1.f / L : 1.f) : 0.f;
-      if (whole) {
-        if (p.lse) {
-          const int bt = row_out[tid] / p.H, h = row_out[tid] % p.H;
-          p.lse[(static_cast<long long>(b) * p.H + h) * p.T + (bt - b * p.T)] =
-              L > 0.f ? (m + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+      const bool good = ok && *abort_flag == 0;
+      named_barrier(nbar, 128);
+      const bool whole = it.whole();
+      // the share's partial: the second where the sequence starts in it, else the first
+      const long long part =
+          (static_cast<long long>(group * 2 + (it.t0 == 0 ? 1 : 0)) * p.units + it.u) * NR + r0;
+      if (kt < rows_here && kt < RPT) {
+        const float4 l4 = *reinterpret_cast<const float4*>(red + (r0 + kt) * 4);
+        float L = l4.x + l4.y + l4.z + l4.w;
+        float m = ref[kt];
+        if (!row_live(buf)[r0 + kt] || !good) {  // an empty row (or a CTA that gave up)
+          L = 0.f;
+          m = -INFINITY;
         }
-      } else {
-        p.part_m[split * total_rows + row_out[tid]] = L > 0.f ? m : -INFINITY;
-        p.part_l[split * total_rows + row_out[tid]] = L;
+        shift[kt] = L > 0.f ? (whole ? 1.f / L : 1.f) : 0.f;
+        if (!whole) {
+          p.part_m[part + kt] = L > 0.f ? m : -INFINITY;
+          p.part_l[part + kt] = L;
+        } else if (p.lse) {
+          p.lse[row_lse(buf)[r0 + kt]] = L > 0.f ? (m + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+        }
       }
-    }
-    named_barrier(1, 128);
-    const int f0 = C::M_O == 64 ? warp * 16 + lane : warp * 32 + lane;
-    const bool holds = C::M_O == 128 || lane < 16;
-    for (int blk = 0; blk < C::BLKS; ++blk) {
-      if (blk * 128 >= p.d) continue;
-      const int f = blk * 128 + f0;
+      if (kt < RPT) ref[kt] = 0.f;  // (for the next unit)
+      named_barrier(nbar, 128);
+      const int f0 = C::M_O == 64 ? w4 * 16 + lane : kt;
+      const bool holds = C::M_O == 128 || lane < 16;
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) {
-        if (g * 16 >= rows_here) continue;
-        float o[16];
+      for (int blk = 0; blk < C::BLKS; ++blk) {
+        if (blk * 128 >= p.d) continue;
+        const int f = blk * 128 + f0;
+        const bool stores = holds && f < p.d;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[r] = 0.f;
-        if (n > 0) {
+        for (int g = 0; g < GROUPS; ++g) {
+          if (g * GW >= rows_here) continue;
+          float o[GW];
+          uint32_t y[C::PP][GW];
 #pragma unroll
-          for (int piece = C::PP - 1; piece >= 0; --piece) {
-            uint32_t t[16];
-            tmem_ld16(t_lane + C::TM_O + blk * C::NP + piece * NR + g * 16, t);
-            tmem_ld_wait();
+          for (int piece = 0; piece < C::PP; ++piece)
+            tmem_ld_cols<GW>(t_lane + C::TM_O + blk * C::NP + piece * NR + r0 + g * GW, y[piece]);
+          tmem_ld_wait();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] += __uint_as_float(t[r]);
+          for (int r = 0; r < GW; ++r) {
+            o[r] = __uint_as_float(y[C::PP - 1][r]);
+#pragma unroll
+            for (int piece = C::PP - 2; piece >= 0; --piece) o[r] += __uint_as_float(y[piece][r]);
+          }
+          if (!stores) continue;
+          const int rows = min(GW, rows_here - g * GW);
+          if (whole) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + f;
+            const int* outs = row_out(buf) + r0 + g * GW;
+#pragma unroll
+            for (int r = 0; r < GW; ++r) {
+              if (r >= rows) break;
+              const float a = shift[g * GW + r];
+              out[static_cast<long long>(outs[r]) * p.d] = __float2bfloat16_rn(a > 0.f ? o[r] * a : 0.f);
+            }
+          } else {
+            float* out = p.part_o + (part + g * GW) * W + f;
+#pragma unroll
+            for (int r = 0; r < GW; ++r) {
+              if (r >= rows) break;
+              out[r * W] = shift[g * GW + r] > 0.f ? o[r] : 0.f;
+            }
           }
         }
-        if (holds && f < p.d) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int row = g * 16 + r;
-            if (row >= rows_here) break;
-            const float a = row_alpha[row];
-            const float v = a > 0.f ? o[r] * a : 0.f;
-            const long long at = row_out[row];
-            if (whole)
-              static_cast<__nv_bfloat16*>(p.out)[at * p.d + f] = __float2bfloat16_rn(v);
-            else
-              p.part_o[(split * total_rows + at) * W + f] = v;
-          }
-        }
       }
+      tc_fence_before();
+      mbar_arrive(bar(C::O_FREE));
+      mbar_arrive(bar(C::Q_EMPTY + buf));
     }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -746,47 +1228,86 @@ __global__ void __launch_bounds__(kRowThreads, (RowsCfg<F8, W, NR>::MIN_BLOCKS))
   }
 }
 
-// One warp per output row: merges the splits' partials of its sequence,
-//   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s.
-template <int W>
+// Merges the partials of a unit of the sequence that share c starts inside (when
+// it is the first share that does), eight rows per block:
+//   o = sum_x 2^(m_x - M) o_x / sum_x 2^(m_x - M) l_x,  M = max_x m_x.
+// blockIdx.x = (c - 1) * units + unit, blockIdx.y = block of eight rows.  The
+// partials are the one of the share before (its second) and those of the shares
+// from c on that start inside the sequence (their first).  A row has 8 / rows
+// warps, which divide its partials.
+template <int W, int NR>
 __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsParams p) {
   constexpr int EPL = W / 32;
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const long long rows = static_cast<long long>(p.B) * p.T * p.H;
-  griddep_wait();  // the split kernel's partials are complete and visible
-  if (row >= rows) return;
-  const int b = static_cast<int>(row / (static_cast<long long>(p.T) * p.H));
-  const int splits = rows_work(p, b).active;
-  if (splits == 1) return;  // written by its only split
-  float M = -INFINITY;
-  for (int s = lane; s < splits; s += 32) M = fmaxf(M, p.part_m[s * rows + row]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f;
-  float o[EPL];
+  __shared__ float sums[8][W + 1];
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int c = static_cast<int>(blockIdx.x) / p.units + 1;
+  const int u = static_cast<int>(blockIdx.x) % p.units;
+  griddep_wait();  // the shares' partials are complete and visible
+  const int total = total_weight(p, nullptr);
+  const int shares = share_count(total, p.groups);
+  if (c >= shares) return;
+  const int pos = share_start(total, shares, c);
+  const Place q = find_place(p, pos);
+  const int base = pos - q.lo;
+  if (q.lo <= kUnitCost) return;                                        // not cut here
+  if (share_start(total, shares, c - 1) - base > kUnitCost) return;     // cut before
+  // the first share at or past the sequence's end
+  const int last = static_cast<int>((static_cast<long long>(base + q.wt) * shares + total - 1) / total);
+  const int pieces = 1 + min(last, shares) - c;
+  const int n_rows = p.T * p.G;
+  const int blocks = (n_rows + NR - 1) / NR;
+  const int hk = u / blocks, rb = u % blocks;
+  const int rows = min(8, min(NR, n_rows - rb * NR) - 8 * static_cast<int>(blockIdx.y));
+  if (rows <= 0) return;
+  int per = 8;  // warps per row: the largest power of two that gives every row one
+  while (per * rows > 8) per >>= 1;
+  const int r8 = warp / per, part = warp % per;
+  const bool mine = r8 < rows;
+  float o[EPL], L = 0.f, M = -INFINITY;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float ms = p.part_m[s * rows + row];
-    if (ms == -INFINITY) continue;  // a split whose keys this row does not see
-    const float w = ex2_approx(ms - M);
-    L = fmaf(w, p.part_l[s * rows + row], L);
-    const float* po = p.part_o + (s * rows + row) * W;
+  if (mine) {
+    const long long r = 8 * blockIdx.y + r8;
+    auto slot = [&](int x) {
+      return (static_cast<long long>(x == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + x)) * p.units + u) * NR + r;
+    };
+    for (int x = lane; x < pieces; x += 32) M = fmaxf(M, p.part_m[slot(x)]);
+    M = warp_max(M);
+    if (M != -INFINITY) {
+#pragma unroll 4
+      for (int x = part; x < pieces; x += per) {
+        const long long at = slot(x);
+        const float w = ex2_approx(p.part_m[at] - M);  // 0 for a part the row sees nothing of
+        L = fmaf(w, p.part_l[at], L);
 #pragma unroll
-    for (int e = 0; e < EPL; ++e)
-      if (lane + 32 * e < p.d) o[e] = fmaf(w, po[lane + 32 * e], o[e]);
+        for (int e = 0; e < EPL; ++e) o[e] = fmaf(w, p.part_o[at * W + lane + 32 * e], o[e]);
+      }
+    }
   }
+  if (per > 1) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) sums[warp][lane + 32 * e] = o[e];
+    if (lane == 0) sums[warp][W] = L;
+    __syncthreads();
+    if (part != 0) return;
+    for (int x = 1; x < per; ++x) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) o[e] += sums[warp + x][lane + 32 * e];
+      L += sums[warp + x][W];
+    }
+  }
+  if (!mine) return;
+  const int gr = rb * NR + 8 * static_cast<int>(blockIdx.y) + r8;
+  const int t = gr / p.G, h = hk * p.G + (gr - t * p.G);
   const float inv = L > 0.f ? 1.f / L : 0.f;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * p.d;
+  __nv_bfloat16* dst =
+      static_cast<__nv_bfloat16*>(p.out) + ((static_cast<long long>(q.b) * p.T + t) * p.H + h) * p.d;
 #pragma unroll
   for (int e = 0; e < EPL; ++e)
     if (lane + 32 * e < p.d) dst[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
-  if (p.lse && lane == 0) {
-    const int bt = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
-    p.lse[(static_cast<long long>(b) * p.H + h) * p.T + (bt - b * p.T)] =
+  if (p.lse && lane == 0)
+    p.lse[(static_cast<long long>(q.b) * p.H + h) * p.T + t] =
         L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
-  }
 }
 
 template <bool F8, int W, int NR>
@@ -802,36 +1323,39 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  const int blocks = (p.T * p.G + NR - 1) / NR;
-  const dim3 grid(static_cast<unsigned>(p.B * p.H_kv * blocks), static_cast<unsigned>(p.n_splits));
-  e = launch_serialized(rows_kernel<F8, W, NR>, grid, dim3(kRowThreads), C::SMEM, stream, p);
+  e = launch_serialized(rows_kernel<F8, W, NR>, dim3(static_cast<unsigned>(p.lanes * p.groups)), dim3(C::THREADS),
+                        C::SMEM, stream, p);
   if (e != cudaSuccess) return e;
   int kernels = 1;
-  if (p.n_splits > 1) {
-    const long long rows = static_cast<long long>(p.B) * p.T * p.H;
-    e = launch_serialized(rows_combine_kernel<W>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256),
-                          0, stream, p);
+  if (!p.whole_units) {
+    const int rows = p.T * p.G < NR ? p.T * p.G : NR;
+    e = launch_serialized(rows_combine_kernel<W, NR>,
+                          dim3(static_cast<unsigned>((p.groups - 1) * p.units), static_cast<unsigned>((rows + 7) / 8)),
+                          dim3(256), 0, stream, p);
     kernels = 2;
   }
   if (info) {
     info->kernels = kernels;
-    info->grid = static_cast<int>(grid.x * grid.y);
-    info->block = kRowThreads;
+    info->grid = p.lanes * p.groups;
+    info->block = C::THREADS;
     info->smem = C::SMEM;
   }
   return e;
 }
 
-// Calls f.template operator()<F8, W, NR>() with the kernel's configuration for
-// R rows per key head of d features.
+// Calls f with the kernel's configuration for R rows per key head of d features.
 template <typename F>
 auto with_config(bool f8, int d, int R, F&& f) {
   if (f8) {
-    if (d <= 128) return R <= 16 ? f(RowsCfg<true, 128, 16>{}) : f(RowsCfg<true, 128, 32>{});
-    return R <= 16 ? f(RowsCfg<true, 256, 16>{}) : f(RowsCfg<true, 256, 32>{});
+    if (d <= 128)
+      return R <= 8    ? f(RowsCfg<true, 128, 8>{})
+             : R <= 16 ? f(RowsCfg<true, 128, 16>{})
+                     : (R <= 32 ? f(RowsCfg<true, 128, 32>{}) : f(RowsCfg<true, 128, 64>{}));
+    return R <= 8 ? f(RowsCfg<true, 256, 8>{}) : (R <= 16 ? f(RowsCfg<true, 256, 16>{}) : f(RowsCfg<true, 256, 32>{}));
   }
   if (d <= 64)
-    return R <= 16 ? f(RowsCfg<false, 64, 16>{}) : (R <= 32 ? f(RowsCfg<false, 64, 32>{}) : f(RowsCfg<false, 64, 64>{}));
+    return R <= 16 ? f(RowsCfg<false, 64, 16>{})
+                   : (R <= 32 ? f(RowsCfg<false, 64, 32>{}) : f(RowsCfg<false, 64, 64>{}));
   if (d <= 128)
     return R <= 16 ? f(RowsCfg<false, 128, 16>{})
                    : (R <= 32 ? f(RowsCfg<false, 128, 32>{}) : f(RowsCfg<false, 128, 64>{}));
@@ -840,42 +1364,45 @@ auto with_config(bool f8, int d, int R, F&& f) {
 
 }  // namespace
 
-int rows_splits(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
+RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
   const int R = T * (H / H_kv);
   return with_config(f8, d, R, [&](auto cfg) {
     using C = decltype(cfg);
-    const long long base = static_cast<long long>(B) * H_kv * ((R + C::NR - 1) / C::NR);
-    const long long slots = 152ll * C::MIN_BLOCKS;
-    const int tiles = (Lk + kKeys - 1) / kKeys;
-    // The split count that ends first when every CTA takes its tiles and a
-    // start-up worth two: waves of CTAs x (tiles per split + 2).
-    int best = 1;
-    long long best_cost = -1;
-    for (int S = 1; S <= 64 && 2 * (S - 1) <= tiles; ++S) {
-      const long long waves = (base * S + slots - 1) / slots;
-      const long long cost = waves * ((tiles + S - 1) / S + 2) + (S > 1 ? 2 : 0);
-      if (best_cost < 0 || cost < best_cost) {
-        best = S;
-        best_cost = cost;
-      }
+    RowsPlan plan = {};
+    plan.width = C::W;
+    plan.units = static_cast<long long>(H_kv) * ((R + C::NR - 1) / C::NR);
+    const long long U = plan.units;
+    const long long slots = static_cast<long long>(kSms) * C::MIN_BLOCKS;
+    // What a CTA does, in tiles (a sequence counted at the cache's capacity), for
+    // each number of passes: with whole sequences the fullest group's; with equal
+    // shares one more sequence's cost and the second kernel (some four tiles').
+    const long long weight = (Lk + kKeys - 1) / kKeys + kUnitCost;
+    const long long p0 = (U + slots - 1) / slots;
+    long long best = -1;
+    for (long long P = p0; P < p0 + 8 && P <= U; ++P) {
+      const long long lanes = (U + P - 1) / P;
+      const long long groups = slots / lanes;  // >= 1
+      const long long g_whole = groups < B ? groups : B;
+      const long long whole = P * ((B + g_whole - 1) / g_whole) * weight;
+      const long long g_cut0 = B * weight / kMinShare;
+      const long long g_cut = g_cut0 < 1 ? 1 : (g_cut0 < groups ? g_cut0 : groups);
+      const long long cut = P * ((B * weight + g_cut - 1) / g_cut + kUnitCost) + 4;
+      const bool use_whole = whole <= cut || g_cut == 1;
+      const long long cost = use_whole ? whole : cut;
+      if (best >= 0 && cost >= best) continue;
+      best = cost;
+      plan.lanes = lanes;
+      plan.groups = use_whole ? g_whole : g_cut;
+      plan.whole_units = use_whole;
     }
-    return best;
+    plan.weight = B * weight;
+    plan.part_rows = plan.whole_units ? 0 : static_cast<size_t>(plan.groups) * 2 * U * C::NR;
+    return plan;
   });
 }
 
-int rows_kernel_width(int d, bool f8) {
-  if (f8) return d <= 128 ? 128 : 256;
-  return d <= 64 ? 64 : (d <= 128 ? 128 : 256);
-}
-
+int rows_tile_keys() { return kKeys; }
 int rows_box_keys() { return kBoxKeys; }
-
-long long rows_blocks(int B, int T, int H, int H_kv, int d, bool f8) {
-  const int R = T * (H / H_kv);
-  return with_config(f8, d, R, [&](auto cfg) {
-    return static_cast<long long>(B) * H_kv * ((R + decltype(cfg)::NR - 1) / decltype(cfg)::NR);
-  });
-}
 
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
   return with_config(p.k_scale != nullptr, p.d, p.T * p.G, [&](auto cfg) {

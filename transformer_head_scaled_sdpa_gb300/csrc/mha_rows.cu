@@ -67,6 +67,8 @@
 // MHA_ERR_TIMEOUT).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -104,10 +106,11 @@ struct RowsCfg {
   static constexpr int GROUPS = RPT / GW;
   static constexpr int Q_BYTES = NQ * W * EB;
   static constexpr int P_BYTES = kKeys * NP * EB;
+  static constexpr int P_BUFS = W <= 128 && NR <= 32 ? 2 : 1;  // (beyond, the ring needs the room)
   // barriers (512 bytes), lengths, scales, per-row values of two units and of the softmax
   static constexpr int SCALES = F8 ? kScaleTiles * kKeys * 2 : 0;
   static constexpr int MISC = 512 + 8 * kSeqCache + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
-  static constexpr int FIXED = 2 * Q_BYTES + P_BYTES + MISC + 1024;
+  static constexpr int FIXED = 2 * Q_BYTES + P_BUFS * P_BYTES + MISC + 1024;
   // TMEM: S0 | S1 | O (per 128 features)
   static constexpr int M_O = W == 64 ? 64 : 128;         // rows of the O^T tile
   static constexpr uint32_t TM_S1 = NQ, TM_O = 2 * NQ;
@@ -118,14 +121,14 @@ struct RowsCfg {
   // two CTAs per SM when each can hold two tiles' worth of ring, else one with
   // a deep ring
   static constexpr int SLOTS2 = (115712 - FIXED) / SLOT;
-  static constexpr bool TWO = SLOTS2 >= 4 && WGS == 1 && TMEM_COLS <= 256;
+  static constexpr bool TWO = SLOTS2 >= (BLKS == 1 ? 4 : 5) && WGS == 1 && TMEM_COLS <= 256;
   static constexpr int SLOTS1 = (232448 - FIXED) / SLOT;
   static constexpr int SLOTS = TWO ? SLOTS2 : (SLOTS1 > 16 ? 16 : SLOTS1);
   static constexpr int MIN_BLOCKS = TWO ? 2 : 1;
   static_assert(SLOTS >= 2 * BLKS + 1, "ring: the next K tile while V waits");
   static constexpr int OFF_Q = SLOTS * SLOT;             // + buffer * Q_BYTES
   static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
-  static constexpr int OFF_MISC = OFF_P + P_BYTES;
+  static constexpr int OFF_MISC = OFF_P + P_BUFS * P_BYTES;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   // barriers
@@ -135,9 +138,10 @@ struct RowsCfg {
   static constexpr int Q_FULL = 2 * SLOTS;    // + buffer: Q and the unit's row values (Q_THREADS arrivals)
   static constexpr int Q_EMPTY = Q_FULL + 2;  // + buffer: the last scores and the epilogue are done
   static constexpr int S_FULL = Q_EMPTY + 2;  // + buffer
-  static constexpr int P_FULL = S_FULL + 2;   // every softmax thread
-  static constexpr int PV_DONE = P_FULL + 1;
-  static constexpr int O_FREE = PV_DONE + 1;  // the epilogue has read O (every softmax thread)
+  static constexpr int P_FULL = S_FULL + 2;   // + P buffer (every softmax thread)
+  static constexpr int PV_DONE = P_FULL + P_BUFS;       // + P buffer
+  static constexpr int Q_FIRST = PV_DONE + P_BUFS;      // the first unit's Q (every softmax thread)
+  static constexpr int O_FREE = Q_FIRST + 1;  // the epilogue has read O (every softmax thread)
   static constexpr int DRAIN = O_FREE + 1;
   static constexpr int SC_FULL = DRAIN + 1;            // + tile: scales (8-bit; 32 arrivals)
   static constexpr int SC_EMPTY = SC_FULL + (F8 ? kScaleTiles : 0);  // + tile: read (each softmax warp)
@@ -324,44 +328,55 @@ struct Place {
   int wt;  // weight of the sequence
 };
 
-// Whole warp: the weight of all sequences.  `seq`: where to keep the lengths of
-// up to kSeqCache of them, or null.
-__device__ __forceinline__ int total_weight(const RowsParams& p, int2* seq) {
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  int sum = 0;
-  for (int b = lane; b < p.B; b += 32) {
+// The batch's weights, 32 sequences to a step of a warp.
+struct Scan {
+  int wt;    // this lane's sequence of the current step (0 past the last)
+  int upto;  // weight up to and with it
+};
+__device__ __forceinline__ Scan scan_step(const RowsParams& p, int b0, int before, int2* seq) {
+  const int lane = static_cast<int>(threadIdx.x & 31), b = b0 + lane;
+  Scan r = {0, 0};
+  if (b < p.B) {
     const int2 s = seq_lens(p, b);
     if (seq && b < kSeqCache) seq[b] = s;
-    sum += seq_tiles(p, s) + kUnitCost;
+    r.wt = seq_tiles(p, s) + kUnitCost;
   }
+  r.upto = r.wt;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, r.upto, o);
+    if (lane >= o) r.upto += y;
+  }
+  r.upto += before;
+  return r;
+}
+
+// Whole warp: the weight of all sequences, and the last step's scan (all there is
+// when the batch has at most 32).  `seq`: where to keep the lengths of up to
+// kSeqCache sequences, or null.
+__device__ __forceinline__ int total_weight(const RowsParams& p, int2* seq, Scan* last) {
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    *last = scan_step(p, b0, before, seq);
+    before = __shfl_sync(0xffffffffu, last->upto, 31);
+  }
+  return before;
 }
 
 // Whole warp: where `pos` (less than the total) falls.
-__device__ __forceinline__ Place find_place(const RowsParams& p, int pos) {
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  int before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    const int b = b0 + lane;
-    const int wt = b < p.B ? seq_tiles(p, seq_lens(p, b)) + kUnitCost : 0;
-    int upto = wt;  // inclusive scan
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const unsigned here = __ballot_sync(0xffffffffu, before + upto > pos);
+__device__ __forceinline__ Place find_place(const RowsParams& p, int pos, Scan scan) {
+  for (int b0 = 0, before = 0;; b0 += 32) {
+    if (p.B > 32) scan = scan_step(p, b0, before, nullptr);
+    const unsigned here = __ballot_sync(0xffffffffu, scan.upto > pos);
     if (here != 0 || b0 + 32 >= p.B) {
       const int src = here != 0 ? __ffs(here) - 1 : 31;
       Place q;
       q.b = b0 + src;
-      q.wt = __shfl_sync(0xffffffffu, wt, src);
-      q.lo = __shfl_sync(0xffffffffu, pos - before - (upto - wt), src);
+      q.wt = __shfl_sync(0xffffffffu, scan.wt, src);
+      q.lo = pos - __shfl_sync(0xffffffffu, scan.upto - scan.wt, src);
       return q;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    before = __shfl_sync(0xffffffffu, scan.upto, 31);
   }
 }
 
@@ -486,8 +501,11 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       mbar_init(bar(C::Q_EMPTY + i), 1 + SOFT);
       mbar_init(bar(C::S_FULL + i), 1);
     }
-    mbar_init(bar(C::P_FULL), SOFT);
-    mbar_init(bar(C::PV_DONE), 1);
+    for (int i = 0; i < C::P_BUFS; ++i) {
+      mbar_init(bar(C::P_FULL + i), SOFT);
+      mbar_init(bar(C::PV_DONE + i), 1);
+    }
+    mbar_init(bar(C::Q_FIRST), SOFT);
     mbar_init(bar(C::O_FREE), SOFT);
     mbar_init(bar(C::DRAIN), 1);
     if constexpr (F8) {
@@ -499,52 +517,174 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     *abort_flag = 0;
     fence_mbar_init();
   }
+  __syncthreads();  // the barriers are set up
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
     tmem_relinquish();
+    tc_fence_before();
   }
-  if (warp == kQWarp && lane == 0) {
-    tma_prefetch_desc(&p.tm_k);
-    tma_prefetch_desc(&p.tm_v);
-    tma_prefetch_desc(&p.tm_k_box);
-    tma_prefetch_desc(&p.tm_v_box);
-  }
+  Share at = {0, 0, 0, 0};
   if (warp == kLoadWarp) {
+    if (elect_one()) {
+      tma_prefetch_desc(&p.tm_k);
+      tma_prefetch_desc(&p.tm_v);
+      tma_prefetch_desc(&p.tm_k_box);
+      tma_prefetch_desc(&p.tm_v_box);
+    }
+    __syncwarp();
     griddep_wait();  // global memory only from here on
-    const int total = total_weight(p, seq);
+    Scan scan = {0, 0};
+    const int total = total_weight(p, seq, &scan);
     const int shares = share_count(total, p.groups);
     const int c = static_cast<int>(blockIdx.x) / p.lanes;
-    Share at = {0, 0, 0, 0};
     if (c < shares) {
       int a = share_start(total, shares, c), z = share_start(total, shares, c + 1);
-      Place q = find_place(p, a);
+      Place q = find_place(p, a, scan);
       if (p.whole_units) {
         // both ends to the nearer border of a sequence
         auto border = [&](int pos, const Place& x) { return pos - x.lo + (2 * x.lo >= x.wt ? x.wt : 0); };
         a = border(a, q);
         if (2 * q.lo >= q.wt) ++q.b;
         q.lo = 0;
-        if (z < total) z = border(z, find_place(p, z));
+        if (z < total) z = border(z, find_place(p, z, scan));
       }
       at.b = q.b;
       at.lo = q.lo;
       at.left = z - a;
     }
     if (lane == 0) *share = at;
+    __threadfence_block();
+    __syncwarp();
+    // the other warps learn the share; this one goes on to its loads
+    asm volatile("barrier.cta.arrive 15, %0;" ::"n"(C::THREADS) : "memory");
+  } else {
+    asm volatile("barrier.cta.sync 15, %0;" ::"n"(C::THREADS) : "memory");
+    tc_fence_after();
+    at = *share;
+    griddep_wait();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const Share at = *share;
+  const uint32_t tmem = *tmem_slot;  // (not read by the load warp, which did not wait)
   // the next launch may set itself up (it waits for this grid before it touches
   // global memory)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  griddep_wait();
 
   const int blks = C::BLKS == 1 ? 1 : (p.d + 127) / 128;  // 128-feature blocks in use
   auto unit_hk = [&](const UnitIter& it) { return blocks == 1 ? it.u : it.u / blocks; };
   auto unit_rb = [&](const UnitIter& it) { return blocks == 1 ? 0 : it.u % blocks; };
+
+  // Phase of Q_FULL for unit k (the first unit has a barrier of its own).
+  auto q_phase = [](int k) { return static_cast<uint32_t>(((k >> 1) - ((k & 1) ? 0 : 1)) & 1); };
+  // Buffer and phase of P and its product for tile t.
+  auto p_buf = [](uint32_t t) { return C::P_BUFS == 2 ? t & 1 : 0u; };
+  auto p_phase = [](uint32_t t) { return C::P_BUFS == 2 ? (t >> 1) & 1 : t & 1; };
+  // Output row of row r of a unit (-1 past the last), t: its drafted token.
+  auto out_row = [&](const UnitIter& it, int r, int* t) {
+    const int gr = unit_rb(it) * NR + r;
+    *t = -1;
+    if (gr >= n_rows) return -1;
+    *t = p.G == 1 ? gr : gr / p.G;
+    return (it.b * p.T + *t) * p.H + unit_hk(it) * p.G + (gr - *t * p.G);
+  };
+  // A unit's Q, output rows and mask words into buffer `buf`, by thread qt of a
+  // multiple of 32 (eight threads per row); false when `buffer_free` gave up.
+  auto prepare_q = [&](auto threads, const UnitIter& it, int buf, int qt, auto buffer_free) {
+    constexpr int RP = decltype(threads)::value / 8;
+    constexpr int PER = W / 64;                    // 16-byte pieces of a row per thread
+    constexpr int MOST = PER > 2 ? 2 : 4;
+    constexpr int ROUNDS = NR / RP < 1 ? 1 : NR / RP;
+    constexpr int BATCH = ROUNDS < MOST ? ROUNDS : MOST;  // rows per thread in flight
+    const int sub = qt & 7;
+    const int hk = unit_hk(it);
+    const uint32_t sQ = s_base + C::OFF_Q + buf * C::Q_BYTES;
+    if (NR < RP && (qt >> 3) >= NR) return buffer_free();  // (whole warps)
+    // (the first rows are requested before the buffer is free)
+    for (int rr = 0; rr < NR; rr += RP * BATCH) {
+      uint4 v[BATCH][PER];
+      int t[BATCH], out[BATCH];
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        out[y] = out_row(it, rr + y * RP + (qt >> 3), &t[y]);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                          static_cast<long long>(max(out[y], 0)) * p.d);
+#pragma unroll
+        for (int z = 0; z < PER; ++z) {
+          // 8-bit: 16 elements to a thread, in two pieces; bf16: 8
+          const int piece = F8 ? 2 * (sub + 8 * (z >> 1)) + (z & 1) : sub + 8 * z;
+          v[y][z] = make_uint4(0, 0, 0, 0);
+          if (out[y] >= 0 && 8 * piece < p.d) v[y][z] = __ldg(src + piece);
+        }
+      }
+      if (rr == 0 && !buffer_free()) return false;
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        const int r = rr + y * RP + (qt >> 3);
+        const bool live = t[y] >= 0 && t[y] < it.s.y;
+        if (sub == 0) {
+          row_out(buf)[r] = out[y];
+          row_lse(buf)[r] = out[y] < 0 ? 0 : (it.b * p.H + out[y] % p.H) * p.T + t[y];
+          row_live(buf)[r] = live;
+        }
+        if (sub < kMaskWords) {
+          // (a chain's words: bits 0 .. t)
+          uint64_t word = 0;
+          if (live && p.tree_mask) {
+            if (sub < p.words)
+              word = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t[y]) * p.words + sub);
+          } else if (live) {
+            const int bits = t[y] + 1 - 64 * sub;
+            word = bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
+          }
+          row_mask(buf)[r * kMaskWords + sub] = word;
+        }
+        if constexpr (F8) {
+          float amax = 0.f;
+#pragma unroll
+          for (int z = 0; z < PER; ++z) {
+            const uint32_t q4[4] = {v[y][z].x, v[y][z].y, v[y][z].z, v[y][z].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q4[e])), fabsf(bf16_hi(q4[e]))));
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // q 2^-e with the largest magnitude in [128, 256)
+          const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7, -100);
+          const float inv = pow2i(-e);
+          if (sub == 0) row_factor(buf)[r] = pow2i(e) * p.scale_log2;
+#pragma unroll
+          for (int u = 0; u < PER / 2; ++u) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint4 w4 = v[y][2 * u + z];
+              const uint32_t q4[4] = {w4.x, w4.y, w4.z, w4.w};
+              uint32_t a[4], c2[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float x0 = bf16_lo(q4[x]) * inv, x1 = bf16_hi(q4[x]) * inv;
+                a[x] = pack_e4m3x2(x0, x1);
+                const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[x]));
+                c2[x] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
+              }
+              hi[2 * z] = a[0] | (a[1] << 16);
+              hi[2 * z + 1] = a[2] | (a[3] << 16);
+              lo[2 * z] = c2[0] | (c2[1] << 16);
+              lo[2 * z + 1] = c2[2] | (c2[3] << 16);
+            }
+            const uint32_t to = sQ + (sub + 8 * u) * (C::NQ * 16) + r * 16;
+            st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(to + NR * 16, lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else {
+#pragma unroll
+          for (int z = 0; z < PER; ++z)
+            st_shared_v4(sQ + (sub + 8 * z) * (C::NQ * 16) + r * 16, v[y][z].x, v[y][z].y, v[y][z].z,
+                         v[y][z].w);
+        }
+      }
+    }
+    return true;
+  };
 
   if (warp >= kMmaWarp) {
   if constexpr (C::SPLIT_REGS) regs_decrease<C::REGS_OTHER>();
@@ -666,7 +806,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     int k = 0;             // units
     uint32_t t = 0;        // tiles
     if (more) {
-      wait(C::Q_FULL, 0);
+      wait(C::Q_FIRST, 0);
       if (ok) issue_s(0, unit_q(0), it.count() == 1 ? C::Q_EMPTY : -1);
     }
     while (more && ok) {
@@ -678,12 +818,13 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         if (i + 1 < n) {
           issue_s((t + 1) & 1, unit_q(k), i + 2 == n ? C::Q_EMPTY + (k & 1) : -1);
         } else if (n_next > 0) {
-          wait(C::Q_FULL + ((k + 1) & 1), ((k + 1) >> 1) & 1);
+          wait(C::Q_FULL + ((k + 1) & 1), q_phase(k + 1));
           if (ok) issue_s((t + 1) & 1, unit_q(k + 1), n_next == 1 ? C::Q_EMPTY + ((k + 1) & 1) : -1);
         }
         // (O is free once the last unit's epilogue has read it)
         if (i == 0 && k > 0) wait(C::O_FREE, (k - 1) & 1);
-        wait(C::P_FULL, t & 1);
+        wait(C::P_FULL + p_buf(t), p_phase(t));
+        const uint64_t pd = dp0 + static_cast<uint64_t>((p_buf(t) * C::P_BYTES) >> 4);
 #pragma unroll
         for (int blk = 0; blk < C::BLKS; ++blk) {
           if (blk >= blks) break;
@@ -696,9 +837,9 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
 #pragma unroll
             for (int ks = 0; ks < kKeys / KSTEP; ++ks)
               umma<F8>(d, a + static_cast<uint64_t>((ks * KSTEP * 128) >> 4),
-                       dp0 + static_cast<uint64_t>((ks * KSTEP * 16) >> 4), idesc_o,
+                       pd + static_cast<uint64_t>((ks * KSTEP * 16) >> 4), idesc_o,
                        (i > 0 || ks > 0) ? 1u : 0u);
-            if (blk == blks - 1) umma_commit(bar(C::PV_DONE));
+            if (blk == blks - 1) umma_commit(bar(C::PV_DONE + p_buf(t)));
             umma_commit(bar(C::EMPTY + ring.slot));
           }
           __syncwarp();
@@ -717,27 +858,39 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       // ---- 8-bit: the scales of the tiles to come, four keys per lane
       const int site = kRoleRowsQ * 64;
       uint16_t* ring = reinterpret_cast<uint16_t*>(smem + C::OFF_SCALES);
-      UnitIter it;
       int t = 0;
       bool ok = true;
-      for (bool more = it.start(p, at, seq); more && ok; more = it.next(p, at, seq)) {
+      // The next 32 tiles of a unit are asked into L2 ahead (a plain load waits
+      // behind the ring's copies in the DRAM queues, several tiles' time).
+      auto ahead = [&](const UnitIter& w, int tile) {
+        const long long from = (static_cast<long long>(w.b) * p.H_kv + unit_hk(w)) * p.Lk + (tile + lane) * kKeys;
+        if (tile + lane < w.t1) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.k_scale + from));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.v_scale + from));
+        }
+      };
+      UnitIter it;
+      for (bool more = it.start(p, at, seq); more && ok;) {
+        UnitIter next = it;
+        more = next.next(p, at, seq);
+        if (more) ahead(next, next.t0);
         const int end = seq_end(p, it.s);
         const long long row = (static_cast<long long>(it.b) * p.H_kv + unit_hk(it)) * p.Lk;
-        // (up to four tiles' loads in flight)
+        // (four tiles' loads in flight)
         for (int x = it.t0; x < it.t1 && ok; x += 4) {
+          if (((x - it.t0) & 31) == 16) ahead(it, x + 16);
           const int m = min(4, it.t1 - x);
-          uint32_t kv[4][4];
+          uint32_t k4[4][4], v4[4][4];
 #pragma unroll
           for (int y = 0; y < 4; ++y)
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int key = (x + y) * kKeys + 32 * z + lane;
-              uint32_t a = 127, c = 127;
+              k4[y][z] = v4[y][z] = 127;
               if (y < m && key < end) {
-                a = __ldg(p.k_scale + row + key);
-                c = __ldg(p.v_scale + row + key);
+                k4[y][z] = __ldg(p.k_scale + row + key);
+                v4[y][z] = __ldg(p.v_scale + row + key);
               }
-              kv[y][z] = a | (c << 8);
             }
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -747,140 +900,44 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
                                               p.status, site + C::SC_EMPTY + slot);
             if (!ok) break;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) ring[slot * kKeys + 32 * z + lane] = static_cast<uint16_t>(kv[y][z]);
+            for (int z = 0; z < 4; ++z)
+              ring[slot * kKeys + 32 * z + lane] = static_cast<uint16_t>(k4[y][z] | (v4[y][z] << 8));
             mbar_arrive(bar(C::SC_FULL + slot));
             ++t;
           }
         }
+        it = next;
       }
     } else {
     // ---- the next units' Q, output rows and mask words
     const int site = kRoleRowsQ * 64;
-    constexpr int QT = C::Q_THREADS, RP = QT / 8;  // eight threads per row
-    constexpr int PER = W / 64;                    // 16-byte pieces of a row per thread
-    constexpr int MOST = PER > 2 ? 2 : 4;
-    constexpr int BATCH = NR / RP < MOST ? NR / RP : MOST;  // rows per thread in flight
+    constexpr int QT = C::Q_THREADS;
     const int qt = tid - 32 * kQWarp;
-    const int sub = qt & 7;
     UnitIter it;
     int k = 0;  // units with keys
     for (bool more = it.start<true>(p, at, seq); more; more = it.next<true>(p, at, seq)) {
-      const int buf = k & 1;
-      const uint32_t sQ = s_base + C::OFF_Q + buf * C::Q_BYTES;
-      const int hk = unit_hk(it), rb = unit_rb(it);
-      // output row of row r of the block (-1 past the last), t: its drafted token
-      auto out_row = [&](int r, int* t) {
-        const int gr = rb * NR + r;
-        *t = -1;
-        if (gr >= n_rows) return -1;
-        *t = p.G == 1 ? gr : gr / p.G;
-        return (it.b * p.T + *t) * p.H + hk * p.G + (gr - *t * p.G);
-      };
       if (it.tiles == 0) {
         // no key at all: output 0, log-sum-exp -inf
-        for (int r = qt >> 3; r < NR; r += RP) {
+        for (int r = qt >> 3; r < NR; r += QT / 8) {
           int t;
-          const int out = out_row(r, &t);
+          const int out = out_row(it, r, &t);
           if (out < 0) break;
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d);
-          for (int x = sub; 8 * x < p.d; x += 8) dst[x] = make_uint4(0, 0, 0, 0);
-          if (p.lse && sub == 0) p.lse[(it.b * p.H + out % p.H) * p.T + t] = -INFINITY;
+          for (int x = qt & 7; 8 * x < p.d; x += 8) dst[x] = make_uint4(0, 0, 0, 0);
+          if (p.lse && (qt & 7) == 0) p.lse[(it.b * p.H + out % p.H) * p.T + t] = -INFINITY;
         }
         continue;
       }
-      // (the first rows are requested before the buffer is free)
-      for (int rr = 0; rr < NR; rr += RP * BATCH) {
-        uint4 v[BATCH][PER];
-        int t[BATCH], out[BATCH];
-#pragma unroll
-        for (int y = 0; y < BATCH; ++y) {
-          out[y] = out_row(rr + y * RP + (qt >> 3), &t[y]);
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                            static_cast<long long>(max(out[y], 0)) * p.d);
-#pragma unroll
-          for (int z = 0; z < PER; ++z) {
-            // 8-bit: 16 elements to a thread, in two pieces; bf16: 8
-            const int piece = F8 ? 2 * (sub + 8 * (z >> 1)) + (z & 1) : sub + 8 * z;
-            v[y][z] = make_uint4(0, 0, 0, 0);
-            if (out[y] >= 0 && 8 * piece < p.d) v[y][z] = __ldg(src + piece);
-          }
-        }
-        if (rr == 0 && k >= 2 && !warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, p.status,
-                                            site + C::Q_EMPTY + buf)) {
-          more = false;
-          break;
-        }
-#pragma unroll
-        for (int y = 0; y < BATCH; ++y) {
-          const int r = rr + y * RP + (qt >> 3);
-          const bool live = t[y] >= 0 && t[y] < it.s.y;
-          if (sub == 0) {
-            row_out(buf)[r] = out[y];
-            row_lse(buf)[r] = out[y] < 0 ? 0 : (it.b * p.H + out[y] % p.H) * p.T + t[y];
-            row_live(buf)[r] = live;
-          }
-          if (sub < kMaskWords) {
-            // (a chain's words: bits 0 .. t)
-            uint64_t word = 0;
-            if (live && p.tree_mask) {
-              if (sub < p.words)
-                word = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t[y]) * p.words + sub);
-            } else if (live) {
-              const int bits = t[y] + 1 - 64 * sub;
-              word = bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
-            }
-            row_mask(buf)[r * kMaskWords + sub] = word;
-          }
-          if constexpr (F8) {
-            float amax = 0.f;
-#pragma unroll
-            for (int z = 0; z < PER; ++z) {
-              const uint32_t q4[4] = {v[y][z].x, v[y][z].y, v[y][z].z, v[y][z].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q4[e])), fabsf(bf16_hi(q4[e]))));
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // q 2^-e with the largest magnitude in [128, 256)
-            const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7, -100);
-            const float inv = pow2i(-e);
-            if (sub == 0) row_factor(buf)[r] = pow2i(e) * p.scale_log2;
-#pragma unroll
-            for (int u = 0; u < PER / 2; ++u) {
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const uint4 w4 = v[y][2 * u + z];
-                const uint32_t q4[4] = {w4.x, w4.y, w4.z, w4.w};
-                uint32_t a[4], c2[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const float x0 = bf16_lo(q4[x]) * inv, x1 = bf16_hi(q4[x]) * inv;
-                  a[x] = pack_e4m3x2(x0, x1);
-                  const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[x]));
-                  c2[x] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
-                }
-                hi[2 * z] = a[0] | (a[1] << 16);
-                hi[2 * z + 1] = a[2] | (a[3] << 16);
-                lo[2 * z] = c2[0] | (c2[1] << 16);
-                lo[2 * z + 1] = c2[2] | (c2[3] << 16);
-              }
-              const uint32_t to = sQ + (sub + 8 * u) * (C::NQ * 16) + r * 16;
-              st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
-              st_shared_v4(to + NR * 16, lo[0], lo[1], lo[2], lo[3]);
-            }
-          } else {
-#pragma unroll
-            for (int z = 0; z < PER; ++z)
-              st_shared_v4(sQ + (sub + 8 * z) * (C::NQ * 16) + r * 16, v[y][z].x, v[y][z].y, v[y][z].z,
-                           v[y][z].w);
-          }
-        }
+      const int buf = k & 1;
+      if (k > 0) {  // (the softmax threads prepare the first)
+        const bool ok = prepare_q(std::integral_constant<int, QT>{}, it, buf, qt, [&]() {
+          return k < 2 || warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, p.status,
+                                    site + C::Q_EMPTY + buf);
+        });
+        if (!ok) break;
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::Q_FULL + buf));
       }
-      if (!more) break;
-      fence_proxy_async_smem();
-      mbar_arrive(bar(C::Q_FULL + buf));
       ++k;
     }
     }
@@ -901,7 +958,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     if (kt < RPT) row_ref[r0 + kt] = 0.f;
     named_barrier(nbar, 128);
     UnitIter it;
-    int k = 0, t = 0;  // units, tiles
+    int k = 0;       // units
+    uint32_t t = 0;  // tiles
     for (bool more = it.start(p, at, seq); more; more = it.next(p, at, seq), ++k) {
       const int buf = k & 1, n = it.count();
       const int rows_here = min(NR, n_rows - unit_rb(it) * NR) - r0;  // this warpgroup's (may be <= 0)
@@ -909,7 +967,14 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       float l[RPT];
 #pragma unroll
       for (int r = 0; r < RPT; ++r) l[r] = 0.f;
-      wait(C::Q_FULL + buf, (k >> 1) & 1);
+      if (k > 0) {
+        wait(C::Q_FULL + buf, q_phase(k));
+      } else {
+        prepare_q(std::integral_constant<int, SOFT>{}, it, 0, tid, []() { return true; });
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::Q_FIRST));
+        wait(C::Q_FIRST, 0);
+      }
       const float* factor = row_factor(buf) + r0;
       float* ref = row_ref + r0;
       float* shift = row_shift + r0;  // (in the epilogue: 1 / sum)
@@ -1043,7 +1108,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             }
           }
           if (i > 0) {
-            wait(C::PV_DONE, (t - 1) & 1);
+            wait(C::PV_DONE + p_buf(t - 1), p_phase(t - 1));
             tc_fence_after();
             for (int c = 0; c < C::BLKS * C::PP; ++c)
               for (int g = 0; g < GROUPS; ++g) {
@@ -1062,8 +1127,9 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
         }
         tc_fence_before();
-        // weights; the previous product must have read P
-        if (t > 0) wait(C::PV_DONE, (t - 1) & 1);
+        // weights; the product before must have read this buffer of P
+        if (t >= C::P_BUFS) wait(C::PV_DONE + p_buf(t), p_phase(t - C::P_BUFS));
+        const uint32_t p_at = sP + p_buf(t) * C::P_BYTES;
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
           if (g * GW >= rows_here) continue;
@@ -1101,18 +1167,18 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           constexpr int COL = kKeys * 16;
           if constexpr (F8 && GW == 8) {
             // two pieces to a unit; nothing reads the second half of the last
-            const uint32_t to = sP + kt * 16;
+            const uint32_t to = p_at + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w2[0], w2[1]);
             st_shared_v4(to + COL, w3[0], w3[1], 0, 0);
           } else if constexpr (F8) {
-            const uint32_t to = sP + (r0 / 16 + g) * COL + kt * 16;
+            const uint32_t to = p_at + (r0 / 16 + g) * COL + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w1[2], w1[3]);
             st_shared_v4(to + (NR / 16) * COL, w2[0], w2[1], w2[2], w2[3]);
             st_shared_v4(to + 2 * (NR / 16) * COL, w3[0], w3[1], w3[2], w3[3]);
           } else {
 #pragma unroll
             for (int h = 0; h < GW / 8; ++h) {
-              const uint32_t to = sP + ((r0 + g * GW) / 8 + h) * COL + kt * 16;
+              const uint32_t to = p_at + ((r0 + g * GW) / 8 + h) * COL + kt * 16;
               st_shared_v4(to, w1[4 * h], w1[4 * h + 1], w1[4 * h + 2], w1[4 * h + 3]);
               st_shared_v4(to + (NR / 8) * COL, w2[4 * h], w2[4 * h + 1], w2[4 * h + 2], w2[4 * h + 3]);
             }
@@ -1124,7 +1190,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           // (before V(t) in the ring: K(0) .. K(t), K(t + 1) if there is one,
           // V(0) .. V(t - 1))
           UnitIter next = it;
-          const int before = 2 * t + 1 + (next.next(p, at, seq) ? 1 : 0);
+          const int before = 2 * static_cast<int>(t) + 1 + (i + 1 < n || next.next(p, at, seq) ? 1 : 0);
           for (int blk = 0; blk < blks; ++blk) {
             const int item = before * blks + blk, sl = item % C::SLOTS;
             wait(C::FULL + sl, (item / C::SLOTS) & 1);
@@ -1138,7 +1204,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::P_FULL));
+        mbar_arrive(bar(C::P_FULL + p_buf(t)));
       }
 
       // ---- epilogue: sums over the keys, then O
@@ -1147,7 +1213,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         const float y = warp_sums<RPT>(l, lane);
         if (lane % (32 / RPT) == 0) red[(r0 + lane / (32 / RPT)) * 4 + w4] = y;
       }
-      wait(C::PV_DONE, (t - 1) & 1);
+      wait(C::PV_DONE + p_buf(t - 1), p_phase(t - 1));
       tc_fence_after();
       const bool good = ok && *abort_flag == 0;
       named_barrier(nbar, 128);
@@ -1228,46 +1294,68 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   }
 }
 
-// Merges the partials of a unit of the sequence that share c starts inside (when
-// it is the first share that does), eight rows per block:
+// Merges the partials of a unit of a cut sequence, kCombineRows rows per block:
 //   o = sum_x 2^(m_x - M) o_x / sum_x 2^(m_x - M) l_x,  M = max_x m_x.
-// blockIdx.x = (c - 1) * units + unit, blockIdx.y = block of eight rows.  The
-// partials are the one of the share before (its second) and those of the shares
-// from c on that start inside the sequence (their first).  A row has 8 / rows
-// warps, which divide its partials.
+// blockIdx.x = cut * units + unit, blockIdx.y = block of rows; a cut is a sequence
+// or, where the batch has more sequences than the shares have borders, a border
+// (the first inside its sequence).  With c the first share that starts inside the
+// sequence, the partials are the second of share c - 1 and the first of those from
+// c on that start inside it.  A row has kCombineWarps warps, which divide its
+// partials (many when one long sequence is spread over the machine).
+constexpr int kCombineRows = 4, kCombineWarps = 4;
+__host__ __device__ __forceinline__ bool combine_by_sequence(int B, int groups) { return B < groups; }
 template <int W, int NR>
-__global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(32 * kCombineRows * kCombineWarps)
+    rows_combine_kernel(const __grid_constant__ RowsParams p) {
   constexpr int EPL = W / 32;
-  __shared__ float sums[8][W + 1];
+  __shared__ float sums[kCombineRows * kCombineWarps][W + 1];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int c = static_cast<int>(blockIdx.x) / p.units + 1;
+  const int cut = static_cast<int>(blockIdx.x) / p.units;
   const int u = static_cast<int>(blockIdx.x) % p.units;
-  griddep_wait();  // the shares' partials are complete and visible
-  const int total = total_weight(p, nullptr);
-  const int shares = share_count(total, p.groups);
-  if (c >= shares) return;
-  const int pos = share_start(total, shares, c);
-  const Place q = find_place(p, pos);
-  const int base = pos - q.lo;
-  if (q.lo <= kUnitCost) return;                                        // not cut here
-  if (share_start(total, shares, c - 1) - base > kUnitCost) return;     // cut before
-  // the first share at or past the sequence's end
-  const int last = static_cast<int>((static_cast<long long>(base + q.wt) * shares + total - 1) / total);
-  const int pieces = 1 + min(last, shares) - c;
   const int n_rows = p.T * p.G;
   const int blocks = (n_rows + NR - 1) / NR;
   const int hk = u / blocks, rb = u % blocks;
-  const int rows = min(8, min(NR, n_rows - rb * NR) - 8 * static_cast<int>(blockIdx.y));
-  if (rows <= 0) return;
-  int per = 8;  // warps per row: the largest power of two that gives every row one
-  while (per * rows > 8) per >>= 1;
-  const int r8 = warp / per, part = warp % per;
-  const bool mine = r8 < rows;
+  const int r = kCombineRows * static_cast<int>(blockIdx.y) + warp / kCombineWarps;  // row of the unit
+  const int part = warp % kCombineWarps;
+  const int gr = rb * NR + r;
+  const bool mine = r < NR && gr < n_rows;
+  const int t = mine ? gr / p.G : 0, h = hk * p.G + (gr - t * p.G);
+  griddep_wait();  // the shares' partials are complete and visible
+  Scan scan = {0, 0};
+  const int total = total_weight(p, nullptr, &scan);
+  const int shares = share_count(total, p.groups);
+  // the sequence, where it starts, and the first share that starts past its
+  // first tile
+  int b, base, wt, c;
+  if (combine_by_sequence(p.B, p.groups)) {
+    b = cut;
+    if (p.B > 32) {
+      for (int b0 = 0, before = 0; b0 <= b; b0 += 32) {
+        scan = scan_step(p, b0, before, nullptr);
+        before = __shfl_sync(0xffffffffu, scan.upto, 31);
+      }
+    }
+    wt = __shfl_sync(0xffffffffu, scan.wt, b & 31);
+    base = __shfl_sync(0xffffffffu, scan.upto, b & 31) - wt;
+    c = static_cast<int>((static_cast<long long>(base + kUnitCost + 1) * shares + total - 1) / total);
+    if (c >= shares || share_start(total, shares, c) >= base + wt) return;  // not cut
+  } else {
+    c = cut + 1;
+    if (c >= shares) return;
+    const int pos = share_start(total, shares, c);
+    const Place q = find_place(p, pos, scan);
+    b = q.b;
+    base = pos - q.lo;
+    wt = q.wt;
+    if (q.lo <= kUnitCost || share_start(total, shares, c - 1) - base > kUnitCost) return;
+  }
+  // the first share at or past the sequence's end
+  const int last = static_cast<int>((static_cast<long long>(base + wt) * shares + total - 1) / total);
+  const int pieces = 1 + min(last, shares) - c;
   float o[EPL], L = 0.f, M = -INFINITY;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
   if (mine) {
-    const long long r = 8 * blockIdx.y + r8;
     auto slot = [&](int x) {
       return (static_cast<long long>(x == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + x)) * p.units + u) * NR + r;
     };
@@ -1275,7 +1363,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
     M = warp_max(M);
     if (M != -INFINITY) {
 #pragma unroll 4
-      for (int x = part; x < pieces; x += per) {
+      for (int x = part; x < pieces; x += kCombineWarps) {
         const long long at = slot(x);
         const float w = ex2_approx(p.part_m[at] - M);  // 0 for a part the row sees nothing of
         L = fmaf(w, p.part_l[at], L);
@@ -1284,29 +1372,25 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
       }
     }
   }
-  if (per > 1) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) sums[warp][lane + 32 * e] = o[e];
-    if (lane == 0) sums[warp][W] = L;
-    __syncthreads();
-    if (part != 0) return;
-    for (int x = 1; x < per; ++x) {
+  for (int e = 0; e < EPL; ++e) sums[warp][lane + 32 * e] = o[e];
+  if (lane == 0) sums[warp][W] = L;
+  __syncthreads();
+  if (part != 0 || !mine) return;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] += sums[warp + x][lane + 32 * e];
-      L += sums[warp + x][W];
-    }
+  for (int x = 1; x < kCombineWarps; ++x) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) o[e] += sums[warp + x][lane + 32 * e];
+    L += sums[warp + x][W];
   }
-  if (!mine) return;
-  const int gr = rb * NR + 8 * static_cast<int>(blockIdx.y) + r8;
-  const int t = gr / p.G, h = hk * p.G + (gr - t * p.G);
   const float inv = L > 0.f ? 1.f / L : 0.f;
   __nv_bfloat16* dst =
-      static_cast<__nv_bfloat16*>(p.out) + ((static_cast<long long>(q.b) * p.T + t) * p.H + h) * p.d;
+      static_cast<__nv_bfloat16*>(p.out) + ((static_cast<long long>(b) * p.T + t) * p.H + h) * p.d;
 #pragma unroll
   for (int e = 0; e < EPL; ++e)
     if (lane + 32 * e < p.d) dst[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
   if (p.lse && lane == 0)
-    p.lse[(static_cast<long long>(q.b) * p.H + h) * p.T + t] =
+    p.lse[(static_cast<long long>(b) * p.H + h) * p.T + t] =
         L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
@@ -1330,8 +1414,9 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
   if (!p.whole_units) {
     const int rows = p.T * p.G < NR ? p.T * p.G : NR;
     e = launch_serialized(rows_combine_kernel<W, NR>,
-                          dim3(static_cast<unsigned>((p.groups - 1) * p.units), static_cast<unsigned>((rows + 7) / 8)),
-                          dim3(256), 0, stream, p);
+                          dim3(static_cast<unsigned>((combine_by_sequence(p.B, p.groups) ? p.B : p.groups - 1) * p.units),
+                               static_cast<unsigned>((rows + kCombineRows - 1) / kCombineRows)),
+                          dim3(32 * kCombineRows * kCombineWarps), 0, stream, p);
     kernels = 2;
   }
   if (info) {

@@ -209,26 +209,23 @@ struct RowsParams {
   const int32_t* prefix_lens;  // [B] keys every row sees (clamped to [0, Lk])
   const int32_t* draft_lens;   // [B] rows (and drafted keys) of a sequence, or null: T
   const uint64_t* tree_mask;   // [B, T, words] drafted keys a row sees, or null: j <= t
-  float* part_o;      // [part_rows, kernel width] partials of cut units, or null
-  float* part_m;      // [part_rows]
-  float* part_l;      // [part_rows]
+  float* part_o;      // [n_splits, B*T*H, kernel width]  (n_splits > 1)
+  float* part_m;      // [n_splits, B*T*H]
+  float* part_l;      // [n_splits, B*T*H]
   DeviceStatus* status;
   int B, T, H, H_kv, G;  // G = H / H_kv query heads share a key head
   int Lk, d;
   int drafts;         // 1: drafted keys follow the prefix in the cache; 0: the prefix alone
   int words;          // 64-bit mask words per row
-  int units;          // units (key head, block of rows) per sequence
-  int lanes, groups;  // CTAs: groups (one share of the keys each) of lanes (units)
-  int whole_units;    // 1: shares end at sequence borders, no partials
+  int units;          // (key head, block of rows) pairs per sequence
+  int n_splits;       // splits of the key axis
   float scale_log2;   // scale * log2(e)
 };
 
 // How a launch of these sizes divides its work.
 struct RowsPlan {
-  long long units;    // per sequence
-  long long lanes, groups;
-  long long weight;   // of all sequences at the cache's capacity (a 32-bit count)
-  bool whole_units;
+  long long units;    // (key head, block of rows) pairs per sequence
+  int splits;
   size_t part_rows;   // rows of partials in the workspace (0: none)
   int width;          // features a partial row is kept at
 };

@@ -678,8 +678,8 @@ int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k
 // Most drafted tokens of one step (four mask words).
 static constexpr int kMaxDrafts = 256;
 
-// Workspace of a rows step: partial outputs, maxima and sums of units that the
-// plan's shares cut (none when units stay whole).
+// Workspace of a rows step: partial outputs, maxima and sums of every split
+// (none with a single split).
 static size_t rows_ws_bytes(const mha::RowsPlan& plan) {
   return align256(plan.part_rows * plan.width * 4) + 2 * align256(plan.part_rows * 4);
 }
@@ -749,8 +749,7 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
       return MHA_ERR_ALIAS;
   if (overlaps(lse, lb, out, qb)) return MHA_ERR_ALIAS;
   const mha::RowsPlan plan = mha::rows_plan(B, T, H, H_kv, Lk, d_k, f8);
-  // (weights and blocks are 32-bit counts)
-  if (plan.weight > 0x7fffffffll || plan.groups * plan.units > 0x7fffffffll) return MHA_ERR_SHAPE;
+  if (plan.units * B * plan.splits > 0x7fffffffll) return MHA_ERR_SHAPE;  // (a CTA per unit)
   const size_t need = rows_ws_bytes(plan);
   if (need > 0) {
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u))
@@ -801,9 +800,7 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   p.drafts = drafts ? 1 : 0;
   p.words = words;
   p.units = static_cast<int>(plan.units);
-  p.lanes = static_cast<int>(plan.lanes);
-  p.groups = static_cast<int>(plan.groups);
-  p.whole_units = plan.whole_units ? 1 : 0;
+  p.n_splits = plan.splits;
   p.scale_log2 = effective_scale(scale, d_k) * kLog2e;
   return mha::launch_rows(p, s, &t_info) == cudaSuccess ? MHA_OK : MHA_ERR_LAUNCH;
 }

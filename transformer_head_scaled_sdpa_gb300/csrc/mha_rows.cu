@@ -43,19 +43,19 @@
 // and the sums are rescaled.  Sums are float32, one partial per thread and row,
 // added up once at the end.
 //
-// Work: a unit is (sequence, key head, block of NR rows).  The grid is about one
-// wave of persistent CTAs, in groups of `lanes` CTAs: CTA l of a group takes the
-// key heads and row blocks l, l + lanes, ... (passes), and every CTA of group g
-// the g-th equal share of the batch's keys, counted in tiles plus kUnitCost per
-// sequence (each CTA scans the lengths for its start).  So ragged batches
-// balance, and a group reads the rows of neighbouring heads, which lie side by
-// side in the cache, and the same rows for its row blocks, at the same time: one
-// head's rows alone are 128-byte pieces of DRAM pages (measured, 16 sequences x
-// 96 heads x 2048 keys of 128 features in 8 bits: 161 us when a CTA's share ran
-// over consecutive heads instead).  A share that ends inside a sequence leaves
-// a partial (o, m, l) per unit in the workspace, and rows_combine_kernel merges
-// the partials exactly; where sequences are many and short the shares end at
-// their borders instead and no second kernel runs (rows_plan).
+// Work: a unit is (split, sequence, key head, block of NR rows), with the key head
+// and block the fastest: CTAs that run together read the rows of neighbouring
+// heads, which lie side by side in the cache, and the same rows for their blocks
+// (one head's rows alone are 128-byte pieces of DRAM pages: 161 us for 16
+// sequences x 96 heads x 2048 keys of 128 features in 8 bits when a CTA's work ran
+// over consecutive heads, against 110).  Each sequence's own tiles are divided by
+// the number of splits, so short sequences of a ragged batch use fewer.  The grid
+// has a CTA per unit, but CTAs are persistent: a running CTA cancels CTAs that have
+// not started (cluster launch control) and takes their units, so the launch order
+// balances the work (with equal static shares of the keys CTAs ended 25 % apart).
+// A split of a sequence that has several leaves a partial (o, m, l) in the
+// workspace, and rows_combine_kernel merges them exactly (rows_plan says when keys
+// are split).
 //
 // Roles: 4 warps per 32 rows softmax and epilogue (thread = key = TMEM lane),
 // then one warp each for MMA issue (and TMEM) and TMA, and two that prepare the
@@ -63,7 +63,8 @@
 // 8-bit cache one of them keeps the next tiles' scales in a ring instead).  The MMA
 // warp runs S(0), S(1), PV(0), S(2), PV(1), ... over all tiles of its share
 // without a break at unit borders: the next scores, and the loads of a whole
-// ring, run during a unit's epilogue.  Every wait is bounded (abort flag,
+// ring, run during a unit's epilogue.  The TMA warp also finds the units and
+// publishes them to the others through a queue.  Every wait is bounded (abort flag,
 // MHA_ERR_TIMEOUT).
 #include <cuda_bf16.h>
 
@@ -79,9 +80,8 @@ constexpr int kKeys = 128;         // keys per tile
 constexpr int kBoxKeys = 32;       // keys per small TMA box: a ragged last tile loads only what it needs
 constexpr int kScaleTiles = 8;     // tiles whose 8-bit scales are kept ahead
 constexpr int kSms = 152;
-constexpr int kUnitCost = 2;       // a unit's fixed cost in tiles (its start and epilogue)
-constexpr int kMinShare = 2 + kUnitCost;  // least weight worth a CTA of its own
-constexpr int kSeqCache = 256;     // sequences whose lengths are kept in shared memory
+constexpr int kMaxRowSplits = 64;
+constexpr int kQueue = 4;          // published units
 constexpr int kMaskWords = 4;      // 256 drafted tokens
 constexpr int kRoleRowsLoad = 16, kRoleRowsMma = 17, kRoleRowsSoftmax = 18, kRoleRowsQ = 19;
 
@@ -107,9 +107,9 @@ struct RowsCfg {
   static constexpr int Q_BYTES = NQ * W * EB;
   static constexpr int P_BYTES = kKeys * NP * EB;
   static constexpr int P_BUFS = W <= 128 && NR <= 32 ? 2 : 1;  // (beyond, the ring needs the room)
-  // barriers (512 bytes), lengths, scales, per-row values of two units and of the softmax
+  // barriers (512 bytes), units, scales, per-row values of two units and of the softmax
   static constexpr int SCALES = F8 ? kScaleTiles * kKeys * 2 : 0;
-  static constexpr int MISC = 512 + 8 * kSeqCache + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
+  static constexpr int MISC = 576 + 48 * kQueue + 16 + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
   static constexpr int FIXED = 2 * Q_BYTES + P_BUFS * P_BYTES + MISC + 1024;
   // TMEM: S0 | S1 | O (per 128 features)
   static constexpr int M_O = W == 64 ? 64 : 128;         // rows of the O^T tile
@@ -123,7 +123,7 @@ struct RowsCfg {
   static constexpr int SLOTS2 = (115712 - FIXED) / SLOT;
   static constexpr bool TWO = SLOTS2 >= (BLKS == 1 ? 4 : 5) && WGS == 1 && TMEM_COLS <= 256;
   static constexpr int SLOTS1 = (232448 - FIXED) / SLOT;
-  static constexpr int SLOTS = TWO ? SLOTS2 : (SLOTS1 > 16 ? 16 : SLOTS1);
+  static constexpr int SLOTS = TWO ? SLOTS2 : (SLOTS1 > 12 ? 12 : SLOTS1);
   static constexpr int MIN_BLOCKS = TWO ? 2 : 1;
   static_assert(SLOTS >= 2 * BLKS + 1, "ring: the next K tile while V waits");
   static constexpr int OFF_Q = SLOTS * SLOT;             // + buffer * Q_BYTES
@@ -145,13 +145,17 @@ struct RowsCfg {
   static constexpr int DRAIN = O_FREE + 1;
   static constexpr int SC_FULL = DRAIN + 1;            // + tile: scales (8-bit; 32 arrivals)
   static constexpr int SC_EMPTY = SC_FULL + (F8 ? kScaleTiles : 0);  // + tile: read (each softmax warp)
-  static constexpr int NBAR = SC_EMPTY + (F8 ? kScaleTiles : 0);
+  static constexpr int UNIT_FULL = SC_EMPTY + (F8 ? kScaleTiles : 0);  // + queue slot: published
+  static constexpr int UNIT_EMPTY = UNIT_FULL + kQueue;                // + queue slot: read (each consumer warp)
+  static constexpr int CONSUMERS = 4 * WGS + 3;
+  static constexpr int CLC = UNIT_EMPTY + kQueue;                      // a cancellation's response
+  static constexpr int NBAR = CLC + 1;
   static constexpr int OFF_TMEM = OFF_MISC + 8 * NBAR;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int OFF_START = OFF_TMEM + 8;         // Share
-  static_assert(8 * NBAR + 8 + 16 <= 512, "barrier area");
-  static constexpr int OFF_SEQ = OFF_MISC + 512;         // int2 [kSeqCache]
-  static constexpr int OFF_SCALES = OFF_SEQ + 8 * kSeqCache;  // [kScaleTiles][128]: k's byte, v's byte
+  static_assert(8 * NBAR + 8 <= 512 + 64, "barrier area");
+  static constexpr int OFF_QUEUE = OFF_MISC + 576;       // Unit [kQueue], then the response (16 bytes)
+  static constexpr int OFF_CLC = OFF_QUEUE + 48 * kQueue;
+  static constexpr int OFF_SCALES = OFF_CLC + 16;  // [kScaleTiles][128]: k's byte, v's byte
   static constexpr int OFF_ROWS = OFF_SCALES + SCALES;
   // per buffer: factor, output row, lse index, live [NR each], mask words [NR][4]
   static constexpr int ROWS_BYTES = (16 + 8 * kMaskWords) * NR;
@@ -235,10 +239,25 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 
-// mbar_wait by a whole warp with one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          DeviceStatus* status, int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, site));
+// The bounded wait of mbar_wait in few instructions: one that runs out raises
+// *abort to its site + 1, and the CTA records it in the device status
+// at its end.  (Every role waits in many places; with the status's recording in
+// each of them the roles' code did not fit the instruction caches, and 40 % of the
+// warps' time went to fetching instructions.)
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, volatile int* abort, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+  }
+  *abort = site + 1;
+  return false;
+}
+// By a whole warp with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int site) {
+  return __all_sync(0xffffffffu, thread_wait(bar, parity, abort, site));
 }
 
 // Largest value of the warp.
@@ -301,153 +320,49 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t (&r)[N]
 }
 
 // ---------------------------------------------------------------------------
-// Shares of the work
+// Units
 // ---------------------------------------------------------------------------
-// A sequence's lengths: prefix keys and drafted tokens, clamped.
-__device__ __forceinline__ int2 seq_lens(const RowsParams& p, int b) {
-  const int n = __ldg(p.prefix_lens + b);
-  int live = p.T;
+struct __align__(16) Unit {
+  int b;               // sequence (-1: no more units)
+  int hk, rb, split;   // key head, block of rows, split
+  int t0, t1;          // its tiles (none: a sequence without keys)
+  int n, end;          // keys of the prefix, keys any row may see
+  int live;            // drafted tokens of the sequence
+  int splits;          // of the sequence
+  int pad[2];
+};
+static_assert(sizeof(Unit) == 48, "three 16-byte words");
+
+// A sequence's part in a unit: lengths (clamped), tiles per split, splits.
+__device__ __forceinline__ void unit_keys(const RowsParams& p, Unit* w) {
+  const int n = __ldg(p.prefix_lens + w->b);
+  w->n = n < 0 ? 0 : (n > p.Lk ? p.Lk : n);
+  w->live = p.T;
   if (p.draft_lens) {
-    live = __ldg(p.draft_lens + b);
-    live = live < 0 ? 0 : (live > p.T ? p.T : live);
+    const int live = __ldg(p.draft_lens + w->b);
+    w->live = live < 0 ? 0 : (live > p.T ? p.T : live);
   }
-  return make_int2(n < 0 ? 0 : (n > p.Lk ? p.Lk : n), live);
-}
-// Keys any row may see (none without a row).
-__device__ __forceinline__ int seq_end(const RowsParams& p, int2 s) {
-  return s.y == 0 ? 0 : (p.drafts ? min(p.Lk, s.x + s.y) : s.x);
-}
-__device__ __forceinline__ int seq_tiles(const RowsParams& p, int2 s) {
-  return (seq_end(p, s) + kKeys - 1) / kKeys;
+  w->end = w->live == 0 ? 0 : (p.drafts ? min(p.Lk, w->n + w->live) : w->n);
+  const int tiles = (w->end + kKeys - 1) / kKeys;
+  const int per = (tiles + p.n_splits - 1) / p.n_splits;
+  w->splits = per > 0 ? (tiles + per - 1) / per : 1;
+  w->t0 = min(w->split * per, tiles);
+  w->t1 = min(w->t0 + per, tiles);
 }
 
-// A position in the sequences' weights: sequence and weight before it in that
-// sequence.
-struct Place {
-  int b, lo;
-  int wt;  // weight of the sequence
-};
-
-// The batch's weights, 32 sequences to a step of a warp.
-struct Scan {
-  int wt;    // this lane's sequence of the current step (0 past the last)
-  int upto;  // weight up to and with it
-};
-__device__ __forceinline__ Scan scan_step(const RowsParams& p, int b0, int before, int2* seq) {
-  const int lane = static_cast<int>(threadIdx.x & 31), b = b0 + lane;
-  Scan r = {0, 0};
-  if (b < p.B) {
-    const int2 s = seq_lens(p, b);
-    if (seq && b < kSeqCache) seq[b] = s;
-    r.wt = seq_tiles(p, s) + kUnitCost;
-  }
-  r.upto = r.wt;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, r.upto, o);
-    if (lane >= o) r.upto += y;
-  }
-  r.upto += before;
-  return r;
+__device__ __forceinline__ Unit unit_at(const RowsParams& p, int index, int blocks) {
+  Unit w;
+  const int u = index % p.units, rest = index / p.units;
+  w.hk = blocks == 1 ? u : u / blocks;
+  w.rb = u - w.hk * blocks;
+  w.split = rest / p.B;
+  w.b = rest - w.split * p.B;
+  unit_keys(p, &w);
+  return w;
 }
 
-// Whole warp: the weight of all sequences, and the last step's scan (all there is
-// when the batch has at most 32).  `seq`: where to keep the lengths of up to
-// kSeqCache sequences, or null.
-__device__ __forceinline__ int total_weight(const RowsParams& p, int2* seq, Scan* last) {
-  int before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    *last = scan_step(p, b0, before, seq);
-    before = __shfl_sync(0xffffffffu, last->upto, 31);
-  }
-  return before;
-}
-
-// Whole warp: where `pos` (less than the total) falls.
-__device__ __forceinline__ Place find_place(const RowsParams& p, int pos, Scan scan) {
-  for (int b0 = 0, before = 0;; b0 += 32) {
-    if (p.B > 32) scan = scan_step(p, b0, before, nullptr);
-    const unsigned here = __ballot_sync(0xffffffffu, scan.upto > pos);
-    if (here != 0 || b0 + 32 >= p.B) {
-      const int src = here != 0 ? __ffs(here) - 1 : 31;
-      Place q;
-      q.b = b0 + src;
-      q.wt = __shfl_sync(0xffffffffu, scan.wt, src);
-      q.lo = pos - __shfl_sync(0xffffffffu, scan.upto - scan.wt, src);
-      return q;
-    }
-    before = __shfl_sync(0xffffffffu, scan.upto, 31);
-  }
-}
-
-// Shares that are worth a group each, and where share c starts.
-__device__ __forceinline__ int share_count(int total, int most) {
-  const int n = total / kMinShare;
-  return n < 1 ? 1 : (n < most ? n : most);
-}
-__device__ __forceinline__ int share_start(int total, int shares, int c) {
-  return static_cast<int>(static_cast<long long>(total) * c / shares);
-}
-
-// A group's share (in shared memory).
-struct Share {
-  int b, lo, left, pad;
-};
-
-// The units (parts of units) of a CTA, in order: its passes over the share.
-struct UnitIter {
-  int u;              // key head and block of rows
-  int b, lo;          // sequence, weight of it done before
-  int left;           // weight left from lo on
-  int2 s;             // the sequence's lengths
-  int t0, t1, tiles;  // this part's tiles, of the sequence's
-
-  // kEmpty: units without keys are visited too (they belong to the share that
-  // holds their sequence's start)
-  template <bool kEmpty = false>
-  __device__ __forceinline__ bool start(const RowsParams& p, const Share& at, const int2* seq) {
-    u = static_cast<int>(blockIdx.x) % p.lanes;
-    if (at.left <= 0 || u >= p.units) return false;
-    b = at.b;
-    lo = at.lo;
-    left = at.left;
-    load(p, seq);
-    return here<kEmpty>() || next<kEmpty>(p, at, seq);
-  }
-  template <bool kEmpty = false>
-  __device__ __forceinline__ bool next(const RowsParams& p, const Share& at, const int2* seq) {
-    for (;;) {
-      left -= tiles + kUnitCost - lo;
-      if (left > 0) {
-        lo = 0;
-        ++b;
-      } else {
-        u += p.lanes;
-        if (u >= p.units) return false;
-        b = at.b;
-        lo = at.lo;
-        left = at.left;
-      }
-      load(p, seq);
-      if (here<kEmpty>()) return true;
-    }
-  }
-  template <bool kEmpty>
-  __device__ __forceinline__ bool here() const {
-    return t1 > t0 || (kEmpty && tiles == 0 && lo == 0);
-  }
-  __device__ __forceinline__ void load(const RowsParams& p, const int2* seq) {
-    s = b < kSeqCache ? seq[b] : seq_lens(p, b);
-    tiles = seq_tiles(p, s);
-    t0 = max(0, lo - kUnitCost);
-    t1 = left >= tiles + kUnitCost - lo ? tiles : max(0, lo + left - kUnitCost);
-  }
-  __device__ __forceinline__ int count() const { return t1 - t0; }
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
-};
-
-// A position in the ring of K and V blocks, which are loaded and used in the
-// order K(0) K(1) V(0) K(2) V(1) ... V(last) of the CTA's tiles.
+// A position in the ring of K and V blocks.  A unit's are loaded in the order
+// K(0) K(1) V(0) K(2) V(1) ... V(last).
 template <int SLOTS>
 struct Ring {
   int slot = 0;
@@ -472,8 +387,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   const uint32_t sP = s_base + C::OFF_P;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
-  Share* share = reinterpret_cast<Share*>(smem + C::OFF_START);
-  int2* seq = reinterpret_cast<int2*>(smem + C::OFF_SEQ);
+  Unit* queue = reinterpret_cast<Unit*>(smem + C::OFF_QUEUE);
   auto row_factor = [&](int buf) { return reinterpret_cast<float*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES); };
   auto row_out = [&](int buf) { return reinterpret_cast<int*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES) + NR; };
   auto row_lse = [&](int buf) { return reinterpret_cast<int*>(smem + C::OFF_ROWS + buf * C::ROWS_BYTES) + 2 * NR; };
@@ -508,6 +422,11 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     mbar_init(bar(C::Q_FIRST), SOFT);
     mbar_init(bar(C::O_FREE), SOFT);
     mbar_init(bar(C::DRAIN), 1);
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(bar(C::UNIT_FULL + i), 1);
+      mbar_init(bar(C::UNIT_EMPTY + i), C::CONSUMERS);
+    }
+    mbar_init(bar(C::CLC), 1);
     if constexpr (F8) {
       for (int i = 0; i < kScaleTiles; ++i) {
         mbar_init(bar(C::SC_FULL + i), 32);
@@ -523,164 +442,144 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     tmem_relinquish();
     tc_fence_before();
   }
-  Share at = {0, 0, 0, 0};
   if (warp == kLoadWarp) {
-    if (elect_one()) {
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
-      tma_prefetch_desc(&p.tm_k_box);
-      tma_prefetch_desc(&p.tm_v_box);
-    }
-    __syncwarp();
-    griddep_wait();  // global memory only from here on
-    Scan scan = {0, 0};
-    const int total = total_weight(p, seq, &scan);
-    const int shares = share_count(total, p.groups);
-    const int c = static_cast<int>(blockIdx.x) / p.lanes;
-    if (c < shares) {
-      int a = share_start(total, shares, c), z = share_start(total, shares, c + 1);
-      Place q = find_place(p, a, scan);
-      if (p.whole_units) {
-        // both ends to the nearer border of a sequence
-        auto border = [&](int pos, const Place& x) { return pos - x.lo + (2 * x.lo >= x.wt ? x.wt : 0); };
-        a = border(a, q);
-        if (2 * q.lo >= q.wt) ++q.b;
-        q.lo = 0;
-        if (z < total) z = border(z, find_place(p, z, scan));
-      }
-      at.b = q.b;
-      at.lo = q.lo;
-      at.left = z - a;
-    }
-    if (lane == 0) *share = at;
-    __threadfence_block();
-    __syncwarp();
-    // the other warps learn the share; this one goes on to its loads
+    // (this warp goes on to its loads without the tensor memory's address)
     asm volatile("barrier.cta.arrive 15, %0;" ::"n"(C::THREADS) : "memory");
   } else {
     asm volatile("barrier.cta.sync 15, %0;" ::"n"(C::THREADS) : "memory");
     tc_fence_after();
-    at = *share;
-    griddep_wait();
   }
-  const uint32_t tmem = *tmem_slot;  // (not read by the load warp, which did not wait)
-  // the next launch may set itself up (it waits for this grid before it touches
-  // global memory)
+  const uint32_t tmem = *tmem_slot;  // (not the load warp's, which did not wait)
+  griddep_wait();  // global memory only from here on
+  // the next launch may set itself up once every unit is taken (it waits for this
+  // grid before it touches global memory)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int blks = C::BLKS == 1 ? 1 : (p.d + 127) / 128;  // 128-feature blocks in use
-  auto unit_hk = [&](const UnitIter& it) { return blocks == 1 ? it.u : it.u / blocks; };
-  auto unit_rb = [&](const UnitIter& it) { return blocks == 1 ? 0 : it.u % blocks; };
-
+  // The k-th published unit (each consumer warp takes each, in order); b = -1 at
+  // the end of the work or when the CTA gave up.
+  auto take = [&](int k, int site) {
+    const int slot = k % kQueue;
+    Unit w;
+    if (!warp_wait(bar(C::UNIT_FULL + slot), (k / kQueue) & 1, abort_flag, site + C::UNIT_FULL + slot)) {
+      w.b = -1;
+      return w;
+    }
+    const int4* src = reinterpret_cast<const int4*>(queue + slot);
+    int4* dst = reinterpret_cast<int4*>(&w);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) dst[i] = src[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::UNIT_EMPTY + slot));
+    return w;
+  };
   // Phase of Q_FULL for unit k (the first unit has a barrier of its own).
   auto q_phase = [](int k) { return static_cast<uint32_t>(((k >> 1) - ((k & 1) ? 0 : 1)) & 1); };
   // Buffer and phase of P and its product for tile t.
   auto p_buf = [](uint32_t t) { return C::P_BUFS == 2 ? t & 1 : 0u; };
   auto p_phase = [](uint32_t t) { return C::P_BUFS == 2 ? (t >> 1) & 1 : t & 1; };
   // Output row of row r of a unit (-1 past the last), t: its drafted token.
-  auto out_row = [&](const UnitIter& it, int r, int* t) {
-    const int gr = unit_rb(it) * NR + r;
+  auto out_row = [&](const Unit& it, int r, int* t) {
+    const int gr = it.rb * NR + r;
     *t = -1;
     if (gr >= n_rows) return -1;
     *t = p.G == 1 ? gr : gr / p.G;
-    return (it.b * p.T + *t) * p.H + unit_hk(it) * p.G + (gr - *t * p.G);
+    return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
   };
   // A unit's Q, output rows and mask words into buffer `buf`, by thread qt of a
   // multiple of 32 (eight threads per row); false when `buffer_free` gave up.
-  auto prepare_q = [&](auto threads, const UnitIter& it, int buf, int qt, auto buffer_free) {
+  auto prepare_q = [&](auto threads, const Unit& it, int buf, int qt, auto buffer_free) {
     constexpr int RP = decltype(threads)::value / 8;
     constexpr int PER = W / 64;                    // 16-byte pieces of a row per thread
-    constexpr int MOST = PER > 2 ? 2 : 4;
-    constexpr int ROUNDS = NR / RP < 1 ? 1 : NR / RP;
-    constexpr int BATCH = ROUNDS < MOST ? ROUNDS : MOST;  // rows per thread in flight
     const int sub = qt & 7;
-    const int hk = unit_hk(it);
     const uint32_t sQ = s_base + C::OFF_Q + buf * C::Q_BYTES;
     if (NR < RP && (qt >> 3) >= NR) return buffer_free();  // (whole warps)
-    // (the first rows are requested before the buffer is free)
-    for (int rr = 0; rr < NR; rr += RP * BATCH) {
-      uint4 v[BATCH][PER];
-      int t[BATCH], out[BATCH];
+    // ask all rows into L2, then take one after the other
+#pragma unroll 1
+    for (int rr = 0; rr < NR; rr += RP) {
+      int t;
+      const int out = out_row(it, rr + (qt >> 3), &t);
+      if (out >= 0 && 64 * sub < p.d)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t*>(p.q) +
+                                                      static_cast<long long>(out) * p.d + 64 * sub));
+    }
+    if (!buffer_free()) return false;
+#pragma unroll 1
+    for (int rr = 0; rr < NR; rr += RP) {
+      const int r = rr + (qt >> 3);
+      int t;
+      const int out = out_row(it, r, &t);
+      const bool live = t >= 0 && t < it.live;
+      uint4 v[PER];
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                        static_cast<long long>(max(out, 0)) * p.d);
 #pragma unroll
-      for (int y = 0; y < BATCH; ++y) {
-        out[y] = out_row(it, rr + y * RP + (qt >> 3), &t[y]);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                          static_cast<long long>(max(out[y], 0)) * p.d);
+      for (int z = 0; z < PER; ++z) {
+        // 8-bit: 16 elements to a thread, in two pieces; bf16: 8
+        const int piece = F8 ? 2 * (sub + 8 * (z >> 1)) + (z & 1) : sub + 8 * z;
+        v[z] = make_uint4(0, 0, 0, 0);
+        if (out >= 0 && 8 * piece < p.d) v[z] = __ldg(src + piece);
+      }
+      if (sub == 0) {
+        row_out(buf)[r] = out;
+        row_lse(buf)[r] = out < 0 ? 0 : (it.b * p.H + out % p.H) * p.T + t;
+        row_live(buf)[r] = live;
+      }
+      if (sub < kMaskWords) {
+        // (a chain's words: bits 0 .. t)
+        uint64_t word = 0;
+        if (live && p.tree_mask) {
+          if (sub < p.words)
+            word = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t) * p.words + sub);
+        } else if (live) {
+          const int bits = t + 1 - 64 * sub;
+          word = bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
+        }
+        row_mask(buf)[r * kMaskWords + sub] = word;
+      }
+      if constexpr (F8) {
+        float amax = 0.f;
 #pragma unroll
         for (int z = 0; z < PER; ++z) {
-          // 8-bit: 16 elements to a thread, in two pieces; bf16: 8
-          const int piece = F8 ? 2 * (sub + 8 * (z >> 1)) + (z & 1) : sub + 8 * z;
-          v[y][z] = make_uint4(0, 0, 0, 0);
-          if (out[y] >= 0 && 8 * piece < p.d) v[y][z] = __ldg(src + piece);
+          const uint32_t q4[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q4[e])), fabsf(bf16_hi(q4[e]))));
         }
-      }
-      if (rr == 0 && !buffer_free()) return false;
 #pragma unroll
-      for (int y = 0; y < BATCH; ++y) {
-        const int r = rr + y * RP + (qt >> 3);
-        const bool live = t[y] >= 0 && t[y] < it.s.y;
-        if (sub == 0) {
-          row_out(buf)[r] = out[y];
-          row_lse(buf)[r] = out[y] < 0 ? 0 : (it.b * p.H + out[y] % p.H) * p.T + t[y];
-          row_live(buf)[r] = live;
-        }
-        if (sub < kMaskWords) {
-          // (a chain's words: bits 0 .. t)
-          uint64_t word = 0;
-          if (live && p.tree_mask) {
-            if (sub < p.words)
-              word = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t[y]) * p.words + sub);
-          } else if (live) {
-            const int bits = t[y] + 1 - 64 * sub;
-            word = bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
-          }
-          row_mask(buf)[r * kMaskWords + sub] = word;
-        }
-        if constexpr (F8) {
-          float amax = 0.f;
+        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // q 2^-e with the largest magnitude in [128, 256)
+        const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7, -100);
+        const float inv = pow2i(-e);
+        if (sub == 0) row_factor(buf)[r] = pow2i(e) * p.scale_log2;
 #pragma unroll
-          for (int z = 0; z < PER; ++z) {
-            const uint32_t q4[4] = {v[y][z].x, v[y][z].y, v[y][z].z, v[y][z].w};
+        for (int u = 0; u < PER / 2; ++u) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q4[e])), fabsf(bf16_hi(q4[e]))));
-          }
+          for (int z = 0; z < 2; ++z) {
+            const uint4 w4 = v[2 * u + z];
+            const uint32_t q4[4] = {w4.x, w4.y, w4.z, w4.w};
+            uint32_t a[4], c2[4];
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // q 2^-e with the largest magnitude in [128, 256)
-          const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7, -100);
-          const float inv = pow2i(-e);
-          if (sub == 0) row_factor(buf)[r] = pow2i(e) * p.scale_log2;
-#pragma unroll
-          for (int u = 0; u < PER / 2; ++u) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint4 w4 = v[y][2 * u + z];
-              const uint32_t q4[4] = {w4.x, w4.y, w4.z, w4.w};
-              uint32_t a[4], c2[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float x0 = bf16_lo(q4[x]) * inv, x1 = bf16_hi(q4[x]) * inv;
-                a[x] = pack_e4m3x2(x0, x1);
-                const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[x]));
-                c2[x] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
-              }
-              hi[2 * z] = a[0] | (a[1] << 16);
-              hi[2 * z + 1] = a[2] | (a[3] << 16);
-              lo[2 * z] = c2[0] | (c2[1] << 16);
-              lo[2 * z + 1] = c2[2] | (c2[3] << 16);
+            for (int x = 0; x < 4; ++x) {
+              const float x0 = bf16_lo(q4[x]) * inv, x1 = bf16_hi(q4[x]) * inv;
+              a[x] = pack_e4m3x2(x0, x1);
+              const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[x]));
+              c2[x] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
             }
-            const uint32_t to = sQ + (sub + 8 * u) * (C::NQ * 16) + r * 16;
-            st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(to + NR * 16, lo[0], lo[1], lo[2], lo[3]);
+            hi[2 * z] = a[0] | (a[1] << 16);
+            hi[2 * z + 1] = a[2] | (a[3] << 16);
+            lo[2 * z] = c2[0] | (c2[1] << 16);
+            lo[2 * z + 1] = c2[2] | (c2[3] << 16);
           }
-        } else {
-#pragma unroll
-          for (int z = 0; z < PER; ++z)
-            st_shared_v4(sQ + (sub + 8 * z) * (C::NQ * 16) + r * 16, v[y][z].x, v[y][z].y, v[y][z].z,
-                         v[y][z].w);
+          const uint32_t to = sQ + (sub + 8 * u) * (C::NQ * 16) + r * 16;
+          st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(to + NR * 16, lo[0], lo[1], lo[2], lo[3]);
         }
+      } else {
+#pragma unroll
+        for (int z = 0; z < PER; ++z)
+          st_shared_v4(sQ + (sub + 8 * z) * (C::NQ * 16) + r * 16, v[z].x, v[z].y, v[z].z, v[z].w);
       }
     }
     return true;
@@ -705,7 +604,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           if (blk >= blks) break;
           const int s = ring.slot;
           ok = ok && (loaded < C::SLOTS ||
-                      mbar_wait(bar(C::EMPTY + s), ring.phase ^ 1, abort_flag, p.status, site + C::EMPTY + s));
+                      thread_wait(bar(C::EMPTY + s), ring.phase ^ 1, abort_flag, site + C::EMPTY + s));
           if (!ok) return;
           const int f0 = blk * 128;
           const int chunks = (min(p.d - f0, 128) * C::EB + 127) / 128;
@@ -725,29 +624,46 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           ring.advance();
         }
       };
-      UnitIter it;
-      bool any = false;
-      int v_key = 0, v_end = 0, v_hk = 0, v_b = 0;  // the tile whose V is next
-      for (bool more = it.start(p, at, seq); more && ok; more = it.next(p, at, seq)) {
-        const int hk = unit_hk(it), end = seq_end(p, it.s), b = it.b, t1 = it.t1;
-        for (int x = it.t0; x < t1 && ok; ++x) {
-          load(&p.tm_k, &p.tm_k_box, x * kKeys, end, hk, b);
-          if (any && ok) load(&p.tm_v, &p.tm_v_box, v_key, v_end, v_hk, v_b);
-          any = true;
-          v_key = x * kKeys;
-          v_end = end;
-          v_hk = hk;
-          v_b = b;
-        }
-      }
-      if (any && ok) load(&p.tm_v, &p.tm_v_box, v_key, v_end, v_hk, v_b);
-      // every copy started must land before the CTA exits
+      // The units: this CTA's own, then those of CTAs that have not started; the
+      // next is asked for while one's tiles are loaded.
       volatile int never = 0;
+      int index = static_cast<int>(blockIdx.x), published = 0;
+      auto publish = [&](const Unit& w) {
+        const int slot = published % kQueue;
+        ok = ok && (published < kQueue ||
+                    thread_wait(bar(C::UNIT_EMPTY + slot), ((published / kQueue) - 1) & 1, abort_flag, site + C::UNIT_EMPTY + slot));
+        if (!ok) return;
+        queue[slot] = w;
+        mbar_arrive(bar(C::UNIT_FULL + slot));
+        ++published;
+      };
+      for (uint32_t asked = 0;; ++asked) {
+        mbar_arrive_expect_tx(bar(C::CLC), 16);
+        clc_try_cancel(s_base + C::OFF_CLC, bar(C::CLC));
+        const Unit w = unit_at(p, index, blocks);
+        if (w.split < w.splits) {
+          publish(w);
+          for (int x = w.t0; x < w.t1 && ok; ++x) {
+            load(&p.tm_k, &p.tm_k_box, x * kKeys, w.end, w.hk, w.b);
+            if (x > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (x - 1) * kKeys, w.end, w.hk, w.b);
+          }
+          if (w.t1 > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (w.t1 - 1) * kKeys, w.end, w.hk, w.b);
+        }
+        // (the response lands whatever happens: wait for it even when giving up)
+        ok = mbar_wait(bar(C::CLC), asked & 1, &never, p.status, site + C::CLC) && ok && *abort_flag == 0;
+        if (!ok) break;
+        index = clc_query_first_ctaid_x(s_base + C::OFF_CLC);  // -1: none was left
+        if (index < 0) break;
+        fence_proxy_async_smem();  // (the next response overwrites this one)
+      }
+      Unit end;
+      end.b = -1;
+      publish(end);
+      // every copy started must land before the CTA exits
       for (int x = min(loaded, C::SLOTS); x > 0; --x) {
         // (the slot x before the next one)
         const int s = ring.slot >= x ? ring.slot - x : ring.slot - x + C::SLOTS;
-        mbar_wait(bar(C::FULL + s), ring.slot >= x ? ring.phase : ring.phase ^ 1, &never, p.status,
-                  site + C::FULL + s);
+        mbar_wait(bar(C::FULL + s), ring.slot >= x ? ring.phase : ring.phase ^ 1, &never, p.status, site + C::FULL + s);
       }
     }
     __syncwarp();
@@ -771,7 +687,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     Ring<C::SLOTS> ring;
     bool ok = true;
     auto wait = [&](int id, uint32_t parity) {
-      ok = ok && warp_wait(bar(id), parity, abort_flag, p.status, site + id);
+      ok = ok && warp_wait(bar(id), parity, abort_flag, site + id);
     };
     // scores of the next tile into S buffer `s_buf`; `q`: its unit's Q; `done`: the
     // barrier to tell when the unit's last scores are done, or -1
@@ -801,25 +717,41 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       }
     };
     auto unit_q = [&](int k) { return dq0 + static_cast<uint64_t>(((k & 1) * C::Q_BYTES) >> 4); };
-    UnitIter it;
-    bool more = it.start(p, at, seq);
-    int k = 0;             // units
-    uint32_t t = 0;        // tiles
-    if (more) {
+    int taken = 0;
+    // tiles of the next unit that has any (0: no more units)
+    auto next_tiles = [&]() {
+      for (;;) {
+        const Unit w = take(taken++, site);
+        if (w.b < 0) return 0;
+        if (w.t1 > w.t0) return w.t1 - w.t0;
+      }
+    };
+    int k = 0;        // units with tiles
+    uint32_t t = 0;   // tiles
+    int n = next_tiles();
+    if (n > 0) {
       wait(C::Q_FIRST, 0);
-      if (ok) issue_s(0, unit_q(0), it.count() == 1 ? C::Q_EMPTY : -1);
+      if (ok) issue_s(0, unit_q(0), n == 1 ? C::Q_EMPTY : -1);
     }
-    while (more && ok) {
-      const int n = it.count();
-      more = it.next(p, at, seq);
-      const int n_next = more ? it.count() : 0;
+    while (n > 0 && ok) {
+      int n_next = 0;
       for (int i = 0; i < n && ok; ++i, ++t) {
-        // the next tile's scores, of this unit or the next
+        // The next tile's scores, of this unit or the next (whose first K lies
+        // behind this unit's last V in the ring).
+        Ring<C::SLOTS> v;
         if (i + 1 < n) {
           issue_s((t + 1) & 1, unit_q(k), i + 2 == n ? C::Q_EMPTY + (k & 1) : -1);
-        } else if (n_next > 0) {
-          wait(C::Q_FULL + ((k + 1) & 1), q_phase(k + 1));
-          if (ok) issue_s((t + 1) & 1, unit_q(k + 1), n_next == 1 ? C::Q_EMPTY + ((k + 1) & 1) : -1);
+          v = ring;
+        } else {
+          v = ring;
+#pragma unroll
+          for (int blk = 0; blk < C::BLKS; ++blk)
+            if (blk < blks) ring.advance();
+          n_next = next_tiles();
+          if (n_next > 0) {
+            wait(C::Q_FULL + ((k + 1) & 1), q_phase(k + 1));
+            if (ok) issue_s((t + 1) & 1, unit_q(k + 1), n_next == 1 ? C::Q_EMPTY + ((k + 1) & 1) : -1);
+          }
         }
         // (O is free once the last unit's epilogue has read it)
         if (i == 0 && k > 0) wait(C::O_FREE, (k - 1) & 1);
@@ -828,24 +760,26 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
 #pragma unroll
         for (int blk = 0; blk < C::BLKS; ++blk) {
           if (blk >= blks) break;
-          wait(C::FULL + ring.slot, ring.phase);
+          wait(C::FULL + v.slot, v.phase);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t d = tmem + C::TM_O + blk * C::NP;
-            const uint64_t a = dv0 + static_cast<uint64_t>((ring.slot * C::SLOT) >> 4);
+            const uint64_t a = dv0 + static_cast<uint64_t>((v.slot * C::SLOT) >> 4);
 #pragma unroll
             for (int ks = 0; ks < kKeys / KSTEP; ++ks)
               umma<F8>(d, a + static_cast<uint64_t>((ks * KSTEP * 128) >> 4),
                        pd + static_cast<uint64_t>((ks * KSTEP * 16) >> 4), idesc_o,
                        (i > 0 || ks > 0) ? 1u : 0u);
             if (blk == blks - 1) umma_commit(bar(C::PV_DONE + p_buf(t)));
-            umma_commit(bar(C::EMPTY + ring.slot));
+            umma_commit(bar(C::EMPTY + v.slot));
           }
           __syncwarp();
-          ring.advance();
+          v.advance();
         }
+        if (i + 1 < n) ring = v;
       }
+      n = n_next;
       ++k;
     }
     // every tensor-core operation issued must be complete before TMEM is freed
@@ -860,44 +794,42 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       uint16_t* ring = reinterpret_cast<uint16_t*>(smem + C::OFF_SCALES);
       int t = 0;
       bool ok = true;
-      // The next 32 tiles of a unit are asked into L2 ahead (a plain load waits
-      // behind the ring's copies in the DRAM queues, several tiles' time).
-      auto ahead = [&](const UnitIter& w, int tile) {
-        const long long from = (static_cast<long long>(w.b) * p.H_kv + unit_hk(w)) * p.Lk + (tile + lane) * kKeys;
+      // 32 tiles' scales into L2 (a plain load waits behind the ring's copies in
+      // the DRAM queues, several tiles' time)
+      auto ahead = [&](const Unit& w, int tile) {
+        const long long from = (static_cast<long long>(w.b) * p.H_kv + w.hk) * p.Lk + (tile + lane) * kKeys;
         if (tile + lane < w.t1) {
           asm volatile("prefetch.global.L2 [%0];" ::"l"(p.k_scale + from));
           asm volatile("prefetch.global.L2 [%0];" ::"l"(p.v_scale + from));
         }
       };
-      UnitIter it;
-      for (bool more = it.start(p, at, seq); more && ok;) {
-        UnitIter next = it;
-        more = next.next(p, at, seq);
-        if (more) ahead(next, next.t0);
-        const int end = seq_end(p, it.s);
-        const long long row = (static_cast<long long>(it.b) * p.H_kv + unit_hk(it)) * p.Lk;
-        // (four tiles' loads in flight)
-        for (int x = it.t0; x < it.t1 && ok; x += 4) {
+      for (int taken = 0; ok; ++taken) {
+        const Unit it = take(taken, site);
+        if (it.b < 0) break;
+        ahead(it, it.t0);
+        const long long row = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
+        // (two tiles' loads in flight)
+        for (int x = it.t0; x < it.t1 && ok; x += 2) {
           if (((x - it.t0) & 31) == 16) ahead(it, x + 16);
-          const int m = min(4, it.t1 - x);
-          uint32_t k4[4][4], v4[4][4];
+          const int m = min(2, it.t1 - x);
+          uint32_t k4[2][4], v4[2][4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const int key = (x + y) * kKeys + 32 * z + lane;
               k4[y][z] = v4[y][z] = 127;
-              if (y < m && key < end) {
+              if (y < m && key < it.end) {
                 k4[y][z] = __ldg(p.k_scale + row + key);
                 v4[y][z] = __ldg(p.v_scale + row + key);
               }
             }
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
+          for (int y = 0; y < 2; ++y) {
             if (y >= m || !ok) break;
             const int slot = t % kScaleTiles;
             ok = t < kScaleTiles || warp_wait(bar(C::SC_EMPTY + slot), ((t / kScaleTiles) - 1) & 1, abort_flag,
-                                              p.status, site + C::SC_EMPTY + slot);
+                                              site + C::SC_EMPTY + slot);
             if (!ok) break;
 #pragma unroll
             for (int z = 0; z < 4; ++z)
@@ -906,17 +838,17 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             ++t;
           }
         }
-        it = next;
       }
     } else {
     // ---- the next units' Q, output rows and mask words
     const int site = kRoleRowsQ * 64;
     constexpr int QT = C::Q_THREADS;
     const int qt = tid - 32 * kQWarp;
-    UnitIter it;
     int k = 0;  // units with keys
-    for (bool more = it.start<true>(p, at, seq); more; more = it.next<true>(p, at, seq)) {
-      if (it.tiles == 0) {
+    for (int taken = 0;; ++taken) {
+      const Unit it = take(taken, site);
+      if (it.b < 0) break;
+      if (it.t1 == it.t0) {
         // no key at all: output 0, log-sum-exp -inf
         for (int r = qt >> 3; r < NR; r += QT / 8) {
           int t;
@@ -931,8 +863,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       const int buf = k & 1;
       if (k > 0) {  // (the softmax threads prepare the first)
         const bool ok = prepare_q(std::integral_constant<int, QT>{}, it, buf, qt, [&]() {
-          return k < 2 || warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, p.status,
-                                    site + C::Q_EMPTY + buf);
+          return k < 2 || warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, site + C::Q_EMPTY + buf);
         });
         if (!ok) break;
         fence_proxy_async_smem();
@@ -949,21 +880,24 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     constexpr int RPT = C::RPT, GW = C::GW, GROUPS = C::GROUPS;
     const int wg = warp >> 2, r0 = wg * RPT, kt = tid & 127, w4 = warp & 3;
     const uint32_t nbar = 1 + wg;  // this warpgroup's named barrier
-    const int group = static_cast<int>(blockIdx.x) / p.lanes;
+    const long long total_rows = static_cast<long long>(p.B) * p.T * p.H;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
     bool ok = true;
     auto wait = [&](int id, uint32_t parity) {
-      ok = ok && mbar_wait(bar(id), parity, abort_flag, p.status, site + id);
+      ok = ok && thread_wait(bar(id), parity, abort_flag, site + id);
     };
     if (kt < RPT) row_ref[r0 + kt] = 0.f;
     named_barrier(nbar, 128);
-    UnitIter it;
-    int k = 0;       // units
+    int k = 0;       // units with keys
     uint32_t t = 0;  // tiles
-    for (bool more = it.start(p, at, seq); more; more = it.next(p, at, seq), ++k) {
-      const int buf = k & 1, n = it.count();
-      const int rows_here = min(NR, n_rows - unit_rb(it) * NR) - r0;  // this warpgroup's (may be <= 0)
-      const int k_end = seq_end(p, it.s);
+    for (int taken = 0;; ++taken) {
+      const Unit it = take(taken, site);
+      if (it.b < 0) break;
+      const int n = it.t1 - it.t0;
+      if (n == 0) continue;
+      const int buf = k & 1;
+      const int rows_here = min(NR, n_rows - it.rb * NR) - r0;  // this warpgroup's (may be <= 0)
+      const int k_end = it.end;
       float l[RPT];
 #pragma unroll
       for (int r = 0; r < RPT; ++r) l[r] = 0.f;
@@ -994,12 +928,12 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           vinv = __uint_as_float((254u - vb) << 23);
         }
         // which of this warpgroup's rows see the key (a tile inside the prefix: all)
-        const bool masked = (it.t0 + i + 1) * kKeys > it.s.x;
+        const bool masked = (it.t0 + i + 1) * kKeys > it.n;
         uint32_t sees = ~0u;
-        if (masked && key >= it.s.x) {
+        if (masked && key >= it.n) {
           sees = 0;
           if (key < k_end) {
-            const int j = key - it.s.x;
+            const int j = key - it.n;
             const uint64_t* words = row_mask(buf) + r0 * kMaskWords + (j >> 6);
 #pragma unroll 8
             for (int r = 0; r < RPT; ++r)
@@ -1110,7 +1044,9 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           if (i > 0) {
             wait(C::PV_DONE + p_buf(t - 1), p_phase(t - 1));
             tc_fence_after();
+#pragma unroll 1
             for (int c = 0; c < C::BLKS * C::PP; ++c)
+#pragma unroll 1
               for (int g = 0; g < GROUPS; ++g) {
                 if (g * GW >= rows_here) continue;
                 const uint32_t o_at =
@@ -1187,17 +1123,15 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         if (wg == 0 && (it.t0 + i + 1) * kKeys > k_end) {
           // a ragged last tile: the V rows past the last key may hold anything
           // (0 * NaN would be NaN)
-          // (before V(t) in the ring: K(0) .. K(t), K(t + 1) if there is one,
-          // V(0) .. V(t - 1))
-          UnitIter next = it;
-          const int before = 2 * static_cast<int>(t) + 1 + (i + 1 < n || next.next(p, at, seq) ? 1 : 0);
+          // (a unit's last V is its last item in the ring)
+          const int before = 2 * static_cast<int>(t) + 1;
           for (int blk = 0; blk < blks; ++blk) {
             const int item = before * blks + blk, sl = item % C::SLOTS;
             wait(C::FULL + sl, (item / C::SLOTS) & 1);
             if (key >= k_end) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < C::SLOT / C::CHUNK; ++c)
-#pragma unroll
+#pragma unroll 1
                 for (int u = 0; u < 8; ++u)
                   st_shared_v4(s_base + sl * C::SLOT + c * C::CHUNK + kt * 128 + u * 16, 0, 0, 0, 0);
             }
@@ -1217,10 +1151,9 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       tc_fence_after();
       const bool good = ok && *abort_flag == 0;
       named_barrier(nbar, 128);
-      const bool whole = it.whole();
-      // the share's partial: the second where the sequence starts in it, else the first
-      const long long part =
-          (static_cast<long long>(group * 2 + (it.t0 == 0 ? 1 : 0)) * p.units + it.u) * NR + r0;
+      const bool whole = it.splits == 1;
+      const int* outs = row_out(buf) + r0;
+      const long long part = it.split * total_rows;  // the split's partials
       if (kt < rows_here && kt < RPT) {
         const float4 l4 = *reinterpret_cast<const float4*>(red + (r0 + kt) * 4);
         float L = l4.x + l4.y + l4.z + l4.w;
@@ -1231,8 +1164,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         }
         shift[kt] = L > 0.f ? (whole ? 1.f / L : 1.f) : 0.f;
         if (!whole) {
-          p.part_m[part + kt] = L > 0.f ? m : -INFINITY;
-          p.part_l[part + kt] = L;
+          p.part_m[part + outs[kt]] = L > 0.f ? m : -INFINITY;
+          p.part_l[part + outs[kt]] = L;
         } else if (p.lse) {
           p.lse[row_lse(buf)[r0 + kt]] = L > 0.f ? (m + __log2f(L)) * 0.69314718055994531f : -INFINITY;
         }
@@ -1241,50 +1174,39 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       named_barrier(nbar, 128);
       const int f0 = C::M_O == 64 ? w4 * 16 + lane : kt;
       const bool holds = C::M_O == 128 || lane < 16;
-#pragma unroll
-      for (int blk = 0; blk < C::BLKS; ++blk) {
-        if (blk * 128 >= p.d) continue;
+      // (eight rows at a time and no unrolling past that: this runs once per unit)
+#pragma unroll 1
+      for (int blk = 0; blk < blks; ++blk) {
         const int f = blk * 128 + f0;
         const bool stores = holds && f < p.d;
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-          if (g * GW >= rows_here) continue;
-          float o[GW];
-          uint32_t y[C::PP][GW];
+#pragma unroll 1
+        for (int g = 0; g < rows_here; g += 8) {
+          if (g >= RPT) break;
+          uint32_t y[C::PP][8];
 #pragma unroll
           for (int piece = 0; piece < C::PP; ++piece)
-            tmem_ld_cols<GW>(t_lane + C::TM_O + blk * C::NP + piece * NR + r0 + g * GW, y[piece]);
+            tmem_ld_cols<8>(t_lane + C::TM_O + blk * C::NP + piece * NR + r0 + g, y[piece]);
           tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < GW; ++r) {
-            o[r] = __uint_as_float(y[C::PP - 1][r]);
-#pragma unroll
-            for (int piece = C::PP - 2; piece >= 0; --piece) o[r] += __uint_as_float(y[piece][r]);
-          }
           if (!stores) continue;
-          const int rows = min(GW, rows_here - g * GW);
-          if (whole) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + f;
-            const int* outs = row_out(buf) + r0 + g * GW;
 #pragma unroll
-            for (int r = 0; r < GW; ++r) {
-              if (r >= rows) break;
-              const float a = shift[g * GW + r];
-              out[static_cast<long long>(outs[r]) * p.d] = __float2bfloat16_rn(a > 0.f ? o[r] * a : 0.f);
-            }
-          } else {
-            float* out = p.part_o + (part + g * GW) * W + f;
+          for (int r = 0; r < 8; ++r) {
+            if (g + r >= rows_here) break;
+            float o = __uint_as_float(y[C::PP - 1][r]);
 #pragma unroll
-            for (int r = 0; r < GW; ++r) {
-              if (r >= rows) break;
-              out[r * W] = shift[g * GW + r] > 0.f ? o[r] : 0.f;
-            }
+            for (int piece = C::PP - 2; piece >= 0; --piece) o += __uint_as_float(y[piece][r]);
+            const float a = shift[g + r];
+            const long long row = outs[g + r];
+            if (whole)
+              static_cast<__nv_bfloat16*>(p.out)[row * p.d + f] = __float2bfloat16_rn(a > 0.f ? o * a : 0.f);
+            else
+              p.part_o[(part + row) * W + f] = a > 0.f ? o : 0.f;
           }
         }
       }
       tc_fence_before();
       mbar_arrive(bar(C::O_FREE));
       mbar_arrive(bar(C::Q_EMPTY + buf));
+      ++k;
     }
   }
   __syncthreads();
@@ -1292,105 +1214,72 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+  if (tid == 0 && *abort_flag != 0 && atomicCAS(&p.status->code, 0, 7 /* MHA_ERR_TIMEOUT */) == 0) {
+    p.status->site = *abort_flag - 1;
+    p.status->block = static_cast<int>(blockIdx.x);
+  }
 }
 
-// Merges the partials of a unit of a cut sequence, kCombineRows rows per block:
-//   o = sum_x 2^(m_x - M) o_x / sum_x 2^(m_x - M) l_x,  M = max_x m_x.
-// blockIdx.x = cut * units + unit, blockIdx.y = block of rows; a cut is a sequence
-// or, where the batch has more sequences than the shares have borders, a border
-// (the first inside its sequence).  With c the first share that starts inside the
-// sequence, the partials are the second of share c - 1 and the first of those from
-// c on that start inside it.  A row has kCombineWarps warps, which divide its
-// partials (many when one long sequence is spread over the machine).
-constexpr int kCombineRows = 4, kCombineWarps = 4;
-__host__ __device__ __forceinline__ bool combine_by_sequence(int B, int groups) { return B < groups; }
-template <int W, int NR>
-__global__ void __launch_bounds__(32 * kCombineRows * kCombineWarps)
-    rows_combine_kernel(const __grid_constant__ RowsParams p) {
+// Merges a row's partials:
+//   o = sum_x 2^(m_x - M) o_x / sum_x 2^(m_x - M) l_x,  M = max_x m_x
+// over the splits x of its sequence.  A row has WARPS warps of an eight-warp block,
+// which divide its partials (eight when one long sequence is spread over the
+// machine, one when there are few splits and many rows).
+template <int W, int WARPS>
+__global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsParams p) {
   constexpr int EPL = W / 32;
-  __shared__ float sums[kCombineRows * kCombineWarps][W + 1];
+  __shared__ float sums[8][WARPS > 1 ? W + 1 : 1];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int cut = static_cast<int>(blockIdx.x) / p.units;
-  const int u = static_cast<int>(blockIdx.x) % p.units;
-  const int n_rows = p.T * p.G;
-  const int blocks = (n_rows + NR - 1) / NR;
-  const int hk = u / blocks, rb = u % blocks;
-  const int r = kCombineRows * static_cast<int>(blockIdx.y) + warp / kCombineWarps;  // row of the unit
-  const int part = warp % kCombineWarps;
-  const int gr = rb * NR + r;
-  const bool mine = r < NR && gr < n_rows;
-  const int t = mine ? gr / p.G : 0, h = hk * p.G + (gr - t * p.G);
-  griddep_wait();  // the shares' partials are complete and visible
-  Scan scan = {0, 0};
-  const int total = total_weight(p, nullptr, &scan);
-  const int shares = share_count(total, p.groups);
-  // the sequence, where it starts, and the first share that starts past its
-  // first tile
-  int b, base, wt, c;
-  if (combine_by_sequence(p.B, p.groups)) {
-    b = cut;
-    if (p.B > 32) {
-      for (int b0 = 0, before = 0; b0 <= b; b0 += 32) {
-        scan = scan_step(p, b0, before, nullptr);
-        before = __shfl_sync(0xffffffffu, scan.upto, 31);
-      }
-    }
-    wt = __shfl_sync(0xffffffffu, scan.wt, b & 31);
-    base = __shfl_sync(0xffffffffu, scan.upto, b & 31) - wt;
-    c = static_cast<int>((static_cast<long long>(base + kUnitCost + 1) * shares + total - 1) / total);
-    if (c >= shares || share_start(total, shares, c) >= base + wt) return;  // not cut
-  } else {
-    c = cut + 1;
-    if (c >= shares) return;
-    const int pos = share_start(total, shares, c);
-    const Place q = find_place(p, pos, scan);
-    b = q.b;
-    base = pos - q.lo;
-    wt = q.wt;
-    if (q.lo <= kUnitCost || share_start(total, shares, c - 1) - base > kUnitCost) return;
-  }
-  // the first share at or past the sequence's end
-  const int last = static_cast<int>((static_cast<long long>(base + wt) * shares + total - 1) / total);
-  const int pieces = 1 + min(last, shares) - c;
+  const int part = warp % WARPS;
+  const long long rows = static_cast<long long>(p.B) * p.T * p.H;
+  const long long row = static_cast<long long>(blockIdx.x) * (8 / WARPS) + warp / WARPS;
+  const int bt = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<long long>(bt) * p.H);
+  Unit w;
+  w.b = bt / p.T;
+  w.split = 0;
+  w.splits = 1;
+  griddep_wait();  // the splits' partials are complete and visible
+  if (row < rows) unit_keys(p, &w);
+  const int splits = w.splits;
   float o[EPL], L = 0.f, M = -INFINITY;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
-  if (mine) {
-    auto slot = [&](int x) {
-      return (static_cast<long long>(x == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + x)) * p.units + u) * NR + r;
-    };
-    for (int x = lane; x < pieces; x += 32) M = fmaxf(M, p.part_m[slot(x)]);
+  if (splits > 1) {
+    for (int x = lane; x < splits; x += 32) M = fmaxf(M, p.part_m[x * rows + row]);
     M = warp_max(M);
     if (M != -INFINITY) {
 #pragma unroll 4
-      for (int x = part; x < pieces; x += kCombineWarps) {
-        const long long at = slot(x);
-        const float w = ex2_approx(p.part_m[at] - M);  // 0 for a part the row sees nothing of
-        L = fmaf(w, p.part_l[at], L);
+      for (int x = part; x < splits; x += WARPS) {
+        const long long at = x * rows + row;
+        const float a = ex2_approx(p.part_m[at] - M);  // 0 for a split the row sees nothing of
+        L = fmaf(a, p.part_l[at], L);
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) o[e] = fmaf(w, p.part_o[at * W + lane + 32 * e], o[e]);
+        for (int e = 0; e < EPL; ++e) o[e] = fmaf(a, p.part_o[at * W + lane + 32 * e], o[e]);
       }
     }
   }
+  if constexpr (WARPS > 1) {
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) sums[warp][lane + 32 * e] = o[e];
-  if (lane == 0) sums[warp][W] = L;
-  __syncthreads();
-  if (part != 0 || !mine) return;
+    for (int e = 0; e < EPL; ++e) sums[warp][lane + 32 * e] = o[e];
+    if (lane == 0) sums[warp][W] = L;
+    __syncthreads();
+    if (part == 0) {
 #pragma unroll
-  for (int x = 1; x < kCombineWarps; ++x) {
+      for (int x = 1; x < WARPS; ++x) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) o[e] += sums[warp + x][lane + 32 * e];
-    L += sums[warp + x][W];
+        for (int e = 0; e < EPL; ++e) o[e] += sums[warp + x][lane + 32 * e];
+        L += sums[warp + x][W];
+      }
+    }
   }
+  if (part != 0 || splits <= 1) return;  // (a single split wrote the row itself)
   const float inv = L > 0.f ? 1.f / L : 0.f;
-  __nv_bfloat16* dst =
-      static_cast<__nv_bfloat16*>(p.out) + ((static_cast<long long>(b) * p.T + t) * p.H + h) * p.d;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * p.d;
 #pragma unroll
   for (int e = 0; e < EPL; ++e)
     if (lane + 32 * e < p.d) dst[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
   if (p.lse && lane == 0)
-    p.lse[(static_cast<long long>(b) * p.H + h) * p.T + t] =
+    p.lse[(static_cast<long long>(w.b) * p.H + h) * p.T + (bt - w.b * p.T)] =
         L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
@@ -1407,21 +1296,22 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  e = launch_serialized(rows_kernel<F8, W, NR>, dim3(static_cast<unsigned>(p.lanes * p.groups)), dim3(C::THREADS),
-                        C::SMEM, stream, p);
+  // one CTA per unit; running CTAs take over the units of those not started
+  const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
+  e = launch_serialized(rows_kernel<F8, W, NR>, grid, dim3(C::THREADS), C::SMEM, stream, p);
   if (e != cudaSuccess) return e;
   int kernels = 1;
-  if (!p.whole_units) {
-    const int rows = p.T * p.G < NR ? p.T * p.G : NR;
-    e = launch_serialized(rows_combine_kernel<W, NR>,
-                          dim3(static_cast<unsigned>((combine_by_sequence(p.B, p.groups) ? p.B : p.groups - 1) * p.units),
-                               static_cast<unsigned>((rows + kCombineRows - 1) / kCombineRows)),
-                          dim3(32 * kCombineRows * kCombineWarps), 0, stream, p);
+  if (p.n_splits > 1) {
+    const long long rows = static_cast<long long>(p.B) * p.T * p.H;
+    const bool many = p.n_splits >= 8;
+    const int per_block = many ? 1 : 8;
+    e = launch_serialized(many ? rows_combine_kernel<W, 8> : rows_combine_kernel<W, 1>,
+                          dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)), dim3(256), 0, stream, p);
     kernels = 2;
   }
   if (info) {
     info->kernels = kernels;
-    info->grid = p.lanes * p.groups;
+    info->grid = static_cast<int>(grid.x);
     info->block = C::THREADS;
     info->smem = C::SMEM;
   }
@@ -1456,32 +1346,22 @@ RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
     RowsPlan plan = {};
     plan.width = C::W;
     plan.units = static_cast<long long>(H_kv) * ((R + C::NR - 1) / C::NR);
-    const long long U = plan.units;
+    const long long base = plan.units * B;
     const long long slots = static_cast<long long>(kSms) * C::MIN_BLOCKS;
-    // What a CTA does, in tiles (a sequence counted at the cache's capacity), for
-    // each number of passes: with whole sequences the fullest group's; with equal
-    // shares one more sequence's cost and the second kernel (some four tiles').
-    const long long weight = (Lk + kKeys - 1) / kKeys + kUnitCost;
-    const long long p0 = (U + slots - 1) / slots;
+    const long long tiles = (Lk + kKeys - 1) / kKeys;
+    // Time in half tiles, sequences counted at the cache's capacity: a unit costs
+    // its tiles and one more; with several units to a CTA the last ones end half a
+    // unit apart; partials cost a second kernel (some four tiles).
     long long best = -1;
-    for (long long P = p0; P < p0 + 8 && P <= U; ++P) {
-      const long long lanes = (U + P - 1) / P;
-      const long long groups = slots / lanes;  // >= 1
-      const long long g_whole = groups < B ? groups : B;
-      const long long whole = P * ((B + g_whole - 1) / g_whole) * weight;
-      const long long g_cut0 = B * weight / kMinShare;
-      const long long g_cut = g_cut0 < 1 ? 1 : (g_cut0 < groups ? g_cut0 : groups);
-      const long long cut = P * ((B * weight + g_cut - 1) / g_cut + kUnitCost) + 4;
-      const bool use_whole = whole <= cut || g_cut == 1;
-      const long long cost = use_whole ? whole : cut;
+    for (long long S = 1; S <= kMaxRowSplits && S <= tiles && (S == 1 || base * (S - 1) < 4 * slots); ++S) {
+      const long long per = (tiles + S - 1) / S + 1;
+      const long long units = base * S;
+      const long long cost = (units <= slots ? 2 * per : 2 * units * per / slots + per) + (S > 1 ? 8 : 0);
       if (best >= 0 && cost >= best) continue;
       best = cost;
-      plan.lanes = lanes;
-      plan.groups = use_whole ? g_whole : g_cut;
-      plan.whole_units = use_whole;
+      plan.splits = static_cast<int>(S);
     }
-    plan.weight = B * weight;
-    plan.part_rows = plan.whole_units ? 0 : static_cast<size_t>(plan.groups) * 2 * U * C::NR;
+    plan.part_rows = plan.splits > 1 ? static_cast<size_t>(plan.splits) * B * T * H : 0;
     return plan;
   });
 }

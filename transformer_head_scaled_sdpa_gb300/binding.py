@@ -407,45 +407,52 @@ def mha_decode(q, k_cache, v_cache, cache_lens, out=None, scale: float = 0.0, wo
 # ---------------------------------------------------------------------------
 # the 8-bit cache, and steps of a few rows per sequence over a cache
 # ---------------------------------------------------------------------------
-def _same_device(tensors):
-    """Checks (tensor, name, dtype) triples: dtype, contiguous, all on one CUDA
-    device, which is returned."""
-    device = tensors[0][0].device
+_BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                torch.uint8)
+_F8 = torch.float8_e4m3fn
+
+
+def _refuse(t, name, dtype, index):
+    """Raises what is wrong with a tensor that _check found wrong."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if index < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be on cuda, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, others on cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _check(index, tensors):
+    """Checks (tensor, name, dtype) triples: dtype, contiguous, all on the CUDA
+    device `index`.  (A small step costs as much on the host as on the GPU: one
+    comparison each here, the words in _refuse.)"""
     for t, name, dtype in tensors:
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, {tensors[0][1]} on {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if device.type != "cuda":
-        raise ValueError(f"{tensors[0][1]} must be on cuda, got {device}")
-    return device
+        if t.dtype is not dtype or index < 0 or t.get_device() != index or not t.is_contiguous():
+            _refuse(t, name, dtype, index)
 
 
-def _call_on(device, stream, made, fn_name, args):
-    """Calls an entry with `device` current and its stream (the current one
+def _call_on(index, stream, made, fn, args):
+    """Calls an entry with device `index` current and its stream (the current one
     unless given).  ``made``: tensors allocated here for the call; on a stream
     other than the current one the allocator must not hand them out again
     before that stream is done."""
-    index = device.index
     # (the raw handle: building a Stream object costs more than the launch)
-    current = torch._C._cuda_getCurrentRawStream(index)
-    handle = current
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if stream is not None:
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
-        if handle != current:
-            other = torch.cuda.ExternalStream(handle, device=device)
+        other = stream if isinstance(stream, int) else stream.cuda_stream
+        if other != handle:
+            handle = other
+            other = torch.cuda.ExternalStream(handle, device=index)
             for t in made:
                 t.record_stream(other)
-    fn = getattr(lib(), fn_name)
     if torch.cuda.current_device() == index:
         rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, handle)
-    if rc != MHA_OK:
-        raise MhaError(rc, fn_name)
+    if rc:
+        raise MhaError(rc, fn.__name__)
 
 
 def _row_strides(t, name):
@@ -463,24 +470,22 @@ def _row_strides(t, name):
     return token, seq
 
 
-def _cache_tensors(k_cache, v_cache, k_scale, v_scale):
-    """Checks the shapes of an 8-bit cache; returns (B, Lk, H, d) and the
-    triples for _same_device."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} "
+def _cache_shape(k_cache, v_cache, k_scale, v_scale):
+    """Checks the shapes of an 8-bit cache; returns (B, Lk, H, d)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} "
                          "must be [B, Lk, H, d_k] alike")
-    B, Lk, H, d = k_cache.shape
-    if k_scale.shape != (B, H, Lk) or v_scale.shape != (B, H, Lk):
-        raise ValueError(f"k_scale and v_scale must be [B, H, Lk] = {(B, H, Lk)}")
-    f8 = torch.float8_e4m3fn
-    return (B, Lk, H, d), [(k_cache, "k_cache", f8), (v_cache, "v_cache", f8),
-                           (k_scale, "k_scale", torch.uint8), (v_scale, "v_scale", torch.uint8)]
+    scales = (shape[0], shape[2], shape[1])
+    if k_scale.shape != scales or v_scale.shape != scales:
+        raise ValueError(f"k_scale and v_scale must be [B, H, Lk] = {scales}")
+    return shape
 
 
 def _lens(t, name, B):
     if t.shape != (B,):
         raise ValueError(f"{name} must be [B]")
-    return (t, name, torch.int32)
+    return (t, name, _I32)
 
 
 def mha_cache_write_f8(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=None, stream=None):
@@ -489,26 +494,25 @@ def mha_cache_write_f8(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=N
     k_cache, v_cache [B, Lk, H, d] (float8_e4m3fn), biased exponents k_scale,
     v_scale [B, H, Lk] (uint8).  ``counts`` [B] limits the tokens of a
     sequence; positions outside the cache are dropped."""
-    (B, Lk, H, d), tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
-    if k.dim() != 4 or k.shape[0] != B or k.shape[2] != H or k.shape[3] != d or v.shape != k.shape:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [B, T, H, d_k] of "
+    B, Lk, H, d = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+    shape = k.shape
+    if len(shape) != 4 or shape[0] != B or shape[2] != H or shape[3] != d or v.shape != shape:
+        raise ValueError(f"k {tuple(shape)} and v {tuple(v.shape)} must be [B, T, H, d_k] of "
                          f"the cache {tuple(k_cache.shape)}")
-    T = k.shape[1]
     strides = _row_strides(k, "k")
     if _row_strides(v, "v") != strides:
         raise ValueError("k and v must have the same strides")
-    tensors.append(_lens(start, "start", B))
+    index = k_cache.get_device()
+    _check(index, ((k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8), (k_scale, "k_scale", _U8),
+                   (v_scale, "v_scale", _U8), _lens(start, "start", B)))
     if counts is not None:
-        tensors.append(_lens(counts, "counts", B))
-    device = _same_device(tensors)
+        _check(index, (_lens(counts, "counts", B),))
     for t, name in ((k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, k_cache on {device}")
-    _call_on(device, stream, (), "mha_cache_write_f8",
+        if t.dtype is not _BF16 or t.get_device() != index:
+            _refuse(t, name, _BF16, index)
+    _call_on(index, stream, (), lib().mha_cache_write_f8,
              (k.data_ptr(), v.data_ptr(), *strides, k_cache.data_ptr(), v_cache.data_ptr(),
-              k_scale.data_ptr(), v_scale.data_ptr(), B, T, H, Lk, d, start.data_ptr(),
+              k_scale.data_ptr(), v_scale.data_ptr(), B, shape[1], H, Lk, d, start.data_ptr(),
               counts.data_ptr() if counts is not None else None))
 
 
@@ -516,26 +520,27 @@ def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, 
     """The first lens[b] positions of an 8-bit cache as bf16: returns (k, v)
     [B, Lk, H, d].  Positions from lens[b] on keep what ``k`` and ``v`` held
     (0 when they are allocated here)."""
-    shape, tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
+    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale)
     B, Lk, H, d = shape
-    tensors.append(_lens(lens, "lens", B))
+    index = k_cache.get_device()
+    _check(index, ((k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8), (k_scale, "k_scale", _U8),
+                   (v_scale, "v_scale", _U8), _lens(lens, "lens", B)))
     made = []
+    out = []
     for t, name in ((k, "k"), (v, "v")):
-        if t is not None:
+        if t is None:
+            t = torch.zeros(shape, dtype=_BF16, device=k_cache.device)
+            made.append(t)
+        else:
             if t.shape != shape:
-                raise ValueError(f"{name} must have the cache's shape {shape}")
-            tensors.append((t, name, torch.bfloat16))
-    device = _same_device(tensors)
-    if k is None:
-        k = torch.zeros(shape, dtype=torch.bfloat16, device=device)
-        made.append(k)
-    if v is None:
-        v = torch.zeros(shape, dtype=torch.bfloat16, device=device)
-        made.append(v)
+                raise ValueError(f"{name} must have the cache's shape {tuple(shape)}")
+            _check(index, ((t, name, _BF16),))
+        out.append(t)
     if made and stream is not None:
         # the zeros are written on the current stream
-        _wait_current(device, stream)
-    _call_on(device, stream, made, "mha_cache_read_f8",
+        _wait_current(k_cache.device, stream)
+    k, v = out
+    _call_on(index, stream, made, lib().mha_cache_read_f8,
              (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
               k.data_ptr(), v.data_ptr(), B, H, Lk, d, lens.data_ptr()))
     return k, v
@@ -548,41 +553,41 @@ def _wait_current(device, stream):
     stream.wait_stream(torch.cuda.current_stream(device))
 
 
-def _rows_call(fn_name, q, T, tensors, cache_shape, ptrs, lens, lens_name, extra, out, scale,
-               workspace, stream, return_lse, lse, ws_args, lse_shape):
+def _rows_call(fn, ws_fn, q, cache_shape, tensors, ptrs, lens, extra, out, scale, workspace,
+               stream, return_lse, lse, ws_args, lse_shape):
     """What the steps of a few rows have in common: checks, allocation, call."""
     B, Lk, H_kv, d = cache_shape
-    H = q.shape[-2]
-    if q.shape[0] != B or q.shape[-1] != d or H_kv == 0 or H % H_kv != 0:
-        raise ValueError(f"cache {tuple(cache_shape)} does not match q {tuple(q.shape)}")
-    tensors = [(q, "q", torch.bfloat16)] + tensors + [_lens(lens, lens_name, B)]
-    if out is not None:
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        tensors.append((out, "out", torch.bfloat16))
-    if lse is not None:
-        if lse.shape != lse_shape:
-            raise ValueError(f"lse must be {lse_shape}")
-        tensors.append((lse, "lse", torch.float32))
-    if workspace is not None:
-        tensors.append((workspace, "workspace", torch.uint8))
-    device = _same_device(tensors)
+    q_shape = q.shape
+    if q_shape[0] != B or q_shape[-1] != d or H_kv == 0 or q_shape[-2] % H_kv != 0:
+        raise ValueError(f"cache {tuple(cache_shape)} does not match q {tuple(q_shape)}")
+    index = q.get_device()
+    _check(index, tensors)
     made = []
     if out is None:
         out = torch.empty_like(q)
         made.append(out)
-    if return_lse and lse is None:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
+    elif out.shape != q_shape:
+        raise ValueError("out must have q's shape")
+    else:
+        _check(index, ((out, "out", _BF16),))
+    if lse is not None:
+        if lse.shape != lse_shape:
+            raise ValueError(f"lse must be {lse_shape}")
+        _check(index, ((lse, "lse", _F32),))
+    elif return_lse:
+        lse = torch.empty(lse_shape, dtype=_F32, device=q.device)
         made.append(lse)
     if workspace is None:
-        need = int(getattr(lib(), fn_name + "_workspace_bytes")(*ws_args))
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        need = ws_fn(*ws_args)
+        if need:
+            workspace = torch.empty(need, dtype=_U8, device=q.device)
             made.append(workspace)
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    _call_on(device, stream, made, fn_name,
+    else:
+        _check(index, ((workspace, "workspace", _U8),))
+    _call_on(index, stream, made, fn,
              (q.data_ptr(), *ptrs, out.data_ptr(), lse.data_ptr() if return_lse else None,
-              *ws_args, lens.data_ptr(), *extra, float(scale), *ws))
+              *ws_args, lens.data_ptr(), *extra, scale,
+              *((None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel()))))
     return (out, lse) if return_lse else out
 
 
@@ -608,31 +613,35 @@ def mha_decode_f8(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, s
     tensor) is allocated when not given."""
     if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[1] != 1):
         raise ValueError("q must be [B, H, d] or [B, 1, H, d]")
-    shape, tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
+    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale)
     B, Lk, H_kv, d = shape
     H = q.shape[-2]
-    ptrs = (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
-    return _rows_call("mha_decode_f8", q, 1, tensors, shape, ptrs, cache_lens, "cache_lens", (),
-                      out, scale, workspace, stream, return_lse, lse, (B, H, H_kv, Lk, d), (B, H))
+    h = lib()
+    return _rows_call(
+        h.mha_decode_f8, h.mha_decode_f8_workspace_bytes, q, shape,
+        ((q, "q", _BF16), (k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8),
+         (k_scale, "k_scale", _U8), (v_scale, "v_scale", _U8), _lens(cache_lens, "cache_lens", B)),
+        (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()),
+        cache_lens, (), out, scale, workspace, stream, return_lse, lse, (B, H, H_kv, Lk, d), (B, H))
 
 
-def _tree(fn_name, q, shape, tensors, ptrs, prefix_lens, draft_lens, tree_mask, out, scale,
-          workspace, stream, return_lse, lse):
+def _tree_mask(q, draft_lens, tree_mask):
+    """Checks the shapes of a tree step's q, lengths and mask; returns the mask's
+    and lengths' triples and pointers."""
     if q.dim() != 4:
         raise ValueError("q must be [B, T, H, d]")
-    B, T, H = q.shape[0], q.shape[1], q.shape[2]
+    B, T = q.shape[0], q.shape[1]
+    tensors, drafts, bits = (), None, None
     if draft_lens is not None:
-        tensors.append(_lens(draft_lens, "draft_lens", B))
+        tensors = (_lens(draft_lens, "draft_lens", B),)
+        drafts = draft_lens.data_ptr()
     if tree_mask is not None:
         words = (T + 63) // 64
         if tree_mask.shape != (B, T, words):
             raise ValueError(f"tree_mask must be [B, T, ceil(T / 64)] = {(B, T, words)}")
-        tensors.append((tree_mask, "tree_mask", torch.int64))
-    extra = (draft_lens.data_ptr() if draft_lens is not None else None,
-             tree_mask.data_ptr() if tree_mask is not None else None)
-    return _rows_call(fn_name, q, T, tensors, shape, ptrs, prefix_lens, "prefix_lens", extra, out,
-                      scale, workspace, stream, return_lse, lse,
-                      (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
+        tensors += ((tree_mask, "tree_mask", _I64),)
+        bits = tree_mask.data_ptr()
+    return tensors, (drafts, bits)
 
 
 def mha_decode_tree(q, k_cache, v_cache, prefix_lens, draft_lens=None, tree_mask=None, out=None,
@@ -645,23 +654,37 @@ def mha_decode_tree(q, k_cache, v_cache, prefix_lens, draft_lens=None, tree_mask
     t sees drafted token j where bit j is set (None: a chain, j <= t).
     ``draft_lens`` [B]: drafted tokens per sequence (None: T); rows past them
     get output 0.  Returns out [B, T, H, d], or (out, lse [B, H, T])."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} "
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} "
                          "must be [B, Lk, H_kv, d] alike")
-    tensors = [(k_cache, "k_cache", torch.bfloat16), (v_cache, "v_cache", torch.bfloat16)]
-    return _tree("mha_decode_tree", q, tuple(k_cache.shape), tensors,
-                 (k_cache.data_ptr(), v_cache.data_ptr()), prefix_lens, draft_lens, tree_mask,
-                 out, scale, workspace, stream, return_lse, lse)
+    tree, extra = _tree_mask(q, draft_lens, tree_mask)
+    B, T, H, _ = q.shape
+    h = lib()
+    return _rows_call(
+        h.mha_decode_tree, h.mha_decode_tree_workspace_bytes, q, shape,
+        ((q, "q", _BF16), (k_cache, "k_cache", _BF16), (v_cache, "v_cache", _BF16),
+         _lens(prefix_lens, "prefix_lens", B), *tree),
+        (k_cache.data_ptr(), v_cache.data_ptr()), prefix_lens, extra, out, scale, workspace,
+        stream, return_lse, lse, (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
 
 
 def mha_decode_tree_f8(q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens=None,
                        tree_mask=None, out=None, scale: float = 0.0, workspace=None, stream=None,
                        return_lse: bool = False, lse=None):
     """mha_decode_tree over an 8-bit cache (mha_cache_write_f8's format)."""
-    shape, tensors = _cache_tensors(k_cache, v_cache, k_scale, v_scale)
-    ptrs = (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
-    return _tree("mha_decode_tree_f8", q, shape, tensors, ptrs, prefix_lens, draft_lens, tree_mask,
-                 out, scale, workspace, stream, return_lse, lse)
+    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+    tree, extra = _tree_mask(q, draft_lens, tree_mask)
+    B, T, H, _ = q.shape
+    h = lib()
+    return _rows_call(
+        h.mha_decode_tree_f8, h.mha_decode_tree_f8_workspace_bytes, q, shape,
+        ((q, "q", _BF16), (k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8),
+         (k_scale, "k_scale", _U8), (v_scale, "v_scale", _U8),
+         _lens(prefix_lens, "prefix_lens", B), *tree),
+        (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()),
+        prefix_lens, extra, out, scale, workspace, stream, return_lse, lse,
+        (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
 
 
 def host_workspace_bytes(B, H, Lq, Lk, d_k, elem_bytes) -> int:

@@ -90,9 +90,6 @@ struct RowsCfg {
   static constexpr bool F8 = F8_;
   static constexpr int W = W_;    // widest head
   static constexpr int NR = NR_;  // rows per unit
-  static constexpr int WGS = NR <= 32 ? 1 : NR / 32;     // softmax warpgroups
-  static constexpr int RPT = NR / WGS;                   // rows per softmax thread
-  static constexpr int THREADS = 128 * WGS + 128;
   static constexpr int EB = F8 ? 1 : 2;                  // bytes per cached element
   static constexpr int CHUNK = kKeys * 128;              // [128 keys x 128 B], 128-byte swizzle
   static constexpr int BLKS = W <= 128 ? 1 : 2;          // blocks of 128 features
@@ -102,8 +99,6 @@ struct RowsCfg {
   // columns of S^T and O^T (multiples of 16: what is past the pieces is not read)
   static constexpr int NQ = QP * NR < 16 ? 16 : QP * NR;
   static constexpr int NP = (PP * NR + 15) / 16 * 16;
-  static constexpr int GW = RPT < 16 ? RPT : 16;         // rows handled together
-  static constexpr int GROUPS = RPT / GW;
   static constexpr int Q_BYTES = NQ * W * EB;
   static constexpr int P_BYTES = kKeys * NP * EB;
   static constexpr int P_BUFS = W <= 128 && NR <= 32 ? 2 : 1;  // (beyond, the ring needs the room)
@@ -121,7 +116,13 @@ struct RowsCfg {
   // two CTAs per SM when each can hold two tiles' worth of ring, else one with
   // a deep ring
   static constexpr int SLOTS2 = (115712 - FIXED) / SLOT;
-  static constexpr bool TWO = SLOTS2 >= (BLKS == 1 ? 4 : 5) && WGS == 1 && TMEM_COLS <= 256;
+  static constexpr bool TWO = SLOTS2 >= (BLKS == 1 ? 4 : 5) && NR <= 32 && TMEM_COLS <= 256;
+  // softmax warpgroups: a CTA that has the SM to itself has two from 32 rows on
+  static constexpr int WGS = NR <= 16 || TWO ? 1 : 2;
+  static constexpr int RPT = NR / WGS;                   // rows per softmax thread
+  static constexpr int THREADS = 128 * WGS + 128;
+  static constexpr int GW = RPT < 16 ? RPT : 16;         // rows handled together
+  static constexpr int GROUPS = RPT / GW;
   static constexpr int SLOTS1 = (232448 - FIXED) / SLOT;
   static constexpr int SLOTS = TWO ? SLOTS2 : (SLOTS1 > 12 ? 12 : SLOTS1);
   static constexpr int MIN_BLOCKS = TWO ? 2 : 1;
@@ -165,8 +166,8 @@ struct RowsCfg {
   static constexpr float LIFT = F8 ? 10.f : 0.f;         // weights are 2^LIFT at the reference
   // registers: the softmax warpgroups take from the others
   static constexpr bool SPLIT_REGS = TWO || WGS > 1;
-  static constexpr int REGS_OTHER = NR <= 16 ? 96 : 80;
-  static constexpr int REGS_SOFT = TWO ? 256 - REGS_OTHER : 208;
+  static constexpr int REGS_OTHER = TWO && NR > 16 ? 80 : 96;
+  static constexpr int REGS_SOFT = TWO ? 256 - REGS_OTHER : 200;
   static_assert(!TWO || (REGS_OTHER + REGS_SOFT) * 128 <= 256 * 128, "register split");
   static_assert(WGS != 2 || REGS_OTHER * 128 + REGS_SOFT * 256 <= 168 * 384, "register split");
 };
@@ -254,6 +255,18 @@ __device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, volat
   }
   *abort = site + 1;
   return false;
+}
+// Whether the phase with this parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // By a whole warp with one answer for all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int site) {
@@ -486,6 +499,21 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     *t = p.G == 1 ? gr : gr / p.G;
     return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
   };
+  // Asks a unit's Q and mask words into L2.
+  auto ask_q = [&](const Unit& it, int qt, int threads) {
+#pragma unroll 1
+    for (int r = qt >> 3; r < NR; r += threads >> 3) {
+      int t;
+      const int out = out_row(it, r, &t);
+      if (out < 0) break;
+      if (64 * (qt & 7) < p.d)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t*>(p.q) +
+                                                      static_cast<long long>(out) * p.d + 64 * (qt & 7)));
+      if (p.tree_mask && (qt & 7) == 7)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.tree_mask +
+                                                      (static_cast<long long>(it.b) * p.T + t) * p.words));
+    }
+  };
   // A unit's Q, output rows and mask words into buffer `buf`, by thread qt of a
   // multiple of 32 (eight threads per row); false when `buffer_free` gave up.
   auto prepare_q = [&](auto threads, const Unit& it, int buf, int qt, auto buffer_free) {
@@ -494,23 +522,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     const int sub = qt & 7;
     const uint32_t sQ = s_base + C::OFF_Q + buf * C::Q_BYTES;
     if (NR < RP && (qt >> 3) >= NR) return buffer_free();  // (whole warps)
-    // ask all rows into L2, then take one after the other
-#pragma unroll 1
-    for (int rr = 0; rr < NR; rr += RP) {
-      int t;
-      const int out = out_row(it, rr + (qt >> 3), &t);
-      if (out >= 0 && 64 * sub < p.d)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint16_t*>(p.q) +
-                                                      static_cast<long long>(out) * p.d + 64 * sub));
-    }
-    if (!buffer_free()) return false;
-#pragma unroll 1
-    for (int rr = 0; rr < NR; rr += RP) {
-      const int r = rr + (qt >> 3);
-      int t;
-      const int out = out_row(it, r, &t);
-      const bool live = t >= 0 && t < it.live;
-      uint4 v[PER];
+    auto load_row = [&](int r, int* t, uint4 (&v)[PER]) {
+      const int out = out_row(it, r, t);
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
                                                         static_cast<long long>(max(out, 0)) * p.d);
 #pragma unroll
@@ -520,6 +533,17 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         v[z] = make_uint4(0, 0, 0, 0);
         if (out >= 0 && 8 * piece < p.d) v[z] = __ldg(src + piece);
       }
+      return out;
+    };
+    uint4 v[PER], ahead[PER];
+    int t, t_ahead = -1, out_ahead = -1;
+    int out = load_row(qt >> 3, &t, v);
+    if (!buffer_free()) return false;
+#pragma unroll 1
+    for (int rr = 0; rr < NR; rr += RP) {
+      const int r = rr + (qt >> 3);
+      if (rr + RP < NR) out_ahead = load_row(r + RP, &t_ahead, ahead);
+      const bool live = t >= 0 && t < it.live;
       if (sub == 0) {
         row_out(buf)[r] = out;
         row_lse(buf)[r] = out < 0 ? 0 : (it.b * p.H + out % p.H) * p.T + t;
@@ -581,6 +605,10 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         for (int z = 0; z < PER; ++z)
           st_shared_v4(sQ + (sub + 8 * z) * (C::NQ * 16) + r * 16, v[z].x, v[z].y, v[z].z, v[z].w);
       }
+      out = out_ahead;
+      t = t_ahead;
+#pragma unroll
+      for (int z = 0; z < PER; ++z) v[z] = ahead[z];
     }
     return true;
   };
@@ -624,38 +652,64 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           ring.advance();
         }
       };
-      // The units: this CTA's own, then those of CTAs that have not started; the
-      // next is asked for while one's tiles are loaded.
+      // The units: this CTA's own, then those of CTAs that have not started.  The
+      // next is asked for half-way through a unit's loads and published as soon
+      // as it is known, so that its Q and scales are there when its turn comes.
       volatile int never = 0;
-      int index = static_cast<int>(blockIdx.x), published = 0;
+      int published = 0;
       auto publish = [&](const Unit& w) {
         const int slot = published % kQueue;
         ok = ok && (published < kQueue ||
-                    thread_wait(bar(C::UNIT_EMPTY + slot), ((published / kQueue) - 1) & 1, abort_flag, site + C::UNIT_EMPTY + slot));
+                    thread_wait(bar(C::UNIT_EMPTY + slot), ((published / kQueue) - 1) & 1, abort_flag,
+                                site + C::UNIT_EMPTY + slot));
         if (!ok) return;
         queue[slot] = w;
         mbar_arrive(bar(C::UNIT_FULL + slot));
         ++published;
       };
-      for (uint32_t asked = 0;; ++asked) {
-        mbar_arrive_expect_tx(bar(C::CLC), 16);
-        clc_try_cancel(s_base + C::OFF_CLC, bar(C::CLC));
-        const Unit w = unit_at(p, index, blocks);
-        if (w.split < w.splits) {
-          publish(w);
+      uint32_t answers = 0;
+      bool asked = false, done = false;
+      Unit w = unit_at(p, static_cast<int>(blockIdx.x), blocks), next = w;
+      bool got = w.split < w.splits;  // a unit to work on (false: a split its sequence does not have)
+      if (got) publish(w);
+      while (ok) {
+        const bool works = got;
+        got = false;
+        // the next unit, if its answer is there or `must` be waited for
+        auto poll = [&](bool must) {
+          while (!got && !done && ok) {
+            if (!asked) {
+              mbar_arrive_expect_tx(bar(C::CLC), 16);
+              clc_try_cancel(s_base + C::OFF_CLC, bar(C::CLC));
+              asked = true;
+            }
+            // (the response lands whatever happens: it is waited for even when giving up)
+            if (must) ok = mbar_wait(bar(C::CLC), answers & 1, &never, p.status, site + C::CLC) && *abort_flag == 0;
+            else if (!mbar_test(bar(C::CLC), answers & 1)) return;
+            ++answers;
+            asked = false;
+            const int index = clc_query_first_ctaid_x(s_base + C::OFF_CLC);  // -1: none was left
+            fence_proxy_async_smem();  // (the next response overwrites this one)
+            done = index < 0;
+            if (done || !ok) return;
+            next = unit_at(p, index, blocks);
+            got = next.split < next.splits;
+            if (got) publish(next);
+          }
+        };
+        if (works) {
           for (int x = w.t0; x < w.t1 && ok; ++x) {
             load(&p.tm_k, &p.tm_k_box, x * kKeys, w.end, w.hk, w.b);
             if (x > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (x - 1) * kKeys, w.end, w.hk, w.b);
+            if (2 * (x - w.t0 + 1) >= w.t1 - w.t0) poll(false);
           }
           if (w.t1 > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (w.t1 - 1) * kKeys, w.end, w.hk, w.b);
         }
-        // (the response lands whatever happens: wait for it even when giving up)
-        ok = mbar_wait(bar(C::CLC), asked & 1, &never, p.status, site + C::CLC) && ok && *abort_flag == 0;
-        if (!ok) break;
-        index = clc_query_first_ctaid_x(s_base + C::OFF_CLC);  // -1: none was left
-        if (index < 0) break;
-        fence_proxy_async_smem();  // (the next response overwrites this one)
+        poll(true);
+        if (!got) break;
+        w = next;
       }
+      if (asked) mbar_wait(bar(C::CLC), answers & 1, &never, p.status, site + C::CLC);
       Unit end;
       end.b = -1;
       publish(end);
@@ -718,27 +772,35 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     };
     auto unit_q = [&](int k) { return dq0 + static_cast<uint64_t>(((k & 1) * C::Q_BYTES) >> 4); };
     int taken = 0;
-    // tiles of the next unit that has any (0: no more units)
-    auto next_tiles = [&]() {
+    // Tiles of the next unit that has any (0: no more units) into *n; false when
+    // that is not known yet and may not be waited for.
+    auto next_tiles = [&](bool must, int* n) {
       for (;;) {
+        if (!must && !__all_sync(0xffffffffu, mbar_test(bar(C::UNIT_FULL + taken % kQueue), (taken / kQueue) & 1)))
+          return false;
         const Unit w = take(taken++, site);
-        if (w.b < 0) return 0;
-        if (w.t1 > w.t0) return w.t1 - w.t0;
+        *n = w.b < 0 ? 0 : w.t1 - w.t0;
+        if (w.b < 0 || *n > 0) return true;
       }
     };
     int k = 0;        // units with tiles
     uint32_t t = 0;   // tiles
-    int n = next_tiles();
+    int n = 0;
+    next_tiles(true, &n);
     if (n > 0) {
       wait(C::Q_FIRST, 0);
       if (ok) issue_s(0, unit_q(0), n == 1 ? C::Q_EMPTY : -1);
     }
     while (n > 0 && ok) {
-      int n_next = 0;
+      int n_next = -1;  // (not known)
       for (int i = 0; i < n && ok; ++i, ++t) {
         // The next tile's scores, of this unit or the next (whose first K lies
-        // behind this unit's last V in the ring).
+        // behind this unit's last V in the ring) if it is ready.
         Ring<C::SLOTS> v;
+        bool ahead = i + 1 < n;
+        auto first_scores = [&]() {
+          issue_s((t + 1) & 1, unit_q(k + 1), n_next == 1 ? C::Q_EMPTY + ((k + 1) & 1) : -1);
+        };
         if (i + 1 < n) {
           issue_s((t + 1) & 1, unit_q(k), i + 2 == n ? C::Q_EMPTY + (k & 1) : -1);
           v = ring;
@@ -747,10 +809,9 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
 #pragma unroll
           for (int blk = 0; blk < C::BLKS; ++blk)
             if (blk < blks) ring.advance();
-          n_next = next_tiles();
-          if (n_next > 0) {
-            wait(C::Q_FULL + ((k + 1) & 1), q_phase(k + 1));
-            if (ok) issue_s((t + 1) & 1, unit_q(k + 1), n_next == 1 ? C::Q_EMPTY + ((k + 1) & 1) : -1);
+          if (next_tiles(false, &n_next) && n_next > 0) {
+            ahead = __all_sync(0xffffffffu, mbar_test(bar(C::Q_FULL + ((k + 1) & 1)), q_phase(k + 1)));
+            if (ahead) first_scores();
           }
         }
         // (O is free once the last unit's epilogue has read it)
@@ -777,7 +838,15 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           __syncwarp();
           v.advance();
         }
-        if (i + 1 < n) ring = v;
+        if (i + 1 < n) {
+          ring = v;
+        } else {
+          if (n_next < 0) next_tiles(true, &n_next);
+          if (n_next > 0 && !ahead) {
+            wait(C::Q_FULL + ((k + 1) & 1), q_phase(k + 1));
+            if (ok) first_scores();
+          }
+        }
       }
       n = n_next;
       ++k;
@@ -862,6 +931,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       }
       const int buf = k & 1;
       if (k > 0) {  // (the softmax threads prepare the first)
+        ask_q(it, qt, QT);
         const bool ok = prepare_q(std::integral_constant<int, QT>{}, it, buf, qt, [&]() {
           return k < 2 || warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, site + C::Q_EMPTY + buf);
         });
@@ -886,6 +956,15 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     auto wait = [&](int id, uint32_t parity) {
       ok = ok && thread_wait(bar(id), parity, abort_flag, site + id);
     };
+    {
+      // the first unit's Q before the ring's first copies (it is this CTA's own)
+      Unit own;
+      const int index = static_cast<int>(blockIdx.x), u = index % p.units;
+      own.hk = u / blocks;
+      own.rb = u - own.hk * blocks;
+      own.b = index / p.units % p.B;
+      ask_q(own, tid, SOFT);
+    }
     if (kt < RPT) row_ref[r0 + kt] = 0.f;
     named_barrier(nbar, 128);
     int k = 0;       // units with keys

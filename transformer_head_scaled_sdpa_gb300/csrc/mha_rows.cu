@@ -101,7 +101,7 @@ struct RowsCfg {
   static constexpr int NP = (PP * NR + 15) / 16 * 16;
   static constexpr int Q_BYTES = NQ * W * EB;
   static constexpr int P_BYTES = kKeys * NP * EB;
-  static constexpr int P_BUFS = W <= 128 && NR <= 32 ? 2 : 1;  // (beyond, the ring needs the room)
+  static constexpr int P_BUFS = W <= 128 || (F8 && NR >= 32) ? 2 : 1;
   // barriers (512 bytes), units, scales, per-row values of two units and of the softmax
   static constexpr int SCALES = F8 ? kScaleTiles * kKeys * 2 : 0;
   static constexpr int MISC = 576 + 48 * kQueue + 16 + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
@@ -1302,11 +1302,12 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
 // Merges a row's partials:
 //   o = sum_x 2^(m_x - M) o_x / sum_x 2^(m_x - M) l_x,  M = max_x m_x
 // over the splits x of its sequence.  A row has WARPS warps of an eight-warp block,
-// which divide its partials (eight when one long sequence is spread over the
-// machine, one when there are few splits and many rows).
+// which divide its partials (eight when one long
+// sequence is spread over the machine, one when there are few splits and many rows); a lane holds W / 32 neighbouring
+// features, and a warp's first four o_x are requested together with the m_x.
 template <int W, int WARPS>
 __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int EPL = W / 32;
+  constexpr int EPL = W / 32, AHEAD = 4;
   __shared__ float sums[8][WARPS > 1 ? W + 1 : 1];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int part = warp % WARPS;
@@ -1317,46 +1318,93 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
   w.b = bt / p.T;
   w.split = 0;
   w.splits = 1;
-  griddep_wait();  // the splits' partials are complete and visible
+  // The lengths may be read before the wait: the rows kernel, which does not write
+  // them, let this one start after its own wait for whatever came before.
   if (row < rows) unit_keys(p, &w);
+  griddep_wait();  // the splits' partials are complete and visible
   const int splits = w.splits;
   float o[EPL], L = 0.f, M = -INFINITY;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
   if (splits > 1) {
-    for (int x = lane; x < splits; x += 32) M = fmaxf(M, p.part_m[x * rows + row]);
-    M = warp_max(M);
-    if (M != -INFINITY) {
-#pragma unroll 4
-      for (int x = part; x < splits; x += WARPS) {
-        const long long at = x * rows + row;
-        const float a = ex2_approx(p.part_m[at] - M);  // 0 for a split the row sees nothing of
-        L = fmaf(a, p.part_l[at], L);
+    auto load = [&](int x, float (&y)[EPL]) {
+      const float* src = p.part_o + (x * rows + row) * W + lane * EPL;
+      if constexpr (EPL == 2) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+        y[0] = v.x, y[1] = v.y;
+      } else {
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) o[e] = fmaf(a, p.part_o[at * W + lane + 32 * e], o[e]);
+        for (int e = 0; e < EPL; e += 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src + e));
+          y[e] = v.x, y[e + 1] = v.y, y[e + 2] = v.z, y[e + 3] = v.w;
+        }
+      }
+    };
+    float first[AHEAD][EPL], m[2], a[2];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (part + i * WARPS < splits) load(part + i * WARPS, first[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // (kMaxRowSplits = 64)
+      const int x = lane + 32 * i;
+      m[i] = -INFINITY;
+      a[i] = 0.f;
+      if (x < splits) {
+        m[i] = __ldcg(p.part_m + x * rows + row);
+        a[i] = __ldcg(p.part_l + x * rows + row);
+      }
+    }
+    M = warp_max(fmaxf(m[0], m[1]));
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f = ex2_approx(m[i] - M);  // 0 for a split the row sees nothing of
+        L = fmaf(f, a[i], L);
+        a[i] = f;
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) L += __shfl_xor_sync(0xffffffffu, L, i);
+      auto add = [&](int x, const float (&y)[EPL]) {
+        const float f = __shfl_sync(0xffffffffu, x < 32 ? a[0] : a[1], x & 31);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) o[e] = fmaf(f, y[e], o[e]);
+      };
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (part + i * WARPS < splits) add(part + i * WARPS, first[i]);
+#pragma unroll 4
+      for (int x = part + AHEAD * WARPS; x < splits; x += WARPS) {
+        float y[EPL];
+        load(x, y);
+        add(x, y);
       }
     }
   }
   if constexpr (WARPS > 1) {
+    if (part != 0) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) sums[warp][lane + 32 * e] = o[e];
-    if (lane == 0) sums[warp][W] = L;
+      for (int e = 0; e < EPL; ++e) sums[warp][lane + 32 * e] = o[e];
+    }
     __syncthreads();
     if (part == 0) {
 #pragma unroll
-      for (int x = 1; x < WARPS; ++x) {
+      for (int x = 1; x < WARPS; ++x)
 #pragma unroll
         for (int e = 0; e < EPL; ++e) o[e] += sums[warp + x][lane + 32 * e];
-        L += sums[warp + x][W];
-      }
     }
   }
   if (part != 0 || splits <= 1) return;  // (a single split wrote the row itself)
   const float inv = L > 0.f ? 1.f / L : 0.f;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * p.d;
+  uint32_t out[EPL / 2];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e)
-    if (lane + 32 * e < p.d) dst[lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
+  for (int e = 0; e < EPL; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  // (d is a multiple of 16: a lane's features are all inside it or all past it)
+  if (lane * EPL < p.d) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * p.d + lane * EPL);
+    if constexpr (EPL == 2) *dst = out[0];
+    else if constexpr (EPL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
   if (p.lse && lane == 0)
     p.lse[(static_cast<long long>(w.b) * p.H + h) * p.T + (bt - w.b * p.T)] =
         L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
@@ -1429,13 +1477,18 @@ RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
     const long long slots = static_cast<long long>(kSms) * C::MIN_BLOCKS;
     const long long tiles = (Lk + kKeys - 1) / kKeys;
     // Time in half tiles, sequences counted at the cache's capacity: a unit costs
-    // its tiles and one more; with several units to a CTA the last ones end half a
-    // unit apart; partials cost a second kernel (some four tiles).
+    // its tiles and five more (its Q, first tile and epilogue); with several units
+    // to a CTA the last ones end half a unit apart; partials cost a second kernel
+    // (some four tiles) and are written and read at about the rate of the keys.
+    // (3 sequences x 8 key heads x 4 blocks of 64 rows x 16,411 keys of 128 features,
+    // by splits: 1 141 us, 2 118, 3 105, 5 113, 7 115; 5 x 2 x 2 blocks of 32 rows x
+    // 20,011 keys of 256 features in 8 bits: 4 67 us, 6 52, 7 48, 8 49, 14 51.)
     long long best = -1;
     for (long long S = 1; S <= kMaxRowSplits && S <= tiles && (S == 1 || base * (S - 1) < 4 * slots); ++S) {
-      const long long per = (tiles + S - 1) / S + 1;
+      const long long per = 2 * ((tiles + S - 1) / S) + 10;
       const long long units = base * S;
-      const long long cost = (units <= slots ? 2 * per : 2 * units * per / slots + per) + (S > 1 ? 8 : 0);
+      const long long merge = S == 1 ? 0 : 8 + units * C::NR / (slots * 16 * C::EB);
+      const long long cost = (units <= slots ? per : units * per / slots + per / 2) + merge;
       if (best >= 0 && cost >= best) continue;
       best = cost;
       plan.splits = static_cast<int>(S);

@@ -136,15 +136,15 @@ struct RowsCfg {
   static constexpr int FULL = 0;              // + slot
   static constexpr int EMPTY = SLOTS;         // + slot
   static constexpr int Q_THREADS = F8 ? 32 : 64;
-  static constexpr int Q_FULL = 2 * SLOTS;    // + buffer: Q and the unit's row values (Q_THREADS arrivals)
+  static constexpr int Q_FULL = 2 * SLOTS;    // + buffer: Q and the unit's row values (Q_THREADS / 32 warps)
   static constexpr int Q_EMPTY = Q_FULL + 2;  // + buffer: the last scores and the epilogue are done
   static constexpr int S_FULL = Q_EMPTY + 2;  // + buffer
-  static constexpr int P_FULL = S_FULL + 2;   // + P buffer (every softmax thread)
+  static constexpr int P_FULL = S_FULL + 2;   // + P buffer (every softmax warp)
   static constexpr int PV_DONE = P_FULL + P_BUFS;       // + P buffer
-  static constexpr int Q_FIRST = PV_DONE + P_BUFS;      // the first unit's Q (every softmax thread)
-  static constexpr int O_FREE = Q_FIRST + 1;  // the epilogue has read O (every softmax thread)
+  static constexpr int Q_FIRST = PV_DONE + P_BUFS;      // the first unit's Q (every softmax warp)
+  static constexpr int O_FREE = Q_FIRST + 1;  // the epilogue has read O (every softmax warp)
   static constexpr int DRAIN = O_FREE + 1;
-  static constexpr int SC_FULL = DRAIN + 1;            // + tile: scales (8-bit; 32 arrivals)
+  static constexpr int SC_FULL = DRAIN + 1;            // + tile: scales (8-bit)
   static constexpr int SC_EMPTY = SC_FULL + (F8 ? kScaleTiles : 0);  // + tile: read (each softmax warp)
   static constexpr int UNIT_FULL = SC_EMPTY + (F8 ? kScaleTiles : 0);  // + queue slot: published
   static constexpr int UNIT_EMPTY = UNIT_FULL + kQueue;                // + queue slot: read (each consumer warp)
@@ -204,6 +204,12 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
   } else {
     umma_ss(d, a, b, idesc, acc);
   }
+}
+
+// One arrival for a warp, behind what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
 // True for every thread of a softmax warpgroup when any of them passes true
@@ -424,16 +430,16 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       mbar_init(bar(C::EMPTY + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::Q_FULL + i), C::Q_THREADS);
-      mbar_init(bar(C::Q_EMPTY + i), 1 + SOFT);
+      mbar_init(bar(C::Q_FULL + i), C::Q_THREADS / 32);
+      mbar_init(bar(C::Q_EMPTY + i), 1 + SOFT / 32);
       mbar_init(bar(C::S_FULL + i), 1);
     }
     for (int i = 0; i < C::P_BUFS; ++i) {
-      mbar_init(bar(C::P_FULL + i), SOFT);
+      mbar_init(bar(C::P_FULL + i), SOFT / 32);
       mbar_init(bar(C::PV_DONE + i), 1);
     }
-    mbar_init(bar(C::Q_FIRST), SOFT);
-    mbar_init(bar(C::O_FREE), SOFT);
+    mbar_init(bar(C::Q_FIRST), SOFT / 32);
+    mbar_init(bar(C::O_FREE), SOFT / 32);
     mbar_init(bar(C::DRAIN), 1);
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(bar(C::UNIT_FULL + i), 1);
@@ -442,7 +448,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     mbar_init(bar(C::CLC), 1);
     if constexpr (F8) {
       for (int i = 0; i < kScaleTiles; ++i) {
-        mbar_init(bar(C::SC_FULL + i), 32);
+        mbar_init(bar(C::SC_FULL + i), 1);
         mbar_init(bar(C::SC_EMPTY + i), 4 * C::WGS);
       }
     }
@@ -722,137 +728,144 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    // ---- MMA issuer
+    // ---- MMA issuer (one lane): S(0) S(1) PV(0) S(2) PV(1) ... over all units' tiles
     const int site = kRoleRowsMma * 64;
-    constexpr int KSTEP = F8 ? 32 : 16;                 // reduction elements per MMA
-    const int n_ks = (p.d + KSTEP - 1) / KSTEP;
-    constexpr int KS_BLK = 128 / KSTEP;                 // steps of a 128-feature block
-    constexpr uint32_t idesc_s = F8 ? idesc_f8_f32(128, C::NQ, 0, false, false)
-                                    : idesc_bf16_f32(128, C::NQ, false, false);
-    constexpr uint32_t idesc_o = F8 ? idesc_f8_f32(C::M_O, C::NP, 1, true, true)
-                                    : idesc_bf16_f32(C::M_O, C::NP, true, true);
-    // K: rows of 128 bytes per chunk, 8-row groups 1024 B apart, +32 B per step
-    // inside a chunk.  V transposed: features contiguous in a 128-byte row, next
-    // chunk of features CHUNK apart, 8-key groups 1024 B apart.
-    const uint64_t dk0 = smem_desc_sw128(s_base, 16, 1024);
-    const uint64_t dv0 = smem_desc_sw128(s_base, C::CHUNK, 1024);
-    const uint64_t dq0 = smem_desc_plain(s_base + C::OFF_Q, C::NQ * 16, 128);
-    const uint64_t dp0 = smem_desc_plain(sP, 128, kKeys * 16);
-    Ring<C::SLOTS> ring;
-    bool ok = true;
-    auto wait = [&](int id, uint32_t parity) {
-      ok = ok && warp_wait(bar(id), parity, abort_flag, site + id);
-    };
-    // scores of the next tile into S buffer `s_buf`; `q`: its unit's Q; `done`: the
-    // barrier to tell when the unit's last scores are done, or -1
-    auto issue_s = [&](uint32_t s_buf, uint64_t q, int done) {
-#pragma unroll
-      for (int blk = 0; blk < C::BLKS; ++blk) {
-        if (blk >= blks) break;
-        wait(C::FULL + ring.slot, ring.phase);
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t d = tmem + (s_buf ? C::TM_S1 : 0u);
-          const uint64_t a = dk0 + static_cast<uint64_t>((ring.slot * C::SLOT) >> 4);
-#pragma unroll
-          for (int x = 0; x < KS_BLK; ++x) {
-            const int ks = blk * KS_BLK + x;
-            if (ks < n_ks)
-              umma<F8>(d, a + static_cast<uint64_t>(((x >> 2) * C::CHUNK + (x & 3) * 32) >> 4),
-                       q + static_cast<uint64_t>(ks * 2 * C::NQ), idesc_s, ks > 0 ? 1u : 0u);
+    if (elect_one()) {
+      constexpr int KSTEP = F8 ? 32 : 16;               // reduction elements per MMA
+      const int n_ks = (p.d + KSTEP - 1) / KSTEP;
+      constexpr int KS_BLK = 128 / KSTEP;               // steps of a 128-feature block
+      constexpr uint32_t idesc_s = F8 ? idesc_f8_f32(128, C::NQ, 0, false, false)
+                                      : idesc_bf16_f32(128, C::NQ, false, false);
+      constexpr uint32_t idesc_o = F8 ? idesc_f8_f32(C::M_O, C::NP, 1, true, true)
+                                      : idesc_bf16_f32(C::M_O, C::NP, true, true);
+      // K: rows of 128 bytes per chunk, 8-row groups 1024 B apart, +32 B per step
+      // inside a chunk.  V transposed: features contiguous in a 128-byte row, next
+      // chunk of features CHUNK apart, 8-key groups 1024 B apart.
+      const uint64_t dk0 = smem_desc_sw128(s_base, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(s_base, C::CHUNK, 1024);
+      const uint64_t dq0 = smem_desc_plain(s_base + C::OFF_Q, C::NQ * 16, 128);
+      const uint64_t dp0 = smem_desc_plain(sP, 128, kKeys * 16);
+      bool ok = true;
+      auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
+      // Scores run one tile ahead of the products.  A unit's blocks lie in the ring
+      // in the order K(0) K(1) V(0) K(2) ... V(last): `k_at` and `v_at` count ring
+      // items (tiles of K or V).
+      uint32_t ts = 0, tp = 0;        // tiles whose scores, products are issued
+      uint32_t k_at = 0, v_at = 0;
+      int taken = 0, ks = -1, kp = -1;
+      int s_n = 0, s_i = 0;           // the scores' unit: tiles, tiles issued
+      int n_odd = 0, n_even = 0;      // tiles of odd and even units
+      int p_n = 0, p_i = 0;           // the products' unit
+      bool more = true, q_known = false;
+      while (ok) {
+        // ---- the next tile's scores; at a unit's border only if it and its Q are
+        // there, unless nothing else is left to do
+        if (more && ts < tp + 2) {
+          const bool must = ts == tp;
+          if (s_i == s_n) {
+            const int slot = taken % kQueue;
+            const uint32_t full = bar(C::UNIT_FULL + slot), parity = (taken / kQueue) & 1;
+            if (must) wait(C::UNIT_FULL + slot, parity);
+            if (ok && (must || mbar_test(full, parity))) {
+              const int n = queue[slot].b < 0 ? -1 : queue[slot].t1 - queue[slot].t0;
+              mbar_arrive(bar(C::UNIT_EMPTY + slot));
+              ++taken;
+              if (n == 0) continue;
+              if (n < 0) {
+                more = false;
+              } else {
+                s_n = n;
+                s_i = 0;
+                ++ks;
+                q_known = false;
+              }
+            }
           }
-          if (blk == blks - 1) umma_commit(bar(C::S_FULL + s_buf));
-          umma_commit(bar(C::EMPTY + ring.slot));
-          if (blk == blks - 1 && done >= 0) umma_commit(bar(done));
-        }
-        __syncwarp();
-        ring.advance();
-      }
-    };
-    auto unit_q = [&](int k) { return dq0 + static_cast<uint64_t>(((k & 1) * C::Q_BYTES) >> 4); };
-    int taken = 0;
-    // Tiles of the next unit that has any (0: no more units) into *n; false when
-    // that is not known yet and may not be waited for.
-    auto next_tiles = [&](bool must, int* n) {
-      for (;;) {
-        if (!must && !__all_sync(0xffffffffu, mbar_test(bar(C::UNIT_FULL + taken % kQueue), (taken / kQueue) & 1)))
-          return false;
-        const Unit w = take(taken++, site);
-        *n = w.b < 0 ? 0 : w.t1 - w.t0;
-        if (w.b < 0 || *n > 0) return true;
-      }
-    };
-    int k = 0;        // units with tiles
-    uint32_t t = 0;   // tiles
-    int n = 0;
-    next_tiles(true, &n);
-    if (n > 0) {
-      wait(C::Q_FIRST, 0);
-      if (ok) issue_s(0, unit_q(0), n == 1 ? C::Q_EMPTY : -1);
-    }
-    while (n > 0 && ok) {
-      int n_next = -1;  // (not known)
-      for (int i = 0; i < n && ok; ++i, ++t) {
-        // The next tile's scores, of this unit or the next (whose first K lies
-        // behind this unit's last V in the ring) if it is ready.
-        Ring<C::SLOTS> v;
-        bool ahead = i + 1 < n;
-        auto first_scores = [&]() {
-          issue_s((t + 1) & 1, unit_q(k + 1), n_next == 1 ? C::Q_EMPTY + ((k + 1) & 1) : -1);
-        };
-        if (i + 1 < n) {
-          issue_s((t + 1) & 1, unit_q(k), i + 2 == n ? C::Q_EMPTY + (k & 1) : -1);
-          v = ring;
-        } else {
-          v = ring;
+          if (s_i < s_n && !q_known) {
+            const int id = ks == 0 ? C::Q_FIRST : C::Q_FULL + (ks & 1);
+            const uint32_t parity = ks == 0 ? 0 : q_phase(ks);
+            if (must) wait(id, parity);
+            q_known = ok && (must || mbar_test(bar(id), parity));
+          }
+          if (q_known && s_i < s_n) {
+            const uint64_t q = dq0 + static_cast<uint64_t>(((ks & 1) * C::Q_BYTES) >> 4);
+            const uint32_t d = tmem + ((ts & 1) ? C::TM_S1 : 0u);
+            uint32_t slot = 0;
 #pragma unroll
-          for (int blk = 0; blk < C::BLKS; ++blk)
-            if (blk < blks) ring.advance();
-          if (next_tiles(false, &n_next) && n_next > 0) {
-            ahead = __all_sync(0xffffffffu, mbar_test(bar(C::Q_FULL + ((k + 1) & 1)), q_phase(k + 1)));
-            if (ahead) first_scores();
+            for (int blk = 0; blk < C::BLKS; ++blk) {
+              if (blk >= blks) break;
+              const uint32_t item = k_at * blks + blk;
+              slot = item % C::SLOTS;
+              wait(C::FULL + slot, (item / C::SLOTS) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t a = dk0 + static_cast<uint64_t>((slot * C::SLOT) >> 4);
+#pragma unroll
+              for (int x = 0; x < KS_BLK; ++x) {
+                const int step = blk * KS_BLK + x;
+                if (step < n_ks)
+                  umma<F8>(d, a + static_cast<uint64_t>(((x >> 2) * C::CHUNK + (x & 3) * 32) >> 4),
+                           q + static_cast<uint64_t>(step * 2 * C::NQ), idesc_s, step > 0 ? 1u : 0u);
+              }
+              if (blk < blks - 1) umma_commit(bar(C::EMPTY + slot));
+            }
+            if (!ok) break;
+            umma_commit(bar(C::S_FULL + (ts & 1)));
+            umma_commit(bar(C::EMPTY + slot));
+            if (ks & 1) n_odd = s_n;
+            else n_even = s_n;
+            // (a last tile's K is followed by its own V, after the one before)
+            k_at += s_i + 1 < s_n ? (s_i == 0 ? 1 : 2) : (s_n == 1 ? 2 : 3);
+            ++s_i;
+            if (s_i == s_n) umma_commit(bar(C::Q_EMPTY + (ks & 1)));
+            ++ts;
+            if (must) continue;
           }
         }
-        // (O is free once the last unit's epilogue has read it)
-        if (i == 0 && k > 0) wait(C::O_FREE, (k - 1) & 1);
-        wait(C::P_FULL + p_buf(t), p_phase(t));
-        const uint64_t pd = dp0 + static_cast<uint64_t>((p_buf(t) * C::P_BYTES) >> 4);
+        if (tp == ts) {
+          if (!more) break;
+          continue;
+        }
+        // ---- O += V^T P^T of tile tp
+        if (p_i == p_n) {
+          ++kp;
+          p_n = (kp & 1) ? n_odd : n_even;
+          p_i = 0;
+          // (O is free once the last unit's epilogue has read it)
+          if (kp > 0) wait(C::O_FREE, (kp - 1) & 1);
+          v_at += p_n == 1 ? 1 : 2;  // (from the unit's first item)
+        }
+        wait(C::P_FULL + p_buf(tp), p_phase(tp));
+        const uint64_t pd = dp0 + static_cast<uint64_t>((p_buf(tp) * C::P_BYTES) >> 4);
+        uint32_t slot = 0;
 #pragma unroll
         for (int blk = 0; blk < C::BLKS; ++blk) {
           if (blk >= blks) break;
-          wait(C::FULL + v.slot, v.phase);
+          const uint32_t item = v_at * blks + blk;
+          slot = item % C::SLOTS;
+          wait(C::FULL + slot, (item / C::SLOTS) & 1);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
-            const uint32_t d = tmem + C::TM_O + blk * C::NP;
-            const uint64_t a = dv0 + static_cast<uint64_t>((v.slot * C::SLOT) >> 4);
+          const uint32_t d = tmem + C::TM_O + blk * C::NP;
+          const uint64_t a = dv0 + static_cast<uint64_t>((slot * C::SLOT) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kKeys / KSTEP; ++ks)
-              umma<F8>(d, a + static_cast<uint64_t>((ks * KSTEP * 128) >> 4),
-                       pd + static_cast<uint64_t>((ks * KSTEP * 16) >> 4), idesc_o,
-                       (i > 0 || ks > 0) ? 1u : 0u);
-            if (blk == blks - 1) umma_commit(bar(C::PV_DONE + p_buf(t)));
-            umma_commit(bar(C::EMPTY + v.slot));
-          }
-          __syncwarp();
-          v.advance();
+          for (int step = 0; step < kKeys / KSTEP; ++step)
+            umma<F8>(d, a + static_cast<uint64_t>((step * KSTEP * 128) >> 4),
+                     pd + static_cast<uint64_t>((step * KSTEP * 16) >> 4), idesc_o,
+                     (p_i > 0 || step > 0) ? 1u : 0u);
+          if (blk < blks - 1) umma_commit(bar(C::EMPTY + slot));
         }
-        if (i + 1 < n) {
-          ring = v;
-        } else {
-          if (n_next < 0) next_tiles(true, &n_next);
-          if (n_next > 0 && !ahead) {
-            wait(C::Q_FULL + ((k + 1) & 1), q_phase(k + 1));
-            if (ok) first_scores();
-          }
-        }
+        if (!ok) break;
+        umma_commit(bar(C::PV_DONE + p_buf(tp)));
+        umma_commit(bar(C::EMPTY + slot));
+        ++p_i;
+        // V(i) to V(i + 1): a K between, but before the last; then the next unit
+        v_at += p_i == p_n ? 1 : (p_i + 1 == p_n ? 1 : 2);
+        ++tp;
       }
-      n = n_next;
-      ++k;
+      // every tensor-core operation issued must be complete before TMEM is freed
+      umma_commit(bar(C::DRAIN));
     }
-    // every tensor-core operation issued must be complete before TMEM is freed
-    if (elect_one()) umma_commit(bar(C::DRAIN));
     __syncwarp();
     volatile int never = 0;
     mbar_wait(bar(C::DRAIN), 0, &never, p.status, site + C::DRAIN);
@@ -903,7 +916,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               ring[slot * kKeys + 32 * z + lane] = static_cast<uint16_t>(k4[y][z] | (v4[y][z] << 8));
-            mbar_arrive(bar(C::SC_FULL + slot));
+            warp_arrive(bar(C::SC_FULL + slot), lane);
             ++t;
           }
         }
@@ -937,7 +950,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         });
         if (!ok) break;
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::Q_FULL + buf));
+        warp_arrive(bar(C::Q_FULL + buf), lane);
       }
       ++k;
     }
@@ -985,7 +998,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       } else {
         prepare_q(std::integral_constant<int, SOFT>{}, it, 0, tid, []() { return true; });
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::Q_FIRST));
+        warp_arrive(bar(C::Q_FIRST), lane);
         wait(C::Q_FIRST, 0);
       }
       const float* factor = row_factor(buf) + r0;
@@ -1180,7 +1193,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
           // 16-byte units [column of units][key]: 16 (8-bit) or 8 rows of a piece
           constexpr int COL = kKeys * 16;
-          if constexpr (F8 && GW == 8) {
+          if constexpr (F8 && NR == 8) {
             // two pieces to a unit; nothing reads the second half of the last
             const uint32_t to = p_at + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w2[0], w2[1]);
@@ -1217,7 +1230,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::P_FULL + p_buf(t)));
+        warp_arrive(bar(C::P_FULL + p_buf(t)), lane);
       }
 
       // ---- epilogue: sums over the keys, then O
@@ -1283,8 +1296,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         }
       }
       tc_fence_before();
-      mbar_arrive(bar(C::O_FREE));
-      mbar_arrive(bar(C::Q_EMPTY + buf));
+      warp_arrive(bar(C::O_FREE), lane);
+      warp_arrive(bar(C::Q_EMPTY + buf), lane);
       ++k;
     }
   }

@@ -22,9 +22,9 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libmha.so")
 
 SOURCES = ["mha_abi.cu", "mha_fwd_bf16.cu", "mha_fwd_wide.cu", "mha_fwd_f32.cu", "mha_decode.cu",
-           "mha_bwd.cu", "mha_gemm.cu", "mha_cache.cu", "mha_rows.cu"]
+           "mha_bwd.cu", "mha_gemm.cu", "mha_cache.cu", "mha_rows.cu", "mha_rows_block.cu"]
 HEADERS = [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "fp8.cuh"),
-           os.path.join(CSRC, "kernels.h"),
+           os.path.join(CSRC, "rows.cuh"), os.path.join(CSRC, "kernels.h"),
            os.path.join(INCLUDE, "mha.h"), os.path.join(INCLUDE, "mha_test_hooks.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

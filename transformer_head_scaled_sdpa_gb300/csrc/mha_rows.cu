@@ -72,18 +72,14 @@
 
 #include "fp8.cuh"
 #include "kernels.h"
+#include "rows.cuh"
 
 namespace mha {
 namespace {
 
-constexpr int kKeys = 128;         // keys per tile
-constexpr int kBoxKeys = 32;       // keys per small TMA box: a ragged last tile loads only what it needs
 constexpr int kScaleTiles = 8;     // tiles whose 8-bit scales are kept ahead
-constexpr int kSms = 152;
-constexpr int kMaxRowSplits = 64;
 constexpr int kQueue = 4;          // published units
 constexpr int kMaskWords = 4;      // 256 drafted tokens
-constexpr int kRoleRowsLoad = 16, kRoleRowsMma = 17, kRoleRowsSoftmax = 18, kRoleRowsQ = 19;
 
 template <bool F8_, int W_, int NR_>
 struct RowsCfg {
@@ -206,12 +202,6 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
   }
 }
 
-// One arrival for a warp, behind what all its lanes did.
-__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-}
-
 // True for every thread of a softmax warpgroup when any of them passes true
 // (named barrier `id` over its 128 threads).
 __device__ __forceinline__ bool any_of_128(uint32_t id, bool x) {
@@ -244,39 +234,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// The bounded wait of mbar_wait in few instructions: one that runs out raises
-// *abort to its site + 1, and the CTA records it in the device status
-// at its end.  (Every role waits in many places; with the status's recording in
-// each of them the roles' code did not fit the instruction caches, and 40 % of the
-// warps' time went to fetching instructions.)
-__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, volatile int* abort, int site) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-  }
-  *abort = site + 1;
-  return false;
-}
-// Whether the phase with this parity has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// By a whole warp with one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, int site) {
-  return __all_sync(0xffffffffu, thread_wait(bar, parity, abort, site));
 }
 
 // Largest value of the warp.
@@ -336,48 +293,6 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t (&r)[N]
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
   }
-}
-
-// ---------------------------------------------------------------------------
-// Units
-// ---------------------------------------------------------------------------
-struct __align__(16) Unit {
-  int b;               // sequence (-1: no more units)
-  int hk, rb, split;   // key head, block of rows, split
-  int t0, t1;          // its tiles (none: a sequence without keys)
-  int n, end;          // keys of the prefix, keys any row may see
-  int live;            // drafted tokens of the sequence
-  int splits;          // of the sequence
-  int pad[2];
-};
-static_assert(sizeof(Unit) == 48, "three 16-byte words");
-
-// A sequence's part in a unit: lengths (clamped), tiles per split, splits.
-__device__ __forceinline__ void unit_keys(const RowsParams& p, Unit* w) {
-  const int n = __ldg(p.prefix_lens + w->b);
-  w->n = n < 0 ? 0 : (n > p.Lk ? p.Lk : n);
-  w->live = p.T;
-  if (p.draft_lens) {
-    const int live = __ldg(p.draft_lens + w->b);
-    w->live = live < 0 ? 0 : (live > p.T ? p.T : live);
-  }
-  w->end = w->live == 0 ? 0 : (p.drafts ? min(p.Lk, w->n + w->live) : w->n);
-  const int tiles = (w->end + kKeys - 1) / kKeys;
-  const int per = (tiles + p.n_splits - 1) / p.n_splits;
-  w->splits = per > 0 ? (tiles + per - 1) / per : 1;
-  w->t0 = min(w->split * per, tiles);
-  w->t1 = min(w->t0 + per, tiles);
-}
-
-__device__ __forceinline__ Unit unit_at(const RowsParams& p, int index, int blocks) {
-  Unit w;
-  const int u = index % p.units, rest = index / p.units;
-  w.hk = blocks == 1 ? u : u / blocks;
-  w.rb = u - w.hk * blocks;
-  w.split = rest / p.B;
-  w.b = rest - w.split * p.B;
-  unit_keys(p, &w);
-  return w;
 }
 
 // A position in the ring of K and V blocks.  A unit's are loaded in the order
@@ -1440,17 +1355,8 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
   const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
   e = launch_serialized(rows_kernel<F8, W, NR>, grid, dim3(C::THREADS), C::SMEM, stream, p);
   if (e != cudaSuccess) return e;
-  int kernels = 1;
-  if (p.n_splits > 1) {
-    const long long rows = static_cast<long long>(p.B) * p.T * p.H;
-    const bool many = p.n_splits >= 8;
-    const int per_block = many ? 1 : 8;
-    e = launch_serialized(many ? rows_combine_kernel<W, 8> : rows_combine_kernel<W, 1>,
-                          dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)), dim3(256), 0, stream, p);
-    kernels = 2;
-  }
   if (info) {
-    info->kernels = kernels;
+    info->kernels = 1;
     info->grid = static_cast<int>(grid.x);
     info->block = C::THREADS;
     info->smem = C::SMEM;
@@ -1460,65 +1366,101 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
 
 // Calls f with the kernel's configuration for R rows per key head of d features.
 template <typename F>
-auto with_config(bool f8, int d, int R, F&& f) {
-  if (f8) {
-    if (d <= 128)
-      return R <= 8    ? f(RowsCfg<true, 128, 8>{})
-             : R <= 16 ? f(RowsCfg<true, 128, 16>{})
-                     : (R <= 32 ? f(RowsCfg<true, 128, 32>{}) : f(RowsCfg<true, 128, 64>{}));
-    return R <= 8 ? f(RowsCfg<true, 256, 8>{}) : (R <= 16 ? f(RowsCfg<true, 256, 16>{}) : f(RowsCfg<true, 256, 32>{}));
+void with_config(bool f8, int d, int R, F&& f) {
+  if (f8 && d <= 128) {
+    if (R <= 8) f(RowsCfg<true, 128, 8>{});
+    else if (R <= 16) f(RowsCfg<true, 128, 16>{});
+    else if (R <= 32) f(RowsCfg<true, 128, 32>{});
+    else f(RowsCfg<true, 128, 64>{});
+  } else if (f8) {
+    if (R <= 8) f(RowsCfg<true, 256, 8>{});
+    else if (R <= 16) f(RowsCfg<true, 256, 16>{});
+    else f(RowsCfg<true, 256, 32>{});
+  } else if (d <= 64) {
+    if (R <= 16) f(RowsCfg<false, 64, 16>{});
+    else if (R <= 32) f(RowsCfg<false, 64, 32>{});
+    else f(RowsCfg<false, 64, 64>{});
+  } else if (d <= 128) {
+    if (R <= 16) f(RowsCfg<false, 128, 16>{});
+    else if (R <= 32) f(RowsCfg<false, 128, 32>{});
+    else f(RowsCfg<false, 128, 64>{});
+  } else {
+    if (R <= 16) f(RowsCfg<false, 256, 16>{});
+    else f(RowsCfg<false, 256, 32>{});
   }
-  if (d <= 64)
-    return R <= 16 ? f(RowsCfg<false, 64, 16>{})
-                   : (R <= 32 ? f(RowsCfg<false, 64, 32>{}) : f(RowsCfg<false, 64, 64>{}));
-  if (d <= 128)
-    return R <= 16 ? f(RowsCfg<false, 128, 16>{})
-                   : (R <= 32 ? f(RowsCfg<false, 128, 32>{}) : f(RowsCfg<false, 128, 64>{}));
-  return R <= 16 ? f(RowsCfg<false, 256, 16>{}) : f(RowsCfg<false, 256, 32>{});
+}
+
+// Whether the rows go along the tensor core's M (mha_rows_block.cu).
+bool block_form(bool f8, int d, int R) { return !f8 && d <= 128 && R > 64; }
+
+template <int W>
+cudaError_t launch_combine(const RowsParams& p, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.B) * p.T * p.H;
+  const bool many = p.n_splits >= 8;
+  const int per_block = many ? 1 : 8;
+  return launch_serialized(many ? rows_combine_kernel<W, 8> : rows_combine_kernel<W, 1>,
+                           dim3(static_cast<unsigned>((rows + per_block - 1) / per_block)), dim3(256), 0, stream, p);
 }
 
 }  // namespace
 
 RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
   const int R = T * (H / H_kv);
-  return with_config(f8, d, R, [&](auto cfg) {
-    using C = decltype(cfg);
-    RowsPlan plan = {};
-    plan.width = C::W;
-    plan.units = static_cast<long long>(H_kv) * ((R + C::NR - 1) / C::NR);
-    const long long base = plan.units * B;
-    const long long slots = static_cast<long long>(kSms) * C::MIN_BLOCKS;
-    const long long tiles = (Lk + kKeys - 1) / kKeys;
-    // Time in half tiles, sequences counted at the cache's capacity: a unit costs
-    // its tiles and five more (its Q, first tile and epilogue); with several units
-    // to a CTA the last ones end half a unit apart; partials cost a second kernel
-    // (some four tiles) and are written and read at about the rate of the keys.
-    // (3 sequences x 8 key heads x 4 blocks of 64 rows x 16,411 keys of 128 features,
-    // by splits: 1 141 us, 2 118, 3 105, 5 113, 7 115; 5 x 2 x 2 blocks of 32 rows x
-    // 20,011 keys of 256 features in 8 bits: 4 67 us, 6 52, 7 48, 8 49, 14 51.)
-    long long best = -1;
-    for (long long S = 1; S <= kMaxRowSplits && S <= tiles && (S == 1 || base * (S - 1) < 4 * slots); ++S) {
-      const long long per = 2 * ((tiles + S - 1) / S) + 10;
-      const long long units = base * S;
-      const long long merge = S == 1 ? 0 : 8 + units * C::NR / (slots * 16 * C::EB);
-      const long long cost = (units <= slots ? per : units * per / slots + per / 2) + merge;
-      if (best >= 0 && cost >= best) continue;
-      best = cost;
-      plan.splits = static_cast<int>(S);
-    }
-    plan.part_rows = plan.splits > 1 ? static_cast<size_t>(plan.splits) * B * T * H : 0;
-    return plan;
-  });
+  RowsPlan plan = {};
+  const bool block = block_form(f8, d, R);
+  int rows = kBlockRows, ctas = 1;  // rows per unit, CTAs per SM
+  plan.width = d <= 64 ? 64 : 128;
+  if (!block)
+    with_config(f8, d, R, [&](auto cfg) {
+      using C = decltype(cfg);
+      plan.width = C::W;
+      rows = C::NR;
+      ctas = C::MIN_BLOCKS;
+    });
+  plan.units = static_cast<long long>(H_kv) * ((R + rows - 1) / rows);
+  const long long base = plan.units * B;
+  const long long slots = static_cast<long long>(kSms) * ctas;
+  const long long tiles = (Lk + kKeys - 1) / kKeys;
+  // Time in half tiles, sequences counted at the cache's capacity: a unit costs
+  // its tiles and five more (its Q, first tile and epilogue); with several units
+  // to a CTA the last ones end half a unit apart; partials cost a second kernel
+  // (some four tiles) and are written and read at about the rate of the keys.
+  // (3 sequences x 8 key heads x 4 blocks of 64 rows x 16,411 keys of 128 features,
+  // by splits: 1 141 us, 2 118, 3 105, 5 113, 7 115; 5 x 2 x 2 blocks of 32 rows x
+  // 20,011 keys of 256 features in 8 bits: 4 67 us, 6 52, 7 48, 8 49, 14 51.)
+  long long best = -1;
+  for (long long S = 1; S <= kMaxRowSplits && S <= tiles && (S == 1 || base * (S - 1) < 4 * slots); ++S) {
+    const long long per = 2 * ((tiles + S - 1) / S) + 10;
+    const long long units = base * S;
+    const long long merge = S == 1 ? 0 : 8 + units * rows / (slots * (f8 ? 16 : 32));
+    const long long cost = (units <= slots ? per : units * per / slots + per / 2) + merge;
+    if (best >= 0 && cost >= best) continue;
+    best = cost;
+    plan.splits = static_cast<int>(S);
+  }
+  plan.part_rows = plan.splits > 1 ? static_cast<size_t>(plan.splits) * B * T * H : 0;
+  return plan;
 }
 
 int rows_tile_keys() { return kKeys; }
 int rows_box_keys() { return kBoxKeys; }
 
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
-  return with_config(p.k_scale != nullptr, p.d, p.T * p.G, [&](auto cfg) {
-    using C = decltype(cfg);
-    return launch_rows_cfg<C::F8, C::W, C::NR>(p, stream, info);
-  });
+  const bool f8 = p.k_scale != nullptr;
+  const int R = p.T * p.G;
+  cudaError_t e = cudaSuccess;
+  if (block_form(f8, p.d, R)) {
+    e = launch_rows_block(p, stream, info);
+  } else {
+    with_config(f8, p.d, R, [&](auto cfg) {
+      using C = decltype(cfg);
+      e = launch_rows_cfg<C::F8, C::W, C::NR>(p, stream, info);
+    });
+  }
+  if (e != cudaSuccess || p.n_splits == 1) return e;
+  if (info) info->kernels = 2;
+  if (!f8 && p.d <= 64) return launch_combine<64>(p, stream);
+  return p.d <= 128 ? launch_combine<128>(p, stream) : launch_combine<256>(p, stream);
 }
 
 }  // namespace mha

@@ -1,0 +1,461 @@
+// Attention of many query rows per key head over a bf16 cache, keys split over CTAs.
+//
+// The steps of mha_rows.cu put the keys along the tensor core's M and a unit's rows
+// along its N, which suits a few rows: a tile of K is an operand as TMA wrote it,
+// whatever the number of rows.  From 64 rows on that costs more than it saves: P
+// goes through shared memory, K and V are read there once per block of 64 rows, and
+// shared memory's 128 bytes per cycle bound the step.  Here a unit has up to 256
+// rows, two tiles of 128 along M that share every tile of K and V:
+//   S_g[128 x 128 keys] = Q_g K^T   (Q, K in shared memory, K-major)
+//   O_g[128 x d] += P_g V           (P in tensor memory, V as loaded, MN-major)
+// with p as two bf16 pieces (the first is p cut to 8 bits, the second the rest
+// rounded: 2^-15), which take the columns of the scores they come from.  Thread =
+// row, so maxima and sums need no exchange; the reference m of a row moves only when
+// a tile's largest score exceeds it by more than 2^8, and O is rescaled then.
+//
+// Bound: per tile of 128 keys and 256 rows of 128 features the tensor core reads
+// 2 x 8 x 8 KB (S) and 2 x 16 x 4 KB (PV) of shared memory, TMA writes 64 KB (2,560
+// cycles at 128 bytes), and 32,768 exponentials take 2,048 cycles; the two row tiles
+// alternate between the tensor core and the softmax.
+//
+// Work: a CTA per (split, sequence, key head, block of 256 rows), key heads the
+// fastest (they lie side by side in the cache).  Partials as in mha_rows.cu.
+//
+// Roles: two softmax warpgroups (one per row tile; they also load its Q and write
+// its output), one MMA lane, one TMA lane.  Every wait is bounded.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace mha {
+namespace {
+
+template <int W_>
+struct BlockCfg {
+  static constexpr int W = W_;                          // widest head: 64 or 128
+  static constexpr int CHUNK = kKeys * 128;             // [128 rows x 64 features], 128-byte swizzle
+  static constexpr int TILE = W / 64 * CHUNK;           // a tile of Q, K or V
+  static constexpr int SLOTS = W == 64 ? 8 : 5;         // ring of K and V tiles
+  static constexpr int THREADS = 384;
+  static constexpr int OFF_Q = SLOTS * TILE;            // + row tile * TILE
+  static constexpr int OFF_MISC = OFF_Q + 2 * TILE;
+  static constexpr int SMEM = OFF_MISC + 256 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+  // barriers
+  static constexpr int FULL = 0;             // + slot
+  static constexpr int EMPTY = SLOTS;        // + slot
+  static constexpr int Q_FULL = 2 * SLOTS;   // + row tile (four warps)
+  static constexpr int S_FULL = Q_FULL + 2;  // + row tile
+  static constexpr int P_FULL = S_FULL + 2;  // + row tile (four warps)
+  static constexpr int O_DONE = P_FULL + 2;  // + row tile
+  static constexpr int DRAIN = O_DONE + 2;
+  static constexpr int NBAR = DRAIN + 1;
+  static constexpr int OFF_TMEM = OFF_MISC + 8 * NBAR;
+  static constexpr int OFF_ABORT = OFF_TMEM + 4;
+  static_assert(8 * NBAR + 8 <= 256, "barrier area");
+  // TMEM: S_0 | S_1 (128 columns each, then P_g's two pieces) | O_0 | O_1
+  static constexpr uint32_t TM_O = 256;
+  static constexpr uint32_t TMEM_COLS = 512;
+  // registers: a softmax thread holds a row's 128 scores
+  static constexpr int REGS_SOFT = 208, REGS_OTHER = 88;
+  static_assert(REGS_SOFT * 256 + REGS_OTHER * 128 <= 168 * THREADS, "register split");
+};
+
+constexpr float kSlack = 8.f;  // a row's reference moves beyond this (log2)
+
+// Which of 32 keys from `off` on, counted from the first drafted key, a row sees:
+// all of the prefix (negative), the drafted ones by its mask words, none behind.
+__device__ __forceinline__ uint32_t sees_32(const uint64_t (&mask)[4], int off) {
+  if (off <= -32) return ~0u;
+  if (off >= 256) return 0;
+  if (off < 0) return ((1u << -off) - 1) | static_cast<uint32_t>(mask[0] << -off);
+  uint64_t lo = mask[0], hi = mask[1];
+  if (off >= 192) {
+    lo = mask[3];
+    hi = 0;
+  } else if (off >= 128) {
+    lo = mask[2];
+    hi = mask[3];
+  } else if (off >= 64) {
+    lo = mask[1];
+    hi = mask[2];
+  }
+  const int sh = off & 63;
+  return static_cast<uint32_t>(sh == 0 ? lo : (lo >> sh) | (hi << (64 - sh)));
+}
+
+template <int W>
+__global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
+    rows_block_kernel(const __grid_constant__ RowsParams p) {
+  using C = BlockCfg<W>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t s_base = smem_u32(smem);
+  auto bar = [&](int i) { return s_base + C::OFF_MISC + 8 * i; };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int tid = static_cast<int>(threadIdx.x);
+  constexpr int kMmaWarp = 8, kLoadWarp = 9;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(bar(C::FULL + i), 1);
+      mbar_init(bar(C::EMPTY + i), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(C::Q_FULL + g), 4);
+      mbar_init(bar(C::S_FULL + g), 1);
+      mbar_init(bar(C::P_FULL + g), 4);
+      mbar_init(bar(C::O_DONE + g), 1);
+    }
+    mbar_init(bar(C::DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), C::TMEM_COLS);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // global memory only from here on
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int n_rows = p.T * p.G;
+  const int blocks = (n_rows + kBlockRows - 1) / kBlockRows;
+  const Unit it = unit_at(p, static_cast<int>(blockIdx.x), blocks);
+  const int n = it.t1 - it.t0;
+  const int rows_here = min(kBlockRows, n_rows - it.rb * kBlockRows);
+  const int tiles_m = rows_here > 128 ? 2 : 1;
+  const bool works = it.split < it.splits && n > 0;  // (a split its sequence does not have; no key at all)
+
+  if (warp >= kMmaWarp) {
+    regs_decrease<C::REGS_OTHER>();
+    if (warp == kLoadWarp && works) {
+      // ---- TMA producer (one lane): K(0) V(0) K(1) V(1) ...
+      const int site = kRoleRowsLoad * 64;
+      if (elect_one()) {
+        const int chunks = (p.d + 63) / 64;
+        int item = 0;
+        bool ok = true;
+        auto load = [&](const CUtensorMap* big, const CUtensorMap* small, int key) {
+          const int s = item % C::SLOTS;
+          ok = ok && (item < C::SLOTS || thread_wait(bar(C::EMPTY + s), ((item / C::SLOTS) - 1) & 1, abort_flag,
+                                                     site + C::EMPTY + s));
+          if (!ok) return;
+          // whole in boxes of 128 keys, a ragged last tile in boxes of kBoxKeys as
+          // far as it goes
+          const int boxes = it.end - key >= kKeys ? 0 : (it.end - key + kBoxKeys - 1) / kBoxKeys;
+          mbar_arrive_expect_tx(bar(C::FULL + s), chunks * 128 * (boxes == 0 ? kKeys : boxes * kBoxKeys));
+          for (int c = 0; c < chunks; ++c) {
+            const uint32_t dst = s_base + s * C::TILE + c * C::CHUNK;
+            if (boxes == 0) {
+              tma_load_4d(dst, big, bar(C::FULL + s), 64 * c, it.hk, key, it.b);
+            } else {
+              for (int x = 0; x < boxes; ++x)
+                tma_load_4d(dst + x * kBoxKeys * 128, small, bar(C::FULL + s), 64 * c, it.hk, key + x * kBoxKeys,
+                            it.b);
+            }
+          }
+          ++item;
+        };
+        for (int x = it.t0; x < it.t1 && ok; ++x) {
+          load(&p.tm_k, &p.tm_k_box, x * kKeys);
+          load(&p.tm_v, &p.tm_v_box, x * kKeys);
+        }
+        // every copy started must land before the CTA exits
+        volatile int never = 0;
+        for (int x = max(0, item - C::SLOTS); x < item; ++x)
+          mbar_wait(bar(C::FULL + x % C::SLOTS), (x / C::SLOTS) & 1, &never, p.status, site + x % C::SLOTS);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp && works) {
+      // ---- MMA issuer (one lane)
+      const int site = kRoleRowsMma * 64;
+      if (elect_one()) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(128, kKeys, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(128, W, false, true);
+        const int n_ks = p.d / 16;
+        const uint64_t dq0 = smem_desc_sw128(s_base + C::OFF_Q, 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(s_base, 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(s_base, C::CHUNK, 1024);
+        bool ok = true;
+        auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
+        // tile i's K lies in ring slot 2 i, its V in 2 i + 1 (modulo the ring)
+        for (int i = -1; i < n && ok; ++i) {
+          for (int g = 0; g < tiles_m && ok; ++g) {
+            if (i >= 0) {
+              // O_g += P_g V(i)
+              const int item = 2 * i + 1, slot = item % C::SLOTS;
+              wait(C::P_FULL + g, i & 1);
+              wait(C::FULL + slot, (item / C::SLOTS) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t b = dv0 + static_cast<uint64_t>((slot * C::TILE) >> 4);
+#pragma unroll
+              for (int ks = 0; ks < 2 * (kKeys / 16); ++ks)  // (both pieces of p)
+                umma_ts(tmem + C::TM_O + g * W, tmem + 128 * g + 8 * ks,
+                        b + static_cast<uint64_t>((ks % (kKeys / 16) * 2048) >> 4), idesc_o,
+                        (i > 0 || ks > 0) ? 1u : 0u);
+              if (g == tiles_m - 1) umma_commit(bar(C::EMPTY + slot));
+              if (i + 1 == n) umma_commit(bar(C::O_DONE + g));
+            }
+            if (i + 1 < n) {
+              // S_g of the next tile, over P_g's columns (the tensor core works in order)
+              const int item = 2 * i + 2, slot = item % C::SLOTS;
+              if (i < 0) wait(C::Q_FULL + g, 0);
+              wait(C::FULL + slot, (item / C::SLOTS) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t a = dq0 + static_cast<uint64_t>((g * C::TILE) >> 4);
+              const uint64_t b = dk0 + static_cast<uint64_t>((slot * C::TILE) >> 4);
+#pragma unroll
+              for (int ks = 0; ks < W / 16; ++ks) {
+                if (ks >= n_ks) break;
+                const uint64_t off = static_cast<uint64_t>(((ks >> 2) * C::CHUNK + (ks & 3) * 32) >> 4);
+                umma_ss(tmem + 128 * g, a + off, b + off, idesc_s, ks > 0 ? 1u : 0u);
+              }
+              umma_commit(bar(C::S_FULL + g));
+              if (g == tiles_m - 1) umma_commit(bar(C::EMPTY + slot));
+            }
+          }
+        }
+        // every tensor-core operation issued must be complete before TMEM is freed
+        umma_commit(bar(C::DRAIN));
+        volatile int never = 0;
+        mbar_wait(bar(C::DRAIN), 0, &never, p.status, site + C::DRAIN);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_increase<C::REGS_SOFT>();
+    // ---- softmax: thread = row r of the unit, row tile g
+    const int g = warp >> 2, r = tid, kt = tid & 127;
+    const int row = it.rb * kBlockRows + r;  // (drafted token, query head of the group)
+    const bool exists = r < rows_here;
+    const int t = exists ? row / p.G : 0;
+    const long long out_row =
+        (static_cast<long long>(it.b) * p.T + t) * p.H + it.hk * p.G + (exists ? row - t * p.G : 0);
+    const bool live = exists && t < it.live;
+    const int site = kRoleRowsSoftmax * 64;
+    if (g < tiles_m && works) {
+      bool ok = true;
+      auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
+      // Q (zeros past the last row).  A negative scale's sign goes into it, so that a
+      // row's largest score is that of its largest product.
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + out_row * p.d);
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const uint32_t to = s_base + C::OFF_Q + g * C::TILE + kt * 128;
+#pragma unroll
+        for (int c = 0; c < W / 64; ++c) {
+          uint4 v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            v[x] = make_uint4(0, 0, 0, 0);
+            if (exists && 8 * (8 * c + x) < p.d) v[x] = __ldg(src + 8 * c + x);
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            st_shared_v4(to + c * C::CHUNK + ((x ^ (kt & 7)) << 4), v[x].x ^ flip, v[x].y ^ flip, v[x].z ^ flip,
+                         v[x].w ^ flip);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(bar(C::Q_FULL + g), lane);
+      }
+      uint64_t mask[4];  // the drafted keys the row sees (none: a row that is not live)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        mask[x] = 0;
+        if (live && p.tree_mask) {
+          if (x < p.words) mask[x] = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t) * p.words + x);
+        } else if (live) {
+          const int bits = t + 1 - 64 * x;  // (a chain: bits 0 .. t)
+          mask[x] = bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
+        }
+      }
+      const float scale = fabsf(p.scale_log2);
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t s_at = t_lane + 128 * g, o_at = t_lane + C::TM_O + g * W;
+      float ref = 0.f, l0 = 0.f, l1 = 0.f;
+      bool seen = false;
+      for (int i = 0; i < n; ++i) {
+        const int key0 = (it.t0 + i) * kKeys;
+        wait(C::S_FULL + g, i & 1);
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s[c]);
+        tmem_ld_wait();
+        if (key0 + kKeys > it.n) {
+          // a tile that reaches behind the prefix
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int key = key0 + 32 * c;
+            uint32_t sees = sees_32(mask, key - it.n);
+            if (key + 32 > it.end) sees = key >= it.end ? 0u : sees & ((1u << (it.end - key)) - 1);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((sees >> x) & 1)) s[c][x] = __float_as_uint(-INFINITY);
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) top = fmax3(top, __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
+        top *= scale;
+        const bool rise = top > (seen ? ref + kSlack : -INFINITY);
+        if (__any_sync(0xffffffffu, rise)) {
+          // (what a row without a key so far has in O is 0 at any reference)
+          const float f = rise && seen ? ex2_approx(ref - top) : 1.f;
+          if (rise) {
+            ref = top;
+            seen = true;
+            l0 *= f;
+            l1 *= f;
+          }
+          // (the scores were issued behind the last product, so O is complete)
+          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < W; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st16(o_at + c, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w1[16], w2[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            float p0, p1, y0, y1;
+            fma2(p0, p1, __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]), scale, scale, -ref, -ref);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            add2(l0, l1, l0, l1, p0, p1);
+            // the first piece is cut, not rounded: its bits are p's own
+            const uint32_t u0 = __float_as_uint(p0) & 0xffff0000u, u1 = __float_as_uint(p1) & 0xffff0000u;
+            w1[x >> 1] = __byte_perm(u0, u1, 0x7632);
+            fma2(y0, y1, __uint_as_float(u0), __uint_as_float(u1), -1.f, -1.f, p0, p1);
+            w2[x >> 1] = pack_bf16x2(y0, y1);
+          }
+          tmem_st16(s_at + 16 * c, w1);
+          tmem_st16(s_at + 64 + 16 * c, w2);
+        }
+        if (g == 0 && key0 + kKeys > it.end) {
+          // a ragged last tile: the V rows past the last key may hold anything
+          // (0 * NaN would be NaN); the second row tile's product comes later
+          const int item = 2 * i + 1, slot = item % C::SLOTS;
+          wait(C::FULL + slot, (item / C::SLOTS) & 1);
+          if (key0 + kt >= it.end) {
+#pragma unroll 1
+            for (int x = 0; x < W / 8; ++x)
+              st_shared_v4(s_base + slot * C::TILE + (x >> 3) * C::CHUNK + kt * 128 + (x & 7) * 16, 0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(bar(C::P_FULL + g), lane);
+      }
+
+      // ---- epilogue
+      wait(C::O_DONE + g, 0);
+      tc_fence_after();
+      const bool good = ok && *abort_flag == 0;
+      const float L = live && good ? l0 + l1 : 0.f;
+      const bool whole = it.splits == 1;
+      const float a = L > 0.f ? (whole ? 1.f / L : 1.f) : 0.f;
+      const long long part = static_cast<long long>(it.split) * p.B * p.T * p.H + out_row;
+      if (exists) {
+        if (!whole) {
+          p.part_m[part] = L > 0.f ? ref : -INFINITY;
+          p.part_l[part] = L;
+        } else if (p.lse) {
+          p.lse[(static_cast<long long>(it.b) * p.H + it.hk * p.G + (row - t * p.G)) * p.T + t] =
+              L > 0.f ? (ref + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < W; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(o_at + c, o);
+        tmem_ld_wait();
+        if (!exists || c >= p.d) continue;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = a > 0.f ? __float_as_uint(__uint_as_float(o[x]) * a) : 0u;
+        if (whole) {
+          uint32_t y[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) y[x] = pack_bf16x2(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]));
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * p.d + c);
+          dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+          dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + part * W + c);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+      }
+      tc_fence_before();
+    } else if (n == 0 && it.split == 0 && exists) {
+      // no key at all: output 0, log-sum-exp -inf
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * p.d);
+      for (int x = 0; 8 * x < p.d; ++x) dst[x] = make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        p.lse[(static_cast<long long>(it.b) * p.H + it.hk * p.G + (row - t * p.G)) * p.T + t] = -INFINITY;
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (tid == 0 && *abort_flag != 0 && atomicCAS(&p.status->code, 0, 7 /* MHA_ERR_TIMEOUT */) == 0) {
+    p.status->site = *abort_flag - 1;
+    p.status->block = static_cast<int>(blockIdx.x);
+  }
+}
+
+template <int W>
+cudaError_t launch_block_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
+  using C = BlockCfg<W>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static bool attr_set[64] = {};
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(rows_block_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
+  e = launch_serialized(rows_block_kernel<W>, grid, dim3(C::THREADS), C::SMEM, stream, p);
+  if (e != cudaSuccess) return e;
+  if (info) {
+    info->kernels = 1;
+    info->grid = static_cast<int>(grid.x);
+    info->block = C::THREADS;
+    info->smem = C::SMEM;
+  }
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_rows_block(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
+  return p.d <= 64 ? launch_block_cfg<64>(p, stream, info) : launch_block_cfg<128>(p, stream, info);
+}
+
+}  // namespace mha

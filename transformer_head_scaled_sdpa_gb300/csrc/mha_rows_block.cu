@@ -9,9 +9,10 @@
 //   S_g[128 x 128 keys] = Q_g K^T   (Q, K in shared memory, K-major)
 //   O_g[128 x d] += P_g V           (P in tensor memory, V as loaded, MN-major)
 // with p as two bf16 pieces (the first is p cut to 8 bits, the second the rest
-// rounded: 2^-15), which take the columns of the scores they come from.  Thread =
-// row, so maxima and sums need no exchange; the reference m of a row moves only when
-// a tile's largest score exceeds it by more than 2^8, and O is rescaled then.
+// rounded: 2^-15), which take the scores' columns.  Two threads per row have 64 keys
+// of a tile each; the reference m of a row moves only when a tile's largest score
+// exceeds it by more than 8 (log2), and O is rescaled then: the halves exchange their
+// maxima only when one of a row tile's rows has to move.
 //
 // Bound: per tile of 128 keys and 256 rows of 128 features the tensor core reads
 // 2 x 8 x 8 KB (S) and 2 x 16 x 4 KB (PV) of shared memory, TMA writes 64 KB (2,560
@@ -21,7 +22,7 @@
 // Work: a CTA per (split, sequence, key head, block of 256 rows), key heads the
 // fastest (they lie side by side in the cache).  Partials as in mha_rows.cu.
 //
-// Roles: two softmax warpgroups (one per row tile; they also load its Q and write
+// Roles: four softmax warpgroups (two per row tile; they also load its Q and write
 // its output), one MMA lane, one TMA lane.  Every wait is bounded.
 #include <cuda_bf16.h>
 
@@ -37,17 +38,18 @@ struct BlockCfg {
   static constexpr int CHUNK = kKeys * 128;             // [128 rows x 64 features], 128-byte swizzle
   static constexpr int TILE = W / 64 * CHUNK;           // a tile of Q, K or V
   static constexpr int SLOTS = W == 64 ? 8 : 5;         // ring of K and V tiles
-  static constexpr int THREADS = 384;
+  static constexpr int THREADS = 640;
   static constexpr int OFF_Q = SLOTS * TILE;            // + row tile * TILE
   static constexpr int OFF_MISC = OFF_Q + 2 * TILE;
-  static constexpr int SMEM = OFF_MISC + 256 + 1024;
+  static constexpr int OFF_XCHG = OFF_MISC + 256;       // a value per row [256]
+  static constexpr int SMEM = OFF_XCHG + 1024 + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   // barriers
   static constexpr int FULL = 0;             // + slot
   static constexpr int EMPTY = SLOTS;        // + slot
-  static constexpr int Q_FULL = 2 * SLOTS;   // + row tile (four warps)
+  static constexpr int Q_FULL = 2 * SLOTS;   // + row tile (eight warps)
   static constexpr int S_FULL = Q_FULL + 2;  // + row tile
-  static constexpr int P_FULL = S_FULL + 2;  // + row tile (four warps)
+  static constexpr int P_FULL = S_FULL + 2;  // + row tile (eight warps)
   static constexpr int O_DONE = P_FULL + 2;  // + row tile
   static constexpr int DRAIN = O_DONE + 2;
   static constexpr int NBAR = DRAIN + 1;
@@ -57,32 +59,43 @@ struct BlockCfg {
   // TMEM: S_0 | S_1 (128 columns each, then P_g's two pieces) | O_0 | O_1
   static constexpr uint32_t TM_O = 256;
   static constexpr uint32_t TMEM_COLS = 512;
-  // registers: a softmax thread holds a row's 128 scores
-  static constexpr int REGS_SOFT = 208, REGS_OTHER = 88;
-  static_assert(REGS_SOFT * 256 + REGS_OTHER * 128 <= 168 * THREADS, "register split");
+  // registers: a softmax thread holds 64 scores
+  static constexpr int REGS_SOFT = 104, REGS_OTHER = 64;
+  static_assert(REGS_SOFT * 512 + REGS_OTHER * 128 <= 96 * THREADS, "register split");
 };
 
 constexpr float kSlack = 8.f;  // a row's reference moves beyond this (log2)
 
-// Which of 32 keys from `off` on, counted from the first drafted key, a row sees:
-// all of the prefix (negative), the drafted ones by its mask words, none behind.
-__device__ __forceinline__ uint32_t sees_32(const uint64_t (&mask)[4], int off) {
+// True for every thread of a row tile's two warpgroups when any of them passes true
+// (named barrier `id` over their 256 threads).
+__device__ __forceinline__ bool any_of_256(uint32_t id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Which of 32 keys from `off` on, counted from the first drafted key, the row of
+// drafted token t sees: all of the prefix (negative), the drafted ones by its mask
+// words (or those up to t), none behind.
+__device__ __forceinline__ uint32_t sees_32(const RowsParams& p, int b, int t, bool live, int off) {
   if (off <= -32) return ~0u;
-  if (off >= 256) return 0;
-  if (off < 0) return ((1u << -off) - 1) | static_cast<uint32_t>(mask[0] << -off);
-  uint64_t lo = mask[0], hi = mask[1];
-  if (off >= 192) {
-    lo = mask[3];
-    hi = 0;
-  } else if (off >= 128) {
-    lo = mask[2];
-    hi = mask[3];
-  } else if (off >= 64) {
-    lo = mask[1];
-    hi = mask[2];
-  }
+  auto word = [&](int x) -> uint64_t {
+    if (!live || x >= p.words) return 0;
+    if (p.tree_mask) return __ldg(p.tree_mask + (static_cast<long long>(b) * p.T + t) * p.words + x);
+    const int bits = t + 1 - 64 * x;
+    return bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
+  };
+  if (off < 0) return ((1u << -off) - 1) | static_cast<uint32_t>(word(0) << -off);
   const int sh = off & 63;
-  return static_cast<uint32_t>(sh == 0 ? lo : (lo >> sh) | (hi << (64 - sh)));
+  const uint64_t lo = word(off >> 6) >> sh;
+  return static_cast<uint32_t>(sh <= 32 ? lo : lo | (word((off >> 6) + 1) << (64 - sh)));
 }
 
 template <int W>
@@ -98,7 +111,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int tid = static_cast<int>(threadIdx.x);
-  constexpr int kMmaWarp = 8, kLoadWarp = 9;
+  constexpr int kMmaWarp = 16, kLoadWarp = 17;
 
   if (tid == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
@@ -106,9 +119,9 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
       mbar_init(bar(C::EMPTY + i), 1);
     }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(bar(C::Q_FULL + g), 4);
+      mbar_init(bar(C::Q_FULL + g), 8);
       mbar_init(bar(C::S_FULL + g), 1);
-      mbar_init(bar(C::P_FULL + g), 4);
+      mbar_init(bar(C::P_FULL + g), 8);
       mbar_init(bar(C::O_DONE + g), 1);
     }
     mbar_init(bar(C::DRAIN), 1);
@@ -234,8 +247,9 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
     }
   } else {
     regs_increase<C::REGS_SOFT>();
-    // ---- softmax: thread = row r of the unit, row tile g
-    const int g = warp >> 2, r = tid, kt = tid & 127;
+    // ---- softmax: two threads per row r of the unit, 64 keys of a tile each; row
+    // tile g has the warpgroups g (first half) and g + 2
+    const int g = (warp >> 2) & 1, half = warp >> 3, kt = tid & 127, r = 128 * g + kt;
     const int row = it.rb * kBlockRows + r;  // (drafted token, query head of the group)
     const bool exists = r < rows_here;
     const int t = exists ? row / p.G : 0;
@@ -243,6 +257,16 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
         (static_cast<long long>(it.b) * p.T + t) * p.H + it.hk * p.G + (exists ? row - t * p.G : 0);
     const bool live = exists && t < it.live;
     const int site = kRoleRowsSoftmax * 64;
+    const uint32_t nbar = 1 + g;
+    // op(first half's x, second half's x) for both threads of a row
+    volatile float* between = reinterpret_cast<volatile float*>(smem + C::OFF_XCHG) + r;
+    auto of_row = [&](float x, auto op) {
+      if (half == 0) *between = x;
+      named_barrier(nbar, 256);
+      if (half == 1) *between = x = op(*between, x);
+      named_barrier(nbar, 256);
+      return half == 0 ? *between : x;
+    };
     if (g < tiles_m && works) {
       bool ok = true;
       auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
@@ -252,66 +276,63 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + out_row * p.d);
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const uint32_t to = s_base + C::OFF_Q + g * C::TILE + kt * 128;
+        constexpr int PER = W / 16;  // 16-byte pieces of a row per thread
+        uint4 v[PER];
 #pragma unroll
-        for (int c = 0; c < W / 64; ++c) {
-          uint4 v[8];
+        for (int x = 0; x < PER; ++x) {
+          v[x] = make_uint4(0, 0, 0, 0);
+          if (exists && 8 * (half * PER + x) < p.d) v[x] = __ldg(src + half * PER + x);
+        }
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            v[x] = make_uint4(0, 0, 0, 0);
-            if (exists && 8 * (8 * c + x) < p.d) v[x] = __ldg(src + 8 * c + x);
-          }
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            st_shared_v4(to + c * C::CHUNK + ((x ^ (kt & 7)) << 4), v[x].x ^ flip, v[x].y ^ flip, v[x].z ^ flip,
-                         v[x].w ^ flip);
+        for (int x = 0; x < PER; ++x) {
+          const int y = half * PER + x;
+          st_shared_v4(to + (y >> 3) * C::CHUNK + (((y & 7) ^ (kt & 7)) << 4), v[x].x ^ flip, v[x].y ^ flip,
+                       v[x].z ^ flip, v[x].w ^ flip);
         }
         fence_proxy_async_smem();
         warp_arrive(bar(C::Q_FULL + g), lane);
       }
-      uint64_t mask[4];  // the drafted keys the row sees (none: a row that is not live)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        mask[x] = 0;
-        if (live && p.tree_mask) {
-          if (x < p.words) mask[x] = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t) * p.words + x);
-        } else if (live) {
-          const int bits = t + 1 - 64 * x;  // (a chain: bits 0 .. t)
-          mask[x] = bits >= 64 ? ~0ull : (bits <= 0 ? 0ull : (1ull << bits) - 1);
-        }
-      }
       const float scale = fabsf(p.scale_log2);
       const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t s_at = t_lane + 128 * g, o_at = t_lane + C::TM_O + g * W;
-      float ref = 0.f, l0 = 0.f, l1 = 0.f;
+      float ref = 0.f, l0 = 0.f, l1 = 0.f;  // (the sums: of this thread's keys)
       bool seen = false;
       for (int i = 0; i < n; ++i) {
         const int key0 = (it.t0 + i) * kKeys;
         wait(C::S_FULL + g, i & 1);
         tc_fence_after();
-        uint32_t s[4][32];
+        uint32_t s[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, s[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld32(s_at + 64 * half + 32 * c, s[c]);
         tmem_ld_wait();
         if (key0 + kKeys > it.n) {
           // a tile that reaches behind the prefix
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = key0 + 32 * c;
-            uint32_t sees = sees_32(mask, key - it.n);
+          for (int c = 0; c < 2; ++c) {
+            const int key = key0 + 64 * half + 32 * c;
+            uint32_t sees = sees_32(p, it.b, t, live, key - it.n);
             if (key + 32 > it.end) sees = key >= it.end ? 0u : sees & ((1u << (it.end - key)) - 1);
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               if (!((sees >> x) & 1)) s[c][x] = __float_as_uint(-INFINITY);
           }
         }
-        float top = -INFINITY;
+        float top = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) top = fmax3(top, __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
-        top *= scale;
-        const bool rise = top > (seen ? ref + kSlack : -INFINITY);
-        if (__any_sync(0xffffffffu, rise)) {
+        for (int x = 0; x < 32; x += 2) {
+          top = fmax3(top, __uint_as_float(s[0][x]), __uint_as_float(s[0][x + 1]));
+          top1 = fmax3(top1, __uint_as_float(s[1][x]), __uint_as_float(s[1][x + 1]));
+        }
+        top = fmaxf(top, top1) * scale;
+        const float limit = seen ? ref + kSlack : -INFINITY;
+        // (this barrier also keeps P, which takes the scores' columns, behind the
+        // other half's reading of them)
+        tc_fence_before();
+        const bool moves = any_of_256(nbar, top > limit);
+        tc_fence_after();
+        if (moves) {
+          top = of_row(top, [](float x, float y) { return fmaxf(x, y); });
+          const bool rise = top > limit;
           // (what a row without a key so far has in O is 0 at any reference)
           const float f = rise && seen ? ex2_approx(ref - top) : 1.f;
           if (rise) {
@@ -323,7 +344,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
           // (the scores were issued behind the last product, so O is complete)
           if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-            for (int c = 0; c < W; c += 16) {
+            for (int c = half * (W / 2); c < (half + 1) * (W / 2); c += 16) {
               uint32_t o[16];
               tmem_ld16(o_at + c, o);
               tmem_ld_wait();
@@ -333,13 +354,14 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
             }
           }
         }
+        const float nref = -ref;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t w1[16], w2[16];
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
             float p0, p1, y0, y1;
-            fma2(p0, p1, __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]), scale, scale, -ref, -ref);
+            fma2(p0, p1, __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]), scale, scale, nref, nref);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
             add2(l0, l1, l0, l1, p0, p1);
@@ -349,8 +371,8 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
             fma2(y0, y1, __uint_as_float(u0), __uint_as_float(u1), -1.f, -1.f, p0, p1);
             w2[x >> 1] = pack_bf16x2(y0, y1);
           }
-          tmem_st16(s_at + 16 * c, w1);
-          tmem_st16(s_at + 64 + 16 * c, w2);
+          tmem_st16(s_at + 32 * half + 16 * c, w1);
+          tmem_st16(s_at + 64 + 32 * half + 16 * c, w2);
         }
         if (g == 0 && key0 + kKeys > it.end) {
           // a ragged last tile: the V rows past the last key may hold anything
@@ -359,7 +381,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
           wait(C::FULL + slot, (item / C::SLOTS) & 1);
           if (key0 + kt >= it.end) {
 #pragma unroll 1
-            for (int x = 0; x < W / 8; ++x)
+            for (int x = half * (W / 16); x < (half + 1) * (W / 16); ++x)
               st_shared_v4(s_base + slot * C::TILE + (x >> 3) * C::CHUNK + kt * 128 + (x & 7) * 16, 0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -373,11 +395,12 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
       wait(C::O_DONE + g, 0);
       tc_fence_after();
       const bool good = ok && *abort_flag == 0;
-      const float L = live && good ? l0 + l1 : 0.f;
+      const float sum = of_row(l0 + l1, [](float x, float y) { return x + y; });
+      const float L = live && good ? sum : 0.f;
       const bool whole = it.splits == 1;
       const float a = L > 0.f ? (whole ? 1.f / L : 1.f) : 0.f;
       const long long part = static_cast<long long>(it.split) * p.B * p.T * p.H + out_row;
-      if (exists) {
+      if (exists && half == 0) {
         if (!whole) {
           p.part_m[part] = L > 0.f ? ref : -INFINITY;
           p.part_l[part] = L;
@@ -387,7 +410,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
         }
       }
 #pragma unroll 1
-      for (int c = 0; c < W; c += 16) {
+      for (int c = half * (W / 2); c < (half + 1) * (W / 2); c += 16) {
         uint32_t o[16];
         tmem_ld16(o_at + c, o);
         tmem_ld_wait();
@@ -408,7 +431,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
         }
       }
       tc_fence_before();
-    } else if (n == 0 && it.split == 0 && exists) {
+    } else if (n == 0 && it.split == 0 && exists && half == 0) {
       // no key at all: output 0, log-sum-exp -inf
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * p.d);
       for (int x = 0; 8 * x < p.d; ++x) dst[x] = make_uint4(0, 0, 0, 0);

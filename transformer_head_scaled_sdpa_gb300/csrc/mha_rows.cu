@@ -100,7 +100,7 @@ struct RowsCfg {
   static constexpr int P_BUFS = W <= 128 || (F8 && NR >= 32) ? 2 : 1;
   // barriers (512 bytes), units, scales, per-row values of two units and of the softmax
   static constexpr int SCALES = F8 ? kScaleTiles * kKeys * 2 : 0;
-  static constexpr int MISC = 576 + 48 * kQueue + 16 + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
+  static constexpr int MISC = 576 + 48 * kQueue + 16 + 160 + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
   static constexpr int FIXED = 2 * Q_BYTES + P_BUFS * P_BYTES + MISC + 1024;
   // TMEM: S0 | S1 | O (per 128 features)
   static constexpr int M_O = W == 64 ? 64 : 128;         // rows of the O^T tile
@@ -152,7 +152,8 @@ struct RowsCfg {
   static_assert(8 * NBAR + 8 <= 512 + 64, "barrier area");
   static constexpr int OFF_QUEUE = OFF_MISC + 576;       // Unit [kQueue], then the response (16 bytes)
   static constexpr int OFF_CLC = OFF_QUEUE + 48 * kQueue;
-  static constexpr int OFF_SCALES = OFF_CLC + 16;  // [kScaleTiles][128]: k's byte, v's byte
+  static constexpr int OFF_TABLE = OFF_CLC + 16;  // sequences' first parts [33], tiles of a split (160 bytes)
+  static constexpr int OFF_SCALES = OFF_TABLE + 160;  // [kScaleTiles][128]: k's byte, v's byte
   static constexpr int OFF_ROWS = OFF_SCALES + SCALES;
   // per buffer: factor, output row, lse index, live [NR each], mask words [NR][4]
   static constexpr int ROWS_BYTES = (16 + 8 * kMaskWords) * NR;
@@ -539,6 +540,28 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   if (warp == kLoadWarp) {
     // ---- TMA producer (one lane)
     const int site = kRoleRowsLoad * 64;
+    int* table = reinterpret_cast<int*>(smem + C::OFF_TABLE);
+    if (balanced(p)) {
+      int first, splits, per;
+      balance(p, lane, &first, &splits, &per);
+      if (lane < p.B) table[lane + 1] = first + splits;
+      if (lane == 0) {
+        table[0] = 0;
+        table[p.B + 1] = per;
+      }
+      __syncwarp();
+    }
+    auto unit_at = [&](int index) {
+      const int part = index / p.units;
+      if (!balanced(p)) return unit_of(p, index, blocks, part % p.B, part / p.B, 0);
+      int b = 0;
+      while (b < p.B && part >= table[b + 1]) ++b;
+      if (b == p.B) {
+        Unit none = {};
+        return none;
+      }
+      return unit_of(p, index, blocks, b, part - table[b], table[p.B + 1]);
+    };
     if (elect_one()) {
       Ring<C::SLOTS> ring;
       int loaded = 0;  // slots filled so far
@@ -590,8 +613,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       };
       uint32_t answers = 0;
       bool asked = false, done = false;
-      Unit w = unit_at(p, static_cast<int>(blockIdx.x), blocks), next = w;
-      bool got = w.split < w.splits;  // a unit to work on (false: a split its sequence does not have)
+      Unit w = unit_at(static_cast<int>(blockIdx.x)), next = w;
+      bool got = w.splits > 0;  // a unit to work on
       if (got) publish(w);
       while (ok) {
         const bool works = got;
@@ -613,8 +636,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             fence_proxy_async_smem();  // (the next response overwrites this one)
             done = index < 0;
             if (done || !ok) return;
-            next = unit_at(p, index, blocks);
-            got = next.split < next.splits;
+            next = unit_at(index);
+            got = next.splits > 0;
             if (got) publish(next);
           }
         };
@@ -878,13 +901,12 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     constexpr int RPT = C::RPT, GW = C::GW, GROUPS = C::GROUPS;
     const int wg = warp >> 2, r0 = wg * RPT, kt = tid & 127, w4 = warp & 3;
     const uint32_t nbar = 1 + wg;  // this warpgroup's named barrier
-    const long long total_rows = static_cast<long long>(p.B) * p.T * p.H;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
     bool ok = true;
     auto wait = [&](int id, uint32_t parity) {
       ok = ok && thread_wait(bar(id), parity, abort_flag, site + id);
     };
-    {
+    if (!balanced(p)) {
       // the first unit's Q before the ring's first copies (it is this CTA's own)
       Unit own;
       const int index = static_cast<int>(blockIdx.x), u = index % p.units;
@@ -1160,7 +1182,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       named_barrier(nbar, 128);
       const bool whole = it.splits == 1;
       const int* outs = row_out(buf) + r0;
-      const long long part = it.split * total_rows;  // the split's partials
+      const long long part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
       if (kt < rows_here && kt < RPT) {
         const float4 l4 = *reinterpret_cast<const float4*>(red + (r0 + kt) * 4);
         float L = l4.x + l4.y + l4.z + l4.w;
@@ -1242,21 +1264,29 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
   const long long rows = static_cast<long long>(p.B) * p.T * p.H;
   const long long row = static_cast<long long>(blockIdx.x) * (8 / WARPS) + warp / WARPS;
   const int bt = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<long long>(bt) * p.H);
-  Unit w;
-  w.b = bt / p.T;
-  w.split = 0;
-  w.splits = 1;
+  const int b = bt / p.T;
   // The lengths may be read before the wait: the rows kernel, which does not write
   // them, let this one start after its own wait for whatever came before.
-  if (row < rows) unit_keys(p, &w);
+  int splits = 1;
+  long long at = row, step = rows;  // the first partial; from one to the next
+  if (row < rows) {
+    if (balanced(p)) {
+      int first, per;
+      balance(p, lane, &first, &splits, &per);
+      splits = __shfl_sync(0xffffffffu, splits, b);
+      step = static_cast<long long>(p.T) * p.H;
+      at += (__shfl_sync(0xffffffffu, first, b) - b) * step;
+    } else {
+      splits = unit_of(p, 0, 1, b, 0, 0).splits;
+    }
+  }
   griddep_wait();  // the splits' partials are complete and visible
-  const int splits = w.splits;
   float o[EPL], L = 0.f, M = -INFINITY;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) o[e] = 0.f;
   if (splits > 1) {
     auto load = [&](int x, float (&y)[EPL]) {
-      const float* src = p.part_o + (x * rows + row) * W + lane * EPL;
+      const float* src = p.part_o + (at + x * step) * W + lane * EPL;
       if constexpr (EPL == 2) {
         const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
         y[0] = v.x, y[1] = v.y;
@@ -1278,8 +1308,8 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
       m[i] = -INFINITY;
       a[i] = 0.f;
       if (x < splits) {
-        m[i] = __ldcg(p.part_m + x * rows + row);
-        a[i] = __ldcg(p.part_l + x * rows + row);
+        m[i] = __ldcg(p.part_m + at + x * step);
+        a[i] = __ldcg(p.part_l + at + x * step);
       }
     }
     M = warp_max(fmaxf(m[0], m[1]));
@@ -1334,7 +1364,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
     else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
   }
   if (p.lse && lane == 0)
-    p.lse[(static_cast<long long>(w.b) * p.H + h) * p.T + (bt - w.b * p.T)] =
+    p.lse[(static_cast<long long>(b) * p.H + h) * p.T + (bt - b * p.T)] =
         L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 

@@ -141,11 +141,26 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
 
   const int n_rows = p.T * p.G;
   const int blocks = (n_rows + kBlockRows - 1) / kBlockRows;
-  const Unit it = unit_at(p, static_cast<int>(blockIdx.x), blocks);
+  Unit it;
+  {
+    const int index = static_cast<int>(blockIdx.x), part = index / p.units;
+    int b = part % p.B, split = part / p.B, per = 0;
+    bool there = true;
+    if (balanced(p)) {
+      int first, splits;
+      balance(p, lane, &first, &splits, &per);
+      const unsigned has = __ballot_sync(0xffffffffu, part >= first && part < first + splits);
+      there = has != 0;
+      b = max(0, __ffs(has) - 1);
+      split = part - __shfl_sync(0xffffffffu, first, b);
+    }
+    it = unit_of(p, index, blocks, b, split, per);
+    if (!there) it.splits = 0;
+  }
   const int n = it.t1 - it.t0;
   const int rows_here = min(kBlockRows, n_rows - it.rb * kBlockRows);
   const int tiles_m = rows_here > 128 ? 2 : 1;
-  const bool works = it.split < it.splits && n > 0;  // (a split its sequence does not have; no key at all)
+  const bool works = it.splits > 0 && n > 0;  // (no such unit; no key at all)
 
   if (warp >= kMmaWarp) {
     regs_decrease<C::REGS_OTHER>();
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
       const float L = live && good ? sum : 0.f;
       const bool whole = it.splits == 1;
       const float a = L > 0.f ? (whole ? 1.f / L : 1.f) : 0.f;
-      const long long part = static_cast<long long>(it.split) * p.B * p.T * p.H + out_row;
+      const long long part = static_cast<long long>(it.part - it.b) * p.T * p.H + out_row;
       if (exists && half == 0) {
         if (!whole) {
           p.part_m[part] = L > 0.f ? ref : -INFINITY;
@@ -431,7 +446,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
         }
       }
       tc_fence_before();
-    } else if (n == 0 && it.split == 0 && exists && half == 0) {
+    } else if (it.splits > 0 && n == 0 && exists && half == 0) {
       // no key at all: output 0, log-sum-exp -inf
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * p.d);
       for (int x = 0; 8 * x < p.d; ++x) dst[x] = make_uint4(0, 0, 0, 0);

@@ -57,40 +57,72 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // ---------------------------------------------------------------------------
 struct __align__(16) Unit {
   int b;               // sequence (-1: no more units)
-  int hk, rb, split;   // key head, block of rows, split
+  int hk, rb;          // key head, block of rows
+  int part;            // number of the (split, sequence): its place in the partials
   int t0, t1;          // its tiles (none: a sequence without keys)
   int n, end;          // keys of the prefix, keys any row may see
   int live;            // drafted tokens of the sequence
-  int splits;          // of the sequence
+  int splits;          // of the sequence (0: no such unit)
   int pad[2];
 };
 static_assert(sizeof(Unit) == 48, "three 16-byte words");
 
-// A sequence's part in a unit: lengths (clamped), tiles per split, splits.
-__device__ __forceinline__ void unit_keys(const RowsParams& p, Unit* w) {
-  const int n = __ldg(p.prefix_lens + w->b);
-  w->n = n < 0 ? 0 : (n > p.Lk ? p.Lk : n);
-  w->live = p.T;
-  if (p.draft_lens) {
-    const int live = __ldg(p.draft_lens + w->b);
-    w->live = live < 0 ? 0 : (live > p.T ? p.T : live);
-  }
-  w->end = w->live == 0 ? 0 : (p.drafts ? min(p.Lk, w->n + w->live) : w->n);
-  const int tiles = (w->end + kKeys - 1) / kKeys;
-  const int per = (tiles + p.n_splits - 1) / p.n_splits;
-  w->splits = per > 0 ? (tiles + per - 1) / per : 1;
-  w->t0 = min(w->split * per, tiles);
-  w->t1 = min(w->t0 + per, tiles);
+// A sequence's lengths (clamped): returns the keys that any row may see.
+__device__ __forceinline__ int seq_end(const RowsParams& p, int b, int* n, int* live) {
+  *n = min(max(__ldg(p.prefix_lens + b), 0), p.Lk);
+  *live = p.draft_lens ? min(max(__ldg(p.draft_lens + b), 0), p.T) : p.T;
+  return *live == 0 ? 0 : (p.drafts ? min(p.Lk, *n + *live) : *n);
 }
 
-__device__ __forceinline__ Unit unit_at(const RowsParams& p, int index, int blocks) {
+// Splits of up to 32 sequences' keys go by one number of tiles for all of them, the
+// smallest with which the units fit the launch (p.n_splits per sequence on average):
+// a long sequence of a ragged batch then has more splits than a short one, and units
+// are of one size.  (Equal numbers of splits, by lengths: 5 sequences of 7,001 to
+// 20,000 keys BAL1; 3 of 9,001 to 16,300 BAL2.)  With more sequences the units of
+// different sizes even out over the machine, and each is divided by p.n_splits.
+constexpr int kBalanced = 32;
+__device__ __forceinline__ bool balanced(const RowsParams& p) { return p.n_splits > 1 && p.B <= kBalanced; }
+
+// By a whole warp: lane b has sequence b's first (split, sequence) number and splits;
+// *per: tiles of a split.
+__device__ __forceinline__ void balance(const RowsParams& p, int lane, int* first, int* splits, int* per) {
+  int n, live;
+  const int tiles = lane < p.B ? (seq_end(p, lane, &n, &live) + kKeys - 1) / kKeys : 0;
+  const int most = __reduce_max_sync(0xffffffffu, tiles), all = __reduce_add_sync(0xffffffffu, tiles);
+  const int units = p.n_splits * p.B;
+  const int lo = max(1, max((all + units - 1) / units, (most + kMaxRowSplits - 1) / kMaxRowSplits));
+  const int hi = max(lo, (most + p.n_splits - 1) / p.n_splits);  // (fits: p.n_splits each)
+  const int mine = lane == 31 ? hi : min(hi, lo + lane * ((hi - lo) / 32 + 1));
+  int sum = 0;
+  for (int b = 0; b < p.B; ++b) sum += max(1, (__shfl_sync(0xffffffffu, tiles, b) + mine - 1) / mine);
+  const unsigned fits = __ballot_sync(0xffffffffu, sum <= units);
+  *per = __shfl_sync(0xffffffffu, mine, __ffs(fits) - 1);
+  *splits = lane < p.B ? max(1, (tiles + *per - 1) / *per) : 0;
+  int last = *splits;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, last, o);
+    if (lane >= o) last += x;
+  }
+  *first = last - *splits;
+}
+
+// Unit `index` of a launch, of sequence b whose keys are in `splits` splits of `per`
+// tiles.
+__device__ __forceinline__ Unit unit_of(const RowsParams& p, int index, int blocks, int b, int split, int per) {
   Unit w;
-  const int u = index % p.units, rest = index / p.units;
+  const int u = index % p.units;
   w.hk = blocks == 1 ? u : u / blocks;
   w.rb = u - w.hk * blocks;
-  w.split = rest / p.B;
-  w.b = rest - w.split * p.B;
-  unit_keys(p, &w);
+  w.part = index / p.units;
+  w.b = b;
+  w.end = seq_end(p, b, &w.n, &w.live);
+  const int tiles = (w.end + kKeys - 1) / kKeys;
+  if (per == 0) per = (tiles + p.n_splits - 1) / p.n_splits;  // (not balanced)
+  w.splits = per > 0 ? max(1, (tiles + per - 1) / per) : 1;
+  if (split >= w.splits) w.splits = 0;
+  w.t0 = min(split * per, tiles);
+  w.t1 = min(w.t0 + per, tiles);
   return w;
 }
 

@@ -114,7 +114,7 @@ struct RowsCfg {
   static constexpr int SLOTS2 = (115712 - FIXED) / SLOT;
   static constexpr bool TWO = SLOTS2 >= (BLKS == 1 ? 4 : 5) && NR <= 32 && TMEM_COLS <= 256;
   // softmax warpgroups: a CTA that has the SM to itself has two from 32 rows on
-  static constexpr int WGS = NR <= 16 || TWO ? 1 : 2;
+  static constexpr int WGS = NR <= 8 || (NR <= 16 && !TWO) ? 1 : 2;
   static constexpr int RPT = NR / WGS;                   // rows per softmax thread
   static constexpr int THREADS = 128 * WGS + 128;
   static constexpr int GW = RPT < 16 ? RPT : 16;         // rows handled together
@@ -163,10 +163,10 @@ struct RowsCfg {
   static constexpr float LIFT = F8 ? 10.f : 0.f;         // weights are 2^LIFT at the reference
   // registers: the softmax warpgroups take from the others
   static constexpr bool SPLIT_REGS = TWO || WGS > 1;
-  static constexpr int REGS_OTHER = TWO && NR > 16 ? 80 : 96;
-  static constexpr int REGS_SOFT = TWO ? 256 - REGS_OTHER : 200;
-  static_assert(!TWO || (REGS_OTHER + REGS_SOFT) * 128 <= 256 * 128, "register split");
-  static_assert(WGS != 2 || REGS_OTHER * 128 + REGS_SOFT * 256 <= 168 * 384, "register split");
+  static constexpr int REGS_OTHER = TWO && WGS == 2 ? 64 : 96;
+  static constexpr int REGS_SOFT = TWO ? (WGS == 2 ? 88 : 256 - REGS_OTHER) : 200;
+  static_assert(!TWO || WGS == 2 || (REGS_OTHER + REGS_SOFT) * 128 <= 256 * 128, "register split");
+  static_assert(WGS != 2 || REGS_OTHER * 128 + REGS_SOFT * 256 <= (TWO ? 80 : 168) * 384, "register split");
 };
 
 // Shared-memory matrix descriptor without swizzle: core matrices of 8 rows x
@@ -1135,6 +1135,12 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             const uint32_t to = p_at + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w2[0], w2[1]);
             st_shared_v4(to + COL, w3[0], w3[1], 0, 0);
+          } else if constexpr (F8 && GW == 8) {
+            // half a unit
+            const uint32_t to = p_at + r0 / 16 * COL + kt * 16 + (r0 & 8);
+            st_shared_v2(to, w1[0], w1[1]);
+            st_shared_v2(to + (NR / 16) * COL, w2[0], w2[1]);
+            st_shared_v2(to + 2 * (NR / 16) * COL, w3[0], w3[1]);
           } else if constexpr (F8) {
             const uint32_t to = p_at + (r0 / 16 + g) * COL + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w1[2], w1[3]);

@@ -195,13 +195,20 @@ struct CacheParams {
 long long cache_blocks(int B, int T, int H);
 cudaError_t launch_cache(const CacheParams& p, bool write, cudaStream_t stream, LaunchInfo* info);
 
-// A few query rows per sequence over a cache, mha_rows.cu.
+// A few query rows per sequence over a cache.
+enum RowsForm {
+  kRowsKeys,    // keys along the tensor core's M (mha_rows.cu)
+  kRowsBlock,   // rows along its M (mha_rows_block.cu)
+  kRowsShort,   // CUDA cores (mha_rows_short.cu)
+};
 struct RowsParams {
   CUtensorMap tm_k;   // [B, Lk, H_kv, d] bf16, or e4m3 codes when k_scale is set;
   CUtensorMap tm_v;   // box {128 bytes, 1, rows_tile_keys(), 1}, 128-byte swizzle
   CUtensorMap tm_k_box;  // the same with boxes of rows_box_keys() keys
   CUtensorMap tm_v_box;
   const void* q;      // [B, T, H, d] bf16
+  const void* k_codes;     // the 8-bit cache itself (mha_rows_short.cu reads it without TMA)
+  const void* v_codes;
   const uint8_t* k_scale;  // [B, H_kv, Lk] biased exponents, or null (bf16 cache)
   const uint8_t* v_scale;
   void* out;          // [B, T, H, d] bf16
@@ -219,11 +226,13 @@ struct RowsParams {
   int words;          // 64-bit mask words per row
   int units;          // (key head, block of rows) pairs per sequence
   int n_splits;       // splits of the key axis
+  RowsForm form;
   float scale_log2;   // scale * log2(e)
 };
 
 // How a launch of these sizes divides its work.
 struct RowsPlan {
+  RowsForm form;
   long long units;    // (key head, block of rows) pairs per sequence
   int splits;
   size_t part_rows;   // rows of partials in the workspace (0: none)

@@ -769,11 +769,15 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   auto encode = [&](CUtensorMap* m, const void* base, int keys) {
     return f8 ? encode_map_f8(m, base, B, Lk, H_kv, d_k, keys) : encode_map(m, base, B, Lk, H_kv, d_k, keys);
   };
-  if (!encode(&p.tm_k, k_cache, mha::rows_tile_keys()) || !encode(&p.tm_v, v_cache, mha::rows_tile_keys()) ||
+  if (plan.form != mha::kRowsShort &&
+      (!encode(&p.tm_k, k_cache, mha::rows_tile_keys()) || !encode(&p.tm_v, v_cache, mha::rows_tile_keys()) ||
       !encode(&p.tm_k_box, k_cache, mha::rows_box_keys()) ||
-      !encode(&p.tm_v_box, v_cache, mha::rows_box_keys()))
+      !encode(&p.tm_v_box, v_cache, mha::rows_box_keys())))
     return MHA_ERR_UNSUPPORTED;
   p.q = q;
+  p.k_codes = k_cache;
+  p.v_codes = v_cache;
+  p.form = plan.form;
   p.k_scale = f8 ? k_scale : nullptr;
   p.v_scale = f8 ? v_scale : nullptr;
   p.out = out;

@@ -1426,8 +1426,20 @@ void with_config(bool f8, int d, int R, F&& f) {
   }
 }
 
-// Whether the rows go along the tensor core's M (mha_rows_block.cu).
-bool block_form(bool f8, int d, int R) { return !f8 && d <= 128 && R > 64; }
+// The kernel for T rows of G query heads per key head.
+//   More than 64 rows over a bf16 cache: along M (3 x 8 key heads x 16,000 keys of
+//   128 features: 60 rows 56 us along N and 58 along M, 96 rows 68 and 58, 128 rows
+//   68 and 60; 64 rows of 8 blocks: 566 and 269 at 2,048 rows x 32,000 keys).
+//   A row or two over a short 8-bit cache: the CUDA cores (features x keys of the
+//   cache, full: 128 x 8 heads 64 x 64 15 us here and 25 on the tensor cores, 64 x
+//   128 17 and 23, 64 x 256 23 and 25, half full 10 and 23; 16 x 96 heads 128 x 64
+//   21 and 29, 128 x 128 27 and 27, 128 x 256 44 and 33; two rows 64 x 256 31 and
+//   25).
+RowsForm rows_form(bool f8, int d, int T, int G, int Lk) {
+  if (!f8 && d <= 128 && T * G > 64) return kRowsBlock;
+  if (f8 && T == 1 && G <= kShortRows && static_cast<long long>(Lk) * d * G <= kShortWork) return kRowsShort;
+  return kRowsKeys;
+}
 
 template <int W>
 cudaError_t launch_combine(const RowsParams& p, cudaStream_t stream) {
@@ -1443,10 +1455,15 @@ cudaError_t launch_combine(const RowsParams& p, cudaStream_t stream) {
 RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
   const int R = T * (H / H_kv);
   RowsPlan plan = {};
-  const bool block = block_form(f8, d, R);
+  plan.form = rows_form(f8, d, T, H / H_kv, Lk);
+  if (plan.form == kRowsShort) {
+    plan.units = H_kv;
+    plan.splits = 1;
+    return plan;
+  }
   int rows = kBlockRows, ctas = 1;  // rows per unit, CTAs per SM
   plan.width = d <= 64 ? 64 : 128;
-  if (!block)
+  if (plan.form == kRowsKeys)
     with_config(f8, d, R, [&](auto cfg) {
       using C = decltype(cfg);
       plan.width = C::W;
@@ -1485,7 +1502,9 @@ cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* in
   const bool f8 = p.k_scale != nullptr;
   const int R = p.T * p.G;
   cudaError_t e = cudaSuccess;
-  if (block_form(f8, p.d, R)) {
+  if (p.form == kRowsShort) {
+    e = launch_rows_short(p, stream, info);
+  } else if (p.form == kRowsBlock) {
     e = launch_rows_block(p, stream, info);
   } else {
     with_config(f8, p.d, R, [&](auto cfg) {

@@ -285,11 +285,9 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
     if (g < tiles_m && works) {
       bool ok = true;
       auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
-      // Q (zeros past the last row).  A negative scale's sign goes into it, so that a
-      // row's largest score is that of its largest product.
+      // Q (zeros past the last row)
       {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + out_row * p.d);
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const uint32_t to = s_base + C::OFF_Q + g * C::TILE + kt * 128;
         constexpr int PER = W / 16;  // 16-byte pieces of a row per thread
         uint4 v[PER];
@@ -301,13 +299,12 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
           const int y = half * PER + x;
-          st_shared_v4(to + (y >> 3) * C::CHUNK + (((y & 7) ^ (kt & 7)) << 4), v[x].x ^ flip, v[x].y ^ flip,
-                       v[x].z ^ flip, v[x].w ^ flip);
+          st_shared_v4(to + (y >> 3) * C::CHUNK + (((y & 7) ^ (kt & 7)) << 4), v[x].x, v[x].y, v[x].z, v[x].w);
         }
         fence_proxy_async_smem();
         warp_arrive(bar(C::Q_FULL + g), lane);
       }
-      const float scale = fabsf(p.scale_log2);
+      const float scale = p.scale_log2;  // (positive)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t s_at = t_lane + 128 * g, o_at = t_lane + C::TM_O + g * W;
       float ref = 0.f, l0 = 0.f, l1 = 0.f;  // (the sums: of this thread's keys)

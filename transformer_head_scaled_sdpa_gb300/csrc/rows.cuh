@@ -77,8 +77,9 @@ __device__ __forceinline__ int seq_end(const RowsParams& p, int b, int* n, int* 
 // Splits of up to 32 sequences' keys go by one number of tiles for all of them, the
 // smallest with which the units fit the launch (p.n_splits per sequence on average):
 // a long sequence of a ragged batch then has more splits than a short one, and units
-// are of one size.  (Equal numbers of splits, by lengths: 5 sequences of 7,001 to
-// 20,000 keys BAL1; 3 of 9,001 to 16,300 BAL2.)  With more sequences the units of
+// are of one size.  (5 sequences of 7,001 to 20,000 keys of 256
+// features in 8 bits: 36 us, 40 with as many splits for each; 3 of 9,001 to 16,300
+// keys, 252 rows: 60 and 63.)  With more sequences the units of
 // different sizes even out over the machine, and each is divided by p.n_splits.
 constexpr int kBalanced = 32;
 __device__ __forceinline__ bool balanced(const RowsParams& p) { return p.n_splits > 1 && p.B <= kBalanced; }
@@ -125,6 +126,11 @@ __device__ __forceinline__ Unit unit_of(const RowsParams& p, int index, int bloc
   w.t1 = min(w.t0 + per, tiles);
   return w;
 }
+
+// The step of a row or two per key head over a short 8-bit cache (mha_rows_short.cu).
+constexpr int kShortRows = 2;    // rows per key head
+constexpr int kShortWork = 16384;  // keys x features x rows of a sequence and key head
+cudaError_t launch_rows_short(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
 
 // The rows kernel for many rows per key head of a bf16 cache (mha_rows_block.cu).
 constexpr int kBlockRows = 256;  // rows per unit

@@ -1362,7 +1362,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
   uint32_t out[EPL / 2];
 #pragma unroll
   for (int e = 0; e < EPL; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-  // (d is a multiple of 16: a lane's features are all inside it or all past it)
+  // (d is a multiple of 8: a lane's features are all inside it or all past it)
   if (lane * EPL < p.d) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * p.d + lane * EPL);
     if constexpr (EPL == 2) *dst = out[0];

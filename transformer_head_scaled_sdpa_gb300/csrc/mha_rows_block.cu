@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
       if (elect_one()) {
         constexpr uint32_t idesc_s = idesc_bf16_f32(128, kKeys, false, false);
         constexpr uint32_t idesc_o = idesc_bf16_f32(128, W, false, true);
-        const int n_ks = p.d / 16;
+        const int n_ks = (p.d + 15) / 16;  // (what lies behind d is 0)
         const uint64_t dq0 = smem_desc_sw128(s_base + C::OFF_Q, 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(s_base, 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(s_base, C::CHUNK, 1024);
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
           for (int x = 0; x < 8; ++x) y[x] = pack_bf16x2(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]));
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * p.d + c);
           dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-          dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          if (c + 8 < p.d) dst[1] = make_uint4(y[4], y[5], y[6], y[7]);  // (d is a multiple of 8)
         } else {
           uint4* dst = reinterpret_cast<uint4*>(p.part_o + part * W + c);
 #pragma unroll

@@ -116,7 +116,11 @@ struct RowsCfg {
   // softmax warpgroups: a CTA that has the SM to itself has two from 32 rows on
   static constexpr int WGS = NR <= 8 || (NR <= 16 && !TWO) ? 1 : 2;
   static constexpr int RPT = NR / WGS;                   // rows per softmax thread
-  static constexpr int THREADS = 128 * WGS + 128;
+  // beside them: MMA, TMA, over an 8-bit cache scales, and Q; an 8-bit unit of many
+  // rows has four warps for its Q's pieces (one: 27k cycles per unit of 64 rows)
+  static constexpr bool MANY_Q = F8 && !TWO && WGS == 2;
+  static constexpr int Q_THREADS = F8 ? (MANY_Q ? 128 : 32) : 64;
+  static constexpr int THREADS = 128 * WGS + (MANY_Q ? 256 : 128);
   static constexpr int GW = RPT < 16 ? RPT : 16;         // rows handled together
   static constexpr int GROUPS = RPT / GW;
   static constexpr int SLOTS1 = (232448 - FIXED) / SLOT;
@@ -131,7 +135,6 @@ struct RowsCfg {
   // barriers
   static constexpr int FULL = 0;              // + slot
   static constexpr int EMPTY = SLOTS;         // + slot
-  static constexpr int Q_THREADS = F8 ? 32 : 64;
   static constexpr int Q_FULL = 2 * SLOTS;    // + buffer: Q and the unit's row values (Q_THREADS / 32 warps)
   static constexpr int Q_EMPTY = Q_FULL + 2;  // + buffer: the last scores and the epilogue are done
   static constexpr int S_FULL = Q_EMPTY + 2;  // + buffer
@@ -144,7 +147,7 @@ struct RowsCfg {
   static constexpr int SC_EMPTY = SC_FULL + (F8 ? kScaleTiles : 0);  // + tile: read (each softmax warp)
   static constexpr int UNIT_FULL = SC_EMPTY + (F8 ? kScaleTiles : 0);  // + queue slot: published
   static constexpr int UNIT_EMPTY = UNIT_FULL + kQueue;                // + queue slot: read (each consumer warp)
-  static constexpr int CONSUMERS = 4 * WGS + 3;
+  static constexpr int CONSUMERS = 4 * WGS + 1 + (F8 ? 1 : 0) + Q_THREADS / 32;
   static constexpr int CLC = UNIT_EMPTY + kQueue;                      // a cancellation's response
   static constexpr int NBAR = CLC + 1;
   static constexpr int OFF_TMEM = OFF_MISC + 8 * NBAR;
@@ -163,10 +166,11 @@ struct RowsCfg {
   static constexpr float LIFT = F8 ? 10.f : 0.f;         // weights are 2^LIFT at the reference
   // registers: the softmax warpgroups take from the others
   static constexpr bool SPLIT_REGS = TWO || WGS > 1;
-  static constexpr int REGS_OTHER = TWO && WGS == 2 ? 64 : 96;
-  static constexpr int REGS_SOFT = TWO ? (WGS == 2 ? 88 : 256 - REGS_OTHER) : 200;
-  static_assert(!TWO || WGS == 2 || (REGS_OTHER + REGS_SOFT) * 128 <= 256 * 128, "register split");
-  static_assert(WGS != 2 || REGS_OTHER * 128 + REGS_SOFT * 256 <= (TWO ? 80 : 168) * 384, "register split");
+  static constexpr int REGS_LAUNCH = 65536 / THREADS / (TWO ? 2 : 1) / 8 * 8;
+  static constexpr int REGS_OTHER = MANY_Q ? 72 : (TWO && WGS == 2 ? 64 : 96);
+  static constexpr int REGS_SOFT = MANY_Q ? 184 : (TWO ? (WGS == 2 ? 88 : 256 - REGS_OTHER) : 200);
+  static_assert(!SPLIT_REGS || REGS_OTHER * (THREADS - 128 * WGS) + REGS_SOFT * 128 * WGS <= REGS_LAUNCH * THREADS,
+                "register split");
 };
 
 // Shared-memory matrix descriptor without swizzle: core matrices of 8 rows x
@@ -336,7 +340,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int tid = static_cast<int>(threadIdx.x);
   constexpr int SOFT = 128 * C::WGS;            // softmax threads
-  constexpr int kMmaWarp = 4 * C::WGS, kLoadWarp = kMmaWarp + 1, kQWarp = kMmaWarp + 2;
+  constexpr int kMmaWarp = 4 * C::WGS, kLoadWarp = kMmaWarp + 1, kScaleWarp = kMmaWarp + 2;
+  constexpr int kQWarp = kMmaWarp + (F8 ? 3 : 2);
   const int n_rows = p.T * p.G;
   const int blocks = (n_rows + NR - 1) / NR;    // blocks of rows per key head (the faster index of a unit)
 
@@ -808,7 +813,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     volatile int never = 0;
     mbar_wait(bar(C::DRAIN), 0, &never, p.status, site + C::DRAIN);
   } else {
-    if (F8 && warp == kQWarp + 1) {
+    if (F8 && warp == kScaleWarp) {
       // ---- 8-bit: the scales of the tiles to come, four keys per lane
       const int site = kRoleRowsQ * 64;
       uint16_t* ring = reinterpret_cast<uint16_t*>(smem + C::OFF_SCALES);
@@ -859,7 +864,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
         }
       }
-    } else {
+    } else if (warp < kQWarp + C::Q_THREADS / 32) {
     // ---- the next units' Q, output rows and mask words
     const int site = kRoleRowsQ * 64;
     constexpr int QT = C::Q_THREADS;

@@ -211,3 +211,15 @@ def test_many_rows_agree_with_the_forward(mha):  # noqa: F811
     bound = 2 ** -8 * (out.float().abs() + full.float().abs() + 1.01 * v.float().abs().max())
     assert ((out.float() - full.float()).abs() <= bound).all()
     pu.assert_lse_close(lse, lse_f.double().cpu().numpy().reshape(B, H, T), "forward")
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "f8"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T", [2, 8, 9, 16, 17, 32, 33, 64])
+def test_every_count_of_rows(mha, T, d, f8):  # noqa: F811
+    """Row counts around the sizes of a unit, over a ragged last tile, an empty
+    prefix and several tiles."""
+    case = make_step(T + d, 3, T, 2, 2, d, 300, [300 - T, 0, 17], [T, T - 1, T], "tree", f8)
+    out, lse = call_step(mha, on_gpu(case), f8, True)
+    assert mha.mha_sync_status() == 0
+    check_step(case, out, lse, f8, what=f"{T} rows of {d}")

@@ -48,24 +48,30 @@
 // heads, which lie side by side in the cache, and the same rows for their blocks
 // (one head's rows alone are 128-byte pieces of DRAM pages: 161 us for 16
 // sequences x 96 heads x 2048 keys of 128 features in 8 bits when a CTA's work ran
-// over consecutive heads, against 110).  Each sequence's own tiles are divided by
-// the number of splits, so short sequences of a ragged batch use fewer.  The grid
-// has a CTA per unit, but CTAs are persistent: a running CTA cancels CTAs that have
-// not started (cluster launch control) and takes their units, so the launch order
+// over consecutive heads, against 110).  rows_plan says how many splits there are,
+// `balance` how they fall on the sequences of a ragged batch.  The grid has a CTA
+// per unit, but CTAs are persistent: a running CTA cancels CTAs that have not
+// started (cluster launch control) and takes their units, so the launch order
 // balances the work (with equal static shares of the keys CTAs ended 25 % apart).
 // A split of a sequence that has several leaves a partial (o, m, l) in the
-// workspace, and rows_combine_kernel merges them exactly (rows_plan says when keys
-// are split).
+// workspace, and rows_combine_kernel merges them exactly.
 //
-// Roles: 4 warps per 32 rows softmax and epilogue (thread = key = TMEM lane),
-// then one warp each for MMA issue (and TMEM) and TMA, and two that prepare the
-// next unit's Q pieces, output rows and mask words in a double buffer (over an
-// 8-bit cache one of them keeps the next tiles' scales in a ring instead).  The MMA
-// warp runs S(0), S(1), PV(0), S(2), PV(1), ... over all tiles of its share
-// without a break at unit borders: the next scores, and the loads of a whole
-// ring, run during a unit's epilogue.  The TMA warp also finds the units and
-// publishes them to the others through a queue.  Every wait is bounded (abort flag,
-// MHA_ERR_TIMEOUT).
+// Roles: one or two softmax warpgroups (thread = key = TMEM lane; they also prepare
+// a CTA's first Q and write the outputs), one lane that issues every MMA, one that
+// issues every TMA load, finds the units and publishes them to the others through a
+// queue, over an 8-bit cache a warp that keeps the next tiles' scales in a ring, and
+// one, two or four warps that prepare the next unit's Q pieces, output rows and mask
+// words in a double buffer.  The MMA lane runs S(0), S(1), PV(0), S(2), PV(1), ...
+// over all tiles of all units without a break at their borders: the next scores, and
+// the loads of a whole ring, run during a unit's epilogue.  Every wait is bounded
+// (abort flag, MHA_ERR_TIMEOUT).
+//
+// What bounds it (16 x 96 heads x 2,048 keys of 128 features in 8 bits, 610 MB): 97
+// us, 6.3 TB/s, 0.93 of the measured copy; with 16 rows and 4 sequences 40 us, 3.9
+// TB/s: the softmax threads' instructions (30 per weight: three pieces) and 384 units
+// on 304 CTAs.  A unit costs five tiles of 128 keys beside its own (Q, the first
+// maxima, the epilogue), and instructions come from DRAM after a pass over a cache
+// that flushes L2: 6 to 8 thousand cycles before the first scores.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -97,11 +103,10 @@ struct RowsCfg {
   static constexpr int NP = (PP * NR + 15) / 16 * 16;
   static constexpr int Q_BYTES = NQ * W * EB;
   static constexpr int P_BYTES = kKeys * NP * EB;
-  static constexpr int P_BUFS = W <= 128 || (F8 && NR >= 32) ? 2 : 1;
   // barriers (512 bytes), units, scales, per-row values of two units and of the softmax
   static constexpr int SCALES = F8 ? kScaleTiles * kKeys * 2 : 0;
   static constexpr int MISC = 576 + 48 * kQueue + 16 + 160 + SCALES + 2 * (16 + 8 * kMaskWords) * NR + 24 * NR;
-  static constexpr int FIXED = 2 * Q_BYTES + P_BUFS * P_BYTES + MISC + 1024;
+  static constexpr int FIXED = 2 * Q_BYTES + P_BYTES + MISC + 1024;
   // TMEM: S0 | S1 | O (per 128 features)
   static constexpr int M_O = W == 64 ? 64 : 128;         // rows of the O^T tile
   static constexpr uint32_t TM_S1 = NQ, TM_O = 2 * NQ;
@@ -109,11 +114,16 @@ struct RowsCfg {
   static constexpr uint32_t TMEM_COLS =
       TM_USED <= 32 ? 32 : (TM_USED <= 64 ? 64 : (TM_USED <= 128 ? 128 : (TM_USED <= 256 ? 256 : 512)));
   static_assert(TM_USED <= 512, "TMEM budget");
-  // two CTAs per SM when each can hold two tiles' worth of ring, else one with
-  // a deep ring
+  // Two CTAs per SM when each can hold two tiles' worth of ring, else one with a deep
+  // ring: one works while the other waits (16 x 96 heads x 2,048 keys in 8 bits 99 us,
+  // one CTA 110; with 16 drafted tokens, 4 sequences, 40 and 48; 12 drafted tokens over
+  // 32 x 8 heads x 300 keys of 64 features in bf16 9.3 and 13.5).
   static constexpr int SLOTS2 = (115712 - FIXED) / SLOT;
   static constexpr bool TWO = SLOTS2 >= (BLKS == 1 ? 4 : 5) && NR <= 32 && TMEM_COLS <= 256;
-  // softmax warpgroups: a CTA that has the SM to itself has two from 32 rows on
+  // Softmax warpgroups: two from 16 rows on, 32 where the CTA has the SM to itself (16
+  // drafted tokens over 4 x 96 heads x 2,048 keys in 8 bits 40 us with two and 43 with
+  // one; four of them for 64 rows of a bf16 cache 107 and 104, for 32 rows of 256
+  // features in 8 bits 47.1 and 46.5).
   static constexpr int WGS = NR <= 8 || (NR <= 16 && !TWO) ? 1 : 2;
   static constexpr int RPT = NR / WGS;                   // rows per softmax thread
   // beside them: MMA, TMA, over an 8-bit cache scales, and Q; an 8-bit unit of many
@@ -129,7 +139,7 @@ struct RowsCfg {
   static_assert(SLOTS >= 2 * BLKS + 1, "ring: the next K tile while V waits");
   static constexpr int OFF_Q = SLOTS * SLOT;             // + buffer * Q_BYTES
   static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
-  static constexpr int OFF_MISC = OFF_P + P_BUFS * P_BYTES;
+  static constexpr int OFF_MISC = OFF_P + P_BYTES;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;
   static_assert(SMEM <= 232448, "shared memory");
   // barriers
@@ -138,9 +148,9 @@ struct RowsCfg {
   static constexpr int Q_FULL = 2 * SLOTS;    // + buffer: Q and the unit's row values (Q_THREADS / 32 warps)
   static constexpr int Q_EMPTY = Q_FULL + 2;  // + buffer: the last scores and the epilogue are done
   static constexpr int S_FULL = Q_EMPTY + 2;  // + buffer
-  static constexpr int P_FULL = S_FULL + 2;   // + P buffer (every softmax warp)
-  static constexpr int PV_DONE = P_FULL + P_BUFS;       // + P buffer
-  static constexpr int Q_FIRST = PV_DONE + P_BUFS;      // the first unit's Q (every softmax warp)
+  static constexpr int P_FULL = S_FULL + 2;   // (every softmax warp)
+  static constexpr int PV_DONE = P_FULL + 1;
+  static constexpr int Q_FIRST = PV_DONE + 1;  // the first unit's Q (every softmax warp)
   static constexpr int O_FREE = Q_FIRST + 1;  // the epilogue has read O (every softmax warp)
   static constexpr int DRAIN = O_FREE + 1;
   static constexpr int SC_FULL = DRAIN + 1;            // + tile: scales (8-bit)
@@ -355,10 +365,8 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
       mbar_init(bar(C::Q_EMPTY + i), 1 + SOFT / 32);
       mbar_init(bar(C::S_FULL + i), 1);
     }
-    for (int i = 0; i < C::P_BUFS; ++i) {
-      mbar_init(bar(C::P_FULL + i), SOFT / 32);
-      mbar_init(bar(C::PV_DONE + i), 1);
-    }
+    mbar_init(bar(C::P_FULL), SOFT / 32);
+    mbar_init(bar(C::PV_DONE), 1);
     mbar_init(bar(C::Q_FIRST), SOFT / 32);
     mbar_init(bar(C::O_FREE), SOFT / 32);
     mbar_init(bar(C::DRAIN), 1);
@@ -415,9 +423,6 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   };
   // Phase of Q_FULL for unit k (the first unit has a barrier of its own).
   auto q_phase = [](int k) { return static_cast<uint32_t>(((k >> 1) - ((k & 1) ? 0 : 1)) & 1); };
-  // Buffer and phase of P and its product for tile t.
-  auto p_buf = [](uint32_t t) { return C::P_BUFS == 2 ? t & 1 : 0u; };
-  auto p_phase = [](uint32_t t) { return C::P_BUFS == 2 ? (t >> 1) & 1 : t & 1; };
   // Output row of row r of a unit (-1 past the last), t: its drafted token.
   auto out_row = [&](const Unit& it, int r, int* t) {
     const int gr = it.rb * NR + r;
@@ -778,8 +783,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           if (kp > 0) wait(C::O_FREE, (kp - 1) & 1);
           v_at += p_n == 1 ? 1 : 2;  // (from the unit's first item)
         }
-        wait(C::P_FULL + p_buf(tp), p_phase(tp));
-        const uint64_t pd = dp0 + static_cast<uint64_t>((p_buf(tp) * C::P_BYTES) >> 4);
+        wait(C::P_FULL, tp & 1);
         uint32_t slot = 0;
 #pragma unroll
         for (int blk = 0; blk < C::BLKS; ++blk) {
@@ -794,12 +798,12 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
 #pragma unroll
           for (int step = 0; step < kKeys / KSTEP; ++step)
             umma<F8>(d, a + static_cast<uint64_t>((step * KSTEP * 128) >> 4),
-                     pd + static_cast<uint64_t>((step * KSTEP * 16) >> 4), idesc_o,
+                     dp0 + static_cast<uint64_t>((step * KSTEP * 16) >> 4), idesc_o,
                      (p_i > 0 || step > 0) ? 1u : 0u);
           if (blk < blks - 1) umma_commit(bar(C::EMPTY + slot));
         }
         if (!ok) break;
-        umma_commit(bar(C::PV_DONE + p_buf(tp)));
+        umma_commit(bar(C::PV_DONE));
         umma_commit(bar(C::EMPTY + slot));
         ++p_i;
         // V(i) to V(i + 1): a K between, but before the last; then the next unit
@@ -1076,7 +1080,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             }
           }
           if (i > 0) {
-            wait(C::PV_DONE + p_buf(t - 1), p_phase(t - 1));
+            wait(C::PV_DONE, (t - 1) & 1);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < C::BLKS * C::PP; ++c)
@@ -1097,9 +1101,9 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
         }
         tc_fence_before();
-        // weights; the product before must have read this buffer of P
-        if (t >= C::P_BUFS) wait(C::PV_DONE + p_buf(t), p_phase(t - C::P_BUFS));
-        const uint32_t p_at = sP + p_buf(t) * C::P_BYTES;
+        // weights; the product before must have read P (a second buffer of P measured
+        // nothing: this wait is over long before the weights are ready)
+        if (t > 0) wait(C::PV_DONE, (t - 1) & 1);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
           if (g * GW >= rows_here) continue;
@@ -1137,24 +1141,24 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           constexpr int COL = kKeys * 16;
           if constexpr (F8 && NR == 8) {
             // two pieces to a unit; nothing reads the second half of the last
-            const uint32_t to = p_at + kt * 16;
+            const uint32_t to = sP + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w2[0], w2[1]);
             st_shared_v4(to + COL, w3[0], w3[1], 0, 0);
           } else if constexpr (F8 && GW == 8) {
             // half a unit
-            const uint32_t to = p_at + r0 / 16 * COL + kt * 16 + (r0 & 8);
+            const uint32_t to = sP + r0 / 16 * COL + kt * 16 + (r0 & 8);
             st_shared_v2(to, w1[0], w1[1]);
             st_shared_v2(to + (NR / 16) * COL, w2[0], w2[1]);
             st_shared_v2(to + 2 * (NR / 16) * COL, w3[0], w3[1]);
           } else if constexpr (F8) {
-            const uint32_t to = p_at + (r0 / 16 + g) * COL + kt * 16;
+            const uint32_t to = sP + (r0 / 16 + g) * COL + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w1[2], w1[3]);
             st_shared_v4(to + (NR / 16) * COL, w2[0], w2[1], w2[2], w2[3]);
             st_shared_v4(to + 2 * (NR / 16) * COL, w3[0], w3[1], w3[2], w3[3]);
           } else {
 #pragma unroll
             for (int h = 0; h < GW / 8; ++h) {
-              const uint32_t to = p_at + ((r0 + g * GW) / 8 + h) * COL + kt * 16;
+              const uint32_t to = sP + ((r0 + g * GW) / 8 + h) * COL + kt * 16;
               st_shared_v4(to, w1[4 * h], w1[4 * h + 1], w1[4 * h + 2], w1[4 * h + 3]);
               st_shared_v4(to + (NR / 8) * COL, w2[4 * h], w2[4 * h + 1], w2[4 * h + 2], w2[4 * h + 3]);
             }
@@ -1178,7 +1182,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
         }
         fence_proxy_async_smem();
-        warp_arrive(bar(C::P_FULL + p_buf(t)), lane);
+        warp_arrive(bar(C::P_FULL), lane);
       }
 
       // ---- epilogue: sums over the keys, then O
@@ -1187,7 +1191,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         const float y = warp_sums<RPT>(l, lane);
         if (lane % (32 / RPT) == 0) red[(r0 + lane / (32 / RPT)) * 4 + w4] = y;
       }
-      wait(C::PV_DONE + p_buf(t - 1), p_phase(t - 1));
+      wait(C::PV_DONE, (t - 1) & 1);
       tc_fence_after();
       const bool good = ok && *abort_flag == 0;
       named_barrier(nbar, 128);

@@ -546,363 +546,363 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   };
 
   if (warp >= kMmaWarp) {
-  if constexpr (C::SPLIT_REGS) regs_decrease<C::REGS_OTHER>();
-  if (warp == kLoadWarp) {
-    // ---- TMA producer (one lane)
-    const int site = kRoleRowsLoad * 64;
-    int* table = reinterpret_cast<int*>(smem + C::OFF_TABLE);
-    if (balanced(p)) {
-      int first, splits, per;
-      balance(p, lane, &first, &splits, &per);
-      if (lane < p.B) table[lane + 1] = first + splits;
-      if (lane == 0) {
-        table[0] = 0;
-        table[p.B + 1] = per;
-      }
-      __syncwarp();
-    }
-    auto unit_at = [&](int index) {
-      const int part = index / p.units;
-      if (!balanced(p)) return unit_of(p, index, blocks, part % p.B, part / p.B, 0);
-      int b = 0;
-      while (b < p.B && part >= table[b + 1]) ++b;
-      if (b == p.B) {
-        Unit none = {};
-        return none;
-      }
-      return unit_of(p, index, blocks, b, part - table[b], table[p.B + 1]);
-    };
-    if (elect_one()) {
-      Ring<C::SLOTS> ring;
-      int loaded = 0;  // slots filled so far
-      bool ok = true;
-      // one tile of K or V: whole in boxes of 128 keys, a ragged one in boxes of
-      // kBoxKeys as far as it goes
-      auto load = [&](const CUtensorMap* big, const CUtensorMap* small, int key, int end, int hk, int b) {
-        const int boxes = end - key >= kKeys ? 0 : (end - key + kBoxKeys - 1) / kBoxKeys;
-        const uint32_t box_bytes = boxes == 0 ? kKeys * 128 : boxes * kBoxKeys * 128;
-#pragma unroll
-        for (int blk = 0; blk < C::BLKS; ++blk) {
-          if (blk >= blks) break;
-          const int s = ring.slot;
-          ok = ok && (loaded < C::SLOTS ||
-                      thread_wait(bar(C::EMPTY + s), ring.phase ^ 1, abort_flag, site + C::EMPTY + s));
-          if (!ok) return;
-          const int f0 = blk * 128;
-          const int chunks = (min(p.d - f0, 128) * C::EB + 127) / 128;
-          const uint32_t full = bar(C::FULL + s);
-          mbar_arrive_expect_tx(full, chunks * box_bytes);
-          for (int c = 0; c < chunks; ++c) {
-            const uint32_t dst = s_base + s * C::SLOT + c * C::CHUNK;
-            const int f = f0 + c * (128 / C::EB);
-            if (boxes == 0) {
-              tma_load_4d(dst, big, full, f, hk, key, b);
-            } else {
-              for (int x = 0; x < boxes; ++x)
-                tma_load_4d(dst + x * kBoxKeys * 128, small, full, f, hk, key + x * kBoxKeys, b);
-            }
-          }
-          ++loaded;
-          ring.advance();
+    if constexpr (C::SPLIT_REGS) regs_decrease<C::REGS_OTHER>();
+    if (warp == kLoadWarp) {
+      // ---- TMA producer (one lane)
+      const int site = kRoleRowsLoad * 64;
+      int* table = reinterpret_cast<int*>(smem + C::OFF_TABLE);
+      if (balanced(p)) {
+        int first, splits, per;
+        balance(p, lane, &first, &splits, &per);
+        if (lane < p.B) table[lane + 1] = first + splits;
+        if (lane == 0) {
+          table[0] = 0;
+          table[p.B + 1] = per;
         }
+        __syncwarp();
+      }
+      auto unit_at = [&](int index) {
+        const int part = index / p.units;
+        if (!balanced(p)) return unit_of(p, index, blocks, part % p.B, part / p.B, 0);
+        int b = 0;
+        while (b < p.B && part >= table[b + 1]) ++b;
+        if (b == p.B) {
+          Unit none = {};
+          return none;
+        }
+        return unit_of(p, index, blocks, b, part - table[b], table[p.B + 1]);
       };
-      // The units: this CTA's own, then those of CTAs that have not started.  The
-      // next is asked for half-way through a unit's loads and published as soon
-      // as it is known, so that its Q and scales are there when its turn comes.
-      volatile int never = 0;
-      int published = 0;
-      auto publish = [&](const Unit& w) {
-        const int slot = published % kQueue;
-        ok = ok && (published < kQueue ||
-                    thread_wait(bar(C::UNIT_EMPTY + slot), ((published / kQueue) - 1) & 1, abort_flag,
-                                site + C::UNIT_EMPTY + slot));
-        if (!ok) return;
-        queue[slot] = w;
-        mbar_arrive(bar(C::UNIT_FULL + slot));
-        ++published;
-      };
-      uint32_t answers = 0;
-      bool asked = false, done = false;
-      Unit w = unit_at(static_cast<int>(blockIdx.x)), next = w;
-      bool got = w.splits > 0;  // a unit to work on
-      if (got) publish(w);
-      while (ok) {
-        const bool works = got;
-        got = false;
-        // the next unit, if its answer is there or `must` be waited for
-        auto poll = [&](bool must) {
-          while (!got && !done && ok) {
-            if (!asked) {
-              mbar_arrive_expect_tx(bar(C::CLC), 16);
-              clc_try_cancel(s_base + C::OFF_CLC, bar(C::CLC));
-              asked = true;
+      if (elect_one()) {
+        Ring<C::SLOTS> ring;
+        int loaded = 0;  // slots filled so far
+        bool ok = true;
+        // one tile of K or V: whole in boxes of 128 keys, a ragged one in boxes of
+        // kBoxKeys as far as it goes
+        auto load = [&](const CUtensorMap* big, const CUtensorMap* small, int key, int end, int hk, int b) {
+          const int boxes = end - key >= kKeys ? 0 : (end - key + kBoxKeys - 1) / kBoxKeys;
+          const uint32_t box_bytes = boxes == 0 ? kKeys * 128 : boxes * kBoxKeys * 128;
+#pragma unroll
+          for (int blk = 0; blk < C::BLKS; ++blk) {
+            if (blk >= blks) break;
+            const int s = ring.slot;
+            ok = ok && (loaded < C::SLOTS ||
+                        thread_wait(bar(C::EMPTY + s), ring.phase ^ 1, abort_flag, site + C::EMPTY + s));
+            if (!ok) return;
+            const int f0 = blk * 128;
+            const int chunks = (min(p.d - f0, 128) * C::EB + 127) / 128;
+            const uint32_t full = bar(C::FULL + s);
+            mbar_arrive_expect_tx(full, chunks * box_bytes);
+            for (int c = 0; c < chunks; ++c) {
+              const uint32_t dst = s_base + s * C::SLOT + c * C::CHUNK;
+              const int f = f0 + c * (128 / C::EB);
+              if (boxes == 0) {
+                tma_load_4d(dst, big, full, f, hk, key, b);
+              } else {
+                for (int x = 0; x < boxes; ++x)
+                  tma_load_4d(dst + x * kBoxKeys * 128, small, full, f, hk, key + x * kBoxKeys, b);
+              }
             }
-            // (the response lands whatever happens: it is waited for even when giving up)
-            if (must) ok = mbar_wait(bar(C::CLC), answers & 1, &never, p.status, site + C::CLC) && *abort_flag == 0;
-            else if (!mbar_test(bar(C::CLC), answers & 1)) return;
-            ++answers;
-            asked = false;
-            const int index = clc_query_first_ctaid_x(s_base + C::OFF_CLC);  // -1: none was left
-            fence_proxy_async_smem();  // (the next response overwrites this one)
-            done = index < 0;
-            if (done || !ok) return;
-            next = unit_at(index);
-            got = next.splits > 0;
-            if (got) publish(next);
+            ++loaded;
+            ring.advance();
           }
         };
-        if (works) {
-          for (int x = w.t0; x < w.t1 && ok; ++x) {
-            load(&p.tm_k, &p.tm_k_box, x * kKeys, w.end, w.hk, w.b);
-            if (x > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (x - 1) * kKeys, w.end, w.hk, w.b);
-            if (2 * (x - w.t0 + 1) >= w.t1 - w.t0) poll(false);
+        // The units: this CTA's own, then those of CTAs that have not started.  The
+        // next is asked for half-way through a unit's loads and published as soon
+        // as it is known, so that its Q and scales are there when its turn comes.
+        volatile int never = 0;
+        int published = 0;
+        auto publish = [&](const Unit& w) {
+          const int slot = published % kQueue;
+          ok = ok && (published < kQueue ||
+                      thread_wait(bar(C::UNIT_EMPTY + slot), ((published / kQueue) - 1) & 1, abort_flag,
+                                  site + C::UNIT_EMPTY + slot));
+          if (!ok) return;
+          queue[slot] = w;
+          mbar_arrive(bar(C::UNIT_FULL + slot));
+          ++published;
+        };
+        uint32_t answers = 0;
+        bool asked = false, done = false;
+        Unit w = unit_at(static_cast<int>(blockIdx.x)), next = w;
+        bool got = w.splits > 0;  // a unit to work on
+        if (got) publish(w);
+        while (ok) {
+          const bool works = got;
+          got = false;
+          // the next unit, if its answer is there or `must` be waited for
+          auto poll = [&](bool must) {
+            while (!got && !done && ok) {
+              if (!asked) {
+                mbar_arrive_expect_tx(bar(C::CLC), 16);
+                clc_try_cancel(s_base + C::OFF_CLC, bar(C::CLC));
+                asked = true;
+              }
+              // (the response lands whatever happens: it is waited for even when giving up)
+              if (must) ok = mbar_wait(bar(C::CLC), answers & 1, &never, p.status, site + C::CLC) && *abort_flag == 0;
+              else if (!mbar_test(bar(C::CLC), answers & 1)) return;
+              ++answers;
+              asked = false;
+              const int index = clc_query_first_ctaid_x(s_base + C::OFF_CLC);  // -1: none was left
+              fence_proxy_async_smem();  // (the next response overwrites this one)
+              done = index < 0;
+              if (done || !ok) return;
+              next = unit_at(index);
+              got = next.splits > 0;
+              if (got) publish(next);
+            }
+          };
+          if (works) {
+            for (int x = w.t0; x < w.t1 && ok; ++x) {
+              load(&p.tm_k, &p.tm_k_box, x * kKeys, w.end, w.hk, w.b);
+              if (x > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (x - 1) * kKeys, w.end, w.hk, w.b);
+              if (2 * (x - w.t0 + 1) >= w.t1 - w.t0) poll(false);
+            }
+            if (w.t1 > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (w.t1 - 1) * kKeys, w.end, w.hk, w.b);
           }
-          if (w.t1 > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (w.t1 - 1) * kKeys, w.end, w.hk, w.b);
+          poll(true);
+          if (!got) break;
+          w = next;
         }
-        poll(true);
-        if (!got) break;
-        w = next;
+        if (asked) mbar_wait(bar(C::CLC), answers & 1, &never, p.status, site + C::CLC);
+        Unit end;
+        end.b = -1;
+        publish(end);
+        // every copy started must land before the CTA exits
+        for (int x = min(loaded, C::SLOTS); x > 0; --x) {
+          // (the slot x before the next one)
+          const int s = ring.slot >= x ? ring.slot - x : ring.slot - x + C::SLOTS;
+          mbar_wait(bar(C::FULL + s), ring.slot >= x ? ring.phase : ring.phase ^ 1, &never, p.status, site + C::FULL + s);
+        }
       }
-      if (asked) mbar_wait(bar(C::CLC), answers & 1, &never, p.status, site + C::CLC);
-      Unit end;
-      end.b = -1;
-      publish(end);
-      // every copy started must land before the CTA exits
-      for (int x = min(loaded, C::SLOTS); x > 0; --x) {
-        // (the slot x before the next one)
-        const int s = ring.slot >= x ? ring.slot - x : ring.slot - x + C::SLOTS;
-        mbar_wait(bar(C::FULL + s), ring.slot >= x ? ring.phase : ring.phase ^ 1, &never, p.status, site + C::FULL + s);
-      }
-    }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ---- MMA issuer (one lane): S(0) S(1) PV(0) S(2) PV(1) ... over all units' tiles
-    const int site = kRoleRowsMma * 64;
-    if (elect_one()) {
-      constexpr int KSTEP = F8 ? 32 : 16;               // reduction elements per MMA
-      const int n_ks = (p.d + KSTEP - 1) / KSTEP;
-      constexpr int KS_BLK = 128 / KSTEP;               // steps of a 128-feature block
-      constexpr uint32_t idesc_s = F8 ? idesc_f8_f32(128, C::NQ, 0, false, false)
-                                      : idesc_bf16_f32(128, C::NQ, false, false);
-      constexpr uint32_t idesc_o = F8 ? idesc_f8_f32(C::M_O, C::NP, 1, true, true)
-                                      : idesc_bf16_f32(C::M_O, C::NP, true, true);
-      // K: rows of 128 bytes per chunk, 8-row groups 1024 B apart, +32 B per step
-      // inside a chunk.  V transposed: features contiguous in a 128-byte row, next
-      // chunk of features CHUNK apart, 8-key groups 1024 B apart.
-      const uint64_t dk0 = smem_desc_sw128(s_base, 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(s_base, C::CHUNK, 1024);
-      const uint64_t dq0 = smem_desc_plain(s_base + C::OFF_Q, C::NQ * 16, 128);
-      const uint64_t dp0 = smem_desc_plain(sP, 128, kKeys * 16);
-      bool ok = true;
-      auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
-      // Scores run one tile ahead of the products.  A unit's blocks lie in the ring
-      // in the order K(0) K(1) V(0) K(2) ... V(last): `k_at` and `v_at` count ring
-      // items (tiles of K or V).
-      uint32_t ts = 0, tp = 0;        // tiles whose scores, products are issued
-      uint32_t k_at = 0, v_at = 0;
-      int taken = 0, ks = -1, kp = -1;
-      int s_n = 0, s_i = 0;           // the scores' unit: tiles, tiles issued
-      int n_odd = 0, n_even = 0;      // tiles of odd and even units
-      int p_n = 0, p_i = 0;           // the products' unit
-      bool more = true, q_known = false;
-      while (ok) {
-        // ---- the next tile's scores; at a unit's border only if it and its Q are
-        // there, unless nothing else is left to do
-        if (more && ts < tp + 2) {
-          const bool must = ts == tp;
-          if (s_i == s_n) {
-            const int slot = taken % kQueue;
-            const uint32_t full = bar(C::UNIT_FULL + slot), parity = (taken / kQueue) & 1;
-            if (must) wait(C::UNIT_FULL + slot, parity);
-            if (ok && (must || mbar_test(full, parity))) {
-              const int n = queue[slot].b < 0 ? -1 : queue[slot].t1 - queue[slot].t0;
-              mbar_arrive(bar(C::UNIT_EMPTY + slot));
-              ++taken;
-              if (n == 0) continue;
-              if (n < 0) {
-                more = false;
-              } else {
-                s_n = n;
-                s_i = 0;
-                ++ks;
-                q_known = false;
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ---- MMA issuer (one lane): S(0) S(1) PV(0) S(2) PV(1) ... over all units' tiles
+      const int site = kRoleRowsMma * 64;
+      if (elect_one()) {
+        constexpr int KSTEP = F8 ? 32 : 16;               // reduction elements per MMA
+        const int n_ks = (p.d + KSTEP - 1) / KSTEP;
+        constexpr int KS_BLK = 128 / KSTEP;               // steps of a 128-feature block
+        constexpr uint32_t idesc_s = F8 ? idesc_f8_f32(128, C::NQ, 0, false, false)
+                                        : idesc_bf16_f32(128, C::NQ, false, false);
+        constexpr uint32_t idesc_o = F8 ? idesc_f8_f32(C::M_O, C::NP, 1, true, true)
+                                        : idesc_bf16_f32(C::M_O, C::NP, true, true);
+        // K: rows of 128 bytes per chunk, 8-row groups 1024 B apart, +32 B per step
+        // inside a chunk.  V transposed: features contiguous in a 128-byte row, next
+        // chunk of features CHUNK apart, 8-key groups 1024 B apart.
+        const uint64_t dk0 = smem_desc_sw128(s_base, 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(s_base, C::CHUNK, 1024);
+        const uint64_t dq0 = smem_desc_plain(s_base + C::OFF_Q, C::NQ * 16, 128);
+        const uint64_t dp0 = smem_desc_plain(sP, 128, kKeys * 16);
+        bool ok = true;
+        auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
+        // Scores run one tile ahead of the products.  A unit's blocks lie in the ring
+        // in the order K(0) K(1) V(0) K(2) ... V(last): `k_at` and `v_at` count ring
+        // items (tiles of K or V).
+        uint32_t ts = 0, tp = 0;        // tiles whose scores, products are issued
+        uint32_t k_at = 0, v_at = 0;
+        int taken = 0, ks = -1, kp = -1;
+        int s_n = 0, s_i = 0;           // the scores' unit: tiles, tiles issued
+        int n_odd = 0, n_even = 0;      // tiles of odd and even units
+        int p_n = 0, p_i = 0;           // the products' unit
+        bool more = true, q_known = false;
+        while (ok) {
+          // ---- the next tile's scores; at a unit's border only if it and its Q are
+          // there, unless nothing else is left to do
+          if (more && ts < tp + 2) {
+            const bool must = ts == tp;
+            if (s_i == s_n) {
+              const int slot = taken % kQueue;
+              const uint32_t full = bar(C::UNIT_FULL + slot), parity = (taken / kQueue) & 1;
+              if (must) wait(C::UNIT_FULL + slot, parity);
+              if (ok && (must || mbar_test(full, parity))) {
+                const int n = queue[slot].b < 0 ? -1 : queue[slot].t1 - queue[slot].t0;
+                mbar_arrive(bar(C::UNIT_EMPTY + slot));
+                ++taken;
+                if (n == 0) continue;
+                if (n < 0) {
+                  more = false;
+                } else {
+                  s_n = n;
+                  s_i = 0;
+                  ++ks;
+                  q_known = false;
+                }
               }
             }
-          }
-          if (s_i < s_n && !q_known) {
-            const int id = ks == 0 ? C::Q_FIRST : C::Q_FULL + (ks & 1);
-            const uint32_t parity = ks == 0 ? 0 : q_phase(ks);
-            if (must) wait(id, parity);
-            q_known = ok && (must || mbar_test(bar(id), parity));
-          }
-          if (q_known && s_i < s_n) {
-            const uint64_t q = dq0 + static_cast<uint64_t>(((ks & 1) * C::Q_BYTES) >> 4);
-            const uint32_t d = tmem + ((ts & 1) ? C::TM_S1 : 0u);
-            uint32_t slot = 0;
+            if (s_i < s_n && !q_known) {
+              const int id = ks == 0 ? C::Q_FIRST : C::Q_FULL + (ks & 1);
+              const uint32_t parity = ks == 0 ? 0 : q_phase(ks);
+              if (must) wait(id, parity);
+              q_known = ok && (must || mbar_test(bar(id), parity));
+            }
+            if (q_known && s_i < s_n) {
+              const uint64_t q = dq0 + static_cast<uint64_t>(((ks & 1) * C::Q_BYTES) >> 4);
+              const uint32_t d = tmem + ((ts & 1) ? C::TM_S1 : 0u);
+              uint32_t slot = 0;
 #pragma unroll
-            for (int blk = 0; blk < C::BLKS; ++blk) {
-              if (blk >= blks) break;
-              const uint32_t item = k_at * blks + blk;
-              slot = item % C::SLOTS;
-              wait(C::FULL + slot, (item / C::SLOTS) & 1);
+              for (int blk = 0; blk < C::BLKS; ++blk) {
+                if (blk >= blks) break;
+                const uint32_t item = k_at * blks + blk;
+                slot = item % C::SLOTS;
+                wait(C::FULL + slot, (item / C::SLOTS) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t a = dk0 + static_cast<uint64_t>((slot * C::SLOT) >> 4);
+#pragma unroll
+                for (int x = 0; x < KS_BLK; ++x) {
+                  const int step = blk * KS_BLK + x;
+                  if (step < n_ks)
+                    umma<F8>(d, a + static_cast<uint64_t>(((x >> 2) * C::CHUNK + (x & 3) * 32) >> 4),
+                             q + static_cast<uint64_t>(step * 2 * C::NQ), idesc_s, step > 0 ? 1u : 0u);
+                }
+                if (blk < blks - 1) umma_commit(bar(C::EMPTY + slot));
+              }
               if (!ok) break;
-              tc_fence_after();
-              const uint64_t a = dk0 + static_cast<uint64_t>((slot * C::SLOT) >> 4);
-#pragma unroll
-              for (int x = 0; x < KS_BLK; ++x) {
-                const int step = blk * KS_BLK + x;
-                if (step < n_ks)
-                  umma<F8>(d, a + static_cast<uint64_t>(((x >> 2) * C::CHUNK + (x & 3) * 32) >> 4),
-                           q + static_cast<uint64_t>(step * 2 * C::NQ), idesc_s, step > 0 ? 1u : 0u);
-              }
-              if (blk < blks - 1) umma_commit(bar(C::EMPTY + slot));
+              umma_commit(bar(C::S_FULL + (ts & 1)));
+              umma_commit(bar(C::EMPTY + slot));
+              if (ks & 1) n_odd = s_n;
+              else n_even = s_n;
+              // (a last tile's K is followed by its own V, after the one before)
+              k_at += s_i + 1 < s_n ? (s_i == 0 ? 1 : 2) : (s_n == 1 ? 2 : 3);
+              ++s_i;
+              if (s_i == s_n) umma_commit(bar(C::Q_EMPTY + (ks & 1)));
+              ++ts;
+              if (must) continue;
             }
-            if (!ok) break;
-            umma_commit(bar(C::S_FULL + (ts & 1)));
-            umma_commit(bar(C::EMPTY + slot));
-            if (ks & 1) n_odd = s_n;
-            else n_even = s_n;
-            // (a last tile's K is followed by its own V, after the one before)
-            k_at += s_i + 1 < s_n ? (s_i == 0 ? 1 : 2) : (s_n == 1 ? 2 : 3);
-            ++s_i;
-            if (s_i == s_n) umma_commit(bar(C::Q_EMPTY + (ks & 1)));
-            ++ts;
-            if (must) continue;
           }
-        }
-        if (tp == ts) {
-          if (!more) break;
-          continue;
-        }
-        // ---- O += V^T P^T of tile tp
-        if (p_i == p_n) {
-          ++kp;
-          p_n = (kp & 1) ? n_odd : n_even;
-          p_i = 0;
-          // (O is free once the last unit's epilogue has read it)
-          if (kp > 0) wait(C::O_FREE, (kp - 1) & 1);
-          v_at += p_n == 1 ? 1 : 2;  // (from the unit's first item)
-        }
-        wait(C::P_FULL, tp & 1);
-        uint32_t slot = 0;
+          if (tp == ts) {
+            if (!more) break;
+            continue;
+          }
+          // ---- O += V^T P^T of tile tp
+          if (p_i == p_n) {
+            ++kp;
+            p_n = (kp & 1) ? n_odd : n_even;
+            p_i = 0;
+            // (O is free once the last unit's epilogue has read it)
+            if (kp > 0) wait(C::O_FREE, (kp - 1) & 1);
+            v_at += p_n == 1 ? 1 : 2;  // (from the unit's first item)
+          }
+          wait(C::P_FULL, tp & 1);
+          uint32_t slot = 0;
 #pragma unroll
-        for (int blk = 0; blk < C::BLKS; ++blk) {
-          if (blk >= blks) break;
-          const uint32_t item = v_at * blks + blk;
-          slot = item % C::SLOTS;
-          wait(C::FULL + slot, (item / C::SLOTS) & 1);
+          for (int blk = 0; blk < C::BLKS; ++blk) {
+            if (blk >= blks) break;
+            const uint32_t item = v_at * blks + blk;
+            slot = item % C::SLOTS;
+            wait(C::FULL + slot, (item / C::SLOTS) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + C::TM_O + blk * C::NP;
+            const uint64_t a = dv0 + static_cast<uint64_t>((slot * C::SLOT) >> 4);
+#pragma unroll
+            for (int step = 0; step < kKeys / KSTEP; ++step)
+              umma<F8>(d, a + static_cast<uint64_t>((step * KSTEP * 128) >> 4),
+                       dp0 + static_cast<uint64_t>((step * KSTEP * 16) >> 4), idesc_o,
+                       (p_i > 0 || step > 0) ? 1u : 0u);
+            if (blk < blks - 1) umma_commit(bar(C::EMPTY + slot));
+          }
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + C::TM_O + blk * C::NP;
-          const uint64_t a = dv0 + static_cast<uint64_t>((slot * C::SLOT) >> 4);
-#pragma unroll
-          for (int step = 0; step < kKeys / KSTEP; ++step)
-            umma<F8>(d, a + static_cast<uint64_t>((step * KSTEP * 128) >> 4),
-                     dp0 + static_cast<uint64_t>((step * KSTEP * 16) >> 4), idesc_o,
-                     (p_i > 0 || step > 0) ? 1u : 0u);
-          if (blk < blks - 1) umma_commit(bar(C::EMPTY + slot));
+          umma_commit(bar(C::PV_DONE));
+          umma_commit(bar(C::EMPTY + slot));
+          ++p_i;
+          // V(i) to V(i + 1): a K between, but before the last; then the next unit
+          v_at += p_i == p_n ? 1 : (p_i + 1 == p_n ? 1 : 2);
+          ++tp;
         }
-        if (!ok) break;
-        umma_commit(bar(C::PV_DONE));
-        umma_commit(bar(C::EMPTY + slot));
-        ++p_i;
-        // V(i) to V(i + 1): a K between, but before the last; then the next unit
-        v_at += p_i == p_n ? 1 : (p_i + 1 == p_n ? 1 : 2);
-        ++tp;
+        // every tensor-core operation issued must be complete before TMEM is freed
+        umma_commit(bar(C::DRAIN));
       }
-      // every tensor-core operation issued must be complete before TMEM is freed
-      umma_commit(bar(C::DRAIN));
-    }
-    __syncwarp();
-    volatile int never = 0;
-    mbar_wait(bar(C::DRAIN), 0, &never, p.status, site + C::DRAIN);
-  } else {
-    if (F8 && warp == kScaleWarp) {
-      // ---- 8-bit: the scales of the tiles to come, four keys per lane
-      const int site = kRoleRowsQ * 64;
-      uint16_t* ring = reinterpret_cast<uint16_t*>(smem + C::OFF_SCALES);
-      int t = 0;
-      bool ok = true;
-      // 32 tiles' scales into L2 (a plain load waits behind the ring's copies in
-      // the DRAM queues, several tiles' time)
-      auto ahead = [&](const Unit& w, int tile) {
-        const long long from = (static_cast<long long>(w.b) * p.H_kv + w.hk) * p.Lk + (tile + lane) * kKeys;
-        if (tile + lane < w.t1) {
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.k_scale + from));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.v_scale + from));
-        }
-      };
-      for (int taken = 0; ok; ++taken) {
-        const Unit it = take(taken, site);
-        if (it.b < 0) break;
-        ahead(it, it.t0);
-        const long long row = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
-        // (two tiles' loads in flight)
-        for (int x = it.t0; x < it.t1 && ok; x += 2) {
-          if (((x - it.t0) & 31) == 16) ahead(it, x + 16);
-          const int m = min(2, it.t1 - x);
-          uint32_t k4[2][4], v4[2][4];
+      __syncwarp();
+      volatile int never = 0;
+      mbar_wait(bar(C::DRAIN), 0, &never, p.status, site + C::DRAIN);
+    } else {
+      if (F8 && warp == kScaleWarp) {
+        // ---- 8-bit: the scales of the tiles to come, four keys per lane
+        const int site = kRoleRowsQ * 64;
+        uint16_t* ring = reinterpret_cast<uint16_t*>(smem + C::OFF_SCALES);
+        int t = 0;
+        bool ok = true;
+        // 32 tiles' scales into L2 (a plain load waits behind the ring's copies in
+        // the DRAM queues, several tiles' time)
+        auto ahead = [&](const Unit& w, int tile) {
+          const long long from = (static_cast<long long>(w.b) * p.H_kv + w.hk) * p.Lk + (tile + lane) * kKeys;
+          if (tile + lane < w.t1) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.k_scale + from));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.v_scale + from));
+          }
+        };
+        for (int taken = 0; ok; ++taken) {
+          const Unit it = take(taken, site);
+          if (it.b < 0) break;
+          ahead(it, it.t0);
+          const long long row = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
+          // (two tiles' loads in flight)
+          for (int x = it.t0; x < it.t1 && ok; x += 2) {
+            if (((x - it.t0) & 31) == 16) ahead(it, x + 16);
+            const int m = min(2, it.t1 - x);
+            uint32_t k4[2][4], v4[2][4];
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const int key = (x + y) * kKeys + 32 * z + lane;
-              k4[y][z] = v4[y][z] = 127;
-              if (y < m && key < it.end) {
-                k4[y][z] = __ldg(p.k_scale + row + key);
-                v4[y][z] = __ldg(p.v_scale + row + key);
+              for (int z = 0; z < 4; ++z) {
+                const int key = (x + y) * kKeys + 32 * z + lane;
+                k4[y][z] = v4[y][z] = 127;
+                if (y < m && key < it.end) {
+                  k4[y][z] = __ldg(p.k_scale + row + key);
+                  v4[y][z] = __ldg(p.v_scale + row + key);
+                }
               }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              if (y >= m || !ok) break;
+              const int slot = t % kScaleTiles;
+              ok = t < kScaleTiles || warp_wait(bar(C::SC_EMPTY + slot), ((t / kScaleTiles) - 1) & 1, abort_flag,
+                                                site + C::SC_EMPTY + slot);
+              if (!ok) break;
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                ring[slot * kKeys + 32 * z + lane] = static_cast<uint16_t>(k4[y][z] | (v4[y][z] << 8));
+              warp_arrive(bar(C::SC_FULL + slot), lane);
+              ++t;
             }
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if (y >= m || !ok) break;
-            const int slot = t % kScaleTiles;
-            ok = t < kScaleTiles || warp_wait(bar(C::SC_EMPTY + slot), ((t / kScaleTiles) - 1) & 1, abort_flag,
-                                              site + C::SC_EMPTY + slot);
-            if (!ok) break;
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              ring[slot * kKeys + 32 * z + lane] = static_cast<uint16_t>(k4[y][z] | (v4[y][z] << 8));
-            warp_arrive(bar(C::SC_FULL + slot), lane);
-            ++t;
           }
         }
-      }
-    } else if (warp < kQWarp + C::Q_THREADS / 32) {
-    // ---- the next units' Q, output rows and mask words
-    const int site = kRoleRowsQ * 64;
-    constexpr int QT = C::Q_THREADS;
-    const int qt = tid - 32 * kQWarp;
-    int k = 0;  // units with keys
-    for (int taken = 0;; ++taken) {
-      const Unit it = take(taken, site);
-      if (it.b < 0) break;
-      if (it.t1 == it.t0) {
-        // no key at all: output 0, log-sum-exp -inf
-        for (int r = qt >> 3; r < NR; r += QT / 8) {
-          int t;
-          const int out = out_row(it, r, &t);
-          if (out < 0) break;
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d);
-          for (int x = qt & 7; 8 * x < p.d; x += 8) dst[x] = make_uint4(0, 0, 0, 0);
-          if (p.lse && (qt & 7) == 0) p.lse[(it.b * p.H + out % p.H) * p.T + t] = -INFINITY;
+      } else if (warp < kQWarp + C::Q_THREADS / 32) {
+        // ---- the next units' Q, output rows and mask words
+        const int site = kRoleRowsQ * 64;
+        constexpr int QT = C::Q_THREADS;
+        const int qt = tid - 32 * kQWarp;
+        int k = 0;  // units with keys
+        for (int taken = 0;; ++taken) {
+          const Unit it = take(taken, site);
+          if (it.b < 0) break;
+          if (it.t1 == it.t0) {
+            // no key at all: output 0, log-sum-exp -inf
+            for (int r = qt >> 3; r < NR; r += QT / 8) {
+              int t;
+              const int out = out_row(it, r, &t);
+              if (out < 0) break;
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d);
+              for (int x = qt & 7; 8 * x < p.d; x += 8) dst[x] = make_uint4(0, 0, 0, 0);
+              if (p.lse && (qt & 7) == 0) p.lse[(it.b * p.H + out % p.H) * p.T + t] = -INFINITY;
+            }
+            continue;
+          }
+          const int buf = k & 1;
+          if (k > 0) {  // (the softmax threads prepare the first)
+            ask_q(it, qt, QT);
+            const bool ok = prepare_q(std::integral_constant<int, QT>{}, it, buf, qt, [&]() {
+              return k < 2 || warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, site + C::Q_EMPTY + buf);
+            });
+            if (!ok) break;
+            fence_proxy_async_smem();
+            warp_arrive(bar(C::Q_FULL + buf), lane);
+          }
+          ++k;
         }
-        continue;
       }
-      const int buf = k & 1;
-      if (k > 0) {  // (the softmax threads prepare the first)
-        ask_q(it, qt, QT);
-        const bool ok = prepare_q(std::integral_constant<int, QT>{}, it, buf, qt, [&]() {
-          return k < 2 || warp_wait(bar(C::Q_EMPTY + buf), ((k >> 1) - 1) & 1, abort_flag, site + C::Q_EMPTY + buf);
-        });
-        if (!ok) break;
-        fence_proxy_async_smem();
-        warp_arrive(bar(C::Q_FULL + buf), lane);
-      }
-      ++k;
     }
-    }
-  }
   } else {
     if constexpr (C::SPLIT_REGS) regs_increase<C::REGS_SOFT>();
     // ---- softmax: thread = key; warpgroup wg has rows r0 .. r0 + RPT - 1
@@ -989,44 +989,44 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           constexpr int LG = F8 ? 1 : GROUPS;
 #pragma unroll
           for (int g0 = 0; g0 < GROUPS; g0 += LG) {
-          if (g0 * GW >= rows_here) continue;
-          uint32_t c1[LG][GW], c2[F8 ? LG : 1][GW];
+            if (g0 * GW >= rows_here) continue;
+            uint32_t c1[LG][GW], c2[F8 ? LG : 1][GW];
 #pragma unroll
-          for (int g = 0; g < LG; ++g) {
-            if ((g0 + g) * GW >= rows_here) continue;
-            tmem_ld_cols<GW>(s_at + (g0 + g) * GW, c1[g]);
-            if constexpr (F8) tmem_ld_cols<GW>(s_at + NR + (g0 + g) * GW, c2[g]);
-          }
-          tmem_ld_wait();
+            for (int g = 0; g < LG; ++g) {
+              if ((g0 + g) * GW >= rows_here) continue;
+              tmem_ld_cols<GW>(s_at + (g0 + g) * GW, c1[g]);
+              if constexpr (F8) tmem_ld_cols<GW>(s_at + NR + (g0 + g) * GW, c2[g]);
+            }
+            tmem_ld_wait();
 #pragma unroll
-          for (int gg = 0; gg < LG; ++gg) {
-            const int g = g0 + gg;
-            if (g * GW >= rows_here) continue;
+            for (int gg = 0; gg < LG; ++gg) {
+              const int g = g0 + gg;
+              if (g * GW >= rows_here) continue;
 #pragma unroll
-            for (int r = 0; r < GW; r += 4) {
-              float* y = x + g * GW + r;
-              const float4 m = *reinterpret_cast<const float4*>(ref + g * GW + r);
-              const uint32_t* a = c1[gg] + r;
-              if constexpr (F8) {
-                const float4 f = *reinterpret_cast<const float4*>(factor + g * GW + r);
-                const uint32_t* c = c2[gg] + r;
-                float b[4], h[4];
-                fma2(b[0], b[1], __uint_as_float(c[0]), __uint_as_float(c[1]), 1.f / 32.f, 1.f / 32.f,
-                     __uint_as_float(a[0]), __uint_as_float(a[1]));
-                fma2(b[2], b[3], __uint_as_float(c[2]), __uint_as_float(c[3]), 1.f / 32.f, 1.f / 32.f,
-                     __uint_as_float(a[2]), __uint_as_float(a[3]));
-                mul2(h[0], h[1], f.x, f.y, kf, kf);
-                mul2(h[2], h[3], f.z, f.w, kf, kf);
-                fma2(y[0], y[1], b[0], b[1], h[0], h[1], ev - m.x, ev - m.y);
-                fma2(y[2], y[3], b[2], b[3], h[2], h[3], ev - m.z, ev - m.w);
-              } else {
-                fma2(y[0], y[1], __uint_as_float(a[0]), __uint_as_float(a[1]), p.scale_log2, p.scale_log2, -m.x,
-                     -m.y);
-                fma2(y[2], y[3], __uint_as_float(a[2]), __uint_as_float(a[3]), p.scale_log2, p.scale_log2, -m.z,
-                     -m.w);
+              for (int r = 0; r < GW; r += 4) {
+                float* y = x + g * GW + r;
+                const float4 m = *reinterpret_cast<const float4*>(ref + g * GW + r);
+                const uint32_t* a = c1[gg] + r;
+                if constexpr (F8) {
+                  const float4 f = *reinterpret_cast<const float4*>(factor + g * GW + r);
+                  const uint32_t* c = c2[gg] + r;
+                  float b[4], h[4];
+                  fma2(b[0], b[1], __uint_as_float(c[0]), __uint_as_float(c[1]), 1.f / 32.f, 1.f / 32.f,
+                       __uint_as_float(a[0]), __uint_as_float(a[1]));
+                  fma2(b[2], b[3], __uint_as_float(c[2]), __uint_as_float(c[3]), 1.f / 32.f, 1.f / 32.f,
+                       __uint_as_float(a[2]), __uint_as_float(a[3]));
+                  mul2(h[0], h[1], f.x, f.y, kf, kf);
+                  mul2(h[2], h[3], f.z, f.w, kf, kf);
+                  fma2(y[0], y[1], b[0], b[1], h[0], h[1], ev - m.x, ev - m.y);
+                  fma2(y[2], y[3], b[2], b[3], h[2], h[3], ev - m.z, ev - m.w);
+                } else {
+                  fma2(y[0], y[1], __uint_as_float(a[0]), __uint_as_float(a[1]), p.scale_log2, p.scale_log2, -m.x,
+                       -m.y);
+                  fma2(y[2], y[3], __uint_as_float(a[2]), __uint_as_float(a[3]), p.scale_log2, p.scale_log2, -m.z,
+                       -m.w);
+                }
               }
             }
-          }
           }
           if (masked) {
 #pragma unroll

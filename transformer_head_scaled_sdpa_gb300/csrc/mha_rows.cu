@@ -403,6 +403,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   // grid before it touches global memory)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  const bool ordered = longest_first(p, kSms * C::MIN_BLOCKS);
   const int blks = C::BLKS == 1 ? 1 : (p.d + 127) / 128;  // 128-feature blocks in use
   // The k-th published unit (each consumer warp takes each, in order); b = -1 at
   // the end of the work or when the CTA gave up.
@@ -560,10 +561,15 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           table[p.B + 1] = per;
         }
         __syncwarp();
+      } else if (ordered) {
+        const int place = place_of(p, lane);
+        if (lane < p.B) table[place] = lane;
+        __syncwarp();
       }
       auto unit_at = [&](int index) {
         const int part = index / p.units;
-        if (!balanced(p)) return unit_of(p, index, blocks, part % p.B, part / p.B, 0);
+        if (!balanced(p))
+          return unit_of(p, index, blocks, ordered ? table[part] : part % p.B, part / p.B, 0);
         int b = 0;
         while (b < p.B && part >= table[b + 1]) ++b;
         if (b == p.B) {
@@ -915,7 +921,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
     auto wait = [&](int id, uint32_t parity) {
       ok = ok && thread_wait(bar(id), parity, abort_flag, site + id);
     };
-    if (!balanced(p)) {
+    if (!balanced(p) && !ordered) {
       // the first unit's Q before the ring's first copies (it is this CTA's own)
       Unit own;
       const int index = static_cast<int>(blockIdx.x), u = index % p.units;

@@ -321,7 +321,12 @@ int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k
  *              allowed when that is 0); not shared with a concurrent call.
  * The tensor cores read the codes as they are.  q enters as two e4m3 pieces
  * that give its bf16 values back (to 2^-22 of the row's largest), the weights
- * as three e5m2 pieces (2^-11 relative); products accumulate in float32.
+ * as three e5m2 pieces (2^-11 relative); products accumulate in float32.  A
+ * weight is kept relative to the row's largest a_j 2^(s_j - 127) (s_j: the V
+ * row's scale byte): V rows of a sequence and head whose scales differ by more
+ * than 2^100 are outside this accuracy.  One or two query heads per key head
+ * over a short cache (Lk * d_k * H / H_kv <= 16384) are computed in float32
+ * on the CUDA cores.
  */
 int mha_decode_f8(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                   const uint8_t* v_scale, void* out, float* lse, int B, int H, int H_kv, int Lk,
@@ -354,7 +359,7 @@ size_t mha_decode_f8_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k);
  * must hold finite values.  T up to 256 (MHA_ERR_UNSUPPORTED beyond); other
  * arguments, the workspace and errors as mha_decode_f8.
  * Products accumulate in float32; over a bf16 cache the weights enter the
- * product with V as two bf16 pieces (2^-16 relative).
+ * product with V as two bf16 pieces (2^-15 relative).
  */
 int mha_decode_tree(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
                     int B, int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,

@@ -14,10 +14,14 @@
 // exceeds it by more than 8 (log2), and O is rescaled then: the halves exchange their
 // maxima only when one of a row tile's rows has to move.
 //
-// Bound: per tile of 128 keys and 256 rows of 128 features the tensor core reads
-// 2 x 8 x 8 KB (S) and 2 x 16 x 4 KB (PV) of shared memory, TMA writes 64 KB (2,560
-// cycles at 128 bytes), and 32,768 exponentials take 2,048 cycles; the two row tiles
-// alternate between the tensor core and the softmax.
+// Bound: the tensor core.  A tile of 128 keys takes 256 rows of 128 features 16
+// products of 128 x 128 x 16 for S and 32 for PV (both pieces), 64 cycles each; its
+// 32,768 exponentials take 2,048 cycles and shared memory 2,560 (S reads 2 x 8 x 8
+// KB, PV 2 x 16 x 4 KB, TMA writes 64 KB, at 128 bytes a cycle).  The two row tiles
+// alternate between the tensor core and the softmax: 4,100 cycles measured, 56 % of
+// the tensor core over a launch.  3 sequences of 9,001 to 16,300 keys x 8 key heads x
+// 252 rows: 58 us (104 with the rows along N); one thread per row with 128 scores in
+// registers instead of two with 64: 61 and 63 us before the splits were balanced.
 //
 // Work: a CTA per (split, sequence, key head, block of 256 rows), key heads the
 // fastest (they lie side by side in the cache).  Partials as in mha_rows.cu.

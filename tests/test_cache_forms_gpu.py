@@ -167,6 +167,29 @@ def test_ragged_splits(mha, shape, f8):  # noqa: F811
     check_step(case, out, lse, f8, what=str(shape[:6]))
 
 
+LONGEST_FIRST = [
+    # B, T, H, H_kv, d, Lk, prefix, f8: more units than CTAs run at once, no splits
+    (3, 65, 60, 60, 64, 130, [3, 65, 20], False),       # rows along M
+    (2, 70, 80, 80, 16, 90, [0, 20], False),
+    (32, 3, 10, 10, 64, 60, None, False),
+    (5, 2, 70, 70, 128, 200, [1, 198, 0, 60, 198], True),
+    (4, 20, 40, 40, 256, 60, [40, 0, 7, 39], True),
+]
+
+
+@pytest.mark.parametrize("shape", LONGEST_FIRST, ids=lambda s: "x".join(map(str, s[:6])))
+def test_longest_first(mha, shape):  # noqa: F811
+    B, T, H, H_kv, d, Lk, prefix, f8 = shape
+    if prefix is None:
+        prefix = np.random.default_rng(4).integers(0, Lk - T + 1, size=B).tolist()
+    case = make_step(sum(shape[:6]), B, T, H, H_kv, d, Lk, prefix, None, "tree", f8)
+    out, lse = call_step(mha, on_gpu(case), f8, True)
+    launch = mha.last_launch_info()
+    assert launch["kernels"] == 1 and launch["grid"] > 152
+    assert mha.mha_sync_status() == 0
+    check_step(case, out, lse, f8, what=str(shape[:6]))
+
+
 @pytest.mark.parametrize("kind", ["block", "short"])
 def test_forms_repeat(mha, kind):  # noqa: F811
     """The same bits on every call, from two streams at once, and from a captured

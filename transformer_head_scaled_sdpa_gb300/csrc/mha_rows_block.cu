@@ -158,7 +158,10 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
       b = max(0, __ffs(has) - 1);
       split = part - __shfl_sync(0xffffffffu, first, b);
     }
-    if (longest_first(p, kSms)) b = __ffs(__ballot_sync(0xffffffffu, lane < p.B && place_of(p, lane) == b)) - 1;
+    if (longest_first(p, kSms)) {
+      const int place = place_of(p, lane);  // (by the whole warp)
+      b = __ffs(__ballot_sync(0xffffffffu, lane < p.B && place == b)) - 1;
+    }
     it = unit_of(p, index, blocks, b, split, per);
     if (!there) it.splits = 0;
   }

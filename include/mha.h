@@ -271,6 +271,8 @@ size_t mha_decode_static_scratch_bytes(void);
  *   k_scale, v_scale  [B, H, Lk] uint8: a biased exponent per position and
  *                     head; byte s scales its row's codes by 2^(s - 127).
  *   d_k               a multiple of 16 from 16 to 256.
+ *   Lk                up to 2^31 - 1024 (MHA_ERR_SHAPE beyond; likewise for the
+ *                     steps below).
  *
  * mha_cache_write_f8 -- quantises T new rows per sequence into the cache.
  * Row x = k[b, t, h] (v likewise) goes to position start[b] + t as

@@ -151,6 +151,8 @@ RAGGED = [
     (33, 2, 1, 1, 64, 6000, None),
     (4, 1, 2, 1, 64, 40000, [39000, 0, 0, 0]),     # one sequence has all the splits
     (3, 1, 4, 4, 128, 5000, [0, 0, 0]),
+    (33, 40, 2, 1, 64, 2000, None),                # 80 rows, not balanced
+    (6, 40, 2, 1, 128, 3000, None),                # 80 rows, balanced
 ]
 
 
@@ -159,12 +161,24 @@ RAGGED = [
 def test_ragged_splits(mha, shape, f8):  # noqa: F811
     B, T, H, H_kv, d, Lk, lens = shape
     if lens is None:
-        lens = (6000 * np.random.default_rng(1).random(B) ** 3).astype(int).tolist()
+        lens = (Lk * np.random.default_rng(1).random(B) ** 3).astype(int).tolist()
     case = make_step(sum(shape[:6]), B, T, H, H_kv, d, Lk, lens, None, "tree", f8)
     out, lse = call_step(mha, on_gpu(case), f8, True)
     assert mha.last_launch_info()["kernels"] == 2
     assert mha.mha_sync_status() == 0
     check_step(case, out, lse, f8, what=str(shape[:6]))
+
+
+def test_read_of_negative_lengths(mha):  # noqa: F811
+    """A length below zero reads nothing, the least one too."""
+    x = cu.random_rows(1, (3, 40, 2, 16))
+    codes, scales = cu.f8_cache(x)
+    out = [torch.full((3, 40, 2, 16), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    mha.mha_cache_read_f8(codes.cuda(), codes.cuda(), scales.cuda(), scales.cuda(),
+                          i32([-2 ** 31, -1, 1]).cuda(), k=out[0], v=out[1])
+    assert mha.mha_sync_status() == 0
+    for t in out:
+        assert (t[:2] == 7.0).all() and (t[2, 1:] == 7.0).all() and not (t[2, 0] == 7.0).all()
 
 
 LONGEST_FIRST = [

@@ -120,6 +120,18 @@ def test_step_refusals(lib, fn):
     assert step(lib, fn, B=0) == OK and step(lib, fn, H=0, H_kv=0, q=None) == OK
 
 
+def test_more_positions_than_an_int_counts(lib):
+    """A capacity whose last tile would not fit an int is refused, not wrapped."""
+    far = 2 ** 31 - 1
+    assert write(lib, B=1, H=1, Lk=far, d=16) == SHAPE
+    assert write(lib, B=1, H=1, T=far, d=16) == SHAPE
+    assert write(lib, B=1, H=1, T=1 << 30, ts=1 << 40, d=16) == SHAPE
+    assert read(lib, B=1, H=1, Lk=far, d=16) == SHAPE
+    for fn in ("mha_decode_f8", "mha_decode_tree", "mha_decode_tree_f8"):
+        assert step(lib, fn, B=1, T=1, H=1, H_kv=1, Lk=far, d=16) == SHAPE
+    assert lib.mha_decode_f8_workspace_bytes(1, 1, 1, far, 16) == 0
+
+
 def test_workspace_rules(lib):
     ws = lib.mha_decode_f8_workspace_bytes
     assert ws(2, 32, 8, 65536, 24) == 0 and ws(2, 32, 5, 65536, 128) == 0

@@ -565,9 +565,12 @@ size_t mha_decode_static_scratch_bytes(void) { return kDecodeStaticScratchBytes;
 static bool f8_width_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
 
 // The bytes of codes and of scales that a cache [B, Lk, H, d] holds.
+// Most positions of a cache, and tokens of a call: a tile past them fits an int.
+static constexpr int kMaxPositions = 0x7fffffff - 1023;
+
 static bool cache_sizes(int B, int H, int Lk, int d, size_t* codes, size_t* scales) {
   const long long rows = static_cast<long long>(B) * H;
-  if (rows > 0x7fffffffll || rows * Lk > (1ll << 40)) return false;
+  if (Lk > kMaxPositions || rows > 0x7fffffffll || rows * Lk > (1ll << 40)) return false;
   *scales = static_cast<size_t>(rows) * Lk;
   *codes = *scales * d;
   return true;
@@ -581,11 +584,12 @@ int mha_cache_write_f8(const void* k, const void* v, long long token_stride, lon
   if (B < 0 || T < 0 || H < 0 || Lk < 0 || token_stride < 0 || seq_stride < 0) return MHA_ERR_SHAPE;
   if (!f8_width_ok(d_k)) return MHA_ERR_UNSUPPORTED;
   size_t codes = 0, scales = 0;
-  if (!cache_sizes(B, H, Lk, d_k, &codes, &scales) ||
+  if (!cache_sizes(B, H, Lk, d_k, &codes, &scales) || T > kMaxPositions ||
       static_cast<long long>(B) * H * T > (1ll << 40))
     return MHA_ERR_SHAPE;
   const long long hd = static_cast<long long>(H) * d_k;
   if (token_stride == 0) token_stride = hd;
+  if (T > 0 && token_stride > (1ll << 50) / T) return MHA_ERR_SHAPE;
   if (seq_stride == 0) seq_stride = T * token_stride;
   if (B == 0 || T == 0 || H == 0 || Lk == 0) return MHA_OK;
   if (token_stride < hd || token_stride > (1ll << 40) || seq_stride < hd || seq_stride > (1ll << 50))
@@ -686,7 +690,7 @@ static size_t rows_ws_bytes(const mha::RowsPlan& plan) {
 
 // Sizes of a rows step: MHA_OK, or the code of what is wrong.
 static int rows_sizes_ok(int B, int T, int H, int H_kv, int Lk, int d_k, bool f8) {
-  if (B < 0 || T < 0 || H < 0 || H_kv < 0 || Lk < 0) return MHA_ERR_SHAPE;
+  if (B < 0 || T < 0 || H < 0 || H_kv < 0 || Lk < 0 || Lk > kMaxPositions) return MHA_ERR_SHAPE;
   if (H > 0 && (H_kv == 0 || H % H_kv != 0)) return MHA_ERR_SHAPE;
   if (!(f8 ? f8_width_ok(d_k) : decode_width_ok(d_k)) || T > kMaxDrafts) return MHA_ERR_UNSUPPORTED;
   const long long bh = static_cast<long long>(B) * H;

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   const int sub = static_cast<int>(threadIdx.x) % GS;
   const bool has0 = 8 * sub < p.d, has1 = 8 * (sub + GS) < p.d;
   if (!r.head_ok || !has0) return;
-  const int last = min(r.nt, __ldg(p.lens + r.b) - r.t0);
+  const int last = min(r.nt, max(__ldg(p.lens + r.b), 0) - r.t0);
   const long long row = ((static_cast<long long>(r.b) * p.Lk + r.t0) * p.H + r.h) * p.d + 8 * sub;
   const uint8_t* src[2] = {static_cast<const uint8_t*>(p.k_cache) + row,
                            static_cast<const uint8_t*>(p.v_cache) + row};

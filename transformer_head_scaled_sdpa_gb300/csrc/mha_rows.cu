@@ -251,6 +251,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 
+// The larger magnitudes of pairs of bf16 (NaN loses).
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(m));
+  return r;
+}
+
 // Largest value of the warp.
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -495,43 +503,37 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         row_mask(buf)[r * kMaskWords + sub] = word;
       }
       if constexpr (F8) {
-        float amax = 0.f;
+        uint32_t top = 0;  // the largest magnitudes of even and odd elements (bf16 pair)
 #pragma unroll
-        for (int z = 0; z < PER; ++z) {
-          const uint32_t q4[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q4[e])), fabsf(bf16_hi(q4[e]))));
-        }
+        for (int z = 0; z < PER; ++z)
+          top = max_abs_bf16x2(max_abs_bf16x2(top, v[z].x, v[z].y), v[z].z, v[z].w);
+        float amax = fmaxf(bf16_lo(top), bf16_hi(top));
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         // q 2^-e with the largest magnitude in [128, 256)
         const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 7, -100);
         const float inv = pow2i(-e);
         if (sub == 0) row_factor(buf)[r] = pow2i(e) * p.scale_log2;
+        // (a loop over eight elements, the rest moving up: unrolled this was most of the
+        // code that a CTA waits for before its first scores)
+        uint32_t to = sQ + sub * (C::NQ * 16) + r * 16;
+#pragma unroll 1
+        for (int z = 0; z < PER; ++z) {
+          const uint32_t q4[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+          uint32_t a[4], c2[4];
 #pragma unroll
-        for (int u = 0; u < PER / 2; ++u) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const uint4 w4 = v[2 * u + z];
-            const uint32_t q4[4] = {w4.x, w4.y, w4.z, w4.w};
-            uint32_t a[4], c2[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float x0 = bf16_lo(q4[x]) * inv, x1 = bf16_hi(q4[x]) * inv;
-              a[x] = pack_e4m3x2(x0, x1);
-              const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[x]));
-              c2[x] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
-            }
-            hi[2 * z] = a[0] | (a[1] << 16);
-            hi[2 * z + 1] = a[2] | (a[3] << 16);
-            lo[2 * z] = c2[0] | (c2[1] << 16);
-            lo[2 * z + 1] = c2[2] | (c2[3] << 16);
+          for (int x = 0; x < 4; ++x) {
+            const float x0 = bf16_lo(q4[x]) * inv, x1 = bf16_hi(q4[x]) * inv;
+            a[x] = pack_e4m3x2(x0, x1);
+            const uint32_t h2 = e4m3x2_to_half2(static_cast<uint16_t>(a[x]));
+            c2[x] = pack_e4m3x2((x0 - half_lo(h2)) * 32.f, (x1 - half_hi(h2)) * 32.f);
           }
-          const uint32_t to = sQ + (sub + 8 * u) * (C::NQ * 16) + r * 16;
-          st_shared_v4(to, hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(to + NR * 16, lo[0], lo[1], lo[2], lo[3]);
+          st_shared_v2(to, a[0] | (a[1] << 16), a[2] | (a[3] << 16));
+          st_shared_v2(to + NR * 16, c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+          // (the other half of the 16 elements, then the next 16 of the thread)
+          to += (z & 1) ? 8 * (C::NQ * 16) - 8 : 8;
+#pragma unroll
+          for (int x = 0; x + 1 < PER; ++x) v[x] = v[x + 1];
         }
       } else {
 #pragma unroll
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
         auto load = [&](const CUtensorMap* big, const CUtensorMap* small, int key, int end, int hk, int b) {
           const int boxes = end - key >= kKeys ? 0 : (end - key + kBoxKeys - 1) / kBoxKeys;
           const uint32_t box_bytes = boxes == 0 ? kKeys * 128 : boxes * kBoxKeys * 128;
-#pragma unroll
+#pragma unroll 1
           for (int blk = 0; blk < C::BLKS; ++blk) {
             if (blk >= blks) break;
             const int s = ring.slot;
@@ -657,15 +659,18 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
               if (got) publish(next);
             }
           };
-          if (works) {
-            for (int x = w.t0; x < w.t1 && ok; ++x) {
-              load(&p.tm_k, &p.tm_k_box, x * kKeys, w.end, w.hk, w.b);
-              if (x > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (x - 1) * kKeys, w.end, w.hk, w.b);
-              if (2 * (x - w.t0 + 1) >= w.t1 - w.t0) poll(false);
+          // K(0) K(1) V(0) K(2) V(1) ... V(last), then the next unit for certain
+          const int n = works ? w.t1 - w.t0 : 0;
+          for (int s = 0;; ++s) {
+            if (s < 2 * n && ok) {
+              const bool last = s == 2 * n - 1, v = last || (s > 0 && (s & 1) == 0);
+              const int x = w.t0 + (last ? n - 1 : (v ? s / 2 - 1 : (s + 1) / 2));
+              load(v ? &p.tm_v : &p.tm_k, v ? &p.tm_v_box : &p.tm_k_box, x * kKeys, w.end, w.hk, w.b);
             }
-            if (w.t1 > w.t0 && ok) load(&p.tm_v, &p.tm_v_box, (w.t1 - 1) * kKeys, w.end, w.hk, w.b);
+            const bool must = s >= 2 * n || !ok;
+            if (s >= n || must) poll(must);
+            if (must) break;
           }
-          poll(true);
           if (!got) break;
           w = next;
         }
@@ -843,24 +848,24 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           if (it.b < 0) break;
           ahead(it, it.t0);
           const long long row = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
-          // (two tiles' loads in flight)
-          for (int x = it.t0; x < it.t1 && ok; x += 2) {
+          // (two tiles' loads in flight; one where the registers are few: 35.2 and 37.0 us
+          // over 5 x 2 key heads x 56 rows of 256 features, 16 x 96 x 1 of 128 94.6 and 93.3)
+          constexpr int BATCH = C::MANY_Q ? 1 : 2;
+          for (int x = it.t0; x < it.t1 && ok; x += BATCH) {
             if (((x - it.t0) & 31) == 16) ahead(it, x + 16);
-            const int m = min(2, it.t1 - x);
-            uint32_t k4[2][4], v4[2][4];
+            const int m = min(BATCH, it.t1 - x);
+            // (a key past the last takes its scales: nothing uses them)
+            uint32_t k4[BATCH][4], v4[BATCH][4];
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
+            for (int y = 0; y < BATCH; ++y)
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
-                const int key = (x + y) * kKeys + 32 * z + lane;
-                k4[y][z] = v4[y][z] = 127;
-                if (y < m && key < it.end) {
-                  k4[y][z] = __ldg(p.k_scale + row + key);
-                  v4[y][z] = __ldg(p.v_scale + row + key);
-                }
+                const int key = min((x + y) * kKeys + 32 * z + lane, it.end - 1);
+                k4[y][z] = __ldg(p.k_scale + row + key);
+                v4[y][z] = __ldg(p.v_scale + row + key);
               }
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < BATCH; ++y) {
               if (y >= m || !ok) break;
               const int slot = t % kScaleTiles;
               ok = t < kScaleTiles || warp_wait(bar(C::SC_EMPTY + slot), ((t / kScaleTiles) - 1) & 1, abort_flag,
@@ -1078,14 +1083,11 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             x[r + 1] -= by.y;
             x[r + 2] -= by.z;
             x[r + 3] -= by.w;
-            if (i > 0) {
-              l[r] *= ex2_approx(-by.x);
-              l[r + 1] *= ex2_approx(-by.y);
-              l[r + 2] *= ex2_approx(-by.z);
-              l[r + 3] *= ex2_approx(-by.w);
-            }
           }
           if (i > 0) {
+#pragma unroll
+            for (int r = 0; r < RPT; ++r)
+              if (r / GW * GW < rows_here) l[r] *= ex2_approx(-shift[r]);
             wait(C::PV_DONE, (t - 1) & 1);
             tc_fence_after();
 #pragma unroll 1

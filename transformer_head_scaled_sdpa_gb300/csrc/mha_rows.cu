@@ -66,12 +66,13 @@
 // the loads of a whole ring, run during a unit's epilogue.  Every wait is bounded
 // (abort flag, MHA_ERR_TIMEOUT).
 //
-// What bounds it (16 x 96 heads x 2,048 keys of 128 features in 8 bits, 610 MB): 97
-// us, 6.3 TB/s, 0.93 of the measured copy; with 16 rows and 4 sequences 40 us, 3.9
+// What bounds it (16 x 96 heads x 2,048 keys of 128 features in 8 bits, 610 MB): 95
+// us, 6.4 TB/s, 0.95 of the measured copy; with 16 rows and 4 sequences 36 us, 4.4
 // TB/s: the softmax threads' instructions (30 per weight: three pieces) and 384 units
 // on 304 CTAs.  A unit costs five tiles of 128 keys beside its own (Q, the first
-// maxima, the epilogue), and instructions come from DRAM after a pass over a cache
-// that flushes L2: 6 to 8 thousand cycles before the first scores.
+// maxima, the epilogue).  Code that runs for the first time costs some 30 cycles an
+// instruction, so what a CTA runs before its first weights (10 to 20 thousand cycles)
+// is kept short: loops where nothing else is lost, one site of each load and wait.
 #include <cuda_bf16.h>
 
 #include <type_traits>

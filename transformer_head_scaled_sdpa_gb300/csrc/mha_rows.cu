@@ -1449,10 +1449,10 @@ void with_config(bool f8, int d, int R, F&& f) {
 //   128 features: 60 rows 56 us along N and 58 along M, 96 rows 68 and 58, 128 rows
 //   68 and 60; 64 rows of 8 blocks: 566 and 269 at 2,048 rows x 32,000 keys).
 //   A row or two over a short 8-bit cache: the CUDA cores (features x keys of the
-//   cache, full: 128 x 8 heads 64 x 64 15 us here and 25 on the tensor cores, 64 x
-//   128 17 and 23, 64 x 256 23 and 25, half full 10 and 23; 16 x 96 heads 128 x 64
-//   21 and 29, 128 x 128 27 and 27, 128 x 256 44 and 33; two rows 64 x 256 31 and
-//   25).
+//   cache, full: 128 x 8 heads 64 x 64 13 us here and 25 on the tensor cores, 64 x
+//   256 17 and 23, half full 8.5 and 23; 64 x 512 27 and 29; 16 x 96 heads 128 x 128
+//   25 and 25, 128 x 256 39 and 33; 1 x 8 heads 64 x 128 9 and 11, 64 x 256 13 and 11;
+//   two rows, 128 x 8 heads 64 x 128 19 and 21).
 RowsForm rows_form(bool f8, int d, int T, int G, int Lk) {
   if (!f8 && d <= 128 && T * G > 64) return kRowsBlock;
   if (f8 && T == 1 && G <= kShortRows && static_cast<long long>(Lk) * d * G <= kShortWork) return kRowsShort;

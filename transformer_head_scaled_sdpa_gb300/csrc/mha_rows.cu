@@ -297,9 +297,13 @@ __device__ __forceinline__ float warp_sums(const float (&v)[N], int lane) {
 // 8 or 16 consecutive 32-bit columns of this warp's TMEM lanes.
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16, "columns");
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
   if constexpr (N == 16) {
     tmem_ld16(at, r);
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at));
   } else {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
@@ -309,9 +313,13 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16, "columns");
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
   if constexpr (N == 16) {
     tmem_st16(at, r);
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
   } else {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -1148,7 +1156,10 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
           // 16-byte units [column of units][key]: 16 (8-bit) or 8 rows of a piece
           constexpr int COL = kKeys * 16;
-          if constexpr (F8 && NR == 8) {
+          if constexpr (F8 && NR == 4) {
+            // the three pieces in one unit
+            st_shared_v4(sP + kt * 16, w1[0], w2[0], w3[0], 0);
+          } else if constexpr (F8 && NR == 8) {
             // two pieces to a unit; nothing reads the second half of the last
             const uint32_t to = sP + kt * 16;
             st_shared_v4(to, w1[0], w1[1], w2[0], w2[1]);
@@ -1418,16 +1429,21 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
   return e;
 }
 
-// Calls f with the kernel's configuration for R rows per key head of d features.
+// Calls f with the kernel's configuration for R rows per key head of d features.  Rows
+// beyond R cost their weights all the same (8 bits, 128 features: one row over 16 x 96
+// heads x 2,048 keys 94.5 us in units of four and 95.4 of eight, four over 2 x 8 x 64k
+// 42.2 and 43.2).
 template <typename F>
 void with_config(bool f8, int d, int R, F&& f) {
   if (f8 && d <= 128) {
-    if (R <= 8) f(RowsCfg<true, 128, 8>{});
+    if (R <= 4) f(RowsCfg<true, 128, 4>{});
+    else if (R <= 8) f(RowsCfg<true, 128, 8>{});
     else if (R <= 16) f(RowsCfg<true, 128, 16>{});
     else if (R <= 32) f(RowsCfg<true, 128, 32>{});
     else f(RowsCfg<true, 128, 64>{});
   } else if (f8) {
-    if (R <= 8) f(RowsCfg<true, 256, 8>{});
+    if (R <= 4) f(RowsCfg<true, 256, 4>{});
+    else if (R <= 8) f(RowsCfg<true, 256, 8>{});
     else if (R <= 16) f(RowsCfg<true, 256, 16>{});
     else f(RowsCfg<true, 256, 32>{});
   } else if (d <= 64) {

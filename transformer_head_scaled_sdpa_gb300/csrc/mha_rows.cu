@@ -1432,7 +1432,8 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
 // Calls f with the kernel's configuration for R rows per key head of d features.  Rows
 // beyond R cost their weights all the same (8 bits, 128 features: one row over 16 x 96
 // heads x 2,048 keys 94.5 us in units of four and 95.4 of eight, four over 2 x 8 x 64k
-// 42.2 and 43.2).
+// 42.2 and 43.2; bf16, 64 features: four over 128 x 8 heads x 250 keys 25 us in units
+// of eight and 27 of sixteen; wider heads, one CTA per SM, the same in both).
 template <typename F>
 void with_config(bool f8, int d, int R, F&& f) {
   if (f8 && d <= 128) {
@@ -1447,7 +1448,8 @@ void with_config(bool f8, int d, int R, F&& f) {
     else if (R <= 16) f(RowsCfg<true, 256, 16>{});
     else f(RowsCfg<true, 256, 32>{});
   } else if (d <= 64) {
-    if (R <= 16) f(RowsCfg<false, 64, 16>{});
+    if (R <= 8) f(RowsCfg<false, 64, 8>{});
+    else if (R <= 16) f(RowsCfg<false, 64, 16>{});
     else if (R <= 32) f(RowsCfg<false, 64, 32>{});
     else f(RowsCfg<false, 64, 64>{});
   } else if (d <= 128) {

@@ -1094,9 +1094,11 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             x[r + 3] -= by.w;
           }
           if (i > 0) {
+            // (a row's first key may move its reference down by any amount; its sums and
+            // O are 0 then, and a factor above 1 could be infinite: 0 * inf)
 #pragma unroll
             for (int r = 0; r < RPT; ++r)
-              if (r / GW * GW < rows_here) l[r] *= ex2_approx(-shift[r]);
+              if (r / GW * GW < rows_here) l[r] *= ex2_approx(fminf(-shift[r], 0.f));
             wait(C::PV_DONE, (t - 1) & 1);
             tc_fence_after();
 #pragma unroll 1
@@ -1111,7 +1113,7 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
                 tmem_ld_wait();
 #pragma unroll
                 for (int r = 0; r < GW; ++r)
-                  o[r] = __float_as_uint(__uint_as_float(o[r]) * ex2_approx(-shift[g * GW + r]));
+                  o[r] = __float_as_uint(__uint_as_float(o[r]) * ex2_approx(fminf(-shift[g * GW + r], 0.f)));
                 tmem_st_cols<GW>(o_at, o);
               }
             tmem_st_wait();

@@ -1,0 +1,79 @@
+"""Calls on a stream other than the current one, whose outputs and workspaces
+come from the current stream's memory: that memory may be a tensor's that was
+just freed there and is still in use by what is queued on it."""
+import pytest
+import torch
+
+from tests import cache_util as cu
+from tests.test_cache_gpu import call_step, i32, make_step, mha, on_gpu  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+SLEEP = 40_000_000   # cycles: some 20 ms, far more than a call takes
+
+
+def behind_a_reader(like, call):
+    """Calls `call` on another stream just after a tensor of `like`'s size was freed
+    on the current one, where its last reader is still waiting; returns the call's
+    result and whether that reader saw what the tensor held."""
+    torch.cuda.synchronize()
+    held = torch.full_like(like, 3.0)
+    copy = torch.zeros_like(like)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(SLEEP)
+    copy.copy_(held)
+    at = held.data_ptr()
+    del held
+    result = call(side)
+    first = result[0]
+    reused = first.data_ptr() == at
+    torch.cuda.synchronize()
+    return result, reused, bool((copy == 3.0).all())
+
+
+STEPS = [
+    ("decode_f8", (8, 1, 8, 8, 64, 200), [200, 0, 1, 127, 128, 129, 199, 60]),   # CUDA cores
+    ("decode_f8", (2, 1, 8, 2, 128, 9000), [8000, 33]),                          # splits: a workspace
+    ("tree", (2, 5, 8, 2, 128, 9000), [8000, 33]),
+    ("tree", (2, 40, 8, 2, 128, 900), [800, 33]),
+    ("tree_f8", (2, 5, 8, 2, 128, 9000), [8000, 33]),
+]
+
+
+@pytest.mark.parametrize("kind,shape,lens", STEPS, ids=lambda x: str(x) if isinstance(x, str) else "")
+@pytest.mark.parametrize("as_int", [True, False], ids=["handle", "object"])
+def test_steps_wait_for_their_memory(mha, kind, shape, lens, as_int):  # noqa: F811
+    f8, with_drafts = kind != "tree", kind != "decode_f8"
+    g = on_gpu(make_step(60, *shape, lens, None, "tree" if with_drafts else None, f8, with_drafts))
+    want = call_step(mha, g, f8, with_drafts)
+    # (a tensor of the output's size is what the allocator hands out again)
+    got, reused, kept = behind_a_reader(
+        want[0], lambda s: call_step(mha, g, f8, with_drafts, stream=s.cuda_stream if as_int else s))
+    assert mha.mha_sync_status() == 0
+    assert reused and kept
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_read_waits_for_its_memory(mha):  # noqa: F811
+    x = cu.random_rows(1, (3, 400, 4, 64))
+    codes, scales = cu.f8_cache(x)
+    dev = [codes.cuda(), codes.cuda(), scales.cuda(), scales.cuda(), i32([400, 0, 77]).cuda()]
+    want = mha.mha_cache_read_f8(*dev)
+    got, reused, kept = behind_a_reader(want[0], lambda s: mha.mha_cache_read_f8(*dev, stream=s))
+    assert mha.mha_sync_status() == 0
+    assert reused and kept
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_default_stream_from_another(mha):  # noqa: F811
+    """stream=0, the default stream, while another is current."""
+    g = on_gpu(make_step(61, 2, 1, 8, 2, 128, 9000, [8000, 33], None, None, True, False))
+    want = call_step(mha, g, True, False)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for stream in (0, torch.cuda.default_stream()):
+            got = call_step(mha, g, True, False, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert mha.mha_sync_status() == 0

@@ -434,18 +434,18 @@ def _check(index, tensors):
 
 def _call_on(index, stream, made, fn, args):
     """Calls an entry with device `index` current and its stream (the current one
-    unless given).  ``made``: tensors allocated here for the call; on a stream
-    other than the current one the allocator must not hand them out again
-    before that stream is done."""
+    unless given).  ``made``: tensors allocated here for the call, from the
+    current stream's memory.  A stream other than the current one waits for it
+    first (what was queued there may still use that memory under another name),
+    and the allocator does not hand them out again before that stream is done."""
     # (the raw handle: building a Stream object costs more than the launch)
     handle = torch._C._cuda_getCurrentRawStream(index)
     if stream is not None:
         other = stream if isinstance(stream, int) else stream.cuda_stream
         if other != handle:
             handle = other
-            other = torch.cuda.ExternalStream(handle, device=index)
-            for t in made:
-                t.record_stream(other)
+            if made:
+                _hand_over(index, stream, made)
     if torch.cuda.current_device() == index:
         rc = fn(*args, handle)
     else:
@@ -453,6 +453,18 @@ def _call_on(index, stream, made, fn, args):
             rc = fn(*args, handle)
     if rc:
         raise MhaError(rc, fn.__name__)
+
+
+def _hand_over(index, stream, made):
+    """Gives tensors of the current stream's memory to another stream (a Stream or
+    a raw handle)."""
+    if isinstance(stream, int):
+        # (ExternalStream takes handle 0, the default stream, for no stream at all)
+        stream = (torch.cuda.ExternalStream(stream, device=index) if stream
+                  else torch.cuda.default_stream(index))
+    stream.wait_stream(torch.cuda.current_stream(index))
+    for t in made:
+        t.record_stream(stream)
 
 
 def _row_strides(t, name):
@@ -536,21 +548,11 @@ def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, 
                 raise ValueError(f"{name} must have the cache's shape {tuple(shape)}")
             _check(index, ((t, name, _BF16),))
         out.append(t)
-    if made and stream is not None:
-        # the zeros are written on the current stream
-        _wait_current(k_cache.device, stream)
     k, v = out
     _call_on(index, stream, made, lib().mha_cache_read_f8,
              (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
               k.data_ptr(), v.data_ptr(), B, H, Lk, d, lens.data_ptr()))
     return k, v
-
-
-def _wait_current(device, stream):
-    """Makes ``stream`` wait for what the current stream has queued."""
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    stream.wait_stream(torch.cuda.current_stream(device))
 
 
 def _rows_call(fn, ws_fn, q, cache_shape, tensors, ptrs, lens, extra, out, scale, workspace,

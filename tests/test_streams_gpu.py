@@ -77,3 +77,40 @@ def test_default_stream_from_another(mha):  # noqa: F811
             torch.cuda.synchronize()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert mha.mha_sync_status() == 0
+
+
+def older_calls(mha):
+    """The entries that read no 8-bit cache, on small inputs: (name, call(stream))."""
+    def t(seed, *shape):
+        return cu.random_rows(seed, shape).cuda()
+
+    q, k, v, do = (t(s, 2, 96, 4, 64) for s in range(4))
+    lens = i32([96, 50]).cuda()
+    out, lse = mha.mha_fwd(q, k, v, return_lse=True)
+    f = [x.float() for x in (q, k, v)]
+    narrow, one = v[..., :32].contiguous(), q[:, 0].contiguous()
+    x, w_qkv, w_o = t(5, 2, 96, 256), t(6, 256, 3 * 256), t(7, 256, 256)
+    cache = [t(8 + i, 2, 3000, 4, 64) for i in range(2)]
+    clens = i32([3000, 1700]).cuda()
+    return {
+        "mha_fwd": lambda s: mha.mha_fwd(q, k, v, stream=s, return_lse=True),
+        "mha_fwd_dv": lambda s: mha.mha_fwd(q, k, narrow, stream=s, return_lse=True),
+        "mha_fwd_f32": lambda s: mha.mha_fwd_f32(*f, mask_kind=2, key_lens=lens, stream=s, return_lse=True),
+        "mha_bwd": lambda s: mha.mha_bwd(q, k, v, out, do, lse, stream=s),
+        "mha_layer_fwd": lambda s: (mha.mha_layer_fwd(x, w_qkv, w_o, 4, stream=s),),
+        "mha_gemm_bf16": lambda s: (mha.mha_gemm_bf16(x[0], w_qkv, stream=s),),
+        "mha_decode": lambda s: mha.mha_decode(one, *cache, clens, stream=s, return_lse=True),
+        "mha_decode_static": lambda s: mha.mha_decode_static(one, *cache, clens, stream=s, return_lse=True),
+    }
+
+
+@pytest.mark.parametrize("name", ["mha_fwd", "mha_fwd_dv", "mha_fwd_f32", "mha_bwd", "mha_layer_fwd",
+                                  "mha_gemm_bf16", "mha_decode", "mha_decode_static"])
+def test_other_entries_wait_for_their_memory(mha, name):  # noqa: F811
+    call = older_calls(mha)[name]
+    want = call(None)
+    got, _, kept = behind_a_reader(want[0], call)
+    assert mha.mha_sync_status() == 0
+    assert kept
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -67,3 +67,16 @@ def test_current_stream_waits_for_nothing(rec, stream):
 def test_callers_buffers_need_no_wait(rec):
     """With every buffer the caller's own, streams stay independent."""
     assert rec.call(9, []) == [("call", 9)]
+
+
+@pytest.mark.parametrize("handle", [9, 0])
+@pytest.mark.parametrize("as_int", [True, False], ids=["handle", "object"])
+def test_handle_of_another_stream(rec, handle, as_int):
+    """The entries that take a handle: the wait comes with it."""
+    rec.Tensor.get_device = lambda self: 0
+    stream = handle if as_int else rec.Stream(handle)
+    assert binding._stream_handle(stream, [rec.Tensor()]) == handle
+    assert rec.events == [("wait", handle, CURRENT), ("record", handle)]
+    rec.events.clear()
+    assert binding._stream_handle(stream) == handle and binding._stream_handle(CURRENT, [rec.Tensor()]) == CURRENT
+    assert rec.events == []

@@ -4,6 +4,12 @@ Argument marshalling only: every step of the attention forward runs in the
 library's CUDA kernels.  Tensors are torch tensors (device memory and streams
 come from PyTorch); their shapes are [B, L, H, d_k].  If the library has not
 been built, or cannot be loaded, every call raises: there is no fallback.
+
+``stream`` is a Stream or a raw handle (0: the default stream); the current
+stream when not given.  Outputs and workspaces that are not given come from the
+current stream's memory, so a call that makes any of them on another stream
+first makes that stream wait for the current one; inputs are the caller's to
+order.
 """
 from __future__ import annotations
 
@@ -128,12 +134,30 @@ def mha_status_string(code: int) -> str:
     return lib().mha_status_string(int(code)).decode()
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, made=()) -> int:
+    """The stream's raw handle (the current stream's when None).  ``made``: tensors
+    allocated here for the call, handed over to a stream other than the current
+    one."""
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if made and handle != torch._C._cuda_getCurrentRawStream(made[0].get_device()):
+        _hand_over(made[0].get_device(), stream, made)
+    return handle
+
+
+def _hand_over(index, stream, made):
+    """Gives tensors of the current stream's memory to another stream (a Stream or
+    a raw handle): it waits for the current stream, on which what is queued may
+    still use that memory under another name, and the allocator does not hand
+    the tensors out again before that stream is done."""
     if isinstance(stream, int):
-        return stream
-    return stream.cuda_stream
+        # (ExternalStream takes handle 0, the default stream, for no stream at all)
+        stream = (torch.cuda.ExternalStream(stream, device=index) if stream
+                  else torch.cuda.default_stream(index))
+    stream.wait_stream(torch.cuda.current_stream(index))
+    for t in made:
+        t.record_stream(stream)
 
 
 def _shape(q, k, v, allow_dv=False):
@@ -162,8 +186,10 @@ def _call_fwd(fn_name, dtype, q, k, v, out, mask_kind, key_lens, scale, stream,
     d_v = v.shape[3]
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _check_tensor(t, n, dtype, "cuda")
+    made = []
     if out is None:
         out = torch.empty((B, Lq, H, d_v), dtype=dtype, device=q.device)
+        made.append(out)
     _check_tensor(out, "out", dtype, "cuda")
     if tuple(out.shape) != (B, Lq, H, d_v):
         raise ValueError("out must be [B, Lq, H, d_v]")
@@ -178,6 +204,7 @@ def _call_fwd(fn_name, dtype, q, k, v, out, mask_kind, key_lens, scale, stream,
         if want_lse:
             if lse is None:
                 lse = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device)
+                made.append(lse)
             _check_tensor(lse, "lse", torch.float32, "cuda")
             if tuple(lse.shape) != (B, H, Lq):
                 raise ValueError("lse must be [B, H, Lq]")
@@ -185,26 +212,27 @@ def _call_fwd(fn_name, dtype, q, k, v, out, mask_kind, key_lens, scale, stream,
         rc = getattr(lib(), fn_name)(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                      lse.data_ptr() if want_lse else None, B, H, Lq, Lk, d, d_v,
                                      int(mask_kind), lens_ptr, float(scale),
-                                     _stream_handle(stream))
+                                     _stream_handle(stream, made))
         if rc != MHA_OK:
             raise MhaError(rc, fn_name)
         return (out, lse) if want_lse else out
     if not want_lse:
         rc = getattr(lib(), fn_name)(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                      B, H, Lq, Lk, d, int(mask_kind), lens_ptr, float(scale),
-                                     _stream_handle(stream))
+                                     _stream_handle(stream, made))
         if rc != MHA_OK:
             raise MhaError(rc, fn_name)
         return out
     if lse is None:
         lse = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device)
+        made.append(lse)
     _check_tensor(lse, "lse", torch.float32, "cuda")
     if tuple(lse.shape) != (B, H, Lq):
         raise ValueError("lse must be [B, H, Lq]")
     fn_name += "_lse"
     rc = getattr(lib(), fn_name)(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                  lse.data_ptr(), B, H, Lq, Lk, d, int(mask_kind), lens_ptr,
-                                 float(scale), _stream_handle(stream))
+                                 float(scale), _stream_handle(stream, made))
     if rc != MHA_OK:
         raise MhaError(rc, fn_name)
     return out, lse
@@ -239,6 +267,7 @@ def mha_bwd(q, k, v, out, dout, lse, mask_kind: int = 0, key_lens=None, scale: f
     _check_tensor(lse, "lse", torch.float32, "cuda")
     if tuple(lse.shape) != (B, H, Lq):
         raise ValueError("lse must be [B, H, Lq]")
+    given = (dq, dk, dv, workspace)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -254,10 +283,11 @@ def mha_bwd(q, k, v, out, dout, lse, mask_kind: int = 0, key_lens=None, scale: f
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     _check_tensor(workspace, "workspace", torch.uint8, "cuda")
+    made = [t for t, g in zip((dq, dk, dv, workspace), given) if g is None]
     rc = lib().mha_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                        dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                        dv.data_ptr(), B, H, Lq, Lk, d, int(mask_kind), lens_ptr, float(scale),
-                       workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+                       workspace.data_ptr(), workspace.numel(), _stream_handle(stream, made))
     if rc != MHA_OK:
         raise MhaError(rc, "mha_bwd")
     return dq, dk, dv
@@ -290,8 +320,10 @@ def mha_layer_fwd(x, w_qkv, w_o, H: int, mem=None, mask_kind: int = 0, key_lens=
         tensors.append((mem, "mem"))
     for t, n in tensors:
         _check_tensor(t, n, torch.bfloat16, "cuda")
+    made = []
     if y is None:
         y = torch.empty_like(x)
+        made.append(y)
     _check_tensor(y, "y", torch.bfloat16, "cuda")
     if tuple(y.shape) != tuple(x.shape):
         raise ValueError("y must have x's shape")
@@ -302,11 +334,12 @@ def mha_layer_fwd(x, w_qkv, w_o, H: int, mem=None, mask_kind: int = 0, key_lens=
     need = layer_workspace_bytes(B, Lq, Lk, d_model, H, d_k)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+        made.append(workspace)
     _check_tensor(workspace, "workspace", torch.uint8, "cuda")
     rc = lib().mha_layer_fwd(x.data_ptr(), mem.data_ptr() if mem is not None else None,
                              w_qkv.data_ptr(), w_o.data_ptr(), y.data_ptr(), B, Lq, Lk, d_model,
                              H, d_k, int(mask_kind), lens_ptr, float(scale), workspace.data_ptr(),
-                             workspace.numel(), _stream_handle(stream))
+                             workspace.numel(), _stream_handle(stream, made))
     if rc != MHA_OK:
         raise MhaError(rc, "mha_layer_fwd")
     return y
@@ -324,13 +357,15 @@ def mha_gemm_bf16(a, b, c=None, stream=None):
     if b.shape[0] != K:
         raise ValueError(f"inner sizes differ: a {tuple(a.shape)}, b {tuple(b.shape)}")
     N = b.shape[1]
+    made = []
     if c is None:
         c = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        made.append(c)
     if c.dim() != 2 or tuple(c.shape) != (M, N) or c.dtype != torch.bfloat16 or c.stride(1) != 1:
         raise ValueError("c must be a row-major bf16 [M, N] matrix")
     rc = lib().mha_gemm_bf16(a.data_ptr(), b.data_ptr(), c.data_ptr(), M, N, K,
                              max(a.stride(0), K), max(b.stride(0), N), max(c.stride(0), N),
-                             _stream_handle(stream))
+                             _stream_handle(stream, made))
     if rc != MHA_OK:
         raise MhaError(rc, "mha_gemm_bf16")
     return c
@@ -369,8 +404,10 @@ def mha_decode(q, k_cache, v_cache, cache_lens, out=None, scale: float = 0.0, wo
     _check_tensor(cache_lens, "cache_lens", torch.int32, "cuda")
     if tuple(cache_lens.shape) != (B,):
         raise ValueError("cache_lens must be [B]")
+    made = []
     if out is None:
         out = torch.empty_like(q)
+        made.append(out)
     _check_tensor(out, "out", torch.bfloat16, "cuda")
     if tuple(out.shape) != tuple(q.shape):
         raise ValueError("out must have q's shape")
@@ -378,6 +415,7 @@ def mha_decode(q, k_cache, v_cache, cache_lens, out=None, scale: float = 0.0, wo
     if return_lse:
         if lse is None:
             lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+            made.append(lse)
         _check_tensor(lse, "lse", torch.float32, "cuda")
         if tuple(lse.shape) != (B, H):
             raise ValueError("lse must be [B, H]")
@@ -385,20 +423,21 @@ def mha_decode(q, k_cache, v_cache, cache_lens, out=None, scale: float = 0.0, wo
     if _static:
         rc = lib().mha_decode_static(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                      out.data_ptr(), lse_ptr, B, H, Lk, d,
-                                     cache_lens.data_ptr(), float(scale), _stream_handle(stream))
+                                     cache_lens.data_ptr(), float(scale), _stream_handle(stream, made))
         if rc != MHA_OK:
             raise MhaError(rc, "mha_decode_static")
         return (out, lse) if return_lse else out
     need = decode_workspace_bytes(B, H, Lk, d)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        made.append(workspace)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         _check_tensor(workspace, "workspace", torch.uint8, "cuda")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
     rc = lib().mha_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
                           lse_ptr, B, H, Lk, d, cache_lens.data_ptr(), float(scale), ws_ptr,
-                          ws_bytes, _stream_handle(stream))
+                          ws_bytes, _stream_handle(stream, made))
     if rc != MHA_OK:
         raise MhaError(rc, "mha_decode")
     return (out, lse) if return_lse else out
@@ -434,10 +473,8 @@ def _check(index, tensors):
 
 def _call_on(index, stream, made, fn, args):
     """Calls an entry with device `index` current and its stream (the current one
-    unless given).  ``made``: tensors allocated here for the call, from the
-    current stream's memory.  A stream other than the current one waits for it
-    first (what was queued there may still use that memory under another name),
-    and the allocator does not hand them out again before that stream is done."""
+    unless given).  ``made``: tensors allocated here for the call, handed over to
+    a stream other than the current one."""
     # (the raw handle: building a Stream object costs more than the launch)
     handle = torch._C._cuda_getCurrentRawStream(index)
     if stream is not None:
@@ -453,18 +490,6 @@ def _call_on(index, stream, made, fn, args):
             rc = fn(*args, handle)
     if rc:
         raise MhaError(rc, fn.__name__)
-
-
-def _hand_over(index, stream, made):
-    """Gives tensors of the current stream's memory to another stream (a Stream or
-    a raw handle)."""
-    if isinstance(stream, int):
-        # (ExternalStream takes handle 0, the default stream, for no stream at all)
-        stream = (torch.cuda.ExternalStream(stream, device=index) if stream
-                  else torch.cuda.default_stream(index))
-    stream.wait_stream(torch.cuda.current_stream(index))
-    for t in made:
-        t.record_stream(stream)
 
 
 def _row_strides(t, name):

@@ -286,9 +286,10 @@ size_t mha_decode_static_scratch_bytes(void);
  *                 aligned, strides multiples of 8 (0: dense rows, T tokens to
  *                 a sequence), so the K and V columns of a packed projection
  *                 are read in place.
- *   start         device int32 [B], the first position of each sequence.
- *   counts        device int32 [B] or NULL (T): tokens t >= counts[b] are not
- *                 written (clamped to [0, T]).
+ *   start         device int32 [B], 4-byte aligned: the first position of each
+ *                 sequence.
+ *   counts        device int32 [B], 4-byte aligned, or NULL (T): tokens
+ *                 t >= counts[b] are not written (clamped to [0, T]).
  * A token whose position falls outside [0, Lk) is dropped; every other row of
  * the cache is left as it was.  A NaN is kept as a NaN code; infinities
  * saturate the row's scale (the attention entries want finite rows).
@@ -305,7 +306,8 @@ int mha_cache_write_f8(const void* k, const void* v, long long token_stride, lon
  * bf16: k[b, j, h] = code * 2^(s - 127), exact (a code has 4 significant bits).
  *   k, v   device bf16 [B, Lk, H, d_k], 16-byte aligned; positions from
  *          lens[b] on are left as they were.
- *   lens   device int32 [B] (clamped to [0, Lk]); required (MHA_ERR_NULL).
+ *   lens   device int32 [B], 4-byte aligned (clamped to [0, Lk]); required
+ *          (MHA_ERR_NULL).
  */
 int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                       const uint8_t* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,

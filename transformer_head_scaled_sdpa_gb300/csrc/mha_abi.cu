@@ -597,6 +597,7 @@ int mha_cache_write_f8(const void* k, const void* v, long long token_stride, lon
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !start) return MHA_ERR_NULL;
   if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
         reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) ||
+      ((reinterpret_cast<uintptr_t>(start) | reinterpret_cast<uintptr_t>(counts)) & 3u) ||
       (token_stride | seq_stride) % 8 != 0)
     return MHA_ERR_UNSUPPORTED;
   const size_t span = (static_cast<size_t>(B - 1) * seq_stride +
@@ -647,8 +648,9 @@ int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k
   if (!cache_sizes(B, H, Lk, d_k, &codes, &scales)) return MHA_ERR_SHAPE;
   if (scales == 0) return MHA_OK;
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !lens) return MHA_ERR_NULL;
-  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
-       reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u)
+  if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+        reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) ||
+      (reinterpret_cast<uintptr_t>(lens) & 3u))
     return MHA_ERR_UNSUPPORTED;
   const void* ins[5] = {k_cache, v_cache, k_scale, v_scale, lens};
   const size_t ins_b[5] = {codes, codes, scales, scales, static_cast<size_t>(B) * 4};

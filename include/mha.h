@@ -285,7 +285,8 @@ size_t mha_decode_static_scratch_bytes(void);
  *                 elements with its H * d_k values contiguous; 16-byte
  *                 aligned, strides multiples of 8 (0: dense rows, T tokens to
  *                 a sequence), so the K and V columns of a packed projection
- *                 are read in place.
+ *                 are read in place.  Rows that reach past 2^50 elements:
+ *                 MHA_ERR_SHAPE.
  *   start         device int32 [B], 4-byte aligned: the first position of each
  *                 sequence.
  *   counts        device int32 [B], 4-byte aligned, or NULL (T): tokens

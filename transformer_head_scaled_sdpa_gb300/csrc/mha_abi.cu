@@ -564,10 +564,13 @@ size_t mha_decode_static_scratch_bytes(void) { return kDecodeStaticScratchBytes;
 // 8-bit cache rows: multiples of 16 (16-byte strides for the tensor maps)
 static bool f8_width_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
 
-// The bytes of codes and of scales that a cache [B, Lk, H, d] holds.
 // Most positions of a cache, and tokens of a call: a tile past them fits an int.
 static constexpr int kMaxPositions = 0x7fffffff - 1023;
+// Elements that the strided rows of a call may span: far beyond any memory, and
+// twice their number plus any address fits 64 bits.
+static constexpr long long kMaxSpan = 1ll << 50;
 
+// The bytes of codes and of scales that a cache [B, Lk, H, d] holds.
 static bool cache_sizes(int B, int H, int Lk, int d, size_t* codes, size_t* scales) {
   const long long rows = static_cast<long long>(B) * H;
   if (Lk > kMaxPositions || rows > 0x7fffffffll || rows * Lk > (1ll << 40)) return false;
@@ -589,11 +592,13 @@ int mha_cache_write_f8(const void* k, const void* v, long long token_stride, lon
     return MHA_ERR_SHAPE;
   const long long hd = static_cast<long long>(H) * d_k;
   if (token_stride == 0) token_stride = hd;
-  if (T > 0 && token_stride > (1ll << 50) / T) return MHA_ERR_SHAPE;
+  if (T > 0 && token_stride > kMaxSpan / T) return MHA_ERR_SHAPE;
   if (seq_stride == 0) seq_stride = T * token_stride;
   if (B == 0 || T == 0 || H == 0 || Lk == 0) return MHA_OK;
-  if (token_stride < hd || token_stride > (1ll << 40) || seq_stride < hd || seq_stride > (1ll << 50))
+  if (token_stride < hd || token_stride > (1ll << 40) || seq_stride < hd || seq_stride > kMaxSpan)
     return MHA_ERR_SHAPE;
+  // (the last sequence's rows end within kMaxSpan too)
+  if (B > 1 && seq_stride > (kMaxSpan - T * token_stride) / (B - 1)) return MHA_ERR_SHAPE;
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !start) return MHA_ERR_NULL;
   if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
         reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) ||

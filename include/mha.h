@@ -96,8 +96,8 @@ typedef enum {
  *             columns); wider heads (to 256) run on a kernel of their own
  *             with 64-key tiles and Q held in tensor memory.
  *   mask_kind one of mha_mask_kind.
- *   key_lens  device pointer to B int32 values, read only when the mask
- *             includes key padding (may be NULL otherwise).
+ *   key_lens  device pointer to B int32 values, 4-byte aligned, read only when
+ *             the mask includes key padding (may be NULL otherwise).
  *   scale     multiplier of q.k (the inverse temperature; the formula page
  *             transformer-attention, section 証明, takes the divisor tau > 0);
  *             0 selects 1/sqrt(d_k).  NaN, infinite or negative values are
@@ -217,8 +217,8 @@ size_t mha_bwd_workspace_bytes(int B, int H, int Lq, int Lk, int d_k);
  *   out        device, bf16 [B, H, d_k]; must not overlap q or the caches.
  *   lse        NULL, or device float32 [B, H] receiving each row's natural-log
  *              log-sum-exp (-inf when cache_lens[b] <= 0).
- *   cache_lens device int32 [B], clamped to [0, Lk]; required (MHA_ERR_MASK
- *              when NULL).  A sequence with no key gets output 0.
+ *   cache_lens device int32 [B], 4-byte aligned, clamped to [0, Lk]; required
+ *              (MHA_ERR_MASK when NULL).  A sequence with no key gets output 0.
  *   d_k        a multiple of 8 from 8 to 256 (a head narrower than 64, 128
  *              or 256 runs on the kernel of that width with the rest of each
  *              row read as zero).  scale as in mha_fwd (0 selects 1/sqrt(d_k)).

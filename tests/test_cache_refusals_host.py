@@ -1,8 +1,8 @@
-"""Arguments of the 8-bit cache's entries that would reach the kernels as bad
-addresses: refused by the C entries before any CUDA call (the pointers are
-never dereferenced)."""
+"""Arguments that would reach the kernels as bad addresses: refused by the C
+entries before any CUDA call (the pointers are never dereferenced)."""
 import pytest
 
+from tests import test_abi_host as abi
 from tests.test_cache_host import ALIAS, COUNTS, K, SHAPE, START, UNSUP, lib, read, write  # noqa: F401
 
 
@@ -27,3 +27,12 @@ def test_strides_that_wrap(lib):  # noqa: F811
     # check for overlaps has its say
     assert write(lib, B=1, T=5, H=3, ss=far, kc=K) == ALIAS
     assert write(lib, B=2, T=1, H=1, ss=far - 64, kc=K + 2 * (far - 64)) == ALIAS
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_misaligned_lengths_of_the_other_entries(lib, off):  # noqa: F811
+    assert abi.dec(lib, lens=abi.LENS_D + off) == UNSUP
+    for fn in ("mha_fwd", "mha_fwd_f32"):
+        assert abi.fwd(lib, fn, mask=2, lens=abi.LENS + off) == UNSUP
+    assert abi.bwd(lib, mask=2, lens=abi.LENS + off) == UNSUP
+    assert abi.layer(lib, mask=2, lens=abi.LENS + off) == UNSUP

@@ -167,7 +167,8 @@ int check_args(const void* q, const void* k, const void* v, void* out, int B, in
                          (Lk > 0 ? (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v))
                                  : 0)) &
                         (align - 1);
-  if (mis) return MHA_ERR_UNSUPPORTED;
+  if (mis || (has_padding(mask_kind) && (reinterpret_cast<uintptr_t>(key_lens) & 3u)))
+    return MHA_ERR_UNSUPPORTED;
   const size_t ob = sz->o_elems * elem_bytes;
   if (overlaps(out, ob, q, sz->q_elems * elem_bytes) ||
       overlaps(out, ob, k, sz->kv_elems * elem_bytes) ||
@@ -486,7 +487,8 @@ static int decode_step(const void* q, const void* k_cache, const void* v_cache, 
                                     reinterpret_cast<uintptr_t>(v_cache))
                                  : 0)) &
                         15u;
-  if (mis || (reinterpret_cast<uintptr_t>(lse) & 3u)) return MHA_ERR_UNSUPPORTED;
+  if (mis || ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cache_lens)) & 3u))
+    return MHA_ERR_UNSUPPORTED;
   const size_t qb = static_cast<size_t>(bh) * d_k * 2;
   const size_t kb = static_cast<size_t>(cache_rows) * d_k * 2;
   const size_t lb = static_cast<size_t>(bh) * 4;
@@ -1036,9 +1038,10 @@ int mha_layer_fwd(const void* x, const void* mem, const void* w_qkv, const void*
   if (rows_q == 0) return MHA_OK;
   if (!x || !w_qkv || !w_o || !y) return MHA_ERR_NULL;
   if (has_padding(mask_kind) && !key_lens) return MHA_ERR_MASK;
-  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(mem) |
-       reinterpret_cast<uintptr_t>(w_qkv) | reinterpret_cast<uintptr_t>(w_o) |
-       reinterpret_cast<uintptr_t>(y)) & 15u)
+  if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(mem) |
+        reinterpret_cast<uintptr_t>(w_qkv) | reinterpret_cast<uintptr_t>(w_o) |
+        reinterpret_cast<uintptr_t>(y)) & 15u) ||
+      (has_padding(mask_kind) && (reinterpret_cast<uintptr_t>(key_lens) & 3u)))
     return MHA_ERR_UNSUPPORTED;
   const size_t need = mha_layer_workspace_bytes(B, Lq, Lk, d_model, H, d_k);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))

@@ -360,8 +360,10 @@ size_t mha_decode_f8_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k);
  *          chain, row t sees the drafted tokens 0 .. t.
  * A row that sees no key gets output 0 and lse -inf.  Drafted positions past
  * the capacity Lk are not seen.  Positions past the prefix and the drafted
- * tokens may hold anything; every position seen by some row of a sequence
- * must hold finite values.  T up to 256 (MHA_ERR_UNSUPPORTED beyond); other
+ * tokens, and those of drafted tokens that no row sees, may hold anything
+ * (NaN, infinities, any scale byte); a position that some row of the sequence
+ * sees must hold finite values, for the rows it is masked from too (they
+ * multiply its value by 0).  T up to 256 (MHA_ERR_UNSUPPORTED beyond); other
  * arguments, the workspace and errors as mha_decode_f8.
  * Products accumulate in float32; over a bf16 cache the weights enter the
  * product with V as two bf16 pieces (2^-15 relative).

@@ -86,3 +86,42 @@ def test_late_first_keys_with_splits(mha, f8, d, prefix):  # noqa: F811
     assert mha.last_launch_info()["kernels"] == 2
     assert mha.mha_sync_status() == 0
     check_step(case, out, lse, f8, scale=1.0, what=f"{d} features")
+
+
+HIDDEN = [
+    # B, T, H, H_kv, Lk, prefix, drafts
+    (1, 1, 2, 2, 40, [30], None),                  # the only drafted token does not see itself
+    (2, 12, 4, 2, 300, [120, 0], None),            # over a tile's border; no prefix
+    (3, 20, 4, 4, 290, [255, 40, 7], [20, 0, 13]),
+    (1, 100, 3, 3, 500, [100], None),              # over three tiles
+    (2, 200, 2, 1, 460, [250, 3], [200, 150]),     # blocks of rows; rows past the drafted tokens
+    (1, 250, 8, 2, 4000, [3700], None),            # splits
+]
+
+
+@pytest.mark.parametrize("f8,d", KINDS, ids=lambda x: str(x))
+@pytest.mark.parametrize("shape", HIDDEN, ids=lambda s: "x".join(map(str, s[:5])))
+def test_drafted_positions_no_row_sees(mha, f8, d, shape):  # noqa: F811
+    """A drafted position whose bit no row sets may hold anything: NaN and
+    infinities (8-bit: NaN codes, the largest scale byte) reach no row."""
+    B, T, H, H_kv, Lk, prefix, drafts = shape
+    hidden = np.arange(T) % 5 == 2 if T > 1 else np.array([True])
+    hidden[T // 2: T // 2 + 4] = True
+    keep = cu.tree_bits(np.random.default_rng(T), B, T)
+    words = (T + 63) // 64
+    shown = bits_of(np.tile(~hidden, (T, 1)))[0, 0].reshape(1, 1, words)
+    case = make_step(sum(shape[:5]) + d, B, T, H, H_kv, d, Lk, prefix, drafts, keep & shown, f8)
+    for b in range(B):
+        live = T if drafts is None else drafts[b]
+        for j in np.nonzero(hidden[:live])[0]:
+            at = prefix[b] + j
+            for n in ("k", "v"):
+                case[n + "_ref"][b, at] = 0.0
+                if f8:
+                    case[n + "c"].view(torch.uint8)[b, at] = 0x7F
+                    case[n + "s"][b, :, at] = 255
+                else:
+                    case[n + "c"][b, at] = float("nan") if j % 2 else float("-inf")
+    out, lse = call_step(mha, on_gpu(case), f8, True)
+    assert mha.mha_sync_status() == 0
+    check_step(case, out, lse, f8, what=f"{shape[:5]} of {d}")

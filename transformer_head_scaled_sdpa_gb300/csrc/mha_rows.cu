@@ -985,18 +985,31 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           ev = static_cast<float>(static_cast<int>(vb) - 127);
           vinv = __uint_as_float((254u - vb) << 23);
         }
-        // which of this warpgroup's rows see the key (a tile inside the prefix: all)
+        // Which of this warp's 32 keys each row sees (a tile inside the prefix: all), a
+        // row's bits to a lane: the prefix, then the row's mask words up to the last key.
+        // A key that no row of the unit sees is hidden.
+        constexpr int WINS = (NR + 31) / 32;
         const bool masked = (it.t0 + i + 1) * kKeys > it.n;
-        uint32_t sees = ~0u;
-        if (masked && key >= it.n) {
-          sees = 0;
-          if (key < k_end) {
-            const int j = key - it.n;
-            const uint64_t* words = row_mask(buf) + r0 * kMaskWords + (j >> 6);
-#pragma unroll 8
-            for (int r = 0; r < RPT; ++r)
-              sees |= static_cast<uint32_t>((words[r * kMaskWords] >> (j & 63)) & 1) << r;
+        uint32_t win = 0;  // (of row r0 / 32 * 32 + lane)
+        bool hidden = false;
+        if (masked) {
+          const int off = key - lane - it.n, x = off >> 5, left = k_end - (key - lane);
+          const uint32_t prefix = off >= 0 ? 0u : (off <= -32 ? ~0u : (1u << -off) - 1);
+          const uint32_t here = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1);
+          uint32_t any = 0;
+#pragma unroll
+          for (int a = 0; a < WINS; ++a) {
+            uint32_t w[2] = {0, 0};
+            if (lane + 32 * a < NR) {
+              const uint32_t* words = reinterpret_cast<const uint32_t*>(row_mask(buf) + (lane + 32 * a) * kMaskWords);
+              if (x >= 0 && x < 2 * kMaskWords) w[0] = words[x];
+              if (x >= -1 && x < 2 * kMaskWords - 1) w[1] = words[x + 1];
+            }
+            const uint32_t bits = (__funnelshift_r(w[0], w[1], off & 31) | prefix) & here;
+            if (a == 0 || wg == a) win = bits;
+            any |= bits;
           }
+          hidden = !((__reduce_or_sync(0xffffffffu, any) >> lane) & 1);
         }
         wait(C::S_FULL + (t & 1), (t >> 1) & 1);
         tc_fence_after();
@@ -1050,8 +1063,10 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
           }
           if (masked) {
 #pragma unroll
-            for (int r = 0; r < RPT; ++r)
-              if (!((sees >> r) & 1)) x[r] = -INFINITY;
+            for (int r = 0; r < RPT; ++r) {
+              const uint32_t row = __shfl_sync(0xffffffffu, win, (r0 + r) & 31);
+              if (!((row >> lane) & 1)) x[r] = -INFINITY;
+            }
           }
         }
         bool move = forced;
@@ -1186,15 +1201,14 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
             }
           }
         }
-        if (wg == 0 && (it.t0 + i + 1) * kKeys > k_end) {
-          // a ragged last tile: the V rows past the last key may hold anything
-          // (0 * NaN would be NaN)
-          // (a unit's last V is its last item in the ring)
-          const int before = 2 * static_cast<int>(t) + 1;
+        if (wg == 0 && masked && __any_sync(0xffffffffu, hidden)) {
+          // a hidden key's V may hold anything, and 0 * NaN would be NaN (the ring has
+          // K(0) K(1) V(0) K(2) ... V(last) of a unit)
+          const int before = 2 * static_cast<int>(t) + (i + 1 < n ? 2 : 1);
           for (int blk = 0; blk < blks; ++blk) {
             const int item = before * blks + blk, sl = item % C::SLOTS;
             wait(C::FULL + sl, (item / C::SLOTS) & 1);
-            if (key >= k_end) {
+            if (hidden) {
 #pragma unroll 1
               for (int c = 0; c < C::SLOT / C::CHUNK; ++c)
 #pragma unroll 1

@@ -59,7 +59,8 @@ struct BlockCfg {
   static constexpr int NBAR = DRAIN + 1;
   static constexpr int OFF_TMEM = OFF_MISC + 8 * NBAR;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static_assert(8 * NBAR + 8 <= 256, "barrier area");
+  static constexpr int OFF_SHOWN = OFF_MISC + 224;      // drafted keys that some row sees (256 bits)
+  static_assert(8 * NBAR + 8 <= 224, "barrier area");
   // TMEM: S_0 | S_1 (128 columns each, then P_g's two pieces) | O_0 | O_1
   static constexpr uint32_t TM_O = 256;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
   auto bar = [&](int i) { return s_base + C::OFF_MISC + 8 * i; };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+  uint32_t* shown = reinterpret_cast<uint32_t*>(smem + C::OFF_SHOWN);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int tid = static_cast<int>(threadIdx.x);
   constexpr int kMmaWarp = 16, kLoadWarp = 17;
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
       mbar_init(bar(C::O_DONE + g), 1);
     }
     mbar_init(bar(C::DRAIN), 1);
+    for (int i = 0; i < 8; ++i) shown[i] = 0;
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -293,6 +296,17 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
     if (g < tiles_m && works) {
       bool ok = true;
       auto wait = [&](int id, uint32_t parity) { ok = ok && thread_wait(bar(id), parity, abort_flag, site + id); };
+      // The mask words of the unit's rows together, for the tiles of drafted keys: a word
+      // of every 64th token to a thread (asked for ahead of Q).
+      uint64_t any = 0;
+      if (g == 0 && p.tree_mask && it.t1 * kKeys > it.n && (tid & 3) < p.words) {
+        const int first = it.rb * kBlockRows / p.G + ((kt + 128 * half) >> 2);
+        const int last = min((it.rb * kBlockRows + rows_here - 1) / p.G, it.live - 1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (first + 64 * x <= last)
+            any |= __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + first + 64 * x) * p.words + (tid & 3));
+      }
       // Q (zeros past the last row)
       {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + out_row * p.d);
@@ -311,6 +325,11 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
         }
         fence_proxy_async_smem();
         warp_arrive(bar(C::Q_FULL + g), lane);
+      }
+      if (any) {
+        // (the barrier of the first tile comes before these are read)
+        atomicOr(shown + 2 * (tid & 3), static_cast<uint32_t>(any));
+        atomicOr(shown + 2 * (tid & 3) + 1, static_cast<uint32_t>(any >> 32));
       }
       const float scale = p.scale_log2;  // (positive)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -394,17 +413,22 @@ __global__ void __launch_bounds__(BlockCfg<W>::THREADS, 1)
           tmem_st16(s_at + 32 * half + 16 * c, w1);
           tmem_st16(s_at + 64 + 32 * half + 16 * c, w2);
         }
-        if (g == 0 && key0 + kKeys > it.end) {
-          // a ragged last tile: the V rows past the last key may hold anything
-          // (0 * NaN would be NaN); the second row tile's product comes later
-          const int item = 2 * i + 1, slot = item % C::SLOTS;
-          wait(C::FULL + slot, (item / C::SLOTS) & 1);
-          if (key0 + kt >= it.end) {
+        if (g == 0 && key0 + kKeys > it.n) {
+          // V rows that no row of the unit sees may hold anything, and 0 * NaN would be
+          // NaN: those past the last key, and drafted ones whose bit no row sets; the
+          // second row tile's product comes later
+          const int key = key0 + kt, j = key - it.n;
+          const bool hidden = key >= it.end || (p.tree_mask && j >= 0 && !((shown[j >> 5] >> (j & 31)) & 1));
+          if (__any_sync(0xffffffffu, hidden)) {
+            const int item = 2 * i + 1, slot = item % C::SLOTS;
+            wait(C::FULL + slot, (item / C::SLOTS) & 1);
+            if (hidden) {
 #pragma unroll 1
-            for (int x = half * (W / 16); x < (half + 1) * (W / 16); ++x)
-              st_shared_v4(s_base + slot * C::TILE + (x >> 3) * C::CHUNK + kt * 128 + (x & 7) * 16, 0, 0, 0, 0);
+              for (int x = half * (W / 16); x < (half + 1) * (W / 16); ++x)
+                st_shared_v4(s_base + slot * C::TILE + (x >> 3) * C::CHUNK + kt * 128 + (x & 7) * 16, 0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
         }
         tmem_st_wait();
         tc_fence_before();

@@ -109,9 +109,15 @@ __device__ __forceinline__ void balance(const RowsParams& p, int lane, int* firs
 }
 
 // Up to 32 sequences of a launch with more units than can run at once go longest
-// first, so that the last units are short ones (96 key heads, 1,024 to 2,048 keys of
-// 128 features: 16 sequences in 8 bits 95.9 us and 98.2 as they come; 4 with 16 drafted
-// tokens 37.6 and 39.8; 4 with 25 over a bf16 cache 56.9 and 56.0).
+// first, so that the last units are short ones and the time does not depend on the
+// order of the batch.  us, with it and as they come in three orders:
+//   8 bits, 16 x 96 heads x 1,024 to 2,048 keys of 128       94.3   93.2 93.2 96.3
+//     4 x 96 heads with 16 drafted tokens                    36.5   35.7 36.2 42.0
+//     5 x 64 heads x 100 to 2,000 keys, 80 drafted           93.1   99.2 99.7 100
+//   bf16, 3 x 96 heads x 500 to 4,000 keys of 128, 5 drafted 55.8   58.6 58.7 60.5
+//     4 x 96 heads x 1,024 to 2,048 keys, 25 drafted         56.2   56.0 56.3 57.6
+//     rows along M, 3 x 96 heads x 500 to 4,000, 100 drafted 87.6  103.4 110.3 110.3
+//     against it: 32 x 40 heads x 30 to 1,000 keys, 8 drafted 63.6  58.7 60.2 61.1
 __device__ __forceinline__ bool longest_first(const RowsParams& p, int slots) {
   return p.n_splits == 1 && p.B > 1 && p.B <= kBalanced && static_cast<int>(gridDim.x) > slots;
 }

@@ -114,3 +114,33 @@ def test_other_entries_wait_for_their_memory(mha, name):  # noqa: F811
     assert kept
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_kernels_of_two_streams_share_the_machine(mha):  # noqa: F811
+    """Steps of every form and the forward, each stream's calls one after the other
+    and the two streams' at once: all of them want tensor memory, and each step
+    lets its stream's next launch set itself up while it runs."""
+    steps = []
+    for i, (kind, shape, lens) in enumerate(STEPS):
+        f8, with_drafts = kind != "tree", kind != "decode_f8"
+        steps.append((on_gpu(make_step(70 + i, *shape, lens, None, "tree" if with_drafts else None, f8,
+                                       with_drafts)), f8, with_drafts))
+    q, k, v = (cu.random_rows(s, (2, 128, 8, 64)).cuda() for s in range(3))
+
+    def round_of():
+        got = [x for g, f8, drafts in steps for x in call_step(mha, g, f8, drafts)]
+        return got + [mha.mha_fwd(q, k, v)]
+
+    want = round_of()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    results = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                results.append(round_of())
+    torch.cuda.synchronize()
+    assert mha.mha_sync_status() == 0
+    for got in results:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

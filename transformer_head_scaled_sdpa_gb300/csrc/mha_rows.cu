@@ -417,8 +417,9 @@ __global__ void __launch_bounds__((RowsCfg<F8, W, NR>::THREADS), (RowsCfg<F8, W,
   const uint32_t tmem = *tmem_slot;  // (not the load warp's, which did not wait)
   griddep_wait();  // global memory only from here on
   // the next launch may set itself up once every unit is taken (it waits for this
-  // grid before it touches global memory)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // grid before it touches global memory) and every CTA has its tensor memory, which
+  // the load warp does not know
+  if (warp != kLoadWarp) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const bool ordered = longest_first(p, kSms * C::MIN_BLOCKS);
   const int blks = C::BLKS == 1 ? 1 : (p.d + 127) / 128;  // 128-feature blocks in use

@@ -279,8 +279,9 @@ size_t mha_decode_static_scratch_bytes(void);
  *     e = the smallest integer >= -64 with max |x| <= 448 * 2^e,
  *     code = x * 2^-e rounded to e4m3 (nearest even),  scale byte e + 127
  * (448 is the largest e4m3 value).  The scale is a power of two: the one
- * rounding is the code's, at most 2^-4 of a value whose magnitude is at least
- * 2^-14 of the row's largest.
+ * rounding is the code's, at most 2^-4 |x| or 2^(e - 10), whichever is larger.
+ * The first decides for values of at least 2^-13 of the row's largest where that
+ * is above 2^-56 (below, e stays at -64 and small rows run out of code range).
  *   k, v          device bf16, row (b, t) at b * seq_stride + t * token_stride
  *                 elements with its H * d_k values contiguous; 16-byte
  *                 aligned, strides multiples of 8 (0: dense rows, T tokens to

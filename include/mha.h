@@ -327,12 +327,13 @@ int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k
  *              allowed when that is 0); not shared with a concurrent call.
  * The tensor cores read the codes as they are.  q enters as two e4m3 pieces
  * that give its bf16 values back (to 2^-22 of the row's largest), the weights
- * as three e5m2 pieces (2^-11 relative); products accumulate in float32.  A
- * weight is kept relative to the row's largest a_j 2^(s_j - 127) (s_j: the V
- * row's scale byte): V rows of a sequence and head whose scales differ by more
- * than 2^100 are outside this accuracy.  One or two query heads per key head
- * over a short cache (Lk * d_k * H / H_kv <= 16384) are computed in float32
- * on the CUDA cores.
+ * as three e5m2 pieces (2^-11 relative, and no closer than 2^-27 of the row's
+ * largest); products and the denominator's float32 weights accumulate in
+ * float32.  A weight is kept relative to the row's largest a_j 2^(s_j - 127)
+ * (s_j: the V row's scale byte): V rows of a sequence and head whose scales
+ * differ by more than 2^100 are outside this accuracy.  One or two query heads
+ * per key head over a short cache (Lk * d_k * H / H_kv <= 16384) are computed
+ * in float32 on the CUDA cores.
  */
 int mha_decode_f8(const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                   const uint8_t* v_scale, void* out, float* lse, int B, int H, int H_kv, int Lk,
@@ -354,8 +355,9 @@ size_t mha_decode_f8_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k);
  *   prefix_lens  device int32 [B], clamped to [0, Lk]; required
  *          (MHA_ERR_MASK when NULL): the positions every drafted token sees.
  *   draft_lens   device int32 [B] or NULL (T): drafted tokens of a sequence,
- *          clamped to [0, T].  Rows t >= draft_lens[b] get output 0 and lse
- *          -inf, and their keys are seen by no row.
+ *          clamped to [0, T].  Rows t >= draft_lens[b] (whose q may hold
+ *          anything) get output 0 and lse -inf, and their keys are seen by no
+ *          row.
  *   tree_mask    device uint64 [B, T, ceil(T / 64)] or NULL: row t sees
  *          drafted token j when bit j % 64 of word j / 64 is set.  NULL: a
  *          chain, row t sees the drafted tokens 0 .. t.

@@ -125,3 +125,39 @@ def test_drafted_positions_no_row_sees(mha, f8, d, shape):  # noqa: F811
     out, lse = call_step(mha, on_gpu(case), f8, True)
     assert mha.mha_sync_status() == 0
     check_step(case, out, lse, f8, what=f"{shape[:5]} of {d}")
+
+
+@pytest.mark.parametrize("f8,d", KINDS, ids=lambda x: str(x))
+@pytest.mark.parametrize("shape", [(3, 7, 4, 2, 200), (2, 100, 2, 2, 500), (3, 40, 8, 2, 9000)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_rows_past_the_drafted_tokens_hold_anything(mha, f8, d, shape):  # noqa: F811
+    """A padded batch: the queries of rows past draft_lens (NaN, the largest values)
+    and their mask words reach no other row."""
+    B, T, H, H_kv, Lk = shape
+    drafts = [T - 3, 0, T][:B]
+    case = make_step(B + T, B, T, H, H_kv, d, Lk, [Lk - T, 5, 40][:B], drafts, "tree", f8)
+    for b, live in enumerate(drafts):
+        case["q"][b, live:] = torch.tensor([float("nan"), float("inf"), 3e38, -3e38]).to(
+            torch.bfloat16).repeat(d // 4)
+        case["mask"][b, live:] = -1
+    g = on_gpu(case)
+    out, lse = call_step(mha, g, f8, True)
+    assert mha.mha_sync_status() == 0
+    for b, live in enumerate(drafts):
+        case["q"][b, live:] = 0.0
+    check_step(case, out, lse, f8, what=f"{shape} of {d}")
+
+
+def test_nothing_to_do(mha):  # noqa: F811
+    """No sequence, no token: nothing is launched, and shapes come back."""
+    for B, T in ((0, 3), (2, 0)):
+        case = make_step(1, B, T, 4, 2, 64, 30, [5] * B, None, None, True)
+        g = on_gpu(case)
+        for f8 in (True, False):
+            if not f8:
+                g["kc"], g["vc"] = (torch.zeros((B, 30, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+            out, lse = call_step(mha, g, f8, True)
+            assert out.shape == (B, T, 4, 64) and lse.shape == (B, 4, T)
+        k = torch.zeros((B, T, 2, 64), dtype=torch.bfloat16, device="cuda")
+        mha.mha_cache_write_f8(k, k, *(on_gpu(case)[n] for n in ("kc", "vc", "ks", "vs")), g["prefix"])
+    assert mha.mha_sync_status() == 0

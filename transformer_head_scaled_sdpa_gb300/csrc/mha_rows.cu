@@ -47,11 +47,11 @@
 // and block the fastest: CTAs that run together read the rows of neighbouring
 // heads, which lie side by side in the cache, and the same rows for their blocks
 // (one head's rows alone are 128-byte pieces of DRAM pages: 161 us for 16
-// sequences x 96 heads x 2048 keys of 128 features in 8 bits when a CTA's work ran
-// over consecutive heads, against 110).  rows_plan says how many splits there are,
-// `balance` how they fall on the sequences of a ragged batch.  The grid has a CTA
-// per unit, but CTAs are persistent: a running CTA cancels CTAs that have not
-// started (cluster launch control) and takes their units, so the launch order
+// sequences x 96 heads x 1,024 to 2,048 keys of 128 features in 8 bits when a CTA's
+// work ran over consecutive heads, against 110).  rows_plan says how many splits
+// there are, `balance` how they fall on the sequences of a ragged batch.  The grid
+// has a CTA per unit, but CTAs are persistent: a running CTA cancels CTAs that have
+// not started (cluster launch control) and takes their units, so the launch order
 // balances the work (with equal static shares of the keys CTAs ended 25 % apart).
 // A split of a sequence that has several leaves a partial (o, m, l) in the
 // workspace, and rows_combine_kernel merges them exactly.
@@ -66,9 +66,9 @@
 // the loads of a whole ring, run during a unit's epilogue.  Every wait is bounded
 // (abort flag, MHA_ERR_TIMEOUT).
 //
-// What bounds it (16 x 96 heads x 2,048 keys of 128 features in 8 bits, 610 MB): 95
-// us, 6.4 TB/s, 0.95 of the measured copy; with 16 rows and 4 sequences 36 us, 4.4
-// TB/s: the softmax threads' instructions (30 per weight: three pieces) and 384 units
+// What bounds it (16 x 96 heads x 1,024 to 2,048 keys of 128 features in 8 bits, 610
+// MB): 94 us, 6.5 TB/s, 0.95 of the measured copy; with 16 rows and 4 sequences (157
+// MB) 36.5 us, 4.3 TB/s: the softmax threads' instructions (30 per weight: three pieces) and 384 units
 // on 304 CTAs.  A unit costs five tiles of 128 keys beside its own (Q, the first
 // maxima, the epilogue).  Code that runs for the first time costs some 30 cycles an
 // instruction, so what a CTA runs before its first weights (10 to 20 thousand cycles)
@@ -116,14 +116,14 @@ struct RowsCfg {
       TM_USED <= 32 ? 32 : (TM_USED <= 64 ? 64 : (TM_USED <= 128 ? 128 : (TM_USED <= 256 ? 256 : 512)));
   static_assert(TM_USED <= 512, "TMEM budget");
   // Two CTAs per SM when each can hold two tiles' worth of ring, else one with a deep
-  // ring: one works while the other waits (16 x 96 heads x 2,048 keys in 8 bits 99 us,
-  // one CTA 110; with 16 drafted tokens, 4 sequences, 40 and 48; 12 drafted tokens over
-  // 32 x 8 heads x 300 keys of 64 features in bf16 9.3 and 13.5).
+  // ring: one works while the other waits (8 bits, 96 heads x 1,024 to 2,048 keys: 16
+  // sequences 99 us, one CTA 110; 4 with 16 drafted tokens 40 and 48; bf16, 64 features,
+  // 32 x 8 heads x 30 to 280 keys with 12 drafted tokens 9.3 and 13.5).
   static constexpr int SLOTS2 = (115712 - FIXED) / SLOT;
   static constexpr bool TWO = SLOTS2 >= (BLKS == 1 ? 4 : 5) && NR <= 32 && TMEM_COLS <= 256;
   // Softmax warpgroups: two from 16 rows on, 32 where the CTA has the SM to itself (16
-  // drafted tokens over 4 x 96 heads x 2,048 keys in 8 bits 40 us with two and 43 with
-  // one; four of them for 64 rows of a bf16 cache 107 and 104, for 32 rows of 256
+  // drafted tokens over 4 x 96 heads x 1,024 to 2,048 keys in 8 bits 40 us with two and
+  // 43 with one; four of them for 64 rows of a bf16 cache 107 and 104, for 32 rows of 256
   // features in 8 bits 47.1 and 46.5).
   static constexpr int WGS = NR <= 8 || (NR <= 16 && !TWO) ? 1 : 2;
   static constexpr int RPT = NR / WGS;                   // rows per softmax thread
@@ -1448,9 +1448,9 @@ cudaError_t launch_rows_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo
 
 // Calls f with the kernel's configuration for R rows per key head of d features.  Rows
 // beyond R cost their weights all the same (8 bits, 128 features: one row over 16 x 96
-// heads x 2,048 keys 94.5 us in units of four and 95.4 of eight, four over 2 x 8 x 64k
-// 42.2 and 43.2; bf16, 64 features: four over 128 x 8 heads x 250 keys 25 us in units
-// of eight and 27 of sixteen; wider heads, one CTA per SM, the same in both).
+// heads x 1,024 to 2,048 keys 94.5 us in units of four and 95.4 of eight, four over 2 x
+// 8 x 40k to 65k 42.2 and 43.2; bf16, 64 features: four over 128 x 8 heads x 250 keys 25
+// us in units of eight and 27 of sixteen; wider heads, one CTA per SM, the same in both).
 template <typename F>
 void with_config(bool f8, int d, int R, F&& f) {
   if (f8 && d <= 128) {
@@ -1483,11 +1483,17 @@ void with_config(bool f8, int d, int R, F&& f) {
 //   More than 64 rows over a bf16 cache: along M (3 x 8 key heads x 16,000 keys of
 //   128 features: 60 rows 56 us along N and 58 along M, 96 rows 68 and 58, 128 rows
 //   68 and 60; 64 rows of 8 blocks: 566 and 269 at 2,048 rows x 32,000 keys).
-//   A row or two over a short 8-bit cache: the CUDA cores (features x keys of the
-//   cache, full: 128 x 8 heads 64 x 64 13 us here and 25 on the tensor cores, 64 x
-//   256 17 and 23, half full 8.5 and 23; 64 x 512 27 and 29; 16 x 96 heads 128 x 128
-//   25 and 25, 128 x 256 39 and 33; 1 x 8 heads 64 x 128 9 and 11, 64 x 256 13 and 11;
-//   two rows, 128 x 8 heads 64 x 128 19 and 21).
+//   A row or two over a short 8-bit cache: the CUDA cores.  us there and on the tensor
+//   cores, calls of a graph that read from DRAM, features x keys of full caches:
+//     128 x 8 heads   64 x 64  5.7 and 16.1    64 x 256 10.8 and 17.0 (16 to 256 keys
+//                     9.2 and 17.6)            64 x 512 17.3 and 21.2
+//     16 x 96 heads   128 x 128 16.5 and 19.4  128 x 256 28.3 and 22.4
+//     16 x 8 heads    64 x 256 7.2 and 6.1
+//     1 x 8 heads     64 x 128 3.2 and 4.6     64 x 256 4.6 and 5.0
+//     32 x 4 heads    256 x 64 6.4 and 7.0
+//     128 x 8 key heads of two rows            64 x 128 11.1 and 14.6
+//   One border for any width and number of heads (keys x features x rows): narrow heads
+//   just past it would gain 4 us here, a hundred heads at its end 1 us there.
 RowsForm rows_form(bool f8, int d, int T, int G, int Lk) {
   if (!f8 && d <= 128 && T * G > 64) return kRowsBlock;
   if (f8 && T == 1 && G <= kShortRows && static_cast<long long>(Lk) * d * G <= kShortWork) return kRowsShort;

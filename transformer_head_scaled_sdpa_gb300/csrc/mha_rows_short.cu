@@ -14,7 +14,8 @@
 // Work per pair of codes: one conversion to two halves, two to float32, two fused
 // multiply-adds per row, so the arithmetic of 128 x 8 heads x 136 keys (mean) of 64
 // features is about 1 us spread over the machine: latency (lengths, keys, merge)
-// bounds it, 8.5 us where the tensor cores' form takes 23 and the bytes alone 2.7.
+// bounds it, 9.2 us from DRAM (7.4 with the cache in L2) where the tensor cores' form
+// takes 17.6 and the bytes alone 2.7.
 #include <cuda_bf16.h>
 
 #include "fp8.cuh"
@@ -39,7 +40,8 @@ __device__ __forceinline__ void codes_to_float(uint32_t x, float* y) {
 template <int GS, int NR>
 __global__ void __launch_bounds__(32 * kShortWarps) rows_short_kernel(const __grid_constant__ RowsParams p) {
   // Keys in flight per group of lanes: more cost registers, and with them CTAs per SM
-  // (128 x 8 heads, 16 to 256 keys of 64 features: one 9.0 us, two 8.5, four 9.8).
+  // (from DRAM, 64 features: 128 x 8 heads x 16 to 256 keys one 9.8 us, two 9.2, four
+  // 11.1; 1 x 8 heads x 256 keys 4.8, 4.6 and 4.3).
   constexpr int STEP = 2;
   constexpr int GROUPS = 32 / GS;      // keys side by side in a warp
   constexpr int KEYS = kShortWarps * GROUPS;

@@ -384,6 +384,123 @@ int mha_decode_tree_f8(const void* q, const void* k_cache, const void* v_cache,
 size_t mha_decode_tree_f8_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k);
 
 /*
+ * The 4-bit key/value cache: a quarter of a bf16 cache's bytes.  Not from the
+ * pages; its format is this library's definition.
+ *   k_cache, v_cache  [B, Lk, H, d_k / 2] bytes, 16-byte aligned: two 4-bit codes
+ *                     each, feature 2 i in the low four bits of byte i, 2 i + 1
+ *                     in the high ones.
+ *   k_scale, v_scale  [B, H, Lk, 2] bf16, 4-byte aligned: per position and head
+ *                     the row's offset and step; code c stands for
+ *                     offset + c * step.
+ *   d_k               a multiple of 32 from 32 to 256.
+ *   Lk                as the 8-bit cache.
+ *
+ * mha_cache_write_q4 -- quantises T new rows per sequence into the cache.  Row
+ * x = k[b, t, h] (v likewise) goes to position start[b] + t as
+ *     offset = min x
+ *     step = the smallest bf16 number >= (max x - min x) / 15, 2^-13 max |x|
+ *            and 2^-60
+ *     code = the integer nearest to (x - offset) / step, a tie to the lower
+ * all three decided exactly.  A value comes back to half a step.  A row that
+ * holds a NaN or an infinity, or whose spread max x - min x passes float32's
+ * range, gets offset NaN and codes 0 (the attention entries want finite rows).
+ * Other arguments, and what is dropped or left as it was, as
+ * mha_cache_write_f8.
+ */
+int mha_cache_write_q4(const void* k, const void* v, long long token_stride, long long seq_stride,
+                       void* k_cache, void* v_cache, void* k_scale, void* v_scale, int B, int T,
+                       int H, int Lk, int d_k, const int32_t* start, const int32_t* counts,
+                       void* stream);
+
+/*
+ * mha_cache_read_q4 -- the first lens[b] positions of a 4-bit cache as bf16:
+ * offset + code * step in float32, rounded to bf16.  Arguments as
+ * mha_cache_read_f8.
+ */
+int mha_cache_read_q4(const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,
+                      const int32_t* lens, void* stream);
+
+/*
+ * mha_decode_q4, mha_decode_tree_q4 -- mha_decode_f8 and mha_decode_tree_f8 over
+ * a 4-bit cache: the same steps, arguments, workspaces and errors, caches and
+ * scales as mha_cache_write_q4 writes them with H_kv heads (H_kv * d_k below
+ * 2^32, MHA_ERR_SHAPE).  The values attended to are offset + code * step
+ * themselves, not rounded to bf16.
+ * The tensor cores multiply the codes; a key's offset and step are applied to its
+ * scores and weights in float32.  q enters in fp16, scaled by a power of two (to
+ * 2^-39 of the row's largest), the weights in fp16 (2^-12 relative, and no closer
+ * than 2^-33 of the row's largest); products and the denominator's float32
+ * weights accumulate in float32.  A weight is kept relative to the row's
+ * largest a_j step_j (step_j: the V row's): V rows of a sequence and head whose
+ * steps differ by more than 2^100 are outside this accuracy.
+ */
+int mha_decode_q4(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                  const void* v_scale, void* out, float* lse, int B, int H, int H_kv, int Lk,
+                  int d_k, const int32_t* cache_lens, float scale, void* workspace,
+                  size_t workspace_bytes, void* stream);
+size_t mha_decode_q4_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k);
+int mha_decode_tree_q4(const void* q, const void* k_cache, const void* v_cache,
+                       const void* k_scale, const void* v_scale, void* out, float* lse,
+                       int B, int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
+                       const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t mha_decode_tree_q4_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k);
+
+/* What a cache's rows are kept as. */
+typedef enum {
+    MHA_CACHE_BF16 = 0, /* [B, Lk, H, d_k] bf16, no scales (d_k as mha_decode) */
+    MHA_CACHE_F8 = 1,   /* as mha_cache_write_f8 writes them */
+    MHA_CACHE_Q4 = 2    /* as mha_cache_write_q4 writes them */
+} mha_cache_format;
+
+/*
+ * mha_cache_fork -- sequences of a cache go on with others' rows, in place:
+ *     row (b, j) := row (parent[b], j) as it was before the call,
+ *     first[b] <= j < lens[b], for keys, values and scales.
+ * Beam search keeps the best continuations (four, cookipedia article, section
+ * "Transformer 全体"); a beam that is dropped takes over the cache of one that
+ * goes on.  Any parents do, each other's too.
+ *   k_cache, v_cache, k_scale, v_scale   a cache of this format, 16-byte aligned
+ *              (the 4-bit scales 4-byte); overlapping neither each other nor the
+ *              arrays below (MHA_ERR_ALIAS).  The scales of MHA_CACHE_BF16 are
+ *              not looked at.
+ *   format     one of mha_cache_format (MHA_ERR_UNSUPPORTED).
+ *   parent     device int32 [B]: the sequence that b's rows come from; b itself,
+ *              or a number outside [0, B), leaves b as it is.
+ *   first      device int32 [B] or NULL (0): the first position that moves (what
+ *              came before is the same in both); below 0 counts as 0.
+ *   lens       device int32 [B]: positions that b holds, clamped to Lk.  Others
+ *              are left as they were.
+ *   B          up to 1024 (MHA_ERR_UNSUPPORTED beyond).
+ * Arrays are 4-byte aligned.  Returns MHA_OK once enqueued, MHA_ERR_SHAPE,
+ * MHA_ERR_NULL, MHA_ERR_UNSUPPORTED or MHA_ERR_ALIAS.
+ */
+int mha_cache_fork(void* k_cache, void* v_cache, void* k_scale, void* v_scale, int format, int B,
+                   int H, int Lk, int d_k, const int32_t* parent, const int32_t* first,
+                   const int32_t* lens, void* stream);
+
+/*
+ * mha_cache_compact -- the accepted tokens of a tree step move next to the
+ * prefix, in place:
+ *     row (b, prefix_lens[b] + i) := row (b, prefix_lens[b] + path[b, i]) as it
+ *     was before the call, 0 <= i < path_lens[b], for keys, values and scales.
+ * After mha_decode_tree (over any of the caches) the sequence goes on with
+ * path_lens[b] more tokens: the new prefix is prefix_lens[b] + path_lens[b].
+ *   prefix_lens  device int32 [B], clamped to [0, Lk]: as the step's.
+ *   path       device int32 [B, T]: numbers of drafted tokens, in any order.  A
+ *              number outside [0, T), or a position past Lk on either side,
+ *              leaves row i as it is.
+ *   path_lens  device int32 [B] or NULL (T), clamped to [0, T].
+ *   T          up to 256 (MHA_ERR_UNSUPPORTED beyond).
+ * The rows moved from, where they are not moved to, stay as they were.  Other
+ * arguments and errors as mha_cache_fork (B without its limit).
+ */
+int mha_cache_compact(void* k_cache, void* v_cache, void* k_scale, void* v_scale, int format, int B,
+                      int T, int H, int Lk, int d_k, const int32_t* prefix_lens,
+                      const int32_t* path, const int32_t* path_lens, void* stream);
+
+/*
  * mha_layer_fwd -- one multi-head attention layer ("Attention Is All You
  * Need", Section 3.2.2):
  *     y = MultiHead(x, m, m) = Concat(head_1, ..., head_H) W^O,

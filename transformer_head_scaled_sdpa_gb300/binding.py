@@ -96,17 +96,25 @@ def lib():
             h.mha_decode_static_scratch_bytes.argtypes = []
             h.mha_decode_workspace_bytes.restype = ctypes.c_size_t
             h.mha_decode_workspace_bytes.argtypes = [_c_i] * 4
-            h.mha_cache_write_f8.restype = _c_i
-            h.mha_cache_write_f8.argtypes = [_c_p] * 2 + [ctypes.c_longlong] * 2 + [_c_p] * 4 + \
-                [_c_i] * 5 + [_c_p] * 3
-            h.mha_cache_read_f8.restype = _c_i
-            h.mha_cache_read_f8.argtypes = [_c_p] * 6 + [_c_i] * 4 + [_c_p] * 2
-            h.mha_decode_f8.restype = _c_i
-            h.mha_decode_f8.argtypes = [_c_p] * 7 + [_c_i] * 5 + [_c_p, ctypes.c_float, _c_p,
-                                                                  ctypes.c_size_t, _c_p]
-            h.mha_decode_f8_workspace_bytes.restype = ctypes.c_size_t
-            h.mha_decode_f8_workspace_bytes.argtypes = [_c_i] * 5
-            for name, n_ptr in (("mha_decode_tree", 5), ("mha_decode_tree_f8", 7)):
+            for kind in ("f8", "q4"):
+                write, read = getattr(h, "mha_cache_write_" + kind), getattr(h, "mha_cache_read_" + kind)
+                write.restype = _c_i
+                write.argtypes = [_c_p] * 2 + [ctypes.c_longlong] * 2 + [_c_p] * 4 + [_c_i] * 5 + [_c_p] * 3
+                read.restype = _c_i
+                read.argtypes = [_c_p] * 6 + [_c_i] * 4 + [_c_p] * 2
+                decode = getattr(h, "mha_decode_" + kind)
+                decode.restype = _c_i
+                decode.argtypes = [_c_p] * 7 + [_c_i] * 5 + [_c_p, ctypes.c_float, _c_p,
+                                                             ctypes.c_size_t, _c_p]
+                need = getattr(h, f"mha_decode_{kind}_workspace_bytes")
+                need.restype = ctypes.c_size_t
+                need.argtypes = [_c_i] * 5
+            h.mha_cache_fork.restype = _c_i
+            h.mha_cache_fork.argtypes = [_c_p] * 4 + [_c_i] * 5 + [_c_p] * 4
+            h.mha_cache_compact.restype = _c_i
+            h.mha_cache_compact.argtypes = [_c_p] * 4 + [_c_i] * 6 + [_c_p] * 4
+            for name, n_ptr in (("mha_decode_tree", 5), ("mha_decode_tree_f8", 7),
+                                ("mha_decode_tree_q4", 7)):
                 getattr(h, name).restype = _c_i
                 getattr(h, name).argtypes = [_c_p] * n_ptr + [_c_i] * 6 + [_c_p] * 3 + \
                     [ctypes.c_float, _c_p, ctypes.c_size_t, _c_p]
@@ -444,7 +452,7 @@ def mha_decode(q, k_cache, v_cache, cache_lens, out=None, scale: float = 0.0, wo
 
 
 # ---------------------------------------------------------------------------
-# the 8-bit cache, and steps of a few rows per sequence over a cache
+# the 8-bit and the 4-bit cache, and steps of a few rows per sequence over a cache
 # ---------------------------------------------------------------------------
 _BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
                                 torch.uint8)
@@ -507,16 +515,16 @@ def _row_strides(t, name):
     return token, seq
 
 
-def _cache_shape(k_cache, v_cache, k_scale, v_scale):
-    """Checks the shapes of an 8-bit cache; returns (B, Lk, H, d)."""
+def _cache_shape(k_cache, v_cache, k_scale, v_scale, q4=False):
+    """Checks the shapes of an 8-bit or a 4-bit cache; returns (B, Lk, H, d)."""
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} "
-                         "must be [B, Lk, H, d_k] alike")
-    scales = (shape[0], shape[2], shape[1])
+                         f"must be [B, Lk, H, {'d_k / 2' if q4 else 'd_k'}] alike")
+    scales = (shape[0], shape[2], shape[1], 2) if q4 else (shape[0], shape[2], shape[1])
     if k_scale.shape != scales or v_scale.shape != scales:
-        raise ValueError(f"k_scale and v_scale must be [B, H, Lk] = {scales}")
-    return shape
+        raise ValueError(f"k_scale and v_scale must be [B, H, Lk{', 2' if q4 else ''}] = {scales}")
+    return (*shape[:3], 2 * shape[3]) if q4 else shape
 
 
 def _lens(t, name, B):
@@ -525,13 +533,14 @@ def _lens(t, name, B):
     return (t, name, _I32)
 
 
-def mha_cache_write_f8(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=None, stream=None):
-    """Quantises new rows k, v [B, T, H, d] (bf16; rows of a packed projection
-    are read in place) into the 8-bit cache at positions start[b] .. : codes
-    k_cache, v_cache [B, Lk, H, d] (float8_e4m3fn), biased exponents k_scale,
-    v_scale [B, H, Lk] (uint8).  ``counts`` [B] limits the tokens of a
-    sequence; positions outside the cache are dropped."""
-    B, Lk, H, d = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+def _cache_tensors(k_cache, v_cache, k_scale, v_scale, q4):
+    codes, scales = (_U8, _BF16) if q4 else (_F8, _U8)
+    return ((k_cache, "k_cache", codes), (v_cache, "v_cache", codes), (k_scale, "k_scale", scales),
+            (v_scale, "v_scale", scales))
+
+
+def _cache_write(fn, q4, k, v, k_cache, v_cache, k_scale, v_scale, start, counts, stream):
+    B, Lk, H, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, q4)
     shape = k.shape
     if len(shape) != 4 or shape[0] != B or shape[2] != H or shape[3] != d or v.shape != shape:
         raise ValueError(f"k {tuple(shape)} and v {tuple(v.shape)} must be [B, T, H, d_k] of "
@@ -540,28 +549,23 @@ def mha_cache_write_f8(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=N
     if _row_strides(v, "v") != strides:
         raise ValueError("k and v must have the same strides")
     index = k_cache.get_device()
-    _check(index, ((k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8), (k_scale, "k_scale", _U8),
-                   (v_scale, "v_scale", _U8), _lens(start, "start", B)))
+    _check(index, (*_cache_tensors(k_cache, v_cache, k_scale, v_scale, q4), _lens(start, "start", B)))
     if counts is not None:
         _check(index, (_lens(counts, "counts", B),))
     for t, name in ((k, "k"), (v, "v")):
         if t.dtype is not _BF16 or t.get_device() != index:
             _refuse(t, name, _BF16, index)
-    _call_on(index, stream, (), lib().mha_cache_write_f8,
+    _call_on(index, stream, (), fn,
              (k.data_ptr(), v.data_ptr(), *strides, k_cache.data_ptr(), v_cache.data_ptr(),
               k_scale.data_ptr(), v_scale.data_ptr(), B, shape[1], H, Lk, d, start.data_ptr(),
               counts.data_ptr() if counts is not None else None))
 
 
-def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, stream=None):
-    """The first lens[b] positions of an 8-bit cache as bf16: returns (k, v)
-    [B, Lk, H, d].  Positions from lens[b] on keep what ``k`` and ``v`` held
-    (0 when they are allocated here)."""
-    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+def _cache_read(fn, q4, k_cache, v_cache, k_scale, v_scale, lens, k, v, stream):
+    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale, q4)
     B, Lk, H, d = shape
     index = k_cache.get_device()
-    _check(index, ((k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8), (k_scale, "k_scale", _U8),
-                   (v_scale, "v_scale", _U8), _lens(lens, "lens", B)))
+    _check(index, (*_cache_tensors(k_cache, v_cache, k_scale, v_scale, q4), _lens(lens, "lens", B)))
     made = []
     out = []
     for t, name in ((k, "k"), (v, "v")):
@@ -570,14 +574,51 @@ def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, 
             made.append(t)
         else:
             if t.shape != shape:
-                raise ValueError(f"{name} must have the cache's shape {tuple(shape)}")
+                raise ValueError(f"{name} must have the shape [B, Lk, H, d_k] = {tuple(shape)}")
             _check(index, ((t, name, _BF16),))
         out.append(t)
     k, v = out
-    _call_on(index, stream, made, lib().mha_cache_read_f8,
+    _call_on(index, stream, made, fn,
              (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
               k.data_ptr(), v.data_ptr(), B, H, Lk, d, lens.data_ptr()))
     return k, v
+
+
+def mha_cache_write_f8(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=None, stream=None):
+    """Quantises new rows k, v [B, T, H, d] (bf16; rows of a packed projection
+    are read in place) into the 8-bit cache at positions start[b] .. : codes
+    k_cache, v_cache [B, Lk, H, d] (float8_e4m3fn), biased exponents k_scale,
+    v_scale [B, H, Lk] (uint8).  ``counts`` [B] limits the tokens of a
+    sequence; positions outside the cache are dropped."""
+    _cache_write(lib().mha_cache_write_f8, False, k, v, k_cache, v_cache, k_scale, v_scale, start,
+                 counts, stream)
+
+
+def mha_cache_write_q4(k, v, k_cache, v_cache, k_scale, v_scale, start, counts=None, stream=None):
+    """Quantises new rows k, v [B, T, H, d] (bf16; rows of a packed projection
+    are read in place) into the 4-bit cache at positions start[b] .. : packed
+    codes k_cache, v_cache [B, Lk, H, d / 2] (uint8, feature 2 i in the low four
+    bits of byte i), offsets and steps k_scale, v_scale [B, H, Lk, 2] (bf16; code
+    c stands for offset + c * step).  ``counts`` [B] limits the tokens of a
+    sequence; positions outside the cache are dropped."""
+    _cache_write(lib().mha_cache_write_q4, True, k, v, k_cache, v_cache, k_scale, v_scale, start,
+                 counts, stream)
+
+
+def mha_cache_read_f8(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, stream=None):
+    """The first lens[b] positions of an 8-bit cache as bf16: returns (k, v)
+    [B, Lk, H, d].  Positions from lens[b] on keep what ``k`` and ``v`` held
+    (0 when they are allocated here)."""
+    return _cache_read(lib().mha_cache_read_f8, False, k_cache, v_cache, k_scale, v_scale, lens, k,
+                       v, stream)
+
+
+def mha_cache_read_q4(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, stream=None):
+    """The first lens[b] positions of a 4-bit cache as bf16 (offset + code * step,
+    rounded): returns (k, v) [B, Lk, H, d].  Positions from lens[b] on keep what
+    ``k`` and ``v`` held (0 when they are allocated here)."""
+    return _cache_read(lib().mha_cache_read_q4, True, k_cache, v_cache, k_scale, v_scale, lens, k,
+                       v, stream)
 
 
 def _rows_call(fn, ws_fn, q, cache_shape, tensors, ptrs, lens, extra, out, scale, workspace,
@@ -630,6 +671,29 @@ def decode_tree_f8_workspace_bytes(B, T, H, H_kv, Lk, d_k) -> int:
     return int(lib().mha_decode_tree_f8_workspace_bytes(B, T, H, H_kv, Lk, d_k))
 
 
+def decode_q4_workspace_bytes(B, H, H_kv, Lk, d_k) -> int:
+    return int(lib().mha_decode_q4_workspace_bytes(B, H, H_kv, Lk, d_k))
+
+
+def decode_tree_q4_workspace_bytes(B, T, H, H_kv, Lk, d_k) -> int:
+    return int(lib().mha_decode_tree_q4_workspace_bytes(B, T, H, H_kv, Lk, d_k))
+
+
+def _decode(fn, ws_fn, q4, q, k_cache, v_cache, k_scale, v_scale, cache_lens, out, scale, workspace,
+            stream, return_lse, lse):
+    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[1] != 1):
+        raise ValueError("q must be [B, H, d] or [B, 1, H, d]")
+    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale, q4)
+    B, Lk, H_kv, d = shape
+    H = q.shape[-2]
+    return _rows_call(
+        fn, ws_fn, q, shape,
+        ((q, "q", _BF16), *_cache_tensors(k_cache, v_cache, k_scale, v_scale, q4),
+         _lens(cache_lens, "cache_lens", B)),
+        (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()),
+        cache_lens, (), out, scale, workspace, stream, return_lse, lse, (B, H, H_kv, Lk, d), (B, H))
+
+
 def mha_decode_f8(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, scale: float = 0.0,
                   workspace=None, stream=None, return_lse: bool = False, lse=None):
     """One decode step over an 8-bit cache: q [B, H, d] (or [B, 1, H, d], bf16)
@@ -638,18 +702,18 @@ def mha_decode_f8(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, s
     query head h reads key head h // (H / H_kv).  Returns out (q's shape), or
     (out, lse) with ``return_lse`` (lse [B, H]).  ``workspace`` (uint8 CUDA
     tensor) is allocated when not given."""
-    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[1] != 1):
-        raise ValueError("q must be [B, H, d] or [B, 1, H, d]")
-    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale)
-    B, Lk, H_kv, d = shape
-    H = q.shape[-2]
     h = lib()
-    return _rows_call(
-        h.mha_decode_f8, h.mha_decode_f8_workspace_bytes, q, shape,
-        ((q, "q", _BF16), (k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8),
-         (k_scale, "k_scale", _U8), (v_scale, "v_scale", _U8), _lens(cache_lens, "cache_lens", B)),
-        (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()),
-        cache_lens, (), out, scale, workspace, stream, return_lse, lse, (B, H, H_kv, Lk, d), (B, H))
+    return _decode(h.mha_decode_f8, h.mha_decode_f8_workspace_bytes, False, q, k_cache, v_cache,
+                   k_scale, v_scale, cache_lens, out, scale, workspace, stream, return_lse, lse)
+
+
+def mha_decode_q4(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, scale: float = 0.0,
+                  workspace=None, stream=None, return_lse: bool = False, lse=None):
+    """mha_decode_f8 over a 4-bit cache: k_cache, v_cache [B, Lk, H_kv, d / 2],
+    scales [B, H_kv, Lk, 2] (mha_cache_write_q4's format)."""
+    h = lib()
+    return _decode(h.mha_decode_q4, h.mha_decode_q4_workspace_bytes, True, q, k_cache, v_cache,
+                   k_scale, v_scale, cache_lens, out, scale, workspace, stream, return_lse, lse)
 
 
 def _tree_mask(q, draft_lens, tree_mask):
@@ -696,22 +760,101 @@ def mha_decode_tree(q, k_cache, v_cache, prefix_lens, draft_lens=None, tree_mask
         stream, return_lse, lse, (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
 
 
-def mha_decode_tree_f8(q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens=None,
-                       tree_mask=None, out=None, scale: float = 0.0, workspace=None, stream=None,
-                       return_lse: bool = False, lse=None):
-    """mha_decode_tree over an 8-bit cache (mha_cache_write_f8's format)."""
-    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale)
+def _decode_tree_scaled(fn, ws_fn, q4, q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens,
+                        tree_mask, out, scale, workspace, stream, return_lse, lse):
+    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale, q4)
     tree, extra = _tree_mask(q, draft_lens, tree_mask)
     B, T, H, _ = q.shape
-    h = lib()
     return _rows_call(
-        h.mha_decode_tree_f8, h.mha_decode_tree_f8_workspace_bytes, q, shape,
-        ((q, "q", _BF16), (k_cache, "k_cache", _F8), (v_cache, "v_cache", _F8),
-         (k_scale, "k_scale", _U8), (v_scale, "v_scale", _U8),
+        fn, ws_fn, q, shape,
+        ((q, "q", _BF16), *_cache_tensors(k_cache, v_cache, k_scale, v_scale, q4),
          _lens(prefix_lens, "prefix_lens", B), *tree),
         (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()),
         prefix_lens, extra, out, scale, workspace, stream, return_lse, lse,
         (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
+
+
+def mha_decode_tree_f8(q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens=None,
+                       tree_mask=None, out=None, scale: float = 0.0, workspace=None, stream=None,
+                       return_lse: bool = False, lse=None):
+    """mha_decode_tree over an 8-bit cache (mha_cache_write_f8's format)."""
+    h = lib()
+    return _decode_tree_scaled(h.mha_decode_tree_f8, h.mha_decode_tree_f8_workspace_bytes, False, q,
+                               k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens,
+                               tree_mask, out, scale, workspace, stream, return_lse, lse)
+
+
+def mha_decode_tree_q4(q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens=None,
+                       tree_mask=None, out=None, scale: float = 0.0, workspace=None, stream=None,
+                       return_lse: bool = False, lse=None):
+    """mha_decode_tree over a 4-bit cache (mha_cache_write_q4's format)."""
+    h = lib()
+    return _decode_tree_scaled(h.mha_decode_tree_q4, h.mha_decode_tree_q4_workspace_bytes, True, q,
+                               k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens,
+                               tree_mask, out, scale, workspace, stream, return_lse, lse)
+
+
+# ---------------------------------------------------------------------------
+# rows of a cache moved in place
+# ---------------------------------------------------------------------------
+_FORMATS = {_BF16: 0, _F8: 1, _U8: 2}  # mha_cache_format by the cache's dtype
+
+
+def _moved_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a cache of any format; returns (format, (B, Lk, H, d), tensors)."""
+    fmt = _FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise TypeError(f"k_cache must be {_BF16}, {_F8} or {_U8} (4 bits), got {k_cache.dtype}")
+    if fmt:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an 8-bit or a 4-bit cache needs k_scale and v_scale")
+        return fmt, _cache_shape(k_cache, v_cache, k_scale, v_scale, fmt == 2), \
+            _cache_tensors(k_cache, v_cache, k_scale, v_scale, fmt == 2)
+    if k_scale is not None or v_scale is not None:
+        raise ValueError("a bf16 cache has no scales")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} "
+                         "must be [B, Lk, H, d_k] alike")
+    return fmt, shape, ((k_cache, "k_cache", _BF16), (v_cache, "v_cache", _BF16))
+
+
+def mha_cache_fork(k_cache, v_cache, parent, lens, first=None, k_scale=None, v_scale=None, stream=None):
+    """Sequences go on with others' cached rows, in place: row (b, j) becomes row
+    (parent[b], j) as it was before the call, first[b] <= j < lens[b] (``first``
+    None: 0), in keys, values and scales.  The cache is bf16 [B, Lk, H, d], 8-bit
+    (float8_e4m3fn) or 4-bit (uint8) with its scales; parent, lens and first are
+    int32 [B].  A parent of b itself, or outside [0, B), leaves b as it is."""
+    fmt, (B, Lk, H, d), tensors = _moved_cache(k_cache, v_cache, k_scale, v_scale)
+    index = k_cache.get_device()
+    _check(index, (*tensors, _lens(parent, "parent", B), _lens(lens, "lens", B)))
+    if first is not None:
+        _check(index, (_lens(first, "first", B),))
+    _call_on(index, stream, (), lib().mha_cache_fork,
+             (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if fmt else None,
+              v_scale.data_ptr() if fmt else None, fmt, B, H, Lk, d, parent.data_ptr(),
+              first.data_ptr() if first is not None else None, lens.data_ptr()))
+
+
+def mha_cache_compact(k_cache, v_cache, prefix_lens, path, path_lens=None, k_scale=None, v_scale=None,
+                      stream=None):
+    """The accepted tokens of a tree step move next to the prefix, in place: row
+    (b, prefix_lens[b] + i) becomes row (b, prefix_lens[b] + path[b, i]) as it was
+    before the call, i < path_lens[b] (None: all T), in keys, values and scales.
+    path int32 [B, T] holds numbers of drafted tokens (one outside [0, T) leaves
+    row i as it is); caches as mha_cache_fork."""
+    fmt, (B, Lk, H, d), tensors = _moved_cache(k_cache, v_cache, k_scale, v_scale)
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError("path must be [B, T]")
+    index = k_cache.get_device()
+    _check(index, (*tensors, _lens(prefix_lens, "prefix_lens", B), (path, "path", _I32)))
+    if path_lens is not None:
+        _check(index, (_lens(path_lens, "path_lens", B),))
+    _call_on(index, stream, (), lib().mha_cache_compact,
+             (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if fmt else None,
+              v_scale.data_ptr() if fmt else None, fmt, B, path.shape[1], H, Lk, d,
+              prefix_lens.data_ptr(), path.data_ptr(),
+              path_lens.data_ptr() if path_lens is not None else None))
 
 
 def host_workspace_bytes(B, H, Lq, Lk, d_k, elem_bytes) -> int:

@@ -175,15 +175,18 @@ struct GemmParams {
 // of 128 x 256, or 256 x 256 when K is long); adds one to info->kernels.
 cudaError_t launch_gemm(const GemmParams& p, cudaStream_t stream, LaunchInfo* info);
 
-// The 8-bit cache: rows written (quantised) or read back, mha_cache.cu.
+// What a cache's rows are kept as.
+enum CacheKind { kCacheBf16, kCacheF8, kCacheQ4 };
+
+// The 8-bit and the 4-bit cache: rows written (quantised) or read back, mha_cache.cu.
 struct CacheParams {
   const void* k;  // write: bf16 rows [B, T, H, d], row_elems and seq_elems apart
   const void* v;
   long long row_elems, seq_elems;
-  void* k_cache;  // [B, Lk, H, d] e4m3 codes
+  void* k_cache;  // [B, Lk, H, d] e4m3 codes; [B, Lk, H, d / 2] packed 4-bit codes
   void* v_cache;
-  uint8_t* k_scale;  // [B, H, Lk] biased exponents
-  uint8_t* v_scale;
+  void* k_scale;  // [B, H, Lk] biased exponents (bytes); bf16 pairs (offset, step)
+  void* v_scale;
   void* k_out;  // read: bf16 [B, Lk, H, d]
   void* v_out;
   const int32_t* lens;    // write: first position per sequence; read: positions held
@@ -193,13 +196,33 @@ struct CacheParams {
 
 // Blocks of the launch for these sizes (must fit a grid dimension).
 long long cache_blocks(int B, int T, int H);
-cudaError_t launch_cache(const CacheParams& p, bool write, cudaStream_t stream, LaunchInfo* info);
+cudaError_t launch_cache(const CacheParams& p, CacheKind kind, bool write, cudaStream_t stream, LaunchInfo* info);
+
+// Rows of a cache moved in place (mha_cache_move.cu): every move reads what the rows
+// held before the call.
+struct MoveParams {
+  uint8_t* codes[2];  // K, V: [B, Lk, row_bytes]
+  uint8_t* scales[2]; // [B, H, Lk] of scale_bytes each (0: none)
+  const int32_t* parent;  // fork: [B] the sequence a sequence's rows come from
+  const int32_t* first;   // fork: [B] first position that moves, or null (0); compact: prefix lengths
+  const int32_t* lens;    // fork: [B] positions held; compact: [B] accepted tokens, or null (T)
+  const int32_t* path;    // compact: [B, T] accepted tokens' numbers
+  long long row_bytes;    // of all heads, a multiple of 16
+  int scale_bytes;        // 0, 1 or 4
+  int B, T, H, Lk;
+};
+constexpr int kMaxForkSeqs = 1024;   // sequences of a fork
+// Blocks of a compaction's launch (must fit a grid dimension).
+long long compact_blocks(const MoveParams& p);
+cudaError_t launch_cache_fork(const MoveParams& p, cudaStream_t stream, LaunchInfo* info);
+cudaError_t launch_cache_compact(const MoveParams& p, cudaStream_t stream, LaunchInfo* info);
 
 // A few query rows per sequence over a cache.
 enum RowsForm {
   kRowsKeys,    // keys along the tensor core's M (mha_rows.cu)
   kRowsBlock,   // rows along its M (mha_rows_block.cu)
   kRowsShort,   // CUDA cores (mha_rows_short.cu)
+  kRowsQ4,      // a 4-bit cache (mha_rows_q4.cu)
 };
 struct RowsParams {
   CUtensorMap tm_k;   // [B, Lk, H_kv, d] bf16, or e4m3 codes when k_scale is set;
@@ -207,9 +230,9 @@ struct RowsParams {
   CUtensorMap tm_k_box;  // the same with boxes of rows_box_keys() keys
   CUtensorMap tm_v_box;
   const void* q;      // [B, T, H, d] bf16
-  const void* k_codes;     // the 8-bit cache itself (mha_rows_short.cu reads it without TMA)
+  const void* k_codes;     // the cache itself (mha_rows_short.cu and mha_rows_q4.cu read it without TMA)
   const void* v_codes;
-  const uint8_t* k_scale;  // [B, H_kv, Lk] biased exponents, or null (bf16 cache)
+  const uint8_t* k_scale;  // [B, H_kv, Lk] biased exponents, bf16 pairs (4 bits), or null (bf16 cache)
   const uint8_t* v_scale;
   void* out;          // [B, T, H, d] bf16
   float* lse;         // [B, H, T] or null
@@ -238,7 +261,7 @@ struct RowsPlan {
   size_t part_rows;   // rows of partials in the workspace (0: none)
   int width;          // features a partial row is kept at
 };
-RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8);
+RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, CacheKind kind);
 int rows_tile_keys();
 int rows_box_keys();
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);

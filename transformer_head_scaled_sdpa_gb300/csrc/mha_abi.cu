@@ -565,6 +565,18 @@ size_t mha_decode_static_scratch_bytes(void) { return kDecodeStaticScratchBytes;
 // ---------------------------------------------------------------------------
 // 8-bit cache rows: multiples of 16 (16-byte strides for the tensor maps)
 static bool f8_width_ok(int d) { return d >= 16 && d <= 256 && d % 16 == 0; }
+// 4-bit cache rows: multiples of 32 (16-byte rows)
+static bool q4_width_ok(int d) { return d >= 32 && d <= 256 && d % 32 == 0; }
+static bool width_ok(mha::CacheKind kind, int d) {
+  return kind == mha::kCacheF8 ? f8_width_ok(d) : (kind == mha::kCacheQ4 ? q4_width_ok(d) : decode_width_ok(d));
+}
+// Bytes of d values of a cache, and of a row's scale.
+static size_t row_bytes(mha::CacheKind kind, int d) {
+  return kind == mha::kCacheF8 ? d : (kind == mha::kCacheQ4 ? d / 2 : 2 * d);
+}
+static size_t scale_bytes(mha::CacheKind kind) {
+  return kind == mha::kCacheF8 ? 1 : (kind == mha::kCacheQ4 ? 4 : 0);
+}
 
 // Most positions of a cache, and tokens of a call: a tile past them fits an int.
 static constexpr int kMaxPositions = 0x7fffffff - 1023;
@@ -572,24 +584,25 @@ static constexpr int kMaxPositions = 0x7fffffff - 1023;
 // twice their number plus any address fits 64 bits.
 static constexpr long long kMaxSpan = 1ll << 50;
 
-// The bytes of codes and of scales that a cache [B, Lk, H, d] holds.
-static bool cache_sizes(int B, int H, int Lk, int d, size_t* codes, size_t* scales) {
+// The bytes of rows and of scales that a cache [B, Lk, H, d] holds.
+static bool cache_sizes(mha::CacheKind kind, int B, int H, int Lk, int d, size_t* codes, size_t* scales) {
   const long long rows = static_cast<long long>(B) * H;
   if (Lk > kMaxPositions || rows > 0x7fffffffll || rows * Lk > (1ll << 40)) return false;
-  *scales = static_cast<size_t>(rows) * Lk;
-  *codes = *scales * d;
+  *scales = static_cast<size_t>(rows) * Lk * scale_bytes(kind);
+  *codes = static_cast<size_t>(rows) * Lk * row_bytes(kind, d);
   return true;
 }
 
-int mha_cache_write_f8(const void* k, const void* v, long long token_stride, long long seq_stride,
-                       void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int B,
+// New rows into a quantised cache.
+static int cache_write(mha::CacheKind kind, const void* k, const void* v, long long token_stride,
+                       long long seq_stride, void* k_cache, void* v_cache, void* k_scale, void* v_scale, int B,
                        int T, int H, int Lk, int d_k, const int32_t* start, const int32_t* counts,
                        void* stream) {
   t_info = mha::LaunchInfo{};
   if (B < 0 || T < 0 || H < 0 || Lk < 0 || token_stride < 0 || seq_stride < 0) return MHA_ERR_SHAPE;
-  if (!f8_width_ok(d_k)) return MHA_ERR_UNSUPPORTED;
+  if (!width_ok(kind, d_k)) return MHA_ERR_UNSUPPORTED;
   size_t codes = 0, scales = 0;
-  if (!cache_sizes(B, H, Lk, d_k, &codes, &scales) || T > kMaxPositions ||
+  if (!cache_sizes(kind, B, H, Lk, d_k, &codes, &scales) || T > kMaxPositions ||
       static_cast<long long>(B) * H * T > (1ll << 40))
     return MHA_ERR_SHAPE;
   const long long hd = static_cast<long long>(H) * d_k;
@@ -605,6 +618,8 @@ int mha_cache_write_f8(const void* k, const void* v, long long token_stride, lon
   if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
         reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) ||
       ((reinterpret_cast<uintptr_t>(start) | reinterpret_cast<uintptr_t>(counts)) & 3u) ||
+      (kind == mha::kCacheQ4 &&
+       ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)) ||
       (token_stride | seq_stride) % 8 != 0)
     return MHA_ERR_UNSUPPORTED;
   const size_t span = (static_cast<size_t>(B - 1) * seq_stride +
@@ -640,31 +655,35 @@ int mha_cache_write_f8(const void* k, const void* v, long long token_stride, lon
   p.H = H;
   p.Lk = Lk;
   p.d = d_k;
-  return mha::launch_cache(p, true, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess
+  return mha::launch_cache(p, kind, true, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess
              ? MHA_OK
              : MHA_ERR_LAUNCH;
 }
 
-int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
-                      const uint8_t* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,
+// The first positions of a quantised cache back as bf16.
+static int cache_read(mha::CacheKind kind, const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,
                       const int32_t* lens, void* stream) {
   t_info = mha::LaunchInfo{};
   if (B < 0 || H < 0 || Lk < 0) return MHA_ERR_SHAPE;
-  if (!f8_width_ok(d_k)) return MHA_ERR_UNSUPPORTED;
+  if (!width_ok(kind, d_k)) return MHA_ERR_UNSUPPORTED;
   size_t codes = 0, scales = 0;
-  if (!cache_sizes(B, H, Lk, d_k, &codes, &scales)) return MHA_ERR_SHAPE;
+  if (!cache_sizes(kind, B, H, Lk, d_k, &codes, &scales)) return MHA_ERR_SHAPE;
   if (scales == 0) return MHA_OK;
+  const size_t values = static_cast<size_t>(B) * H * Lk * d_k * 2;
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !lens) return MHA_ERR_NULL;
   if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
         reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) ||
-      (reinterpret_cast<uintptr_t>(lens) & 3u))
+      (reinterpret_cast<uintptr_t>(lens) & 3u) ||
+      (kind == mha::kCacheQ4 &&
+       ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)))
     return MHA_ERR_UNSUPPORTED;
   const void* ins[5] = {k_cache, v_cache, k_scale, v_scale, lens};
   const size_t ins_b[5] = {codes, codes, scales, scales, static_cast<size_t>(B) * 4};
   for (int i = 0; i < 5; ++i)
-    if (overlaps(k, 2 * codes, ins[i], ins_b[i]) || overlaps(v, 2 * codes, ins[i], ins_b[i]))
+    if (overlaps(k, values, ins[i], ins_b[i]) || overlaps(v, values, ins[i], ins_b[i]))
       return MHA_ERR_ALIAS;
-  if (overlaps(k, 2 * codes, v, 2 * codes)) return MHA_ERR_ALIAS;
+  if (overlaps(k, values, v, values)) return MHA_ERR_ALIAS;
   if (mha::cache_blocks(B, Lk, H) > 0x7fffffffll) return MHA_ERR_SHAPE;
   DeviceState* dev = nullptr;
   const int rc = device_state(&dev);
@@ -673,8 +692,8 @@ int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k
   std::memset(&p, 0, sizeof(p));
   p.k_cache = const_cast<void*>(k_cache);
   p.v_cache = const_cast<void*>(v_cache);
-  p.k_scale = const_cast<uint8_t*>(k_scale);
-  p.v_scale = const_cast<uint8_t*>(v_scale);
+  p.k_scale = const_cast<void*>(k_scale);
+  p.v_scale = const_cast<void*>(v_scale);
   p.k_out = k;
   p.v_out = v;
   p.lens = lens;
@@ -683,9 +702,37 @@ int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k
   p.H = H;
   p.Lk = Lk;
   p.d = d_k;
-  return mha::launch_cache(p, false, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess
+  return mha::launch_cache(p, kind, false, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess
              ? MHA_OK
              : MHA_ERR_LAUNCH;
+}
+
+int mha_cache_write_f8(const void* k, const void* v, long long token_stride, long long seq_stride,
+                       void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int B,
+                       int T, int H, int Lk, int d_k, const int32_t* start, const int32_t* counts,
+                       void* stream) {
+  return cache_write(mha::kCacheF8, k, v, token_stride, seq_stride, k_cache, v_cache, k_scale, v_scale, B, T, H,
+                     Lk, d_k, start, counts, stream);
+}
+
+int mha_cache_write_q4(const void* k, const void* v, long long token_stride, long long seq_stride,
+                       void* k_cache, void* v_cache, void* k_scale, void* v_scale, int B, int T,
+                       int H, int Lk, int d_k, const int32_t* start, const int32_t* counts,
+                       void* stream) {
+  return cache_write(mha::kCacheQ4, k, v, token_stride, seq_stride, k_cache, v_cache, k_scale, v_scale, B, T, H,
+                     Lk, d_k, start, counts, stream);
+}
+
+int mha_cache_read_f8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                      const uint8_t* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,
+                      const int32_t* lens, void* stream) {
+  return cache_read(mha::kCacheF8, k_cache, v_cache, k_scale, v_scale, k, v, B, H, Lk, d_k, lens, stream);
+}
+
+int mha_cache_read_q4(const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, void* k, void* v, int B, int H, int Lk, int d_k,
+                      const int32_t* lens, void* stream) {
+  return cache_read(mha::kCacheQ4, k_cache, v_cache, k_scale, v_scale, k, v, B, H, Lk, d_k, lens, stream);
 }
 
 // Most drafted tokens of one step (four mask words).
@@ -698,48 +745,57 @@ static size_t rows_ws_bytes(const mha::RowsPlan& plan) {
 }
 
 // Sizes of a rows step: MHA_OK, or the code of what is wrong.
-static int rows_sizes_ok(int B, int T, int H, int H_kv, int Lk, int d_k, bool f8) {
+static int rows_sizes_ok(int B, int T, int H, int H_kv, int Lk, int d_k, mha::CacheKind kind) {
   if (B < 0 || T < 0 || H < 0 || H_kv < 0 || Lk < 0 || Lk > kMaxPositions) return MHA_ERR_SHAPE;
   if (H > 0 && (H_kv == 0 || H % H_kv != 0)) return MHA_ERR_SHAPE;
-  if (!(f8 ? f8_width_ok(d_k) : decode_width_ok(d_k)) || T > kMaxDrafts) return MHA_ERR_UNSUPPORTED;
+  if (!width_ok(kind, d_k) || T > kMaxDrafts) return MHA_ERR_UNSUPPORTED;
   const long long bh = static_cast<long long>(B) * H;
   if (bh > 0x7fffffffll || bh * T > 0x7fffffffll || bh * Lk > (1ll << 40)) return MHA_ERR_SHAPE;
+  // (a 4-bit row's distance from the next position's fits an int)
+  if (kind == mha::kCacheQ4 && static_cast<long long>(H_kv) * d_k > 0xfffffffell) return MHA_ERR_SHAPE;
   return MHA_OK;
 }
 
-static size_t rows_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k, bool f8) {
-  if (rows_sizes_ok(B, T, H, H_kv, Lk, d_k, f8) != MHA_OK ||
+static size_t rows_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k, mha::CacheKind kind) {
+  if (rows_sizes_ok(B, T, H, H_kv, Lk, d_k, kind) != MHA_OK ||
       static_cast<long long>(B) * T * H == 0)
     return 0;
-  return rows_ws_bytes(mha::rows_plan(B, T, H, H_kv, Lk, d_k, f8));
+  return rows_ws_bytes(mha::rows_plan(B, T, H, H_kv, Lk, d_k, kind));
 }
 
 size_t mha_decode_f8_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k) {
-  return rows_workspace_bytes(B, 1, H, H_kv, Lk, d_k, true);
+  return rows_workspace_bytes(B, 1, H, H_kv, Lk, d_k, mha::kCacheF8);
 }
 size_t mha_decode_tree_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k) {
-  return rows_workspace_bytes(B, T, H, H_kv, Lk, d_k, false);
+  return rows_workspace_bytes(B, T, H, H_kv, Lk, d_k, mha::kCacheBf16);
 }
 size_t mha_decode_tree_f8_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k) {
-  return rows_workspace_bytes(B, T, H, H_kv, Lk, d_k, true);
+  return rows_workspace_bytes(B, T, H, H_kv, Lk, d_k, mha::kCacheF8);
+}
+size_t mha_decode_q4_workspace_bytes(int B, int H, int H_kv, int Lk, int d_k) {
+  return rows_workspace_bytes(B, 1, H, H_kv, Lk, d_k, mha::kCacheQ4);
+}
+size_t mha_decode_tree_q4_workspace_bytes(int B, int T, int H, int H_kv, int Lk, int d_k) {
+  return rows_workspace_bytes(B, T, H, H_kv, Lk, d_k, mha::kCacheQ4);
 }
 
-// T query rows per sequence against a cache (8-bit when f8): the keys of the
+// T query rows per sequence against a cache: the keys of the
 // prefix and, with `drafts`, of the drafted tokens after it.
 static int rows_step(const void* q, const void* k_cache, const void* v_cache,
-                     const uint8_t* k_scale, const uint8_t* v_scale, void* out, float* lse, int B,
+                     const void* k_scale, const void* v_scale, void* out, float* lse, int B,
                      int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
-                     bool drafts, const int32_t* draft_lens, const uint64_t* tree_mask, bool f8,
+                     bool drafts, const int32_t* draft_lens, const uint64_t* tree_mask, mha::CacheKind kind,
                      float scale, void* workspace, size_t workspace_bytes, void* stream) {
   t_info = mha::LaunchInfo{};
-  int rc = rows_sizes_ok(B, T, H, H_kv, Lk, d_k, f8);
+  const bool f8 = kind == mha::kCacheF8, scaled = kind != mha::kCacheBf16;
+  int rc = rows_sizes_ok(B, T, H, H_kv, Lk, d_k, kind);
   if (rc != MHA_OK) return rc;
   if (!std::isfinite(scale) || scale < 0.f) return MHA_ERR_SCALE;
   const long long rows = static_cast<long long>(B) * T * H;
   if (rows == 0) return MHA_OK;
   if (!q || !out) return MHA_ERR_NULL;
   if (!prefix_lens) return MHA_ERR_MASK;
-  if (Lk > 0 && (!k_cache || !v_cache || (f8 && (!k_scale || !v_scale)))) return MHA_ERR_NULL;
+  if (Lk > 0 && (!k_cache || !v_cache || (scaled && (!k_scale || !v_scale)))) return MHA_ERR_NULL;
   const uintptr_t mis = (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
                          (Lk > 0 ? (reinterpret_cast<uintptr_t>(k_cache) |
                                     reinterpret_cast<uintptr_t>(v_cache))
@@ -747,12 +803,14 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
                         15u;
   if (mis || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
       ((reinterpret_cast<uintptr_t>(prefix_lens) | reinterpret_cast<uintptr_t>(draft_lens)) & 3u) ||
-      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u) ||
+      (kind == mha::kCacheQ4 && Lk > 0 &&
+       ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)))
     return MHA_ERR_UNSUPPORTED;
   const int words = (T + 63) / 64;
   const size_t qb = static_cast<size_t>(rows) * d_k * 2;
-  const size_t scales = static_cast<size_t>(B) * H_kv * Lk;
-  const size_t kb = scales * d_k * (f8 ? 1 : 2);
+  const size_t cached = static_cast<size_t>(B) * H_kv * Lk;
+  const size_t kb = cached * row_bytes(kind, d_k), scales = cached * scale_bytes(kind);
   const size_t lb = static_cast<size_t>(rows) * 4;
   const void* ins[8] = {q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens, tree_mask};
   const size_t ins_b[8] = {qb, kb, kb, scales, scales, static_cast<size_t>(B) * 4,
@@ -761,7 +819,7 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
     if (overlaps(out, qb, ins[i], ins_b[i]) || overlaps(lse, lb, ins[i], ins_b[i]))
       return MHA_ERR_ALIAS;
   if (overlaps(lse, lb, out, qb)) return MHA_ERR_ALIAS;
-  const mha::RowsPlan plan = mha::rows_plan(B, T, H, H_kv, Lk, d_k, f8);
+  const mha::RowsPlan plan = mha::rows_plan(B, T, H, H_kv, Lk, d_k, kind);
   if (plan.units * B * plan.splits > 0x7fffffffll) return MHA_ERR_SHAPE;  // (a CTA per unit)
   const size_t need = rows_ws_bytes(plan);
   if (need > 0) {
@@ -782,7 +840,7 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   auto encode = [&](CUtensorMap* m, const void* base, int keys) {
     return f8 ? encode_map_f8(m, base, B, Lk, H_kv, d_k, keys) : encode_map(m, base, B, Lk, H_kv, d_k, keys);
   };
-  if (plan.form != mha::kRowsShort &&
+  if (plan.form != mha::kRowsShort && plan.form != mha::kRowsQ4 &&
       (!encode(&p.tm_k, k_cache, mha::rows_tile_keys()) || !encode(&p.tm_v, v_cache, mha::rows_tile_keys()) ||
       !encode(&p.tm_k_box, k_cache, mha::rows_box_keys()) ||
       !encode(&p.tm_v_box, v_cache, mha::rows_box_keys())))
@@ -791,8 +849,8 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   p.k_codes = k_cache;
   p.v_codes = v_cache;
   p.form = plan.form;
-  p.k_scale = f8 ? k_scale : nullptr;
-  p.v_scale = f8 ? v_scale : nullptr;
+  p.k_scale = scaled ? static_cast<const uint8_t*>(k_scale) : nullptr;
+  p.v_scale = scaled ? static_cast<const uint8_t*>(v_scale) : nullptr;
   p.out = out;
   p.lse = lse;
   p.prefix_lens = prefix_lens;
@@ -827,7 +885,7 @@ int mha_decode_f8(const void* q, const void* k_cache, const void* v_cache, const
                   int d_k, const int32_t* cache_lens, float scale, void* workspace,
                   size_t workspace_bytes, void* stream) {
   return rows_step(q, k_cache, v_cache, k_scale, v_scale, out, lse, B, 1, H, H_kv, Lk, d_k,
-                   cache_lens, false, nullptr, nullptr, true, scale, workspace, workspace_bytes,
+                   cache_lens, false, nullptr, nullptr, mha::kCacheF8, scale, workspace, workspace_bytes,
                    stream);
 }
 
@@ -836,7 +894,7 @@ int mha_decode_tree(const void* q, const void* k_cache, const void* v_cache, voi
                     const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
                     void* workspace, size_t workspace_bytes, void* stream) {
   return rows_step(q, k_cache, v_cache, nullptr, nullptr, out, lse, B, T, H, H_kv, Lk, d_k,
-                   prefix_lens, true, draft_lens, tree_mask, false, scale, workspace,
+                   prefix_lens, true, draft_lens, tree_mask, mha::kCacheBf16, scale, workspace,
                    workspace_bytes, stream);
 }
 
@@ -846,8 +904,117 @@ int mha_decode_tree_f8(const void* q, const void* k_cache, const void* v_cache,
                        const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
                        void* workspace, size_t workspace_bytes, void* stream) {
   return rows_step(q, k_cache, v_cache, k_scale, v_scale, out, lse, B, T, H, H_kv, Lk, d_k,
-                   prefix_lens, true, draft_lens, tree_mask, true, scale, workspace,
+                   prefix_lens, true, draft_lens, tree_mask, mha::kCacheF8, scale, workspace,
                    workspace_bytes, stream);
+}
+
+int mha_decode_q4(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                  const void* v_scale, void* out, float* lse, int B, int H, int H_kv, int Lk,
+                  int d_k, const int32_t* cache_lens, float scale, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  return rows_step(q, k_cache, v_cache, k_scale, v_scale, out, lse, B, 1, H, H_kv, Lk, d_k,
+                   cache_lens, false, nullptr, nullptr, mha::kCacheQ4, scale, workspace, workspace_bytes,
+                   stream);
+}
+
+int mha_decode_tree_q4(const void* q, const void* k_cache, const void* v_cache,
+                       const void* k_scale, const void* v_scale, void* out, float* lse,
+                       int B, int T, int H, int H_kv, int Lk, int d_k, const int32_t* prefix_lens,
+                       const int32_t* draft_lens, const uint64_t* tree_mask, float scale,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return rows_step(q, k_cache, v_cache, k_scale, v_scale, out, lse, B, T, H, H_kv, Lk, d_k,
+                   prefix_lens, true, draft_lens, tree_mask, mha::kCacheQ4, scale, workspace,
+                   workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of a cache moved in place.
+// ---------------------------------------------------------------------------
+// What both moves check of the cache; `small`: the int32 arrays, null where not given,
+// and their numbers of elements.
+static int move_args(int format, void* k_cache, void* v_cache, void* k_scale, void* v_scale, int B, int T, int H,
+                     int Lk, int d_k, const int32_t* const (&small)[3], const size_t (&small_n)[3],
+                     mha::MoveParams* p) {
+  t_info = mha::LaunchInfo{};
+  if (format != MHA_CACHE_BF16 && format != MHA_CACHE_F8 && format != MHA_CACHE_Q4) return MHA_ERR_UNSUPPORTED;
+  const mha::CacheKind kind = format == MHA_CACHE_F8   ? mha::kCacheF8
+                              : format == MHA_CACHE_Q4 ? mha::kCacheQ4
+                                                       : mha::kCacheBf16;
+  if (B < 0 || T < 0 || H < 0 || Lk < 0) return MHA_ERR_SHAPE;
+  if (!width_ok(kind, d_k)) return MHA_ERR_UNSUPPORTED;
+  size_t codes = 0, scales = 0;
+  if (!cache_sizes(kind, B, H, Lk, d_k, &codes, &scales)) return MHA_ERR_SHAPE;
+  const bool scaled = kind != mha::kCacheBf16;
+  if (codes == 0) return MHA_OK;
+  if (!k_cache || !v_cache || (scaled && (!k_scale || !v_scale))) return MHA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u) return MHA_ERR_UNSUPPORTED;
+  if (kind == mha::kCacheQ4 &&
+      ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u))
+    return MHA_ERR_UNSUPPORTED;
+  void* outs[4] = {k_cache, v_cache, scaled ? k_scale : nullptr, scaled ? v_scale : nullptr};
+  const size_t outs_b[4] = {codes, codes, scales, scales};
+  for (int i = 0; i < 3; ++i)
+    if (reinterpret_cast<uintptr_t>(small[i]) & 3u) return MHA_ERR_UNSUPPORTED;
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (overlaps(outs[o], outs_b[o], small[i], small_n[i] * 4)) return MHA_ERR_ALIAS;
+    for (int i = o + 1; i < 4; ++i)
+      if (overlaps(outs[o], outs_b[o], outs[i], outs_b[i])) return MHA_ERR_ALIAS;
+  }
+  std::memset(p, 0, sizeof(*p));
+  for (int c = 0; c < 2; ++c) {
+    p->codes[c] = static_cast<uint8_t*>(outs[c]);
+    p->scales[c] = static_cast<uint8_t*>(outs[2 + c]);
+  }
+  p->row_bytes = static_cast<long long>(H) * static_cast<long long>(row_bytes(kind, d_k));
+  p->scale_bytes = static_cast<int>(scale_bytes(kind));
+  p->B = B;
+  p->T = T;
+  p->H = H;
+  p->Lk = Lk;
+  return MHA_OK;
+}
+
+int mha_cache_fork(void* k_cache, void* v_cache, void* k_scale, void* v_scale, int format, int B,
+                   int H, int Lk, int d_k, const int32_t* parent, const int32_t* first,
+                   const int32_t* lens, void* stream) {
+  mha::MoveParams p;
+  const size_t n = B < 0 ? 0 : static_cast<size_t>(B);
+  int rc = move_args(format, k_cache, v_cache, k_scale, v_scale, B, 1, H, Lk, d_k, {parent, first, lens}, {n, n, n},
+                     &p);
+  if (rc != MHA_OK || B == 0 || H == 0 || Lk == 0) return rc;
+  if (B > mha::kMaxForkSeqs) return MHA_ERR_UNSUPPORTED;
+  if (!parent || !lens) return MHA_ERR_NULL;
+  DeviceState* dev = nullptr;
+  rc = device_state(&dev);
+  if (rc != MHA_OK) return rc;
+  p.parent = parent;
+  p.first = first;
+  p.lens = lens;
+  return mha::launch_cache_fork(p, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess ? MHA_OK
+                                                                                              : MHA_ERR_LAUNCH;
+}
+
+int mha_cache_compact(void* k_cache, void* v_cache, void* k_scale, void* v_scale, int format, int B,
+                      int T, int H, int Lk, int d_k, const int32_t* prefix_lens,
+                      const int32_t* path, const int32_t* path_lens, void* stream) {
+  mha::MoveParams p;
+  const size_t n = B < 0 ? 0 : static_cast<size_t>(B);
+  int rc = move_args(format, k_cache, v_cache, k_scale, v_scale, B, T, H, Lk, d_k, {prefix_lens, path, path_lens},
+                     {n, n * (T < 0 ? 0 : static_cast<size_t>(T)), n}, &p);
+  if (rc != MHA_OK || B == 0 || T == 0 || H == 0 || Lk == 0) return rc;
+  if (T > kMaxDrafts) return MHA_ERR_UNSUPPORTED;
+  if (!prefix_lens || !path) return MHA_ERR_NULL;
+  p.first = prefix_lens;
+  p.path = path;
+  p.lens = path_lens;
+  if (mha::compact_blocks(p) > 0x7fffffffll) return MHA_ERR_SHAPE;
+  DeviceState* dev = nullptr;
+  rc = device_state(&dev);
+  if (rc != MHA_OK) return rc;
+  return mha::launch_cache_compact(p, static_cast<cudaStream_t>(stream), &t_info) == cudaSuccess
+             ? MHA_OK
+             : MHA_ERR_LAUNCH;
 }
 
 size_t mha_bwd_workspace_bytes(int B, int H, int Lq, int Lk, int d_k) {

@@ -23,6 +23,7 @@
 
 #include "fp8.cuh"
 #include "kernels.h"
+#include "q4.cuh"
 
 namespace mha {
 namespace {
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
         const uint4 a = x[u][c][0], b = x[u][c][1];
         if (has0) *reinterpret_cast<uint2*>(to) = make_uint2(codes4(a.x, a.y, f), codes4(a.z, a.w, f));
         if (has1) *reinterpret_cast<uint2*>(to + 8 * GS) = make_uint2(codes4(b.x, b.y, f), codes4(b.z, b.w, f));
-        if (sub == 0) (c == 0 ? p.k_scale : p.v_scale)[scale_row + t] = static_cast<uint8_t>(s);
+        if (sub == 0) static_cast<uint8_t*>(c == 0 ? p.k_scale : p.v_scale)[scale_row + t] = static_cast<uint8_t>(s);
       }
     }
   }
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
                            static_cast<const uint8_t*>(p.v_cache) + row};
   uint16_t* dst[2] = {static_cast<uint16_t*>(p.k_out) + row, static_cast<uint16_t*>(p.v_out) + row};
   const long long scale_row = (static_cast<long long>(r.b) * p.H + r.h) * p.Lk + r.t0;
-  const uint8_t* scale[2] = {p.k_scale + scale_row, p.v_scale + scale_row};
+  const uint8_t* scale[2] = {static_cast<const uint8_t*>(p.k_scale) + scale_row,
+                             static_cast<const uint8_t*>(p.v_scale) + scale_row};
   const long long pos = static_cast<long long>(p.H) * p.d;  // elements between positions
   for (int t0 = r.t; t0 < last; t0 += 2 * r.step) {
     uint2 x[2][2][2];
@@ -195,8 +197,161 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   }
 }
 
+// ---------------------------------------------------------------------------
+// 4 bits (q4.cuh): the same tiles of positions x heads, eight codes to a word.
+// ---------------------------------------------------------------------------
+
+// (min, -max) of eight bf16 (a NaN stays).
+__device__ __forceinline__ __nv_bfloat162 low_high8(const uint4& x) {
+  const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&x);
+  const __nv_bfloat162 lo = __hmin2_nan(__hmin2_nan(v[0], v[1]), __hmin2_nan(v[2], v[3]));
+  const __nv_bfloat162 hi = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+  return __halves2bfloat162(__hmin_nan(__low2bfloat16(lo), __high2bfloat16(lo)),
+                            __hneg(__hmax_nan(__low2bfloat16(hi), __high2bfloat16(hi))));
+}
+
+// Eight bf16 to a word of codes.
+__device__ __forceinline__ uint32_t codes8(const uint4& x, const RowQ4& r) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c |= (code_q4(bf16_lo(w[i]), r) << (8 * i)) | (code_q4(bf16_hi(w[i]), r) << (8 * i + 4));
+  return c;
+}
+
+// GS: lanes per row, the power of two >= d / 16
 template <int GS>
-cudaError_t launch_gs(const CacheParams& p, bool write, unsigned blocks, cudaStream_t s, LaunchInfo* info) {
+__global__ void __launch_bounds__(kThreads) cache_write_q4_kernel(const __grid_constant__ CacheParams p) {
+  griddep_wait();
+  const Rows r = thread_rows<GS>(p);
+  const int sub = static_cast<int>(threadIdx.x) % GS;
+  const bool has0 = 8 * sub < p.d, has1 = 8 * (sub + GS) < p.d;
+  const int start = __ldg(p.lens + r.b);
+  int count = p.T;
+  if (p.counts) {
+    const int c = __ldg(p.counts + r.b);
+    count = c < 0 ? 0 : (c < p.T ? c : p.T);
+  }
+  // positions first .. last - 1 of the tile are written
+  const long long at0 = static_cast<long long>(start) + r.t0;
+  const int first = at0 < 0 ? static_cast<int>(min(-at0, static_cast<long long>(r.nt))) : 0;
+  const int last = static_cast<int>(
+      max(0ll, min(static_cast<long long>(min(r.nt, count - r.t0)), static_cast<long long>(p.Lk) - at0)));
+  const long long src_row = p.seq_elems * r.b + static_cast<long long>(r.h) * p.d + 8 * sub;
+  const uint16_t* src[2] = {static_cast<const uint16_t*>(p.k) + src_row,
+                            static_cast<const uint16_t*>(p.v) + src_row};
+  const long long pos_bytes = static_cast<long long>(p.H) * (p.d / 2);  // between positions of the cache
+  const long long dst_row = (static_cast<long long>(r.b) * p.Lk + at0) * pos_bytes +
+                            static_cast<long long>(r.h) * (p.d / 2) + 4 * sub;
+  uint8_t* dst[2] = {static_cast<uint8_t*>(p.k_cache) + dst_row, static_cast<uint8_t*>(p.v_cache) + dst_row};
+  const long long scale_row = (static_cast<long long>(r.b) * p.H + r.h) * p.Lk + at0;
+  // (the loop's bound is the same for every lane: the shuffles are the whole
+  // warp's)
+  for (int base = 0; base < r.nt; base += 2 * r.step) {
+    uint4 x[2][2][2] = {};  // [position][K, V][piece]
+    bool on[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = base + u * r.step + r.t;
+      on[u] = r.head_ok && t >= first && t < last;
+      if (!on[u]) continue;
+      const long long o = p.row_elems * (r.t0 + t);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (has0) x[u][c][0] = __ldg(reinterpret_cast<const uint4*>(src[c] + o));
+        if (has1) x[u][c][1] = __ldg(reinterpret_cast<const uint4*>(src[c] + o + 8 * GS));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = base + u * r.step + r.t;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        // (a lane without a piece has +-infinity, which loses to every value)
+        __nv_bfloat162 m = __halves2bfloat162(__ushort_as_bfloat16(0x7f80), __ushort_as_bfloat16(0x7f80));
+        if (has0) m = low_high8(x[u][c][0]);
+        if (has1) m = __hmin2_nan(m, low_high8(x[u][c][1]));
+#pragma unroll
+        for (int o = 1; o < GS; o <<= 1) m = __hmin2_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (!on[u]) continue;
+        const RowQ4 row = row_q4(__low2float(m), -__high2float(m));
+        const bool bad = row.lo != row.lo;
+        uint8_t* to = dst[c] + t * pos_bytes;
+        if (has0) *reinterpret_cast<uint32_t*>(to) = bad ? 0 : codes8(x[u][c][0], row);
+        if (has1) *reinterpret_cast<uint32_t*>(to + 4 * GS) = bad ? 0 : codes8(x[u][c][1], row);
+        if (sub == 0)
+          static_cast<uint32_t*>(c == 0 ? p.k_scale : p.v_scale)[scale_row + t] =
+              (__float_as_uint(row.lo) >> 16) | (__float_as_uint(row.step) & 0xffff0000u);
+      }
+    }
+  }
+}
+
+// Eight codes to bf16: lo + c * step, rounded to float32 and then to bf16.
+__device__ __forceinline__ uint4 values8(uint32_t c, float lo, float step) {
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // (128 + c as a bf16 number has the code in its last bits)
+    const float a = __uint_as_float(0x43000000u | (((c >> (8 * i)) & 15u) << 16));
+    const float b = __uint_as_float(0x43000000u | (((c >> (8 * i + 4)) & 15u) << 16));
+    float x0, x1;
+    add2(x0, x1, a, b, -128.f, -128.f);
+    fma2(x0, x1, x0, x1, step, step, lo, lo);
+    y[i] = pack_bf16x2(x0, x1);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+template <int GS>
+__global__ void __launch_bounds__(kThreads) cache_read_q4_kernel(const __grid_constant__ CacheParams p) {
+  griddep_wait();
+  const Rows r = thread_rows<GS>(p);
+  const int sub = static_cast<int>(threadIdx.x) % GS;
+  const bool has0 = 8 * sub < p.d, has1 = 8 * (sub + GS) < p.d;
+  if (!r.head_ok || !has0) return;
+  const int last = min(r.nt, max(__ldg(p.lens + r.b), 0) - r.t0);
+  const long long row = ((static_cast<long long>(r.b) * p.Lk + r.t0) * p.H + r.h) * p.d + 8 * sub;
+  const uint8_t* src[2] = {static_cast<const uint8_t*>(p.k_cache) + row / 2,
+                           static_cast<const uint8_t*>(p.v_cache) + row / 2};
+  uint16_t* dst[2] = {static_cast<uint16_t*>(p.k_out) + row, static_cast<uint16_t*>(p.v_out) + row};
+  const long long scale_row = (static_cast<long long>(r.b) * p.H + r.h) * p.Lk + r.t0;
+  const uint32_t* scale[2] = {static_cast<const uint32_t*>(p.k_scale) + scale_row,
+                              static_cast<const uint32_t*>(p.v_scale) + scale_row};
+  const long long pos = static_cast<long long>(p.H) * p.d;  // elements between positions
+  for (int t0 = r.t; t0 < last; t0 += 2 * r.step) {
+    uint32_t x[2][2][2], s[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = t0 + u * r.step;
+      if (t >= last) continue;
+      const long long o = t * pos / 2;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        x[u][c][0] = __ldg(reinterpret_cast<const uint32_t*>(src[c] + o));
+        if (has1) x[u][c][1] = __ldg(reinterpret_cast<const uint32_t*>(src[c] + o + 4 * GS));
+        s[u][c] = __ldg(scale[c] + t);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = t0 + u * r.step;
+      if (t >= last) continue;
+      const long long o = t * pos;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float lo = bf16_lo(s[u][c]), step = bf16_hi(s[u][c]);
+        *reinterpret_cast<uint4*>(dst[c] + o) = values8(x[u][c][0], lo, step);
+        if (has1) *reinterpret_cast<uint4*>(dst[c] + o + 8 * GS) = values8(x[u][c][1], lo, step);
+      }
+    }
+  }
+}
+
+template <int GS>
+cudaError_t launch_gs(const CacheParams& p, CacheKind kind, bool write, unsigned blocks, cudaStream_t s,
+                      LaunchInfo* info) {
   // as many positions at a time as the block has threads for, or as there are
   const int fit = kThreads / (GS * kTileHeads);
   int threads = (p.T < fit ? p.T : fit) * GS * kTileHeads;
@@ -207,8 +362,9 @@ cudaError_t launch_gs(const CacheParams& p, bool write, unsigned blocks, cudaStr
     info->block = threads;
     info->smem = 0;
   }
-  return write ? launch_serialized(cache_write_kernel<GS>, dim3(blocks), dim3(threads), 0, s, p)
-               : launch_serialized(cache_read_kernel<GS>, dim3(blocks), dim3(threads), 0, s, p);
+  auto* kernel = kind == kCacheQ4 ? (write ? cache_write_q4_kernel<GS> : cache_read_q4_kernel<GS>)
+                                  : (write ? cache_write_kernel<GS> : cache_read_kernel<GS>);
+  return launch_serialized(kernel, dim3(blocks), dim3(threads), 0, s, p);
 }
 
 }  // namespace
@@ -218,14 +374,14 @@ long long cache_blocks(int B, int T, int H) {
          ((H + kTileHeads - 1) / kTileHeads);
 }
 
-cudaError_t launch_cache(const CacheParams& p, bool write, cudaStream_t stream, LaunchInfo* info) {
+cudaError_t launch_cache(const CacheParams& p, CacheKind kind, bool write, cudaStream_t stream, LaunchInfo* info) {
   const unsigned blocks = static_cast<unsigned>(cache_blocks(p.B, p.T, p.H));
   const int lanes = p.d / 16;
-  if (lanes <= 1) return launch_gs<1>(p, write, blocks, stream, info);
-  if (lanes <= 2) return launch_gs<2>(p, write, blocks, stream, info);
-  if (lanes <= 4) return launch_gs<4>(p, write, blocks, stream, info);
-  if (lanes <= 8) return launch_gs<8>(p, write, blocks, stream, info);
-  return launch_gs<16>(p, write, blocks, stream, info);
+  if (lanes <= 1) return launch_gs<1>(p, kind, write, blocks, stream, info);
+  if (lanes <= 2) return launch_gs<2>(p, kind, write, blocks, stream, info);
+  if (lanes <= 4) return launch_gs<4>(p, kind, write, blocks, stream, info);
+  if (lanes <= 8) return launch_gs<8>(p, kind, write, blocks, stream, info);
+  return launch_gs<16>(p, kind, write, blocks, stream, info);
 }
 
 }  // namespace mha

@@ -1511,10 +1511,11 @@ cudaError_t launch_combine(const RowsParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
+RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, CacheKind kind) {
   const int R = T * (H / H_kv);
+  const bool f8 = kind == kCacheF8;
   RowsPlan plan = {};
-  plan.form = rows_form(f8, d, T, H / H_kv, Lk);
+  plan.form = kind == kCacheQ4 ? kRowsQ4 : rows_form(f8, d, T, H / H_kv, Lk);
   if (plan.form == kRowsShort) {
     plan.units = H_kv;
     plan.splits = 1;
@@ -1529,6 +1530,12 @@ RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, bool f8) {
       rows = C::NR;
       ctas = C::MIN_BLOCKS;
     });
+  if (plan.form == kRowsQ4) {
+    const RowsQ4Shape shape = rows_q4_shape(d, R);
+    plan.width = shape.width;
+    rows = shape.rows;
+    ctas = shape.ctas;
+  }
   plan.units = static_cast<long long>(H_kv) * ((R + rows - 1) / rows);
   const long long base = plan.units * B;
   const long long slots = static_cast<long long>(kSms) * ctas;
@@ -1558,10 +1565,12 @@ int rows_tile_keys() { return kKeys; }
 int rows_box_keys() { return kBoxKeys; }
 
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
-  const bool f8 = p.k_scale != nullptr;
+  const bool q4 = p.form == kRowsQ4, f8 = !q4 && p.k_scale != nullptr;
   const int R = p.T * p.G;
   cudaError_t e = cudaSuccess;
-  if (p.form == kRowsShort) {
+  if (q4) {
+    e = launch_rows_q4(p, stream, info);
+  } else if (p.form == kRowsShort) {
     e = launch_rows_short(p, stream, info);
   } else if (p.form == kRowsBlock) {
     e = launch_rows_block(p, stream, info);

@@ -161,4 +161,11 @@ cudaError_t launch_rows_short(const RowsParams& p, cudaStream_t stream, LaunchIn
 constexpr int kBlockRows = 256;  // rows per unit
 cudaError_t launch_rows_block(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
 
+// The step over a 4-bit cache (mha_rows_q4.cu).
+struct RowsQ4Shape {
+  int width, rows, ctas;  // features a partial row is kept at, rows per unit, CTAs per SM
+};
+RowsQ4Shape rows_q4_shape(int d, int R);
+cudaError_t launch_rows_q4(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
+
 }  // namespace mha

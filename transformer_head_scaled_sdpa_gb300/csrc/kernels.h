@@ -227,10 +227,11 @@ enum RowsForm {
 struct RowsParams {
   CUtensorMap tm_k;   // [B, Lk, H_kv, d] bf16, or e4m3 codes when k_scale is set;
   CUtensorMap tm_v;   // box {128 bytes, 1, rows_tile_keys(), 1}, 128-byte swizzle
-  CUtensorMap tm_k_box;  // the same with boxes of rows_box_keys() keys
+                      // (4 bits: box {width / 2 bytes, 1, kRowsQ4Keys, 1}, a row's swizzle)
+  CUtensorMap tm_k_box;  // the same with boxes of rows_box_keys() (kRowsQ4Box) keys
   CUtensorMap tm_v_box;
   const void* q;      // [B, T, H, d] bf16
-  const void* k_codes;     // the cache itself (mha_rows_short.cu and mha_rows_q4.cu read it without TMA)
+  const void* k_codes;     // the cache itself (mha_rows_short.cu reads it without TMA)
   const void* v_codes;
   const uint8_t* k_scale;  // [B, H_kv, Lk] biased exponents, bf16 pairs (4 bits), or null (bf16 cache)
   const uint8_t* v_scale;
@@ -264,6 +265,8 @@ struct RowsPlan {
 RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, CacheKind kind);
 int rows_tile_keys();
 int rows_box_keys();
+// Keys of the 4-bit kernel's TMA boxes: a warp's tile, and a piece of a ragged one.
+constexpr int kRowsQ4Keys = 32, kRowsQ4Box = 8;
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
 
 }  // namespace mha

@@ -225,6 +225,24 @@ bool encode_map_f8(CUtensorMap* m, const void* base, int B, int L, int H, int d,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4-D map over a 4-bit cache's packed rows [B, L, H, d / 2]; box = the kernel's width
+// (64, 128 or 256 features) x 1 head x `rows` rows x 1 sequence, rows of 32 bytes as they
+// are, of 64 or 128 with the swizzle of that size.
+bool encode_map_q4(CUtensorMap* m, const void* base, int B, int L, int H, int d, int width, int rows) {
+  const cuuint64_t row = static_cast<cuuint64_t>(d) / 2;
+  const cuuint64_t dims[4] = {row, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(L),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {row, row * H, row * H * L};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(width / 2), 1, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  width == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                              : (width == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B),
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // lse, when requested: [B, H, Lq] float32, 4-byte aligned, overlapping none of
@@ -837,13 +855,15 @@ static int rows_step(const void* q, const void* k_cache, const void* v_cache,
   if (Lk == 0) return no_keys(out, qb, lse, static_cast<size_t>(rows), s);
   mha::RowsParams p;
   std::memset(&p, 0, sizeof(p));
+  const int tile = kind == mha::kCacheQ4 ? mha::kRowsQ4Keys : mha::rows_tile_keys();
+  const int small = kind == mha::kCacheQ4 ? mha::kRowsQ4Box : mha::rows_box_keys();
   auto encode = [&](CUtensorMap* m, const void* base, int keys) {
+    if (kind == mha::kCacheQ4) return encode_map_q4(m, base, B, Lk, H_kv, d_k, plan.width, keys);
     return f8 ? encode_map_f8(m, base, B, Lk, H_kv, d_k, keys) : encode_map(m, base, B, Lk, H_kv, d_k, keys);
   };
-  if (plan.form != mha::kRowsShort && plan.form != mha::kRowsQ4 &&
-      (!encode(&p.tm_k, k_cache, mha::rows_tile_keys()) || !encode(&p.tm_v, v_cache, mha::rows_tile_keys()) ||
-      !encode(&p.tm_k_box, k_cache, mha::rows_box_keys()) ||
-      !encode(&p.tm_v_box, v_cache, mha::rows_box_keys())))
+  if (plan.form != mha::kRowsShort &&
+      (!encode(&p.tm_k, k_cache, tile) || !encode(&p.tm_v, v_cache, tile) ||
+       !encode(&p.tm_k_box, k_cache, small) || !encode(&p.tm_v_box, v_cache, small)))
     return MHA_ERR_UNSUPPORTED;
   p.q = q;
   p.k_codes = k_cache;

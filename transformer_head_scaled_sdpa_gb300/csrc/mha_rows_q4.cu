@@ -46,26 +46,54 @@ namespace mha {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr float kLift = 8.f;    // weights are 2^kLift at their reference
-constexpr float kSlack = 7.f;   // and stay below 2^(kLift + kSlack), inside fp16's range
+constexpr int kTile = kRowsQ4Keys;  // keys of a warp's tile
+constexpr float kLift = 8.f;        // weights are 2^kLift at their reference
+constexpr float kSlack = 7.f;       // and stay below 2^(kLift + kSlack), inside fp16's range
 constexpr float kNoRef = -3.0e38f;  // a row that has seen no key
+constexpr int kRoleRowsQ4 = 20;
 
-template <int W_, int NT_, int KT_, int CTAS_>
+// W: widest head; NT: blocks of 8 rows; FEW: a row or two, whose columns hold four
+// parts of the keys each; ST: tiles in a warp's ring; CTAS: per SM.
+template <int W_, int NT_, bool FEW_, int ST_, int CTAS_>
 struct Q4Cfg {
-  static constexpr int W = W_;        // widest head
-  static constexpr int NT = NT_;      // blocks of 8 rows
-  static constexpr int KT = KT_;      // keys a warp has in registers
-  static constexpr int CTAS = CTAS_;  // per SM
-  static constexpr int NR = 8 * NT;
-  static constexpr int MT = KT / 16;  // blocks of 16 keys
-  static constexpr int KW = W / 32;   // words of a key's row per lane
-  static constexpr int VW = W / 64;   // words of a value's row per lane
-  static constexpr int FT = W / 16;   // blocks of 16 features
+  static constexpr int W = W_, NT = NT_, ST = ST_, CTAS = CTAS_;
+  static constexpr bool FEW = FEW_;
+  static_assert(!FEW || NT == 1, "one block of columns");
+  static constexpr int NR = FEW ? 2 : 8 * NT;  // rows of a unit
+  static constexpr int ROW = W / 2;            // bytes of a tile's row
+  static constexpr int KW = W / 32;            // words of a key's row per lane
+  static constexpr int VW = W / 64;            // words of a value's row per lane
+  static constexpr int FT = W / 16;            // blocks of 16 features
   static constexpr bool Q_SHARED = W * NT > 128;  // Q's fragments in shared memory
   // merge: a warp's row of sums, eight lanes' features 4 floats apart
-  static constexpr int GS = W / 8 + 4;
-  static constexpr int RS = 8 * GS + 2;
+  static constexpr int GS = W / 8 + 4, RS = 8 * GS + 2;
+  static constexpr int TILE = kTile * ROW;     // bytes of a tile's keys, and of its values
+  static constexpr int RING = ST * 2 * TILE;   // a warp's; its sums at the end
+  static_assert(RING >= 8 * RS * 4 && RING % 1024 == 0, "ring");
+  static constexpr int OFF_BAR = kWarps * RING;                  // [warp][stage]
+  static constexpr int OFF_ABORT = OFF_BAR + kWarps * ST * 8;
+  static constexpr int OFF_MASKS = (OFF_ABORT + 4 + 15) / 16 * 16;  // uint64 [NR][4]
+  static constexpr int OFF_STATS = OFF_MASKS + NR * 32;          // float [warp][NR][3]
+  static constexpr int OFF_KEYS = (OFF_STATS + kWarps * NR * 12 + 15) / 16 * 16;  // float4 [warp][32], float [warp][32]
+  static constexpr int OFF_Q = OFF_KEYS + (FEW ? 0 : kWarps * kTile * 20);        // uint2 [2 KW NT][32]
+  static constexpr int SMEM = OFF_Q + (Q_SHARED ? 2 * KW * NT * 256 : 0) + 1024;
 };
+
+// Where row g of a block of 8 scores lies in its block of 8 keys.  A lane of scores
+// (g, j) reads the key of row g, one of values the keys of rows 2 j and 2 j + 1; in
+// this order neither reads two rows out of the same banks at once (W 64: rows of 32
+// bytes as they are; 128: of 64, TMA's 64-byte swizzle; 256: of 128, the 128-byte one).
+template <int W>
+__device__ __forceinline__ int key_of_row(int g) {
+  constexpr uint32_t order = W == 64 ? 0x53427160u : (W == 128 ? 0x65217430u : 0x36147250u);
+  return static_cast<int>((order >> (4 * g)) & 7u);
+}
+// Byte `at` of row `key` of a tile as TMA wrote it.
+template <int W>
+__device__ __forceinline__ uint32_t tile_at(int key, int at) {
+  const int chunk = W == 64 ? at >> 4 : (W == 128 ? (at >> 4) ^ ((key >> 1) & 3) : (at >> 4) ^ (key & 7));
+  return static_cast<uint32_t>(key * (W / 2) + chunk * 16 + (at & 15));
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -94,30 +122,59 @@ __device__ __forceinline__ float lg2_approx(float x) {
   return y;
 }
 
-// N consecutive words (N * 4-byte aligned up to 16).
+// N consecutive words of shared memory.
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t* w) {
+__device__ __forceinline__ void ld_shared(uint32_t at, uint32_t* w) {
   if constexpr (N == 1) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
   } else if constexpr (N == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-    w[0] = v.x, w[1] = v.y;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
   } else {
     static_assert(N == 4, "words");
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at)
+                 : "memory");
   }
+}
+
+// What a key's offset and step, and its value's, come to in a step.
+struct KeyFactors {
+  float step, lo;         // of the key
+  float v_log, v_inv, v_ofs;  // of the value: log2 step, 1 / step, lo / step
+};
+__device__ __forceinline__ KeyFactors key_factors(uint32_t k, uint32_t v) {
+  KeyFactors f;
+  f.step = bf16_hi(k);
+  f.lo = bf16_lo(k);
+  const float step = bf16_hi(v);
+  f.v_log = lg2_approx(step);
+  f.v_inv = __frcp_rn(step);
+  f.v_ofs = bf16_lo(v) * f.v_inv;
+  return f;
 }
 
 template <class C>
 __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int W = C::W, NT = C::NT, KT = C::KT, MT = C::MT, KW = C::KW, VW = C::VW, FT = C::FT, NR = C::NR;
-  __shared__ __align__(16) float sums[kWarps][NR][C::RS];   // O of each warp
-  __shared__ float stats[kWarps][NR][3];                    // m, l and the offsets' sum
-  __shared__ uint64_t masks[NR][4];
-  __shared__ uint2 q_frags[C::Q_SHARED ? 2 * KW * NT : 1][32];
+  constexpr int W = C::W, NT = C::NT, KW = C::KW, VW = C::VW, FT = C::FT, NR = C::NR;
+  constexpr bool FEW = C::FEW;
+  constexpr int MT = kTile / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
+  uint64_t(*masks)[4] = reinterpret_cast<uint64_t(*)[4]>(smem + C::OFF_MASKS);
+  float(*stats)[NR][3] = reinterpret_cast<float(*)[NR][3]>(smem + C::OFF_STATS);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, j = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  const uint32_t bars = smem_u32(smem) + C::OFF_BAR + warp * C::ST * 8;
+  if (lane == 0) {
+    for (int s = 0; s < C::ST; ++s) mbar_init(bars + 8 * s, 1);
+    if (warp == 0) *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
   griddep_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -141,6 +198,45 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
     it = unit_of(p, index, blocks, part % p.B, part / p.B, 0);
   }
   if (it.splits == 0) return;
+
+  // ---- a warp's tiles: keys first + 32 warp .., every 128; two copies of each in flight
+  const int stop = min(it.t1 * kKeys, it.end);
+  const int first = it.t0 * kKeys + warp * kTile;
+  auto request = [&](int key, int stage) {
+    const uint32_t bar = bars + 8 * stage, dst = ring + stage * 2 * C::TILE;
+    const int rows = min(kTile, stop - key);
+    if (rows == kTile) {
+      mbar_arrive_expect_tx(bar, 2 * C::TILE);
+      tma_load_4d(dst, &p.tm_k, bar, 0, it.hk, key, it.b);
+      tma_load_4d(dst + C::TILE, &p.tm_v, bar, 0, it.hk, key, it.b);
+    } else {
+      // a ragged one in boxes of kRowsQ4Box keys as far as it goes (what lies behind in
+      // the ring are some codes: finite, and their weights are 0)
+      const int boxes = (rows + kRowsQ4Box - 1) / kRowsQ4Box;
+      mbar_arrive_expect_tx(bar, 2 * boxes * kRowsQ4Box * C::ROW);
+      for (int x = 0; x < boxes; ++x) {
+        const uint32_t to = dst + x * kRowsQ4Box * C::ROW;
+        tma_load_4d(to, &p.tm_k_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
+        tma_load_4d(to + C::TILE, &p.tm_v_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
+      }
+    }
+  };
+  if (lane == 0)
+    for (int s = 0; s < C::ST; ++s)
+      if (first + s * kKeys < stop) request(first + s * kKeys, s);
+  // lane's key's offsets and steps, a tile ahead (keys past the end: the last one's)
+  const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
+  const uint32_t* k_scale = reinterpret_cast<const uint32_t*>(p.k_scale) + scales;
+  const uint32_t* v_scale = reinterpret_cast<const uint32_t*>(p.v_scale) + scales;
+  // (lane (g, j) has row g of block j of 8 keys)
+  const int own = 8 * j + key_of_row<W>(g);
+  uint32_t ks = 0, vs = 0;
+  if (first < stop) {
+    const int key = min(first + own, stop - 1);
+    ks = __ldg(k_scale + key);
+    vs = __ldg(v_scale + key);
+  }
+
   // Output row of row r of the unit (-1 past the last), t: its drafted token.
   auto out_row = [&](int r, int* t) {
     const int gr = it.rb * NR + r;
@@ -150,63 +246,16 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
     return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
   };
 
-  const int stop = min(it.t1 * kKeys, it.end);  // keys first .. stop - 1 are the unit's
-  const long long pitch = static_cast<long long>(p.H_kv) * (p.d / 2);  // bytes between positions
-  const int key_bytes = static_cast<int>(pitch);
-  const long long base = static_cast<long long>(it.b) * p.Lk * pitch + static_cast<long long>(it.hk) * (p.d / 2);
-  // lane's part of a key's row: bytes 4 KW j (16 j and 64 + 16 j when 256 wide), of a value's: 4 VW g
-  constexpr int KV = KW > 4 ? 4 : KW;  // words loaded at once
-  const uint8_t* k_at = static_cast<const uint8_t*>(p.k_codes) + base + 4 * KV * j;
-  const uint8_t* v_at = static_cast<const uint8_t*>(p.v_codes) + base + 4 * VW * g;
-  const bool k_has[2] = {8 * KV * j < p.d, 128 + 8 * KV * j < p.d};
-  const bool v_has = 8 * VW * g < p.d;  // (d is a multiple of 32: a lane's part is inside the row or past it)
-  const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
-  const uint32_t* k_scale = reinterpret_cast<const uint32_t*>(p.k_scale) + scales;
-  const uint32_t* v_scale = reinterpret_cast<const uint32_t*>(p.v_scale) + scales;
-
-  uint32_t kc[MT][2][KW], vc[MT][4][VW], ks[MT][2], vs[MT][2];
-  // (keys past the end are the last one again: their weight is 0)
-  auto load_k = [&](int key0) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = min(key0 + 16 * m + 8 * h + g, stop - 1);
-        const uint8_t* at = k_at + static_cast<long long>(key) * key_bytes;
-#pragma unroll
-        for (int w = 0; w < KW; w += KV) {
-#pragma unroll
-          for (int x = 0; x < KV; ++x) kc[m][h][w + x] = 0;
-          if (k_has[w / KV]) load_words<KV>(at + 16 * w, kc[m][h] + w);
-        }
-        ks[m][h] = __ldg(k_scale + key);
-        vs[m][h] = __ldg(v_scale + key);
-      }
-  };
-  auto load_v = [&](int key0) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int key = min(key0 + 16 * m + 2 * j + (x & 1) + 8 * (x >> 1), stop - 1);
-#pragma unroll
-        for (int y = 0; y < VW; ++y) vc[m][x][y] = 0;
-        if (v_has) load_words<VW>(v_at + static_cast<long long>(key) * key_bytes, vc[m][x]);
-      }
-  };
-  int key0 = it.t0 * kKeys + warp * KT;
-  if (key0 < stop) {
-    load_k(key0);
-    load_v(key0);
-  }
-
-  // ---- Q: lane (g, j) holds the features of its part of the keys' rows, of rows 8 n + g
+  // ---- Q: lane (g, j) holds the features of its part of the keys' rows, of the row of
+  // column 8 n + g (FEW: the even columns are row 0, the odd ones row 1)
   uint2 q[C::Q_SHARED ? 1 : 2 * KW * NT];
-  float fa[NT][2], fb[NT][2];  // factors of a row's product and of its sum: rows 8 n + 2 j, + 1
+  uint2* q_shared = reinterpret_cast<uint2*>(smem + C::OFF_Q) + lane;
+  float fa[NT][2], fb[NT][2];  // factors of a row's product and of its sum: columns 8 n + 2 j, + 1
+  constexpr int KV = KW > 4 ? 4 : KW;  // words loaded at once: 16 j .. (256 wide: and 64 + 16 j ..)
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     int t;
-    const int out = out_row(8 * n + g, &t);
+    const int out = out_row(FEW ? g & 1 : 8 * n + g, &t);
     const bool live = out >= 0 && t < it.live;
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + static_cast<long long>(max(out, 0)) * p.d;
     uint4 v[KW];
@@ -237,7 +286,7 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
         const uint2 b = make_uint2(pack_f16x2(y[2 * h], y[4 + 2 * h]),
                                    pack_f16x2(y[2 * h + 1] * 0.0625f, y[5 + 2 * h] * 0.0625f));
         if constexpr (C::Q_SHARED) {
-          if (warp == 0) q_frags[(2 * w + h) * NT + n][lane] = b;
+          if (warp == 0) q_shared[((2 * w + h) * NT + n) * 32] = b;
         } else {
           q[(2 * w + h) * NT + n] = b;
         }
@@ -248,8 +297,9 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
     const float f = pow2i(e) * p.scale_log2;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      fa[n][r] = __shfl_sync(0xffffffffu, f * 16777216.f, 8 * j + 4 * r);
-      fb[n][r] = __shfl_sync(0xffffffffu, f * sum, 8 * j + 4 * r);
+      const int from = FEW ? 4 * r : 8 * j + 4 * r;
+      fa[n][r] = __shfl_sync(0xffffffffu, f * 16777216.f, from);
+      fb[n][r] = __shfl_sync(0xffffffffu, f * sum, from);
     }
   }
   // the rows' mask words (a chain's: bits 0 .. t)
@@ -270,7 +320,7 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
   __syncthreads();
 
   float o[NT][FT][4];
-  float ref[NT][2], l[NT][2], ofs[NT][2];
+  float ref[NT][2], l[NT][2], ofs[NT][2];  // references less kLift
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -284,11 +334,24 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
       ofs[n][r] = 0.f;
     }
   }
+  // lane's places in a tile: the key of row g, the values of rows 2 j and 2 j + 1
+  uint32_t k_at[KW / KV], v_at[2];
+#pragma unroll
+  for (int w = 0; w < KW / KV; ++w) k_at[w] = tile_at<W>(key_of_row<W>(g), 64 * w + 4 * KV * j);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) v_at[x] = C::TILE + tile_at<W>(key_of_row<W>(2 * j + x), 4 * VW * g);
+  float4* keys = reinterpret_cast<float4*>(smem + C::OFF_KEYS) + warp * kTile;
+  float* keys_ofs = reinterpret_cast<float*>(smem + C::OFF_KEYS + kWarps * kTile * 16) + warp * kTile;
 
+  bool ok = true;
+  int stage = 0;
+  uint32_t parity = 0;
 #pragma unroll 1
-  for (; key0 < stop; key0 += kWarps * KT) {
-    const int next = key0 + kWarps * KT;
-    // ---- scores: s[n][m] = keys g (+ 8) of block m, rows 2 j, 2 j + 1 of block n
+  for (int key0 = first; key0 < stop; key0 += kKeys) {
+    const uint32_t tile = ring + stage * 2 * C::TILE;
+    ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + stage));
+    if (!ok) break;
+    // ---- scores: s[n][m] = keys of rows g, 8 + g of block m, columns 2 j, 2 j + 1 of block n
     float s[NT][MT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -297,199 +360,307 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[n][m][x] = 0.f;
 #pragma unroll
-    for (int w = 0; w < KW; ++w)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint2 b[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if constexpr (C::Q_SHARED) b[n] = q_frags[(2 * w + h) * NT + n][lane];
-          else b[n] = q[(2 * w + h) * NT + n];
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint32_t x0 = h ? kc[m][0][w] >> 8 : kc[m][0][w], x1 = h ? kc[m][1][w] >> 8 : kc[m][1][w];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma_f16(s[n][m], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, b[n].x, b[n].y);
-        }
-      }
-    // a key's factor, offset, and (log2 of) its value's step
-    float k_lo[MT][2], k_step[MT][2], v_log[MT][2], v_inv[MT][2], v_ofs[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        k_lo[m][h] = bf16_lo(ks[m][h]);
-        k_step[m][h] = bf16_hi(ks[m][h]);
-        const float step = bf16_hi(vs[m][h]);
-        v_log[m][h] = lg2_approx(step);
-        v_inv[m][h] = __frcp_rn(step);
-        v_ofs[m][h] = bf16_lo(vs[m][h]) * v_inv[m][h];
-      }
-    if (next < stop) load_k(next);
-    // ---- weights
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int w0 = 0; w0 < KW; w0 += KV) {
+      uint32_t kc[MT][2][KV];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int h = x >> 1, r = x & 1;
-          s[n][m][x] = fmaf(s[n][m][x] * fa[n][r], k_step[m][h], fmaf(fb[n][r], k_lo[m][h], v_log[m][h]));
-        }
-    const bool masked = key0 + KT > min(it.n, stop);
-    if (masked) {
+        for (int h = 0; h < 2; ++h) ld_shared<KV>(tile + k_at[w0 / KV] + (16 * m + 8 * h) * C::ROW, kc[m][h]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int w = 0; w < KV; ++w)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int key = key0 + 16 * m + 8 * h + g, off = key - it.n;
-          bool any = false;
+          uint2 b[NT];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n) {
+            const int i = (2 * (w0 + w) + h) * NT + n;
+            if constexpr (C::Q_SHARED) b[n] = q_shared[i * 32];
+            else b[n] = q[i];
+          }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              bool sees = key < stop;
-              if (sees && off >= 0)  // (off < 256: the drafted tokens end there)
-                sees = (masks[8 * n + 2 * j + r][off >> 6] >> (off & 63)) & 1;
-              if (!sees) s[n][m][2 * h + r] = -INFINITY;
-              any = any || sees;
-            }
-          // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
-          if (!any) v_inv[m][h] = v_ofs[m][h] = 0.f;
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t x0 = h ? kc[m][0][w] >> 8 : kc[m][0][w], x1 = h ? kc[m][1][w] >> 8 : kc[m][1][w];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_f16(s[n][m], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, b[n].x, b[n].y);
+          }
         }
     }
-    float top = -INFINITY;
+    // ---- weights
+    const KeyFactors mine = key_factors(ks, vs);
+    if (key0 + kKeys < stop) {
+      const int key = min(key0 + kKeys + own, stop - 1);
+      ks = __ldg(k_scale + key);
+      vs = __ldg(v_scale + key);
+    }
+    const bool masked = key0 + kTile > min(it.n, stop);
+    uint32_t pt[NT][MT][2];  // weights transposed: column g, keys of rows 2 j, 2 j + 1 (+ 8)
+    if constexpr (FEW) {
+      // every column pair has all the keys' scores: lane (g, j) takes those of its own key
+      float x[2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int r = 0; r < 2; ++r) {
+        const float lo = j & 1 ? s[0][0][2 + r] : s[0][0][r], hi = j & 1 ? s[0][1][2 + r] : s[0][1][r];
+        x[r] = fmaf((j & 2 ? hi : lo) * fa[0][r], mine.step, fmaf(fb[0][r], mine.lo, mine.v_log));
+      }
+      float v_inv = mine.v_inv, v_ofs = mine.v_ofs;
+      if (masked) {
+        const int key = key0 + own, off = key - it.n;
+        bool any = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) top = fmax3(top, s[n][m][r] - ref[n][r], s[n][m][2 + r] - ref[n][r]);
-    if (__any_sync(0xffffffffu, top > kSlack)) {
-      // references up to this tile's maxima, what was summed down by as much
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
+        for (int r = 0; r < 2; ++r) {
+          bool sees = key < stop;
+          if (sees && off >= 0) sees = (masks[r][off >> 6] >> (off & 63)) & 1;  // (off < 256: drafted tokens end there)
+          if (!sees) x[r] = -INFINITY;
+          any = any || sees;
+        }
+        // (what hides from both may hold anything, and 0 * NaN would be NaN)
+        if (!any) v_inv = v_ofs = 0.f;
+      }
+      if (__any_sync(0xffffffffu, fmaxf(x[0] - ref[0][0], x[1] - ref[0][1]) > kLift + kSlack)) {
+        // references up to this tile's maxima, what was summed down by as much
         float by[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float m = ref[n][r];
+          float m = x[r];
 #pragma unroll
-          for (int x = 0; x < MT; ++x) m = fmax3(m, s[n][x][r], s[n][x][2 + r]);
-#pragma unroll
-          for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-          by[r] = ex2_approx(ref[n][r] - m);
-          ref[n][r] = m;
-          l[n][r] *= by[r];
-          ofs[n][r] *= by[r];
+          for (int z = 1; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+          m = fmaxf(ref[0][r], m - kLift);
+          by[r] = ex2_approx(ref[0][r] - m);
+          ref[0][r] = m;
+          l[0][r] *= by[r];
+          ofs[0][r] *= by[r];
         }
 #pragma unroll
         for (int f = 0; f < FT; ++f)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) o[n][f][x] *= by[x & 1];
+          for (int z = 0; z < 4; ++z) o[0][f][z] *= by[z & 1];
       }
-    }
-    uint32_t pt[NT][MT][2];  // weights transposed: row g, keys 2 j, 2 j + 1 (+ 8)
+      const float w0 = ex2_approx(x[0] - ref[0][0]), w1 = ex2_approx(x[1] - ref[0][1]);
+      fma2(l[0][0], l[0][1], w0, w1, v_inv, v_inv, l[0][0], l[0][1]);
+      const uint32_t w = pack_f16x2(w0, w1);
+      // (the offsets with the rounded weights, as the codes have them: what the
+      // rounding does to both is relative to the value, not to its two parts)
+      fma2(ofs[0][0], ofs[0][1], half_lo(w), half_hi(w), v_ofs, v_ofs, ofs[0][0], ofs[0][1]);
+      // columns 2 j, 2 j + 1 of block j's keys: a column pair sums a quarter of the keys
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) pt[0][m][h] = transposed(j == 2 * m + h ? w : 0u);
+    } else {
+      // the keys' factors by way of shared memory: lane's own key to the lanes of its row
+      const int slot = 8 * j + g;  // (row g of block j)
+      __syncwarp();  // (the tile before is read)
+      keys[slot] = make_float4(mine.step, mine.lo, mine.v_log, mine.v_inv);
+      keys_ofs[slot] = mine.v_ofs;
+      __syncwarp();
+      float4 kf[MT][2];
+      float v_ofs[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float w0 = ex2_approx(s[n][m][2 * h] - ref[n][0] + kLift);
-          const float w1 = ex2_approx(s[n][m][2 * h + 1] - ref[n][1] + kLift);
-          l[n][0] = fmaf(w0, v_inv[m][h], l[n][0]);
-          l[n][1] = fmaf(w1, v_inv[m][h], l[n][1]);
-          const uint32_t w = pack_f16x2(w0, w1);
-          // (the offsets with the rounded weights, as the codes have them: what the
-          // rounding does to both is relative to the value, not to its two parts)
-          ofs[n][0] = fmaf(half_lo(w), v_ofs[m][h], ofs[n][0]);
-          ofs[n][1] = fmaf(half_hi(w), v_ofs[m][h], ofs[n][1]);
-          pt[n][m][h] = transposed(w);
+          kf[m][h] = keys[16 * m + 8 * h + g];
+          v_ofs[m][h] = keys_ofs[16 * m + 8 * h + g];
         }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float t0, t1, u0, u1;
+            mul2(t0, t1, s[n][m][2 * h], s[n][m][2 * h + 1], fa[n][0], fa[n][1]);
+            fma2(u0, u1, fb[n][0], fb[n][1], kf[m][h].y, kf[m][h].y, kf[m][h].z, kf[m][h].z);
+            fma2(s[n][m][2 * h], s[n][m][2 * h + 1], t0, t1, kf[m][h].x, kf[m][h].x, u0, u1);
+          }
+      if (masked) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = key0 + 16 * m + 8 * h + key_of_row<W>(g), off = key - it.n;
+            bool any = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                bool sees = key < stop;
+                if (sees && off >= 0)  // (off < 256: the drafted tokens end there)
+                  sees = (masks[8 * n + 2 * j + r][off >> 6] >> (off & 63)) & 1;
+                if (!sees) s[n][m][2 * h + r] = -INFINITY;
+                any = any || sees;
+              }
+            // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
+            if (!any) kf[m][h].w = v_ofs[m][h] = 0.f;
+          }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float m = fmaxf(s[n][0][r], s[n][0][2 + r]);
+#pragma unroll
+          for (int x = 1; x < MT; ++x) m = fmax3(m, s[n][x][r], s[n][x][2 + r]);
+          top = fmaxf(top, m - ref[n][r]);
+        }
+      if (__any_sync(0xffffffffu, top > kLift + kSlack)) {
+        // references up to this tile's maxima, what was summed down by as much
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float by[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float m = fmaxf(s[n][0][r], s[n][0][2 + r]);
+#pragma unroll
+            for (int x = 1; x < MT; ++x) m = fmax3(m, s[n][x][r], s[n][x][2 + r]);
+#pragma unroll
+            for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+            m = fmaxf(ref[n][r], m - kLift);
+            by[r] = ex2_approx(ref[n][r] - m);
+            ref[n][r] = m;
+            l[n][r] *= by[r];
+            ofs[n][r] *= by[r];
+          }
+#pragma unroll
+          for (int f = 0; f < FT; ++f)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[n][f][x] *= by[x & 1];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float w0, w1;
+            add2(w0, w1, s[n][m][2 * h], s[n][m][2 * h + 1], -ref[n][0], -ref[n][1]);
+            w0 = ex2_approx(w0);
+            w1 = ex2_approx(w1);
+            fma2(l[n][0], l[n][1], w0, w1, kf[m][h].w, kf[m][h].w, l[n][0], l[n][1]);
+            const uint32_t w = pack_f16x2(w0, w1);
+            // (the offsets with the rounded weights, as the codes have them: what the
+            // rounding does to both is relative to the value, not to its two parts)
+            fma2(ofs[n][0], ofs[n][1], half_lo(w), half_hi(w), v_ofs[m][h], v_ofs[m][h], ofs[n][0], ofs[n][1]);
+            pt[n][m][h] = transposed(w);
+          }
+    }
     // ---- o += V^T P^T
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
+      uint32_t vc[4][VW];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) ld_shared<VW>(tile + v_at[x & 1] + (16 * m + 8 * (x >> 1)) * C::ROW, vc[x]);
 #pragma unroll
       for (int y = 0; y < VW; ++y)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const uint32_t sel = 0x4400u + 0x1111u * b;  // byte b of two keys' words
-          const uint32_t x0 = __byte_perm(vc[m][0][y], vc[m][1][y], sel);
-          const uint32_t x1 = __byte_perm(vc[m][2][y], vc[m][3][y], sel);
+          const uint32_t x0 = __byte_perm(vc[0][y], vc[1][y], sel);
+          const uint32_t x1 = __byte_perm(vc[2][y], vc[3][y], sel);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             mma_f16(o[n][4 * y + b], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu, x1 & 0x00f000f0u,
                     pt[n][m][0], pt[n][m][1]);
         }
-    if (next < stop) load_v(next);
+    }
+    __syncwarp();  // (every lane has read the tile)
+    if (lane == 0 && key0 + C::ST * kKeys < stop) request(key0 + C::ST * kKeys, stage);
+    if (++stage == C::ST) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+  if (!ok) {
+    // gave up: the copies in flight must land before the CTA exits (each wait is bounded)
+    volatile int never = 0;
+    for (int s = 0; s < C::ST; ++s) mbar_wait(bars + 8 * s, parity ^ (s < stage ? 1 : 0), &never, p.status, 0);
   }
 
   // ---- the warps' sums together
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
 #pragma unroll
-      for (int z = 4; z < 32; z <<= 1) {
+      for (int z = FEW ? 1 : 4; z < 32; z <<= 1) {
         l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], z);
         ofs[n][r] += __shfl_xor_sync(0xffffffffu, ofs[n][r], z);
       }
-      if (g == 0) {
-        stats[warp][8 * n + 2 * j + r][0] = ref[n][r];
-        stats[warp][8 * n + 2 * j + r][1] = l[n][r];
-        stats[warp][8 * n + 2 * j + r][2] = ofs[n][r];
+      const int row = FEW ? r : 8 * n + 2 * j + r;
+      if (FEW ? lane == 0 : g == 0) {
+        stats[warp][row][0] = ref[n][r];
+        stats[warp][row][1] = l[n][r];
+        stats[warp][row][2] = ofs[n][r];
       }
+    }
+  const bool whole = it.splits == 1;
+  const long long first_part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
+  auto sums = [&](int w, int column, int at) {
+    return reinterpret_cast<float*>(smem + w * C::RING) + column * C::RS + at;
+  };
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (n > 0) {
+      if (it.rb * NR + 8 * n >= n_rows) break;
+      __syncthreads();  // (the block before is read)
     }
 #pragma unroll
     for (int f = 0; f < FT; ++f)
 #pragma unroll
       for (int x = 0; x < 4; ++x)  // (codes are 2^-24, odd features 2^-20)
-        sums[warp][8 * n + 2 * j + (x & 1)][C::GS * g + 2 * f + (x >> 1)] =
-            o[n][f][x] * (x >> 1 ? 1048576.f : 16777216.f);
-  }
-  __syncthreads();
-  const bool whole = it.splits == 1;
-  const long long first_part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
-  for (int x = static_cast<int>(threadIdx.x); x < NR * (W / 2); x += 32 * kWarps) {
-    const int r = x / (W / 2), f = 2 * (x % (W / 2));
-    int t;
-    const int out = out_row(r, &t);
-    if (out < 0) break;  // (rows only grow)
-    float m = kNoRef;
+        *sums(warp, 2 * j + (x & 1), C::GS * g + 2 * f + (x >> 1)) = o[n][f][x] * (x >> 1 ? 1048576.f : 16777216.f);
+    __syncthreads();
+    for (int x = static_cast<int>(threadIdx.x); x < (FEW ? 2 : 8) * (W / 2); x += 32 * kWarps) {
+      const int c = x / (W / 2), r = 8 * n + c, f = 2 * (x % (W / 2));
+      int t;
+      const int out = out_row(r, &t);
+      if (out < 0) break;  // (rows only grow)
+      float m = kNoRef;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stats[w][r][0]);
-    float y0 = 0.f, y1 = 0.f, L = 0.f;
-    if (t < it.live && m != kNoRef) {
-      float add = 0.f;
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stats[w][r][0]);
+      float y0 = 0.f, y1 = 0.f, L = 0.f;
+      if (t < it.live && m != kNoRef && *abort_flag == 0) {
+        float add = 0.f;
+        const int at = C::GS * (f / (W / 8)) + f % (W / 8);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float a = ex2_approx(stats[w][r][0] - m);
-        const float2 v = *reinterpret_cast<const float2*>(&sums[w][r][C::GS * (f / (W / 8)) + f % (W / 8)]);
-        L = fmaf(a, stats[w][r][1], L);
-        add = fmaf(a, stats[w][r][2], add);
-        y0 = fmaf(a, v.x, y0);
-        y1 = fmaf(a, v.y, y1);
+        for (int w = 0; w < kWarps; ++w) {
+          const float a = ex2_approx(stats[w][r][0] - m);
+          L = fmaf(a, stats[w][r][1], L);
+          add = fmaf(a, stats[w][r][2], add);
+          float2 v = *reinterpret_cast<const float2*>(sums(w, c, at));
+          if constexpr (FEW) {
+#pragma unroll
+            for (int z = 2; z < 8; z += 2) {
+              const float2 u = *reinterpret_cast<const float2*>(sums(w, z + c, at));
+              v.x += u.x;
+              v.y += u.y;
+            }
+          }
+          y0 = fmaf(a, v.x, y0);
+          y1 = fmaf(a, v.y, y1);
+        }
+        y0 += add;
+        y1 += add;
       }
-      y0 += add;
-      y1 += add;
-    }
-    if (!whole) {
-      if (f == 0) {
-        p.part_m[first_part + out] = L == 0.f ? -INFINITY : m - kLift;
-        p.part_l[first_part + out] = L;
+      if (!whole) {
+        if (f == 0) {
+          p.part_m[first_part + out] = L == 0.f ? -INFINITY : m;
+          p.part_l[first_part + out] = L;
+        }
+        *reinterpret_cast<float2*>(p.part_o + (first_part + out) * W + f) = make_float2(y0, y1);
+        continue;
       }
-      *reinterpret_cast<float2*>(p.part_o + (first_part + out) * W + f) = make_float2(y0, y1);
-      continue;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      if (f < p.d)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d + f) =
+            pack_bf16x2(y0 * inv, y1 * inv);
+      if (p.lse && f == 0)
+        p.lse[(static_cast<long long>(it.b) * p.H + out % p.H) * p.T + t] =
+            L == 0.f ? -INFINITY : (m + __log2f(L)) * 0.69314718055994531f;
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    if (f < p.d)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d + f) =
-          pack_bf16x2(y0 * inv, y1 * inv);
-    if (p.lse && f == 0)
-      p.lse[(static_cast<long long>(it.b) * p.H + out % p.H) * p.T + t] =
-          L == 0.f ? -INFINITY : (m - kLift + __log2f(L)) * 0.69314718055994531f;
   }
 }
 
@@ -497,14 +668,42 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
 template <typename F>
 void with_config(int d, int R, F&& f) {
   if (d <= 64) {
-    if (R <= 8) f(Q4Cfg<64, 1, 32, 5>{});
-    else f(Q4Cfg<64, 2, 32, 4>{});
+    if (R <= 2) f(Q4Cfg<64, 1, true, 4, 6>{});
+    else if (R <= 8) f(Q4Cfg<64, 1, false, 4, 5>{});
+    else f(Q4Cfg<64, 2, false, 4, 4>{});
   } else if (d <= 128) {
-    if (R <= 8) f(Q4Cfg<128, 1, 32, 4>{});
-    else f(Q4Cfg<128, 2, 32, 2>{});
+    if (R <= 2) f(Q4Cfg<128, 1, true, 2, 5>{});
+    else if (R <= 8) f(Q4Cfg<128, 1, false, 2, 4>{});
+    else if (R <= 16) f(Q4Cfg<128, 2, false, 3, 3>{});
+    else f(Q4Cfg<128, 4, false, 3, 2>{});
   } else {
-    f(Q4Cfg<256, 1, 16, 3>{});
+    if (R <= 2) f(Q4Cfg<256, 1, true, 2, 3>{});
+    else if (R <= 8) f(Q4Cfg<256, 1, false, 2, 3>{});
+    else f(Q4Cfg<256, 2, false, 2, 2>{});
   }
+}
+
+template <class C>
+cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static bool attr_set[64] = {};
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(rows_q4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
+  e = launch_serialized(rows_q4_kernel<C>, grid, dim3(32 * kWarps), C::SMEM, stream, p);
+  if (info) {
+    info->kernels = 1;
+    info->grid = static_cast<int>(grid.x);
+    info->block = 32 * kWarps;
+    info->smem = C::SMEM;
+  }
+  return e;
 }
 
 }  // namespace
@@ -522,16 +721,7 @@ RowsQ4Shape rows_q4_shape(int d, int R) {
 
 cudaError_t launch_rows_q4(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
   cudaError_t e = cudaSuccess;
-  const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
-  with_config(p.d, p.T * p.G, [&](auto cfg) {
-    e = launch_serialized(rows_q4_kernel<decltype(cfg)>, grid, dim3(32 * kWarps), 0, stream, p);
-  });
-  if (info) {
-    info->kernels = 1;
-    info->grid = static_cast<int>(grid.x);
-    info->block = 32 * kWarps;
-    info->smem = 0;
-  }
+  with_config(p.d, p.T * p.G, [&](auto cfg) { e = launch_cfg<decltype(cfg)>(p, stream, info); });
   return e;
 }
 

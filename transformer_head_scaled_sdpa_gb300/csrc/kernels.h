@@ -265,8 +265,8 @@ struct RowsPlan {
 RowsPlan rows_plan(int B, int T, int H, int H_kv, int Lk, int d, CacheKind kind);
 int rows_tile_keys();
 int rows_box_keys();
-// Keys of the 4-bit kernel's TMA boxes: a warp's tile, and a piece of a ragged one.
-constexpr int kRowsQ4Keys = 32, kRowsQ4Box = 8;
+// Keys of the 4-bit kernels' TMA boxes: a tile, and a piece of a ragged one.
+constexpr int kRowsQ4Keys = 128, kRowsQ4Box = 16;
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
 
 }  // namespace mha

@@ -226,8 +226,8 @@ bool encode_map_f8(CUtensorMap* m, const void* base, int B, int L, int H, int d,
 }
 
 // 4-D map over a 4-bit cache's packed rows [B, L, H, d / 2]; box = the kernel's width
-// (64, 128 or 256 features) x 1 head x `rows` rows x 1 sequence, rows of 32 bytes as they
-// are, of 64 or 128 with the swizzle of that size.
+// (64, 128 or 256 features) x 1 head x `rows` rows x 1 sequence, with the swizzle of a
+// row's size (32, 64 or 128 bytes).
 bool encode_map_q4(CUtensorMap* m, const void* base, int B, int L, int H, int d, int width, int rows) {
   const cuuint64_t row = static_cast<cuuint64_t>(d) / 2;
   const cuuint64_t dims[4] = {row, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(L),
@@ -237,7 +237,7 @@ bool encode_map_q4(CUtensorMap* m, const void* base, int B, int L, int H, int d,
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  width == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                  width == 64 ? CU_TENSOR_MAP_SWIZZLE_32B
                               : (width == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B),
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -35,27 +35,28 @@ struct Move {
 // The largest power of two of columns with which m moves (1 .. kBlockItems) of each are a block's items.
 __device__ __forceinline__ int log_columns(int m) { return 31 - __clz(kBlockItems / m); }
 
-// One element of type V for each of `count` items: source(i) and target(i) are its
-// addresses (null: nothing to move).
+// One element of type V for each of `count` items: locate(i, &to, &from) gives its
+// addresses, false where nothing moves.  (Asked again for the writes: eight pairs of
+// addresses kept beside eight elements took 124 registers.)
 template <typename V, typename F>
-__device__ __forceinline__ void move_items(int count, F&& addresses) {
+__device__ __forceinline__ void move_items(int count, F&& locate) {
   V x[kItems];
-  V* to[kItems];
 #pragma unroll
   for (int u = 0; u < kItems; ++u) {
     const int i = static_cast<int>(threadIdx.x) + u * kThreads;
-    to[u] = nullptr;
-    if (i < count) {
-      const V* from = nullptr;
-      addresses(i, &to[u], &from);
-      // (a coherent load: the source may be written later in this launch)
-      if (to[u]) x[u] = __ldcg(from);
-    }
+    V* to;
+    const V* from;
+    // (a coherent load: the source may be written later in this launch)
+    if (i < count && locate(i, &to, &from)) x[u] = __ldcg(from);
   }
   __syncthreads();
 #pragma unroll
-  for (int u = 0; u < kItems; ++u)
-    if (to[u]) *to[u] = x[u];
+  for (int u = 0; u < kItems; ++u) {
+    const int i = static_cast<int>(threadIdx.x) + u * kThreads;
+    V* to;
+    const V* from;
+    if (i < count && locate(i, &to, &from)) *to = x[u];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -69,16 +70,17 @@ __device__ __forceinline__ void fork_scales(const MoveParams& p, const Move* mov
   move_items<S>(n << lg, [&](int i, S** to, const S** from) {
     const Move m = moves[i >> lg];
     const long long e = e0 + (i & ((1 << lg) - 1));
-    if (e >= all) return;
+    if (e >= all) return false;
     const long long h = e / span;
     const int j = lo + static_cast<int>(e - h * span);
-    if (j < m.first || j >= m.end) return;
+    if (j < m.first || j >= m.end) return false;
     *to = at + (static_cast<long long>(m.to) * p.H + h) * p.Lk + j;
     *from = at + (static_cast<long long>(m.from) * p.H + h) * p.Lk + j;
+    return true;
   });
 }
 
-__global__ void __launch_bounds__(kThreads) cache_fork_kernel(const __grid_constant__ MoveParams p) {
+__global__ void __launch_bounds__(kThreads, 4) cache_fork_kernel(const __grid_constant__ MoveParams p) {
   __shared__ Move moves[kMaxForkSeqs];
   __shared__ int count, lowest, highest;
   if (threadIdx.x == 0) {
@@ -118,9 +120,10 @@ __global__ void __launch_bounds__(kThreads) cache_fork_kernel(const __grid_const
       move_items<uint4>(n << lg, [&](int i, uint4** to, const uint4** from) {
         const Move m = moves[i >> lg];
         const long long q = q0 + (i & ((1 << lg) - 1));
-        if (q >= stop || q < m.first * pieces || q >= m.end * pieces) return;
+        if (q >= stop || q < m.first * pieces || q >= m.end * pieces) return false;
         *to = at + m.to * seq + q;
         *from = at + m.from * seq + q;
+        return true;
       });
     } else {
       const long long y = x - 2 * chunks;
@@ -145,9 +148,10 @@ __device__ __forceinline__ void compact_scales(const MoveParams& p, const Move* 
   move_items<S>(n << lg, [&](int i, S** to, const S** from) {
     const Move m = moves[i >> lg];
     const int h = h0 + (i & ((1 << lg) - 1));
-    if (h >= p.H) return;
+    if (h >= p.H) return false;
     *to = at + static_cast<long long>(h) * p.Lk + m.to;
     *from = at + static_cast<long long>(h) * p.Lk + m.from;
+    return true;
   });
 }
 
@@ -183,9 +187,10 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
     move_items<uint4>(n << lg, [&](int i, uint4** to, const uint4** from) {
       const Move m = moves[i >> lg];
       const long long q = q0 + (i & ((1 << lg) - 1));
-      if (q >= pieces) return;
+      if (q >= pieces) return false;
       *to = at + m.to * pieces + q;
       *from = at + m.from * pieces + q;
+      return true;
     });
   } else {
     const int y = x - 2 * chunks, c = y >= scale_chunks, h0 = (c ? y - scale_chunks : y) << lg;
@@ -222,10 +227,10 @@ long long compact_blocks(const MoveParams& p) {
 }
 
 cudaError_t launch_cache_fork(const MoveParams& p, cudaStream_t stream, LaunchInfo* info) {
-  // blocks for every item that the capacity allows, at most six to an SM: what moves
+  // blocks for every item that the capacity allows, at most eight to an SM: what moves
   // is known on the device alone
   const double items = 2. * p.B * p.Lk * (p.row_bytes / 16 + (p.scale_bytes ? p.H : 0));
-  const unsigned most = 152 * 6;
+  const unsigned most = 152 * 8;
   const unsigned grid = items < static_cast<double>(most) * kBlockItems
                             ? static_cast<unsigned>(items / kBlockItems) + 1
                             : most;

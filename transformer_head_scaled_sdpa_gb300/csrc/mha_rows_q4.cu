@@ -45,65 +45,51 @@
 namespace mha {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTile = kRowsQ4Keys;  // keys of a warp's tile
-constexpr float kLift = 8.f;        // weights are 2^kLift at their reference
-constexpr float kSlack = 7.f;       // and stay below 2^(kLift + kSlack), inside fp16's range
+constexpr int kTile = 32;           // keys of a warp's part of a tile of kKeys
 constexpr float kNoRef = -3.0e38f;  // a row that has seen no key
 constexpr int kRoleRowsQ4 = 20;
+constexpr float kLift = 8.f;        // weights are 2^kLift at their reference
+constexpr float kLimit = 15.f;      // and stay below 2^kLimit, inside fp16's range
 
-// W: widest head; NT: blocks of 8 rows; FEW: a row or two, whose columns hold four
-// parts of the keys each; ST: tiles in a warp's ring; CTAS: per SM.
-template <int W_, int NT_, bool FEW_, int ST_, int CTAS_>
-struct Q4Cfg {
-  static constexpr int W = W_, NT = NT_, ST = ST_, CTAS = CTAS_;
-  static constexpr bool FEW = FEW_;
-  static_assert(!FEW || NT == 1, "one block of columns");
-  static constexpr int NR = FEW ? 2 : 8 * NT;  // rows of a unit
-  static constexpr int ROW = W / 2;            // bytes of a tile's row
-  static constexpr int KW = W / 32;            // words of a key's row per lane
-  static constexpr int VW = W / 64;            // words of a value's row per lane
-  static constexpr int FT = W / 16;            // blocks of 16 features
-  static constexpr bool Q_SHARED = W * NT > 128;  // Q's fragments in shared memory
-  // merge: a warp's row of sums, eight lanes' features 4 floats apart
-  static constexpr int GS = W / 8 + 4, RS = 8 * GS + 2;
-  static constexpr int TILE = kTile * ROW;     // bytes of a tile's keys, and of its values
-  static constexpr int RING = ST * 2 * TILE;   // a warp's; its sums at the end
-  static_assert(RING >= 8 * RS * 4 && RING % 1024 == 0, "ring");
-  static constexpr int OFF_BAR = kWarps * RING;                  // [warp][stage]
-  static constexpr int OFF_ABORT = OFF_BAR + kWarps * ST * 8;
-  static constexpr int OFF_MASKS = (OFF_ABORT + 4 + 15) / 16 * 16;  // uint64 [NR][4]
-  static constexpr int OFF_STATS = OFF_MASKS + NR * 32;          // float [warp][NR][3]
-  static constexpr int OFF_KEYS = (OFF_STATS + kWarps * NR * 12 + 15) / 16 * 16;  // float4 [warp][32], float [warp][32]
-  static constexpr int OFF_Q = OFF_KEYS + (FEW ? 0 : kWarps * kTile * 20);        // uint2 [2 KW NT][32]
-  static constexpr int SMEM = OFF_Q + (Q_SHARED ? 2 * KW * NT * 256 : 0) + 1024;
-};
-
-// Where row g of a block of 8 scores lies in its block of 8 keys.  A lane of scores
-// (g, j) reads the key of row g, one of values the keys of rows 2 j and 2 j + 1; in
-// this order neither reads two rows out of the same banks at once (W 64: rows of 32
-// bytes as they are; 128: of 64, TMA's 64-byte swizzle; 256: of 128, the 128-byte one).
+// Swizzle of TMA's rows of W / 2 bytes (32, 64 or 128): 16-byte piece c of row `key` of a
+// tile lies at piece c ^ swizzle(key), so that the eight rows of a matrix lie in
+// different banks.
 template <int W>
-__device__ __forceinline__ int key_of_row(int g) {
-  constexpr uint32_t order = W == 64 ? 0x53427160u : (W == 128 ? 0x65217430u : 0x36147250u);
-  return static_cast<int>((order >> (4 * g)) & 7u);
-}
-// Byte `at` of row `key` of a tile as TMA wrote it.
-template <int W>
-__device__ __forceinline__ uint32_t tile_at(int key, int at) {
-  const int chunk = W == 64 ? at >> 4 : (W == 128 ? (at >> 4) ^ ((key >> 1) & 3) : (at >> 4) ^ (key & 7));
-  return static_cast<uint32_t>(key * (W / 2) + chunk * 16 + (at & 15));
+__device__ __forceinline__ int swizzle(int key) {
+  return W == 64 ? (key >> 2) & 1 : (W == 128 ? (key >> 1) & 3 : key & 7);
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
+// D += A B, 16 x 16 by 16 x 8 in fp16, ...
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// ... onto 0.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// Four matrices of 8 rows x 16 bytes: lane (g, j) gets bytes 4 j .. of row g, ...
+__device__ __forceinline__ void ld_rows(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// ... or the g-th 16 bits of rows 2 j and 2 j + 1.
+__device__ __forceinline__ void ld_columns16(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -121,26 +107,15 @@ __device__ __forceinline__ float lg2_approx(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// N consecutive words of shared memory.
-template <int N>
-__device__ __forceinline__ void ld_shared(uint32_t at, uint32_t* w) {
-  if constexpr (N == 1) {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
-  } else if constexpr (N == 2) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
-  } else {
-    static_assert(N == 4, "words");
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(at)
-                 : "memory");
-  }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // What a key's offset and step, and its value's, come to in a step.
 struct KeyFactors {
-  float step, lo;         // of the key
+  float step, lo;             // of the key
   float v_log, v_inv, v_ofs;  // of the value: log2 step, 1 / step, lo / step
 };
 __device__ __forceinline__ KeyFactors key_factors(uint32_t k, uint32_t v) {
@@ -149,16 +124,237 @@ __device__ __forceinline__ KeyFactors key_factors(uint32_t k, uint32_t v) {
   f.lo = bf16_lo(k);
   const float step = bf16_hi(v);
   f.v_log = lg2_approx(step);
-  f.v_inv = __frcp_rn(step);
+  f.v_inv = rcp_approx(step);
   f.v_ofs = bf16_lo(v) * f.v_inv;
   return f;
 }
 
+// A fragment of codes: the low nibbles of the halves of two words, and the next ones
+// (16 times too large).
+__device__ __forceinline__ void codes_of(uint32_t (&a)[4], uint32_t w0, uint32_t w1, bool across) {
+  a[0] = w0 & 0x000f000fu;
+  a[across ? 2 : 1] = w0 & 0x00f000f0u;
+  a[across ? 1 : 2] = w1 & 0x000f000fu;
+  a[3] = w1 & 0x00f000f0u;
+}
+
+// Scores of a warp's 32 keys with NQ blocks of 8 columns.  `at`: lane's address for
+// ld_rows (row lane % 16, 16-byte piece lane / 16), frag(i, x): Q's fragment of reduction
+// step i and column block x.  (A product waits some 27 cycles for the one before on the
+// same sums, so there are four or more sums to take turns: two blocks of keys, and of one
+// block of columns the even and odd steps apart.)
+template <int W, int NQ, typename F>
+__device__ __forceinline__ void score_products(uint32_t at, float (&s)[2][NQ][4], int nq, F&& frag) {
+  constexpr int PARTS = NQ == 1 ? 2 : 1;
+  float part[2][4];
+#pragma unroll
+  for (int c = 0; c < W / 32; c += 2) {
+    uint32_t w[2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) ld_rows((at + 16 * m * (W / 2)) ^ (16 * c), w[m]);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        codes_of(a[m], z & 1 ? w[m][z & 2] >> 8 : w[m][z & 2], z & 1 ? w[m][(z & 2) + 1] >> 8 : w[m][(z & 2) + 1], true);
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+        if (x >= nq) break;
+        const uint2 b = frag(2 * c + z, x);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float(&y)[4] = PARTS == 2 && (z & 1) ? part[m] : s[m][x];
+          if (c == 0 && z < PARTS) mma_f16_first(y, a[m], b.x, b.y);
+          else mma_f16(y, a[m], b.x, b.y);
+        }
+      }
+    }
+  }
+  if constexpr (PARTS == 2) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[m][0][i] += part[m][i];
+  }
+}
+
+// This CTA's unit of a launch whose sequences' units are of `blocks` blocks of rows;
+// false when it has none.
+__device__ __forceinline__ bool this_unit(const RowsParams& p, int blocks, int slots, int lane, Unit* unit) {
+  const int index = static_cast<int>(blockIdx.x), part = index / p.units;
+  if (balanced(p)) {
+    int first, splits, per;
+    balance(p, lane, &first, &splits, &per);
+    const unsigned here = __ballot_sync(0xffffffffu, lane < p.B && part >= first && part < first + splits);
+    if (here == 0) return false;  // (more units than the sequences have splits)
+    const int b = __ffs(here) - 1;
+    *unit = unit_of(p, index, blocks, b, part - __shfl_sync(0xffffffffu, first, b), __shfl_sync(0xffffffffu, per, 0));
+  } else if (longest_first(p, slots)) {
+    const int place = place_of(p, lane);
+    const unsigned here = __ballot_sync(0xffffffffu, lane < p.B && place == part);
+    *unit = unit_of(p, index, blocks, __ffs(here) - 1, 0, 0);
+  } else {
+    *unit = unit_of(p, index, blocks, part % p.B, part / p.B, 0);
+  }
+  return unit->splits > 0;
+}
+
+// A row's fragments of Q: lane (g, j) has the features 32 c + 8 j .. + 7 (v[c]) of its
+// column's row; put(i, b) gets the fragment of reduction step i.  Returns the factors
+// of the row's product with codes and of its sum (every lane of the column's).
+template <int KC, typename F>
+__device__ __forceinline__ float2 q_fragments(const uint4 (&v)[KC], float scale_log2, F&& put) {
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < KC; ++c) {
+    const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[y])), fabsf(bf16_hi(x[y]))));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // q 2^-e with the largest magnitude in [2^14, 2^15)
+  const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100);
+  const float inv = pow2i(-e);
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < KC; ++c) {
+    const float y[8] = {bf16_lo(v[c].x) * inv, bf16_hi(v[c].x) * inv, bf16_lo(v[c].y) * inv, bf16_hi(v[c].y) * inv,
+                        bf16_lo(v[c].z) * inv, bf16_hi(v[c].z) * inv, bf16_lo(v[c].w) * inv, bf16_hi(v[c].w) * inv};
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sum += y[x];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      put(2 * c + h, make_uint2(pack_f16x2(y[2 * h], y[4 + 2 * h]),
+                                pack_f16x2(y[2 * h + 1] * 0.0625f, y[5 + 2 * h] * 0.0625f)));
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  const float f = pow2i(e) * scale_log2;
+  return make_float2(f * 16777216.f, f * sum);  // (codes are 2^-24)
+}
+
+// Word x % 4 of the mask of row x / 4 (a chain's: bits 0 .. t).
+template <typename F>
+__device__ __forceinline__ uint64_t mask_word(const RowsParams& p, const Unit& it, int x, F&& out_row) {
+  int t;
+  const int out = out_row(x >> 2, &t), word = x & 3;
+  if (out < 0 || t >= it.live || it.end <= it.n) return 0;
+  if (p.tree_mask)
+    return word < p.words ? __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t) * p.words + word) : 0;
+  const int count = t + 1 - 64 * word;
+  return count >= 64 ? ~0ull : (count <= 0 ? 0ull : (1ull << count) - 1);
+}
+
+// Adds one to a count in shared memory, behind what the warp read and ahead of what it
+// does next; returns the count before.
+__device__ __forceinline__ uint32_t arrive_count(uint32_t at) {
+  uint32_t n;
+  asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(n) : "r"(at) : "memory");
+  return n;
+}
+
+// The offsets and steps of the key and the value that a thread owns in each tile, copied
+// into shared memory kAhead tiles ahead.  (Loaded into registers, even a tile ahead, they
+// were waited for within the tile: the hardware counts a warp's outstanding operations in
+// a few counters, and one that other, short operations shared with them was not empty
+// before they had come: 1,500 of a tile's 2,600 cycles.)
+constexpr int kAhead = 3;
+struct Scales {
+  static constexpr int BYTES = (kAhead + 1) * 128 * 8;
+  uint32_t at;               // the thread's slot 0
+  const uint32_t *k, *v;     // of position 0
+  int own, stop;             // the thread's key of a tile; keys past `stop` are its last one
+  __device__ __forceinline__ void copy(int i, int tile0) const {
+    if (tile0 < stop) {
+      const int key = min(tile0 + own, stop - 1);
+      const uint32_t to = at + (i & kAhead) * 1024;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(k + key) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4), "l"(v + key) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void start(int first) const {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) copy(i, first + i * kKeys);
+  }
+  // Tile i's words (its place in the unit), and the copy of tile i + kAhead's.
+  __device__ __forceinline__ uint2 get(int i, int tile0) const {
+    copy(i + kAhead, tile0 + kAhead * kKeys);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    uint2 w;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(at + (i & kAhead) * 1024) : "memory");
+    return w;
+  }
+};
+static_assert((kAhead & (kAhead + 1)) == 0, "slots by a mask");
+
+// What a CTA loads: tiles of kKeys keys and values into a ring of ST stages.
+template <int W>
+struct Loader {
+  static constexpr int ROW = W / 2, TILE = kKeys * ROW;
+  const RowsParams& p;
+  const Unit& it;
+  int stop;
+  __device__ __forceinline__ void operator()(uint32_t dst, uint32_t bar, int key) const {
+    const int rows = stop - key;
+    if (rows >= kKeys) {
+      mbar_arrive_expect_tx(bar, 2 * TILE);
+      tma_load_4d(dst, &p.tm_k, bar, 0, it.hk, key, it.b);
+      tma_load_4d(dst + TILE, &p.tm_v, bar, 0, it.hk, key, it.b);
+      return;
+    }
+    // a ragged one in boxes of kRowsQ4Box keys as far as it goes (what lies behind in the
+    // ring are some codes: finite, and their weights are 0)
+    const int boxes = (rows + kRowsQ4Box - 1) / kRowsQ4Box;
+    mbar_arrive_expect_tx(bar, 2 * boxes * kRowsQ4Box * ROW);
+#pragma unroll 1
+    for (int x = 0; x < boxes; ++x) {
+      const uint32_t to = dst + x * kRowsQ4Box * ROW;
+      tma_load_4d(to, &p.tm_k_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
+      tma_load_4d(to + TILE, &p.tm_v_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Up to sixteen rows: of every tile of 128 keys a warp has 32, with sums and references
+// of its own; no warp waits for another.
+// W: widest head; ROWS: 1, 2 or a multiple of 8; ST: stages of the ring; CTAS: per SM.
+// ---------------------------------------------------------------------------
+template <int W_, int ROWS_, int ST_, int CTAS_>
+struct Q4Cfg {
+  static constexpr int W = W_, NR = ROWS_, ST = ST_, CTAS = CTAS_;
+  static constexpr int WP = 4;
+  static constexpr bool FEW = NR <= 2, SHARES = false;
+  static constexpr int NT = FEW ? 1 : NR / 8;      // blocks of 8 columns
+  static constexpr int ROW = W / 2;                // bytes of a tile's row
+  static constexpr int KC = W / 32;                // 16-byte pieces of a row: 32 features
+  static constexpr int FT = W / 16;                // blocks of 16 features
+  static constexpr bool Q_SHARED = KC * NT > 4;    // Q's fragments in shared memory
+  // merge: a warp's columns of sums, with 4 floats between 8 features' groups
+  static constexpr int GS = W / 8 + 4, RS = 8 * GS + 2;
+  static constexpr int TILE = kKeys * ROW;         // bytes of a tile's keys, and of its values
+  static constexpr int SUMS = 8 * NT * RS * 4;     // a warp's, in the ring at the end
+  static constexpr int RING = ST * 2 * TILE;
+  static_assert(RING >= WP * SUMS, "ring");
+  static constexpr int OFF_BAR = RING;             // barriers [stage], warps that left it [stage]
+  static constexpr int OFF_ABORT = OFF_BAR + ST * 12;
+  static constexpr int OFF_MASKS = (OFF_ABORT + 4 + 15) / 16 * 16;  // uint64 [NR][4]
+  static constexpr int OFF_STATS = OFF_MASKS + NR * 32;             // float [warp][NR][3]
+  static constexpr int OFF_SCALES = (OFF_STATS + WP * NR * 12 + 15) / 16 * 16;
+  static constexpr int OFF_KEYS = OFF_SCALES + Scales::BYTES;  // float4 [warp][32], float [warp][32]
+  static constexpr int OFF_Q = OFF_KEYS + (FEW ? 0 : WP * kTile * 20);        // uint2 [2 KC NT][32]
+  static constexpr int SMEM = OFF_Q + (Q_SHARED ? 2 * KC * NT * 256 : 0) + 1024;
+};
+
 template <class C>
-__global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int W = C::W, NT = C::NT, KW = C::KW, VW = C::VW, FT = C::FT, NR = C::NR;
+__global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int W = C::W, NT = C::NT, KC = C::KC, FT = C::FT, NR = C::NR;
   constexpr bool FEW = C::FEW;
   constexpr int MT = kTile / 16;
+  constexpr int LANE_ROWS = NR == 1 ? 1 : 2;  // rows of a lane's scores
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -167,76 +363,24 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
   float(*stats)[NR][3] = reinterpret_cast<float(*)[NR][3]>(smem + C::OFF_STATS);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, j = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * C::RING;
-  const uint32_t bars = smem_u32(smem) + C::OFF_BAR + warp * C::ST * 8;
-  if (lane == 0) {
-    for (int s = 0; s < C::ST; ++s) mbar_init(bars + 8 * s, 1);
-    if (warp == 0) *abort_flag = 0;
+  const uint32_t ring = smem_u32(smem), full = ring + C::OFF_BAR, left = full + 8 * C::ST;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(full + 8 * s, 1);
+      reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * C::ST)[s] = 0;
+    }
+    *abort_flag = 0;
     fence_mbar_init();
   }
-  __syncwarp();
   griddep_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's unit
   const int n_rows = p.T * p.G;
-  const int blocks = (n_rows + NR - 1) / NR;
-  const int index = static_cast<int>(blockIdx.x), part = index / p.units;
   Unit it;
-  if (balanced(p)) {
-    int first, splits, per;
-    balance(p, lane, &first, &splits, &per);
-    const unsigned here = __ballot_sync(0xffffffffu, lane < p.B && part >= first && part < first + splits);
-    if (here == 0) return;  // (more units than the sequences have splits)
-    const int b = __ffs(here) - 1;
-    it = unit_of(p, index, blocks, b, part - __shfl_sync(0xffffffffu, first, b), __shfl_sync(0xffffffffu, per, 0));
-  } else if (longest_first(p, kSms * C::CTAS)) {
-    const int place = place_of(p, lane);
-    const unsigned here = __ballot_sync(0xffffffffu, lane < p.B && place == part);
-    it = unit_of(p, index, blocks, __ffs(here) - 1, 0, 0);
-  } else {
-    it = unit_of(p, index, blocks, part % p.B, part / p.B, 0);
-  }
-  if (it.splits == 0) return;
+  if (!this_unit(p, (n_rows + NR - 1) / NR, kSms * C::CTAS, lane, &it)) return;
 
-  // ---- a warp's tiles: keys first + 32 warp .., every 128; two copies of each in flight
-  const int stop = min(it.t1 * kKeys, it.end);
-  const int first = it.t0 * kKeys + warp * kTile;
-  auto request = [&](int key, int stage) {
-    const uint32_t bar = bars + 8 * stage, dst = ring + stage * 2 * C::TILE;
-    const int rows = min(kTile, stop - key);
-    if (rows == kTile) {
-      mbar_arrive_expect_tx(bar, 2 * C::TILE);
-      tma_load_4d(dst, &p.tm_k, bar, 0, it.hk, key, it.b);
-      tma_load_4d(dst + C::TILE, &p.tm_v, bar, 0, it.hk, key, it.b);
-    } else {
-      // a ragged one in boxes of kRowsQ4Box keys as far as it goes (what lies behind in
-      // the ring are some codes: finite, and their weights are 0)
-      const int boxes = (rows + kRowsQ4Box - 1) / kRowsQ4Box;
-      mbar_arrive_expect_tx(bar, 2 * boxes * kRowsQ4Box * C::ROW);
-      for (int x = 0; x < boxes; ++x) {
-        const uint32_t to = dst + x * kRowsQ4Box * C::ROW;
-        tma_load_4d(to, &p.tm_k_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
-        tma_load_4d(to + C::TILE, &p.tm_v_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
-      }
-    }
-  };
-  if (lane == 0)
-    for (int s = 0; s < C::ST; ++s)
-      if (first + s * kKeys < stop) request(first + s * kKeys, s);
-  // lane's key's offsets and steps, a tile ahead (keys past the end: the last one's)
-  const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
-  const uint32_t* k_scale = reinterpret_cast<const uint32_t*>(p.k_scale) + scales;
-  const uint32_t* v_scale = reinterpret_cast<const uint32_t*>(p.v_scale) + scales;
-  // (lane (g, j) has row g of block j of 8 keys)
-  const int own = 8 * j + key_of_row<W>(g);
-  uint32_t ks = 0, vs = 0;
-  if (first < stop) {
-    const int key = min(first + own, stop - 1);
-    ks = __ldg(k_scale + key);
-    vs = __ldg(v_scale + key);
-  }
-
+  const int stop = min(it.t1 * kKeys, it.end), first = it.t0 * kKeys;
+  const Loader<W> load{p, it, stop};
   // Output row of row r of the unit (-1 past the last), t: its drafted token.
   auto out_row = [&](int r, int* t) {
     const int gr = it.rb * NR + r;
@@ -245,82 +389,59 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
     *t = p.G == 1 ? gr : gr / p.G;
     return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
   };
-
-  // ---- Q: lane (g, j) holds the features of its part of the keys' rows, of the row of
-  // column 8 n + g (FEW: the even columns are row 0, the odd ones row 1)
-  uint2 q[C::Q_SHARED ? 1 : 2 * KW * NT];
-  uint2* q_shared = reinterpret_cast<uint2*>(smem + C::OFF_Q) + lane;
-  float fa[NT][2], fb[NT][2];  // factors of a row's product and of its sum: columns 8 n + 2 j, + 1
-  constexpr int KV = KW > 4 ? 4 : KW;  // words loaded at once: 16 j .. (256 wide: and 64 + 16 j ..)
+  // Plain loads first, all of them together: behind the ring's copies each would wait
+  // for several tiles.  The offsets and steps (FEW: lane (g, j) owns key g of block j of
+  // 8; else key `lane`) ...
+  const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
+  const int own = kTile * warp + (FEW ? 8 * j + g : lane);
+  const Scales words{ring + C::OFF_SCALES + 8 * threadIdx.x, reinterpret_cast<const uint32_t*>(p.k_scale) + scales,
+                     reinterpret_cast<const uint32_t*>(p.v_scale) + scales, own, stop};
+  words.start(first);
+  // ... Q: lane (g, j) holds the features 32 c + 8 j .. of the row of column g of each block
+  // of columns (FEW: the even columns are row 0, the odd ones row 1) ...
+  uint4 v[NT][KC];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     int t;
-    const int out = out_row(FEW ? g & 1 : 8 * n + g, &t);
+    const int out = out_row(NR == 1 ? 0 : (NR == 2 ? g & 1 : 8 * n + g), &t);
     const bool live = out >= 0 && t < it.live;
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + static_cast<long long>(max(out, 0)) * p.d;
-    uint4 v[KW];
-    float amax = 0.f;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      const int f = (w / KV) * 128 + 8 * KV * j + 8 * (w % KV);
-      v[w] = make_uint4(0, 0, 0, 0);
-      if (live && f < p.d) v[w] = __ldg(reinterpret_cast<const uint4*>(src + f));
-      const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[y])), fabsf(bf16_hi(x[y]))));
+    for (int c = 0; c < KC; ++c) {
+      v[n][c] = make_uint4(0, 0, 0, 0);
+      if (live && 32 * c < p.d) v[n][c] = __ldg(reinterpret_cast<const uint4*>(src + 32 * c + 8 * j));
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // q 2^-e with the largest magnitude in [2^14, 2^15)
-    const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100);
-    const float inv = pow2i(-e);
-    float sum = 0.f;
+  }
+  // ... and the rows' masks
+  static_assert(NR * 4 <= 32 * C::WP, "a word to a thread");
+  const uint64_t bits = threadIdx.x < NR * 4 ? mask_word(p, it, static_cast<int>(threadIdx.x), out_row) : 0;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < C::ST; ++s)
+      if (first + s * kKeys < stop) load(ring + s * 2 * C::TILE, full + 8 * s, first + s * kKeys);
+
+  uint2 q[C::Q_SHARED ? 1 : 2 * KC * NT];
+  uint2* q_shared = reinterpret_cast<uint2*>(smem + C::OFF_Q) + lane;
+  float fa[NT][2], fb[NT][2];  // factors of a row's product and of its sum: columns 8 n + 2 j, + 1
 #pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      const float y[8] = {bf16_lo(v[w].x) * inv, bf16_hi(v[w].x) * inv, bf16_lo(v[w].y) * inv, bf16_hi(v[w].y) * inv,
-                          bf16_lo(v[w].z) * inv, bf16_hi(v[w].z) * inv, bf16_lo(v[w].w) * inv, bf16_hi(v[w].w) * inv};
-#pragma unroll
-      for (int x = 0; x < 8; ++x) sum += y[x];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 b = make_uint2(pack_f16x2(y[2 * h], y[4 + 2 * h]),
-                                   pack_f16x2(y[2 * h + 1] * 0.0625f, y[5 + 2 * h] * 0.0625f));
-        if constexpr (C::Q_SHARED) {
-          if (warp == 0) q_shared[((2 * w + h) * NT + n) * 32] = b;
-        } else {
-          q[(2 * w + h) * NT + n] = b;
-        }
+  for (int n = 0; n < NT; ++n) {
+    const float2 f = q_fragments<KC>(v[n], p.scale_log2, [&](int i, uint2 b) {
+      if constexpr (C::Q_SHARED) {
+        if (warp == 0) q_shared[(i * NT + n) * 32] = b;
+      } else {
+        q[i * NT + n] = b;
       }
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    const float f = pow2i(e) * p.scale_log2;
+    });
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int from = FEW ? 4 * r : 8 * j + 4 * r;
-      fa[n][r] = __shfl_sync(0xffffffffu, f * 16777216.f, from);
-      fb[n][r] = __shfl_sync(0xffffffffu, f * sum, from);
+      fa[n][r] = __shfl_sync(0xffffffffu, f.x, 8 * j + 4 * r);
+      fb[n][r] = __shfl_sync(0xffffffffu, f.y, 8 * j + 4 * r);
     }
   }
-  // the rows' mask words (a chain's: bits 0 .. t)
-  for (int x = static_cast<int>(threadIdx.x); x < NR * 4; x += 32 * kWarps) {
-    int t;
-    const int out = out_row(x >> 2, &t), word = x & 3;
-    uint64_t bits = 0;
-    if (out >= 0 && t < it.live && it.end > it.n) {
-      if (p.tree_mask) {
-        if (word < p.words) bits = __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t) * p.words + word);
-      } else {
-        const int count = t + 1 - 64 * word;
-        bits = count >= 64 ? ~0ull : (count <= 0 ? 0ull : (1ull << count) - 1);
-      }
-    }
-    masks[x >> 2][word] = bits;
-  }
-  __syncthreads();
+  if (threadIdx.x < NR * 4) masks[threadIdx.x >> 2][threadIdx.x & 3] = bits;
+  __syncthreads();  // (the barriers are set up, too)
 
   float o[NT][FT][4];
-  float ref[NT][2], l[NT][2], ofs[NT][2];  // references less kLift
+  float ref[NT][2], l[NT][2], ofs[NT][2];  // references less kLift; sums of weights, of the offsets' shares
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -334,256 +455,219 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
       ofs[n][r] = 0.f;
     }
   }
-  // lane's places in a tile: the key of row g, the values of rows 2 j and 2 j + 1
-  uint32_t k_at[KW / KV], v_at[2];
-#pragma unroll
-  for (int w = 0; w < KW / KV; ++w) k_at[w] = tile_at<W>(key_of_row<W>(g), 64 * w + 4 * KV * j);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) v_at[x] = C::TILE + tile_at<W>(key_of_row<W>(2 * j + x), 4 * VW * g);
+  // lane's row and piece of the warp's part of a tile, for ldmatrix
+  const int row16 = lane & 15;
+  const uint32_t at = (kTile * warp + row16) * C::ROW + 16 * (swizzle<W>(row16) ^ (lane >> 4));
   float4* keys = reinterpret_cast<float4*>(smem + C::OFF_KEYS) + warp * kTile;
-  float* keys_ofs = reinterpret_cast<float*>(smem + C::OFF_KEYS + kWarps * kTile * 16) + warp * kTile;
+  float* keys_ofs = reinterpret_cast<float*>(smem + C::OFF_KEYS + C::WP * kTile * 16) + warp * kTile;
 
   bool ok = true;
-  int stage = 0;
+  int stage = 0, i = 0;
   uint32_t parity = 0;
 #pragma unroll 1
-  for (int key0 = first; key0 < stop; key0 += kKeys) {
+  for (int tile0 = first; tile0 < stop; tile0 += kKeys, ++i) {
     const uint32_t tile = ring + stage * 2 * C::TILE;
-    ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + stage));
-    if (!ok) break;
-    // ---- scores: s[n][m] = keys of rows g, 8 + g of block m, columns 2 j, 2 j + 1 of block n
-    float s[NT][MT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[n][m][x] = 0.f;
-#pragma unroll
-    for (int w0 = 0; w0 < KW; w0 += KV) {
-      uint32_t kc[MT][2][KV];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) ld_shared<KV>(tile + k_at[w0 / KV] + (16 * m + 8 * h) * C::ROW, kc[m][h]);
-#pragma unroll
-      for (int w = 0; w < KV; ++w)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint2 b[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int i = (2 * (w0 + w) + h) * NT + n;
-            if constexpr (C::Q_SHARED) b[n] = q_shared[i * 32];
-            else b[n] = q[i];
-          }
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t x0 = h ? kc[m][0][w] >> 8 : kc[m][0][w], x1 = h ? kc[m][1][w] >> 8 : kc[m][1][w];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_f16(s[n][m], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, b[n].x, b[n].y);
-          }
-        }
-    }
-    // ---- weights
-    const KeyFactors mine = key_factors(ks, vs);
-    if (key0 + kKeys < stop) {
-      const int key = min(key0 + kKeys + own, stop - 1);
-      ks = __ldg(k_scale + key);
-      vs = __ldg(v_scale + key);
-    }
-    const bool masked = key0 + kTile > min(it.n, stop);
-    uint32_t pt[NT][MT][2];  // weights transposed: column g, keys of rows 2 j, 2 j + 1 (+ 8)
-    if constexpr (FEW) {
-      // every column pair has all the keys' scores: lane (g, j) takes those of its own key
-      float x[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float lo = j & 1 ? s[0][0][2 + r] : s[0][0][r], hi = j & 1 ? s[0][1][2 + r] : s[0][1][r];
-        x[r] = fmaf((j & 2 ? hi : lo) * fa[0][r], mine.step, fmaf(fb[0][r], mine.lo, mine.v_log));
-      }
-      float v_inv = mine.v_inv, v_ofs = mine.v_ofs;
-      if (masked) {
-        const int key = key0 + own, off = key - it.n;
-        bool any = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          bool sees = key < stop;
-          if (sees && off >= 0) sees = (masks[r][off >> 6] >> (off & 63)) & 1;  // (off < 256: drafted tokens end there)
-          if (!sees) x[r] = -INFINITY;
-          any = any || sees;
-        }
-        // (what hides from both may hold anything, and 0 * NaN would be NaN)
-        if (!any) v_inv = v_ofs = 0.f;
-      }
-      if (__any_sync(0xffffffffu, fmaxf(x[0] - ref[0][0], x[1] - ref[0][1]) > kLift + kSlack)) {
-        // references up to this tile's maxima, what was summed down by as much
-        float by[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float m = x[r];
-#pragma unroll
-          for (int z = 1; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-          m = fmaxf(ref[0][r], m - kLift);
-          by[r] = ex2_approx(ref[0][r] - m);
-          ref[0][r] = m;
-          l[0][r] *= by[r];
-          ofs[0][r] *= by[r];
-        }
-#pragma unroll
-        for (int f = 0; f < FT; ++f)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) o[0][f][z] *= by[z & 1];
-      }
-      const float w0 = ex2_approx(x[0] - ref[0][0]), w1 = ex2_approx(x[1] - ref[0][1]);
-      fma2(l[0][0], l[0][1], w0, w1, v_inv, v_inv, l[0][0], l[0][1]);
-      const uint32_t w = pack_f16x2(w0, w1);
-      // (the offsets with the rounded weights, as the codes have them: what the
-      // rounding does to both is relative to the value, not to its two parts)
-      fma2(ofs[0][0], ofs[0][1], half_lo(w), half_hi(w), v_ofs, v_ofs, ofs[0][0], ofs[0][1]);
-      // columns 2 j, 2 j + 1 of block j's keys: a column pair sums a quarter of the keys
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) pt[0][m][h] = transposed(j == 2 * m + h ? w : 0u);
-    } else {
+    const uint2 kv = words.get(i, tile0);
+    KeyFactors mine = key_factors(kv.x, kv.y);
+    if constexpr (!FEW) {
       // the keys' factors by way of shared memory: lane's own key to the lanes of its row
-      const int slot = 8 * j + g;  // (row g of block j)
       __syncwarp();  // (the tile before is read)
-      keys[slot] = make_float4(mine.step, mine.lo, mine.v_log, mine.v_inv);
-      keys_ofs[slot] = mine.v_ofs;
-      __syncwarp();
-      float4 kf[MT][2];
-      float v_ofs[MT][2];
+      keys[lane] = make_float4(mine.step, mine.lo, mine.v_log, mine.v_inv);
+      keys_ofs[lane] = mine.v_ofs;
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + stage));
+    if (!ok) break;
+    const int key0 = tile0 + kTile * warp;
+    if (key0 < stop) {
+      // ---- scores: s[m][n] = keys g, 8 + g of block m of 16, columns 2 j, 2 j + 1 of block n
+      float s[MT][NT][4];
+      score_products<W, NT>(tile + at, s, NT, [&](int i, int n) {
+        if constexpr (C::Q_SHARED) return q_shared[(i * NT + n) * 32];
+        else return q[i * NT + n];
+      });
+      // ---- weights
+      const bool masked = key0 + kTile > min(it.n, stop);
+      uint32_t pt[MT][NT][2];  // weights transposed: column g, keys 2 j, 2 j + 1 (+ 8)
+      if constexpr (FEW) {
+        // every column pair has all the keys' scores: lane (g, j) takes those of its own key
+        float x[LANE_ROWS], top = -INFINITY;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int r = 0; r < LANE_ROWS; ++r) {
+          const float lo = j & 1 ? s[0][0][2 + r] : s[0][0][r], hi = j & 1 ? s[1][0][2 + r] : s[1][0][r];
+          x[r] = fmaf((j & 2 ? hi : lo) * fa[0][r], mine.step, fmaf(fb[0][r], mine.lo, mine.v_log));
+        }
+        if (masked) {
+          const int key = tile0 + own, off = key - it.n;
+          bool any = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          kf[m][h] = keys[16 * m + 8 * h + g];
-          v_ofs[m][h] = keys_ofs[16 * m + 8 * h + g];
+          for (int r = 0; r < LANE_ROWS; ++r) {
+            bool sees = key < stop;
+            if (sees && off >= 0) sees = (masks[r][off >> 6] >> (off & 63)) & 1;  // (off < 256: drafted tokens end there)
+            if (!sees) x[r] = -INFINITY;
+            any = any || sees;
+          }
+          // (what hides from both may hold anything, and 0 * NaN would be NaN)
+          if (!any) mine.v_inv = mine.v_ofs = 0.f;
         }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int r = 0; r < LANE_ROWS; ++r) top = fmaxf(top, x[r] - ref[0][r]);
+        if (__any_sync(0xffffffffu, top > kLimit)) {
+          // references up to this tile's maxima, what was summed down by as much
+          float by[2] = {1.f, 1.f};
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int r = 0; r < LANE_ROWS; ++r) {
+            float m = x[r];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float t0, t1, u0, u1;
-            mul2(t0, t1, s[n][m][2 * h], s[n][m][2 * h + 1], fa[n][0], fa[n][1]);
-            fma2(u0, u1, fb[n][0], fb[n][1], kf[m][h].y, kf[m][h].y, kf[m][h].z, kf[m][h].z);
-            fma2(s[n][m][2 * h], s[n][m][2 * h + 1], t0, t1, kf[m][h].x, kf[m][h].x, u0, u1);
-          }
-      if (masked) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = key0 + 16 * m + 8 * h + key_of_row<W>(g), off = key - it.n;
-            bool any = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                bool sees = key < stop;
-                if (sees && off >= 0)  // (off < 256: the drafted tokens end there)
-                  sees = (masks[8 * n + 2 * j + r][off >> 6] >> (off & 63)) & 1;
-                if (!sees) s[n][m][2 * h + r] = -INFINITY;
-                any = any || sees;
-              }
-            // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
-            if (!any) kf[m][h].w = v_ofs[m][h] = 0.f;
-          }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float m = fmaxf(s[n][0][r], s[n][0][2 + r]);
-#pragma unroll
-          for (int x = 1; x < MT; ++x) m = fmax3(m, s[n][x][r], s[n][x][2 + r]);
-          top = fmaxf(top, m - ref[n][r]);
-        }
-      if (__any_sync(0xffffffffu, top > kLift + kSlack)) {
-        // references up to this tile's maxima, what was summed down by as much
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float by[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float m = fmaxf(s[n][0][r], s[n][0][2 + r]);
-#pragma unroll
-            for (int x = 1; x < MT; ++x) m = fmax3(m, s[n][x][r], s[n][x][2 + r]);
-#pragma unroll
-            for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-            m = fmaxf(ref[n][r], m - kLift);
-            by[r] = ex2_approx(ref[n][r] - m);
-            ref[n][r] = m;
-            l[n][r] *= by[r];
-            ofs[n][r] *= by[r];
+            for (int z = 1; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+            m = fmaxf(ref[0][r], m - kLift);
+            by[r] = ex2_approx(ref[0][r] - m);
+            ref[0][r] = m;
+            l[0][r] *= by[r];
+            ofs[0][r] *= by[r];
           }
 #pragma unroll
           for (int f = 0; f < FT; ++f)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) o[n][f][x] *= by[x & 1];
+            for (int z = 0; z < 4; ++z) o[0][f][z] *= by[NR == 1 ? 0 : z & 1];
         }
-      }
+        uint32_t w;
+        if constexpr (NR == 1) {
+          const float w0 = ex2_approx(x[0] - ref[0][0]);
+          l[0][0] = fmaf(w0, mine.v_inv, l[0][0]);
+          w = pack_f16x2(w0, 0.f);
+          // (the offsets with the rounded weights, as the codes have them: what the
+          // rounding does to both is relative to the value, not to its two parts)
+          ofs[0][0] = fmaf(half_lo(w), mine.v_ofs, ofs[0][0]);
+        } else {
+          const float w0 = ex2_approx(x[0] - ref[0][0]), w1 = ex2_approx(x[1] - ref[0][1]);
+          fma2(l[0][0], l[0][1], w0, w1, mine.v_inv, mine.v_inv, l[0][0], l[0][1]);
+          w = pack_f16x2(w0, w1);
+          fma2(ofs[0][0], ofs[0][1], half_lo(w), half_hi(w), mine.v_ofs, mine.v_ofs, ofs[0][0], ofs[0][1]);
+        }
+        // columns 2 j, 2 j + 1 of block j's keys: a column pair sums a quarter of the keys
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) pt[m][0][h] = transposed(j == 2 * m + h ? w : 0u);
+      } else {
+        float v_inv[MT][2], v_ofs[MT][2];
+        float top = -INFINITY;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float w0, w1;
-            add2(w0, w1, s[n][m][2 * h], s[n][m][2 * h + 1], -ref[n][0], -ref[n][1]);
-            w0 = ex2_approx(w0);
-            w1 = ex2_approx(w1);
-            fma2(l[n][0], l[n][1], w0, w1, kf[m][h].w, kf[m][h].w, l[n][0], l[n][1]);
-            const uint32_t w = pack_f16x2(w0, w1);
-            // (the offsets with the rounded weights, as the codes have them: what the
-            // rounding does to both is relative to the value, not to its two parts)
-            fma2(ofs[n][0], ofs[n][1], half_lo(w), half_hi(w), v_ofs[m][h], v_ofs[m][h], ofs[n][0], ofs[n][1]);
-            pt[n][m][h] = transposed(w);
+            const float4 kf = keys[16 * m + 8 * h + g];
+            v_inv[m][h] = kf.w;
+            v_ofs[m][h] = keys_ofs[16 * m + 8 * h + g];
+            bool any = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float* y = s[m][n] + 2 * h;
+              float t0, t1, u0, u1;
+              mul2(t0, t1, y[0], y[1], fa[n][0], fa[n][1]);
+              fma2(u0, u1, fb[n][0], fb[n][1], kf.y, kf.y, kf.z, kf.z);
+              fma2(y[0], y[1], t0, t1, kf.x, kf.x, u0, u1);
+            }
+            if (masked) {
+              const int key = key0 + 16 * m + 8 * h + g, off = key - it.n;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  bool sees = key < stop;
+                  if (sees && off >= 0)  // (off < 256: the drafted tokens end there)
+                    sees = (masks[8 * n + 2 * j + r][off >> 6] >> (off & 63)) & 1;
+                  if (!sees) s[m][n][2 * h + r] = -INFINITY;
+                  any = any || sees;
+                }
+              // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
+              if (!any) v_inv[m][h] = v_ofs[m][h] = 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) top = fmax3(top, s[m][n][2 * h] - ref[n][0], s[m][n][2 * h + 1] - ref[n][1]);
           }
-    }
-    // ---- o += V^T P^T
+        if (__any_sync(0xffffffffu, top > kLimit)) {
+          // references up to this tile's maxima, what was summed down by as much
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      uint32_t vc[4][VW];
+          for (int n = 0; n < NT; ++n) {
+            float by[2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) ld_shared<VW>(tile + v_at[x & 1] + (16 * m + 8 * (x >> 1)) * C::ROW, vc[x]);
+            for (int r = 0; r < 2; ++r) {
+              float m = fmaxf(s[0][n][r], s[0][n][2 + r]);
 #pragma unroll
-      for (int y = 0; y < VW; ++y)
+              for (int x = 1; x < MT; ++x) m = fmax3(m, s[x][n][r], s[x][n][2 + r]);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t sel = 0x4400u + 0x1111u * b;  // byte b of two keys' words
-          const uint32_t x0 = __byte_perm(vc[0][y], vc[1][y], sel);
-          const uint32_t x1 = __byte_perm(vc[2][y], vc[3][y], sel);
+              for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+              m = fmaxf(ref[n][r], m - kLift);
+              by[r] = ex2_approx(ref[n][r] - m);
+              ref[n][r] = m;
+              l[n][r] *= by[r];
+              ofs[n][r] *= by[r];
+            }
+#pragma unroll
+            for (int f = 0; f < FT; ++f)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) o[n][f][z] *= by[z & 1];
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma_f16(o[n][4 * y + b], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu, x1 & 0x00f000f0u,
-                    pt[n][m][0], pt[n][m][1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float w0, w1;
+              add2(w0, w1, s[m][n][2 * h], s[m][n][2 * h + 1], -ref[n][0], -ref[n][1]);
+              w0 = ex2_approx(w0);
+              w1 = ex2_approx(w1);
+              fma2(l[n][0], l[n][1], w0, w1, v_inv[m][h], v_inv[m][h], l[n][0], l[n][1]);
+              const uint32_t w = pack_f16x2(w0, w1);
+              // (the offsets with the rounded weights, as above)
+              fma2(ofs[n][0], ofs[n][1], half_lo(w), half_hi(w), v_ofs[m][h], v_ofs[m][h], ofs[n][0], ofs[n][1]);
+              pt[m][n][h] = transposed(w);
+            }
+      }
+      // ---- o += V^T P^T, 16 keys at a time
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < KC; c += 2) {
+          uint32_t w[4];
+          ld_columns16((tile + C::TILE + 16 * m * C::ROW + at) ^ (16 * c), w);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            uint32_t a[4];
+            codes_of(a, z & 1 ? w[z & 2] >> 8 : w[z & 2], z & 1 ? w[(z & 2) + 1] >> 8 : w[(z & 2) + 1], false);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * c + z], a, pt[m][n][0], pt[m][n][1]);
+          }
         }
+      __syncwarp();  // (every lane has read the tile)
     }
-    __syncwarp();  // (every lane has read the tile)
-    if (lane == 0 && key0 + C::ST * kKeys < stop) request(key0 + C::ST * kKeys, stage);
+    // the last warp to leave a stage fills it again
+    if (lane == 0 && arrive_count(left + 4 * stage) % C::WP == C::WP - 1 && tile0 + C::ST * kKeys < stop)
+      load(tile, full + 8 * stage, tile0 + C::ST * kKeys);
+    __syncwarp();
     if (++stage == C::ST) {
       stage = 0;
       parity ^= 1;
     }
   }
-  if (!ok) {
+  __syncthreads();
+  if (*abort_flag != 0 && threadIdx.x == 0) {
     // gave up: the copies in flight must land before the CTA exits (each wait is bounded)
     volatile int never = 0;
-    for (int s = 0; s < C::ST; ++s) mbar_wait(bars + 8 * s, parity ^ (s < stage ? 1 : 0), &never, p.status, 0);
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_wait(full + 8 * s, 0, &never, p.status, 0);
+      mbar_wait(full + 8 * s, 1, &never, p.status, 0);
+    }
   }
 
   // ---- the warps' sums together
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < LANE_ROWS; ++r) {
 #pragma unroll
       for (int z = FEW ? 1 : 4; z < 32; z <<= 1) {
         l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], z);
@@ -599,67 +683,417 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
   const bool whole = it.splits == 1;
   const long long first_part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
   auto sums = [&](int w, int column, int at) {
-    return reinterpret_cast<float*>(smem + w * C::RING) + column * C::RS + at;
+    return reinterpret_cast<float*>(smem + w * C::SUMS) + column * C::RS + at;
   };
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (n > 0) {
-      if (it.rb * NR + 8 * n >= n_rows) break;
-      __syncthreads();  // (the block before is read)
-    }
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int f = 0; f < FT; ++f)
 #pragma unroll
-      for (int x = 0; x < 4; ++x)  // (codes are 2^-24, odd features 2^-20)
-        *sums(warp, 2 * j + (x & 1), C::GS * g + 2 * f + (x >> 1)) = o[n][f][x] * (x >> 1 ? 1048576.f : 16777216.f);
-    __syncthreads();
-    for (int x = static_cast<int>(threadIdx.x); x < (FEW ? 2 : 8) * (W / 2); x += 32 * kWarps) {
-      const int c = x / (W / 2), r = 8 * n + c, f = 2 * (x % (W / 2));
-      int t;
-      const int out = out_row(r, &t);
-      if (out < 0) break;  // (rows only grow)
-      float m = kNoRef;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, stats[w][r][0]);
-      float y0 = 0.f, y1 = 0.f, L = 0.f;
-      if (t < it.live && m != kNoRef && *abort_flag == 0) {
-        float add = 0.f;
-        const int at = C::GS * (f / (W / 8)) + f % (W / 8);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float a = ex2_approx(stats[w][r][0] - m);
-          L = fmaf(a, stats[w][r][1], L);
-          add = fmaf(a, stats[w][r][2], add);
-          float2 v = *reinterpret_cast<const float2*>(sums(w, c, at));
-          if constexpr (FEW) {
-#pragma unroll
-            for (int z = 2; z < 8; z += 2) {
-              const float2 u = *reinterpret_cast<const float2*>(sums(w, z + c, at));
-              v.x += u.x;
-              v.y += u.y;
-            }
-          }
-          y0 = fmaf(a, v.x, y0);
-          y1 = fmaf(a, v.y, y1);
-        }
-        y0 += add;
-        y1 += add;
+      for (int x = 0; x < 4; ++x) {
+        // (codes are 2^-24, odd features 2^-20; groups of W / 8 features are GS floats apart)
+        const int feature = 32 * (f >> 1) + 4 * g + 2 * (f & 1) + (x >> 1);
+        *sums(warp, 8 * n + 2 * j + (x & 1), feature / (W / 8) * C::GS + feature % (W / 8)) =
+            o[n][f][x] * (x >> 1 ? 1048576.f : 16777216.f);
       }
+  __syncthreads();
+  // (a row to a warp: once per unit, so short code counts)
+#pragma unroll 1
+  for (int r = warp; r < NR; r += C::WP) {
+    int t;
+    const int out = out_row(r, &t);
+    if (out < 0) break;
+    float m = kNoRef;
+#pragma unroll
+    for (int w = 0; w < C::WP; ++w) m = fmaxf(m, stats[w][r][0]);
+    float a[C::WP], L = 0.f, add = 0.f;
+    const bool live = t < it.live && m != kNoRef && *abort_flag == 0;
+#pragma unroll
+    for (int w = 0; w < C::WP; ++w) {
+      a[w] = live ? ex2_approx(stats[w][r][0] - m) : 0.f;
+      if (live) {
+        L = fmaf(a[w], stats[w][r][1], L);
+        add = fmaf(a[w], stats[w][r][2], add);
+      }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    if (lane == 0) {
       if (!whole) {
-        if (f == 0) {
-          p.part_m[first_part + out] = L == 0.f ? -INFINITY : m;
-          p.part_l[first_part + out] = L;
-        }
-        *reinterpret_cast<float2*>(p.part_o + (first_part + out) * W + f) = make_float2(y0, y1);
-        continue;
-      }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      if (f < p.d)
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d + f) =
-            pack_bf16x2(y0 * inv, y1 * inv);
-      if (p.lse && f == 0)
+        p.part_m[first_part + out] = L == 0.f ? -INFINITY : m;
+        p.part_l[first_part + out] = L;
+      } else if (p.lse) {
         p.lse[(static_cast<long long>(it.b) * p.H + out % p.H) * p.T + t] =
             L == 0.f ? -INFINITY : (m + __log2f(L)) * 0.69314718055994531f;
+      }
+    }
+#pragma unroll 1
+    for (int f = 2 * lane; f < W; f += 64) {
+      const int at = C::GS * (f / (W / 8)) + f % (W / 8);
+      float y0 = add, y1 = add;
+#pragma unroll
+      for (int w = 0; w < C::WP; ++w) {
+#pragma unroll
+        for (int z = 0; z < (FEW ? 8 : 1); z += 2) {
+          const float2 u = *reinterpret_cast<const float2*>(sums(w, z + r, at));
+          y0 = fmaf(a[w], u.x, y0);
+          y1 = fmaf(a[w], u.y, y1);
+        }
+      }
+      if (!live) y0 = y1 = 0.f;  // (what is not live may be anything)
+      if (!whole)
+        *reinterpret_cast<float2*>(p.part_o + (first_part + out) * W + f) = make_float2(y0, y1);
+      else if (f < p.d)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d + f) =
+            pack_bf16x2(y0 * inv, y1 * inv);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// More rows: a CTA's warps share a tile of 128 keys.  Each has 32 of the keys for the
+// scores, and a quarter of the features, over all 128 keys, for the output: the codes are
+// unpacked once for all rows, and a warp's output takes a quarter of the registers.
+// The weights pass through shared memory, the references are the CTA's.
+// ---------------------------------------------------------------------------
+template <int W_, int NT_, int ST_, int CTAS_>
+struct Q4BlockCfg {
+  static constexpr int W = W_, NT = NT_, ST = ST_, CTAS = CTAS_;
+  static constexpr int WP = 4, NR = 8 * NT;
+  static constexpr bool SHARES = true;
+  static_assert(WP * kTile == kKeys && W >= 128, "a tile of the splits' size, 32 features to a warp");
+  static constexpr int ROW = W / 2;            // bytes of a tile's row
+  static constexpr int KC = W / 32;            // 16-byte pieces of a row: 32 features
+  static constexpr int WC = KC / WP;           // a warp's
+  static constexpr int FT = 2 * WC;            // blocks of 16 features of a warp
+  static constexpr int TILE = kKeys * ROW;     // bytes of a tile's keys, and of its values
+  static constexpr int OFF_P = ST * 2 * TILE;                    // uint2 [8 blocks of 16 keys][NT][32]
+  static constexpr int OFF_Q = OFF_P + 8 * NT * 256;             // uint2 [2 KC][NT][32]
+  static constexpr int OFF_KEYS = OFF_Q + 2 * KC * NT * 256;     // float4 [128], float [128]
+  static constexpr int OFF_SCALES = OFF_KEYS + kKeys * 20;
+  static constexpr int OFF_ROWS = OFF_SCALES + Scales::BYTES;         // float2 [NR]: the rows' factors
+  static constexpr int OFF_STATS = OFF_ROWS + NR * 8;            // float2 [warp][NR]; maxima float [warp][NR]
+  static constexpr int OFF_MASKS = OFF_STATS + WP * NR * 8;      // uint64 [NR][4]
+  static constexpr int OFF_BAR = OFF_MASKS + NR * 32;
+  static constexpr int SMEM = OFF_BAR + ST * 8 + 16 + 1024;
+  static_assert(SMEM <= 232448 && OFF_P % 1024 == 0, "shared memory");
+};
+
+template <class C>
+__global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int W = C::W, NT = C::NT, KC = C::KC, FT = C::FT, NR = C::NR, WP = C::WP;
+  constexpr int MT = kTile / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t ring = smem_u32(smem), bars = ring + C::OFF_BAR;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::ST * 8);
+  uint64_t(*masks)[4] = reinterpret_cast<uint64_t(*)[4]>(smem + C::OFF_MASKS);
+  float2* factors = reinterpret_cast<float2*>(smem + C::OFF_ROWS);
+  float2(*stats)[NR] = reinterpret_cast<float2(*)[NR]>(smem + C::OFF_STATS);
+  float(*maxima)[NR] = reinterpret_cast<float(*)[NR]>(smem + C::OFF_STATS);
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int g = lane >> 2, j = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) mbar_init(bars + 8 * s, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int n_rows = p.T * p.G;
+  Unit it;
+  if (!this_unit(p, (n_rows + NR - 1) / NR, kSms * C::CTAS, lane, &it)) return;
+  const int stop = min(it.t1 * kKeys, it.end), first = it.t0 * kKeys;
+  const int rows_here = min(NR, n_rows - it.rb * NR);
+  const Loader<W> load{p, it, stop};
+  auto out_row = [&](int r, int* t) {
+    const int gr = it.rb * NR + r;
+    *t = -1;
+    if (gr >= n_rows) return -1;
+    *t = p.G == 1 ? gr : gr / p.G;
+    return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
+  };
+  // plain loads before the ring's, as above: offsets and steps ...
+  const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
+  const Scales words{ring + C::OFF_SCALES + 8 * threadIdx.x, reinterpret_cast<const uint32_t*>(p.k_scale) + scales,
+                     reinterpret_cast<const uint32_t*>(p.v_scale) + scales, static_cast<int>(threadIdx.x), stop};
+  words.start(first);
+  // ... Q, a warp's block of 8 rows, and the rows' masks
+  static_assert(NT <= WP && NR * 4 <= 32 * WP, "a block to a warp, a word to a thread");
+  uint4 v[KC];
+  {
+    int t;
+    const int out = warp < NT ? out_row(8 * warp + g, &t) : -1;
+    const bool live = out >= 0 && t < it.live;
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + static_cast<long long>(max(out, 0)) * p.d;
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      v[c] = make_uint4(0, 0, 0, 0);
+      if (live && 32 * c < p.d) v[c] = __ldg(reinterpret_cast<const uint4*>(src + 32 * c + 8 * j));
+    }
+  }
+  const uint64_t bits = threadIdx.x < NR * 4 ? mask_word(p, it, static_cast<int>(threadIdx.x), out_row) : 0;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < C::ST; ++s)
+      if (first + s * kKeys < stop) load(ring + s * 2 * C::TILE, bars + 8 * s, first + s * kKeys);
+  uint2* q_frags = reinterpret_cast<uint2*>(smem + C::OFF_Q) + lane;
+  if (warp < NT) {
+    const float2 f = q_fragments<KC>(v, p.scale_log2, [&](int i, uint2 b) { q_frags[(i * NT + warp) * 32] = b; });
+    if (j == 0) factors[8 * warp + g] = f;
+  }
+  if (threadIdx.x < NR * 4) masks[threadIdx.x >> 2][threadIdx.x & 3] = bits;
+  __syncthreads();  // (the barriers are set up, too)
+
+  float o[NT][FT][4];
+  float ref[NT][2], l[NT][2], ofs[NT][2];  // references less kLift; sums over the warp's keys
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int f = 0; f < FT; ++f)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[n][f][x] = 0.f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      ref[n][r] = kNoRef;
+      l[n][r] = 0.f;
+      ofs[n][r] = 0.f;
+    }
+  }
+  const int row16 = lane & 15;
+  const uint32_t k_at = (kTile * warp + row16) * C::ROW + 16 * (swizzle<W>(row16) ^ (lane >> 4));
+  // of values a warp has pieces WC warp ..: two at a time, or one of two blocks of 16 keys
+  const int v_row = C::WC == 1 ? lane : row16;
+  const uint32_t v_at = C::TILE + v_row * C::ROW + 16 * (swizzle<W>(v_row) ^ (C::WC * warp + (C::WC == 1 ? 0 : lane >> 4)));
+  float4* keys = reinterpret_cast<float4*>(smem + C::OFF_KEYS) + kTile * warp;
+  float* keys_ofs = reinterpret_cast<float*>(smem + C::OFF_KEYS + kKeys * 16) + kTile * warp;
+  uint2* p_frags = reinterpret_cast<uint2*>(smem + C::OFF_P) + lane;
+
+  bool gave_up = false;
+  int stage = 0, i = 0;
+  uint32_t parity = 0;
+#pragma unroll 1
+  for (int tile0 = first; tile0 < stop; tile0 += kKeys, ++i) {
+    const uint32_t tile = ring + stage * 2 * C::TILE;
+    const uint2 kv = words.get(i, tile0);
+    const KeyFactors mine = key_factors(kv.x, kv.y);
+    // the keys' factors by way of shared memory: lane's own key to the lanes of its row
+    __syncwarp();  // (the tile before is read)
+    keys[lane] = make_float4(mine.step, mine.lo, mine.v_log, mine.v_inv);
+    keys_ofs[lane] = mine.v_ofs;
+    const bool ok = mbar_wait(bars + 8 * stage, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + 32 + stage);
+    // ---- scores of the warp's keys
+    __syncwarp();  // (ldmatrix wants the warp together; the factors are there)
+    float s[MT][NT][4];
+    score_products<W, NT>(tile + k_at, s, (rows_here + 7) / 8, [&](int i, int n) { return q_frags[(i * NT + n) * 32]; });
+    float v_inv[MT][2], v_ofs[MT][2];
+    const int key0 = tile0 + kTile * warp;
+    const bool masked = key0 + kTile > min(it.n, stop);
+    float top = -INFINITY;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 kf = keys[16 * m + 8 * h + g];
+        v_inv[m][h] = kf.w;
+        v_ofs[m][h] = keys_ofs[16 * m + 8 * h + g];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (8 * n >= rows_here) break;
+          const float4 f = *reinterpret_cast<const float4*>(factors + 8 * n + 2 * j);
+          float* y = s[m][n] + 2 * h;
+          float t0, t1, u0, u1;
+          mul2(t0, t1, y[0], y[1], f.x, f.z);
+          fma2(u0, u1, f.y, f.w, kf.y, kf.y, kf.z, kf.z);
+          fma2(y[0], y[1], t0, t1, kf.x, kf.x, u0, u1);
+        }
+        if (masked) {
+          const int key = key0 + 16 * m + 8 * h + g, off = key - it.n;
+          bool any = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              bool sees = key < stop;
+              if (sees && off >= 0)  // (off < 256: the drafted tokens end there)
+                sees = (masks[8 * n + 2 * j + r][off >> 6] >> (off & 63)) & 1;
+              if (!sees) s[m][n][2 * h + r] = -INFINITY;
+              any = any || sees;
+            }
+          // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
+          if (!any) v_inv[m][h] = v_ofs[m][h] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (8 * n >= rows_here) break;
+          top = fmax3(top, s[m][n][2 * h] - ref[n][0], s[m][n][2 * h + 1] - ref[n][1]);
+        }
+      }
+    // (behind this every warp is done with the tile before: its stage and the weights'
+    // buffer are free)
+    const bool move = __syncthreads_or(top > kLimit);
+    const int before = stage == 0 ? C::ST - 1 : stage - 1;
+    if (threadIdx.x == 0 && tile0 > first && tile0 + (C::ST - 1) * kKeys < stop)
+      load(ring + before * 2 * C::TILE, bars + 8 * before, tile0 + (C::ST - 1) * kKeys);
+    if (move) {
+      // references up to this tile's maxima, what was summed down by as much
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (8 * n >= rows_here) break;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float m = fmaxf(s[0][n][r], s[0][n][2 + r]);
+#pragma unroll
+          for (int y = 1; y < MT; ++y) m = fmax3(m, s[y][n][r], s[y][n][2 + r]);
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+          if (g == 0) maxima[warp][8 * n + 2 * j + r] = m;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (8 * n >= rows_here) break;
+        float by[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 8 * n + 2 * j + r;
+          float m = fmax3(maxima[0][row], maxima[1][row], fmaxf(maxima[2][row], maxima[3][row]));
+          m = fmaxf(ref[n][r], m - kLift);
+          by[r] = ex2_approx(ref[n][r] - m);
+          ref[n][r] = m;
+          l[n][r] *= by[r];
+          ofs[n][r] *= by[r];
+        }
+#pragma unroll
+        for (int f = 0; f < FT; ++f)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) o[n][f][z] *= by[z & 1];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (8 * n >= rows_here) break;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t pt[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float w0, w1;
+          add2(w0, w1, s[m][n][2 * h], s[m][n][2 * h + 1], -ref[n][0], -ref[n][1]);
+          w0 = ex2_approx(w0);
+          w1 = ex2_approx(w1);
+          fma2(l[n][0], l[n][1], w0, w1, v_inv[m][h], v_inv[m][h], l[n][0], l[n][1]);
+          const uint32_t w = pack_f16x2(w0, w1);
+          // (the offsets with the rounded weights, as in the kernel above)
+          fma2(ofs[n][0], ofs[n][1], half_lo(w), half_hi(w), v_ofs[m][h], v_ofs[m][h], ofs[n][0], ofs[n][1]);
+          pt[h] = transposed(w);
+        }
+        p_frags[((MT * warp + m) * NT + n) * 32] = make_uint2(pt[0], pt[1]);
+      }
+    }
+    gave_up = __syncthreads_or(!ok);  // the weights are there
+    if (gave_up) break;
+    // ---- o += V^T P^T of the warp's features, 16 keys at a time
+    uint2 w[NT];
+    auto weights = [&](int k) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (8 * n < rows_here) w[n] = p_frags[(k * NT + n) * 32];
+    };
+    auto products = [&](int c, uint32_t y0, uint32_t y1) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        uint32_t a[4];
+        codes_of(a, z ? y0 >> 8 : y0, z ? y1 >> 8 : y1, false);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (8 * n >= rows_here) break;
+          mma_f16(o[n][2 * c + z], a, w[n].x, w[n].y);
+        }
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kKeys / 16; k += C::WC == 1 ? 2 : 1) {
+      uint32_t y[4];
+      ld_columns16(tile + v_at + 16 * k * C::ROW, y);
+      weights(k);
+      products(0, y[0], y[1]);
+      if constexpr (C::WC == 1) weights(k + 1);
+      products(C::WC == 1 ? 0 : 1, y[2], y[3]);
+    }
+    if (++stage == C::ST) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+  if (gave_up && threadIdx.x == 0) {
+    // the copies in flight must land before the CTA exits (each wait is bounded)
+    volatile int never = 0;
+    for (int s = 0; s < C::ST; ++s) mbar_wait(bars + 8 * s, parity ^ (s < stage ? 1 : 0), &never, p.status, 0);
+  }
+
+  // ---- the warps' sums together
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int z = 4; z < 32; z <<= 1) {
+        l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], z);
+        ofs[n][r] += __shfl_xor_sync(0xffffffffu, ofs[n][r], z);
+      }
+    }
+  __syncthreads();  // (the maxima lie where the sums go)
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (g == 0) stats[warp][8 * n + 2 * j + r] = make_float2(l[n][r], ofs[n][r]);
+  __syncthreads();
+  const bool whole = it.splits == 1;
+  const long long first_part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (8 * n >= rows_here) break;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      int t;
+      const int row = 8 * n + 2 * j + r, out = out_row(row, &t);
+      if (out < 0) continue;
+      float L = 0.f, add = 0.f;
+#pragma unroll
+      for (int w = 0; w < WP; ++w) {
+        const float2 y = stats[w][row];
+        L += y.x;
+        add += y.y;
+      }
+      const bool live = t < it.live && ref[n][r] != kNoRef && !gave_up;
+      if (!live) L = 0.f;
+      if (warp == 0 && g == 0) {
+        if (!whole) {
+          p.part_m[first_part + out] = L == 0.f ? -INFINITY : ref[n][r];
+          p.part_l[first_part + out] = L;
+        } else if (p.lse) {
+          p.lse[(static_cast<long long>(it.b) * p.H + out % p.H) * p.T + t] =
+              L == 0.f ? -INFINITY : (ref[n][r] + __log2f(L)) * 0.69314718055994531f;
+        }
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int c = 0; c < C::WC; ++c) {
+        const int f = 32 * (C::WC * warp + c) + 4 * g;  // four features
+        float y[4];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {  // (codes are 2^-24, odd features 2^-20)
+          y[2 * z] = live ? fmaf(o[n][2 * c + z][r], 16777216.f, add) : 0.f;
+          y[2 * z + 1] = live ? fmaf(o[n][2 * c + z][2 + r], 1048576.f, add) : 0.f;
+        }
+        if (!whole)
+          *reinterpret_cast<float4*>(p.part_o + (first_part + out) * W + f) = make_float4(y[0], y[1], y[2], y[3]);
+        else if (f < p.d)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d + f) =
+              make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
+      }
     }
   }
 }
@@ -668,19 +1102,30 @@ __global__ void __launch_bounds__(32 * kWarps, C::CTAS) rows_q4_kernel(const __g
 template <typename F>
 void with_config(int d, int R, F&& f) {
   if (d <= 64) {
-    if (R <= 2) f(Q4Cfg<64, 1, true, 4, 6>{});
-    else if (R <= 8) f(Q4Cfg<64, 1, false, 4, 5>{});
-    else f(Q4Cfg<64, 2, false, 4, 4>{});
+    if (R == 1) f(Q4Cfg<64, 1, 4, 6>{});
+    else if (R == 2) f(Q4Cfg<64, 2, 4, 6>{});
+    else if (R <= 8) f(Q4Cfg<64, 8, 4, 4>{});
+    else if (R <= 16) f(Q4Cfg<64, 16, 4, 3>{});
+    else f(Q4Cfg<64, 32, 7, 2>{});
   } else if (d <= 128) {
-    if (R <= 2) f(Q4Cfg<128, 1, true, 2, 5>{});
-    else if (R <= 8) f(Q4Cfg<128, 1, false, 2, 4>{});
-    else if (R <= 16) f(Q4Cfg<128, 2, false, 3, 3>{});
-    else f(Q4Cfg<128, 4, false, 3, 2>{});
+    if (R == 1) f(Q4Cfg<128, 1, 3, 4>{});
+    else if (R == 2) f(Q4Cfg<128, 2, 3, 4>{});
+    else if (R <= 8) f(Q4Cfg<128, 8, 2, 4>{});
+    else if (R <= 16) f(Q4Cfg<128, 16, 3, 3>{});
+    else f(Q4BlockCfg<128, 4, 3, 2>{});
   } else {
-    if (R <= 2) f(Q4Cfg<256, 1, true, 2, 3>{});
-    else if (R <= 8) f(Q4Cfg<256, 1, false, 2, 3>{});
-    else f(Q4Cfg<256, 2, false, 2, 2>{});
+    if (R == 1) f(Q4Cfg<256, 1, 2, 3>{});
+    else if (R == 2) f(Q4Cfg<256, 2, 2, 3>{});
+    else if (R <= 8) f(Q4Cfg<256, 8, 2, 3>{});
+    else if (R <= 16) f(Q4BlockCfg<256, 2, 2, 2>{});
+    else f(Q4BlockCfg<256, 4, 2, 2>{});
   }
+}
+
+template <class C>
+constexpr auto kernel_of() {
+  if constexpr (C::SHARES) return rows_q4_block_kernel<C>;
+  else return rows_q4_kernel<C>;
 }
 
 template <class C>
@@ -691,16 +1136,16 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
   static bool attr_set[64] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(rows_q4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(kernel_of<C>(), cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
-  e = launch_serialized(rows_q4_kernel<C>, grid, dim3(32 * kWarps), C::SMEM, stream, p);
+  e = launch_serialized(kernel_of<C>(), grid, dim3(32 * C::WP), C::SMEM, stream, p);
   if (info) {
     info->kernels = 1;
     info->grid = static_cast<int>(grid.x);
-    info->block = 32 * kWarps;
+    info->block = 32 * C::WP;
     info->smem = C::SMEM;
   }
   return e;

@@ -15,9 +15,11 @@
 // registers, waits for its threads, and writes.  No second buffer, no order, one launch
 // for keys, values and scales.
 //
-// Bound by memory: a fork reads every source row and writes every moved one; a block
-// has 32 KB in flight.  A compaction moves a few rows: its time is that of a launch and
-// of two dependent reads.
+// Bound by memory: a fork reads every source row and writes every moved one, a block with
+// two buffers of 32 KB (8-bit, 4 x 4 beams of 96 heads, 280 MB: 57 us, 4.9 TB/s; three
+// blocks to an SM; smaller buffers move shorter runs of each row: 16 KB with four blocks 69
+// us, with six 81; eight elements in each thread's registers 81).  A compaction moves a few
+// rows: its time, 2 us, is that of a launch and of two dependent reads.
 #include "kernels.h"
 
 namespace mha {
@@ -26,62 +28,63 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kItems = 8;                       // per thread
 constexpr int kBlockItems = kThreads * kItems;  // moves of one block at a time
+constexpr int kMaxLog = 8;                      // a block's columns: at most a thread each
 
 struct Move {
-  int to, from;    // sequences (fork), positions after the prefix (compact)
+  int to, from;    // sequences (fork), positions (compact)
   int first, end;  // fork: positions that move
 };
 
-// The largest power of two of columns with which m moves (1 .. kBlockItems) of each are a block's items.
-__device__ __forceinline__ int log_columns(int m) { return 31 - __clz(kBlockItems / m); }
+// Columns (log2) of a block when m moves (1 .. items) of each are its items.
+__host__ __device__ __forceinline__ int log_columns(int m, int items) {
+  int lg = 0;
+  while (lg < kMaxLog && (2 << lg) * m <= items) ++lg;
+  return lg;
+}
 
-// One element of type V for each of `count` items: locate(i, &to, &from) gives its
-// addresses, false where nothing moves.  (Asked again for the writes: eight pairs of
-// addresses kept beside eight elements took 124 registers.)
-template <typename V, typename F>
-__device__ __forceinline__ void move_items(int count, F&& locate) {
+// All moves of 2^lg columns of elements V.  `column`: the thread's column (threads tid,
+// tid + 2^lg, ... share it) of sequence or position 0, `stride` elements between
+// sequences or positions; `j`: its position, -1: none moves.
+template <typename V>
+__device__ __forceinline__ void move_columns(const Move* moves, int n, int lg, V* column, long long stride, int j) {
   V x[kItems];
+  const int m0 = static_cast<int>(threadIdx.x) >> lg, step = kThreads >> lg;
 #pragma unroll
   for (int u = 0; u < kItems; ++u) {
-    const int i = static_cast<int>(threadIdx.x) + u * kThreads;
-    V* to;
-    const V* from;
+    if (m0 + u * step >= n) break;
+    const Move m = moves[m0 + u * step];
     // (a coherent load: the source may be written later in this launch)
-    if (i < count && locate(i, &to, &from)) x[u] = __ldcg(from);
+    if (j >= m.first && j < m.end) x[u] = __ldcg(column + m.from * stride);
   }
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < kItems; ++u) {
-    const int i = static_cast<int>(threadIdx.x) + u * kThreads;
-    V* to;
-    const V* from;
-    if (i < count && locate(i, &to, &from)) *to = x[u];
+    if (m0 + u * step >= n) break;
+    const Move m = moves[m0 + u * step];
+    if (j >= m.first && j < m.end) column[m.to * stride] = x[u];
   }
 }
 
 // ---------------------------------------------------------------------------
 // fork
 // ---------------------------------------------------------------------------
+constexpr int kForkBlocks = 3;    // per SM
+constexpr int kForkItems = 2048;  // of a block at a time (kMaxForkSeqs at least)
+static_assert(kForkItems >= kMaxForkSeqs && kForkItems <= kBlockItems, "a column of every sequence");
+
 template <typename S>
-__device__ __forceinline__ void fork_scales(const MoveParams& p, const Move* moves, int n, int c, long long e0, int lg,
+__device__ __forceinline__ void fork_scales(const MoveParams& p, const Move* moves, int n, int lg, int c, long long e,
                                             int lo, int span) {
-  S* at = reinterpret_cast<S*>(p.scales[c]);
-  const long long all = static_cast<long long>(p.H) * span;
-  move_items<S>(n << lg, [&](int i, S** to, const S** from) {
-    const Move m = moves[i >> lg];
-    const long long e = e0 + (i & ((1 << lg) - 1));
-    if (e >= all) return false;
-    const long long h = e / span;
-    const int j = lo + static_cast<int>(e - h * span);
-    if (j < m.first || j >= m.end) return false;
-    *to = at + (static_cast<long long>(m.to) * p.H + h) * p.Lk + j;
-    *from = at + (static_cast<long long>(m.from) * p.H + h) * p.Lk + j;
-    return true;
-  });
+  // (head e / span, position lo + e % span)
+  const long long h = e / span;
+  const int j = h < p.H ? lo + static_cast<int>(e - h * span) : -1;
+  move_columns(moves, n, lg, reinterpret_cast<S*>(p.scales[c]) + h * p.Lk + max(j, 0),
+               static_cast<long long>(p.H) * p.Lk, j);
 }
 
-__global__ void __launch_bounds__(kThreads, 4) cache_fork_kernel(const __grid_constant__ MoveParams p) {
-  __shared__ Move moves[kMaxForkSeqs];
+__global__ void __launch_bounds__(kThreads, kForkBlocks) cache_fork_kernel(const __grid_constant__ MoveParams p) {
+  extern __shared__ __align__(16) uint8_t held[];  // [2][kForkItems] of 16 bytes, then a move of every sequence
+  Move* moves = reinterpret_cast<Move*>(held + 2 * 16 * kForkItems);
   __shared__ int count, lowest, highest;
   if (threadIdx.x == 0) {
     count = 0;
@@ -105,55 +108,64 @@ __global__ void __launch_bounds__(kThreads, 4) cache_fork_kernel(const __grid_co
   const int n = count;
   if (n == 0) return;
   // a block's columns: 2^lg pieces of the rows of the positions lo .. lo + span - 1, or
-  // 2^lg scales of all heads at these positions
-  const int lg = log_columns(n), lo = lowest, span = highest - lo;
-  const long long pieces = p.row_bytes / 16, all = span * pieces;
-  const long long chunks = (all + (1 << lg) - 1) >> lg;
+  // 2^scale_lg scales of all heads at these positions
+  const int lg = log_columns(n, kForkItems), scale_lg = log_columns(n, kBlockItems), lo = lowest, span = highest - lo;
+  const int own = static_cast<int>(threadIdx.x) & ((1 << lg) - 1);
+  const long long pieces = p.row_bytes / 16, seq = p.Lk * pieces;
+  const long long chunks = (span * pieces + (1 << lg) - 1) >> lg;
   const long long scale_chunks =
-      p.scale_bytes ? (static_cast<long long>(p.H) * span + (1 << lg) - 1) >> lg : 0;
-  for (long long x = blockIdx.x; x < 2 * (chunks + scale_chunks); x += gridDim.x) {
+      p.scale_bytes ? (static_cast<long long>(p.H) * span + (1 << scale_lg) - 1) >> scale_lg : 0;
+  // The codes by way of shared memory, the next columns' copies while these are written
+  // (a thread writes what it copied; the barrier is for the others' rows).
+  const uint32_t slots = smem_u32(held) + 16 * threadIdx.x;
+  const int m0 = static_cast<int>(threadIdx.x) >> lg, step = kThreads >> lg;
+  auto columns = [&](long long x, int* j) {
+    const int c = x >= chunks;
+    const long long q = ((c ? x - chunks : x) << lg) + own;  // from position lo on
+    *j = q < span * pieces ? lo + static_cast<int>(q / pieces) : -1;
+    return reinterpret_cast<uint4*>(p.codes[c]) + lo * pieces + q;
+  };
+  auto copy = [&](long long x, int buffer) {
     if (x < 2 * chunks) {
-      const int c = x >= chunks;
-      const long long q0 = lo * pieces + ((c ? x - chunks : x) << lg), stop = (lo + static_cast<long long>(span)) * pieces;
-      uint4* at = reinterpret_cast<uint4*>(p.codes[c]);
-      const long long seq = p.Lk * pieces;
-      move_items<uint4>(n << lg, [&](int i, uint4** to, const uint4** from) {
-        const Move m = moves[i >> lg];
-        const long long q = q0 + (i & ((1 << lg) - 1));
-        if (q >= stop || q < m.first * pieces || q >= m.end * pieces) return false;
-        *to = at + m.to * seq + q;
-        *from = at + m.from * seq + q;
-        return true;
-      });
-    } else {
-      const long long y = x - 2 * chunks;
-      const int c = y >= scale_chunks;
-      const long long e0 = (c ? y - scale_chunks : y) << lg;
-      if (p.scale_bytes == 1) fork_scales<uint8_t>(p, moves, n, c, e0, lg, lo, span);
-      else fork_scales<uint32_t>(p, moves, n, c, e0, lg, lo, span);
+      int j;
+      const uint4* column = columns(x, &j);
+      uint32_t to = slots + buffer * (16 * kForkItems);
+      for (int i = m0; i < n; i += step, to += 16 * kThreads) {
+        const Move m = moves[i];
+        if (j >= m.first && j < m.end)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(column + m.from * seq) : "memory");
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  copy(blockIdx.x, 0);
+  int buffer = 0;
+  long long x = blockIdx.x;
+  for (; x < 2 * chunks; x += gridDim.x, buffer ^= 1) {
+    copy(x + gridDim.x, buffer ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    int j;
+    uint4* column = columns(x, &j);
+    const uint4* from = reinterpret_cast<const uint4*>(held) + buffer * kForkItems + threadIdx.x;
+    for (int i = m0; i < n; i += step, from += kThreads) {
+      const Move m = moves[i];
+      if (j >= m.first && j < m.end) column[m.to * seq] = *from;
+    }
+  }
+  for (; x < 2 * (chunks + scale_chunks); x += gridDim.x) {
+    const long long y = x - 2 * chunks;
+    const int c = y >= scale_chunks;
+    const long long e = ((c ? y - scale_chunks : y) << scale_lg) + (threadIdx.x & ((1u << scale_lg) - 1));
+    if (p.scale_bytes == 1) fork_scales<uint8_t>(p, moves, n, scale_lg, c, e, lo, span);
+    else fork_scales<uint32_t>(p, moves, n, scale_lg, c, e, lo, span);
   }
 }
 
 // ---------------------------------------------------------------------------
 // compact
 // ---------------------------------------------------------------------------
-constexpr int kMaxMoves = 256;      // drafted tokens of a step
-constexpr int kMaxPieceLog = 7;     // a block's columns are at most 2 KB of a row
-
-template <typename S>
-__device__ __forceinline__ void compact_scales(const MoveParams& p, const Move* moves, int n, int c, long long at0,
-                                               int h0, int lg) {
-  S* at = reinterpret_cast<S*>(p.scales[c]) + at0;
-  move_items<S>(n << lg, [&](int i, S** to, const S** from) {
-    const Move m = moves[i >> lg];
-    const int h = h0 + (i & ((1 << lg) - 1));
-    if (h >= p.H) return false;
-    *to = at + static_cast<long long>(h) * p.Lk + m.to;
-    *from = at + static_cast<long long>(h) * p.Lk + m.from;
-    return true;
-  });
-}
+constexpr int kMaxMoves = 256;  // drafted tokens of a step
 
 // Block x of sequence b: its K or V columns x of 2^lg pieces, or the scales of 2^lg heads.
 __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_constant__ MoveParams p, int lg, int chunks,
@@ -174,29 +186,24 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
     Move m;
     m.to = prefix + i;
     m.from = prefix + from;
-    m.first = m.end = 0;
+    m.first = 0;
+    m.end = 1;
     moves[atomicAdd(&count, 1)] = m;
   }
   __syncthreads();
   const int n = count;
   if (n == 0) return;
+  const int own = static_cast<int>(threadIdx.x) & ((1 << lg) - 1);
   if (x < 2 * chunks) {
     const int c = x >= chunks;
-    const long long pieces = p.row_bytes / 16, q0 = static_cast<long long>(c ? x - chunks : x) << lg;
-    uint4* at = reinterpret_cast<uint4*>(p.codes[c]) + static_cast<long long>(b) * p.Lk * pieces;
-    move_items<uint4>(n << lg, [&](int i, uint4** to, const uint4** from) {
-      const Move m = moves[i >> lg];
-      const long long q = q0 + (i & ((1 << lg) - 1));
-      if (q >= pieces) return false;
-      *to = at + m.to * pieces + q;
-      *from = at + m.from * pieces + q;
-      return true;
-    });
+    const long long pieces = p.row_bytes / 16, q = (static_cast<long long>(c ? x - chunks : x) << lg) + own;
+    move_columns(moves, n, lg, reinterpret_cast<uint4*>(p.codes[c]) + static_cast<long long>(b) * p.Lk * pieces + q, pieces,
+                 q < pieces ? 0 : -1);
   } else {
-    const int y = x - 2 * chunks, c = y >= scale_chunks, h0 = (c ? y - scale_chunks : y) << lg;
-    const long long at0 = static_cast<long long>(b) * p.H * p.Lk;
-    if (p.scale_bytes == 1) compact_scales<uint8_t>(p, moves, n, c, at0, h0, lg);
-    else compact_scales<uint32_t>(p, moves, n, c, at0, h0, lg);
+    const int y = x - 2 * chunks, c = y >= scale_chunks, h = ((c ? y - scale_chunks : y) << lg) + own;
+    const long long at = (static_cast<long long>(b) * p.H + h) * p.Lk;
+    if (p.scale_bytes == 1) move_columns(moves, n, lg, p.scales[c] + at, 1, h < p.H ? 0 : -1);
+    else move_columns(moves, n, lg, reinterpret_cast<uint32_t*>(p.scales[c]) + at, 1, h < p.H ? 0 : -1);
   }
 }
 
@@ -208,12 +215,6 @@ void say(LaunchInfo* info, unsigned grid) {
   info->smem = 0;
 }
 
-// Columns (a power of two) of a compaction's block when up to T tokens move.
-int compact_log(int T) {
-  int lg = 0;
-  while (lg < kMaxPieceLog && (2 << lg) * T <= kBlockItems) ++lg;
-  return lg;
-}
 long long compact_chunks(const MoveParams& p, int lg) { return (p.row_bytes / 16 + (1 << lg) - 1) >> lg; }
 long long compact_scale_chunks(const MoveParams& p, int lg) {
   return p.scale_bytes ? (static_cast<long long>(p.H) + (1 << lg) - 1) >> lg : 0;
@@ -222,24 +223,36 @@ long long compact_scale_chunks(const MoveParams& p, int lg) {
 }  // namespace
 
 long long compact_blocks(const MoveParams& p) {
-  const int lg = compact_log(p.T);
+  const int lg = log_columns(p.T, kBlockItems);
   return p.B * 2 * (compact_chunks(p, lg) + compact_scale_chunks(p, lg));
 }
 
 cudaError_t launch_cache_fork(const MoveParams& p, cudaStream_t stream, LaunchInfo* info) {
-  // blocks for every item that the capacity allows, at most eight to an SM: what moves
+  // blocks for every item that the capacity allows, at most kForkBlocks to an SM: what moves
   // is known on the device alone
   const double items = 2. * p.B * p.Lk * (p.row_bytes / 16 + (p.scale_bytes ? p.H : 0));
-  const unsigned most = 152 * 8;
+  const unsigned most = 152 * kForkBlocks;
   const unsigned grid = items < static_cast<double>(most) * kBlockItems
                             ? static_cast<unsigned>(items / kBlockItems) + 1
                             : most;
   say(info, grid);
-  return launch_serialized(cache_fork_kernel, dim3(grid), dim3(kThreads), 0, stream, p);
+  constexpr int kMostSmem = 2 * 16 * kForkItems + kMaxForkSeqs * static_cast<int>(sizeof(Move));
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static bool attr_set[64] = {};
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(cache_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  return launch_serialized(cache_fork_kernel, dim3(grid), dim3(kThreads),
+                           2 * 16 * kForkItems + p.B * sizeof(Move), stream, p);
 }
 
 cudaError_t launch_cache_compact(const MoveParams& p, cudaStream_t stream, LaunchInfo* info) {
-  const int lg = compact_log(p.T);
+  const int lg = log_columns(p.T, kBlockItems);
   const unsigned grid = static_cast<unsigned>(compact_blocks(p));
   say(info, grid);
   return launch_serialized(cache_compact_kernel, dim3(grid), dim3(kThreads), 0, stream, p, lg,

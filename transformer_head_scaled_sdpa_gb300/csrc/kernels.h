@@ -195,7 +195,7 @@ struct CacheParams {
 };
 
 // Blocks of the launch for these sizes (must fit a grid dimension).
-long long cache_blocks(int B, int T, int H);
+long long cache_blocks(CacheKind kind, int B, int T, int H);
 cudaError_t launch_cache(const CacheParams& p, CacheKind kind, bool write, cudaStream_t stream, LaunchInfo* info);
 
 // Rows of a cache moved in place (mha_cache_move.cu): every move reads what the rows

@@ -652,7 +652,7 @@ static int cache_write(mha::CacheKind kind, const void* k, const void* v, long l
     for (int i = o + 1; i < 4; ++i)
       if (overlaps(outs[o], outs_b[o], outs[i], outs_b[i])) return MHA_ERR_ALIAS;
   }
-  if (mha::cache_blocks(B, T, H) > 0x7fffffffll) return MHA_ERR_SHAPE;
+  if (mha::cache_blocks(kind, B, T, H) > 0x7fffffffll) return MHA_ERR_SHAPE;
   DeviceState* dev = nullptr;
   const int rc = device_state(&dev);
   if (rc != MHA_OK) return rc;
@@ -702,7 +702,7 @@ static int cache_read(mha::CacheKind kind, const void* k_cache, const void* v_ca
     if (overlaps(k, values, ins[i], ins_b[i]) || overlaps(v, values, ins[i], ins_b[i]))
       return MHA_ERR_ALIAS;
   if (overlaps(k, values, v, values)) return MHA_ERR_ALIAS;
-  if (mha::cache_blocks(B, Lk, H) > 0x7fffffffll) return MHA_ERR_SHAPE;
+  if (mha::cache_blocks(kind, B, Lk, H) > 0x7fffffffll) return MHA_ERR_SHAPE;
   DeviceState* dev = nullptr;
   const int rc = device_state(&dev);
   if (rc != MHA_OK) return rc;

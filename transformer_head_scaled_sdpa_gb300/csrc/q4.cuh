@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "fp8.cuh"
+#include "ptx.cuh"
 
 namespace mha {
 
@@ -21,7 +22,9 @@ namespace mha {
 constexpr float kMinStep = 8.67361738e-19f;  // 2^-60
 
 struct RowQ4 {
-  float lo, step, inv;  // (inv: a little above 1 / step)
+  float lo, step;
+  float inv;     // a little below 1 / step
+  bool careful;  // codes_q4 has to look twice
 };
 
 // The row's offset and step from its smallest and largest value.
@@ -32,6 +35,7 @@ __device__ __forceinline__ RowQ4 row_q4(float lo, float hi) {
     r.lo = __int_as_float(0x7fc00000);
     r.step = kMinStep;
     r.inv = 0.f;
+    r.careful = false;
     return r;
   }
   r.lo = lo + 0.f;  // (-0 as 0)
@@ -41,18 +45,48 @@ __device__ __forceinline__ RowQ4 row_q4(float lo, float hi) {
   for (int i = 0; i < 2; ++i)
     if (!(__fmaf_rd(15.f, s, lo) >= hi)) s = __uint_as_float(__float_as_uint(s) + 0x10000u);
   r.step = fmaxf(fmaxf(s, fmaxf(fabsf(lo), fabsf(hi)) * 0x1p-13f), kMinStep);
-  r.inv = __frcp_rn(r.step) * 1.000004f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(r.step));  // (to 2^-23)
+  r.inv = inv * (1.f - 0x1p-20f);
+  const float zero = -r.lo * inv, part = zero - floorf(zero);
+  r.careful = (r.lo != 0.f && fabsf(r.lo) < 0.0148f * r.step) || fabsf(part - 0.5f) < 0.0149f;
   return r;
 }
 
-// A value's code.  The first estimate is the code or the one above (its factor is a
-// little too large); x at or below the middle between it and the one below takes that.
+constexpr float kToInteger = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+
+// A value's code, whatever the row.  The first estimate is the code or the one above (its
+// factor is a little too large); x at or below the middle between it and the one below
+// takes that.
 __device__ __forceinline__ uint32_t code_q4(float x, const RowQ4& r) {
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-  const float up = fmaf(x - r.lo, r.inv, kRound);
-  const float k = up - kRound;
+  const float up = fmaf(x - r.lo, r.inv * (1.f + 0x1p-17f), kToInteger);
   const uint32_t c = __float_as_uint(up) & 15u;
-  return x > __fmaf_rd(k - 0.5f, r.step, r.lo) ? c : c - 1u;
+  return x > __fmaf_rd(up - kToInteger - 0.5f, r.step, r.lo) ? c : c - 1u;
+}
+
+// The codes of eight values, four bits each, the first in the lowest.  For nearly all rows
+// one rounded product decides.  q = (x - lo) / step against a middle h = k + 1/2: where
+// they differ, by u / (2 step) at least, u the last place of x, of lo or half of step's,
+// whichever is finest; relative to q, u / (2 (x - lo)).  Where |x| and |lo| are at least
+// 2^-10 (x - lo) (or lo is 0) that is 2^-19 or more, while the product is below q by 2^-20
+// with an error of 2^-21.6: it lies on q's side of h, and below h when q = h.  Else q is
+// within 15 * 2^-10 of -lo / step (x near 0), or lo is that near 0: rows where -lo / step
+// is that near to a middle, or to 0, are `careful`.
+__device__ __forceinline__ uint32_t codes_q4(const float (&x)[8], const RowQ4& r) {
+  uint32_t c = 0;
+  if (r.careful) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c |= code_q4(x[i], r) << (4 * i);
+    return c;
+  }
+#pragma unroll
+  for (int i = 6; i >= 0; i -= 2) {
+    float a, b;
+    add2(a, b, x[i], x[i + 1], -r.lo, -r.lo);
+    fma2(a, b, a, b, r.inv, r.inv, kToInteger, kToInteger);
+    c = (c * 16u + __float_as_uint(b)) * 16u + __float_as_uint(a);
+  }
+  return c - 0x4b400000u * 0x11111111u;  // (less kToInteger's bits in every place)
 }
 
 }  // namespace mha

@@ -290,31 +290,37 @@ struct Scales {
 };
 static_assert((kAhead & (kAhead + 1)) == 0, "slots by a mask");
 
-// What a CTA loads: tiles of kKeys keys and values into a ring of ST stages.
+// What a CTA loads: tiles of kKeys keys or values.
 template <int W>
 struct Loader {
   static constexpr int ROW = W / 2, TILE = kKeys * ROW;
   const RowsParams& p;
   const Unit& it;
   int stop;
-  __device__ __forceinline__ void operator()(uint32_t dst, uint32_t bar, int key) const {
-    const int rows = stop - key;
-    if (rows >= kKeys) {
-      mbar_arrive_expect_tx(bar, 2 * TILE);
-      tma_load_4d(dst, &p.tm_k, bar, 0, it.hk, key, it.b);
-      tma_load_4d(dst + TILE, &p.tm_v, bar, 0, it.hk, key, it.b);
+  // (a ragged tile in boxes of kRowsQ4Box keys as far as it goes; what lies behind in the
+  // ring are some codes: finite, and their weights are 0)
+  __device__ __forceinline__ int boxes(int key) const {
+    return stop - key >= kKeys ? 0 : (stop - key + kRowsQ4Box - 1) / kRowsQ4Box;
+  }
+  __device__ __forceinline__ uint32_t bytes(int key) const {
+    const int n = boxes(key);
+    return n == 0 ? TILE : n * kRowsQ4Box * ROW;
+  }
+  __device__ __forceinline__ void copy(uint32_t dst, uint32_t bar, int key, bool v) const {
+    const int n = boxes(key);
+    if (n == 0) {
+      tma_load_4d(dst, v ? &p.tm_v : &p.tm_k, bar, 0, it.hk, key, it.b);
       return;
     }
-    // a ragged one in boxes of kRowsQ4Box keys as far as it goes (what lies behind in the
-    // ring are some codes: finite, and their weights are 0)
-    const int boxes = (rows + kRowsQ4Box - 1) / kRowsQ4Box;
-    mbar_arrive_expect_tx(bar, 2 * boxes * kRowsQ4Box * ROW);
 #pragma unroll 1
-    for (int x = 0; x < boxes; ++x) {
-      const uint32_t to = dst + x * kRowsQ4Box * ROW;
-      tma_load_4d(to, &p.tm_k_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
-      tma_load_4d(to + TILE, &p.tm_v_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
-    }
+    for (int x = 0; x < n; ++x)
+      tma_load_4d(dst + x * kRowsQ4Box * ROW, v ? &p.tm_v_box : &p.tm_k_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
+  }
+  // Keys and values side by side.
+  __device__ __forceinline__ void operator()(uint32_t dst, uint32_t bar, int key) const {
+    mbar_arrive_expect_tx(bar, 2 * bytes(key));
+    copy(dst, bar, key, false);
+    copy(dst + TILE, bar, key, true);
   }
 };
 
@@ -333,8 +339,7 @@ struct Q4Cfg {
   static constexpr int KC = W / 32;                // 16-byte pieces of a row: 32 features
   static constexpr int FT = W / 16;                // blocks of 16 features
   static constexpr bool Q_SHARED = KC * NT > 4;    // Q's fragments in shared memory
-  // merge: a warp's columns of sums, with 4 floats between 8 features' groups
-  static constexpr int GS = W / 8 + 4, RS = 8 * GS + 2;
+  static constexpr int RS = W + 4;                 // merge: floats of a warp's column of sums (16-byte stores hit all banks)
   static constexpr int TILE = kKeys * ROW;         // bytes of a tile's keys, and of its values
   static constexpr int SUMS = 8 * NT * RS * 4;     // a warp's, in the ring at the end
   static constexpr int RING = ST * 2 * TILE;
@@ -685,17 +690,15 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
   auto sums = [&](int w, int column, int at) {
     return reinterpret_cast<float*>(smem + w * C::SUMS) + column * C::RS + at;
   };
+  // (four features of a piece, 4 g .. + 3, of the two columns of each block)
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int f = 0; f < FT; ++f)
+    for (int c = 0; c < KC; ++c)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        // (codes are 2^-24, odd features 2^-20; groups of W / 8 features are GS floats apart)
-        const int feature = 32 * (f >> 1) + 4 * g + 2 * (f & 1) + (x >> 1);
-        *sums(warp, 8 * n + 2 * j + (x & 1), feature / (W / 8) * C::GS + feature % (W / 8)) =
-            o[n][f][x] * (x >> 1 ? 1048576.f : 16777216.f);
-      }
+      for (int r = 0; r < 2; ++r)
+        *reinterpret_cast<float4*>(sums(warp, 8 * n + 2 * j + r, 32 * c + 4 * g)) =
+            make_float4(o[n][2 * c][r], o[n][2 * c][2 + r], o[n][2 * c + 1][r], o[n][2 * c + 1][2 + r]);
   __syncthreads();
   // (a row to a warp: once per unit, so short code counts)
 #pragma unroll 1
@@ -728,18 +731,19 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
     }
 #pragma unroll 1
     for (int f = 2 * lane; f < W; f += 64) {
-      const int at = C::GS * (f / (W / 8)) + f % (W / 8);
-      float y0 = add, y1 = add;
+      float y0 = 0.f, y1 = 0.f;
 #pragma unroll
       for (int w = 0; w < C::WP; ++w) {
 #pragma unroll
         for (int z = 0; z < (FEW ? 8 : 1); z += 2) {
-          const float2 u = *reinterpret_cast<const float2*>(sums(w, z + r, at));
+          const float2 u = *reinterpret_cast<const float2*>(sums(w, z + r, f));
           y0 = fmaf(a[w], u.x, y0);
           y1 = fmaf(a[w], u.y, y1);
         }
       }
-      if (!live) y0 = y1 = 0.f;  // (what is not live may be anything)
+      // (codes are 2^-24, odd features' 2^-20; what is not live may be anything)
+      y0 = live ? fmaf(y0, 16777216.f, add) : 0.f;
+      y1 = live ? fmaf(y1, 1048576.f, add) : 0.f;
       if (!whole)
         *reinterpret_cast<float2*>(p.part_o + (first_part + out) * W + f) = make_float2(y0, y1);
       else if (f < p.d)
@@ -755,9 +759,9 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
 // unpacked once for all rows, and a warp's output takes a quarter of the registers.
 // The weights pass through shared memory, the references are the CTA's.
 // ---------------------------------------------------------------------------
-template <int W_, int NT_, int ST_, int CTAS_>
+template <int W_, int NT_, int SL_, int CTAS_>
 struct Q4BlockCfg {
-  static constexpr int W = W_, NT = NT_, ST = ST_, CTAS = CTAS_;
+  static constexpr int W = W_, NT = NT_, SL = SL_, CTAS = CTAS_;
   static constexpr int WP = 4, NR = 8 * NT;
   static constexpr bool SHARES = true;
   static_assert(WP * kTile == kKeys && W >= 128, "a tile of the splits' size, 32 features to a warp");
@@ -765,8 +769,8 @@ struct Q4BlockCfg {
   static constexpr int KC = W / 32;            // 16-byte pieces of a row: 32 features
   static constexpr int WC = KC / WP;           // a warp's
   static constexpr int FT = 2 * WC;            // blocks of 16 features of a warp
-  static constexpr int TILE = kKeys * ROW;     // bytes of a tile's keys, and of its values
-  static constexpr int OFF_P = ST * 2 * TILE;                    // uint2 [8 blocks of 16 keys][NT][32]
+  static constexpr int TILE = kKeys * ROW;     // bytes of a tile's keys, and of its values: a slot of the ring
+  static constexpr int OFF_P = SL * TILE;                        // uint2 [8 blocks of 16 keys][NT][32]
   static constexpr int OFF_Q = OFF_P + 8 * NT * 256;             // uint2 [2 KC][NT][32]
   static constexpr int OFF_KEYS = OFF_Q + 2 * KC * NT * 256;     // float4 [128], float [128]
   static constexpr int OFF_SCALES = OFF_KEYS + kKeys * 20;
@@ -774,7 +778,8 @@ struct Q4BlockCfg {
   static constexpr int OFF_STATS = OFF_ROWS + NR * 8;            // float2 [warp][NR]; maxima float [warp][NR]
   static constexpr int OFF_MASKS = OFF_STATS + WP * NR * 8;      // uint64 [NR][4]
   static constexpr int OFF_BAR = OFF_MASKS + NR * 32;
-  static constexpr int SMEM = OFF_BAR + ST * 8 + 16 + 1024;
+  static constexpr int SMEM = OFF_BAR + SL * 8 + 16 + 1024;
+  static_assert(SL >= 3, "the next keys while values wait");
   static_assert(SMEM <= 232448 && OFF_P % 1024 == 0, "shared memory");
 };
 
@@ -786,7 +791,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t ring = smem_u32(smem), bars = ring + C::OFF_BAR;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::ST * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::SL * 8);
   uint64_t(*masks)[4] = reinterpret_cast<uint64_t(*)[4]>(smem + C::OFF_MASKS);
   float2* factors = reinterpret_cast<float2*>(smem + C::OFF_ROWS);
   float2(*stats)[NR] = reinterpret_cast<float2(*)[NR]>(smem + C::OFF_STATS);
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(cons
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int g = lane >> 2, j = lane & 3;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::ST; ++s) mbar_init(bars + 8 * s, 1);
+    for (int s = 0; s < C::SL; ++s) mbar_init(bars + 8 * s, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -833,9 +838,15 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(cons
     }
   }
   const uint64_t bits = threadIdx.x < NR * 4 ? mask_word(p, it, static_cast<int>(threadIdx.x), out_row) : 0;
+  // item x of the ring: the keys (even) or values (odd) of tile x / 2, in slot x % SL
+  auto request = [&](int x, int slot) {
+    const int key = first + (x >> 1) * kKeys;
+    if (key >= stop) return;
+    mbar_arrive_expect_tx(bars + 8 * slot, load.bytes(key));
+    load.copy(ring + slot * C::TILE, bars + 8 * slot, key, x & 1);
+  };
   if (threadIdx.x == 0)
-    for (int s = 0; s < C::ST; ++s)
-      if (first + s * kKeys < stop) load(ring + s * 2 * C::TILE, bars + 8 * s, first + s * kKeys);
+    for (int s = 0; s < C::SL; ++s) request(s, s);
   uint2* q_frags = reinterpret_cast<uint2*>(smem + C::OFF_Q) + lane;
   if (warp < NT) {
     const float2 f = q_fragments<KC>(v, p.scale_log2, [&](int i, uint2 b) { q_frags[(i * NT + warp) * 32] = b; });
@@ -863,28 +874,27 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(cons
   const uint32_t k_at = (kTile * warp + row16) * C::ROW + 16 * (swizzle<W>(row16) ^ (lane >> 4));
   // of values a warp has pieces WC warp ..: two at a time, or one of two blocks of 16 keys
   const int v_row = C::WC == 1 ? lane : row16;
-  const uint32_t v_at = C::TILE + v_row * C::ROW + 16 * (swizzle<W>(v_row) ^ (C::WC * warp + (C::WC == 1 ? 0 : lane >> 4)));
+  const uint32_t v_at = v_row * C::ROW + 16 * (swizzle<W>(v_row) ^ (C::WC * warp + (C::WC == 1 ? 0 : lane >> 4)));
   float4* keys = reinterpret_cast<float4*>(smem + C::OFF_KEYS) + kTile * warp;
   float* keys_ofs = reinterpret_cast<float*>(smem + C::OFF_KEYS + kKeys * 16) + kTile * warp;
   uint2* p_frags = reinterpret_cast<uint2*>(smem + C::OFF_P) + lane;
 
   bool gave_up = false;
-  int stage = 0, i = 0;
+  int slot = 0, i = 0;      // the slot and parity of tile i's keys
   uint32_t parity = 0;
 #pragma unroll 1
   for (int tile0 = first; tile0 < stop; tile0 += kKeys, ++i) {
-    const uint32_t tile = ring + stage * 2 * C::TILE;
     const uint2 kv = words.get(i, tile0);
     const KeyFactors mine = key_factors(kv.x, kv.y);
     // the keys' factors by way of shared memory: lane's own key to the lanes of its row
     __syncwarp();  // (the tile before is read)
     keys[lane] = make_float4(mine.step, mine.lo, mine.v_log, mine.v_inv);
     keys_ofs[lane] = mine.v_ofs;
-    const bool ok = mbar_wait(bars + 8 * stage, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + 32 + stage);
+    bool ok = mbar_wait(bars + 8 * slot, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + 32 + slot);
     // ---- scores of the warp's keys
     __syncwarp();  // (ldmatrix wants the warp together; the factors are there)
     float s[MT][NT][4];
-    score_products<W, NT>(tile + k_at, s, (rows_here + 7) / 8, [&](int i, int n) { return q_frags[(i * NT + n) * 32]; });
+    score_products<W, NT>(ring + slot * C::TILE + k_at, s, (rows_here + 7) / 8, [&](int i, int n) { return q_frags[(i * NT + n) * 32]; });
     float v_inv[MT][2], v_ofs[MT][2];
     const int key0 = tile0 + kTile * warp;
     const bool masked = key0 + kTile > min(it.n, stop);
@@ -928,12 +938,20 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(cons
           top = fmax3(top, s[m][n][2 * h] - ref[n][0], s[m][n][2 * h + 1] - ref[n][1]);
         }
       }
-    // (behind this every warp is done with the tile before: its stage and the weights'
-    // buffer are free)
+    // (behind this every warp is done with these keys and the values before: their slots
+    // and the weights' buffer are free)
     const bool move = __syncthreads_or(top > kLimit);
-    const int before = stage == 0 ? C::ST - 1 : stage - 1;
-    if (threadIdx.x == 0 && tile0 > first && tile0 + (C::ST - 1) * kKeys < stop)
-      load(ring + before * 2 * C::TILE, bars + 8 * before, tile0 + (C::ST - 1) * kKeys);
+    if (threadIdx.x == 0) {
+      if (i > 0) request(2 * i - 1 + C::SL, slot == 0 ? C::SL - 1 : slot - 1);
+      request(2 * i + C::SL, slot);
+    }
+    auto advance = [&]() {
+      if (++slot == C::SL) {
+        slot = 0;
+        parity ^= 1;
+      }
+    };
+    advance();
     if (move) {
       // references up to this tile's maxima, what was summed down by as much
 #pragma unroll
@@ -991,6 +1009,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(cons
         p_frags[((MT * warp + m) * NT + n) * 32] = make_uint2(pt[0], pt[1]);
       }
     }
+    ok = mbar_wait(bars + 8 * slot, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + 32 + slot) && ok;
     gave_up = __syncthreads_or(!ok);  // the weights are there
     if (gave_up) break;
     // ---- o += V^T P^T of the warp's features, 16 keys at a time
@@ -1015,21 +1034,21 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(cons
 #pragma unroll
     for (int k = 0; k < kKeys / 16; k += C::WC == 1 ? 2 : 1) {
       uint32_t y[4];
-      ld_columns16(tile + v_at + 16 * k * C::ROW, y);
+      ld_columns16(ring + slot * C::TILE + v_at + 16 * k * C::ROW, y);
       weights(k);
       products(0, y[0], y[1]);
       if constexpr (C::WC == 1) weights(k + 1);
       products(C::WC == 1 ? 0 : 1, y[2], y[3]);
     }
-    if (++stage == C::ST) {
-      stage = 0;
-      parity ^= 1;
-    }
+    advance();
   }
   if (gave_up && threadIdx.x == 0) {
     // the copies in flight must land before the CTA exits (each wait is bounded)
     volatile int never = 0;
-    for (int s = 0; s < C::ST; ++s) mbar_wait(bars + 8 * s, parity ^ (s < stage ? 1 : 0), &never, p.status, 0);
+    for (int s = 0; s < C::SL; ++s) {
+      mbar_wait(bars + 8 * s, 0, &never, p.status, 0);
+      mbar_wait(bars + 8 * s, 1, &never, p.status, 0);
+    }
   }
 
   // ---- the warps' sums together
@@ -1112,13 +1131,13 @@ void with_config(int d, int R, F&& f) {
     else if (R == 2) f(Q4Cfg<128, 2, 3, 4>{});
     else if (R <= 8) f(Q4Cfg<128, 8, 2, 4>{});
     else if (R <= 16) f(Q4Cfg<128, 16, 3, 3>{});
-    else f(Q4BlockCfg<128, 4, 3, 2>{});
+    else f(Q4BlockCfg<128, 4, 4, 2>{});
   } else {
     if (R == 1) f(Q4Cfg<256, 1, 2, 3>{});
     else if (R == 2) f(Q4Cfg<256, 2, 2, 3>{});
     else if (R <= 8) f(Q4Cfg<256, 8, 2, 3>{});
-    else if (R <= 16) f(Q4BlockCfg<256, 2, 2, 2>{});
-    else f(Q4BlockCfg<256, 4, 2, 2>{});
+    else if (R <= 16) f(Q4BlockCfg<256, 2, 3, 3>{});
+    else f(Q4BlockCfg<256, 2, 3, 3>{});
   }
 }
 

@@ -14,6 +14,7 @@ order.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -621,15 +622,58 @@ def mha_cache_read_q4(k_cache, v_cache, k_scale, v_scale, lens, k=None, v=None, 
                        v, stream)
 
 
-def _rows_call(fn, ws_fn, q, cache_shape, tensors, ptrs, lens, extra, out, scale, workspace,
-               stream, return_lse, lse, ws_args, lse_shape):
-    """What the steps of a few rows have in common: checks, allocation, call."""
-    B, Lk, H_kv, d = cache_shape
+@functools.lru_cache(maxsize=4096)
+def _need(name, *sizes):
+    """A workspace's bytes by its entry's name and sizes (a small step costs as much on
+    the host as on the GPU, and looking this up less than asking)."""
+    return getattr(lib(), name)(*sizes)
+
+
+_CODES = {0: (_BF16, None), 1: (_F8, _U8), 2: (_U8, _BF16)}  # dtypes of rows and scales by mha_cache_format
+
+
+def _step(fn, fmt, q, k_cache, v_cache, k_scale, v_scale, lens_name, lens, tree, out, scale,
+          workspace, stream, return_lse, lse):
+    """A step of a few rows over a cache of format ``fmt``: checks, allocation, call.
+    ``tree``: None for a decode step (q [B, H, d]), else (draft_lens, tree_mask)."""
     q_shape = q.shape
-    if q_shape[0] != B or q_shape[-1] != d or H_kv == 0 or q_shape[-2] % H_kv != 0:
-        raise ValueError(f"cache {tuple(cache_shape)} does not match q {tuple(q_shape)}")
+    if fmt:
+        shape = B, Lk, H_kv, d = _cache_shape(k_cache, v_cache, k_scale, v_scale, fmt == 2)
+    else:
+        shape = k_cache.shape
+        if len(shape) != 4 or v_cache.shape != shape:
+            raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} "
+                             "must be [B, Lk, H_kv, d] alike")
+        B, Lk, H_kv, d = shape
+    H = q_shape[-2]
+    extra_tensors = ()
+    if tree is None:
+        extra, sizes, lse_shape = (), (B, H, H_kv, Lk, d), (B, H)
+    else:
+        extra_tensors, extra = _tree_mask(q_shape, *tree)
+        T = q_shape[1]
+        sizes, lse_shape = (B, T, H, H_kv, Lk, d), (B, H, T)
+    if q_shape[0] != B or q_shape[-1] != d or H_kv == 0 or H % H_kv != 0:
+        raise ValueError(f"cache {tuple(shape)} does not match q {tuple(q_shape)}")
+    if lens.shape != (B,):
+        raise ValueError(f"{lens_name} must be [B]")
     index = q.get_device()
-    _check(index, tensors)
+    codes, pairs = _CODES[fmt]
+    # (a small step costs as much on the host as on the GPU: the words are in _check)
+    if (index < 0 or q.dtype is not _BF16 or k_cache.dtype is not codes or v_cache.dtype is not codes
+            or lens.dtype is not _I32 or k_cache.get_device() != index or v_cache.get_device() != index
+            or lens.get_device() != index
+            or not (q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                    and lens.is_contiguous())
+            or (fmt and (k_scale.dtype is not pairs or v_scale.dtype is not pairs
+                         or k_scale.get_device() != index or v_scale.get_device() != index
+                         or not (k_scale.is_contiguous() and v_scale.is_contiguous())))):
+        _check(index, ((q, "q", _BF16),
+                       *(_cache_tensors(k_cache, v_cache, k_scale, v_scale, fmt == 2) if fmt else
+                         ((k_cache, "k_cache", _BF16), (v_cache, "v_cache", _BF16))),
+                       (lens, lens_name, _I32)))
+    if extra_tensors:
+        _check(index, extra_tensors)
     made = []
     if out is None:
         out = torch.empty_like(q)
@@ -643,19 +687,22 @@ def _rows_call(fn, ws_fn, q, cache_shape, tensors, ptrs, lens, extra, out, scale
             raise ValueError(f"lse must be {lse_shape}")
         _check(index, ((lse, "lse", _F32),))
     elif return_lse:
-        lse = torch.empty(lse_shape, dtype=_F32, device=q.device)
+        lse = q.new_empty(lse_shape, dtype=_F32)
         made.append(lse)
+    room = (None, 0)
     if workspace is None:
-        need = ws_fn(*ws_args)
+        need = _need(fn.__name__ + "_workspace_bytes", *sizes)
         if need:
-            workspace = torch.empty(need, dtype=_U8, device=q.device)
+            workspace = q.new_empty(need, dtype=_U8)
             made.append(workspace)
+            room = (workspace.data_ptr(), need)
     else:
         _check(index, ((workspace, "workspace", _U8),))
+        room = (workspace.data_ptr(), workspace.numel())
+    ptrs = (k_scale.data_ptr(), v_scale.data_ptr()) if fmt else ()
     _call_on(index, stream, made, fn,
-             (q.data_ptr(), *ptrs, out.data_ptr(), lse.data_ptr() if return_lse else None,
-              *ws_args, lens.data_ptr(), *extra, scale,
-              *((None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel()))))
+             (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *ptrs, out.data_ptr(),
+              lse.data_ptr() if return_lse else None, *sizes, lens.data_ptr(), *extra, scale, *room))
     return (out, lse) if return_lse else out
 
 
@@ -679,19 +726,10 @@ def decode_tree_q4_workspace_bytes(B, T, H, H_kv, Lk, d_k) -> int:
     return int(lib().mha_decode_tree_q4_workspace_bytes(B, T, H, H_kv, Lk, d_k))
 
 
-def _decode(fn, ws_fn, q4, q, k_cache, v_cache, k_scale, v_scale, cache_lens, out, scale, workspace,
-            stream, return_lse, lse):
-    if q.dim() not in (3, 4) or (q.dim() == 4 and q.shape[1] != 1):
+def _one_row(q):
+    dims = q.dim()
+    if dims != 3 and (dims != 4 or q.shape[1] != 1):
         raise ValueError("q must be [B, H, d] or [B, 1, H, d]")
-    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale, q4)
-    B, Lk, H_kv, d = shape
-    H = q.shape[-2]
-    return _rows_call(
-        fn, ws_fn, q, shape,
-        ((q, "q", _BF16), *_cache_tensors(k_cache, v_cache, k_scale, v_scale, q4),
-         _lens(cache_lens, "cache_lens", B)),
-        (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()),
-        cache_lens, (), out, scale, workspace, stream, return_lse, lse, (B, H, H_kv, Lk, d), (B, H))
 
 
 def mha_decode_f8(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, scale: float = 0.0,
@@ -702,26 +740,31 @@ def mha_decode_f8(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, s
     query head h reads key head h // (H / H_kv).  Returns out (q's shape), or
     (out, lse) with ``return_lse`` (lse [B, H]).  ``workspace`` (uint8 CUDA
     tensor) is allocated when not given."""
+    _one_row(q)
     h = lib()
-    return _decode(h.mha_decode_f8, h.mha_decode_f8_workspace_bytes, False, q, k_cache, v_cache,
-                   k_scale, v_scale, cache_lens, out, scale, workspace, stream, return_lse, lse)
+    return _step(h.mha_decode_f8, 1, q, k_cache, v_cache, k_scale,
+                 v_scale, "cache_lens", cache_lens, None, out, scale, workspace, stream, return_lse, lse)
 
 
 def mha_decode_q4(q, k_cache, v_cache, k_scale, v_scale, cache_lens, out=None, scale: float = 0.0,
                   workspace=None, stream=None, return_lse: bool = False, lse=None):
     """mha_decode_f8 over a 4-bit cache: k_cache, v_cache [B, Lk, H_kv, d / 2],
     scales [B, H_kv, Lk, 2] (mha_cache_write_q4's format)."""
+    _one_row(q)
     h = lib()
-    return _decode(h.mha_decode_q4, h.mha_decode_q4_workspace_bytes, True, q, k_cache, v_cache,
-                   k_scale, v_scale, cache_lens, out, scale, workspace, stream, return_lse, lse)
+    return _step(h.mha_decode_q4, 2, q, k_cache, v_cache, k_scale,
+                 v_scale, "cache_lens", cache_lens, None, out, scale, workspace, stream, return_lse, lse)
 
 
-def _tree_mask(q, draft_lens, tree_mask):
-    """Checks the shapes of a tree step's q, lengths and mask; returns the mask's
-    and lengths' triples and pointers."""
+def _rows(q):
     if q.dim() != 4:
         raise ValueError("q must be [B, T, H, d]")
-    B, T = q.shape[0], q.shape[1]
+
+
+def _tree_mask(q_shape, draft_lens, tree_mask):
+    """Checks the shapes of a tree step's lengths and mask; returns their triples and
+    pointers."""
+    B, T = q_shape[0], q_shape[1]
     tensors, drafts, bits = (), None, None
     if draft_lens is not None:
         tensors = (_lens(draft_lens, "draft_lens", B),)
@@ -745,53 +788,33 @@ def mha_decode_tree(q, k_cache, v_cache, prefix_lens, draft_lens=None, tree_mask
     t sees drafted token j where bit j is set (None: a chain, j <= t).
     ``draft_lens`` [B]: drafted tokens per sequence (None: T); rows past them
     get output 0.  Returns out [B, T, H, d], or (out, lse [B, H, T])."""
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} "
-                         "must be [B, Lk, H_kv, d] alike")
-    tree, extra = _tree_mask(q, draft_lens, tree_mask)
-    B, T, H, _ = q.shape
+    _rows(q)
     h = lib()
-    return _rows_call(
-        h.mha_decode_tree, h.mha_decode_tree_workspace_bytes, q, shape,
-        ((q, "q", _BF16), (k_cache, "k_cache", _BF16), (v_cache, "v_cache", _BF16),
-         _lens(prefix_lens, "prefix_lens", B), *tree),
-        (k_cache.data_ptr(), v_cache.data_ptr()), prefix_lens, extra, out, scale, workspace,
-        stream, return_lse, lse, (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
-
-
-def _decode_tree_scaled(fn, ws_fn, q4, q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens,
-                        tree_mask, out, scale, workspace, stream, return_lse, lse):
-    shape = _cache_shape(k_cache, v_cache, k_scale, v_scale, q4)
-    tree, extra = _tree_mask(q, draft_lens, tree_mask)
-    B, T, H, _ = q.shape
-    return _rows_call(
-        fn, ws_fn, q, shape,
-        ((q, "q", _BF16), *_cache_tensors(k_cache, v_cache, k_scale, v_scale, q4),
-         _lens(prefix_lens, "prefix_lens", B), *tree),
-        (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()),
-        prefix_lens, extra, out, scale, workspace, stream, return_lse, lse,
-        (B, T, H, shape[2], shape[1], shape[3]), (B, H, T))
+    return _step(h.mha_decode_tree, 0, q, k_cache, v_cache, None, None,
+                 "prefix_lens", prefix_lens, (draft_lens, tree_mask), out, scale, workspace, stream,
+                 return_lse, lse)
 
 
 def mha_decode_tree_f8(q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens=None,
                        tree_mask=None, out=None, scale: float = 0.0, workspace=None, stream=None,
                        return_lse: bool = False, lse=None):
     """mha_decode_tree over an 8-bit cache (mha_cache_write_f8's format)."""
+    _rows(q)
     h = lib()
-    return _decode_tree_scaled(h.mha_decode_tree_f8, h.mha_decode_tree_f8_workspace_bytes, False, q,
-                               k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens,
-                               tree_mask, out, scale, workspace, stream, return_lse, lse)
+    return _step(h.mha_decode_tree_f8, 1, q, k_cache, v_cache,
+                 k_scale, v_scale, "prefix_lens", prefix_lens, (draft_lens, tree_mask), out, scale,
+                 workspace, stream, return_lse, lse)
 
 
 def mha_decode_tree_q4(q, k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens=None,
                        tree_mask=None, out=None, scale: float = 0.0, workspace=None, stream=None,
                        return_lse: bool = False, lse=None):
     """mha_decode_tree over a 4-bit cache (mha_cache_write_q4's format)."""
+    _rows(q)
     h = lib()
-    return _decode_tree_scaled(h.mha_decode_tree_q4, h.mha_decode_tree_q4_workspace_bytes, True, q,
-                               k_cache, v_cache, k_scale, v_scale, prefix_lens, draft_lens,
-                               tree_mask, out, scale, workspace, stream, return_lse, lse)
+    return _step(h.mha_decode_tree_q4, 2, q, k_cache, v_cache,
+                 k_scale, v_scale, "prefix_lens", prefix_lens, (draft_lens, tree_mask), out, scale,
+                 workspace, stream, return_lse, lse)
 
 
 # ---------------------------------------------------------------------------
@@ -801,22 +824,26 @@ _FORMATS = {_BF16: 0, _F8: 1, _U8: 2}  # mha_cache_format by the cache's dtype
 
 
 def _moved_cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks a cache of any format; returns (format, (B, Lk, H, d), tensors)."""
-    fmt = _FORMATS.get(k_cache.dtype)
+    """Checks a cache of any format; returns (format, (B, Lk, H, d), pointers, device)."""
+    dtype = k_cache.dtype
+    fmt = _FORMATS.get(dtype)
     if fmt is None:
-        raise TypeError(f"k_cache must be {_BF16}, {_F8} or {_U8} (4 bits), got {k_cache.dtype}")
+        raise TypeError(f"k_cache must be {_BF16}, {_F8} or {_U8} (4 bits), got {dtype}")
+    index = k_cache.get_device()
     if fmt:
         if k_scale is None or v_scale is None:
             raise ValueError("an 8-bit or a 4-bit cache needs k_scale and v_scale")
-        return fmt, _cache_shape(k_cache, v_cache, k_scale, v_scale, fmt == 2), \
-            _cache_tensors(k_cache, v_cache, k_scale, v_scale, fmt == 2)
+        shape = _cache_shape(k_cache, v_cache, k_scale, v_scale, fmt == 2)
+        _check(index, _cache_tensors(k_cache, v_cache, k_scale, v_scale, fmt == 2))
+        return fmt, shape, (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()), index
     if k_scale is not None or v_scale is not None:
         raise ValueError("a bf16 cache has no scales")
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} "
-                         "must be [B, Lk, H, d_k] alike")
-    return fmt, shape, ((k_cache, "k_cache", _BF16), (v_cache, "v_cache", _BF16))
+                         "must be [B, Lk, H_kv, d] alike")
+    _check(index, ((k_cache, "k_cache", _BF16), (v_cache, "v_cache", _BF16)))
+    return fmt, shape, (k_cache.data_ptr(), v_cache.data_ptr(), None, None), index
 
 
 def mha_cache_fork(k_cache, v_cache, parent, lens, first=None, k_scale=None, v_scale=None, stream=None):
@@ -825,15 +852,13 @@ def mha_cache_fork(k_cache, v_cache, parent, lens, first=None, k_scale=None, v_s
     None: 0), in keys, values and scales.  The cache is bf16 [B, Lk, H, d], 8-bit
     (float8_e4m3fn) or 4-bit (uint8) with its scales; parent, lens and first are
     int32 [B].  A parent of b itself, or outside [0, B), leaves b as it is."""
-    fmt, (B, Lk, H, d), tensors = _moved_cache(k_cache, v_cache, k_scale, v_scale)
-    index = k_cache.get_device()
-    _check(index, (*tensors, _lens(parent, "parent", B), _lens(lens, "lens", B)))
+    fmt, (B, Lk, H, d), ptrs, index = _moved_cache(k_cache, v_cache, k_scale, v_scale)
+    _check(index, (_lens(parent, "parent", B), _lens(lens, "lens", B)))
     if first is not None:
         _check(index, (_lens(first, "first", B),))
     _call_on(index, stream, (), lib().mha_cache_fork,
-             (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if fmt else None,
-              v_scale.data_ptr() if fmt else None, fmt, B, H, Lk, d, parent.data_ptr(),
-              first.data_ptr() if first is not None else None, lens.data_ptr()))
+             (*ptrs, fmt, B, H, Lk, d, parent.data_ptr(), first.data_ptr() if first is not None else None,
+              lens.data_ptr()))
 
 
 def mha_cache_compact(k_cache, v_cache, prefix_lens, path, path_lens=None, k_scale=None, v_scale=None,
@@ -843,17 +868,15 @@ def mha_cache_compact(k_cache, v_cache, prefix_lens, path, path_lens=None, k_sca
     before the call, i < path_lens[b] (None: all T), in keys, values and scales.
     path int32 [B, T] holds numbers of drafted tokens (one outside [0, T) leaves
     row i as it is); caches as mha_cache_fork."""
-    fmt, (B, Lk, H, d), tensors = _moved_cache(k_cache, v_cache, k_scale, v_scale)
-    if path.dim() != 2 or path.shape[0] != B:
+    path_shape = path.shape
+    if len(path_shape) != 2 or path_shape[0] != k_cache.shape[0]:
         raise ValueError("path must be [B, T]")
-    index = k_cache.get_device()
-    _check(index, (*tensors, _lens(prefix_lens, "prefix_lens", B), (path, "path", _I32)))
+    fmt, (B, Lk, H, d), ptrs, index = _moved_cache(k_cache, v_cache, k_scale, v_scale)
+    _check(index, (_lens(prefix_lens, "prefix_lens", B), (path, "path", _I32)))
     if path_lens is not None:
         _check(index, (_lens(path_lens, "path_lens", B),))
     _call_on(index, stream, (), lib().mha_cache_compact,
-             (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if fmt else None,
-              v_scale.data_ptr() if fmt else None, fmt, B, path.shape[1], H, Lk, d,
-              prefix_lens.data_ptr(), path.data_ptr(),
+             (*ptrs, fmt, B, path_shape[1], H, Lk, d, prefix_lens.data_ptr(), path.data_ptr(),
               path_lens.data_ptr() if path_lens is not None else None))
 
 

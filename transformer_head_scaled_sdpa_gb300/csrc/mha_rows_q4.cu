@@ -144,7 +144,7 @@ __device__ __forceinline__ void codes_of(uint32_t (&a)[4], uint32_t w0, uint32_t
 // same sums, so there are four or more sums to take turns: two blocks of keys, and of one
 // block of columns the even and odd steps apart.)
 template <int W, int NQ, typename F>
-__device__ __forceinline__ void score_products(uint32_t at, float (&s)[2][NQ][4], int nq, F&& frag) {
+__device__ __forceinline__ void score_products(uint32_t at, float (&s)[2][NQ][4], F&& frag) {
   constexpr int PARTS = NQ == 1 ? 2 : 1;
   float part[2][4];
 #pragma unroll
@@ -160,7 +160,6 @@ __device__ __forceinline__ void score_products(uint32_t at, float (&s)[2][NQ][4]
         codes_of(a[m], z & 1 ? w[m][z & 2] >> 8 : w[m][z & 2], z & 1 ? w[m][(z & 2) + 1] >> 8 : w[m][(z & 2) + 1], true);
 #pragma unroll
       for (int x = 0; x < NQ; ++x) {
-        if (x >= nq) break;
         const uint2 b = frag(2 * c + z, x);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
@@ -333,7 +332,7 @@ template <int W_, int ROWS_, int ST_, int CTAS_>
 struct Q4Cfg {
   static constexpr int W = W_, NR = ROWS_, ST = ST_, CTAS = CTAS_;
   static constexpr int WP = 4;
-  static constexpr bool FEW = NR <= 2, SHARES = false;
+  static constexpr bool FEW = NR <= 2;
   static constexpr int NT = FEW ? 1 : NR / 8;      // blocks of 8 columns
   static constexpr int ROW = W / 2;                // bytes of a tile's row
   static constexpr int KC = W / 32;                // 16-byte pieces of a row: 32 features
@@ -486,7 +485,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
     if (key0 < stop) {
       // ---- scores: s[m][n] = keys g, 8 + g of block m of 16, columns 2 j, 2 j + 1 of block n
       float s[MT][NT][4];
-      score_products<W, NT>(tile + at, s, NT, [&](int i, int n) {
+      score_products<W, NT>(tile + at, s, [&](int i, int n) {
         if constexpr (C::Q_SHARED) return q_shared[(i * NT + n) * 32];
         else return q[i * NT + n];
       });
@@ -658,6 +657,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
       parity ^= 1;
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // (gave up: offsets and steps, too, are in flight)
   __syncthreads();
   if (*abort_flag != 0 && threadIdx.x == 0) {
     // gave up: the copies in flight must land before the CTA exits (each wait is bounded)
@@ -753,370 +753,6 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
   }
 }
 
-// ---------------------------------------------------------------------------
-// More rows: a CTA's warps share a tile of 128 keys.  Each has 32 of the keys for the
-// scores, and a quarter of the features, over all 128 keys, for the output: the codes are
-// unpacked once for all rows, and a warp's output takes a quarter of the registers.
-// The weights pass through shared memory, the references are the CTA's.
-// ---------------------------------------------------------------------------
-template <int W_, int NT_, int SL_, int CTAS_>
-struct Q4BlockCfg {
-  static constexpr int W = W_, NT = NT_, SL = SL_, CTAS = CTAS_;
-  static constexpr int WP = 4, NR = 8 * NT;
-  static constexpr bool SHARES = true;
-  static_assert(WP * kTile == kKeys && W >= 128, "a tile of the splits' size, 32 features to a warp");
-  static constexpr int ROW = W / 2;            // bytes of a tile's row
-  static constexpr int KC = W / 32;            // 16-byte pieces of a row: 32 features
-  static constexpr int WC = KC / WP;           // a warp's
-  static constexpr int FT = 2 * WC;            // blocks of 16 features of a warp
-  static constexpr int TILE = kKeys * ROW;     // bytes of a tile's keys, and of its values: a slot of the ring
-  static constexpr int OFF_P = SL * TILE;                        // uint2 [8 blocks of 16 keys][NT][32]
-  static constexpr int OFF_Q = OFF_P + 8 * NT * 256;             // uint2 [2 KC][NT][32]
-  static constexpr int OFF_KEYS = OFF_Q + 2 * KC * NT * 256;     // float4 [128], float [128]
-  static constexpr int OFF_SCALES = OFF_KEYS + kKeys * 20;
-  static constexpr int OFF_ROWS = OFF_SCALES + Scales::BYTES;         // float2 [NR]: the rows' factors
-  static constexpr int OFF_STATS = OFF_ROWS + NR * 8;            // float2 [warp][NR]; maxima float [warp][NR]
-  static constexpr int OFF_MASKS = OFF_STATS + WP * NR * 8;      // uint64 [NR][4]
-  static constexpr int OFF_BAR = OFF_MASKS + NR * 32;
-  static constexpr int SMEM = OFF_BAR + SL * 8 + 16 + 1024;
-  static_assert(SL >= 3, "the next keys while values wait");
-  static_assert(SMEM <= 232448 && OFF_P % 1024 == 0, "shared memory");
-};
-
-template <class C>
-__global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_block_kernel(const __grid_constant__ RowsParams p) {
-  constexpr int W = C::W, NT = C::NT, KC = C::KC, FT = C::FT, NR = C::NR, WP = C::WP;
-  constexpr int MT = kTile / 16;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  const uint32_t ring = smem_u32(smem), bars = ring + C::OFF_BAR;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::SL * 8);
-  uint64_t(*masks)[4] = reinterpret_cast<uint64_t(*)[4]>(smem + C::OFF_MASKS);
-  float2* factors = reinterpret_cast<float2*>(smem + C::OFF_ROWS);
-  float2(*stats)[NR] = reinterpret_cast<float2(*)[NR]>(smem + C::OFF_STATS);
-  float(*maxima)[NR] = reinterpret_cast<float(*)[NR]>(smem + C::OFF_STATS);
-  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int g = lane >> 2, j = lane & 3;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::SL; ++s) mbar_init(bars + 8 * s, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  griddep_wait();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int n_rows = p.T * p.G;
-  Unit it;
-  if (!this_unit(p, (n_rows + NR - 1) / NR, kSms * C::CTAS, lane, &it)) return;
-  const int stop = min(it.t1 * kKeys, it.end), first = it.t0 * kKeys;
-  const int rows_here = min(NR, n_rows - it.rb * NR);
-  const Loader<W> load{p, it, stop};
-  auto out_row = [&](int r, int* t) {
-    const int gr = it.rb * NR + r;
-    *t = -1;
-    if (gr >= n_rows) return -1;
-    *t = p.G == 1 ? gr : gr / p.G;
-    return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
-  };
-  // plain loads before the ring's, as above: offsets and steps ...
-  const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
-  const Scales words{ring + C::OFF_SCALES + 8 * threadIdx.x, reinterpret_cast<const uint32_t*>(p.k_scale) + scales,
-                     reinterpret_cast<const uint32_t*>(p.v_scale) + scales, static_cast<int>(threadIdx.x), stop};
-  words.start(first);
-  // ... Q, a warp's block of 8 rows, and the rows' masks
-  static_assert(NT <= WP && NR * 4 <= 32 * WP, "a block to a warp, a word to a thread");
-  uint4 v[KC];
-  {
-    int t;
-    const int out = warp < NT ? out_row(8 * warp + g, &t) : -1;
-    const bool live = out >= 0 && t < it.live;
-    const uint16_t* src = static_cast<const uint16_t*>(p.q) + static_cast<long long>(max(out, 0)) * p.d;
-#pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      v[c] = make_uint4(0, 0, 0, 0);
-      if (live && 32 * c < p.d) v[c] = __ldg(reinterpret_cast<const uint4*>(src + 32 * c + 8 * j));
-    }
-  }
-  const uint64_t bits = threadIdx.x < NR * 4 ? mask_word(p, it, static_cast<int>(threadIdx.x), out_row) : 0;
-  // item x of the ring: the keys (even) or values (odd) of tile x / 2, in slot x % SL
-  auto request = [&](int x, int slot) {
-    const int key = first + (x >> 1) * kKeys;
-    if (key >= stop) return;
-    mbar_arrive_expect_tx(bars + 8 * slot, load.bytes(key));
-    load.copy(ring + slot * C::TILE, bars + 8 * slot, key, x & 1);
-  };
-  if (threadIdx.x == 0)
-    for (int s = 0; s < C::SL; ++s) request(s, s);
-  uint2* q_frags = reinterpret_cast<uint2*>(smem + C::OFF_Q) + lane;
-  if (warp < NT) {
-    const float2 f = q_fragments<KC>(v, p.scale_log2, [&](int i, uint2 b) { q_frags[(i * NT + warp) * 32] = b; });
-    if (j == 0) factors[8 * warp + g] = f;
-  }
-  if (threadIdx.x < NR * 4) masks[threadIdx.x >> 2][threadIdx.x & 3] = bits;
-  __syncthreads();  // (the barriers are set up, too)
-
-  float o[NT][FT][4];
-  float ref[NT][2], l[NT][2], ofs[NT][2];  // references less kLift; sums over the warp's keys
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int f = 0; f < FT; ++f)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[n][f][x] = 0.f;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      ref[n][r] = kNoRef;
-      l[n][r] = 0.f;
-      ofs[n][r] = 0.f;
-    }
-  }
-  const int row16 = lane & 15;
-  const uint32_t k_at = (kTile * warp + row16) * C::ROW + 16 * (swizzle<W>(row16) ^ (lane >> 4));
-  // of values a warp has pieces WC warp ..: two at a time, or one of two blocks of 16 keys
-  const int v_row = C::WC == 1 ? lane : row16;
-  const uint32_t v_at = v_row * C::ROW + 16 * (swizzle<W>(v_row) ^ (C::WC * warp + (C::WC == 1 ? 0 : lane >> 4)));
-  float4* keys = reinterpret_cast<float4*>(smem + C::OFF_KEYS) + kTile * warp;
-  float* keys_ofs = reinterpret_cast<float*>(smem + C::OFF_KEYS + kKeys * 16) + kTile * warp;
-  uint2* p_frags = reinterpret_cast<uint2*>(smem + C::OFF_P) + lane;
-
-  bool gave_up = false;
-  int slot = 0, i = 0;      // the slot and parity of tile i's keys
-  uint32_t parity = 0;
-#pragma unroll 1
-  for (int tile0 = first; tile0 < stop; tile0 += kKeys, ++i) {
-    const uint2 kv = words.get(i, tile0);
-    const KeyFactors mine = key_factors(kv.x, kv.y);
-    // the keys' factors by way of shared memory: lane's own key to the lanes of its row
-    __syncwarp();  // (the tile before is read)
-    keys[lane] = make_float4(mine.step, mine.lo, mine.v_log, mine.v_inv);
-    keys_ofs[lane] = mine.v_ofs;
-    bool ok = mbar_wait(bars + 8 * slot, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + 32 + slot);
-    // ---- scores of the warp's keys
-    __syncwarp();  // (ldmatrix wants the warp together; the factors are there)
-    float s[MT][NT][4];
-    score_products<W, NT>(ring + slot * C::TILE + k_at, s, (rows_here + 7) / 8, [&](int i, int n) { return q_frags[(i * NT + n) * 32]; });
-    float v_inv[MT][2], v_ofs[MT][2];
-    const int key0 = tile0 + kTile * warp;
-    const bool masked = key0 + kTile > min(it.n, stop);
-    float top = -INFINITY;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 kf = keys[16 * m + 8 * h + g];
-        v_inv[m][h] = kf.w;
-        v_ofs[m][h] = keys_ofs[16 * m + 8 * h + g];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (8 * n >= rows_here) break;
-          const float4 f = *reinterpret_cast<const float4*>(factors + 8 * n + 2 * j);
-          float* y = s[m][n] + 2 * h;
-          float t0, t1, u0, u1;
-          mul2(t0, t1, y[0], y[1], f.x, f.z);
-          fma2(u0, u1, f.y, f.w, kf.y, kf.y, kf.z, kf.z);
-          fma2(y[0], y[1], t0, t1, kf.x, kf.x, u0, u1);
-        }
-        if (masked) {
-          const int key = key0 + 16 * m + 8 * h + g, off = key - it.n;
-          bool any = false;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              bool sees = key < stop;
-              if (sees && off >= 0)  // (off < 256: the drafted tokens end there)
-                sees = (masks[8 * n + 2 * j + r][off >> 6] >> (off & 63)) & 1;
-              if (!sees) s[m][n][2 * h + r] = -INFINITY;
-              any = any || sees;
-            }
-          // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
-          if (!any) v_inv[m][h] = v_ofs[m][h] = 0.f;
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (8 * n >= rows_here) break;
-          top = fmax3(top, s[m][n][2 * h] - ref[n][0], s[m][n][2 * h + 1] - ref[n][1]);
-        }
-      }
-    // (behind this every warp is done with these keys and the values before: their slots
-    // and the weights' buffer are free)
-    const bool move = __syncthreads_or(top > kLimit);
-    if (threadIdx.x == 0) {
-      if (i > 0) request(2 * i - 1 + C::SL, slot == 0 ? C::SL - 1 : slot - 1);
-      request(2 * i + C::SL, slot);
-    }
-    auto advance = [&]() {
-      if (++slot == C::SL) {
-        slot = 0;
-        parity ^= 1;
-      }
-    };
-    advance();
-    if (move) {
-      // references up to this tile's maxima, what was summed down by as much
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (8 * n >= rows_here) break;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float m = fmaxf(s[0][n][r], s[0][n][2 + r]);
-#pragma unroll
-          for (int y = 1; y < MT; ++y) m = fmax3(m, s[y][n][r], s[y][n][2 + r]);
-#pragma unroll
-          for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-          if (g == 0) maxima[warp][8 * n + 2 * j + r] = m;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (8 * n >= rows_here) break;
-        float by[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = 8 * n + 2 * j + r;
-          float m = fmax3(maxima[0][row], maxima[1][row], fmaxf(maxima[2][row], maxima[3][row]));
-          m = fmaxf(ref[n][r], m - kLift);
-          by[r] = ex2_approx(ref[n][r] - m);
-          ref[n][r] = m;
-          l[n][r] *= by[r];
-          ofs[n][r] *= by[r];
-        }
-#pragma unroll
-        for (int f = 0; f < FT; ++f)
-#pragma unroll
-          for (int z = 0; z < 4; ++z) o[n][f][z] *= by[z & 1];
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (8 * n >= rows_here) break;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t pt[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float w0, w1;
-          add2(w0, w1, s[m][n][2 * h], s[m][n][2 * h + 1], -ref[n][0], -ref[n][1]);
-          w0 = ex2_approx(w0);
-          w1 = ex2_approx(w1);
-          fma2(l[n][0], l[n][1], w0, w1, v_inv[m][h], v_inv[m][h], l[n][0], l[n][1]);
-          const uint32_t w = pack_f16x2(w0, w1);
-          // (the offsets with the rounded weights, as in the kernel above)
-          fma2(ofs[n][0], ofs[n][1], half_lo(w), half_hi(w), v_ofs[m][h], v_ofs[m][h], ofs[n][0], ofs[n][1]);
-          pt[h] = transposed(w);
-        }
-        p_frags[((MT * warp + m) * NT + n) * 32] = make_uint2(pt[0], pt[1]);
-      }
-    }
-    ok = mbar_wait(bars + 8 * slot, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + 32 + slot) && ok;
-    gave_up = __syncthreads_or(!ok);  // the weights are there
-    if (gave_up) break;
-    // ---- o += V^T P^T of the warp's features, 16 keys at a time
-    uint2 w[NT];
-    auto weights = [&](int k) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (8 * n < rows_here) w[n] = p_frags[(k * NT + n) * 32];
-    };
-    auto products = [&](int c, uint32_t y0, uint32_t y1) {
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        uint32_t a[4];
-        codes_of(a, z ? y0 >> 8 : y0, z ? y1 >> 8 : y1, false);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (8 * n >= rows_here) break;
-          mma_f16(o[n][2 * c + z], a, w[n].x, w[n].y);
-        }
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < kKeys / 16; k += C::WC == 1 ? 2 : 1) {
-      uint32_t y[4];
-      ld_columns16(ring + slot * C::TILE + v_at + 16 * k * C::ROW, y);
-      weights(k);
-      products(0, y[0], y[1]);
-      if constexpr (C::WC == 1) weights(k + 1);
-      products(C::WC == 1 ? 0 : 1, y[2], y[3]);
-    }
-    advance();
-  }
-  if (gave_up && threadIdx.x == 0) {
-    // the copies in flight must land before the CTA exits (each wait is bounded)
-    volatile int never = 0;
-    for (int s = 0; s < C::SL; ++s) {
-      mbar_wait(bars + 8 * s, 0, &never, p.status, 0);
-      mbar_wait(bars + 8 * s, 1, &never, p.status, 0);
-    }
-  }
-
-  // ---- the warps' sums together
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-      for (int z = 4; z < 32; z <<= 1) {
-        l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], z);
-        ofs[n][r] += __shfl_xor_sync(0xffffffffu, ofs[n][r], z);
-      }
-    }
-  __syncthreads();  // (the maxima lie where the sums go)
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      if (g == 0) stats[warp][8 * n + 2 * j + r] = make_float2(l[n][r], ofs[n][r]);
-  __syncthreads();
-  const bool whole = it.splits == 1;
-  const long long first_part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (8 * n >= rows_here) break;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      int t;
-      const int row = 8 * n + 2 * j + r, out = out_row(row, &t);
-      if (out < 0) continue;
-      float L = 0.f, add = 0.f;
-#pragma unroll
-      for (int w = 0; w < WP; ++w) {
-        const float2 y = stats[w][row];
-        L += y.x;
-        add += y.y;
-      }
-      const bool live = t < it.live && ref[n][r] != kNoRef && !gave_up;
-      if (!live) L = 0.f;
-      if (warp == 0 && g == 0) {
-        if (!whole) {
-          p.part_m[first_part + out] = L == 0.f ? -INFINITY : ref[n][r];
-          p.part_l[first_part + out] = L;
-        } else if (p.lse) {
-          p.lse[(static_cast<long long>(it.b) * p.H + out % p.H) * p.T + t] =
-              L == 0.f ? -INFINITY : (ref[n][r] + __log2f(L)) * 0.69314718055994531f;
-        }
-      }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-      for (int c = 0; c < C::WC; ++c) {
-        const int f = 32 * (C::WC * warp + c) + 4 * g;  // four features
-        float y[4];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {  // (codes are 2^-24, odd features 2^-20)
-          y[2 * z] = live ? fmaf(o[n][2 * c + z][r], 16777216.f, add) : 0.f;
-          y[2 * z + 1] = live ? fmaf(o[n][2 * c + z][2 + r], 1048576.f, add) : 0.f;
-        }
-        if (!whole)
-          *reinterpret_cast<float4*>(p.part_o + (first_part + out) * W + f) = make_float4(y[0], y[1], y[2], y[3]);
-        else if (f < p.d)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + static_cast<long long>(out) * p.d + f) =
-              make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
-      }
-    }
-  }
-}
-
 // Calls f with the kernel's configuration for R rows per key head of d features.
 template <typename F>
 void with_config(int d, int R, F&& f) {
@@ -1124,27 +760,18 @@ void with_config(int d, int R, F&& f) {
     if (R == 1) f(Q4Cfg<64, 1, 4, 6>{});
     else if (R == 2) f(Q4Cfg<64, 2, 4, 6>{});
     else if (R <= 8) f(Q4Cfg<64, 8, 4, 4>{});
-    else if (R <= 16) f(Q4Cfg<64, 16, 4, 3>{});
-    else f(Q4Cfg<64, 32, 7, 2>{});
+    else f(Q4Cfg<64, 16, 4, 3>{});
   } else if (d <= 128) {
     if (R == 1) f(Q4Cfg<128, 1, 3, 4>{});
     else if (R == 2) f(Q4Cfg<128, 2, 3, 4>{});
     else if (R <= 8) f(Q4Cfg<128, 8, 2, 4>{});
-    else if (R <= 16) f(Q4Cfg<128, 16, 3, 3>{});
-    else f(Q4BlockCfg<128, 4, 4, 2>{});
+    else f(Q4Cfg<128, 16, 3, 3>{});
   } else {
     if (R == 1) f(Q4Cfg<256, 1, 2, 3>{});
     else if (R == 2) f(Q4Cfg<256, 2, 2, 3>{});
     else if (R <= 8) f(Q4Cfg<256, 8, 2, 3>{});
-    else if (R <= 16) f(Q4BlockCfg<256, 2, 3, 3>{});
-    else f(Q4BlockCfg<256, 2, 3, 3>{});
+    else f(Q4Cfg<256, 16, 3, 2>{});
   }
-}
-
-template <class C>
-constexpr auto kernel_of() {
-  if constexpr (C::SHARES) return rows_q4_block_kernel<C>;
-  else return rows_q4_kernel<C>;
 }
 
 template <class C>
@@ -1155,12 +782,12 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
   static bool attr_set[64] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(kernel_of<C>(), cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(rows_q4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
-  e = launch_serialized(kernel_of<C>(), grid, dim3(32 * C::WP), C::SMEM, stream, p);
+  e = launch_serialized(rows_q4_kernel<C>, grid, dim3(32 * C::WP), C::SMEM, stream, p);
   if (info) {
     info->kernels = 1;
     info->grid = static_cast<int>(grid.x);

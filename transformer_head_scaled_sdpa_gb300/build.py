@@ -23,9 +23,10 @@ LIB_PATH = os.path.join(BUILD_DIR, "libmha.so")
 
 SOURCES = ["mha_abi.cu", "mha_fwd_bf16.cu", "mha_fwd_wide.cu", "mha_fwd_f32.cu", "mha_decode.cu",
            "mha_bwd.cu", "mha_gemm.cu", "mha_cache.cu", "mha_rows.cu", "mha_rows_block.cu",
-           "mha_rows_short.cu", "mha_rows_q4.cu", "mha_cache_move.cu"]
+           "mha_rows_short.cu", "mha_rows_q4.cu", "mha_rows_q4_many.cu",
+           "mha_cache_move.cu"]
 HEADERS = [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "fp8.cuh"),
-           os.path.join(CSRC, "q4.cuh"),
+           os.path.join(CSRC, "q4.cuh"), os.path.join(CSRC, "rows_q4.cuh"),
            os.path.join(CSRC, "rows.cuh"), os.path.join(CSRC, "kernels.h"),
            os.path.join(INCLUDE, "mha.h"), os.path.join(INCLUDE, "mha_test_hooks.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -184,18 +184,6 @@ struct RowsCfg {
                 "register split");
 };
 
-// Shared-memory matrix descriptor without swizzle: core matrices of 8 rows x
-// 16 bytes (128 contiguous bytes).
-//   K-major operand (rows along M/N): lbo = bytes between 16-byte columns along
-//     K, sbo = bytes between 8-row groups along M/N.
-//   MN-major operand (rows along K): sbo = bytes between 16-byte columns along
-//     M/N, lbo = bytes between 8-row groups along K.
-__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
-         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46);
-}
-
 // Instruction descriptor of kind::f8f6f4 with an e4m3 A, an e4m3 (0) or e5m2
 // (1) B and a float32 accumulator (fields as idesc_bf16_f32).
 constexpr uint32_t idesc_f8_f32(int M, int N, uint32_t b_format, bool a_mn_major, bool b_mn_major) {
@@ -216,21 +204,6 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
   } else {
     umma_ss(d, a, b, idesc, acc);
   }
-}
-
-// True for every thread of a softmax warpgroup when any of them passes true
-// (named barrier `id` over its 128 threads).
-__device__ __forceinline__ bool any_of_128(uint32_t id, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "r"(id)
-      : "memory");
-  return r != 0;
 }
 
 // Two fp16 values to e5m2 (nearest even); low half to bits 0-7.
@@ -258,40 +231,6 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t a, uint3
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(m));
   return r;
-}
-
-// Largest value of the warp.
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Sums of N values over the warp, N <= 32 a power of two: each step halves the
-// values a lane keeps and adds its partner's for them.  Lane i returns the sum
-// of value i / (32 / N).
-template <int N>
-__device__ __forceinline__ float warp_sums(const float (&v)[N], int lane) {
-  float x[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = v[i];
-  int keep = N;
-#pragma unroll
-  for (int bit = 16; bit; bit >>= 1) {
-    if (keep > 1) {
-      keep >>= 1;
-      const bool hi = (lane & bit) != 0;
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        if (i >= keep) break;
-        const float send = hi ? x[i] : x[i + keep];
-        x[i] = (hi ? x[i + keep] : x[i]) + __shfl_xor_sync(0xffffffffu, send, bit);
-      }
-    } else {
-      x[0] += __shfl_xor_sync(0xffffffffu, x[0], bit);
-    }
-  }
-  return x[0];
 }
 
 // 8 or 16 consecutive 32-bit columns of this warp's TMEM lanes.

@@ -52,6 +52,67 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, thread_wait(bar, parity, abort, site));
 }
 
+// Shared-memory matrix descriptor without swizzle: core matrices of 8 rows x
+// 16 bytes (128 contiguous bytes).
+//   K-major operand (rows along M/N): lbo = bytes between 16-byte columns along
+//     K, sbo = bytes between 8-row groups along M/N.
+//   MN-major operand (rows along K): sbo = bytes between 16-byte columns along
+//     M/N, lbo = bytes between 8-row groups along K.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// True for every thread of a softmax warpgroup when any of them passes true
+// (named barrier `id` over its 128 threads).
+__device__ __forceinline__ bool any_of_128(uint32_t id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Largest value of the warp.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sums of N values over the warp, N <= 32 a power of two: each step halves the
+// values a lane keeps and adds its partner's for them.  Lane i returns the sum
+// of value i / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&v)[N], int lane) {
+  float x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = v[i];
+  int keep = N;
+#pragma unroll
+  for (int bit = 16; bit; bit >>= 1) {
+    if (keep > 1) {
+      keep >>= 1;
+      const bool hi = (lane & bit) != 0;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= keep) break;
+        const float send = hi ? x[i] : x[i + keep];
+        x[i] = (hi ? x[i + keep] : x[i]) + __shfl_xor_sync(0xffffffffu, send, bit);
+      }
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], bit);
+    }
+  }
+  return x[0];
+}
+
 // ---------------------------------------------------------------------------
 // Units
 // ---------------------------------------------------------------------------

@@ -1,0 +1,162 @@
+// rows_q4.cuh -- what the kernels of the steps over the 4-bit cache share
+// (mha_rows_q4.cu: up to sixteen rows per key head; mha_rows_q4_many.cu: more).
+#pragma once
+
+#include "fp8.cuh"
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace mha {
+
+constexpr float kNoRef = -3.0e38f;  // a row that has seen no key
+constexpr float kLift = 8.f;        // weights are 2^kLift at their reference
+constexpr float kLimit = 15.f;      // and stay below 2^kLimit, inside fp16's range
+
+// Swizzle of TMA's rows of W / 2 bytes (32, 64 or 128): 16-byte piece c of row `key` of a
+// tile lies at piece c ^ swizzle(key), so that the eight rows of a matrix lie in
+// different banks.
+template <int W>
+__device__ __forceinline__ int swizzle(int key) {
+  return W == 64 ? (key >> 2) & 1 : (W == 128 ? (key >> 1) & 3 : key & 7);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What a key's offset and step, and its value's, come to in a step.
+struct KeyFactors {
+  float step, lo;             // of the key
+  float v_log, v_inv, v_ofs;  // of the value: log2 step, 1 / step, lo / step
+};
+__device__ __forceinline__ KeyFactors key_factors(uint32_t k, uint32_t v) {
+  KeyFactors f;
+  f.step = bf16_hi(k);
+  f.lo = bf16_lo(k);
+  const float step = bf16_hi(v);
+  f.v_log = lg2_approx(step);
+  f.v_inv = rcp_approx(step);
+  f.v_ofs = bf16_lo(v) * f.v_inv;
+  return f;
+}
+
+// This CTA's unit of a launch whose sequences' units are of `blocks` blocks of rows;
+// false when it has none.
+__device__ __forceinline__ bool this_unit(const RowsParams& p, int blocks, int slots, int lane, Unit* unit) {
+  const int index = static_cast<int>(blockIdx.x), part = index / p.units;
+  if (balanced(p)) {
+    int first, splits, per;
+    balance(p, lane, &first, &splits, &per);
+    const unsigned here = __ballot_sync(0xffffffffu, lane < p.B && part >= first && part < first + splits);
+    if (here == 0) return false;  // (more units than the sequences have splits)
+    const int b = __ffs(here) - 1;
+    *unit = unit_of(p, index, blocks, b, part - __shfl_sync(0xffffffffu, first, b), __shfl_sync(0xffffffffu, per, 0));
+  } else if (longest_first(p, slots)) {
+    const int place = place_of(p, lane);
+    const unsigned here = __ballot_sync(0xffffffffu, lane < p.B && place == part);
+    *unit = unit_of(p, index, blocks, __ffs(here) - 1, 0, 0);
+  } else {
+    *unit = unit_of(p, index, blocks, part % p.B, part / p.B, 0);
+  }
+  return unit->splits > 0;
+}
+
+// Word x % 4 of the mask of row x / 4 (a chain's: bits 0 .. t).
+template <typename F>
+__device__ __forceinline__ uint64_t mask_word(const RowsParams& p, const Unit& it, int x, F&& out_row) {
+  int t;
+  const int out = out_row(x >> 2, &t), word = x & 3;
+  if (out < 0 || t >= it.live || it.end <= it.n) return 0;
+  if (p.tree_mask)
+    return word < p.words ? __ldg(p.tree_mask + (static_cast<long long>(it.b) * p.T + t) * p.words + word) : 0;
+  const int count = t + 1 - 64 * word;
+  return count >= 64 ? ~0ull : (count <= 0 ? 0ull : (1ull << count) - 1);
+}
+
+// The offsets and steps of the key and the value that a thread owns in each tile, copied
+// into shared memory kAhead tiles ahead.  (Loaded into registers, even a tile ahead, they
+// were waited for within the tile: the hardware counts a warp's outstanding operations in
+// a few counters, and one that other, short operations shared with them was not empty
+// before they had come: 1,500 of a tile's 2,600 cycles.)
+constexpr int kAhead = 3;
+struct Scales {
+  static constexpr int BYTES = (kAhead + 1) * 128 * 8;
+  uint32_t at;               // the thread's slot 0
+  const uint32_t *k, *v;     // of position 0
+  int own, stop;             // the thread's key of a tile; keys past `stop` are its last one
+  __device__ __forceinline__ void copy(int i, int tile0) const {
+    if (tile0 < stop) {
+      const int key = min(tile0 + own, stop - 1);
+      const uint32_t to = at + (i & kAhead) * 1024;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(k + key) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4), "l"(v + key) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void start(int first) const {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) copy(i, first + i * kKeys);
+  }
+  // Tile i's words (its place in the unit), and the copy of tile i + kAhead's.
+  __device__ __forceinline__ uint2 get(int i, int tile0) const {
+    copy(i + kAhead, tile0 + kAhead * kKeys);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+    uint2 w;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(at + (i & kAhead) * 1024) : "memory");
+    return w;
+  }
+};
+static_assert((kAhead & (kAhead + 1)) == 0, "slots by a mask");
+
+// What a CTA loads: tiles of kKeys keys or values.
+template <int W>
+struct Loader {
+  static constexpr int ROW = W / 2, TILE = kKeys * ROW;
+  const RowsParams& p;
+  const Unit& it;
+  int stop;
+  // (a ragged tile in boxes of kRowsQ4Box keys as far as it goes; what lies behind in the
+  // ring are some codes: finite, and their weights are 0)
+  __device__ __forceinline__ int boxes(int key) const {
+    return stop - key >= kKeys ? 0 : (stop - key + kRowsQ4Box - 1) / kRowsQ4Box;
+  }
+  __device__ __forceinline__ uint32_t bytes(int key) const {
+    const int n = boxes(key);
+    return n == 0 ? TILE : n * kRowsQ4Box * ROW;
+  }
+  __device__ __forceinline__ void copy(uint32_t dst, uint32_t bar, int key, bool v) const {
+    const int n = boxes(key);
+    if (n == 0) {
+      tma_load_4d(dst, v ? &p.tm_v : &p.tm_k, bar, 0, it.hk, key, it.b);
+      return;
+    }
+#pragma unroll 1
+    for (int x = 0; x < n; ++x)
+      tma_load_4d(dst + x * kRowsQ4Box * ROW, v ? &p.tm_v_box : &p.tm_k_box, bar, 0, it.hk, key + x * kRowsQ4Box, it.b);
+  }
+  // Keys and values side by side.
+  __device__ __forceinline__ void operator()(uint32_t dst, uint32_t bar, int key) const {
+    mbar_arrive_expect_tx(bar, 2 * bytes(key));
+    copy(dst, bar, key, false);
+    copy(dst + TILE, bar, key, true);
+  }
+};
+
+// More than sixteen rows per key head (mha_rows_q4_many.cu).
+int rows_q4_many_rows(int R);  // of a unit
+cudaError_t launch_rows_q4_many(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
+
+}  // namespace mha

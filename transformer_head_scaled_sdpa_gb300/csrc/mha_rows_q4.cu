@@ -653,13 +653,8 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
 }  // namespace
 
 RowsQ4Shape rows_q4_shape(int d, int R) {
+  if (R > kFewRows) return rows_q4_many_shape(d, R);
   RowsQ4Shape s = {};
-  if (R > kFewRows) {
-    s.width = d <= 64 ? 64 : (d <= 128 ? 128 : 256);
-    s.rows = rows_q4_many_rows(R);
-    s.ctas = 1;
-    return s;
-  }
   with_config(d, R, [&](auto cfg) {
     using C = decltype(cfg);
     s.width = C::W;

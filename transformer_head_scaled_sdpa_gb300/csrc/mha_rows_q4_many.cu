@@ -10,41 +10,46 @@ namespace {
 constexpr int kRoleMany = 21;
 
 // W: widest head; NR: rows of a unit.
-template <int W_, int NR_>
+template <int W_, int NR_, int RPT_, int VST_, int SLOTS_, int CTAS_>
 struct ManyCfg {
-  static constexpr int W = W_, NR = NR_;
+  static constexpr int W = W_, NR = NR_, CTAS = CTAS_;
   static constexpr int ROW = W / 2, TILE = kKeys * ROW;  // packed bytes of a row, of a tile's keys or values
   static constexpr int KC = W / 32;                      // 16-byte pieces of a row
   static constexpr int BLKS = W == 256 ? 2 : 1, FB = W / BLKS;  // blocks of features of the output
   static constexpr int CHUNK = kKeys * 128;              // [128 keys x 64 features] in fp16, 128-byte swizzle
   static constexpr int VBYTES = FB / 64 * CHUNK;
-  static constexpr int KST = 2, VST = W == 256 ? 3 : 2;  // unpacked keys (tensor memory), blocks of values
-  static constexpr int SLOTS = W == 256 ? 4 : 8;         // packed tiles
-  static constexpr int RPT = NR / 2;                     // rows of a softmax thread
+  static constexpr int KST = 2, VST = VST_;              // unpacked keys (tensor memory), blocks of values
+  static constexpr int SLOTS = SLOTS_;                   // packed tiles
+  static constexpr int RPT = RPT_, WGS = NR / RPT;         // rows of a softmax thread, softmax warpgroups
   static constexpr int Q_BYTES = NR * W * 2, P_BYTES = kKeys * NR * 2;
   static constexpr uint32_t TM_K = 0, TM_S = KST * (W / 2), TM_O = TM_S + 2 * NR;
   static constexpr uint32_t TM_USED = TM_O + BLKS * NR;
   static constexpr uint32_t TMEM_COLS = TM_USED <= 128 ? 128 : (TM_USED <= 256 ? 256 : 512);
-  static_assert(TM_USED <= 512 && RPT % 16 == 0 && NR * 4 <= 256, "rows");
+  static_assert(TM_USED <= 512 && TMEM_COLS * CTAS <= 512 && NR % RPT == 0, "tensor memory");
   static constexpr int OFF_RING = VST * VBYTES;
   static constexpr int OFF_Q = OFF_RING + SLOTS * TILE;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_SCALES = OFF_P + P_BYTES;            // a warpgroup's words
-  static constexpr int OFF_MASKS = OFF_SCALES + 2 * Scales::BYTES;  // uint64 [NR][4]
-  static constexpr int OFF_FACTORS = OFF_MASKS + NR * 32;       // float4 [NR / 2]: factors of two rows' products, of their sums
-  static constexpr int OFF_ROWS = OFF_FACTORS + NR * 8;         // float [6][NR], int [NR]
-  static constexpr int OFF_RED = OFF_ROWS + NR * 28;            // float [2][NR][4]
+  static constexpr int OFF_SCALES = OFF_P + 2 * P_BYTES;        // a warpgroup's words
+  static constexpr int OFF_MASKS = OFF_SCALES + WGS * Scales::BYTES;  // uint64 [NR][4]
+  static constexpr int OFF_FACTORS = OFF_MASKS + NR * 32;       // float4 [NR / 2]: of two rows, the factors of offsets, and what scores are taken less (negative)
+  static constexpr int OFF_ROWS = OFF_FACTORS + NR * 8;         // float [5][NR], int [NR]
+  static constexpr int OFF_RED = OFF_ROWS + NR * 24;            // float [2][NR][4]
   // barriers
   static constexpr int FULL = 0, EMPTY = SLOTS;          // + slot
   static constexpr int K_FULL = 2 * SLOTS, K_EMPTY = K_FULL + KST;  // + stage
   static constexpr int V_FULL = K_EMPTY + KST, V_EMPTY = V_FULL + VST;
   static constexpr int Q_FULL = V_EMPTY + VST, S_FULL = Q_FULL + 1;  // + tile & 1
-  static constexpr int P_FULL = S_FULL + 2, PV_DONE = P_FULL + 1, DRAIN = PV_DONE + 1, NBAR = DRAIN + 1;
+  static constexpr int P_FULL = S_FULL + 2, PV_DONE = P_FULL + 2,  // + tile & 1
+                        DRAIN = PV_DONE + 2, NBAR = DRAIN + 1;
   static constexpr int OFF_BAR = OFF_RED + NR * 32;
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR, OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
-  static constexpr int SOFT = 8, UNPACK = 4, THREADS = 32 * (SOFT + UNPACK + 2);  // warps; the last two: MMA, loads
-  static_assert(SMEM <= 232448 && OFF_BAR % 8 == 0 && OFF_MASKS % 16 == 0, "shared memory");
+  static constexpr int SOFT = 4 * WGS, UNPACK = 4;       // warps; behind them MMA, loads, two without work
+  static constexpr int THREADS = 32 * (SOFT + UNPACK + 4);
+  // registers: the softmax warps take from the others
+  static constexpr int REGS = 65536 / CTAS / THREADS / 8 * 8, REGS_OTHER = REGS > 100 ? 88 : 48;
+  static constexpr int REGS_SOFT = (REGS * THREADS - REGS_OTHER * 256) / (32 * SOFT) / 8 * 8;
+  static_assert(SMEM <= (CTAS == 2 ? 115712 : 232448) && OFF_BAR % 8 == 0 && OFF_MASKS % 16 == 0, "shared memory");
 };
 
 // Instruction descriptor of kind::f16 with fp16 operands (fields as idesc_bf16_f32).
@@ -64,10 +69,9 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t* r) {
 // Feature (of eight) at place x of that order.
 __device__ __forceinline__ int feature_at(int x) { return (x >> 1) + 4 * (x & 1); }
 
-template <int W, int NR>
-__global__ void __launch_bounds__((ManyCfg<W, NR>::THREADS), 1)
-    rows_q4_many_kernel(const __grid_constant__ RowsParams p) {
-  using C = ManyCfg<W, NR>;
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const __grid_constant__ RowsParams p) {
+  constexpr int W = C::W, NR = C::NR;
   constexpr int KC = C::KC, RPT = C::RPT, BLKS = C::BLKS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -95,7 +99,9 @@ __global__ void __launch_bounds__((ManyCfg<W, NR>::THREADS), 1)
     mbar_init(bar(C::S_FULL), 1);
     mbar_init(bar(C::S_FULL + 1), 1);
     mbar_init(bar(C::P_FULL), C::SOFT);
+    mbar_init(bar(C::P_FULL + 1), C::SOFT);
     mbar_init(bar(C::PV_DONE), 1);
+    mbar_init(bar(C::PV_DONE + 1), 1);
     mbar_init(bar(C::DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -114,411 +120,428 @@ __global__ void __launch_bounds__((ManyCfg<W, NR>::THREADS), 1)
 
   const int n_rows = p.T * p.G;
   Unit it = {};
-  const bool mine = this_unit(p, (n_rows + NR - 1) / NR, kSms, lane, &it);
+  const bool mine = this_unit(p, (n_rows + NR - 1) / NR, kSms * C::CTAS, lane, &it);
   const int first = it.t0 * kKeys, stop = mine ? min(it.t1 * kKeys, it.end) : 0;
   const int tiles = stop > first ? (stop - first + kKeys - 1) / kKeys : 0;
   auto site = [&](int id) { return kRoleMany * 64 + id; };
 
-  if (!mine) {
-    // (more units than the sequences have splits)
-  } else if (warp == kLoadWarp) {
-    // ---- items K0 K1 V0 K2 V1 ... of packed codes
-    if (lane == 0) {
-      const Loader<W> load{p, it, stop};
-      bool ok = true;
-      for (int x = 0; x < 2 * tiles; ++x) {
-        const int slot = x % C::SLOTS;
-        if (x >= C::SLOTS)
-          ok = thread_wait(bar(C::EMPTY + slot), (x / C::SLOTS - 1) & 1, abort_flag, site(C::EMPTY + slot));
-        if (!ok) break;
-        const bool v = x == 2 * tiles - 1 || (x > 0 && (x & 1) == 0);
-        const int t = x == 2 * tiles - 1 ? tiles - 1 : (v ? x / 2 - 1 : (x + 1) / 2);
-        const int key = first + t * kKeys;
-        mbar_arrive_expect_tx(bar(C::FULL + slot), load.bytes(key));
-        load.copy(base + C::OFF_RING + slot * C::TILE, bar(C::FULL + slot), key, v);
+  if (warp >= C::SOFT) {
+    regs_decrease<C::REGS_OTHER>();
+    if (!mine) {
+      // (more units than the sequences have splits)
+    } else if (warp == kLoadWarp) {
+      // ---- items K0 K1 V0 K2 V1 ... of packed codes
+      if (lane == 0) {
+        const Loader<W> load{p, it, stop};
+        bool ok = true;
+        for (int x = 0; x < 2 * tiles; ++x) {
+          const int slot = x % C::SLOTS;
+          if (x >= C::SLOTS)
+            ok = thread_wait(bar(C::EMPTY + slot), (x / C::SLOTS - 1) & 1, abort_flag, site(C::EMPTY + slot));
+          if (!ok) break;
+          const bool v = x == 2 * tiles - 1 || (x > 0 && (x & 1) == 0);
+          const int t = x == 2 * tiles - 1 ? tiles - 1 : (v ? x / 2 - 1 : (x + 1) / 2);
+          const int key = first + t * kKeys;
+          mbar_arrive_expect_tx(bar(C::FULL + slot), load.bytes(key));
+          load.copy(base + C::OFF_RING + slot * C::TILE, bar(C::FULL + slot), key, v);
+        }
       }
-    }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ---- S(0), S(1), PV(0), S(2), PV(1), ...
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16_f32(128, NR, false, false);
-      constexpr uint32_t idesc_o = idesc_f16_f32(C::FB, NR, true, true);
-      const uint64_t dq = smem_desc_plain(base + C::OFF_Q, NR * 16, 128);
-      const uint64_t dv = smem_desc_sw128(base, C::CHUNK, 1024);
-      const uint64_t dp = smem_desc_plain(base + C::OFF_P, 128, kKeys * 16);
-      const int n_ks = (p.d + 15) / 16;
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ---- S(0), S(1), PV(0), S(2), PV(1), ...
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = idesc_f16_f32(128, NR, false, false);
+        constexpr uint32_t idesc_o = idesc_f16_f32(C::FB, NR, true, true);
+        const uint64_t dq = smem_desc_plain(base + C::OFF_Q, NR * 16, 128);
+        const uint64_t dv = smem_desc_sw128(base, C::CHUNK, 1024);
+        const uint64_t dp = smem_desc_plain(base + C::OFF_P, 128, kKeys * 16);
+        const int n_ks = (p.d + 15) / 16;
+        bool ok = true;
+        auto wait = [&](int id, int parity) {
+          ok = ok && thread_wait(bar(id), parity & 1, abort_flag, site(id));
+          tc_fence_after();
+          return ok;
+        };
+        if (tiles > 0) wait(C::Q_FULL, 0);
+        for (int t = 0; t <= tiles && tiles > 0 && ok; ++t) {
+          if (t < tiles) {
+            // (the scores of tile t - 2 are read: its weights were there for its values' products)
+            const int st = t % C::KST;
+            if (!wait(C::K_FULL + st, t / C::KST)) break;
+            const uint32_t d = tmem + C::TM_S + (t & 1) * NR, a = tmem + C::TM_K + st * (W / 2);
+            for (int k = 0; k < n_ks; ++k)
+              umma_ts(d, a + 8 * k, dq + static_cast<uint64_t>(2 * NR * k), idesc_s, k > 0 ? 1u : 0u);
+            umma_commit(bar(C::S_FULL + (t & 1)));
+            umma_commit(bar(C::K_EMPTY + st));
+          }
+          if (t > 0) {
+            if (!wait(C::P_FULL + ((t - 1) & 1), (t - 1) >> 1)) break;
+#pragma unroll
+            for (int blk = 0; blk < BLKS; ++blk) {
+              const int x = (t - 1) * BLKS + blk, st = x % C::VST;
+              if (!wait(C::V_FULL + st, x / C::VST)) break;
+              const uint64_t a = dv + static_cast<uint64_t>((st * C::VBYTES) >> 4);
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                umma_ss(tmem + C::TM_O + blk * NR, a + static_cast<uint64_t>((k * 2048) >> 4),
+                        dp + static_cast<uint64_t>((((t - 1) & 1) * C::P_BYTES + k * 256) >> 4), idesc_o, (t > 1 || k > 0) ? 1u : 0u);
+              umma_commit(bar(C::V_EMPTY + st));
+            }
+            if (!ok) break;
+            umma_commit(bar(C::PV_DONE + ((t - 1) & 1)));
+          }
+        }
+        // every tensor-core operation issued must be complete before TMEM is freed
+        umma_commit(bar(C::DRAIN));
+      }
+      __syncwarp();
+      volatile int never = 0;
+      mbar_wait(bar(C::DRAIN), 0, &never, p.status, site(C::DRAIN));
+    } else if (warp < kMmaWarp) {
+      // ---- unpacking: a thread has a key
+      const int key = 32 * (warp & 3) + lane;
+      const uint32_t packed = base + C::OFF_RING + key * C::ROW;
+      const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       bool ok = true;
+      int x = 0;
       auto wait = [&](int id, int parity) {
-        ok = ok && thread_wait(bar(id), parity & 1, abort_flag, site(id));
-        tc_fence_after();
+        ok = ok && warp_wait(bar(id), parity & 1, abort_flag, site(id));
         return ok;
       };
-      if (tiles > 0) wait(C::Q_FULL, 0);
-      for (int t = 0; t <= tiles && tiles > 0 && ok; ++t) {
-        if (t < tiles) {
-          // (the scores of tile t - 2 are read: its weights were there for its values' products)
-          const int st = t % C::KST;
-          if (!wait(C::K_FULL + st, t / C::KST)) break;
-          const uint32_t d = tmem + C::TM_S + (t & 1) * NR, a = tmem + C::TM_K + st * (W / 2);
-          for (int k = 0; k < n_ks; ++k)
-            umma_ts(d, a + 8 * k, dq + static_cast<uint64_t>(2 * NR * k), idesc_s, k > 0 ? 1u : 0u);
-          umma_commit(bar(C::S_FULL + (t & 1)));
-          umma_commit(bar(C::K_EMPTY + st));
+      auto words = [&](int slot, int c) { return ld_shared_v4(packed + slot * C::TILE + 16 * (c ^ swizzle<W>(key))); };
+      auto keys = [&](int t) {
+        const int slot = x % C::SLOTS, st = t % C::KST;
+        if (!wait(C::FULL + slot, x / C::SLOTS)) return;
+        if (t >= C::KST && !wait(C::K_EMPTY + st, t / C::KST - 1)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint4 w = words(slot, c);
+          uint32_t r[16];
+          unpack(w.x, r);
+          unpack(w.y, r + 4);
+          unpack(w.z, r + 8);
+          unpack(w.w, r + 12);
+          tmem_st16(tmem + lanes + C::TM_K + st * (W / 2) + 16 * c, r);
         }
-        if (t > 0) {
-          if (!wait(C::P_FULL, t - 1)) break;
+        warp_arrive(bar(C::EMPTY + slot), lane);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(bar(C::K_FULL + st), lane);
+        ++x;
+      };
+      auto values = [&](int t) {
+        const int slot = x % C::SLOTS;
+        if (!wait(C::FULL + slot, x / C::SLOTS)) return;
 #pragma unroll
-          for (int blk = 0; blk < BLKS; ++blk) {
-            const int x = (t - 1) * BLKS + blk, st = x % C::VST;
-            if (!wait(C::V_FULL + st, x / C::VST)) break;
-            const uint64_t a = dv + static_cast<uint64_t>((st * C::VBYTES) >> 4);
+        for (int blk = 0; blk < BLKS; ++blk) {
+          const int y = t * BLKS + blk, st = y % C::VST;
+          if (y >= C::VST && !wait(C::V_EMPTY + st, y / C::VST - 1)) return;
+          const uint32_t to = base + st * C::VBYTES + key * 128;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              umma_ss(tmem + C::TM_O + blk * NR, a + static_cast<uint64_t>((k * 2048) >> 4),
-                      dp + static_cast<uint64_t>((k * 256) >> 4), idesc_o, (t > 1 || k > 0) ? 1u : 0u);
-            umma_commit(bar(C::V_EMPTY + st));
+          for (int c = 0; c < KC / BLKS; ++c) {
+            const uint4 w = words(slot, blk * (KC / BLKS) + c);
+            const uint32_t z[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t r[4];
+              unpack(z[i], r);
+              const int piece = 4 * c + i;
+              st_shared_v4(to + (piece >> 3) * C::CHUNK + (((piece & 7) ^ (key & 7)) << 4), r[0], r[1], r[2], r[3]);
+            }
           }
-          if (!ok) break;
-          umma_commit(bar(C::PV_DONE));
+          fence_proxy_async_smem();
+          if (blk == BLKS - 1) warp_arrive(bar(C::EMPTY + slot), lane);
+          warp_arrive(bar(C::V_FULL + st), lane);
         }
+        ++x;
+      };
+      if (tiles > 0) keys(0);
+      for (int t = 0; t < tiles && ok; ++t) {
+        if (t + 1 < tiles) keys(t + 1);
+        if (ok) values(t);
       }
-      // every tensor-core operation issued must be complete before TMEM is freed
-      umma_commit(bar(C::DRAIN));
-    }
-    __syncwarp();
-    volatile int never = 0;
-    mbar_wait(bar(C::DRAIN), 0, &never, p.status, site(C::DRAIN));
-  } else if (warp >= C::SOFT) {
-    // ---- unpacking: a thread has a key
-    const int key = 32 * (warp & 3) + lane;
-    const uint32_t packed = base + C::OFF_RING + key * C::ROW;
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    bool ok = true;
-    int x = 0;
-    auto wait = [&](int id, int parity) {
-      ok = ok && warp_wait(bar(id), parity & 1, abort_flag, site(id));
-      return ok;
-    };
-    auto words = [&](int slot, int c) { return ld_shared_v4(packed + slot * C::TILE + 16 * (c ^ swizzle<W>(key))); };
-    auto keys = [&](int t) {
-      const int slot = x % C::SLOTS, st = t % C::KST;
-      if (!wait(C::FULL + slot, x / C::SLOTS)) return;
-      if (t >= C::KST && !wait(C::K_EMPTY + st, t / C::KST - 1)) return;
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint4 w = words(slot, c);
-        uint32_t r[16];
-        unpack(w.x, r);
-        unpack(w.y, r + 4);
-        unpack(w.z, r + 8);
-        unpack(w.w, r + 12);
-        tmem_st16(tmem + lanes + C::TM_K + st * (W / 2) + 16 * c, r);
-      }
-      warp_arrive(bar(C::EMPTY + slot), lane);
-      tmem_st_wait();
-      tc_fence_before();
-      warp_arrive(bar(C::K_FULL + st), lane);
-      ++x;
-    };
-    auto values = [&](int t) {
-      const int slot = x % C::SLOTS;
-      if (!wait(C::FULL + slot, x / C::SLOTS)) return;
-#pragma unroll
-      for (int blk = 0; blk < BLKS; ++blk) {
-        const int y = t * BLKS + blk, st = y % C::VST;
-        if (y >= C::VST && !wait(C::V_EMPTY + st, y / C::VST - 1)) return;
-        const uint32_t to = base + st * C::VBYTES + key * 128;
-#pragma unroll
-        for (int c = 0; c < KC / BLKS; ++c) {
-          const uint4 w = words(slot, blk * (KC / BLKS) + c);
-          const uint32_t z[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t r[4];
-            unpack(z[i], r);
-            const int piece = 4 * c + i;
-            st_shared_v4(to + (piece >> 3) * C::CHUNK + (((piece & 7) ^ (key & 7)) << 4), r[0], r[1], r[2], r[3]);
-          }
-        }
-        fence_proxy_async_smem();
-        if (blk == BLKS - 1) warp_arrive(bar(C::EMPTY + slot), lane);
-        warp_arrive(bar(C::V_FULL + st), lane);
-      }
-      ++x;
-    };
-    if (tiles > 0) keys(0);
-    for (int t = 0; t < tiles && ok; ++t) {
-      if (t + 1 < tiles) keys(t + 1);
-      if (ok) values(t);
     }
   } else {
-    // ---- softmax: a thread has a key and half of the rows
-    const int wg = warp >> 2, w4 = warp & 3, kt = tid & 127, r0 = wg * RPT, nbar = 1 + wg;
-    const int rows_here = min(max(n_rows - it.rb * NR - r0, 0), RPT);
-    float4* factors = reinterpret_cast<float4*>(smem + C::OFF_FACTORS);
-    float* row_sub = reinterpret_cast<float*>(smem + C::OFF_ROWS);  // what scores are taken less
-    float* row_ref = row_sub + NR;                                  // references less kLift
-    float* row_by = row_ref + NR;                                   // a move's factors, and differences
-    float* row_down = row_by + NR;
-    float* row_inv = row_down + NR;
-    float* row_add = row_inv + NR;
-    int* row_out = reinterpret_cast<int*>(row_add + NR);
-    float* red = reinterpret_cast<float*>(smem + C::OFF_RED);       // [row][warp], of the second sum behind
-    uint64_t(*masks)[4] = reinterpret_cast<uint64_t(*)[4]>(smem + C::OFF_MASKS);
-    // Output row of row r of the unit (-1 past the last), t: its drafted token.
-    auto out_row = [&](int r, int* t) {
-      const int gr = it.rb * NR + r;
-      *t = -1;
-      if (gr >= n_rows) return -1;
-      *t = p.G == 1 ? gr : gr / p.G;
-      return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
-    };
-    const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
-    const Scales words{base + C::OFF_SCALES + wg * Scales::BYTES + 8 * kt,
-                       reinterpret_cast<const uint32_t*>(p.k_scale) + scales,
-                       reinterpret_cast<const uint32_t*>(p.v_scale) + scales, kt, stop};
-    words.start(first);
-    {
-      // Q: eight features to a lane, W / 8 lanes to a row
-      constexpr int LPR = W / 8, RPW = 32 / LPR, PASSES = NR / (C::SOFT * RPW);
-      const int piece = lane % LPR;
-      uint4 v[PASSES];
-      int outs[PASSES];
+    regs_increase<C::REGS_SOFT>();
+    if (mine) {
+      // ---- softmax: a thread has a key and RPT of the rows
+      const int wg = warp >> 2, w4 = warp & 3, kt = tid & 127, r0 = wg * RPT, nbar = 1 + wg;
+      const int rows_here = min(max(n_rows - it.rb * NR - r0, 0), RPT);
+      float4* factors = reinterpret_cast<float4*>(smem + C::OFF_FACTORS);
+      auto less = [&](int r) { return reinterpret_cast<float*>(factors + r / 2) + 2 + (r & 1); };
+      float* row_ref = reinterpret_cast<float*>(smem + C::OFF_ROWS);  // references less kLift
+      float* row_by = row_ref + NR;                                   // a move's factors, and differences
+      float* row_down = row_by + NR;
+      float* row_inv = row_down + NR;
+      float* row_add = row_inv + NR;
+      int* row_out = reinterpret_cast<int*>(row_add + NR);
+      float* red = reinterpret_cast<float*>(smem + C::OFF_RED);       // [row][warp], of the second sum behind
+      uint64_t(*masks)[4] = reinterpret_cast<uint64_t(*)[4]>(smem + C::OFF_MASKS);
+      // Output row of row r of the unit (-1 past the last), t: its drafted token.
+      auto out_row = [&](int r, int* t) {
+        const int gr = it.rb * NR + r;
+        *t = -1;
+        if (gr >= n_rows) return -1;
+        *t = p.G == 1 ? gr : gr / p.G;
+        return (it.b * p.T + *t) * p.H + it.hk * p.G + (gr - *t * p.G);
+      };
+      const long long scales = (static_cast<long long>(it.b) * p.H_kv + it.hk) * p.Lk;
+      const Scales words{base + C::OFF_SCALES + wg * Scales::BYTES + 8 * kt,
+                         reinterpret_cast<const uint32_t*>(p.k_scale) + scales,
+                         reinterpret_cast<const uint32_t*>(p.v_scale) + scales, kt, stop};
+      words.start(first);
+      float scale;  // of scores: q's and the softmax's
+      {
+        // Q: eight features to a lane, W / 8 lanes to a row
+        constexpr int LPR = W / 8, RPW = 32 / LPR, PASSES = (NR + C::SOFT * RPW - 1) / (C::SOFT * RPW);
+        static_assert(C::SOFT * RPW <= NR, "a row to every group of lanes");
+        const int piece = lane % LPR;
+        uint4 v[PASSES];
+        int outs[PASSES];
 #pragma unroll
-      for (int y = 0; y < PASSES; ++y) {
-        int t;
-        outs[y] = out_row((y * C::SOFT + warp) * RPW + lane / LPR, &t);
-        v[y] = make_uint4(0, 0, 0, 0);
-        if (outs[y] >= 0 && t < it.live && 8 * piece < p.d)
-          v[y] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                      static_cast<long long>(outs[y]) * p.d + 8 * piece));
-      }
-      const uint64_t bits = tid < NR * 4 ? mask_word(p, it, tid, out_row) : 0;
-#pragma unroll
-      for (int y = 0; y < PASSES; ++y) {
-        const int r = (y * C::SOFT + warp) * RPW + lane / LPR;
-        const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+        for (int y = 0; y < PASSES; ++y) {
+          int t;
+          outs[y] = out_row((y * C::SOFT + warp) * RPW + lane / LPR, &t);
+          v[y] = make_uint4(0, 0, 0, 0);
+          if (outs[y] >= 0 && t < it.live && 8 * piece < p.d)
+            v[y] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                        static_cast<long long>(outs[y]) * p.d + 8 * piece));
+        }
+        const uint64_t bits = tid < NR * 4 ? mask_word(p, it, tid, out_row) : 0;
+        // q 2^-e with the unit's largest magnitude in [2^14, 2^15): what a smaller row loses is
+        // 2^-25 of the largest row's scores (a NaN is passed over here)
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
+        for (int y = 0; y < PASSES; ++y) {
+          const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
 #pragma unroll
-        for (int z = 1; z < LPR; z <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, z));
-        // q 2^-e with the largest magnitude in [2^14, 2^15)
+          for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
+        }
+        amax = warp_max(amax);
+        if (lane == 0) red[warp] = amax;
+        named_barrier(8, 32 * C::SOFT);
+#pragma unroll
+        for (int w = 0; w < C::SOFT; ++w) amax = fmaxf(amax, red[w]);
         const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100);
         const float inv = pow2i(-e);
-        float f[8], sum = 0.f;
+        scale = pow2i(e) * p.scale_log2;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[2 * i] = bf16_lo(x[i]) * inv;
-          f[2 * i + 1] = bf16_hi(x[i]) * inv;
-          sum += f[2 * i] + f[2 * i + 1];
-        }
+        for (int y = 0; y < PASSES; ++y) {
+          const int r = (y * C::SOFT + warp) * RPW + lane / LPR;
+          const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+          float f[8], sum = 0.f;
 #pragma unroll
-        for (int z = 1; z < LPR; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
-        st_shared_v4(base + C::OFF_Q + piece * (NR * 16) + r * 16, pack_f16x2(f[0], f[4]),
-                     pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f), pack_f16x2(f[2], f[6]),
-                     pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f));
-        if (piece == 0) {
-          const float a = pow2i(e) * p.scale_log2;
-          float* to = reinterpret_cast<float*>(factors + r / 2) + (r & 1);
-          to[0] = a * 16777216.f;  // (codes are 2^-24)
-          to[2] = a * sum;
-          row_out[r] = outs[y];
-        }
-      }
-      if (tid < NR * 4) masks[tid >> 2][tid & 3] = bits;
-      if (tid < NR) {
-        row_sub[tid] = 0.f;
-        row_ref[tid] = kNoRef;
-      }
-      fence_proxy_async_smem();
-      warp_arrive(bar(C::Q_FULL), lane);
-      named_barrier(3, 32 * C::SOFT);
-    }
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4) << 16);
-    float l[RPT], ofs[RPT];
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(x[i]) * inv;
+            f[2 * i + 1] = bf16_hi(x[i]) * inv;
+            sum += f[2 * i] + f[2 * i + 1];
+          }
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) l[r] = ofs[r] = 0.f;
-    bool ok = true, pending = true;  // a row has no reference yet
-    auto wait = [&](int id, int parity) {
-      ok = warp_wait(bar(id), parity & 1, abort_flag, site(id)) && ok;
-      tc_fence_after();
-    };
-    // a live row of this thread to look after
-    int own_t = -1;
-    const bool own_live = kt < rows_here && out_row(r0 + kt, &own_t) >= 0 && own_t < it.live;
-#pragma unroll 1
-    for (int t = 0; t < tiles; ++t) {
-      const int tile0 = first + t * kKeys;
-      const uint2 kv = words.get(t, tile0);
-      KeyFactors mine_f = key_factors(kv.x, kv.y);
-      wait(C::S_FULL + (t & 1), t >> 1);
-      float x[RPT];
-#pragma unroll
-      for (int g = 0; g < RPT; g += 16) {
-        uint32_t raw[16];
-        tmem_ld16(lanes + C::TM_S + (t & 1) * NR + r0 + g, raw);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[g + i] = __uint_as_float(raw[i]);
-      }
-      tmem_ld_wait();
-      float top = -INFINITY;
-#pragma unroll
-      for (int r = 0; r < RPT; r += 2) {
-        const float4 f = factors[(r0 + r) / 2];
-        const float2 sub = *reinterpret_cast<const float2*>(row_sub + r0 + r);
-        float a0, a1, u0, u1;
-        mul2(a0, a1, x[r], x[r + 1], f.x, f.y);
-        fma2(u0, u1, f.z, f.w, mine_f.lo, mine_f.lo, mine_f.v_log, mine_f.v_log);
-        add2(u0, u1, u0, u1, -sub.x, -sub.y);
-        fma2(x[r], x[r + 1], a0, a1, mine_f.step, mine_f.step, u0, u1);
-      }
-      if (tile0 + kKeys > min(it.n, stop)) {
-        const int key = tile0 + kt, off = key - it.n;
-        bool any = false;
-#pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-          bool sees = key < stop;
-          if (sees && off >= 0) sees = (masks[r0 + r][off >> 6] >> (off & 63)) & 1;  // (off < 256: drafted tokens end there)
-          if (!sees) x[r] = -INFINITY;
-          any = any || sees;
-        }
-        // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
-        if (!any) mine_f.v_inv = mine_f.v_ofs = 0.f;
-      }
-#pragma unroll
-      for (int r = 0; r < RPT; r += 2) top = fmax3(top, x[r], x[r + 1]);
-      if (any_of_128(nbar, pending || top > kLimit)) {
-        // references up to this tile's maxima, what was summed down by as much
-#pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-          const float m = warp_max(x[r]);
-          if (lane == 0) red[(r0 + r) * 4 + w4] = m;
-        }
-        named_barrier(nbar, 128);
-        float ref = 0.f;
-        if (kt < RPT) {
-          const int r = r0 + kt;
-          const float4 m4 = *reinterpret_cast<const float4*>(red + r * 4);
-          const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), old = row_ref[r], sub = row_sub[r];
-          ref = m == -INFINITY ? old : fmaxf(old, m + sub - kLift);
-          row_by[r] = old == kNoRef ? 1.f : ex2_approx(old - ref);  // (nothing is summed up yet)
-          const float now = ref == kNoRef ? 0.f : ref;
-          row_down[r] = sub - now;
-          row_sub[r] = now;
-          row_ref[r] = ref;
-        }
-        pending = any_of_128(nbar, own_live && ref == kNoRef);
-        if (t > 0) wait(C::PV_DONE, t - 1);
-#pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-          const float by = row_by[r0 + r];
-          x[r] += row_down[r0 + r];
-          l[r] *= by;
-          ofs[r] *= by;
-        }
-        if (t > 0) {
-#pragma unroll 1
-          for (int blk = 0; blk < BLKS; ++blk)
-#pragma unroll 1
-            for (int g = 0; g < RPT; g += 16) {
-              const uint32_t at = lanes + C::TM_O + blk * NR + r0 + g;
-              uint32_t raw[16];
-              tmem_ld16(at, raw);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * row_by[r0 + g + i]);
-              tmem_st16(at, raw);
-            }
-          tmem_st_wait();
-        }
-      } else if (t > 0) {
-        wait(C::PV_DONE, t - 1);  // (the weights' buffer is free)
-      }
-      // weights: eight rows of a key side by side
-#pragma unroll
-      for (int r = 0; r < RPT; r += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int y = r + 2 * i;
-          const float w0 = ex2_approx(x[y]), w1 = ex2_approx(x[y + 1]);
-          fma2(l[y], l[y + 1], w0, w1, mine_f.v_inv, mine_f.v_inv, l[y], l[y + 1]);
-          w[i] = pack_f16x2(w0, w1);
-          // (the offsets with the rounded weights, as the codes have them)
-          fma2(ofs[y], ofs[y + 1], half_lo(w[i]), half_hi(w[i]), mine_f.v_ofs, mine_f.v_ofs, ofs[y], ofs[y + 1]);
-        }
-        st_shared_v4(base + C::OFF_P + (r0 + r) / 8 * (kKeys * 16) + kt * 16, w[0], w[1], w[2], w[3]);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      warp_arrive(bar(C::P_FULL), lane);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // (none is left but where a wait ran out)
-
-    // ---- epilogue: sums over the keys, then O
-    {
-      const float y = warp_sums<RPT>(l, lane), z = warp_sums<RPT>(ofs, lane);
-      constexpr int GL = 32 / RPT;  // lanes that hold a row's sums
-      if (lane % GL == 0) {
-        red[(r0 + lane / GL) * 4 + w4] = y;
-        red[(NR + r0 + lane / GL) * 4 + w4] = z;
-      }
-    }
-    if (tiles > 0) wait(C::PV_DONE, tiles - 1);
-    const bool good = tiles > 0 && ok && *abort_flag == 0;
-    named_barrier(nbar, 128);
-    const bool whole = it.splits == 1;
-    const long long first_part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
-    if (kt < rows_here) {
-      const int r = r0 + kt, out = row_out[r];
-      const float4 l4 = *reinterpret_cast<const float4*>(red + r * 4);
-      const float4 o4 = *reinterpret_cast<const float4*>(red + (NR + r) * 4);
-      const float ref = row_ref[r];
-      float L = l4.x + l4.y + l4.z + l4.w;
-      if (!own_live || !good || ref == kNoRef) L = 0.f;
-      row_add[r] = o4.x + o4.y + o4.z + o4.w;
-      row_inv[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
-      if (!whole) {
-        p.part_m[first_part + out] = L == 0.f ? -INFINITY : ref;
-        p.part_l[first_part + out] = L;
-      } else if (p.lse) {
-        p.lse[(static_cast<long long>(it.b) * p.H + out % p.H) * p.T + own_t] =
-            L == 0.f ? -INFINITY : (ref + __log2f(L)) * 0.69314718055994531f;
-      }
-    }
-    named_barrier(nbar, 128);
-    // (of 64 features: sixteen in each quarter of the lanes)
-    const int m = C::FB == 64 ? 16 * w4 + lane : kt, in8 = feature_at(m & 7);
-    const bool holds = C::FB == 128 || lane < 16;
-    const float unit = in8 & 1 ? 1048576.f : 16777216.f;  // (codes are 2^-24, odd features 2^-20)
-#pragma unroll 1
-    for (int blk = 0; blk < BLKS; ++blk) {
-      const int f = blk * 128 + (m & ~7) + in8;
-#pragma unroll 1
-      for (int g = 0; g < rows_here; g += 16) {
-        uint32_t raw[16];
-        tmem_ld16(lanes + C::TM_O + blk * NR + r0 + g, raw);
-        tmem_ld_wait();
-        if (holds && f < (whole ? p.d : W)) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (g + i >= rows_here) break;
-            const int r = r0 + g + i;
-            const float a = row_inv[r];
-            // (a row without keys: what lies there may be anything)
-            const float o = a != 0.f ? fmaf(__uint_as_float(raw[i]), unit, row_add[r]) * a : 0.f;
-            const long long row = row_out[r];
-            if (whole) static_cast<__nv_bfloat16*>(p.out)[row * p.d + f] = __float2bfloat16_rn(o);
-            else p.part_o[(first_part + row) * W + f] = o;
+          for (int z = 1; z < LPR; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
+          st_shared_v4(base + C::OFF_Q + piece * (NR * 16) + r * 16, pack_f16x2(f[0], f[4]),
+                       pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f), pack_f16x2(f[2], f[6]),
+                       pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f));
+          if (piece == 0) {
+            reinterpret_cast<float*>(factors + r / 2)[r & 1] = scale * sum;
+            *less(r) = 0.f;
+            row_ref[r] = kNoRef;
+            row_out[r] = outs[y];
           }
         }
-        __syncwarp();
+        if (tid < NR * 4) masks[tid >> 2][tid & 3] = bits;
+        fence_proxy_async_smem();
+        warp_arrive(bar(C::Q_FULL), lane);
+        named_barrier(8, 32 * C::SOFT);
       }
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4) << 16);
+      float l[RPT], ofs[RPT];
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) l[r] = ofs[r] = 0.f;
+      bool ok = true, pending = true;  // a row has no reference yet
+      auto wait = [&](int id, int parity) {
+        ok = warp_wait(bar(id), parity & 1, abort_flag, site(id)) && ok;
+        tc_fence_after();
+      };
+      // Products of tile t, whose scores or the next tile's have been waited for: those of tile t - 2,
+      // on the same barrier, were done before.
+      auto products = [&](int t) {
+        if (t >= 0) wait(C::PV_DONE + (t & 1), t >> 1);
+      };
+      // a live row of this thread to look after
+      int own_t = -1;
+      const bool own_live = kt < rows_here && out_row(r0 + kt, &own_t) >= 0 && own_t < it.live;
+      uint2 kv = words.get(0, first);
+#pragma unroll 1
+      for (int t = 0; t < tiles; ++t) {
+        const int tile0 = first + t * kKeys;
+        KeyFactors mine_f = key_factors(kv.x, kv.y);
+        wait(C::S_FULL + (t & 1), t >> 1);
+        float x[RPT], u[RPT];
+        {
+          uint32_t raw[RPT];
+          if constexpr (RPT == 32) tmem_ld32(lanes + C::TM_S + (t & 1) * NR + r0, raw);
+          else tmem_ld16(lanes + C::TM_S + (t & 1) * NR + r0, raw);
+          // (beside the load: what offsets and references add)
+#pragma unroll
+          for (int r = 0; r < RPT; r += 2) {
+            const float4 f = factors[(r0 + r) / 2];
+            add2(u[r], u[r + 1], f.z, f.w, mine_f.v_log, mine_f.v_log);
+            fma2(u[r], u[r + 1], f.x, f.y, mine_f.lo, mine_f.lo, u[r], u[r + 1]);
+          }
+          const float a = scale * mine_f.step * 16777216.f;  // (codes are 2^-24)
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < RPT; r += 2)
+            fma2(x[r], x[r + 1], __uint_as_float(raw[r]), __uint_as_float(raw[r + 1]), a, a, u[r], u[r + 1]);
+        }
+        float top = -INFINITY;
+        if (tile0 + kKeys > min(it.n, stop)) {
+          const int key = tile0 + kt, off = key - it.n;
+          bool any = false;
+#pragma unroll
+          for (int r = 0; r < RPT; ++r) {
+            bool sees = key < stop;
+            if (sees && off >= 0) sees = (masks[r0 + r][off >> 6] >> (off & 63)) & 1;  // (off < 256: drafted tokens end there)
+            if (!sees) x[r] = -INFINITY;
+            any = any || sees;
+          }
+          // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
+          if (!any) mine_f.v_inv = mine_f.v_ofs = 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < RPT; r += 2) top = fmax3(top, x[r], x[r + 1]);
+        if (any_of_128(nbar, pending || top > kLimit)) {
+          // references up to this tile's maxima, what was summed down by as much
+#pragma unroll
+          for (int r = 0; r < RPT; ++r) {
+            const float m = warp_max(x[r]);
+            if (lane == 0) red[(r0 + r) * 4 + w4] = m;
+          }
+          named_barrier(nbar, 128);
+          float ref = 0.f;
+          if (kt < RPT) {
+            const int r = r0 + kt;
+            const float4 m4 = *reinterpret_cast<const float4*>(red + r * 4);
+            const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), old = row_ref[r], sub = -*less(r);
+            ref = m == -INFINITY ? old : fmaxf(old, m + sub - kLift);
+            row_by[r] = old == kNoRef ? 1.f : ex2_approx(old - ref);  // (nothing is summed up yet)
+            const float now = ref == kNoRef ? 0.f : ref;
+            row_down[r] = sub - now;
+            *less(r) = -now;
+            row_ref[r] = ref;
+          }
+          pending = any_of_128(nbar, own_live && ref == kNoRef);
+          products(t - 1);
+#pragma unroll
+          for (int r = 0; r < RPT; ++r) {
+            const float by = row_by[r0 + r];
+            x[r] += row_down[r0 + r];
+            l[r] *= by;
+            ofs[r] *= by;
+          }
+          if (t > 0) {
+#pragma unroll 1
+            for (int blk = 0; blk < BLKS; ++blk)
+#pragma unroll 1
+              for (int g = 0; g < RPT; g += 16) {
+                const uint32_t at = lanes + C::TM_O + blk * NR + r0 + g;
+                uint32_t raw[16];
+                tmem_ld16(at, raw);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) * row_by[r0 + g + i]);
+                tmem_st16(at, raw);
+              }
+            tmem_st_wait();
+          }
+        }
+        kv = words.get(t + 1, tile0 + kKeys);  // (asked for long before; used in the next turn)
+        // weights, eight rows of a key side by side, into the buffer that the products of tile
+        // t - 2 have read: the scores' commit came behind them
+        const uint32_t weights = base + C::OFF_P + (t & 1) * C::P_BYTES + r0 / 8 * (kKeys * 16) + kt * 16;
+#pragma unroll
+        for (int r = 0; r < RPT; r += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int y = r + 2 * i;
+            const float w0 = ex2_approx(x[y]), w1 = ex2_approx(x[y + 1]);
+            fma2(l[y], l[y + 1], w0, w1, mine_f.v_inv, mine_f.v_inv, l[y], l[y + 1]);
+            w[i] = pack_f16x2(w0, w1);
+            // (the offsets with the rounded weights, as the codes have them)
+            fma2(ofs[y], ofs[y + 1], half_lo(w[i]), half_hi(w[i]), mine_f.v_ofs, mine_f.v_ofs, ofs[y], ofs[y + 1]);
+          }
+          st_shared_v4(weights + r / 8 * (kKeys * 16), w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(bar(C::P_FULL + (t & 1)), lane);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // (none is left but where a wait ran out)
+
+      // ---- epilogue: sums over the keys, then O
+      {
+        const float y = warp_sums<RPT>(l, lane), z = warp_sums<RPT>(ofs, lane);
+        constexpr int GL = 32 / RPT;  // lanes that hold a row's sums
+        if (lane % GL == 0) {
+          red[(r0 + lane / GL) * 4 + w4] = y;
+          red[(NR + r0 + lane / GL) * 4 + w4] = z;
+        }
+      }
+      products(tiles - 1);
+      const bool good = tiles > 0 && ok && *abort_flag == 0;
+      named_barrier(nbar, 128);
+      const bool whole = it.splits == 1;
+      const long long first_part = static_cast<long long>(it.part - it.b) * p.T * p.H;  // (rows count from sequence 0)
+      if (kt < rows_here) {
+        const int r = r0 + kt, out = row_out[r];
+        const float4 l4 = *reinterpret_cast<const float4*>(red + r * 4);
+        const float4 o4 = *reinterpret_cast<const float4*>(red + (NR + r) * 4);
+        const float ref = row_ref[r];
+        float L = l4.x + l4.y + l4.z + l4.w;
+        if (!own_live || !good || ref == kNoRef) L = 0.f;
+        row_add[r] = o4.x + o4.y + o4.z + o4.w;
+        row_inv[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
+        if (!whole) {
+          p.part_m[first_part + out] = L == 0.f ? -INFINITY : ref;
+          p.part_l[first_part + out] = L;
+        } else if (p.lse) {
+          p.lse[(static_cast<long long>(it.b) * p.H + out % p.H) * p.T + own_t] =
+              L == 0.f ? -INFINITY : (ref + __log2f(L)) * 0.69314718055994531f;
+        }
+      }
+      named_barrier(nbar, 128);
+      // (of 64 features: sixteen in each quarter of the lanes)
+      const int m = C::FB == 64 ? 16 * w4 + lane : kt, in8 = feature_at(m & 7);
+      const bool holds = C::FB == 128 || lane < 16;
+      const float unit = in8 & 1 ? 1048576.f : 16777216.f;  // (codes are 2^-24, odd features 2^-20)
+#pragma unroll 1
+      for (int blk = 0; blk < BLKS; ++blk) {
+        const int f = blk * 128 + (m & ~7) + in8;
+#pragma unroll 1
+        for (int g = 0; g < rows_here; g += 16) {
+          uint32_t raw[16];
+          tmem_ld16(lanes + C::TM_O + blk * NR + r0 + g, raw);
+          tmem_ld_wait();
+          if (holds && f < (whole ? p.d : W)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (g + i >= rows_here) break;
+              const int r = r0 + g + i;
+              const float a = row_inv[r];
+              // (a row without keys: what lies there may be anything)
+              const float o = a != 0.f ? fmaf(__uint_as_float(raw[i]), unit, row_add[r]) * a : 0.f;
+              const long long row = row_out[r];
+              if (whole) static_cast<__nv_bfloat16*>(p.out)[row * p.d + f] = __float2bfloat16_rn(o);
+              else p.part_o[(first_part + row) * W + f] = o;
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
     }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -539,21 +562,20 @@ __global__ void __launch_bounds__((ManyCfg<W, NR>::THREADS), 1)
   }
 }
 
-template <int W, int NR>
+template <class C>
 cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
-  using C = ManyCfg<W, NR>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static bool attr_set[64] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(rows_q4_many_kernel<W, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(rows_q4_many_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const dim3 grid(static_cast<unsigned>(p.B * p.units * p.n_splits));
-  e = launch_serialized(rows_q4_many_kernel<W, NR>, grid, dim3(C::THREADS), C::SMEM, stream, p);
+  e = launch_serialized(rows_q4_many_kernel<C>, grid, dim3(C::THREADS), C::SMEM, stream, p);
   if (info) {
     info->kernels = 1;
     info->grid = static_cast<int>(grid.x);
@@ -563,15 +585,38 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
   return e;
 }
 
+// Calls f with the kernel's configuration for R rows per key head of d features.
+template <typename F>
+void with_many(int d, int R, F&& f) {
+  if (d <= 64) {
+    if (R <= 32) f(ManyCfg<64, 32, 16, 2, 6, 2>{});
+    else f(ManyCfg<64, 64, 32, 2, 8, 1>{});
+  } else if (d <= 128) {
+    if (R <= 32) f(ManyCfg<128, 32, 16, 1, 4, 2>{});
+    else f(ManyCfg<128, 64, 32, 2, 8, 1>{});
+  } else {
+    if (R <= 32) f(ManyCfg<256, 32, 16, 3, 4, 1>{});
+    else f(ManyCfg<256, 64, 32, 3, 3, 1>{});
+  }
+}
+
 }  // namespace
 
-int rows_q4_many_rows(int R) { return R <= 32 ? 32 : 64; }
+RowsQ4Shape rows_q4_many_shape(int d, int R) {
+  RowsQ4Shape s = {};
+  with_many(d, R, [&](auto cfg) {
+    using C = decltype(cfg);
+    s.width = C::W;
+    s.rows = C::NR;
+    s.ctas = C::CTAS;
+  });
+  return s;
+}
 
 cudaError_t launch_rows_q4_many(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
-  const bool few = rows_q4_many_rows(p.T * p.G) == 32;
-  if (p.d <= 64) return few ? launch_cfg<64, 32>(p, stream, info) : launch_cfg<64, 64>(p, stream, info);
-  if (p.d <= 128) return few ? launch_cfg<128, 32>(p, stream, info) : launch_cfg<128, 64>(p, stream, info);
-  return few ? launch_cfg<256, 32>(p, stream, info) : launch_cfg<256, 64>(p, stream, info);
+  cudaError_t e = cudaSuccess;
+  with_many(p.d, p.T * p.G, [&](auto cfg) { e = launch_cfg<decltype(cfg)>(p, stream, info); });
+  return e;
 }
 
 }  // namespace mha

@@ -156,7 +156,7 @@ struct Loader {
 };
 
 // More than sixteen rows per key head (mha_rows_q4_many.cu).
-int rows_q4_many_rows(int R);  // of a unit
+RowsQ4Shape rows_q4_many_shape(int d, int R);
 cudaError_t launch_rows_q4_many(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
 
 }  // namespace mha

@@ -44,11 +44,11 @@ struct ManyCfg {
   static constexpr int OFF_BAR = OFF_RED + NR * 32;
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR, OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
-  static constexpr int SOFT = 4 * WGS, UNPACK = 4;       // warps; behind them MMA, loads, two without work
-  static constexpr int THREADS = 32 * (SOFT + UNPACK + 4);
+  static constexpr int SOFT = 4 * WGS, UNPACK = 4;       // warps (for keys, and for values); behind them MMA, loads, two without work
+  static constexpr int THREADS = 32 * (SOFT + 2 * UNPACK + 4);
   // registers: the softmax warps take from the others
-  static constexpr int REGS = 65536 / CTAS / THREADS / 8 * 8, REGS_OTHER = REGS > 100 ? 88 : 48;
-  static constexpr int REGS_SOFT = (REGS * THREADS - REGS_OTHER * 256) / (32 * SOFT) / 8 * 8;
+  static constexpr int REGS = 65536 / CTAS / THREADS / 8 * 8, REGS_OTHER = 48;
+  static constexpr int REGS_SOFT = (REGS * THREADS - REGS_OTHER * (THREADS - 32 * SOFT)) / (32 * SOFT) / 8 * 8;
   static_assert(SMEM <= (CTAS == 2 ? 115712 : 232448) && OFF_BAR % 8 == 0 && OFF_MASKS % 16 == 0, "shared memory");
 };
 
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  constexpr int kMmaWarp = C::SOFT + C::UNPACK, kLoadWarp = kMmaWarp + 1;
+  constexpr int kMmaWarp = C::SOFT + 2 * C::UNPACK, kLoadWarp = kMmaWarp + 1;
   if (tid == 0) {
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(bar(C::FULL + s), 1);
@@ -148,52 +148,59 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
-      // ---- S(0), S(1), PV(0), S(2), PV(1), ...
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = idesc_f16_f32(128, NR, false, false);
-        constexpr uint32_t idesc_o = idesc_f16_f32(C::FB, NR, true, true);
-        const uint64_t dq = smem_desc_plain(base + C::OFF_Q, NR * 16, 128);
-        const uint64_t dv = smem_desc_sw128(base, C::CHUNK, 1024);
-        const uint64_t dp = smem_desc_plain(base + C::OFF_P, 128, kKeys * 16);
-        const int n_ks = (p.d + 15) / 16;
-        bool ok = true;
-        auto wait = [&](int id, int parity) {
-          ok = ok && thread_wait(bar(id), parity & 1, abort_flag, site(id));
-          tc_fence_after();
-          return ok;
-        };
-        if (tiles > 0) wait(C::Q_FULL, 0);
-        for (int t = 0; t <= tiles && tiles > 0 && ok; ++t) {
-          if (t < tiles) {
-            // (the scores of tile t - 2 are read: its weights were there for its values' products)
-            const int st = t % C::KST;
-            if (!wait(C::K_FULL + st, t / C::KST)) break;
-            const uint32_t d = tmem + C::TM_S + (t & 1) * NR, a = tmem + C::TM_K + st * (W / 2);
-            for (int k = 0; k < n_ks; ++k)
+      // ---- S(0), S(1), PV(0), S(2), PV(1), ...: the warp runs together, so that descriptors stay in
+      // uniform registers, and one lane issues (all of it by one lane: 150 cycles an MMA)
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, NR, false, false);
+      constexpr uint32_t idesc_o = idesc_f16_f32(C::FB, NR, true, true);
+      const uint64_t dq = smem_desc_plain(base + C::OFF_Q, NR * 16, 128);
+      const uint64_t dv = smem_desc_sw128(base, C::CHUNK, 1024);
+      const uint64_t dp = smem_desc_plain(base + C::OFF_P, 128, kKeys * 16);
+      bool ok = true;
+      auto wait = [&](int id, int parity) {
+        ok = ok && warp_wait(bar(id), parity & 1, abort_flag, site(id));
+        tc_fence_after();
+        return ok;
+      };
+      if (tiles > 0) wait(C::Q_FULL, 0);
+#pragma unroll 1
+      for (int t = 0; t <= tiles && tiles > 0 && ok; ++t) {
+        if (t < tiles) {
+          // (the scores of tile t - 2 are read: its weights were there for its values' products)
+          const int st = t % C::KST;
+          if (!wait(C::K_FULL + st, t / C::KST)) break;
+          const uint32_t d = tmem + C::TM_S + (t & 1) * NR, a = tmem + C::TM_K + st * (W / 2);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < W / 16; ++k)  // (features past d are 0 on both sides)
               umma_ts(d, a + 8 * k, dq + static_cast<uint64_t>(2 * NR * k), idesc_s, k > 0 ? 1u : 0u);
             umma_commit(bar(C::S_FULL + (t & 1)));
             umma_commit(bar(C::K_EMPTY + st));
           }
-          if (t > 0) {
-            if (!wait(C::P_FULL + ((t - 1) & 1), (t - 1) >> 1)) break;
+          __syncwarp();
+        }
+        if (t > 0) {
+          const int b = (t - 1) & 1;
+          if (!wait(C::P_FULL + b, (t - 1) >> 1)) break;
 #pragma unroll
-            for (int blk = 0; blk < BLKS; ++blk) {
-              const int x = (t - 1) * BLKS + blk, st = x % C::VST;
-              if (!wait(C::V_FULL + st, x / C::VST)) break;
-              const uint64_t a = dv + static_cast<uint64_t>((st * C::VBYTES) >> 4);
+          for (int blk = 0; blk < BLKS; ++blk) {
+            const int x = (t - 1) * BLKS + blk, st = x % C::VST;
+            if (!wait(C::V_FULL + st, x / C::VST)) break;
+            const uint64_t a = dv + static_cast<uint64_t>((st * C::VBYTES) >> 4);
+            const uint64_t w = dp + static_cast<uint64_t>((b * C::P_BYTES) >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
                 umma_ss(tmem + C::TM_O + blk * NR, a + static_cast<uint64_t>((k * 2048) >> 4),
-                        dp + static_cast<uint64_t>((((t - 1) & 1) * C::P_BYTES + k * 256) >> 4), idesc_o, (t > 1 || k > 0) ? 1u : 0u);
+                        w + static_cast<uint64_t>((k * 256) >> 4), idesc_o, (t > 1 || k > 0) ? 1u : 0u);
               umma_commit(bar(C::V_EMPTY + st));
+              if (blk == BLKS - 1) umma_commit(bar(C::PV_DONE + b));
             }
-            if (!ok) break;
-            umma_commit(bar(C::PV_DONE + ((t - 1) & 1)));
+            __syncwarp();
           }
         }
-        // every tensor-core operation issued must be complete before TMEM is freed
-        umma_commit(bar(C::DRAIN));
       }
+      // every tensor-core operation issued must be complete before TMEM is freed
+      if (elect_one()) umma_commit(bar(C::DRAIN));
       __syncwarp();
       volatile int never = 0;
       mbar_wait(bar(C::DRAIN), 0, &never, p.status, site(C::DRAIN));
@@ -203,13 +210,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
       const uint32_t packed = base + C::OFF_RING + key * C::ROW;
       const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       bool ok = true;
-      int x = 0;
       auto wait = [&](int id, int parity) {
         ok = ok && warp_wait(bar(id), parity & 1, abort_flag, site(id));
         return ok;
       };
       auto words = [&](int slot, int c) { return ld_shared_v4(packed + slot * C::TILE + 16 * (c ^ swizzle<W>(key))); };
       auto keys = [&](int t) {
+        const int x = t == 0 ? 0 : 2 * t - 1;
         const int slot = x % C::SLOTS, st = t % C::KST;
         if (!wait(C::FULL + slot, x / C::SLOTS)) return;
         if (t >= C::KST && !wait(C::K_EMPTY + st, t / C::KST - 1)) return;
@@ -228,9 +235,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(bar(C::K_FULL + st), lane);
-        ++x;
       };
       auto values = [&](int t) {
+        const int x = t + 1 < tiles ? 2 * t + 2 : 2 * t + 1;
         const int slot = x % C::SLOTS;
         if (!wait(C::FULL + slot, x / C::SLOTS)) return;
 #pragma unroll
@@ -254,12 +261,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
           if (blk == BLKS - 1) warp_arrive(bar(C::EMPTY + slot), lane);
           warp_arrive(bar(C::V_FULL + st), lane);
         }
-        ++x;
       };
-      if (tiles > 0) keys(0);
-      for (int t = 0; t < tiles && ok; ++t) {
-        if (t + 1 < tiles) keys(t + 1);
-        if (ok) values(t);
+      if (warp < C::SOFT + C::UNPACK) {
+        for (int t = 0; t < tiles && ok; ++t) keys(t);
+      } else {
+        for (int t = 0; t < tiles && ok; ++t) values(t);
       }
     }
   } else {
@@ -589,10 +595,10 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
 template <typename F>
 void with_many(int d, int R, F&& f) {
   if (d <= 64) {
-    if (R <= 32) f(ManyCfg<64, 32, 16, 2, 6, 2>{});
+    if (R <= 32) f(ManyCfg<64, 32, 16, 2, 8, 1>{});
     else f(ManyCfg<64, 64, 32, 2, 8, 1>{});
   } else if (d <= 128) {
-    if (R <= 32) f(ManyCfg<128, 32, 16, 1, 4, 2>{});
+    if (R <= 32) f(ManyCfg<128, 32, 16, 2, 8, 1>{});
     else f(ManyCfg<128, 64, 32, 2, 8, 1>{});
   } else {
     if (R <= 32) f(ManyCfg<256, 32, 16, 3, 4, 1>{});

@@ -45,7 +45,8 @@ namespace {
 
 constexpr int kTile = 32;           // keys of a warp's part of a tile of kKeys
 constexpr int kRoleRowsQ4 = 20;
-constexpr int kFewRows = 16;  // more go to the other kernel
+// Rows per key head up to which a step is this file's.
+constexpr int few_rows(int d) { return d <= 64 ? 32 : 16; }
 
 // D += A B, 16 x 16 by 16 x 8 in fp16, ...
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -653,7 +654,7 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
 }  // namespace
 
 RowsQ4Shape rows_q4_shape(int d, int R) {
-  if (R > kFewRows) return rows_q4_many_shape(d, R);
+  if (R > few_rows(d)) return rows_q4_many_shape(d, R);
   RowsQ4Shape s = {};
   with_config(d, R, [&](auto cfg) {
     using C = decltype(cfg);
@@ -665,7 +666,7 @@ RowsQ4Shape rows_q4_shape(int d, int R) {
 }
 
 cudaError_t launch_rows_q4(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {
-  if (p.T * p.G > kFewRows) return launch_rows_q4_many(p, stream, info);
+  if (p.T * p.G > few_rows(p.d)) return launch_rows_q4_many(p, stream, info);
   cudaError_t e = cudaSuccess;
   with_config(p.d, p.T * p.G, [&](auto cfg) { e = launch_cfg<decltype(cfg)>(p, stream, info); });
   return e;

@@ -595,11 +595,10 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
 template <typename F>
 void with_many(int d, int R, F&& f) {
   if (d <= 64) {
-    if (R <= 32) f(ManyCfg<64, 32, 16, 2, 8, 1>{});
-    else f(ManyCfg<64, 64, 32, 2, 8, 1>{});
+    f(ManyCfg<64, 64, 16, 2, 8, 1>{});
   } else if (d <= 128) {
     if (R <= 32) f(ManyCfg<128, 32, 16, 2, 8, 1>{});
-    else f(ManyCfg<128, 64, 32, 2, 8, 1>{});
+    else f(ManyCfg<128, 64, 16, 2, 8, 1>{});
   } else {
     if (R <= 32) f(ManyCfg<256, 32, 16, 3, 4, 1>{});
     else f(ManyCfg<256, 64, 32, 3, 3, 1>{});

@@ -41,13 +41,14 @@ struct ManyCfg {
   static constexpr int Q_FULL = V_EMPTY + VST, S_FULL = Q_FULL + 1;  // + tile & 1
   static constexpr int P_FULL = S_FULL + 2, PV_DONE = P_FULL + 2,  // + tile & 1
                         DRAIN = PV_DONE + 2, NBAR = DRAIN + 1;
-  static constexpr int OFF_BAR = OFF_RED + NR * 32;
+  static constexpr int OFF_UNIT = OFF_RED + NR * 32;
+  static constexpr int OFF_BAR = OFF_UNIT + static_cast<int>(sizeof(Unit));
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR, OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
   static constexpr int SOFT = 4 * WGS, UNPACK = 4;       // warps (for keys, and for values); behind them MMA, loads, two without work
   static constexpr int THREADS = 32 * (SOFT + 2 * UNPACK + 4);
   // registers: the softmax warps take from the others
-  static constexpr int REGS = 65536 / CTAS / THREADS / 8 * 8, REGS_OTHER = 48;
+  static constexpr int REGS = 65536 / CTAS / THREADS / 8 * 8, REGS_OTHER = WGS == 4 ? 40 : 56;
   static constexpr int REGS_SOFT = (REGS * THREADS - REGS_OTHER * (THREADS - 32 * SOFT)) / (32 * SOFT) / 8 * 8;
   static_assert(SMEM <= (CTAS == 2 ? 115712 : 232448) && OFF_BAR % 8 == 0 && OFF_MASKS % 16 == 0, "shared memory");
 };
@@ -111,16 +112,24 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
     tmem_relinquish();
     tc_fence_before();
   }
+  griddep_wait();
+  // (one warp finds the unit: all 28 at it were 1,500 cycles of each other's instructions)
+  const int n_rows = p.T * p.G;
+  Unit* unit = reinterpret_cast<Unit*>(smem + C::OFF_UNIT);
+  if (warp == 0) {
+    Unit u = {};
+    const bool has = this_unit(p, (n_rows + NR - 1) / NR, kSms * C::CTAS, lane, &u);
+    u.pad[0] = has;
+    if (lane == 0) *unit = u;
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_wait();
   // (the next launch's CTAs take tensor memory too: only now that this one has its own)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int n_rows = p.T * p.G;
-  Unit it = {};
-  const bool mine = this_unit(p, (n_rows + NR - 1) / NR, kSms * C::CTAS, lane, &it);
+  const Unit it = *unit;
+  const bool mine = it.pad[0] != 0;
   const int first = it.t0 * kKeys, stop = mine ? min(it.t1 * kKeys, it.end) : 0;
   const int tiles = stop > first ? (stop - first + kKeys - 1) / kKeys : 0;
   auto site = [&](int id) { return kRoleMany * 64 + id; };
@@ -598,7 +607,7 @@ void with_many(int d, int R, F&& f) {
     f(ManyCfg<64, 64, 16, 2, 8, 1>{});
   } else if (d <= 128) {
     if (R <= 32) f(ManyCfg<128, 32, 16, 2, 8, 1>{});
-    else f(ManyCfg<128, 64, 16, 2, 8, 1>{});
+    else f(ManyCfg<128, 64, 32, 2, 8, 1>{});
   } else {
     if (R <= 32) f(ManyCfg<256, 32, 16, 3, 4, 1>{});
     else f(ManyCfg<256, 64, 32, 3, 3, 1>{});

@@ -119,39 +119,61 @@ __global__ void __launch_bounds__(kThreads, kForkBlocks) cache_fork_kernel(const
   // (a thread writes what it copied; the barrier is for the others' rows).
   const uint32_t slots = smem_u32(held) + 16 * threadIdx.x;
   const int m0 = static_cast<int>(threadIdx.x) >> lg, step = kThreads >> lg;
-  auto columns = [&](long long x, int* j) {
-    const int c = x >= chunks;
-    const long long q = ((c ? x - chunks : x) << lg) + own;  // from position lo on
-    *j = q < span * pieces ? lo + static_cast<int>(q / pieces) : -1;
-    return reinterpret_cast<uint4*>(p.codes[c]) + lo * pieces + q;
+  // The thread's column of chunk x: piece r of position j.  From one chunk to the next they
+  // are added to (a division each, twice, was a third of the instructions).
+  const int per_row = static_cast<int>(pieces);
+  const long long hop = static_cast<long long>(gridDim.x) << lg;
+  const long long hop_j = hop / pieces;
+  const int hop_r = static_cast<int>(hop - hop_j * pieces);
+  long long x = blockIdx.x, j = -1;
+  int r = 0, c = -1;
+  auto locate = [&]() {  // (x is in keys or values for the first time)
+    c = x >= chunks;
+    const long long q = ((c ? x - chunks : x) << lg) + own;
+    j = q / pieces;
+    r = static_cast<int>(q - j * pieces);
   };
-  auto copy = [&](long long x, int buffer) {
+  auto copy = [&](int buffer) {
+    uint4* column = nullptr;
     if (x < 2 * chunks) {
-      int j;
-      const uint4* column = columns(x, &j);
+      column = reinterpret_cast<uint4*>(p.codes[c]) + (lo + j) * pieces + r;
+      const int at = j < span ? lo + static_cast<int>(j) : -1;
       uint32_t to = slots + buffer * (16 * kForkItems);
       for (int i = m0; i < n; i += step, to += 16 * kThreads) {
         const Move m = moves[i];
-        if (j >= m.first && j < m.end)
+        if (at >= m.first && at < m.end)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(column + m.from * seq) : "memory");
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    return column;
   };
-  copy(blockIdx.x, 0);
+  locate();
+  uint4* column = copy(0);
   int buffer = 0;
-  long long x = blockIdx.x;
-  for (; x < 2 * chunks; x += gridDim.x, buffer ^= 1) {
-    copy(x + gridDim.x, buffer ^ 1);
+  while (x < 2 * chunks) {
+    const int at = j < span ? lo + static_cast<int>(j) : -1;
+    x += gridDim.x;
+    if (c == 0 && x >= chunks) {
+      locate();
+    } else {
+      j += hop_j;
+      r += hop_r;
+      if (r >= per_row) {
+        r -= per_row;
+        ++j;
+      }
+    }
+    uint4* next = copy(buffer ^ 1);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
-    int j;
-    uint4* column = columns(x, &j);
     const uint4* from = reinterpret_cast<const uint4*>(held) + buffer * kForkItems + threadIdx.x;
     for (int i = m0; i < n; i += step, from += kThreads) {
       const Move m = moves[i];
-      if (j >= m.first && j < m.end) column[m.to * seq] = *from;
+      if (at >= m.first && at < m.end) column[m.to * seq] = *from;
     }
+    column = next;
+    buffer ^= 1;
   }
   for (; x < 2 * (chunks + scale_chunks); x += gridDim.x) {
     const long long y = x - 2 * chunks;

@@ -611,9 +611,9 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
 template <typename F>
 void with_config(int d, int R, F&& f) {
   if (d <= 64) {
-    if (R == 1) f(Q4Cfg<64, 1, 4, 6>{});
-    else if (R == 2) f(Q4Cfg<64, 2, 4, 6>{});
-    else if (R <= 8) f(Q4Cfg<64, 8, 4, 4>{});
+    if (R == 1) f(Q4Cfg<64, 1, 3, 7>{});
+    else if (R == 2) f(Q4Cfg<64, 2, 3, 7>{});
+    else if (R <= 8) f(Q4Cfg<64, 8, 2, 5>{});
     else f(Q4Cfg<64, 16, 4, 3>{});
   } else if (d <= 128) {
     if (R == 1) f(Q4Cfg<128, 1, 3, 4>{});
@@ -623,7 +623,7 @@ void with_config(int d, int R, F&& f) {
   } else {
     if (R == 1) f(Q4Cfg<256, 1, 2, 3>{});
     else if (R == 2) f(Q4Cfg<256, 2, 2, 3>{});
-    else if (R <= 8) f(Q4Cfg<256, 8, 2, 3>{});
+    else if (R <= 8) f(Q4Cfg<256, 8, 3, 2>{});
     else f(Q4Cfg<256, 16, 3, 2>{});
   }
 }

@@ -11,15 +11,16 @@
 // one's source may be another's destination.  A fork keeps positions and a
 // compaction keeps sequences, so the byte columns of a cache (one piece of 16 bytes of
 // a row, over the sequences or over a sequence's accepted tokens) are independent: a
-// block takes a column's moves together, reads all their sources into
-// registers, waits for its threads, and writes.  No second buffer, no order, one launch
-// for keys, values and scales.
+// block takes a column's moves together, has all their sources in shared memory (a fork) or
+// registers (a compaction) and its threads at a barrier before it writes one of them.  No
+// second buffer, no order, one launch for keys, values and scales.
 //
 // Bound by memory: a fork reads every source row and writes every moved one, a block with
-// two buffers of 32 KB (8-bit, 4 x 4 beams of 96 heads, 280 MB: 57 us, 4.9 TB/s; three
-// blocks to an SM; smaller buffers move shorter runs of each row: 16 KB with four blocks 69
-// us, with six 81; eight elements in each thread's registers 81).  A compaction moves a few
-// rows: its time, 2 us, is that of a launch and of two dependent reads.
+// two buffers of 32 KB (8-bit, 4 x 4 beams of 96 heads, 280 MB: 53 us, 5.3 TB/s; three
+// blocks to an SM; with smaller buffers, which move shorter runs of each row, 16 KB with
+// four blocks 69 us, with six 81, when 32 KB took 57; eight elements in each thread's
+// registers 81).  A compaction moves a few rows: its time, 2 us, is that of a launch and of
+// two dependent reads.
 #include "kernels.h"
 
 namespace mha {

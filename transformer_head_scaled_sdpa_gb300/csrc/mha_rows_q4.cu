@@ -1,6 +1,6 @@
 // mha_rows_q4.cu -- attention of a few query rows per sequence over the 4-bit
-// key/value cache (the decode step and the step of a tree of drafted tokens),
-// sm_103a.
+// key/value cache (the decode step and the step of a tree of drafted tokens), up to
+// sixteen rows per key head (32 of heads up to 64 features), sm_103a.
 //
 // A cached row of a key head is x = lo + step * c with codes c = 0 .. 15 (q4.cuh), so
 //   s_jr = scale q_r . k_j = scale (stepk_j (q_r . c_j) + lok_j sum_f q_rf)
@@ -10,32 +10,40 @@
 // products take w, the denominator adds w / stepv, the offsets' share of the output is
 // the row's sum of w lov / stepv.
 //
-// The codes go from global memory to registers and from there to the tensor core as
-// they lie: four bits in the low bits of an fp16 are the subnormal c 2^-24, exact, so
-// unpacking is a mask (one per two codes, and a shift per eight; the odd nibbles stay 16
-// times too large, and q, or the output, is divided by 16 there).  Each lane loads the
-// part of a row that its fragment wants:
-//   S^T [16 keys x 8 rows] = K [16 x d] Q^T: lane (g, j) of a warp has the j-th quarter
-//     of the rows of keys g and g + 8; the order of the features along the reduction
-//     is free, and Q is laid out in the same one.
-//   O^T [16 features x 8 rows] += V^T [16 x 16 keys] P^T: lane (g, j) has the g-th
-//     eighth of the rows of keys 2j, 2j + 1, 2j + 8, 2j + 9; two keys' bytes are brought
-//     together by one byte permutation, and their low and high nibbles are the
-//     fragment's two features.
-// The weights' fragment is the scores' transposed (movmatrix).  Nothing passes through
-// shared memory but the four warps' merge at the end of a unit, and no warp waits for
-// another before that.
+// Codes reach the tensor core as they lie: four bits in the low bits of an fp16 are the
+// subnormal c 2^-24, exact, so unpacking is a mask (one per two codes, and a shift per
+// eight; the odd nibbles stay 16 times too large, and q, or the output, is divided by 16
+// there).  A CTA is four warps and a ring of tiles of 128 keys and values, filled by TMA;
+// a warp has 32 keys of a tile, with sums and references of its own, and the four meet
+// once, at the end of the unit.  The last warp to leave a stage refills it.
+//   S^T [16 keys x 8 rows] = K [16 x d] Q^T: ldmatrix gives lane (g, j) bytes 4 j .. of 16
+//     of a key's row; the order of the features along the reduction is free, and Q is laid
+//     out in the same one.
+//   O^T [16 features x 8 rows] += V^T [16 x 16 keys] P^T: ldmatrix.trans gives a lane 16
+//     bits (four features) of two keys, whose nibbles are the fragment's features.
+// The weights' fragment is the scores' transposed (movmatrix).  One or two rows fill the
+// eight columns with copies, so that every column pair has all the scores and each lane
+// computes the weights of one key.
 //
-// mma.sync and not tcgen05: reading the cache bounds a step of a few rows (68 bytes per
-// row of 128 features), and tcgen05's operands lie in shared memory in 8 bits or more:
-// copying the packed tile there, reading it, writing the unpacked tile and reading that
-// are 6 bytes of shared-memory traffic per cached byte, at the rate of HBM more than
-// the 128 bytes a clock that an SM has.
+// mma.sync and not tcgen05 for these few rows: reading the cache bounds them (68 bytes per
+// row of 128 features), and tcgen05 wants the codes in 8 bits or more, in shared or tensor
+// memory: the packed tile written and read, the unpacked one written and read, and a CTA
+// of a dozen warps that hand it on; with it, 4 x 96 heads x 16 rows take 50 us against
+// 34.7 (8 x 48 heads x 16 rows of 64 features x 2,048 to 4,096 keys 77 against 42).  fp8 operands bring nothing here
+// (mma.sync converts e4m3 to fp16 first on this machine).
 //
 // q is scaled by a power of two to [2^14, 2^15) at its row's largest and then exact in
 // fp16 (to 2^-40 of that); the weights are rounded to fp16 (2^-11 relative); products,
-// the denominator and the offsets' sums are float32.  The reference m of a row moves when a
-// tile's largest weight passes it by more than 2^kSlack.
+// the denominator and the offsets' sums are float32.  Weights are 2^kLift at a row's
+// reference m, which moves when a tile's largest weight would pass 2^kLimit.
+//
+// What bounds it: 16 x 96 heads x 1,024 to 2,048 keys of 128 features, 322 MB, 61 us (5.3
+// TB/s; the same launch without the arithmetic 53): 1,536 units on 608 CTAs, each of which
+// waits 4 to 5 us for its lengths, Q and first tile and for its merge, and 0.46 of the
+// issue slots (the masks' and shifts' pipe 0.35, the tensor pipe 0.29).  2 x 8 key heads x
+// 40,001 to 65,537 keys, 4 rows: 30 us, 7 of them latency at both ends and 5 the merge of
+// splits.  4 x 96 heads x 16 rows x 1,024 to 2,048 keys: 34.7 us, one wave of 384 units on
+// 456 CTAs as long as its longest.  128 x 8 heads x 16 to 256 keys of 64 features: 8 us.
 #include <cuda_bf16.h>
 
 #include "rows_q4.cuh"
@@ -178,8 +186,6 @@ __device__ __forceinline__ uint32_t arrive_count(uint32_t at) {
 }
 
 // ---------------------------------------------------------------------------
-// Up to sixteen rows: of every tile of 128 keys a warp has 32, with sums and references
-// of its own; no warp waits for another.
 // W: widest head; ROWS: 1, 2 or a multiple of 8; ST: stages of the ring; CTAS: per SM.
 // ---------------------------------------------------------------------------
 template <int W_, int ROWS_, int ST_, int CTAS_>
@@ -607,7 +613,20 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
   }
 }
 
-// Calls f with the kernel's configuration for R rows per key head of d features.
+// Calls f with the kernel's configuration for R rows per key head of d features.  us over
+// 8 sequences of 2,048 to 4,096 keys, 48 heads of 64 features, 24 of 128 or 12 of 256:
+// as here, in a unit for twice the rows or more, and in units for fewer:
+//   rows     64                128               256
+//    1       28.9 30.3         22.7 23.6         23.4 23.6
+//    2       29.4 33.7 47.9    23.5 25.1 42.6    23.6 24.6 39.2
+//    8       33.7 41.5 77.1    25.7 38.0 62.6    25.6 31.3 59.4
+//   16       42.2 77.2 53.1    37.9 45.4 49.5    32.9 49.4 44.1   (wider: the other kernel)
+//   32       65.4 77.5         45.8      59.3    50.1      67.1   (128, 256: the other kernel)
+// Stages and CTAs to an SM were swept with them.  More CTAs hide the ends of units, more
+// stages the memory: one row of 64 features over 128 x 8 heads x 16 to 256 keys 8.0 us with
+// seven CTAs of three stages, 10.6 with six of four, 9.7 with ten of two; eight rows of 64
+// 33.7 with five CTAs of two stages, 37.1 with four of four; of 256 25.6 with two CTAs of
+// three stages, 32.4 with three of two.
 template <typename F>
 void with_config(int d, int R, F&& f) {
   if (d <= 64) {

@@ -1,5 +1,42 @@
-// mha_rows_q4_many.cu -- attention of more than sixteen query rows per key head over the
-// 4-bit cache, on the 5th-generation tensor cores, sm_103a.
+// mha_rows_q4_many.cu -- attention of many query rows per key head over the 4-bit
+// key/value cache, on the 5th-generation tensor cores, sm_103a: more than sixteen rows
+// (32 of heads up to 64 features); fewer are mha_rows_q4.cu's, whose formulas these are.
+//
+// With rows enough, arithmetic bounds the step, and both products go to tcgen05, keys (then
+// features) along the 128 rows of its tile and the query rows along its columns:
+//   S^T [128 keys x NR] = K Q^T       A: K in tensor memory, a lane per key
+//   O^T [features x NR] += V^T P^T    A: V in shared memory, read transposed; B: weights
+// Codes become fp16 subnormals (c 2^-24, exact; odd ones 16 times too large) on the way
+// there: a thread has a key, takes its packed row from the ring that TMA fills, masks and
+// shifts, and writes keys to tensor memory (tcgen05.st) and values to shared memory in the
+// layout that a 128-byte swizzled TMA tile would have.  A word's eight codes come out in
+// the order 0 4 1 5 2 6 3 7; Q is laid out in it, and the output's rows are read in it.
+// In tensor memory K costs neither shared memory's room nor its bandwidth; V, whose rows
+// are keys and whose lanes would have to be features, would need a transposition there.
+//
+// Softmax: a thread has a key, that is its offset and step, and RPT of the rows; what a
+// row needs (the factor of its sum, its reference) is read by all lanes at once.  Rows of a
+// unit share a power of two in Q, so that a score is one product and one addition beside
+// its offset's; what that costs a row smaller than the unit's largest is 2^-25 of the
+// largest row's scores.  Weights are rounded to fp16 (2^-11 relative); sums, scores and
+// products are float32; the denominator and the offsets' sum stay in a thread's registers
+// until the unit ends.  References move for all keys of a tile, by a vote of the
+// warpgroup, when a weight would pass 2^kLimit; O is then scaled in tensor memory.
+//
+// Roles: softmax warps (8, or 16), four warps that unpack keys, four that unpack values
+// (one group for both: 58 us against 49, 8 x 12 heads x 32 rows of 256 features x 2,048 to
+// 4,096 keys), one that issues the MMAs, one that loads.  Scores and weights have two
+// buffers each, S(t + 1) is formed before PV(t).  The MMA warp runs converged and elects a
+// lane to issue, which keeps descriptors in uniform registers: issued by one lane on its own
+// an MMA took 150 cycles (32 rows of 128 features 64 us against 45).
+//
+// What bounds it: the softmax warps, 1,900 to 2,400 cycles a tile (scores read and scaled
+// 900, vote and waits 500, weights 450), with one CTA to an SM, and 15 to 20 thousand
+// cycles that a unit costs beside its tiles (its lengths 2,600, Q 4,500, first tile 5,000,
+// sums and outputs 5,000).  5 x 2 key heads x 56 rows of 256 features x 7,001 to 20,000
+// keys: 32.4 us (5 of them the merge of splits), 47 on mma.sync in units of 16 rows; 8 x
+// 24 heads x 56 rows of 128 features x 2,048 to 4,096 keys 68 against 93, 252 rows 230
+// against 334.
 #include <cuda_bf16.h>
 
 #include "rows_q4.cuh"
@@ -600,7 +637,12 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
   return e;
 }
 
-// Calls f with the kernel's configuration for R rows per key head of d features.
+// Calls f with the kernel's configuration for R rows per key head of d features.  Units of 32
+// rows up to 32: they hold half the weights (8 x 24 heads of 128 features x 2,048 to 4,096
+// keys, 32 rows: 46 us, 67 in units of 64).  Units of 64 from there on: each unpacks the
+// tiles once for all of them (56 rows 68 us, in two units of 32 98; 252 rows 229 and 312).
+// 16 or 32 rows to a softmax thread: four or two warpgroups.  64 features: 105 us (56 rows,
+// 48 heads) with 16 and 112 with 32; 128: 95 and 69, where registers do not hold 16 warps'.
 template <typename F>
 void with_many(int d, int R, F&& f) {
   if (d <= 64) {

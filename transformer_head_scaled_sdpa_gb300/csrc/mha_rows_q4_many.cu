@@ -15,10 +15,10 @@
 // are keys and whose lanes would have to be features, would need a transposition there.
 //
 // Softmax: a thread has a key, that is its offset and step, and RPT of the rows; what a
-// row needs (the factor of its sum, its reference) is read by all lanes at once.  Rows of a
-// unit share a power of two in Q, so that a score is one product and one addition beside
-// its offset's; what that costs a row smaller than the unit's largest is 2^-25 of the
-// largest row's scores.  Weights are rounded to fp16 (2^-11 relative); sums, scores and
+// row needs (its factors and reference) is read by all lanes at once.  Rows of like sizes
+// share a power of two in Q, and the factor of their products (8 x 24 heads x 56 rows of 128
+// features x 2,048 to 4,096 keys 69 us, 75 with a factor each); a row that is far larger, or
+// infinite, must not take the others' digits, and then each has its own.  Weights are rounded to fp16 (2^-11 relative); sums, scores and
 // products are float32; the denominator and the offsets' sum stay in a thread's registers
 // until the unit ends.  References move for all keys of a tile, by a vote of the
 // warpgroup, when a weight would pass 2^kLimit; O is then scaled in tensor memory.
@@ -39,6 +39,8 @@
 // against 334.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "rows_q4.cuh"
 
 namespace mha {
@@ -47,9 +49,9 @@ namespace {
 constexpr int kRoleMany = 21;
 
 // W: widest head; NR: rows of a unit.
-template <int W_, int NR_, int RPT_, int VST_, int SLOTS_, int CTAS_>
+template <int W_, int NR_, int RPT_, int VST_, int SLOTS_>
 struct ManyCfg {
-  static constexpr int W = W_, NR = NR_, CTAS = CTAS_;
+  static constexpr int W = W_, NR = NR_;
   static constexpr int ROW = W / 2, TILE = kKeys * ROW;  // packed bytes of a row, of a tile's keys or values
   static constexpr int KC = W / 32;                      // 16-byte pieces of a row
   static constexpr int BLKS = W == 256 ? 2 : 1, FB = W / BLKS;  // blocks of features of the output
@@ -62,14 +64,16 @@ struct ManyCfg {
   static constexpr uint32_t TM_K = 0, TM_S = KST * (W / 2), TM_O = TM_S + 2 * NR;
   static constexpr uint32_t TM_USED = TM_O + BLKS * NR;
   static constexpr uint32_t TMEM_COLS = TM_USED <= 128 ? 128 : (TM_USED <= 256 ? 256 : 512);
-  static_assert(TM_USED <= 512 && TMEM_COLS * CTAS <= 512 && NR % RPT == 0, "tensor memory");
+  static_assert(TM_USED <= 512 && NR % RPT == 0, "tensor memory");
   static constexpr int OFF_RING = VST * VBYTES;
   static constexpr int OFF_Q = OFF_RING + SLOTS * TILE;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
   static constexpr int OFF_SCALES = OFF_P + 2 * P_BYTES;        // a warpgroup's words
   static constexpr int OFF_MASKS = OFF_SCALES + WGS * Scales::BYTES;  // uint64 [NR][4]
-  static constexpr int OFF_FACTORS = OFF_MASKS + NR * 32;       // float4 [NR / 2]: of two rows, the factors of offsets, and what scores are taken less (negative)
-  static constexpr int OFF_ROWS = OFF_FACTORS + NR * 8;         // float [5][NR], int [NR]
+  // float4 [NR / 2]: of two rows, the factors of offsets, and what is added to scores; then
+  // float [NR]: of products
+  static constexpr int OFF_FACTORS = OFF_MASKS + NR * 32;
+  static constexpr int OFF_ROWS = OFF_FACTORS + NR * 12;        // float [5][NR], int [NR]
   static constexpr int OFF_RED = OFF_ROWS + NR * 24;            // float [2][NR][4]
   // barriers
   static constexpr int FULL = 0, EMPTY = SLOTS;          // + slot
@@ -82,12 +86,12 @@ struct ManyCfg {
   static constexpr int OFF_BAR = OFF_UNIT + static_cast<int>(sizeof(Unit));
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR, OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
-  static constexpr int SOFT = 4 * WGS, UNPACK = 4;       // warps (for keys, and for values); behind them MMA, loads, two without work
+  static constexpr int SOFT = 4 * WGS, UNPACK = 4;  // warps (for keys, and for values); then MMA, loads, two idle
   static constexpr int THREADS = 32 * (SOFT + 2 * UNPACK + 4);
   // registers: the softmax warps take from the others
-  static constexpr int REGS = 65536 / CTAS / THREADS / 8 * 8, REGS_OTHER = WGS == 4 ? 40 : 56;
+  static constexpr int REGS = 65536 / THREADS / 8 * 8, REGS_OTHER = WGS == 4 ? 40 : 48;
   static constexpr int REGS_SOFT = (REGS * THREADS - REGS_OTHER * (THREADS - 32 * SOFT)) / (32 * SOFT) / 8 * 8;
-  static_assert(SMEM <= (CTAS == 2 ? 115712 : 232448) && OFF_BAR % 8 == 0 && OFF_MASKS % 16 == 0, "shared memory");
+  static_assert(SMEM <= 232448 && OFF_BAR % 8 == 0 && OFF_MASKS % 16 == 0, "shared memory");
 };
 
 // Instruction descriptor of kind::f16 with fp16 operands (fields as idesc_bf16_f32).
@@ -108,7 +112,7 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t* r) {
 __device__ __forceinline__ int feature_at(int x) { return (x >> 1) + 4 * (x & 1); }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __grid_constant__ RowsParams p) {
   constexpr int W = C::W, NR = C::NR;
   constexpr int KC = C::KC, RPT = C::RPT, BLKS = C::BLKS;
   extern __shared__ uint8_t smem_raw[];
@@ -155,7 +159,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
   Unit* unit = reinterpret_cast<Unit*>(smem + C::OFF_UNIT);
   if (warp == 0) {
     Unit u = {};
-    const bool has = this_unit(p, (n_rows + NR - 1) / NR, kSms * C::CTAS, lane, &u);
+    const bool has = this_unit(p, (n_rows + NR - 1) / NR, kSms, lane, &u);
     u.pad[0] = has;
     if (lane == 0) *unit = u;
   }
@@ -322,6 +326,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
       const int rows_here = min(max(n_rows - it.rb * NR - r0, 0), RPT);
       float4* factors = reinterpret_cast<float4*>(smem + C::OFF_FACTORS);
       auto less = [&](int r) { return reinterpret_cast<float*>(factors + r / 2) + 2 + (r & 1); };
+      float* row_scale = reinterpret_cast<float*>(factors + NR / 2);
       float* row_ref = reinterpret_cast<float*>(smem + C::OFF_ROWS);  // references less kLift
       float* row_by = row_ref + NR;                                   // a move's factors, and differences
       float* row_down = row_by + NR;
@@ -343,7 +348,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
                          reinterpret_cast<const uint32_t*>(p.k_scale) + scales,
                          reinterpret_cast<const uint32_t*>(p.v_scale) + scales, kt, stop};
       words.start(first);
-      float scale;  // of scores: q's and the softmax's
+      constexpr int kNone = 1000;
+      int common = kNone;  // the e of all rows
       {
         // Q: eight features to a lane, W / 8 lanes to a row
         constexpr int LPR = W / 8, RPW = 32 / LPR, PASSES = (NR + C::SOFT * RPW - 1) / (C::SOFT * RPW);
@@ -361,27 +367,41 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
                                                         static_cast<long long>(outs[y]) * p.d + 8 * piece));
         }
         const uint64_t bits = tid < NR * 4 ? mask_word(p, it, tid, out_row) : 0;
-        // q 2^-e with the unit's largest magnitude in [2^14, 2^15): what a smaller row loses is
-        // 2^-25 of the largest row's scores (a NaN is passed over here)
-        float amax = 0.f;
+        // q 2^-e with the row's largest magnitude in [2^14, 2^15); where the unit's rows are within
+        // 2^8 of one another (those of zeros aside) with the largest row's e, and one factor for all:
+        // an fp16 of q is then off by up to 2^-27 of its row's largest
+        int e[PASSES], top = -200, low = 200;
 #pragma unroll
         for (int y = 0; y < PASSES; ++y) {
           const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+          float amax = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
+#pragma unroll
+          for (int z = 1; z < LPR; z <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, z));
+          e[y] = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100);
+          if (amax != 0.f) {
+            top = max(top, e[y]);
+            low = min(low, e[y]);
+          }
         }
-        amax = warp_max(amax);
-        if (lane == 0) red[warp] = amax;
+        top = __reduce_max_sync(0xffffffffu, top);
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (lane == 0) *reinterpret_cast<int2*>(red + 2 * warp) = make_int2(top, low);
         named_barrier(8, 32 * C::SOFT);
 #pragma unroll
-        for (int w = 0; w < C::SOFT; ++w) amax = fmaxf(amax, red[w]);
-        const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100);
-        const float inv = pow2i(-e);
-        scale = pow2i(e) * p.scale_log2;
+        for (int w = 0; w < C::SOFT; ++w) {
+          const int2 z = *reinterpret_cast<const int2*>(red + 2 * w);
+          top = max(top, z.x);
+          low = min(low, z.y);
+        }
+        if (low <= top && top - low <= 8 && top < 114) common = top;  // (114: an infinity)
 #pragma unroll
         for (int y = 0; y < PASSES; ++y) {
           const int r = (y * C::SOFT + warp) * RPW + lane / LPR;
           const uint32_t x[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+          if (common != kNone) e[y] = common;
+          const float inv = pow2i(-e[y]);
           float f[8], sum = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -395,7 +415,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
                        pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f), pack_f16x2(f[2], f[6]),
                        pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f));
           if (piece == 0) {
+            const float scale = pow2i(e[y]) * p.scale_log2;
             reinterpret_cast<float*>(factors + r / 2)[r & 1] = scale * sum;
+            row_scale[r] = scale * 16777216.f;  // (codes are 2^-24)
             *less(r) = 0.f;
             row_ref[r] = kNoRef;
             row_out[r] = outs[y];
@@ -410,6 +432,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
       float l[RPT], ofs[RPT];
 #pragma unroll
       for (int r = 0; r < RPT; ++r) l[r] = ofs[r] = 0.f;
+      const float scale_all = common != kNone ? pow2i(common) * p.scale_log2 * 16777216.f : 0.f;
       bool ok = true, pending = true;  // a row has no reference yet
       auto wait = [&](int id, int parity) {
         ok = warp_wait(bar(id), parity & 1, abort_flag, site(id)) && ok;
@@ -429,23 +452,30 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) rows_q4_many_kernel(const
         const int tile0 = first + t * kKeys;
         KeyFactors mine_f = key_factors(kv.x, kv.y);
         wait(C::S_FULL + (t & 1), t >> 1);
-        float x[RPT], u[RPT];
+        float x[RPT];
         {
           uint32_t raw[RPT];
           if constexpr (RPT == 32) tmem_ld32(lanes + C::TM_S + (t & 1) * NR + r0, raw);
           else tmem_ld16(lanes + C::TM_S + (t & 1) * NR + r0, raw);
-          // (beside the load: what offsets and references add)
-#pragma unroll
-          for (int r = 0; r < RPT; r += 2) {
-            const float4 f = factors[(r0 + r) / 2];
-            add2(u[r], u[r + 1], f.z, f.w, mine_f.v_log, mine_f.v_log);
-            fma2(u[r], u[r + 1], f.x, f.y, mine_f.lo, mine_f.lo, u[r], u[r + 1]);
-          }
-          const float a = scale * mine_f.step * 16777216.f;  // (codes are 2^-24)
           tmem_ld_wait();
+          // x = S factor step + (factor' lo + (log2 stepv - m))
+          auto scores = [&](auto own) {
+            const float all = scale_all * mine_f.step;
 #pragma unroll
-          for (int r = 0; r < RPT; r += 2)
-            fma2(x[r], x[r + 1], __uint_as_float(raw[r]), __uint_as_float(raw[r + 1]), a, a, u[r], u[r + 1]);
+            for (int r = 0; r < RPT; r += 2) {
+              const float4 f = factors[(r0 + r) / 2];
+              float u0, u1, a0 = all, a1 = all;
+              add2(u0, u1, f.z, f.w, mine_f.v_log, mine_f.v_log);
+              fma2(u0, u1, f.x, f.y, mine_f.lo, mine_f.lo, u0, u1);
+              if constexpr (own) {
+                const float2 a = *reinterpret_cast<const float2*>(row_scale + r0 + r);
+                mul2(a0, a1, a.x, a.y, mine_f.step, mine_f.step);
+              }
+              fma2(x[r], x[r + 1], __uint_as_float(raw[r]), __uint_as_float(raw[r + 1]), a0, a1, u0, u1);
+            }
+          };
+          if (common != kNone) scores(std::false_type{});
+          else scores(std::true_type{});
         }
         float top = -INFINITY;
         if (tile0 + kKeys > min(it.n, stop)) {
@@ -646,13 +676,13 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
 template <typename F>
 void with_many(int d, int R, F&& f) {
   if (d <= 64) {
-    f(ManyCfg<64, 64, 16, 2, 8, 1>{});
+    f(ManyCfg<64, 64, 16, 2, 8>{});
   } else if (d <= 128) {
-    if (R <= 32) f(ManyCfg<128, 32, 16, 2, 8, 1>{});
-    else f(ManyCfg<128, 64, 32, 2, 8, 1>{});
+    if (R <= 32) f(ManyCfg<128, 32, 16, 2, 8>{});
+    else f(ManyCfg<128, 64, 32, 2, 8>{});
   } else {
-    if (R <= 32) f(ManyCfg<256, 32, 16, 3, 4, 1>{});
-    else f(ManyCfg<256, 64, 32, 3, 3, 1>{});
+    if (R <= 32) f(ManyCfg<256, 32, 16, 3, 4>{});
+    else f(ManyCfg<256, 64, 32, 3, 3>{});
   }
 }
 
@@ -664,7 +694,7 @@ RowsQ4Shape rows_q4_many_shape(int d, int R) {
     using C = decltype(cfg);
     s.width = C::W;
     s.rows = C::NR;
-    s.ctas = C::CTAS;
+    s.ctas = 1;
   });
   return s;
 }

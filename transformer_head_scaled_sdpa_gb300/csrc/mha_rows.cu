@@ -1343,7 +1343,9 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
     }
   }
   if (part != 0 || splits <= 1) return;  // (a single split wrote the row itself)
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  // (over a 4-bit cache a NaN shows; the other kernels' partials hold none)
+  const bool empty = p.form == kRowsQ4 ? L == 0.f : !(L > 0.f);
+  const float inv = empty ? 0.f : 1.f / L;
   uint32_t out[EPL / 2];
 #pragma unroll
   for (int e = 0; e < EPL; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
@@ -1356,7 +1358,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
   }
   if (p.lse && lane == 0)
     p.lse[(static_cast<long long>(b) * p.H + h) * p.T + (bt - b * p.T)] =
-        L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+        empty ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 template <bool F8, int W, int NR>

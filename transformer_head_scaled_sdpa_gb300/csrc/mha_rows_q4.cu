@@ -570,7 +570,8 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
 #pragma unroll
     for (int w = 0; w < C::WP; ++w) m = fmaxf(m, stats[w][r][0]);
     float a[C::WP], L = 0.f, add = 0.f;
-    const bool live = t < it.live && m != kNoRef && *abort_flag == 0;
+    // (a row that saw no key has sums of 0; one whose scores are all NaN has NaN, and shows it)
+    const bool live = t < it.live && *abort_flag == 0;
 #pragma unroll
     for (int w = 0; w < C::WP; ++w) {
       a[w] = live ? ex2_approx(stats[w][r][0] - m) : 0.f;

@@ -582,7 +582,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
         const float4 o4 = *reinterpret_cast<const float4*>(red + (NR + r) * 4);
         const float ref = row_ref[r];
         float L = l4.x + l4.y + l4.z + l4.w;
-        if (!own_live || !good || ref == kNoRef) L = 0.f;
+        // (a row that saw no key has sums of 0; one whose scores are all NaN has NaN, and shows it)
+        if (!own_live || !good) L = 0.f;
         row_add[r] = o4.x + o4.y + o4.z + o4.w;
         row_inv[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
         if (!whole) {

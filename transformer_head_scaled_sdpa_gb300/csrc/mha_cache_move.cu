@@ -122,17 +122,16 @@ __global__ void __launch_bounds__(kThreads, kForkBlocks) cache_fork_kernel(const
   const int m0 = static_cast<int>(threadIdx.x) >> lg, step = kThreads >> lg;
   // The thread's column of chunk x: piece r of position j.  From one chunk to the next they
   // are added to (a division each, twice, was a third of the instructions).
-  const int per_row = static_cast<int>(pieces);
   const long long hop = static_cast<long long>(gridDim.x) << lg;
   const long long hop_j = hop / pieces;
-  const int hop_r = static_cast<int>(hop - hop_j * pieces);
-  long long x = blockIdx.x, j = -1;
-  int r = 0, c = -1;
+  const long long hop_r = hop - hop_j * pieces;
+  long long x = blockIdx.x, j = -1, r = 0;
+  int c = -1;
   auto locate = [&]() {  // (x is in keys or values for the first time)
     c = x >= chunks;
     const long long q = ((c ? x - chunks : x) << lg) + own;
     j = q / pieces;
-    r = static_cast<int>(q - j * pieces);
+    r = q - j * pieces;
   };
   auto copy = [&](int buffer) {
     uint4* column = nullptr;
@@ -160,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, kForkBlocks) cache_fork_kernel(const
     } else {
       j += hop_j;
       r += hop_r;
-      if (r >= per_row) {
-        r -= per_row;
+      if (r >= pieces) {
+        r -= pieces;
         ++j;
       }
     }

@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
       if (lane == 0) {
         const Loader<W> load{p, it, stop};
         bool ok = true;
-        for (int x = 0; x < 2 * tiles; ++x) {
+        int x = 0;
+        for (; x < 2 * tiles; ++x) {
           const int slot = x % C::SLOTS;
           if (x >= C::SLOTS)
             ok = thread_wait(bar(C::EMPTY + slot), (x / C::SLOTS - 1) & 1, abort_flag, site(C::EMPTY + slot));
@@ -195,6 +196,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
           mbar_arrive_expect_tx(bar(C::FULL + slot), load.bytes(key));
           load.copy(base + C::OFF_RING + slot * C::TILE, bar(C::FULL + slot), key, v);
         }
+        // the copies in flight must land before the CTA exits, also where a wait ran out
+        volatile int never = 0;
+        for (int y = max(0, x - C::SLOTS); y < x; ++y)
+          mbar_wait(bar(C::FULL + y % C::SLOTS), (y / C::SLOTS) & 1, &never, p.status, site(C::FULL + y % C::SLOTS));
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -631,17 +636,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  if (tid == 0 && *abort_flag != 0) {
-    // the copies in flight must land before the CTA exits (each wait is bounded)
-    volatile int never = 0;
-    for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_wait(bar(C::FULL + s), 0, &never, p.status, site(s));
-      mbar_wait(bar(C::FULL + s), 1, &never, p.status, site(s));
-    }
-    if (atomicCAS(&p.status->code, 0, 7 /* MHA_ERR_TIMEOUT */) == 0) {
-      p.status->site = *abort_flag - 1;
-      p.status->block = static_cast<int>(blockIdx.x);
-    }
+  if (tid == 0 && *abort_flag != 0 && atomicCAS(&p.status->code, 0, 7 /* MHA_ERR_TIMEOUT */) == 0) {
+    p.status->site = *abort_flag - 1;
+    p.status->block = static_cast<int>(blockIdx.x);
   }
 }
 

@@ -650,6 +650,11 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
   static bool attr_set[64] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
+    // (the softmax warps' registers come from those that a CTA is launched with)
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, rows_q4_many_kernel<C>);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs < C::REGS) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(rows_q4_many_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;

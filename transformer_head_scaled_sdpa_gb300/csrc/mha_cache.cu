@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTileTokens = 32;  // positions per block: one 32-byte sector of a head's scales
-constexpr int kTileTokensQ4 = 16;  // 4 bits: two sectors of a head's offsets and steps
+constexpr int kTileTokensQ4 = 16;  // 4 bits: at most
 constexpr int kTileHeads = 8;    // heads per block
 
 // What a thread works on: pieces `sub` and `sub + GS` (16 bytes of bf16 each) of
@@ -227,10 +227,10 @@ __device__ __forceinline__ uint32_t codes8(const uint4& x, const RowQ4& r) {
 }
 
 // GS: lanes per row, the power of two >= d / 16
-template <int GS>
+template <int GS, int TOKENS>
 __global__ void __launch_bounds__(kThreads, 4) cache_write_q4_kernel(const __grid_constant__ CacheParams p) {
   griddep_wait();
-  const Rows r = thread_rows<GS, kTileTokensQ4>(p);
+  const Rows r = thread_rows<GS, TOKENS>(p);
   const int sub = static_cast<int>(threadIdx.x) % GS;
   const bool has0 = 8 * sub < p.d, has1 = 8 * (sub + GS) < p.d;
   const int start = __ldg(p.lens + r.b);
@@ -310,10 +310,10 @@ __device__ __forceinline__ uint4 values8(uint32_t c, float lo, float step) {
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-template <int GS>
+template <int GS, int TOKENS>
 __global__ void __launch_bounds__(kThreads) cache_read_q4_kernel(const __grid_constant__ CacheParams p) {
   griddep_wait();
-  const Rows r = thread_rows<GS, kTileTokensQ4>(p);
+  const Rows r = thread_rows<GS, TOKENS>(p);
   const int sub = static_cast<int>(threadIdx.x) % GS;
   const bool has0 = 8 * sub < p.d, has1 = 8 * (sub + GS) < p.d;
   if (!r.head_ok || !has0) return;
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_q4_kernel(const __grid_co
 }
 
 template <int GS>
-cudaError_t launch_gs(const CacheParams& p, CacheKind kind, bool write, unsigned blocks, cudaStream_t s,
+cudaError_t launch_gs(const CacheParams& p, CacheKind kind, bool write, int tile, unsigned blocks, cudaStream_t s,
                       LaunchInfo* info) {
   // as many positions at a time as the block has threads for, or as there are
   const int fit = kThreads / (GS * kTileHeads);
@@ -368,27 +368,41 @@ cudaError_t launch_gs(const CacheParams& p, CacheKind kind, bool write, unsigned
     info->block = threads;
     info->smem = 0;
   }
-  auto* kernel = kind == kCacheQ4 ? (write ? cache_write_q4_kernel<GS> : cache_read_q4_kernel<GS>)
-                                  : (write ? cache_write_kernel<GS> : cache_read_kernel<GS>);
+  auto* kernel = write ? cache_write_kernel<GS> : cache_read_kernel<GS>;
+  if (kind == kCacheQ4) {
+    if (tile == 4) kernel = write ? cache_write_q4_kernel<GS, 4> : cache_read_q4_kernel<GS, 4>;
+    else if (tile == 8) kernel = write ? cache_write_q4_kernel<GS, 8> : cache_read_q4_kernel<GS, 8>;
+    else kernel = write ? cache_write_q4_kernel<GS, 16> : cache_read_q4_kernel<GS, 16>;
+  }
   return launch_serialized(kernel, dim3(blocks), dim3(threads), 0, s, p);
 }
 
 }  // namespace
 
+static long long blocks_of(int B, int T, int H, int tokens) {
+  return static_cast<long long>(B) * ((T + tokens - 1) / tokens) * ((H + kTileHeads - 1) / kTileHeads);
+}
+
 long long cache_blocks(CacheKind kind, int B, int T, int H) {
-  const int tokens = kind == kCacheQ4 ? kTileTokensQ4 : kTileTokens;
-  return static_cast<long long>(B) * ((T + tokens - 1) / tokens) *
-         ((H + kTileHeads - 1) / kTileHeads);
+  return blocks_of(B, T, H, kind == kCacheQ4 ? kTileTokensQ4 : kTileTokens);
 }
 
 cudaError_t launch_cache(const CacheParams& p, CacheKind kind, bool write, cudaStream_t stream, LaunchInfo* info) {
-  const unsigned blocks = static_cast<unsigned>(cache_blocks(kind, p.B, p.T, p.H));
+  int tile = kind == kCacheQ4 ? kTileTokensQ4 : kTileTokens;
+  // Few rows in 4 bits: tiles of 8 or 4 positions as long as that makes no more than four blocks
+  // to an SM.  us with 16, 8 and 4, written: 4 x 16 tokens x 96 heads of 128 features 6.6 4.7
+  // 4.2, 2,000 x 2 of 256 10.7 7.0 5.7, 2,000 x 32 of 64 (500, 1,000 and 2,000 blocks) 8.1 8.7
+  // 12.5, 64 x 512 x 8 of 64 20.5 26.2 39.3; read: 2,000
+  // x 2 of 256 4.8 with 16, 3.6 with 4.
+  if (kind == kCacheQ4)
+    while (tile > 4 && blocks_of(p.B, p.T, p.H, tile / 2) <= 4 * 152) tile /= 2;
+  const unsigned blocks = static_cast<unsigned>(blocks_of(p.B, p.T, p.H, tile));
   const int lanes = p.d / 16;
-  if (lanes <= 1) return launch_gs<1>(p, kind, write, blocks, stream, info);
-  if (lanes <= 2) return launch_gs<2>(p, kind, write, blocks, stream, info);
-  if (lanes <= 4) return launch_gs<4>(p, kind, write, blocks, stream, info);
-  if (lanes <= 8) return launch_gs<8>(p, kind, write, blocks, stream, info);
-  return launch_gs<16>(p, kind, write, blocks, stream, info);
+  if (lanes <= 1) return launch_gs<1>(p, kind, write, tile, blocks, stream, info);
+  if (lanes <= 2) return launch_gs<2>(p, kind, write, tile, blocks, stream, info);
+  if (lanes <= 4) return launch_gs<4>(p, kind, write, tile, blocks, stream, info);
+  if (lanes <= 8) return launch_gs<8>(p, kind, write, tile, blocks, stream, info);
+  return launch_gs<16>(p, kind, write, tile, blocks, stream, info);
 }
 
 }  // namespace mha

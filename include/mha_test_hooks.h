@@ -22,6 +22,18 @@ extern "C" {
  */
 void mha_debug_withhold_p(int on);
 
+/*
+ * mha_debug_q4_ring -- the ring of packed tiles that a step of many rows over a
+ * 4-bit cache loads and empties (host code, nothing is launched), for a unit of
+ * `tiles` tiles and a ring of `slots` (at most 32): from the functions that the
+ * kernel itself goes by.
+ *   loads   [2 tiles][4]: of each item, in the order of loading, its slot, 0
+ *           (keys) or 1 (values), its tile, the barrier it completes a phase of.
+ *   keys, values  [tiles][3]: of each wait of the warps that unpack keys (values),
+ *           in their order, the item they are to find, the barrier, the parity.
+ */
+void mha_debug_q4_ring(int slots, int tiles, int* loads, int* keys, int* values);
+
 #ifdef __cplusplus
 }
 #endif

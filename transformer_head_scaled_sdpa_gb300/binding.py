@@ -129,6 +129,8 @@ def lib():
             h.mha_selftest_timeout.argtypes = [_c_p]
             h.mha_debug_withhold_p.restype = None
             h.mha_debug_withhold_p.argtypes = [_c_i]
+            h.mha_debug_q4_ring.restype = None
+            h.mha_debug_q4_ring.argtypes = [_c_i] * 2 + [_c_p] * 3
             h.mha_sync_status.restype = _c_i
             h.mha_sync_status.argtypes = [_c_p]
             h.mha_status_string.restype = ctypes.c_char_p

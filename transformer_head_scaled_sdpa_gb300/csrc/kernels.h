@@ -268,5 +268,7 @@ int rows_box_keys();
 // Keys of the 4-bit kernels' TMA boxes: a tile, and a piece of a ragged one.
 constexpr int kRowsQ4Keys = 128, kRowsQ4Box = 16;
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);
+// The ring of mha_rows_q4_many.cu, for mha_debug_q4_ring.
+void rows_q4_many_ring(int slots, int tiles, int* loads, int* keys, int* values);
 
 }  // namespace mha

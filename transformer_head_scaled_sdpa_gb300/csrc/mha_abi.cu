@@ -1406,6 +1406,10 @@ int mha_selftest_timeout(void* stream) {
 
 void mha_debug_withhold_p(int on) { g_withhold_p = on ? 1 : 0; }
 
+void mha_debug_q4_ring(int slots, int tiles, int* loads, int* keys, int* values) {
+  mha::rows_q4_many_ring(slots, tiles, loads, keys, values);
+}
+
 int mha_sync_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MHA_ERR_LAUNCH;

@@ -76,8 +76,8 @@ struct ManyCfg {
   static constexpr int OFF_ROWS = OFF_FACTORS + NR * 12;        // float [5][NR], int [NR]
   static constexpr int OFF_RED = OFF_ROWS + NR * 24;            // float [2][NR][4]
   // barriers
-  static constexpr int FULL = 0, EMPTY = SLOTS;          // + slot
-  static constexpr int K_FULL = 2 * SLOTS, K_EMPTY = K_FULL + KST;  // + stage
+  static constexpr int FULL_K = 0, FULL_V = SLOTS, EMPTY = 2 * SLOTS;  // + slot
+  static constexpr int K_FULL = 3 * SLOTS, K_EMPTY = K_FULL + KST;  // + stage
   static constexpr int V_FULL = K_EMPTY + KST, V_EMPTY = V_FULL + VST;
   static constexpr int Q_FULL = V_EMPTY + VST, S_FULL = Q_FULL + 1;  // + tile & 1
   static constexpr int P_FULL = S_FULL + 2, PV_DONE = P_FULL + 2,  // + tile & 1
@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
   constexpr int kMmaWarp = C::SOFT + 2 * C::UNPACK, kLoadWarp = kMmaWarp + 1;
   if (tid == 0) {
     for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_init(bar(C::FULL + s), 1);
+      mbar_init(bar(C::FULL_K + s), 1);
+      mbar_init(bar(C::FULL_V + s), 1);
       mbar_init(bar(C::EMPTY + s), C::UNPACK);
     }
     for (int s = 0; s < C::KST; ++s) {
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
   const bool mine = it.pad[0] != 0;
   const int first = it.t0 * kKeys, stop = mine ? min(it.t1 * kKeys, it.end) : 0;
   const int tiles = stop > first ? (stop - first + kKeys - 1) / kKeys : 0;
+  const RingItems items{C::SLOTS, tiles};
   auto site = [&](int id) { return kRoleMany * 64 + id; };
 
   if (warp >= C::SOFT) {
@@ -185,21 +187,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
         const Loader<W> load{p, it, stop};
         bool ok = true;
         int x = 0;
+        SlotParity keys, values;  // of what was sent
         for (; x < 2 * tiles; ++x) {
-          const int slot = x % C::SLOTS;
+          const int slot = items.slot(x);
           if (x >= C::SLOTS)
             ok = thread_wait(bar(C::EMPTY + slot), (x / C::SLOTS - 1) & 1, abort_flag, site(C::EMPTY + slot));
           if (!ok) break;
-          const bool v = x == 2 * tiles - 1 || (x > 0 && (x & 1) == 0);
-          const int t = x == 2 * tiles - 1 ? tiles - 1 : (v ? x / 2 - 1 : (x + 1) / 2);
-          const int key = first + t * kKeys;
-          mbar_arrive_expect_tx(bar(C::FULL + slot), load.bytes(key));
-          load.copy(base + C::OFF_RING + slot * C::TILE, bar(C::FULL + slot), key, v);
+          const bool v = items.is_values(x);
+          const int key = first + items.tile(x) * kKeys, full = (v ? C::FULL_V : C::FULL_K) + slot;
+          if (v) values.next(slot);
+          else keys.next(slot);
+          mbar_arrive_expect_tx(bar(full), load.bytes(key));
+          load.copy(base + C::OFF_RING + slot * C::TILE, bar(full), key, v);
         }
         // the copies in flight must land before the CTA exits, also where a wait ran out
         volatile int never = 0;
-        for (int y = max(0, x - C::SLOTS); y < x; ++y)
-          mbar_wait(bar(C::FULL + y % C::SLOTS), (y / C::SLOTS) & 1, &never, p.status, site(C::FULL + y % C::SLOTS));
+        for (int y = max(0, x - C::SLOTS); y < x; ++y) {
+          const int slot = items.slot(y);
+          const bool v = items.is_values(y);  // (the slot's last item, and so the last of its barrier)
+          const int full = (v ? C::FULL_V : C::FULL_K) + slot;
+          mbar_wait(bar(full), v ? values.last(slot) : keys.last(slot), &never, p.status, site(full));
+        }
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -265,15 +273,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
       const uint32_t packed = base + C::OFF_RING + key * C::ROW;
       const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       bool ok = true;
+      SlotParity landed;  // of this group's items
       auto wait = [&](int id, int parity) {
         ok = ok && warp_wait(bar(id), parity & 1, abort_flag, site(id));
         return ok;
       };
       auto words = [&](int slot, int c) { return ld_shared_v4(packed + slot * C::TILE + 16 * (c ^ swizzle<W>(key))); };
       auto keys = [&](int t) {
-        const int x = t == 0 ? 0 : 2 * t - 1;
-        const int slot = x % C::SLOTS, st = t % C::KST;
-        if (!wait(C::FULL + slot, x / C::SLOTS)) return;
+        const int slot = items.slot(items.keys(t)), st = t % C::KST;
+        if (!wait(C::FULL_K + slot, landed.next(slot))) return;
         if (t >= C::KST && !wait(C::K_EMPTY + st, t / C::KST - 1)) return;
         tc_fence_after();
 #pragma unroll
@@ -292,9 +300,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
         warp_arrive(bar(C::K_FULL + st), lane);
       };
       auto values = [&](int t) {
-        const int x = t + 1 < tiles ? 2 * t + 2 : 2 * t + 1;
-        const int slot = x % C::SLOTS;
-        if (!wait(C::FULL + slot, x / C::SLOTS)) return;
+        const int slot = items.slot(items.values(t));
+        if (!wait(C::FULL_V + slot, landed.next(slot))) return;
 #pragma unroll
         for (int blk = 0; blk < BLKS; ++blk) {
           const int y = t * BLKS + blk, st = y % C::VST;
@@ -700,6 +707,26 @@ RowsQ4Shape rows_q4_many_shape(int d, int R) {
     s.ctas = 1;
   });
   return s;
+}
+
+void rows_q4_many_ring(int slots, int tiles, int* loads, int* keys, int* values) {
+  const RingItems items{slots, tiles};
+  for (int x = 0; x < 2 * tiles; ++x, loads += 4) {
+    const bool v = items.is_values(x);
+    loads[0] = items.slot(x);
+    loads[1] = v;
+    loads[2] = items.tile(x);
+    loads[3] = (v ? slots : 0) + items.slot(x);
+  }
+  SlotParity landed[2];
+  for (int t = 0; t < tiles; ++t, keys += 3, values += 3) {
+    keys[0] = items.keys(t);
+    keys[1] = items.slot(keys[0]);
+    keys[2] = landed[0].next(keys[1]);
+    values[0] = items.values(t);
+    values[1] = slots + items.slot(values[0]);
+    values[2] = landed[1].next(items.slot(values[0]));
+  }
 }
 
 cudaError_t launch_rows_q4_many(const RowsParams& p, cudaStream_t stream, LaunchInfo* info) {

@@ -155,6 +155,32 @@ struct Loader {
   }
 };
 
+// The packed tiles of a unit in the order in which mha_rows_q4_many.cu loads them: K0 K1 V0 K2
+// V1 ..., item x to slot x % slots of its ring.
+struct RingItems {
+  int slots, tiles;
+  __host__ __device__ int slot(int x) const { return x % slots; }
+  __host__ __device__ int keys(int t) const { return t == 0 ? 0 : 2 * t - 1; }
+  __host__ __device__ int values(int t) const { return t + 1 < tiles ? 2 * t + 2 : 2 * t + 1; }
+  __host__ __device__ bool is_values(int x) const { return x == 2 * tiles - 1 || (x > 0 && (x & 1) == 0); }
+  __host__ __device__ int tile(int x) const {
+    return x == 2 * tiles - 1 ? tiles - 1 : (is_values(x) ? x / 2 - 1 : (x + 1) / 2);
+  }
+};
+// Keys and values are emptied by warps of their own, and a slot has a barrier for each of the
+// two: a wait by parity cannot tell a phase from the one before the last, so who waits on a
+// barrier must have waited for each of its phases.  The parities of one of the two, a bit to
+// a slot, turned with every item:
+struct SlotParity {
+  uint32_t bits = 0;
+  __host__ __device__ int next(int slot) {
+    const int parity = static_cast<int>(bits >> slot) & 1;
+    bits ^= 1u << slot;
+    return parity;
+  }
+  __host__ __device__ int last(int slot) const { return static_cast<int>(~bits >> slot) & 1; }
+};
+
 // More than sixteen rows per key head (mha_rows_q4_many.cu).
 RowsQ4Shape rows_q4_many_shape(int d, int R);
 cudaError_t launch_rows_q4_many(const RowsParams& p, cudaStream_t stream, LaunchInfo* info);

@@ -432,8 +432,9 @@ int mha_cache_read_q4(const void* k_cache, const void* v_cache, const void* k_sc
  * 2^-39 of the row's largest; to 2^-27 where more than 16 rows share a key head),
  * the weights in fp16 (2^-12 relative, and no closer than 2^-33 of the row's
  * largest); products and the denominator's float32 weights accumulate in float32.
- * A NaN in a row's query, or in a key or value that it sees, shows in that row of
- * out and of lse, and in no other.  A weight is kept relative to the row's
+ * A NaN in a row's query, or in a key or value that it sees (a drafted one
+ * included), shows in that row of out and of lse, and in no other: what a row does
+ * not see may hold anything.  A weight is kept relative to the row's
  * largest a_j step_j (step_j: the V row's): V rows of a sequence and head whose
  * steps differ by more than 2^100 are outside this accuracy.
  */

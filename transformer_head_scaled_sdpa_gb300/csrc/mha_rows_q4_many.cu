@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
         const int tile0 = first + t * kKeys;
-        KeyFactors mine_f = key_factors(kv.x, kv.y);
+        const KeyFactors mine_f = key_factors(kv.x, kv.y);
         wait(C::S_FULL + (t & 1), t >> 1);
         float x[RPT];
         {
@@ -491,17 +491,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
         }
         float top = -INFINITY;
         if (tile0 + kKeys > min(it.n, stop)) {
-          const int key = tile0 + kt, off = key - it.n;
-          bool any = false;
+          const KeyMask mask(tile0 + kt, stop, it.n);
 #pragma unroll
-          for (int r = 0; r < RPT; ++r) {
-            bool sees = key < stop;
-            if (sees && off >= 0) sees = (masks[r0 + r][off >> 6] >> (off & 63)) & 1;  // (off < 256: drafted tokens end there)
-            if (!sees) x[r] = -INFINITY;
-            any = any || sees;
-          }
-          // (what hides from all of them may hold anything, and 0 * NaN would be NaN)
-          if (!any) mine_f.v_inv = mine_f.v_ofs = 0.f;
+          for (int r = 0; r < RPT; ++r) x[r] = mask.seen_by(masks, r0 + r) ? x[r] : -INFINITY;
         }
 #pragma unroll
         for (int r = 0; r < RPT; r += 2) top = fmax3(top, x[r], x[r + 1]);

@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
       __syncwarp();  // (the tile before is read)
       keys[lane] = make_float4(mine.step, mine.lo, mine.v_log, mine.v_inv);
       keys_ofs[lane] = mine.v_ofs;
+      __syncwarp();  // (read by the other lanes: the vote below orders no memory among them)
     }
     ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * stage, parity, abort_flag, p.status, kRoleRowsQ4 * 64 + stage));
     if (!ok) break;

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
             float m = x[r];
 #pragma unroll
             for (int z = 1; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-            m = fmaxf(ref[0][r], m - kLift);
+            m = fmaxf(ref[0][r], lifted(m));
             by[r] = ex2_approx(ref[0][r] - m);
             ref[0][r] = m;
             l[0][r] *= by[r];
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
               for (int x = 1; x < MT; ++x) m = fmax3(m, s[x][n][r], s[x][n][2 + r]);
 #pragma unroll
               for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-              m = fmaxf(ref[n][r], m - kLift);
+              m = fmaxf(ref[n][r], lifted(m));
               by[r] = ex2_approx(ref[n][r] - m);
               ref[n][r] = m;
               l[n][r] *= by[r];

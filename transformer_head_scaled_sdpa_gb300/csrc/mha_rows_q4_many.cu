@@ -511,9 +511,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
             const float4 m4 = *reinterpret_cast<const float4*>(red + r * 4);
             const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), old = row_ref[r], sub = -*less(r);
             ref = m == -INFINITY ? old : fmaxf(old, m + sub - kLift);
-            row_by[r] = old == kNoRef ? 1.f : ex2_approx(old - ref);  // (nothing is summed up yet)
             const float now = ref == kNoRef ? 0.f : ref;
-            row_down[r] = sub - now;
+            float down = sub - now;
+            // (where references are so large that their places are not far below kLift, m must come
+            // to lie in the weights' range all the same: the distance is then m's own)
+            if (m + down > kLimit || (ref > old && m + down < 0.f)) down = -lifted(m);
+            row_by[r] = old == kNoRef ? 1.f : ex2_approx(down);  // (nothing is summed up yet)
+            row_down[r] = down;
             *less(r) = -now;
             row_ref[r] = ref;
           }

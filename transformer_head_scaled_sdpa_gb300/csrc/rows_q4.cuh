@@ -11,6 +11,9 @@ namespace mha {
 constexpr float kNoRef = -3.0e38f;  // a row that has seen no key
 constexpr float kLift = 8.f;        // weights are 2^kLift at their reference
 constexpr float kLimit = 15.f;      // and stay below 2^kLimit, inside fp16's range
+// (A reference is a score less kLift.  Scores near 2^27 have places of 16, and to the nearest of
+// them a reference could lie 16 below its score: it is rounded up.)
+__device__ __forceinline__ float lifted(float m) { return __fadd_ru(m, -kLift); }
 
 // Swizzle of TMA's rows of W / 2 bytes (32, 64 or 128): 16-byte piece c of row `key` of a
 // tile lies at piece c ^ swizzle(key), so that the eight rows of a matrix lie in

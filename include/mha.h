@@ -432,6 +432,8 @@ int mha_cache_read_q4(const void* k_cache, const void* v_cache, const void* k_sc
  * 2^-39 of the row's largest; to 2^-27 where more than 16 rows share a key head),
  * the weights in fp16 (2^-12 relative, and no closer than 2^-33 of the row's
  * largest); products and the denominator's float32 weights accumulate in float32.
+ * Scores are finite where d_k * scale * max |q| * max |k|, over the rows and the
+ * positions of a sequence and key head, is below 2^120.
  * A NaN in a row's query, or in a key or value that it sees (a drafted one
  * included), shows in that row of out and of lse, and in no other: what a row does
  * not see may hold anything.  A weight is kept relative to the row's

@@ -143,10 +143,14 @@ __device__ __forceinline__ void score_products(uint32_t at, float (&s)[2][NQ][4]
 }
 
 // A row's fragments of Q: lane (g, j) has the features 32 c + 8 j .. + 7 (v[c]) of its
-// column's row; put(i, b) gets the fragment of reduction step i.  Returns the factors
-// of the row's product with codes and of its sum (every lane of the column's).
+// column's row; put(i, b) gets the fragment of reduction step i.  Returns the e of its
+// factor 2^e and its sum (every lane of the column's).
+struct QRow {
+  int e;
+  float sum;
+};
 template <int KC, typename F>
-__device__ __forceinline__ float2 q_fragments(const uint4 (&v)[KC], float scale_log2, F&& put) {
+__device__ __forceinline__ QRow q_fragments(const uint4 (&v)[KC], F&& put) {
   float amax = 0.f;
 #pragma unroll
   for (int c = 0; c < KC; ++c) {
@@ -173,8 +177,7 @@ __device__ __forceinline__ float2 q_fragments(const uint4 (&v)[KC], float scale_
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  const float f = pow2i(e) * scale_log2;
-  return make_float2(f * 16777216.f, f * sum);  // (codes are 2^-24)
+  return {e, sum};
 }
 
 // Adds one to a count in shared memory, behind what the warp read and ahead of what it
@@ -285,20 +288,29 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
 
   uint2 q[C::Q_SHARED ? 1 : 2 * KC * NT];
   uint2* q_shared = reinterpret_cast<uint2*>(smem + C::OFF_Q) + lane;
-  float fa[NT][2], fb[NT][2];  // factors of a row's product and of its sum: columns 8 n + 2 j, + 1
+  QRow rows[NT];
+  int top_e = -200;  // of the unit's rows; an infinite one, whose scores are none, has 114
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const float2 f = q_fragments<KC>(v[n], p.scale_log2, [&](int i, uint2 b) {
+    rows[n] = q_fragments<KC>(v[n], [&](int i, uint2 b) {
       if constexpr (C::Q_SHARED) {
         if (warp == 0) q_shared[(i * NT + n) * 32] = b;
       } else {
         q[i * NT + n] = b;
       }
     });
+    if (rows[n].e < 114) top_e = max(top_e, rows[n].e);
+  }
+  const int shift = factor_shift(__reduce_max_sync(0xffffffffu, top_e), p.scale_log2);
+  const float key_scale = pow2i(shift);
+  float fa[NT][2], fb[NT][2];  // factors of a row's product and of its sum: columns 8 n + 2 j, + 1
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float f = pow2i(rows[n].e) * pow2i(-shift) * p.scale_log2;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      fa[n][r] = __shfl_sync(0xffffffffu, f.x, 8 * j + 4 * r);
-      fb[n][r] = __shfl_sync(0xffffffffu, f.y, 8 * j + 4 * r);
+      fa[n][r] = __shfl_sync(0xffffffffu, f * 16777216.f, 8 * j + 4 * r);  // (codes are 2^-24)
+      fb[n][r] = __shfl_sync(0xffffffffu, f * rows[n].sum, 8 * j + 4 * r);
     }
   }
   if (threadIdx.x < NR * 4) masks[threadIdx.x >> 2][threadIdx.x & 3] = bits;
@@ -332,7 +344,7 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
   for (int tile0 = first; tile0 < stop; tile0 += kKeys, ++i) {
     const uint32_t tile = ring + stage * 2 * C::TILE;
     const uint2 kv = words.get(i, tile0);
-    KeyFactors mine = key_factors(kv.x, kv.y);
+    KeyFactors mine = key_factors(kv.x, kv.y, key_scale);
     if constexpr (!FEW) {
       // the keys' factors by way of shared memory: lane's own key to the lanes of its row
       __syncwarp();  // (the tile before is read)

@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
       words.start(first);
       constexpr int kNone = 1000;
       int common = kNone;  // the e of all rows
+      float key_scale, factor_scale;
       {
         // Q: eight features to a lane, W / 8 lanes to a row
         constexpr int LPR = W / 8, RPW = 32 / LPR, PASSES = (NR + C::SOFT * RPW - 1) / (C::SOFT * RPW);
@@ -393,8 +394,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
           for (int z = 1; z < LPR; z <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, z));
           e[y] = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100);
           if (amax != 0.f) {
-            top = max(top, e[y]);
-            low = min(low, e[y]);
+            if (amax < INFINITY) top = max(top, e[y]);
+            low = min(low, amax < INFINITY ? e[y] : -300);  // (an infinity: no common factor)
           }
         }
         top = __reduce_max_sync(0xffffffffu, top);
@@ -407,7 +408,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
           top = max(top, z.x);
           low = min(low, z.y);
         }
-        if (low <= top && top - low <= 8 && top < 114) common = top;  // (114: an infinity)
+        if (low <= top && top - low <= 8) common = top;
+        const int shift = factor_shift(top, p.scale_log2);
+        key_scale = pow2i(shift);
+        factor_scale = pow2i(-shift) * p.scale_log2;
 #pragma unroll
         for (int y = 0; y < PASSES; ++y) {
           const int r = (y * C::SOFT + warp) * RPW + lane / LPR;
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
                        pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f), pack_f16x2(f[2], f[6]),
                        pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f));
           if (piece == 0) {
-            const float scale = pow2i(e[y]) * p.scale_log2;
+            const float scale = pow2i(e[y]) * factor_scale;
             reinterpret_cast<float*>(factors + r / 2)[r & 1] = scale * sum;
             row_scale[r] = scale * 16777216.f;  // (codes are 2^-24)
             *less(r) = 0.f;
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
       float l[RPT], ofs[RPT];
 #pragma unroll
       for (int r = 0; r < RPT; ++r) l[r] = ofs[r] = 0.f;
-      const float scale_all = common != kNone ? pow2i(common) * p.scale_log2 * 16777216.f : 0.f;
+      const float scale_all = common != kNone ? pow2i(common) * factor_scale * 16777216.f : 0.f;
       bool ok = true, pending = true;  // a row has no reference yet
       auto wait = [&](int id, int parity) {
         ok = warp_wait(bar(id), parity & 1, abort_flag, site(id)) && ok;
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
         const int tile0 = first + t * kKeys;
-        const KeyFactors mine_f = key_factors(kv.x, kv.y);
+        const KeyFactors mine_f = key_factors(kv.x, kv.y, key_scale);
         wait(C::S_FULL + (t & 1), t >> 1);
         float x[RPT];
         {

@@ -40,6 +40,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// Queries are scaled by powers of two, 2^-e to a row.  A row's factor, 2^(e + 24) times the
+// scale, would pass float32's range from |q| = 2^118 / scale on, though its scores be finite:
+// for a unit with a factor above 2^100 (top: the largest e of its finite rows) all factors are
+// taken 2^shift smaller and the keys' steps and offsets as much larger.  These stay in
+// range: the scores of that largest row are finite (include/mha.h has the bound).
+__device__ __forceinline__ int factor_shift(int top, float scale_log2) {
+  const int exponent = static_cast<int>(__float_as_uint(scale_log2) >> 23) - 127;
+  return min(max(top + 24 + exponent - 100, 0), 100);
+}
+
 // What a key's offset and step, and its value's, come to in a step.  A value's pair that is
 // not finite (the write's NaN offset; a step of 0 is as much) makes the scores NaN, and its
 // factors are 0: a row that sees the position is then NaN in out and in lse, and one that does
@@ -48,10 +58,11 @@ struct KeyFactors {
   float step, lo;             // of the key
   float v_log, v_inv, v_ofs;  // of the value: log2 step, 1 / step, lo / step
 };
-__device__ __forceinline__ KeyFactors key_factors(uint32_t k, uint32_t v) {
+// (key_scale: 2^shift)
+__device__ __forceinline__ KeyFactors key_factors(uint32_t k, uint32_t v, float key_scale) {
   KeyFactors f;
-  f.step = bf16_hi(k);
-  f.lo = bf16_lo(k);
+  f.step = bf16_hi(k) * key_scale;
+  f.lo = bf16_lo(k) * key_scale;
   const float step = bf16_hi(v);
   f.v_log = lg2_approx(step);
   f.v_inv = rcp_approx(step);

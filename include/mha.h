@@ -499,7 +499,8 @@ int mha_cache_fork(void* k_cache, void* v_cache, void* k_scale, void* v_scale, i
  *   path_lens  device int32 [B] or NULL (T), clamped to [0, T].
  *   T          up to 256 (MHA_ERR_UNSUPPORTED beyond).
  * The rows moved from, where they are not moved to, stay as they were.  Other
- * arguments and errors as mha_cache_fork (B without its limit).
+ * arguments and errors as mha_cache_fork (B without its limit, but MHA_ERR_SHAPE
+ * where the launch would pass a grid's 2^31 - 1 blocks).
  */
 int mha_cache_compact(void* k_cache, void* v_cache, void* k_scale, void* v_scale, int format, int B,
                       int T, int H, int Lk, int d_k, const int32_t* prefix_lens,

@@ -246,7 +246,7 @@ long long compact_scale_chunks(const MoveParams& p, int lg) {
 
 long long compact_blocks(const MoveParams& p) {
   const int lg = log_columns(p.T, kBlockItems);
-  return p.B * 2 * (compact_chunks(p, lg) + compact_scale_chunks(p, lg));
+  return 2ll * p.B * (compact_chunks(p, lg) + compact_scale_chunks(p, lg));
 }
 
 cudaError_t launch_cache_fork(const MoveParams& p, cudaStream_t stream, LaunchInfo* info) {

@@ -428,10 +428,11 @@ int mha_cache_read_q4(const void* k_cache, const void* v_cache, const void* k_sc
  * 2^32, MHA_ERR_SHAPE).  The values attended to are offset + code * step
  * themselves, not rounded to bf16.
  * The tensor cores multiply the codes; a key's offset and step are applied to its
- * scores and weights in float32.  q enters in fp16, scaled by a power of two (to
- * 2^-39 of the row's largest; to 2^-27 where more than 16 rows share a key head),
- * the weights in fp16 (2^-12 relative, and no closer than 2^-33 of the row's
- * largest); products and the denominator's float32 weights accumulate in float32.
+ * scores and weights in float32.  q enters in fp16, scaled by a power of two (off by
+ * up to 2^-35 of the row's largest, of 2^-86 where that is larger; by up to 2^-27
+ * where more than 16 rows share a key head), the weights in fp16 (2^-11 relative,
+ * and no closer than 2^-33 of the row's largest); products and the denominator's
+ * float32 weights accumulate in float32.
  * Scores are finite where d_k * scale * max |q| * max |k|, over the rows and the
  * positions of a sequence and key head, is below 2^120.
  * A NaN in a row's query, or in a key or value that it sees (a drafted one

@@ -108,3 +108,37 @@ def test_a_large_scale(mha, T):  # noqa: F811
         case["q"][:] = 0.0
         case["q"][..., 3] = size
         one_key_wins(case, mha, 3, scale, f"|q| {size:.3g}, scale {scale:.3g}")
+
+
+# What the header states of q: off by up to 2^-35 of its row's largest, and to 2^-27 where rows
+# that share a factor are up to 2^8 larger.  In a packed row's even features it is 2^-39
+# (2^-31): the odd ones' codes are 16 times too large, and q is rounded to fp16 16 times smaller.
+EVEN, ODD = 2.0 ** -39, 2.0 ** -35
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,smaller", [(1, 0), (2, 0), (8, 0), (16, 0), (40, 0), (40, 8)])
+@pytest.mark.parametrize("feature", [1, 2, 7, 20, 31])
+def test_small_features_beside_a_large_one(mha, d, T, smaller, feature):  # noqa: F811
+    """Queries of 1 in feature 0 (2^-8 in every second row, where the rows' common factor leaves
+    eight binary places fewer) and of 2^-31 to 2^-28 in another, keys of that other alone, a scale
+    of 2^30.  lse is off by no more than a score is: scale |k| times q's error."""
+    n, scale = 150, 2.0 ** 30
+    case = make_step(d + T, 1, T, 1, 1, d, n + T, [n], None, None)
+    rng = np.random.default_rng(d + T + feature)
+    k = torch.zeros((1, n + T, 1, d))
+    k[0, :, 0, feature] = torch.from_numpy(rng.uniform(0.5, 3.0, size=n + T)).float()
+    case["kc"], case["ks"] = qu.q4_cache(k.to(torch.bfloat16))
+    case["q"][:] = 0.0
+    case["q"][..., 0] = 1.0
+    case["q"][:, 1::2, :, 0] = 2.0 ** -smaller
+    case["q"][0, :, 0, feature] = torch.from_numpy(rng.uniform(-1, 1, size=T) * 2.0 ** -28).to(torch.bfloat16)
+    _, lse = call_step(mha, on_gpu(case), True, scale=scale)
+    assert mha.mha_sync_status() == 0
+    kv, _ = qu.cache_f64(case["kc"], case["ks"])
+    assert (kv[..., 0] == 0).all()
+    s = scale * cu.f64(case["q"])[0, :, 0, feature, None] * kv[0, None, :, 0, feature]
+    s = np.where(np.arange(n + T)[None] <= n + np.arange(T)[:, None], s, -np.inf)
+    ref = np.log(np.exp(s - s.max(-1, keepdims=True)).sum(-1)) + s.max(-1)
+    room = pu.LSE_ABS + pu.LSE_REL * np.abs(ref) + scale * (ODD if feature & 1 else EVEN) * kv.max()
+    assert (np.abs(cu.f64(lse)[0, 0] - ref) <= room).all()

@@ -32,9 +32,10 @@
 // 34.7 (8 x 48 heads x 16 rows of 64 features x 2,048 to 4,096 keys 77 against 42).  fp8 operands bring nothing here
 // (mma.sync converts e4m3 to fp16 first on this machine).
 //
-// q is scaled by a power of two to [2^14, 2^15) at its row's largest and then exact in
-// fp16 (to 2^-40 of that); the weights are rounded to fp16 (2^-11 relative); products,
-// the denominator and the offsets' sums are float32.  Weights are 2^kLift at a row's
+// q is scaled by a power of two to [2^14, 2^15) at its row's largest and then exact in fp16
+// to half its smallest place, 2^-25: 2^-39 of the row's largest, and 2^-35 in the odd
+// features, which are divided by 16 first.  The weights are rounded to fp16 (2^-11 relative);
+// products, the denominator and the offsets' sums are float32.  Weights are 2^kLift at a row's
 // reference m, which moves when a tile's largest weight would pass 2^kLimit.
 //
 // What bounds it: 16 x 96 heads x 1,024 to 2,048 keys of 128 features, 322 MB, 61 us (5.3

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
         const uint64_t bits = tid < NR * 4 ? mask_word(p, it, tid, out_row) : 0;
         // q 2^-e with the row's largest magnitude in [2^14, 2^15); where the unit's rows are within
         // 2^8 of one another (those of zeros aside) with the largest row's e, and one factor for all:
-        // an fp16 of q is then off by up to 2^-27 of its row's largest
+        // an fp16 of q is then off by up to 2^-27 of its row's largest (2^-31 in even features)
         int e[PASSES], top = -200, low = 200;
 #pragma unroll
         for (int y = 0; y < PASSES; ++y) {

@@ -35,7 +35,7 @@
 // q is scaled by a power of two to [2^14, 2^15) at its row's largest and then exact in fp16
 // to half its smallest place, 2^-25: 2^-39 of the row's largest, and 2^-35 in the odd
 // features, which are divided by 16 first.  The weights are rounded to fp16 (2^-11 relative);
-// products, the denominator and the offsets' sums are float32.  Weights are 2^kLift at a row's
+// products' sums (rows_q4.cuh: what they cut), the denominator and the offsets' are float32.  Weights are 2^kLift at a row's
 // reference m, which moves when a tile's largest weight would pass 2^kLimit.
 //
 // What bounds it: 16 x 96 heads x 1,024 to 2,048 keys of 128 features, 322 MB, 61 us (5.3

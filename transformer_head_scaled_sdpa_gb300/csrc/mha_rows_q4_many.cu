@@ -18,8 +18,9 @@
 // row needs (its factors and reference) is read by all lanes at once.  Rows of like sizes
 // share a power of two in Q, and the factor of their products (8 x 24 heads x 56 rows of 128
 // features x 2,048 to 4,096 keys 69 us, 75 with a factor each); a row that is far larger, or
-// infinite, must not take the others' digits, and then each has its own.  Weights are rounded to fp16 (2^-11 relative); sums, scores and
-// products are float32; the denominator and the offsets' sum stay in a thread's registers
+// infinite, must not take the others' digits, and then each has its own.  Weights are rounded to
+// fp16 (2^-11 relative); scores and sums are float32 (rows_q4.cuh: what sums of products cut);
+// the denominator and the offsets' sum stay in a thread's registers
 // until the unit ends.  References move for all keys of a tile, by a vote of the
 // warpgroup, when a weight would pass 2^kLimit; O is then scaled in tensor memory.
 //

@@ -8,6 +8,14 @@
 
 namespace mha {
 
+// Codes are fp16 subnormals to the tensor cores, c 2^-24, exact; but their products are aligned
+// by the factors' exponents, a subnormal's as 2^-14, and of the sixteen that are added at a time
+// each is cut 25 places below the largest: at 2^-15 of the largest q (or weight) of the sixteen,
+// times a code of 1.  (Measured, on mma.sync and tcgen05 alike.)  A q within 2^8 of that largest
+// loses nothing, having eight bits; an output loses less than 16 x 2^-15 of the largest weight
+// times its step for each sixteen keys, as much as fp16 takes from the weight.  Codes made normal numbers by a product
+// more per two of them lose nothing there, and time: 16 x 96 heads x 1,024 to 2,048 keys 59.9 to
+// 64.0 us, 4 x 96 heads x 16 rows 35.1 to 38.0, 8 x 24 heads x 56 rows 68.1 to 70.5.
 constexpr float kNoRef = -3.0e38f;  // a row that has seen no key
 constexpr float kLift = 8.f;        // weights are 2^kLift at their reference
 constexpr float kLimit = 15.f;      // and stay below 2^kLimit, inside fp16's range

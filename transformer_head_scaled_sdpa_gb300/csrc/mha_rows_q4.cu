@@ -28,8 +28,8 @@
 // mma.sync and not tcgen05 for these few rows: reading the cache bounds them (68 bytes per
 // row of 128 features), and tcgen05 wants the codes in 8 bits or more, in shared or tensor
 // memory: the packed tile written and read, the unpacked one written and read, and a CTA
-// of a dozen warps that hand it on; with it, 4 x 96 heads x 16 rows take 50 us against
-// 34.7 (8 x 48 heads x 16 rows of 64 features x 2,048 to 4,096 keys 77 against 42).  fp8 operands bring nothing here
+// of a dozen warps that hand it on; with it, 4 x 96 heads x 16 rows take 52 us against
+// 35 (8 x 48 heads x 16 rows of 64 features x 2,048 to 4,096 keys 109 against 43).  fp8 operands bring nothing here
 // (mma.sync converts e4m3 to fp16 first on this machine).
 //
 // q is scaled by a power of two to [2^14, 2^15) at its row's largest and then exact in fp16
@@ -43,7 +43,7 @@
 // waits 4 to 5 us for its lengths, Q and first tile and for its merge, and 0.46 of the
 // issue slots (the masks' and shifts' pipe 0.35, the tensor pipe 0.29).  2 x 8 key heads x
 // 40,001 to 65,537 keys, 4 rows: 30 us, 7 of them latency at both ends and 5 the merge of
-// splits.  4 x 96 heads x 16 rows x 1,024 to 2,048 keys: 34.7 us, one wave of 384 units on
+// splits.  4 x 96 heads x 16 rows x 1,024 to 2,048 keys: 35.0 us, one wave of 384 units on
 // 456 CTAs as long as its longest.  128 x 8 heads x 16 to 256 keys of 64 features: 8 us.
 #include <cuda_bf16.h>
 
@@ -632,17 +632,17 @@ __global__ void __launch_bounds__(32 * C::WP, C::CTAS) rows_q4_kernel(const __gr
 // Calls f with the kernel's configuration for R rows per key head of d features.  us over
 // 8 sequences of 2,048 to 4,096 keys, 48 heads of 64 features, 24 of 128 or 12 of 256:
 // as here, in a unit for twice the rows or more, and in units for fewer:
-//   rows     64                128               256
-//    1       28.9 30.3         22.7 23.6         23.4 23.6
-//    2       29.4 33.7 47.9    23.5 25.1 42.6    23.6 24.6 39.2
-//    8       33.7 41.5 77.1    25.7 38.0 62.6    25.6 31.3 59.4
-//   16       42.2 77.2 53.1    37.9 45.4 49.5    32.9 49.4 44.1   (wider: the other kernel)
-//   32       65.4 77.5         45.8      59.3    50.1      67.1   (128, 256: the other kernel)
+//   rows     64                 128               256
+//    1       28.4  29.5         22.6 23.3         23.4 23.6
+//    2       29.8  30.3 52.6    23.7 25.2 43.2    23.6 25.0 39.5
+//    8       31.4  41.5 73.3    25.9 38.6 62.7    26.4 31.6 60.0
+//   16       42.6 109.2 50.9    39.8 47.6 49.8    33.0 51.9 51.8   (wider: the other kernel)
+//   32       66.5 110.4         48.9      60.0    52.6      68.7   (128, 256: the other kernel)
 // Stages and CTAs to an SM were swept with them.  More CTAs hide the ends of units, more
 // stages the memory: one row of 64 features over 128 x 8 heads x 16 to 256 keys 8.0 us with
-// seven CTAs of three stages, 10.6 with six of four, 9.7 with ten of two; eight rows of 64
-// 33.7 with five CTAs of two stages, 37.1 with four of four; of 256 25.6 with two CTAs of
-// three stages, 32.4 with three of two.
+// seven CTAs of three stages, 10.6 with six of four, 9.8 with ten of two; eight rows of 64
+// 31.3 with five CTAs of two stages, 37.6 with four of four; of 256 26.4 with two CTAs of
+// three stages, 32.5 with three of two.
 template <typename F>
 void with_config(int d, int R, F&& f) {
   if (d <= 64) {

@@ -17,7 +17,7 @@
 // Softmax: a thread has a key, that is its offset and step, and RPT of the rows; what a
 // row needs (its factors and reference) is read by all lanes at once.  Rows of like sizes
 // share a power of two in Q, and the factor of their products (8 x 24 heads x 56 rows of 128
-// features x 2,048 to 4,096 keys 69 us, 75 with a factor each); a row that is far larger, or
+// features x 2,048 to 4,096 keys 68 us, 75 with a factor each); a row that is far larger, or
 // infinite, must not take the others' digits, and then each has its own.  Weights are rounded to
 // fp16 (2^-11 relative); scores and sums are float32 (rows_q4.cuh: what sums of products cut);
 // the denominator and the offsets' sum stay in a thread's registers
@@ -25,19 +25,19 @@
 // warpgroup, when a weight would pass 2^kLimit; O is then scaled in tensor memory.
 //
 // Roles: softmax warps (8, or 16), four warps that unpack keys, four that unpack values
-// (one group for both: 58 us against 49, 8 x 12 heads x 32 rows of 256 features x 2,048 to
-// 4,096 keys), one that issues the MMAs, one that loads.  Scores and weights have two
+// (one group for both: 58 us when this took 49, 8 x 12 heads x 32 rows of 256 features x 2,048
+// to 4,096 keys), one that issues the MMAs, one that loads.  Scores and weights have two
 // buffers each, S(t + 1) is formed before PV(t).  The MMA warp runs converged and elects a
 // lane to issue, which keeps descriptors in uniform registers: issued by one lane on its own
-// an MMA took 150 cycles (32 rows of 128 features 64 us against 45).
+// an MMA took 150 cycles (32 rows of 128 features 64 us when this took 45).
 //
 // What bounds it: the softmax warps, 1,900 to 2,400 cycles a tile (scores read and scaled
 // 900, vote and waits 500, weights 450), with one CTA to an SM, and 15 to 20 thousand
 // cycles that a unit costs beside its tiles (its lengths 2,600, Q 4,500, first tile 5,000,
 // sums and outputs 5,000).  5 x 2 key heads x 56 rows of 256 features x 7,001 to 20,000
-// keys: 32.4 us (5 of them the merge of splits), 47 on mma.sync in units of 16 rows; 8 x
-// 24 heads x 56 rows of 128 features x 2,048 to 4,096 keys 68 against 93, 252 rows 230
-// against 334.
+// keys: 33.4 us (5 of them the merge of splits), 47 on mma.sync in units of 16 rows; 8 x
+// 24 heads x 56 rows of 128 features x 2,048 to 4,096 keys 68 against 95, 252 rows 232
+// against 350.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -680,10 +680,10 @@ cudaError_t launch_cfg(const RowsParams& p, cudaStream_t stream, LaunchInfo* inf
 
 // Calls f with the kernel's configuration for R rows per key head of d features.  Units of 32
 // rows up to 32: they hold half the weights (8 x 24 heads of 128 features x 2,048 to 4,096
-// keys, 32 rows: 46 us, 67 in units of 64).  Units of 64 from there on: each unpacks the
-// tiles once for all of them (56 rows 68 us, in two units of 32 98; 252 rows 229 and 312).
-// 16 or 32 rows to a softmax thread: four or two warpgroups.  64 features: 105 us (56 rows,
-// 48 heads) with 16 and 112 with 32; 128: 95 and 69, where registers do not hold 16 warps'.
+// keys, 32 rows: 49 us, 67 in units of 64).  Units of 64 from there on: each unpacks the
+// tiles once for all of them (56 rows 68 us, in two units of 32 81; 252 rows 232 and 311).
+// 16 or 32 rows to a softmax thread: four or two warpgroups.  64 features: 111.6 us (56 rows,
+// 48 heads) with 16 and 112.5 with 32; 128: 92 and 68, where registers do not hold 16 warps'.
 template <typename F>
 void with_many(int d, int R, F&& f) {
   if (d <= 64) {

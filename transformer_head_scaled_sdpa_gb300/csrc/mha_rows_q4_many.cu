@@ -81,8 +81,9 @@ struct ManyCfg {
   static constexpr int K_FULL = 3 * SLOTS, K_EMPTY = K_FULL + KST;  // + stage
   static constexpr int V_FULL = K_EMPTY + KST, V_EMPTY = V_FULL + VST;
   static constexpr int Q_FULL = V_EMPTY + VST, S_FULL = Q_FULL + 1;  // + tile & 1
-  static constexpr int P_FULL = S_FULL + 2, PV_DONE = P_FULL + 2,  // + tile & 1
-                        DRAIN = PV_DONE + 2, NBAR = DRAIN + 1;
+  static constexpr int P_FULL = S_FULL + 2;  // + tile & 1
+  static constexpr int BUT_LAST = P_FULL + 2, DRAIN = BUT_LAST + 1;  // the products of all tiles but the last, of all
+  static constexpr int NBAR = DRAIN + 1;
   static constexpr int OFF_UNIT = OFF_RED + NR * 32;
   static constexpr int OFF_BAR = OFF_UNIT + static_cast<int>(sizeof(Unit));
   static constexpr int OFF_TMEM = OFF_BAR + 8 * NBAR, OFF_ABORT = OFF_TMEM + 4;
@@ -144,8 +145,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
     mbar_init(bar(C::S_FULL + 1), 1);
     mbar_init(bar(C::P_FULL), C::SOFT);
     mbar_init(bar(C::P_FULL + 1), C::SOFT);
-    mbar_init(bar(C::PV_DONE), 1);
-    mbar_init(bar(C::PV_DONE + 1), 1);
+    mbar_init(bar(C::BUT_LAST), 1);
     mbar_init(bar(C::DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
                 umma_ss(tmem + C::TM_O + blk * NR, a + static_cast<uint64_t>((k * 2048) >> 4),
                         w + static_cast<uint64_t>((k * 256) >> 4), idesc_o, (t > 1 || k > 0) ? 1u : 0u);
               umma_commit(bar(C::V_EMPTY + st));
-              if (blk == BLKS - 1) umma_commit(bar(C::PV_DONE + b));
+              if (blk == BLKS - 1 && t == tiles - 1) umma_commit(bar(C::BUT_LAST));
             }
             __syncwarp();
           }
@@ -455,10 +455,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
         ok = warp_wait(bar(id), parity & 1, abort_flag, site(id)) && ok;
         tc_fence_after();
       };
-      // Products of tile t, whose scores or the next tile's have been waited for: those of tile t - 2,
-      // on the same barrier, were done before.
-      auto products = [&](int t) {
-        if (t >= 0) wait(C::PV_DONE + (t & 1), t >> 1);
+      // The products of all tiles before t, whose scores have been waited for: they come before the
+      // scores of t + 1, whose commit covers them.  (A barrier for each tile's products, waited for at
+      // these moves alone, would pass unseen phases, which a wait by parity cannot tell apart.)
+      auto products_before = [&](int t) {
+        if (t > 0) {
+          if (t + 1 < tiles) wait(C::S_FULL + ((t + 1) & 1), (t + 1) >> 1);
+          else wait(C::BUT_LAST, 0);
+        }
       };
       // a live row of this thread to look after
       int own_t = -1;
@@ -527,7 +531,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
             row_ref[r] = ref;
           }
           pending = any_of_128(nbar, own_live && ref == kNoRef);
-          products(t - 1);
+          products_before(t);
 #pragma unroll
           for (int r = 0; r < RPT; ++r) {
             const float by = row_by[r0 + r];
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) rows_q4_many_kernel(const __gri
           red[(NR + r0 + lane / GL) * 4 + w4] = z;
         }
       }
-      products(tiles - 1);
+      if (tiles > 0) wait(C::DRAIN, 0);
       const bool good = tiles > 0 && ok && *abort_flag == 0;
       named_barrier(nbar, 128);
       const bool whole = it.splits == 1;

@@ -17,7 +17,7 @@
 // Softmax: a thread has a key, that is its offset and step, and RPT of the rows; what a
 // row needs (its factors and reference) is read by all lanes at once.  Rows of like sizes
 // share a power of two in Q, and the factor of their products (8 x 24 heads x 56 rows of 128
-// features x 2,048 to 4,096 keys 68 us, 75 with a factor each); a row that is far larger, or
+// features x 2,048 to 4,096 keys 68 us, 74 with a factor each); a row that is far larger, or
 // infinite, must not take the others' digits, and then each has its own.  Weights are rounded to
 // fp16 (2^-11 relative); scores and sums are float32 (rows_q4.cuh: what sums of products cut);
 // the denominator and the offsets' sum stay in a thread's registers
